@@ -163,6 +163,87 @@ moe_status moe_forward_host_experts(const moe_dims* d, const void* x, const moe_
                                     void* out, void* shadow, size_t shadow_bytes, void* workspace, size_t ws_bytes,
                                     void* stream);
 
+/* ---- 4-bit weights with group scales -------------------------------------------------------
+ * The pages' layer reads its experts' weights from HBM once per step; in 4 bits they are 3.4 to
+ * 3.9 times smaller. (The pages store bf16 only; this form of the weights has no counterpart.)
+ * A matrix [rows, cols] (the [Out, In] layouts above) is held as one 4-bit code per weight and,
+ * for every `group` consecutive columns of a row, a bf16 scale s:
+ *   w[n, k] = s[n, k / group] * v,   v = code - 8       MOE_W4_INT4
+ *                                    v = code - z       MOE_W4_INT4_ZP (z: the group's zero point, 0 .. 127)
+ *                                    v = sign * {0, 0.5, 1, 1.5, 2, 3, 4, 6}[code & 7]  MOE_W4_E2M1
+ *                                                       (sign: bit 3 of the code)
+ * group is 32, 64 or 128 and divides cols.
+ * Products use v exactly and apply the scale to each group's fp32 sum in fp32 (below 256 tokens
+ * in the layer and the linear layer; from there on the tensor-core path multiplies by s * v
+ * rounded once to bf16).
+ * Packed form (moe_w4_size bytes, 16-byte aligned): matrices one after another, each a sequence
+ * of strips of 16 rows (layout MOE_W4_ROWS: rows 16j .. 16j+15; MOE_W4_GATE_UP, for the merged
+ * [2I, H] tensors: gate rows 8j .. 8j+7, then the matching up rows I+8j .. I+8j+7); a strip is a
+ * sequence of records of 128 columns:
+ *   1024 bytes of codes: little-endian 32-bit words [r / 8][r % 8][t][c] (r the strip row, t and
+ *     c = 0 .. 3); a word holds columns 32c + 8t + e, e = 0 .. 7: even e in its low half, odd e in
+ *     its high half, as the (e / 2)-th code of that half. INT4, INT4_ZP: code i in bits 4i .. 4i+3.
+ *     E2M1: the sign bits of codes 0 .. 3 in bits 15, 12, 9, 14 and their other three bits, high to
+ *     low, in bits (8, 7, 6), (5, 4, 3), (2, 1, 0), (13, 10, 11)
+ *   16 x (128 / group) scales [r][group], bf16
+ *   16 x (128 / group) zero points [r][group], bytes (INT4_ZP only)
+ * Rows and columns past the matrix have codes of value 0, scale 0 and zero point 0. */
+typedef enum { MOE_W4_INT4 = 0, MOE_W4_INT4_ZP = 1, MOE_W4_E2M1 = 2 } moe_w4_codes;
+typedef enum { MOE_W4_ROWS = 0, MOE_W4_GATE_UP = 1 } moe_w4_layout;
+typedef struct {
+    int32_t format; /* moe_w4_codes */
+    int32_t group;  /* columns to a scale: 32, 64 or 128 */
+} moe_w4_format;
+
+/* Bytes of n packed matrices [rows, cols]; 0 when the format or shape is not supported:
+ * n >= 0, rows >= 1, 32 <= cols <= 65536, cols % group == 0, rows * cols < 2^40 / max(n, 1). */
+size_t moe_w4_size(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols);
+
+/* Quantises n bf16 matrices w [n, rows, cols] into packed form. Per group, in fp32 with correctly
+ * rounded divisions and ties to even:
+ *   INT4     s = bf16(max|w| / 7), code = clamp(rint(w / s), -8, 7) + 8
+ *   INT4_ZP  over the values and 0: s = bf16(max / 15 - min / 15), z = min(rint(-min / s), 15),
+ *            code = clamp(rint(w / s) + z, 0, 15)
+ *   E2M1     s = bf16(max|w| / 6), code = the nearest of the format's values to w / s
+ * A group whose scale rounds to 0 is stored as zeros; one that holds a NaN or an infinity gets a
+ * NaN scale, so every product with it is NaN. MOE_W4_GATE_UP needs rows % 16 == 0.
+ * n = 0 is a no-op. Errors: MOE_ERR_INVALID_ARG (NULL, unknown format or layout, overlapping
+ * buffers), MOE_ERR_UNSUPPORTED_SHAPE, MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE_TOO_SMALL when
+ * packed_bytes < moe_w4_size. A product may follow on the same stream without any other work
+ * between (these calls order their writes before the early reads described above). */
+moe_status moe_w4_quantize(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols, int32_t layout, const void* w,
+                           void* packed, size_t packed_bytes, void* stream);
+
+/* Packs a checkpoint's codes: codes [n, rows, cols / 2] bytes (even column in the low nibble),
+ * scales [n, rows, cols / group] bf16, zeros [n, rows, cols / group] bytes (INT4_ZP only, else
+ * NULL; bit 7 is ignored). Otherwise as moe_w4_quantize. */
+moe_status moe_w4_pack(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols, int32_t layout, const void* codes,
+                       const void* scales, const void* zeros, void* packed, size_t packed_bytes, void* stream);
+
+/* The weights a packed form stands for: w [n, rows, cols] bf16, s * v rounded once. */
+moe_status moe_w4_dequantize(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols, int32_t layout,
+                             const void* packed, size_t packed_bytes, void* w, void* stream);
+
+/* Linear layer on packed weights (layout MOE_W4_ROWS, one matrix [N, K]):
+ *   out[t, n] = bf16( sum_k x[t, k] * w[n, k] + bias[n] )      fp32 sums in a fixed order
+ *   x [T, K], bias [N] or NULL, out [T, N], all bf16 (bias 2-byte aligned); out must not overlap x.
+ * T = 0 is a no-op; T * N and T * K < 2^40. The workspace (moe_w4_linear_workspace_size bytes,
+ * zero-filled once by moe_workspace_init) holds the error word of moe_last_device_error; calls
+ * that may overlap in time need one each. x, bias, the weights and the workspace are read after
+ * the previous kernel on `stream` is complete. */
+size_t moe_w4_linear_workspace_size(const moe_w4_format* f, int32_t T, int32_t N, int32_t K);
+moe_status moe_w4_linear(const moe_w4_format* f, int32_t T, int32_t N, int32_t K, const void* x, const void* packed,
+                         size_t packed_bytes, const void* bias, void* out, void* workspace, size_t ws_bytes,
+                         void* stream);
+
+/* moe_forward with the experts' weights packed: w->gate_up (E matrices [2I, H]) and
+ * w->shared_gate_up in layout MOE_W4_GATE_UP, w->down (E matrices [H, I]) and w->shared_down in
+ * layout MOE_W4_ROWS, all in format f; router_w, router_b and shared_gate are bf16 as ever. Same
+ * dims (with I and Is multiples of f->group), flags, workspace (moe_workspace_size), taps and
+ * errors as moe_forward. */
+moe_status moe_forward_w4(const moe_dims* d, const moe_w4_format* f, const void* x, const moe_weights* w,
+                          const void* residual, void* out, void* workspace, size_t ws_bytes, void* stream);
+
 /* RMSNorm of the pre-MoE norm ("RMSNorm -> MoE FFN -> +residual", "Qwen3.6-35B-A3B --
  * Architecture Overview", Stage 2; "Qwen3.6 35B-A3B", Blocks: RmsNorm):
  *   xn[t,h] = bf16( x[t,h] / sqrt(mean_h x[t,h]^2 + eps) * gamma[h] )   (fp32 arithmetic)
@@ -218,7 +299,9 @@ enum {
     MOE_KERNEL_ROUTER_STATS = 13,   /* load-balancing statistics (moe_router_stats) */
     MOE_KERNEL_FETCH_EXPERTS = 14,  /* touched experts copied from host memory (moe_forward_host_experts) */
     MOE_KERNEL_COPY_ROWS = 15,      /* token rows to or from mapped host memory (moe_forward_host_io) */
-    MOE_KERNEL_COUNT = 16
+    MOE_KERNEL_W4_PACK = 16,        /* quantising, packing, dequantising 4-bit weights */
+    MOE_KERNEL_W4_LINEAR = 17,      /* moe_w4_linear                                */
+    MOE_KERNEL_COUNT = 18
 };
 
 /* Benchmarking aid. While set, every launch of `kernel` made by this library records

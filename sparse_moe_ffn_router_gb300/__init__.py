@@ -11,8 +11,14 @@ from .binding import (  # noqa: F401
     FLAG_BF16_SCORES,
     TEST_SUPPRESS_SCORE,
     TEST_SUPPRESS_STAGE,
+    W4_E2M1,
+    W4_GATE_UP,
+    W4_INT4,
+    W4_INT4_ZP,
+    W4_ROWS,
     ForwardHostIO,
     MoEError,
+    W4Format,
     Weights,
     library_path,
     load_library,
@@ -28,8 +34,16 @@ from .binding import (  # noqa: F401
     moe_route,
     moe_route_noalloc,
     moe_router_stats,
+    moe_forward_w4,
+    moe_w4_dequantize,
+    moe_w4_linear,
+    moe_w4_pack,
+    moe_w4_quantize,
+    moe_w4_size,
     moe_workspace_init,
     moe_workspace_size,
     moe_workspace_tap,
+    new_w4,
+    new_w4_linear_workspace,
     new_workspace,
 )

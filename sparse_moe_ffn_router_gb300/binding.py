@@ -20,11 +20,12 @@ MOE_STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHA
 EXPORTED = ["moe_workspace_size", "moe_workspace_init", "moe_route", "moe_forward", "moe_rmsnorm",
             "moe_last_device_error", "moe_workspace_tap", "moe_set_trace", "moe_launch_count", "moe_route_noalloc", "moe_status_string",
             "moe_router_stats", "moe_expert_shadow_size", "moe_forward_host_experts", "moe_forward_host_io",
-            "moe_test_set_wait"]
+            "moe_test_set_wait", "moe_w4_size", "moe_w4_quantize", "moe_w4_pack", "moe_w4_dequantize",
+            "moe_w4_linear_workspace_size", "moe_w4_linear", "moe_forward_w4"]
 KERNELS = {"router_scores": 0, "router_topk": 1, "dispatch_local": 2, "dispatch_scan": 3, "dispatch_scatter": 4,
            "gate_up": 5, "down": 6, "combine": 7, "rmsnorm": 8, "shared_gate": 9, "gather": 10, "gemm_plan": 11,
            "decode_fused": 12, "router_stats": 13, "fetch_experts": 14,
-           "copy_rows": 15}
+           "copy_rows": 15, "w4_pack": 16, "w4_linear": 17}
 
 
 # moe_dims.flags: router and shared-gate scores rounded to bf16 before ranking and sigmoid
@@ -32,6 +33,19 @@ FLAG_BF16_SCORES = 1
 # moe_test_set_wait: the signal held back so that a bounded device wait runs out
 TEST_SUPPRESS_SCORE = 1
 TEST_SUPPRESS_STAGE = 2
+
+
+# moe_w4_format.format and the layout of a packed matrix
+W4_INT4 = 0
+W4_INT4_ZP = 1
+W4_E2M1 = 2
+W4_ROWS = 0
+W4_GATE_UP = 1
+
+
+class W4Format(ctypes.Structure):
+    """moe_w4_format: the codes (W4_INT4, W4_INT4_ZP, W4_E2M1) and the columns to a scale (32, 64, 128)."""
+    _fields_ = [("format", ctypes.c_int32), ("group", ctypes.c_int32)]
 
 
 class Dims(ctypes.Structure):
@@ -119,6 +133,21 @@ def load_library(build_if_missing: bool = True):
             lib.moe_forward_host_experts.argtypes = [D, P, W, P, P, P, S, P, S, P]
             lib.moe_forward_host_io.restype = st
             lib.moe_forward_host_io.argtypes = [D, P, W, P, P, P, P, P, S, P]
+            F, I32 = ctypes.POINTER(W4Format), ctypes.c_int32
+            lib.moe_w4_size.restype = S
+            lib.moe_w4_size.argtypes = [F, I32, I32, I32]
+            lib.moe_w4_quantize.restype = st
+            lib.moe_w4_quantize.argtypes = [F, I32, I32, I32, I32, P, P, S, P]
+            lib.moe_w4_pack.restype = st
+            lib.moe_w4_pack.argtypes = [F, I32, I32, I32, I32, P, P, P, P, S, P]
+            lib.moe_w4_dequantize.restype = st
+            lib.moe_w4_dequantize.argtypes = [F, I32, I32, I32, I32, P, S, P, P]
+            lib.moe_w4_linear_workspace_size.restype = S
+            lib.moe_w4_linear_workspace_size.argtypes = [F, I32, I32, I32]
+            lib.moe_w4_linear.restype = st
+            lib.moe_w4_linear.argtypes = [F, I32, I32, I32, P, P, S, P, P, P, S, P]
+            lib.moe_forward_w4.restype = st
+            lib.moe_forward_w4.argtypes = [D, F, P, W, P, P, P, S, P]
             lib.moe_test_set_wait.restype = st
             lib.moe_test_set_wait.argtypes = [ctypes.c_uint64, ctypes.c_int]
             lib.moe_status_string.restype = ctypes.c_char_p
@@ -296,6 +325,103 @@ class ForwardHostIO:
         n = self._nbytes
         _check(self._fn(self._fixed[0], _ptr_cpu(x, n), self._fixed[1], _ptr_cpu(residual, n), _ptr_cpu(out, n),
                         *self._staging), "moe_forward_host_io")
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def _bf16(t, what: str):
+    if t is not None and t.dtype != torch.bfloat16:
+        raise TypeError(f"{what} must be bfloat16, got {t.dtype}")
+    return _ptr(t)
+
+
+def moe_w4_size(fmt: W4Format, rows: int, cols: int, n: int = 1) -> int:
+    """Bytes of n packed 4-bit matrices [rows, cols] (0 when the format or shape is not supported)."""
+    return int(load_library().moe_w4_size(ctypes.byref(fmt), int(n), int(rows), int(cols)))
+
+
+def new_w4(fmt: W4Format, rows: int, cols: int, n: int = 1, device="cuda") -> torch.Tensor:
+    """An uninitialised uint8 CUDA tensor [n, bytes of one packed matrix]."""
+    b = moe_w4_size(fmt, rows, cols, 1)
+    if b == 0 or n < 0:
+        raise MoEError(2, "moe_w4_size")
+    return torch.empty(int(n), b, dtype=torch.uint8, device=device)
+
+
+def _matrices(t) -> tuple[int, int, int]:
+    if t.dim() not in (2, 3):
+        raise ValueError("weights are [rows, cols] or [n, rows, cols]")
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+def moe_w4_quantize(fmt: W4Format, w, packed, layout: int = W4_ROWS, stream=None):
+    """packed = the 4-bit form of the bf16 weights w [rows, cols] or [n, rows, cols]."""
+    n, rows, cols = _matrices(w)
+    _check(load_library().moe_w4_quantize(ctypes.byref(fmt), n, rows, cols, int(layout), _bf16(w, "w"), _ptr(packed),
+                                          _nbytes(packed), _stream(stream)), "moe_w4_quantize")
+
+
+def moe_w4_pack(fmt: W4Format, codes, scales, zeros, packed, layout: int = W4_ROWS, stream=None):
+    """packed = a checkpoint's codes [.., rows, cols / 2] uint8 (even column in the low nibble), scales
+    [.., rows, cols / group] bf16 and zero points [.., rows, cols / group] uint8 (or None)."""
+    n, rows, half = _matrices(codes)
+    groups = (*codes.shape[:-1], 2 * half // fmt.group if fmt.group > 0 else 0)
+    if codes.dtype != torch.uint8 or (zeros is not None and zeros.dtype != torch.uint8):
+        raise TypeError("codes and zeros must be uint8")
+    if tuple(scales.shape) != groups or (zeros is not None and tuple(zeros.shape) != groups):
+        raise ValueError(f"scales and zeros must be {list(groups)}")
+    _check(load_library().moe_w4_pack(ctypes.byref(fmt), n, rows, 2 * half, int(layout), _ptr(codes),
+                                      _bf16(scales, "scales"), _ptr(zeros), _ptr(packed), _nbytes(packed),
+                                      _stream(stream)), "moe_w4_pack")
+
+
+def moe_w4_dequantize(fmt: W4Format, packed, w, layout: int = W4_ROWS, stream=None):
+    """w [rows, cols] or [n, rows, cols] = the bf16 weights the packed form stands for."""
+    n, rows, cols = _matrices(w)
+    _check(load_library().moe_w4_dequantize(ctypes.byref(fmt), n, rows, cols, int(layout), _ptr(packed),
+                                            _nbytes(packed), _bf16(w, "w"), _stream(stream)), "moe_w4_dequantize")
+
+
+def new_w4_linear_workspace(fmt: W4Format, T: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    """A zero-filled uint8 device workspace for moe_w4_linear at these sizes."""
+    n = int(load_library().moe_w4_linear_workspace_size(ctypes.byref(fmt), int(T), int(N), int(K)))
+    if n == 0:
+        raise MoEError(2, "moe_w4_linear_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def moe_w4_linear(fmt: W4Format, x, packed, bias, out, workspace, stream=None):
+    """out [T, N] = x [T, K] . W^T + bias, with W [N, K] packed (layout W4_ROWS)."""
+    if x.dim() != 2 or out.dim() != 2 or x.shape[0] != out.shape[0]:
+        raise ValueError("x is [T, K] and out [T, N]")
+    T, K = x.shape
+    N = out.shape[1]
+    if bias is not None and tuple(bias.shape) != (N,):
+        raise ValueError(f"bias must be [{N}]")
+    _check(load_library().moe_w4_linear(ctypes.byref(fmt), T, N, K, _bf16(x, "x"), _ptr(packed), _nbytes(packed),
+                                        _bf16(bias, "bias"), _bf16(out, "out"), _ptr(workspace), _nbytes(workspace),
+                                        _stream(stream)), "moe_w4_linear")
+
+
+def moe_forward_w4(dims, fmt: W4Format, x, weights: Weights, residual, out, workspace, stream=None):
+    """moe_forward with weights.gate_up, down, shared_gate_up and shared_down in packed 4-bit form
+    (uint8 tensors of moe_w4_size bytes; gate_up layouts W4_GATE_UP, down layouts W4_ROWS)."""
+    d = _dims(dims)
+    need = {"gate_up": (2 * d.I, d.H, d.E), "down": (d.H, d.I, d.E), "shared_gate_up": (2 * d.Is, d.H, 1),
+            "shared_down": (d.H, d.Is, 1)}
+    for name, (rows, cols, n) in need.items():
+        t = getattr(weights, name)
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{name} must be packed 4-bit weights (uint8)")
+        if _nbytes(t) < moe_w4_size(fmt, rows, cols, n):
+            raise ValueError(f"{name} holds {_nbytes(t)} bytes, {n} packed [{rows}, {cols}] need "
+                             f"{moe_w4_size(fmt, rows, cols, n)}")
+    w = weights.to_c()
+    _check(load_library().moe_forward_w4(ctypes.byref(d), ctypes.byref(fmt), _ptr(x), ctypes.byref(w), _ptr(residual),
+                                         _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "moe_forward_w4")
 
 
 def moe_rmsnorm(dims, x, gamma, eps: float, xn, stream=None):

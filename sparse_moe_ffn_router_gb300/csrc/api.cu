@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "launch.h"
+#include "w4.cuh"
 
 namespace moe {
 
@@ -410,6 +411,132 @@ extern "C" moe_status moe_forward_host_experts(const moe_dims* d, const void* x,
     a.gate_up = sgu;
     a.down = sdn;
     if (e == cudaSuccess) e = launch_after_routing(a, s);
+    return cuda_status(e);
+}
+
+// ---------------------------------------------------------------------------------------
+// packed 4-bit weights
+
+namespace {
+
+bool w4_format_known(const moe_w4_format* f) {
+    return f && (f->format == MOE_W4_INT4 || f->format == MOE_W4_INT4_ZP || f->format == MOE_W4_E2M1) &&
+           (f->group == 32 || f->group == 64 || f->group == 128);
+}
+
+bool w4_shape(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols) {
+    if (n < 0 || rows < 1 || cols < 32 || cols > 65536 || cols % f->group) return false;
+    return (int64_t)rows * cols < ((int64_t)1 << 40) / (n > 0 ? n : 1);
+}
+
+// Checks shared by quantise, pack and dequantise. *empty: nothing to do.
+moe_status w4_check(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols, int32_t layout, const void* packed,
+                    size_t packed_bytes, bool* empty) {
+    if (!w4_format_known(f) || (layout != MOE_W4_ROWS && layout != MOE_W4_GATE_UP) || n < 0) return MOE_ERR_INVALID_ARG;
+    if (!w4_shape(f, n, rows, cols) || (layout == MOE_W4_GATE_UP && rows % 16)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    *empty = n == 0;
+    if (*empty) return MOE_OK;
+    if (!packed) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(packed)) return MOE_ERR_MISALIGNED;
+    return packed_bytes < moe_w4_size(f, n, rows, cols) ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+}
+
+}  // namespace
+
+extern "C" size_t moe_w4_size(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols) {
+    if (!w4_format_known(f) || !w4_shape(f, n, rows, cols)) return 0;
+    return (size_t)n * w4_matrix_bytes(f->format, f->group, rows, cols);
+}
+
+extern "C" moe_status moe_w4_quantize(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols, int32_t layout,
+                                      const void* w, void* packed, size_t packed_bytes, void* stream) {
+    bool empty = false;
+    const moe_status st = w4_check(f, n, rows, cols, layout, packed, packed_bytes, &empty);
+    if (st != MOE_OK || empty) return st;
+    if (!w) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(w)) return MOE_ERR_MISALIGNED;
+    if (overlap(w, (size_t)n * rows * cols * 2, packed, moe_w4_size(f, n, rows, cols))) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_w4_quantize(*f, n, rows, cols, layout == MOE_W4_GATE_UP, (const bf16*)w, (uint8_t*)packed,
+                                          sm_count(), (cudaStream_t)stream));
+}
+
+extern "C" moe_status moe_w4_pack(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols, int32_t layout,
+                                  const void* codes, const void* scales, const void* zeros, void* packed,
+                                  size_t packed_bytes, void* stream) {
+    bool empty = false;
+    const moe_status st = w4_check(f, n, rows, cols, layout, packed, packed_bytes, &empty);
+    if (st != MOE_OK || empty) return st;
+    if (!codes || !scales || (zeros != nullptr) != (f->format == MOE_W4_INT4_ZP)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned16(scales) || (zeros && !aligned16(zeros))) return MOE_ERR_MISALIGNED;
+    const size_t bytes = moe_w4_size(f, n, rows, cols), groups = (size_t)n * rows * (cols / f->group);
+    if (overlap(codes, (size_t)n * rows * cols / 2, packed, bytes) || overlap(scales, groups * 2, packed, bytes) ||
+        (zeros && overlap(zeros, groups, packed, bytes)))
+        return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_w4_pack(*f, n, rows, cols, layout == MOE_W4_GATE_UP, (const uint8_t*)codes,
+                                      (const bf16*)scales, (const uint8_t*)zeros, (uint8_t*)packed, sm_count(),
+                                      (cudaStream_t)stream));
+}
+
+extern "C" moe_status moe_w4_dequantize(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols, int32_t layout,
+                                        const void* packed, size_t packed_bytes, void* w, void* stream) {
+    bool empty = false;
+    const moe_status st = w4_check(f, n, rows, cols, layout, packed, packed_bytes, &empty);
+    if (st != MOE_OK || empty) return st;
+    if (!w) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(w)) return MOE_ERR_MISALIGNED;
+    if (overlap(w, (size_t)n * rows * cols * 2, packed, moe_w4_size(f, n, rows, cols))) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_w4_dequantize(*f, n, rows, cols, layout == MOE_W4_GATE_UP, (const uint8_t*)packed, (bf16*)w,
+                                            sm_count(), (cudaStream_t)stream));
+}
+
+extern "C" size_t moe_w4_linear_workspace_size(const moe_w4_format* f, int32_t T, int32_t N, int32_t K) {
+    if (!w4_format_known(f) || T < 0 || !w4_shape(f, 1, N, K)) return 0;
+    return align256(sizeof(WsHeader));
+}
+
+extern "C" moe_status moe_w4_linear(const moe_w4_format* f, int32_t T, int32_t N, int32_t K, const void* x,
+                                    const void* packed, size_t packed_bytes, const void* bias, void* out, void* workspace,
+                                    size_t ws_bytes, void* stream) {
+    if (!w4_format_known(f) || T < 0) return MOE_ERR_INVALID_ARG;
+    if (!w4_shape(f, 1, N, K) || (int64_t)T * N >= (int64_t)1 << 40 || (int64_t)T * K >= (int64_t)1 << 40)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MOE_OK;
+    if (!x || !packed || !out || !workspace) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(packed) || !aligned16(out) || !aligned16(workspace) || ((uintptr_t)bias & 1u))
+        return MOE_ERR_MISALIGNED;
+    if (packed_bytes < moe_w4_size(f, 1, N, K) || ws_bytes < moe_w4_linear_workspace_size(f, T, N, K))
+        return MOE_ERR_WORKSPACE_TOO_SMALL;
+    const size_t xb = (size_t)T * K * 2, ob = (size_t)T * N * 2;
+    if (overlap(x, xb, out, ob) || overlap(packed, packed_bytes, out, ob) || (bias && overlap(bias, (size_t)N * 2, out, ob)))
+        return MOE_ERR_INVALID_ARG;
+    W4LinearArgs l = {};
+    l.w = (const uint8_t*)packed;
+    l.x = (const bf16*)x;
+    l.bias = (const bf16*)bias;
+    l.out = (bf16*)out;
+    l.T = T; l.N = N; l.K = K;
+    l.num_sms = sm_count();
+    l.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    l.err = &((WsHeader*)workspace)->err;
+    return cuda_status(launch_w4_linear(*f, l, (cudaStream_t)stream));
+}
+
+extern "C" moe_status moe_forward_w4(const moe_dims* d, const moe_w4_format* f, const void* x, const moe_weights* w,
+                                     const void* residual, void* out, void* workspace, size_t ws_bytes, void* stream) {
+    if (!w4_format_known(f)) return MOE_ERR_INVALID_ARG;
+    Plan p;
+    LayerArgs a;
+    moe_status st = prepare(d, x, w, workspace, ws_bytes, &p, &a);
+    if (st != MOE_OK) return st;
+    if (d->I % f->group || d->Is % f->group) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (d->T == 0) return MOE_OK;
+    st = check_output(d, x, residual, out);
+    if (st != MOE_OK) return st;
+    a.residual = (const bf16*)residual;
+    a.out = (bf16*)out;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = launch_routing(a, s);
+    if (e == cudaSuccess) e = launch_w4_experts(a, *f, s);
     return cuda_status(e);
 }
 

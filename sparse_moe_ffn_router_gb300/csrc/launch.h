@@ -120,6 +120,27 @@ cudaError_t launch_decode_fused(const LayerArgs& a, cudaStream_t s);
 cudaError_t launch_stream_experts(const LayerArgs& a, cudaStream_t s);
 cudaError_t launch_dispatch(const LayerArgs& a, cudaStream_t s);
 cudaError_t launch_experts(const LayerArgs& a, cudaStream_t s);
+
+// Packed 4-bit weights (w4.cuh).
+struct W4LinearArgs {
+    const uint8_t* w;   // packed [N, K]
+    const bf16* x;      // [T, K]
+    const bf16* bias;   // [N] or NULL
+    bf16* out;          // [T, N]
+    int T, N, K;
+    int num_sms;
+    uint64_t wait_ns;
+    uint32_t* err;
+};
+cudaError_t launch_w4_quantize(const moe_w4_format& f, int n, int rows, int cols, bool gate_up, const bf16* w,
+                               uint8_t* packed, int num_sms, cudaStream_t s);
+cudaError_t launch_w4_pack(const moe_w4_format& f, int n, int rows, int cols, bool gate_up, const uint8_t* codes,
+                           const bf16* scales, const uint8_t* zeros, uint8_t* packed, int num_sms, cudaStream_t s);
+cudaError_t launch_w4_dequantize(const moe_w4_format& f, int n, int rows, int cols, bool gate_up, const uint8_t* packed,
+                                 bf16* w, int num_sms, cudaStream_t s);
+cudaError_t launch_w4_linear(const moe_w4_format& f, const W4LinearArgs& l, cudaStream_t s);
+// Gate_up, down and combine of a layer whose expert weights are packed (a.gate_up .. a.sd).
+cudaError_t launch_w4_experts(const LayerArgs& a, const moe_w4_format& f, cudaStream_t s);
 cudaError_t launch_rmsnorm(const bf16* x, const bf16* gamma, float eps, bf16* xn, int T, int H, cudaStream_t s);
 
 }  // namespace moe

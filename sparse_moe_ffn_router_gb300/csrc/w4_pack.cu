@@ -1,0 +1,297 @@
+// w4_pack.cu -- making and reading packed 4-bit weights (layout in w4.cuh): quantising bf16
+// weights, packing a checkpoint's codes, and writing packed weights out as bf16.
+//
+// All three pass over the data once and are bound by HBM: quantising reads 2 bytes and writes
+// 0.52 to 0.59 bytes a weight, dequantising the reverse. A warp takes one record (16 rows by 128
+// columns): lane 4g + t holds, of rows g and g + 8, the columns 32 c + 8 t + 0 .. 7 of every
+// 32-column piece c -- the order of the packed words, so its codes leave as two 16-byte stores
+// that the warp makes contiguous, and its weights come in 16 bytes a piece, four lanes to a
+// 64-byte run of a row. A group's largest weight is a maximum over the lane's 8 values and the
+// four lanes of a row (two shuffles).
+#include "launch.h"
+#include "w4.cuh"
+
+namespace moe {
+
+namespace {
+
+struct W4PackArgs {
+    const bf16* w;         // quantise: [n, rows, cols]
+    bf16* out;             // dequantise: [n, rows, cols]
+    const uint8_t* codes;  // pack: [n, rows, cols / 2], even column in the low nibble
+    const bf16* scales;    // pack: [n, rows, cols / G]
+    const uint8_t* zeros;  // pack: [n, rows, cols / G] (INT4_ZP)
+    uint8_t* packed;
+    int n, rows, cols, gate_up;
+};
+
+// Matrix row of strip row r.
+__device__ __forceinline__ int w4_row(const W4PackArgs& a, int strip, int r) {
+    if (!a.gate_up) return strip * 16 + r;
+    return r < 8 ? strip * 8 + r : (a.rows >> 1) + strip * 8 + (r - 8);
+}
+
+// A code's place in its 16-bit half: i-th code (0 .. 3) of the half.
+template <int FMT>
+__device__ __forceinline__ uint32_t w4_place(uint32_t code, int i) {
+    if (FMT != MOE_W4_E2M1) return code << (4 * i);
+    const uint32_t s = code >> 3, m = code & 7u;
+    if (i == 0) return (s << 15) | (m << 6);
+    if (i == 1) return (s << 12) | (m << 3);
+    if (i == 2) return (s << 9) | m;
+    return (s << 14) | ((m >> 2) << 13) | (((m >> 1) & 1u) << 10) | ((m & 1u) << 11);
+}
+
+// E2M1 code of a value: nearest, halfway cases to the even code, at most 6.
+__device__ __forceinline__ uint32_t e2m1_code(float v) {
+    const float m = fabsf(v);
+    const uint32_t c = (m > 0.25f) + (m >= 0.75f) + (m > 1.25f) + (m >= 1.75f) + (m > 2.5f) + (m >= 3.5f) + (m > 5.0f);
+    return c | (v < 0.f ? 8u : 0u);
+}
+
+__device__ __forceinline__ void st_record(uint8_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
+
+// Stores the scales (and zero points) of one row of a record: lane t = 0 of the row's four.
+template <int FMT, int G>
+__device__ __forceinline__ void st_meta(uint8_t* rec, int row, const bf16 (&s)[W4Rec<FMT, G>::kGroups],
+                                        const uint32_t (&z)[W4Rec<FMT, G>::kGroups]) {
+    constexpr int N = W4Rec<FMT, G>::kGroups;
+    bf16* sp = reinterpret_cast<bf16*>(rec + W4Rec<FMT, G>::kScales) + row * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        sp[i] = s[i];
+        if (FMT == MOE_W4_INT4_ZP) rec[W4Rec<FMT, G>::kZeros + row * N + i] = (uint8_t)z[i];
+    }
+}
+
+// One row of a record quantised by its four lanes. Per group: scale s = bf16(max|w| / 7) for
+// INT4 (/ 6 for E2M1), or bf16(max / 15 - min / 15) over the values and 0 for INT4_ZP with zero
+// point rint(-min / s); codes are the nearest value of w / s (halfway to even). All divisions are
+// fp32, correctly rounded. A group of zeros has scale 0; one with a NaN or an infinity has scale
+// NaN and codes of value 0, so every product with it is NaN.
+template <int FMT, int G>
+__device__ __forceinline__ void quantize_row(const W4PackArgs& a, const bf16* src, int k0, int t, bool live, uint32_t (&words)[4],
+                             bf16 (&sc)[W4Rec<FMT, G>::kGroups], uint32_t (&zp)[W4Rec<FMT, G>::kGroups]) {
+    constexpr int P = G / 32;  // 32-column pieces of a group
+    float v[4][8];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int k = k0 + 32 * c + 8 * t;
+        if (live && k < a.cols)
+            unpack8(ld_stream(src + k), v[c]);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[c][e] = 0.f;
+    }
+#pragma unroll
+    for (int gi = 0; gi < 4 / P; ++gi) {
+        float hi = 0.f, lo = 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int c = gi * P; c < (gi + 1) * P; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = v[c][e];
+                bad |= !(fabsf(x) < INFINITY);
+                if (FMT == MOE_W4_INT4_ZP) {
+                    hi = fmaxf(hi, x);
+                    lo = fminf(lo, x);
+                } else {
+                    hi = fmaxf(hi, fabsf(x));
+                }
+            }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            bad |= __shfl_xor_sync(0xffffffffu, (int)bad, o) != 0;
+        }
+        const float raw = FMT == MOE_W4_INT4_ZP ? __fsub_rn(__fdiv_rn(hi, 15.f), __fdiv_rn(lo, 15.f))
+                                                : __fdiv_rn(hi, FMT == MOE_W4_INT4 ? 7.f : 6.f);
+        const bf16 sb = __float2bfloat16_rn(raw);
+        const float s = __bfloat162float(sb);
+        const bool use = s > 0.f && !bad;
+        const float z = FMT == MOE_W4_INT4_ZP && use ? fminf(rintf(__fdiv_rn(-lo, s)), 15.f) : 0.f;
+        sc[gi] = bad ? __ushort_as_bfloat16(0x7fffu) : sb;
+        zp[gi] = (uint32_t)z;
+#pragma unroll
+        for (int c = gi * P; c < (gi + 1) * P; ++c) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float q = use ? __fdiv_rn(v[c][e], s) : 0.f;
+                uint32_t code;
+                if (FMT == MOE_W4_E2M1)
+                    code = e2m1_code(q);
+                else if (FMT == MOE_W4_INT4)
+                    code = (uint32_t)(int)(fminf(fmaxf(rintf(q), -8.f), 7.f) + 8.f);
+                else
+                    code = (uint32_t)(int)fminf(fmaxf(rintf(q) + z, 0.f), 15.f);
+                w |= w4_place<FMT>(code, e >> 1) << (16 * (e & 1));
+            }
+            words[c] = w;
+        }
+    }
+}
+
+// Codes, scales and zero points of one row of a record from a checkpoint's row-major tensors.
+template <int FMT, int G>
+__device__ __forceinline__ void pack_row(const W4PackArgs& a, int64_t row, int k0, int t, bool live, uint32_t (&words)[4],
+                         bf16 (&sc)[W4Rec<FMT, G>::kGroups], uint32_t (&zp)[W4Rec<FMT, G>::kGroups]) {
+    constexpr int N = W4Rec<FMT, G>::kGroups;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int k = k0 + 32 * c + 8 * t;
+        // eight codes in column order, four bits each; past the matrix: codes of value 0
+        uint32_t in = FMT == MOE_W4_INT4 ? 0x88888888u : 0u;
+        if (live && k < a.cols)
+            in = *reinterpret_cast<const uint32_t*>(a.codes + row * (a.cols / 2) + k / 2);
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w |= w4_place<FMT>((in >> (4 * e)) & 15u, e >> 1) << (16 * (e & 1));
+        words[c] = w;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int g = k0 / G + i;
+        const bool in = live && g < a.cols / G;
+        sc[i] = in ? a.scales[row * (a.cols / G) + g] : __float2bfloat16_rn(0.f);
+        zp[i] = FMT == MOE_W4_INT4_ZP && in ? a.zeros[row * (a.cols / G) + g] & 0x7fu : 0u;
+    }
+}
+
+template <int FMT, int G, bool QUANT>
+__global__ void __launch_bounds__(256) k_w4_pack(W4PackArgs a, int64_t records) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int R = (a.cols + kW4Cols - 1) / kW4Cols, S = (a.rows + kW4Strip - 1) / kW4Strip;
+    const int64_t stride = (int64_t)gridDim.x * 8;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < records; i += stride) {
+        const int64_t sg = i / R;
+        const int k0 = (int)(i - sg * R) * kW4Cols;
+        const int64_t m = sg / S;
+        const int strip = (int)(sg - m * S);
+        uint8_t* rec = a.packed + (size_t)i * W4Rec<FMT, G>::kBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = w4_row(a, strip, g + 8 * h);
+            const bool live = row < a.rows;
+            const int64_t grow = m * a.rows + row;
+            uint32_t words[4];
+            bf16 sc[W4Rec<FMT, G>::kGroups];
+            uint32_t zp[W4Rec<FMT, G>::kGroups];
+            if (QUANT)
+                quantize_row<FMT, G>(a, a.w + grow * a.cols, k0, t, live, words, sc, zp);
+            else
+                pack_row<FMT, G>(a, grow, k0, t, live, words, sc, zp);
+            st_record(rec + 512 * h + lane * 16, make_uint4(words[0], words[1], words[2], words[3]));
+            if (t == 0) st_meta<FMT, G>(rec, g + 8 * h, sc, zp);
+        }
+    }
+}
+
+template <int FMT, int G>
+__global__ void __launch_bounds__(256) k_w4_unpack(W4PackArgs a, int64_t records) {
+    constexpr int N = W4Rec<FMT, G>::kGroups;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int R = (a.cols + kW4Cols - 1) / kW4Cols, S = (a.rows + kW4Strip - 1) / kW4Strip;
+    const int64_t stride = (int64_t)gridDim.x * 8;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < records; i += stride) {
+        const int64_t sg = i / R;
+        const int k0 = (int)(i - sg * R) * kW4Cols;
+        const int64_t m = sg / S;
+        const int strip = (int)(sg - m * S);
+        const uint8_t* rec = a.packed + (size_t)i * W4Rec<FMT, G>::kBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = g + 8 * h, row = w4_row(a, strip, r);
+            if (row >= a.rows) continue;
+            const uint4 v = ld_stream(rec + 512 * h + lane * 16);
+            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+            bf16* dst = a.out + (m * a.rows + row) * a.cols + k0 + 8 * t;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (k0 + 32 * c + 8 * t >= a.cols) continue;
+                const int gi = c * 32 / G;
+                const float s = __bfloat162float(reinterpret_cast<const bf16*>(rec + W4Rec<FMT, G>::kScales)[r * N + gi]);
+                uint32_t bias = 0x43084308u;
+                if (FMT == MOE_W4_INT4_ZP) bias = 0x43004300u | (rec[W4Rec<FMT, G>::kZeros + r * N + gi] * 0x00010001u);
+                uint32_t p[4];
+                w4_decode<FMT>(words[c], bias, p);
+                uint4 o;  // s * v in fp32 (exact: 8 and at most 5 bits), rounded once to bf16
+                o.x = pack_bf16x2(s * bf_lo(p[0]), s * bf_hi(p[0]));
+                o.y = pack_bf16x2(s * bf_lo(p[1]), s * bf_hi(p[1]));
+                o.z = pack_bf16x2(s * bf_lo(p[2]), s * bf_hi(p[2]));
+                o.w = pack_bf16x2(s * bf_lo(p[3]), s * bf_hi(p[3]));
+                *reinterpret_cast<uint4*>(dst + 32 * c) = o;
+            }
+        }
+    }
+}
+
+// An ordinary launch after a kernel that wrote weights: it starts once that kernel is complete
+// and its memory visible, and whatever the library launches next starts after it, so a layer
+// call right after quantising may read the weights early (the ordering contract of moe.h).
+__global__ void k_w4_settle() {}
+
+enum { kOpQuantize, kOpPack, kOpUnpack };
+
+template <int FMT, int G>
+cudaError_t launch_pack(int op, const W4PackArgs& a, int64_t records, unsigned grid, cudaStream_t s) {
+    if (op == kOpQuantize)
+        MOE_LAUNCH(MOE_KERNEL_W4_PACK, s, (k_w4_pack<FMT, G, true><<<grid, 256, 0, s>>>(a, records)));
+    else if (op == kOpPack)
+        MOE_LAUNCH(MOE_KERNEL_W4_PACK, s, (k_w4_pack<FMT, G, false><<<grid, 256, 0, s>>>(a, records)));
+    else
+        MOE_LAUNCH(MOE_KERNEL_W4_PACK, s, (k_w4_unpack<FMT, G><<<grid, 256, 0, s>>>(a, records)));
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && op != kOpUnpack) {
+        MOE_LAUNCH(MOE_KERNEL_W4_PACK, s, (k_w4_settle<<<1, 32, 0, s>>>()));
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+cudaError_t launch(int op, int format, int group, const W4PackArgs& a, int num_sms, cudaStream_t s) {
+    const int64_t records = (int64_t)a.n * ((a.rows + kW4Strip - 1) / kW4Strip) * ((a.cols + kW4Cols - 1) / kW4Cols);
+    const int64_t want = (records + 7) / 8, cap = (int64_t)num_sms * 8;
+    const unsigned grid = (unsigned)(want < cap ? want : cap);
+#define MOE_W4_CASE(F, G) \
+    if (format == F && group == G) return launch_pack<F, G>(op, a, records, grid, s)
+    MOE_W4_CASE(MOE_W4_INT4, 32);
+    MOE_W4_CASE(MOE_W4_INT4, 64);
+    MOE_W4_CASE(MOE_W4_INT4, 128);
+    MOE_W4_CASE(MOE_W4_INT4_ZP, 32);
+    MOE_W4_CASE(MOE_W4_INT4_ZP, 64);
+    MOE_W4_CASE(MOE_W4_INT4_ZP, 128);
+    MOE_W4_CASE(MOE_W4_E2M1, 32);
+    MOE_W4_CASE(MOE_W4_E2M1, 64);
+    MOE_W4_CASE(MOE_W4_E2M1, 128);
+#undef MOE_W4_CASE
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_w4_quantize(const moe_w4_format& f, int n, int rows, int cols, bool gate_up, const bf16* w,
+                               uint8_t* packed, int num_sms, cudaStream_t s) {
+    W4PackArgs a = {};
+    a.w = w; a.packed = packed; a.n = n; a.rows = rows; a.cols = cols; a.gate_up = gate_up;
+    return launch(kOpQuantize, f.format, f.group, a, num_sms, s);
+}
+
+cudaError_t launch_w4_pack(const moe_w4_format& f, int n, int rows, int cols, bool gate_up, const uint8_t* codes,
+                           const bf16* scales, const uint8_t* zeros, uint8_t* packed, int num_sms, cudaStream_t s) {
+    W4PackArgs a = {};
+    a.codes = codes; a.scales = scales; a.zeros = zeros; a.packed = packed;
+    a.n = n; a.rows = rows; a.cols = cols; a.gate_up = gate_up;
+    return launch(kOpPack, f.format, f.group, a, num_sms, s);
+}
+
+cudaError_t launch_w4_dequantize(const moe_w4_format& f, int n, int rows, int cols, bool gate_up, const uint8_t* packed,
+                                 bf16* w, int num_sms, cudaStream_t s) {
+    W4PackArgs a = {};
+    a.packed = const_cast<uint8_t*>(packed); a.out = w; a.n = n; a.rows = rows; a.cols = cols; a.gate_up = gate_up;
+    return launch(kOpUnpack, f.format, f.group, a, num_sms, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,350 @@
+"""The 4-bit weight operators on the GPU against plain 64-bit forms (w4_reference.py), at the sizes
+where they can go wrong, with error bounds derived there."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import sparse_moe_ffn_router_gb300 as moe
+from tests import w4_reference as ref
+
+pytestmark = pytest.mark.gpu
+FG = [(f, g) for f in ref.FORMATS for g in (32, 64, 128)]
+
+
+def check(got, want, bound, what=""):
+    off = (got.double() - want).abs()
+    bad = ~(off <= bound)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} values off, worst {float((off / bound).max()):.2f} x the bound"
+
+
+# ---------------------------------------------------------------------------------------- packing
+
+def test_pack_layout_byte_by_byte():
+    """One record of each format against the layout of moe.h, bit by bit."""
+    for name, group in FG:
+        m = ref.matrices(name, group, 1, 16, 128, seed=3)
+        got = ref.pack(name, group, m)[0].cpu().tolist()
+        codes, scales, zeros = (None if t is None else t[0].cpu() for t in m)
+        per = 128 // group
+        for r in range(16):
+            for k in range(128):
+                c, t, e = k // 32, k % 32 // 8, k % 8
+                at = ((r // 8 * 8 + r % 8) * 4 + t) * 16 + c * 4 + 2 * (e & 1)
+                half, i = got[at] | got[at + 1] << 8, e // 2
+                if name == "e2m1":
+                    bits = [(15, 8, 7, 6), (12, 5, 4, 3), (9, 2, 1, 0), (14, 13, 10, 11)][i]
+                    code = sum(((half >> b) & 1) << s for b, s in zip(bits, (3, 2, 1, 0)))
+                else:
+                    code = half >> (4 * i) & 15
+                assert code == int(codes[r, k]), (name, group, r, k)
+            for i in range(per):
+                at = 1024 + 2 * (r * per + i)
+                assert got[at] | got[at + 1] << 8 == scales.view(torch.int16)[r, i].item() & 0xffff
+                if zeros is not None:
+                    assert got[1024 + 32 * per + r * per + i] == int(zeros[r, i])
+
+
+@pytest.mark.parametrize("name,group", FG)
+@pytest.mark.parametrize("n,rows,cols,layout", [(1, 16, 128, 0), (3, 32, 256, 1), (2, 1, 128, 0), (2, 37, 384, 0), (1, 48, 640, 1), (5, 19, 128 * 3, 0)])
+def test_pack_and_dequantize(name, group, n, rows, cols, layout):
+    m = ref.matrices(name, group, n, rows, cols, seed=rows + cols)
+    out = torch.full((n, rows, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_w4_dequantize(ref.fmt(name, group), ref.pack(name, group, m, layout), out, layout)
+    assert torch.equal(out.double(), ref.values(name, group, m).to(torch.bfloat16).double())
+
+
+@pytest.mark.parametrize("name,group", [(f, 32) for f in ref.FORMATS])
+@pytest.mark.parametrize("cols", [32, 96, 160])
+def test_columns_that_are_no_whole_record(name, group, cols):
+    m = ref.matrices(name, group, 2, 21, cols, seed=cols)
+    out = torch.empty(2, 21, cols, dtype=torch.bfloat16, device="cuda")
+    moe.moe_w4_dequantize(ref.fmt(name, group), ref.pack(name, group, m), out)
+    assert torch.equal(out.double(), ref.values(name, group, m).to(torch.bfloat16).double())
+
+
+@pytest.mark.parametrize("name,group", FG)
+@pytest.mark.parametrize("rows,cols,layout", [(32, 512, 1), (33, 384, 0), (1, 128, 0)])
+def test_quantize(name, group, rows, cols, layout):
+    g = torch.Generator().manual_seed(rows)
+    w = torch.randn(3, rows, cols, generator=g) * torch.exp(3 * torch.randn(3, rows, 1, generator=g))
+    w[0, 0, :group] = 0.0                                # a group of zeros
+    w[1, 0, :group] = w[1, 0, :group].abs()              # one sign only
+    w[2, 0, :group] = -w[2, 0, :group].abs()
+    w[0, -1, -group:] = torch.arange(group) % 16 * 0.25  # values halfway between codes
+    w = w.to(torch.bfloat16).cuda()
+    packed = moe.new_w4(ref.fmt(name, group), rows, cols, 3)
+    moe.moe_w4_quantize(ref.fmt(name, group), w, packed, layout)
+    want = ref.quantize(name, group, w)
+    assert torch.equal(packed, ref.pack(name, group, want, layout))
+
+
+@pytest.mark.parametrize("name", list(ref.FORMATS))
+def test_quantize_extreme_values(name):
+    """The largest and smallest finite weights, and a group with an infinity or a NaN."""
+    w = torch.zeros(1, 16, 128, dtype=torch.bfloat16, device="cuda")
+    big = torch.finfo(torch.bfloat16).max
+    w[0, 0, :32] = big
+    w[0, 1, :32] = -big
+    w[0, 1, 0] = big
+    w[0, 2, :32] = 2.0 ** -133  # the smallest subnormal: the scale rounds to it or to zero
+    w[0, 3, 0] = float("inf")
+    w[0, 4, 40] = float("nan")
+    f = ref.fmt(name, 32)
+    packed, out = moe.new_w4(f, 16, 128), torch.empty_like(w)
+    moe.moe_w4_quantize(f, w, packed)
+    moe.moe_w4_dequantize(f, packed, out)
+    out = out[0].float()
+    assert bool(out[3, :32].isnan().all()) and bool(out[4, 32:64].isnan().all())
+    out[3, :32] = 0
+    out[4, 32:64] = 0
+    # a step of the format at this scale; the largest value times the rounded scale may overflow bf16
+    step = {"int4": 1 / 14, "int4_zp": 1 / 15, "e2m1": 1 / 6}[name] * 1.01 + 2.0 ** -7
+    fine = out.isfinite()
+    assert bool((fine | (w[0].float().abs() == big)).all())
+    top = w[0].float().abs().amax(1, keepdim=True)
+    top[3:5] = 0
+    assert bool(((out - w[0].float().nan_to_num(0, 0, 0)).abs()[fine] <= (step * top + 2.0 ** -133).expand_as(out)[fine]).all())
+
+
+# ---------------------------------------------------------------------------------------- linear
+
+def run_linear(name, group, T, N, K, bias, seed=0, x=None):
+    m = ref.matrices(name, group, 1, N, K, seed=seed + N)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if x is None:
+        x = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
+    b = torch.randn(N, generator=g, device="cuda").to(torch.bfloat16) if bias else None
+    f = ref.fmt(name, group)
+    ws = moe.new_w4_linear_workspace(f, T, N, K)
+    out = torch.full((T + 1, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_w4_linear(f, x, ref.pack(name, group, m), b, out[:T], ws)
+    assert moe.moe_last_device_error(ws) == 0
+    assert bool((out[T] == 3.0).all())  # the row behind the last is left as it was
+    return x, ref.values(name, group, m)[0], b, out[:T]
+
+
+@pytest.mark.parametrize("name,group", FG)
+@pytest.mark.parametrize("T,N,K", [(1, 64, 128), (1, 2048, 2048), (3, 37, 384), (8, 1, 256), (9, 1003, 1408), (1, 500, 8192)])
+def test_linear(name, group, T, N, K):
+    x, w, b, out = run_linear(name, group, T, N, K, bias=T != 3)
+    check(out, *ref.linear(x, w, b))
+
+
+@pytest.mark.parametrize("name", list(ref.FORMATS))
+@pytest.mark.parametrize("T,N,K", [(1, 20, 32), (5, 33, 160), (2, 100, 1440), (17, 300, 2080), (70, 129, 96)])
+def test_linear_odd_columns(name, T, N, K):
+    x, w, b, out = run_linear(name, 32, T, N, K, bias=True)
+    check(out, *ref.linear(x, w, b))
+
+
+@pytest.mark.parametrize("name,group", [("int4", 128), ("int4_zp", 32), ("e2m1", 64)])
+@pytest.mark.parametrize("T,N,K", [(31, 512, 2048), (64, 1000, 1024), (129, 257, 640), (300, 384, 512), (777, 1100, 1920), (1024, 2048, 4096)])
+def test_linear_many_tokens(name, group, T, N, K):
+    x, w, b, out = run_linear(name, group, T, N, K, bias=N % 2 == 0)
+    want, bound = ref.linear(x, w, b)
+    if T >= 16:  # tensor-core path: each weight rounded once to bf16
+        bound = bound + ref.HALF * (x.double().abs() @ w.abs().T)
+    check(out, want, bound)
+
+
+@pytest.mark.parametrize("T", [1, 8, 40, 300])
+def test_linear_nonfinite_rows_stay_apart(T):
+    """NaN and infinities in one token's row reach that row's results only."""
+    x = torch.randn(T, 256, device="cuda").to(torch.bfloat16)
+    x[T // 2, 5] = float("nan")
+    x, w, b, out = run_linear("int4", 32, T, 70, 256, False, x=x)
+    keep = torch.arange(T, device="cuda") != T // 2
+    assert bool(out[T // 2].isnan().all()) and bool(out[keep].isfinite().all())
+    want, bound = ref.linear(x[keep], w, b)
+    check(out[keep], want, bound + ref.HALF * (x[keep].double().abs() @ w.abs().T))
+
+
+def test_linear_repeats_bit_for_bit_and_in_graphs():
+    f = ref.fmt("int4", 64)
+    for T in (1, 7, 33, 260):
+        m = ref.matrices("int4", 64, 1, 520, 1024, seed=T)
+        p = ref.pack("int4", 64, m)
+        x = torch.randn(T, 1024, device="cuda").to(torch.bfloat16)
+        ws, out = moe.new_w4_linear_workspace(f, T, 520, 1024), torch.empty(T, 520, dtype=torch.bfloat16, device="cuda")
+        moe.moe_w4_linear(f, x, p, None, out, ws)
+        first = out.clone()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            moe.moe_w4_linear(f, x, p, None, out, ws)
+        out.zero_()
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+
+
+def test_quantize_then_linear_on_one_stream():
+    """Weights written and used without any other work between."""
+    f = ref.fmt("e2m1", 32)
+    x = torch.randn(4, 2048, device="cuda").to(torch.bfloat16)
+    ws = moe.new_w4_linear_workspace(f, 4, 4096, 2048)
+    packed, out = moe.new_w4(f, 4096, 2048), torch.empty(4, 4096, dtype=torch.bfloat16, device="cuda")
+    for i in range(4):
+        w = torch.randn(4096, 2048, device="cuda").to(torch.bfloat16)
+        torch.cuda.synchronize()
+        moe.moe_w4_quantize(f, w, packed)
+        moe.moe_w4_linear(f, x, packed, None, out, ws)
+        back = torch.empty_like(w)
+        moe.moe_w4_dequantize(f, packed, back)
+        codes = ref.quantize("e2m1", 32, w[None])
+        check(out, *ref.linear(x, ref.values("e2m1", 32, codes)[0], None))
+
+
+# ---------------------------------------------------------------------------------------- layer
+
+class W4Layer:
+    def __init__(self, dims, name, group, seed, bias=False, device="cuda"):
+        T, H, E, K, I, Is = dims[:6]
+        self.dims, self.name, self.group = dims, name, group
+        g = torch.Generator(device=device).manual_seed(seed)
+        self.m = {"gate_up": ref.matrices(name, group, E, 2 * I, H, seed + 1), "down": ref.matrices(name, group, E, H, I, seed + 2),
+                  "shared_gate_up": ref.matrices(name, group, 1, 2 * Is, H, seed + 3),
+                  "shared_down": ref.matrices(name, group, 1, H, Is, seed + 4)}
+        self.v = {k: ref.values(name, group, t) for k, t in self.m.items()}
+        self.router_w = (torch.randn(E, H, generator=g, device=device) * 0.02).to(torch.bfloat16)
+        self.router_b = torch.randn(E, generator=g, device=device).to(torch.bfloat16) if bias else None
+        self.shared_gate = (torch.randn(1, H, generator=g, device=device) / H ** 0.5).to(torch.bfloat16)
+        self.x = torch.randn(T, H, generator=g, device=device).to(torch.bfloat16)
+        self.residual = torch.randn(T, H, generator=g, device=device).to(torch.bfloat16)
+        self.W = moe.Weights(self.router_w, self.router_b, *(ref.pack(name, group, self.m[k], k.endswith("gate_up"))
+                                                             for k in ("gate_up", "down", "shared_gate_up", "shared_down")),
+                             self.shared_gate)
+        # tokens whose scores nearly tie have two right answers: drawn again
+        for _ in range(50):
+            s = self.x.double() @ self.router_w.double().T + (0 if self.router_b is None else self.router_b.double())
+            top = s.sort(dim=1, descending=True).values[:, :K + 1]
+            bad = (top[:, :-1] - top[:, 1:]).amin(1) < 1e-3 if top.shape[1] > 1 else torch.zeros(T, dtype=torch.bool, device=device)
+            if not bool(bad.any()):
+                break
+            self.x[bad] = torch.randn(int(bad.sum()), H, generator=g, device=device).to(torch.bfloat16)
+
+    def reference(self, residual=True, gemm_tokens=256):
+        big = self.dims[0] >= gemm_tokens
+        return ref.layer(self.dims, self.x, self.router_w, self.router_b, self.shared_gate, self.v["gate_up"], self.v["down"],
+                         self.v["shared_gate_up"][0], self.v["shared_down"][0], self.residual if residual else None,
+                         weight_half=ref.HALF if big else 0.0, y_half=ref.HALF if big else 0.0)
+
+    def run(self, residual=True, ws=None, out=None):
+        f = ref.fmt(self.name, self.group)
+        ws = moe.new_workspace(self.dims) if ws is None else ws
+        out = torch.empty_like(self.x) if out is None else out
+        moe.moe_forward_w4(self.dims, f, self.x, self.W, self.residual if residual else None, out, ws)
+        assert moe.moe_last_device_error(ws) == 0
+        return out
+
+
+@pytest.mark.parametrize("name,group", FG)
+@pytest.mark.parametrize("T", [1, 2, 8, 33])
+def test_layer_tiny(name, group, T):
+    L = W4Layer((T, 512, 32, 4, 128, 128), name, group, seed=T)
+    check(L.run(), *L.reference())
+    check(L.run(residual=False), *L.reference(residual=False))
+
+
+@pytest.mark.parametrize("dims,name,group", [
+    ((1, 2048, 64, 8, 512, 512), "int4", 32), ((1, 2048, 256, 8, 512, 512), "e2m1", 32), ((1, 2048, 256, 8, 512, 512), "int4_zp", 128),
+    ((1, 2048, 16, 1, 512, 512), "int4", 64), ((8, 2048, 64, 8, 512, 512), "e2m1", 32), ((64, 2048, 64, 8, 512, 512), "int4_zp", 128),
+    ((255, 2048, 16, 2, 512, 512), "int4", 64), ((255, 128, 8, 8, 64, 64), "int4", 64), ((5, 1280, 21, 3, 192, 448), "int4", 64),
+    ((13, 384, 7, 7, 320, 64), "int4_zp", 32), ((3, 4096, 8, 2, 1024, 2048), "e2m1", 128), ((20, 128, 1, 1, 64, 2048), "int4", 32),
+    ((256, 512, 32, 4, 128, 128), "int4", 32), ((300, 2048, 32, 8, 512, 512), "e2m1", 64), ((777, 640, 11, 3, 192, 320), "int4_zp", 64),
+    ((1000, 128, 8, 2, 64, 64), "int4", 32), ((600, 2048, 256, 8, 512, 512), "int4", 128), ((512, 2304, 9, 8, 576, 128), "e2m1", 32)],
+    ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else str(v))
+def test_layer_shapes(dims, name, group):
+    L = W4Layer(dims, name, group, seed=sum(dims), bias=dims[2] % 2 == 1)
+    check(L.run(), *L.reference())
+
+
+@pytest.mark.parametrize("T", [1, 8, 40, 256])
+def test_layer_over_its_residual_repeated_and_in_graphs(T):
+    L = W4Layer((T, 2048, 32, 8, 512, 512), "int4", 32, seed=T)
+    want, bound = L.reference()
+    ws = moe.new_workspace(L.dims)
+    first = L.run(ws=ws)
+    check(first, want, bound)
+    for _ in range(3):
+        assert torch.equal(L.run(ws=ws), first)
+    over = L.residual.clone()
+    moe.moe_forward_w4(L.dims, ref.fmt("int4", 32), L.x, L.W, over, over, ws)
+    assert torch.equal(over, first)
+    out = torch.zeros_like(first)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for _ in range(3):
+            moe.moe_forward_w4(L.dims, ref.fmt("int4", 32), L.x, L.W, L.residual, out, ws)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first) and moe.moe_last_device_error(ws) == 0
+
+
+def test_layer_routes_as_moe_forward_does():
+    """Same workspace, same taps: ids, weights and shared gate equal moe_forward's on bf16 weights."""
+    T, H, E, K, I, Is = dims = (24, 512, 32, 4, 128, 128)
+    L = W4Layer(dims, "int4", 32, seed=5)
+    ws = moe.new_workspace(dims)
+    got, taps = L.run(ws=ws), {}
+    for tap in (2, 3, 4):
+        off, nb = moe.moe_workspace_tap(dims, tap)
+        taps[tap] = ws[off:off + nb].clone()
+    dense = {}
+    for k, rows, cols in (("gate_up", 2 * I, H), ("down", H, I), ("shared_gate_up", 2 * Is, H), ("shared_down", H, Is)):
+        n = L.m[k][0].shape[0]
+        dense[k] = torch.empty(n, rows, cols, dtype=torch.bfloat16, device="cuda")
+        moe.moe_w4_dequantize(ref.fmt("int4", 32), getattr(L.W, k), dense[k], k.endswith("gate_up"))
+    W = moe.Weights(L.router_w, None, dense["gate_up"], dense["down"], dense["shared_gate_up"], dense["shared_down"], L.shared_gate)
+    out = torch.empty_like(L.x)
+    moe.moe_forward(dims, L.x, W, L.residual, out, ws)
+    for tap in (2, 3, 4):
+        off, nb = moe.moe_workspace_tap(dims, tap)
+        assert torch.equal(taps[tap], ws[off:off + nb])
+    want, bound = ref.layer(dims, L.x, L.router_w, None, L.shared_gate, L.v["gate_up"], L.v["down"], L.v["shared_gate_up"][0],
+                            L.v["shared_down"][0], L.residual, weight_half=ref.HALF)
+    check(out, want, bound)  # the bf16 layer on the weights rounded to bf16
+    check(got, *L.reference())
+
+
+def test_layer_flags_nonfinite_scores():
+    L = W4Layer((4, 512, 32, 4, 128, 128), "int4", 32, seed=9)
+    L.x[2, 7] = float("inf")
+    ws, out = moe.new_workspace(L.dims), torch.empty_like(L.x)
+    moe.moe_forward_w4(L.dims, ref.fmt("int4", 32), L.x, L.W, L.residual, out, ws)
+    assert moe.moe_last_device_error(ws) == 7
+
+
+def test_quantised_stack_of_layers():
+    """bf16 weights quantised, two layers chained by RMSNorm and residual, as a decoder runs them."""
+    T, H, E, K, I, Is = dims = (6, 512, 16, 4, 128, 128)
+    f = ref.fmt("int4", 32)
+    ws = moe.new_workspace(dims)
+    x = torch.randn(T, H, device="cuda").to(torch.bfloat16)
+    for layer in range(2):
+        g = torch.Generator(device="cuda").manual_seed(layer)
+        rnd = lambda *s, std: (torch.randn(*s, generator=g, device="cuda") * std).to(torch.bfloat16)  # noqa: E731
+        dense = {"gate_up": rnd(E, 2 * I, H, std=H ** -0.5), "down": rnd(E, H, I, std=I ** -0.5),
+                 "shared_gate_up": rnd(1, 2 * Is, H, std=H ** -0.5), "shared_down": rnd(1, H, Is, std=Is ** -0.5)}
+        router, gate = rnd(E, H, std=0.02), rnd(1, H, std=H ** -0.5)
+        packed = {}
+        for k, w in dense.items():
+            packed[k] = moe.new_w4(f, w.shape[1], w.shape[2], w.shape[0])
+            moe.moe_w4_quantize(f, w, packed[k], moe.W4_GATE_UP if k.endswith("gate_up") else moe.W4_ROWS)
+        xn, out = torch.empty_like(x), torch.empty_like(x)
+        moe.moe_rmsnorm(dims, x, None, 1e-6, xn)
+        moe.moe_forward_w4(dims, f, xn, moe.Weights(router, None, packed["gate_up"], packed["down"], packed["shared_gate_up"],
+                                                    packed["shared_down"], gate), x, out, ws)
+        ids = torch.empty(T, K, dtype=torch.int32, device="cuda")
+        off, nb = moe.moe_workspace_tap(dims, 3)
+        ids = ws[off:off + nb].view(torch.int32).view(T, K)
+        v = {k: ref.values("int4", 32, ref.quantize("int4", 32, w)) for k, w in dense.items()}
+        check(out, *ref.layer(dims, xn, router, None, gate, v["gate_up"], v["down"], v["shared_gate_up"][0], v["shared_down"][0], x,
+                              ids=ids))
+        x = out

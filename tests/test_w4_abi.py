@@ -1,0 +1,130 @@
+"""Host-side checks of the 4-bit weight entry points: sizes, and refusals before any launch (the
+fake device addresses are never dereferenced)."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+from sparse_moe_ffn_router_gb300 import binding
+from sparse_moe_ffn_router_gb300.binding import CWeights, Dims, W4Format
+
+A = 0x10000000
+FULL = (64, 2048, 256, 8, 512, 512)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return binding.load_library()
+
+
+def F(fmt=0, group=32):
+    return ctypes.byref(W4Format(fmt, group))
+
+
+@pytest.mark.parametrize("fmt,group,record", [(0, 32, 1152), (0, 64, 1088), (0, 128, 1056), (1, 32, 1216), (1, 64, 1120),
+                                              (1, 128, 1072), (2, 32, 1152), (2, 64, 1088), (2, 128, 1056)])
+def test_sizes(lib, fmt, group, record):
+    assert lib.moe_w4_size(F(fmt, group), 1, 16, 128) == record
+    assert lib.moe_w4_size(F(fmt, group), 3, 17, 256) == 3 * 2 * 2 * record  # rows padded to strips
+    assert lib.moe_w4_size(F(fmt, group), 0, 16, 128) == 0
+    assert lib.moe_w4_size(F(fmt, group), 256, 1024, 2048) == 256 * 64 * 16 * record
+    assert lib.moe_w4_size(F(fmt, group), 1, 1, group) == record  # columns padded to records
+    assert lib.moe_w4_size(F(fmt, group), 1, 1, 65536) == 512 * record
+
+
+def test_size_refuses(lib):
+    for f, n, r, c in [(F(3), 1, 16, 128), (F(-1), 1, 16, 128), (F(0, 16), 1, 16, 128), (F(0, 256), 1, 16, 256), (None, 1, 16, 128),
+                       (F(), -1, 16, 128), (F(), 1, 0, 128), (F(), 1, 16, 0), (F(), 1, 16, 48), (F(0, 128), 1, 16, 192),
+                       (F(), 1, 16, 65568), (F(), 1, 2 ** 31 - 1, 65536), (F(), 2 ** 20, 2 ** 20, 2048)]:
+        assert lib.moe_w4_size(f, n, r, c) == 0
+        assert lib.moe_w4_linear_workspace_size(f, 1, r, c) == 0 or n != 1
+
+
+def _quantize(lib, f=None, n=2, rows=32, cols=256, layout=0, w=A, packed=A + 0x1000000, nbytes=1 << 20):
+    return lib.moe_w4_quantize(f or F(), n, rows, cols, layout, w, packed, nbytes, None)
+
+
+def _dequantize(lib, f=None, n=2, rows=32, cols=256, layout=0, w=A, packed=A + 0x1000000, nbytes=1 << 20):
+    return lib.moe_w4_dequantize(f or F(), n, rows, cols, layout, packed, nbytes, w, None)
+
+
+@pytest.mark.parametrize("call", [_quantize, _dequantize])
+def test_conversions_refuse(lib, call):
+    assert call(lib, f=F(3)) == 1 and call(lib, f=F(0, 48)) == 1
+    assert call(lib, layout=2) == 1 and call(lib, n=-1) == 1
+    assert call(lib, rows=0) == 2 and call(lib, cols=40) == 2 and call(lib, f=F(0, 128), cols=320) == 2
+    assert call(lib, layout=1, rows=24) == 2  # gate and up blocks of 8 rows
+    assert call(lib, w=None) == 1 and call(lib, packed=None) == 1
+    assert call(lib, w=A + 2) == 3 and call(lib, packed=A + 0x1000008) == 3
+    need = lib.moe_w4_size(F(), 2, 32, 256)
+    assert call(lib, nbytes=need - 1) == 4
+    assert call(lib, packed=A + 0x100) == 1  # overlap
+    assert call(lib, n=0, w=None, packed=None, nbytes=0) == 0  # nothing to do
+
+
+def test_pack_refuses(lib):
+    def call(f=None, codes=A, scales=A + 0x100000, zeros=None, packed=A + 0x1000000, nbytes=1 << 20, n=2, rows=32):
+        return lib.moe_w4_pack(f or F(), n, rows, 256, 0, codes, scales, zeros, packed, nbytes, None)
+
+    assert call(codes=None) == 1 and call(scales=None) == 1 and call(packed=None) == 1
+    assert call(zeros=A + 0x200000) == 1          # zero points without the format that has them
+    assert call(f=F(1)) == 1                      # and the other way round
+    assert call(codes=A + 4) == 3 and call(scales=A + 0x100002) == 3 and call(f=F(1), zeros=A + 0x200001) == 3
+    assert call(nbytes=100) == 4 and call(scales=A + 0x1000000) == 1 and call(n=0, codes=None) == 0
+
+
+def test_linear_refuses(lib):
+    size = lib.moe_w4_size(F(), 1, 64, 256)
+    ws = lib.moe_w4_linear_workspace_size(F(), 4, 64, 256)
+    assert ws > 0 and ws % 256 == 0
+
+    def call(f=None, T=4, N=64, K=256, x=A, packed=A + 0x100000, pb=size, bias=None, out=A + 0x200000, wsp=A + 0x300000, wb=ws):
+        return lib.moe_w4_linear(f or F(), T, N, K, x, packed, pb, bias, out, wsp, wb, None)
+
+    assert call(f=F(7)) == 1 and call(T=-1) == 1
+    assert call(N=0) == 2 and call(K=100) == 2 and call(K=65568, pb=1 << 30) == 2
+    assert call(x=None) == 1 and call(packed=None) == 1 and call(out=None) == 1 and call(wsp=None) == 1
+    assert call(x=A + 2) == 3 and call(packed=A + 0x100004) == 3 and call(out=A + 0x200002) == 3 and call(wsp=A + 0x300008) == 3
+    assert call(bias=A + 0x400001) == 3
+    assert call(pb=size - 1) == 4 and call(wb=ws - 1) == 4
+    assert call(out=A + 0x10) == 1 and call(out=A + 0x100010) == 1 and call(bias=A + 0x200000) == 1  # overlaps
+    assert call(T=0, x=None, out=None) == 0
+
+
+def test_forward_refuses(lib):
+    names = [f[0] for f in CWeights._fields_]
+
+    def call(dims=FULL, f=None, x=A + 0x100000, w=None, res=None, out=A + 0x800000, ws=A + 0x1000000, wsb=None, **over):
+        d = Dims(*dims)
+        c = CWeights(*[{**{n: None if n == "router_b" else A for n in names}, **over}[n] for n in names])
+        return lib.moe_forward_w4(ctypes.byref(d), f, x, ctypes.byref(c), res, out, ws,
+                                  lib.moe_workspace_size(ctypes.byref(d)) if wsb is None else wsb, None)
+
+    assert call(f=None) == 1 and call(f=F(3)) == 1 and call(f=F(0, 33)) == 1
+    assert call(f=F(), x=None) == 1 and call(f=F(), down=None) == 1 and call(f=F(), out=None) == 1
+    assert call(f=F(), gate_up=A + 8) == 3 and call(f=F(), x=A + 0x100002) == 3
+    assert call(f=F(), out=A + 0x100000) == 1 and call(f=F(), wsb=100) == 4
+    assert call(f=F(0, 128), dims=(64, 2048, 256, 8, 448, 512)) == 2  # I is no multiple of the group
+    assert call(f=F(0, 128), dims=(64, 2048, 256, 8, 512, 320)) == 2
+    assert call(f=F(), dims=(64, 2000, 256, 8, 512, 512)) == 2
+    assert call(f=F(), dims=(0, 2048, 256, 8, 512, 512), x=None, out=None) == 0
+
+
+def test_binding_checks():
+    f = W4Format(0, 32)
+    assert binding.moe_w4_size(f, 16, 128) == 1152
+    w = torch.zeros(16, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        binding.moe_w4_quantize(f, w, torch.zeros(1152, dtype=torch.uint8))  # not on the GPU
+    with pytest.raises(TypeError):
+        binding.moe_w4_quantize(f, w.float(), torch.zeros(1152, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        binding.moe_w4_linear(f, torch.zeros(3, 128, dtype=torch.bfloat16), w, None, torch.zeros(2, 16, dtype=torch.bfloat16), w)
+    with pytest.raises(binding.MoEError):
+        binding.new_w4(W4Format(9, 32), 16, 128, device="cpu")
+    with pytest.raises(TypeError):  # bf16 weights where packed ones are expected
+        binding.moe_forward_w4((1, 128, 8, 2, 64, 64), f, w, binding.Weights(*[w] * 7), None, w, w)
+    with pytest.raises(ValueError):  # packed tensors too small for the dims
+        binding.moe_forward_w4((1, 128, 8, 2, 64, 64), f, w, binding.Weights(*[torch.zeros(16, dtype=torch.uint8)] * 7), None, w, w)
