@@ -81,7 +81,8 @@ class Weights:
         return cls(**{f.name: d.get(f.name) for f in fields(cls)})
 
     def to_c(self) -> CWeights:
-        return CWeights(*[_ptr(getattr(self, f.name)) for f in fields(self)])
+        return CWeights(_ptr(self.router_w), _ptr(self.router_b), _ptr(self.gate_up), _ptr(self.down),
+                        _ptr(self.shared_gate_up), _ptr(self.shared_down), _ptr(self.shared_gate))
 
 
 _lock = threading.Lock()
@@ -95,6 +96,8 @@ def library_path() -> str:
 def load_library(build_if_missing: bool = True):
     """Load libmoe_gb300.so (building it first when it is absent or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if build_if_missing:
@@ -175,8 +178,15 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream object (2.9 us on the GB300 host
+# against 0.1 us), where this torch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -405,22 +415,27 @@ def moe_w4_linear(fmt: W4Format, x, packed, bias, out, workspace, stream=None):
                                         _stream(stream)), "moe_w4_linear")
 
 
+# (format, group) -> bytes of a packed record (16 rows by 128 columns)
+_W4_RECORD = {(f, g): 1024 + 16 * (128 // g) * (3 if f == W4_INT4_ZP else 2)
+              for f in (W4_INT4, W4_INT4_ZP, W4_E2M1) for g in (32, 64, 128)}
+
+
 def moe_forward_w4(dims, fmt: W4Format, x, weights: Weights, residual, out, workspace, stream=None):
     """moe_forward with weights.gate_up, down, shared_gate_up and shared_down in packed 4-bit form
     (uint8 tensors of moe_w4_size bytes; gate_up layouts W4_GATE_UP, down layouts W4_ROWS)."""
     d = _dims(dims)
-    need = {"gate_up": (2 * d.I, d.H, d.E), "down": (d.H, d.I, d.E), "shared_gate_up": (2 * d.Is, d.H, 1),
-            "shared_down": (d.H, d.Is, 1)}
-    for name, (rows, cols, n) in need.items():
-        t = getattr(weights, name)
+    H, I, Is = d.H, d.I, d.Is
+    record = _W4_RECORD.get((fmt.format, fmt.group), 0)
+    h_recs, up, down, sup, sdown = (H + 127) // 128, weights.gate_up, weights.down, weights.shared_gate_up, weights.shared_down
+    for t, need in ((up, d.E * ((2 * I + 15) // 16) * h_recs), (down, d.E * ((H + 15) // 16) * ((I + 127) // 128)),
+                    (sup, ((2 * Is + 15) // 16) * h_recs), (sdown, ((H + 15) // 16) * ((Is + 127) // 128))):
         if t.dtype != torch.uint8:
-            raise TypeError(f"{name} must be packed 4-bit weights (uint8)")
-        if _nbytes(t) < moe_w4_size(fmt, rows, cols, n):
-            raise ValueError(f"{name} holds {_nbytes(t)} bytes, {n} packed [{rows}, {cols}] need "
-                             f"{moe_w4_size(fmt, rows, cols, n)}")
+            raise TypeError("the experts' weights must be packed 4-bit weights (uint8)")
+        if t.numel() < need * record:
+            raise ValueError(f"packed weights of {t.numel()} bytes, the layer's dims need {need * record}")
     w = weights.to_c()
     _check(load_library().moe_forward_w4(ctypes.byref(d), ctypes.byref(fmt), _ptr(x), ctypes.byref(w), _ptr(residual),
-                                         _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+                                         _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
            "moe_forward_w4")
 
 

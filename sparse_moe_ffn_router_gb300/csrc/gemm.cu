@@ -470,6 +470,10 @@ cudaError_t launch_gemm(const CUtensorMap& A0, const CUtensorMap& A1, const CUte
 
 }  // namespace
 
+bool make_bf16_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch, uint32_t box_rows) {
+    return make_map(m, base, rows, cols, pitch, box_rows);
+}
+
 // Router scores of all T tokens on the tensor cores: logits[:, 0:E] = x . Wr^T (+ br).
 cudaError_t launch_router_gemm(const LayerArgs& a, cudaStream_t s) {
     // 64-wide N tiles: the E <= 256 score columns of T/128 token tiles would otherwise give

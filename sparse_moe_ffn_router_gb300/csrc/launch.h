@@ -1,6 +1,8 @@
 // launch.h -- internal interface between the C-ABI entry points and the kernels.
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace moe {
@@ -120,6 +122,8 @@ cudaError_t launch_decode_fused(const LayerArgs& a, cudaStream_t s);
 cudaError_t launch_stream_experts(const LayerArgs& a, cudaStream_t s);
 cudaError_t launch_dispatch(const LayerArgs& a, cudaStream_t s);
 cudaError_t launch_experts(const LayerArgs& a, cudaStream_t s);
+// 2D K-major bf16 tensor [rows, cols] for TMA: box {64, box_rows}, 128-byte swizzle, zeros outside.
+bool make_bf16_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch, uint32_t box_rows);
 
 // Packed 4-bit weights (w4.cuh).
 struct W4LinearArgs {

@@ -83,59 +83,64 @@ __device__ __forceinline__ void w4_decode(uint32_t w, uint32_t bias, uint32_t (&
     }
 }
 
-// A row's scales within a record (fp32) and decoding biases, one per group.
+// One record's share of a lane: the codes, scales and zero points of rows g and g + 8, as they lie
+// in shared memory.
 template <int FMT, int G>
-__device__ __forceinline__ void w4_row_meta(uint32_t rec, int row, float (&s)[W4Rec<FMT, G>::kGroups],
-                                            uint32_t (&bias)[W4Rec<FMT, G>::kGroups]) {
+struct W4Frag {
+    uint4 lo, hi;
+    uint32_t s[2][W4Rec<FMT, G>::kGroups == 4 ? 2 : 1];
+    uint32_t z[2];
+};
+
+template <int FMT, int G>
+__device__ __forceinline__ void w4_load(uint32_t rec, int lane, W4Frag<FMT, G>& f) {
     constexpr int N = W4Rec<FMT, G>::kGroups;
-    uint32_t v[2] = {0u, 0u};
-    const uint32_t at = rec + W4Rec<FMT, G>::kScales + (uint32_t)(row * N * 2);
-    if (N == 4)
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at));
-    else if (N == 2)
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(at));
-    else {
-        uint16_t h;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at));
-        v[0] = h;
-    }
+    f.lo = lds128_smem(rec + (uint32_t)lane * 16u);
+    f.hi = lds128_smem(rec + 512u + (uint32_t)lane * 16u);
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = (i & 1) ? bf_hi(v[i >> 1]) : bf_lo(v[i >> 1]);
-    if (FMT == MOE_W4_INT4_ZP) {
-        uint32_t z = 0;
-        const uint32_t za = rec + W4Rec<FMT, G>::kZeros + (uint32_t)(row * N);
-        if (N == 4)
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(z) : "r"(za));
-        else {
-            uint16_t h = 0;
-            if (N == 2)
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(za));
-            else
-                asm volatile("{\n\t.reg .u32 t;\n\tld.shared.u8 t, [%1];\n\tcvt.u16.u32 %0, t;\n\t}" : "=h"(h) : "r"(za));
-            z = h;
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t row = (uint32_t)(lane >> 2) + 8u * h, at = rec + W4Rec<FMT, G>::kScales + row * (2u * N);
+        if constexpr (N == 4) {
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(f.s[h][0]), "=r"(f.s[h][1]) : "r"(at));
+        } else if constexpr (N == 2) {
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(f.s[h][0]) : "r"(at));
+        } else {
+            uint16_t v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+            f.s[h][0] = v;
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i) bias[i] = 0x43004300u | (((z >> (8 * i)) & 0xffu) * 0x00010001u);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) bias[i] = 0x43084308u;
+        f.z[h] = 0;
+        if (FMT == MOE_W4_INT4_ZP) {
+            const uint32_t za = rec + W4Rec<FMT, G>::kZeros + row * N;
+            if (N == 4)
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(f.z[h]) : "r"(za));
+            else if (N == 2) {
+                uint16_t v;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(za));
+                f.z[h] = v;
+            } else
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(f.z[h]) : "r"(za));
+        }
     }
 }
 
-// acc += one record (16 rows by 128 columns, in shared memory at `rec`) times NT tiles of 8
-// tokens. b[n][4 c + i] are the B operands of lane 4g + t: tokens g of tile n, columns
-// 32 c + 8 t + 2 i, + 1. acc is the m16n8 accumulator of each tile: rows g (0, 1) and g + 8 (2, 3),
-// tokens 2t (0, 2) and 2t + 1 (1, 3). Each group's sum starts at zero and is scaled in fp32.
+template <int FMT, int G>
+__device__ __forceinline__ float w4_scale(const W4Frag<FMT, G>& f, int h, int gi) {
+    return (gi & 1) ? bf_hi(f.s[h][gi >> 1]) : bf_lo(f.s[h][gi >> 1]);
+}
+template <int FMT, int G>
+__device__ __forceinline__ uint32_t w4_bias(const W4Frag<FMT, G>& f, int h, int gi) {
+    if (FMT != MOE_W4_INT4_ZP) return 0x43084308u;
+    return 0x43004300u | (((f.z[h] >> (8 * gi)) & 0xffu) * 0x00010001u);
+}
+
+// acc += one record (16 rows by 128 columns) times NT tiles of 8 tokens. b[n][4 c + i] are the B
+// operands of lane 4g + t: token g of tile n, columns 32 c + 8 t + 2 i, + 1. acc is the m16n8
+// accumulator of each tile: rows g (0, 1) and g + 8 (2, 3), tokens 2t (0, 2) and 2t + 1 (1, 3).
+// Each group's sum starts at zero and is scaled in fp32.
 template <int FMT, int G, int NT>
-__device__ __forceinline__ void w4_mma_record(uint32_t rec, const uint32_t (&b)[NT][16], float (&acc)[NT][4], int lane) {
-    constexpr int N = W4Rec<FMT, G>::kGroups;
-    const uint4 lo = lds128_smem(rec + (uint32_t)lane * 16u);
-    const uint4 hi = lds128_smem(rec + 512u + (uint32_t)lane * 16u);
-    float s0[N], s1[N];
-    uint32_t z0[N], z1[N];
-    w4_row_meta<FMT, G>(rec, lane >> 2, s0, z0);
-    w4_row_meta<FMT, G>(rec, (lane >> 2) + 8, s1, z1);
-    const uint32_t w0[4] = {lo.x, lo.y, lo.z, lo.w}, w1[4] = {hi.x, hi.y, hi.z, hi.w};
+__device__ __forceinline__ void w4_mma_record(const W4Frag<FMT, G>& f, const uint32_t (&b)[NT][16], float (&acc)[NT][4]) {
+    const uint32_t w0[4] = {f.lo.x, f.lo.y, f.lo.z, f.lo.w}, w1[4] = {f.hi.x, f.hi.y, f.hi.z, f.hi.w};
     float d[NT][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -145,20 +150,21 @@ __device__ __forceinline__ void w4_mma_record(uint32_t rec, const uint32_t (&b)[
             for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
         }
         uint32_t p[4], q[4];
-        w4_decode<FMT>(w0[c], z0[gi], p);
-        w4_decode<FMT>(w1[c], z1[gi], q);
+        w4_decode<FMT>(w0[c], w4_bias(f, 0, gi), p);
+        w4_decode<FMT>(w1[c], w4_bias(f, 1, gi), q);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             mma16816(d[n], p[0], q[0], p[1], q[1], b[n][4 * c], b[n][4 * c + 1]);
             mma16816(d[n], p[2], q[2], p[3], q[3], b[n][4 * c + 2], b[n][4 * c + 3]);
         }
         if ((c + 1) * 32 % G == 0) {
+            const float s0 = w4_scale(f, 0, gi), s1 = w4_scale(f, 1, gi);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                acc[n][0] = fmaf(s0[gi], d[n][0], acc[n][0]);
-                acc[n][1] = fmaf(s0[gi], d[n][1], acc[n][1]);
-                acc[n][2] = fmaf(s1[gi], d[n][2], acc[n][2]);
-                acc[n][3] = fmaf(s1[gi], d[n][3], acc[n][3]);
+                acc[n][0] = fmaf(s0, d[n][0], acc[n][0]);
+                acc[n][1] = fmaf(s0, d[n][1], acc[n][1]);
+                acc[n][2] = fmaf(s1, d[n][2], acc[n][2]);
+                acc[n][3] = fmaf(s1, d[n][3], acc[n][3]);
             }
         }
     }

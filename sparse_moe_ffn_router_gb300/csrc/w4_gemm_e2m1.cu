@@ -1,0 +1,11 @@
+// w4_gemm_e2m1.cu -- the tensor-core products of w4_gemm.cuh for MOE_W4_E2M1.
+#include "w4_gemm.cuh"
+
+namespace moe {
+
+cudaError_t launch_w4_gemm_e2m1(int group, int which, const W4GemmArgs& p, const CUtensorMap& a0, const CUtensorMap& a1,
+                              const LayerArgs& a, int bn, cudaStream_t s) {
+    return launch_w4_gemm_f<MOE_W4_E2M1>(group, which, p, a0, a1, a, bn, s);
+}
+
+}  // namespace moe

@@ -1,5 +1,6 @@
 // w4_layer.cu -- launch sequences of the products on packed 4-bit weights: the linear layer and
 // the experts of the MoE layer (the routing before and the combine after are the layer's own).
+#include "w4_gemm.cuh"
 #include "w4_stream.cuh"
 
 namespace moe {
@@ -13,7 +14,75 @@ cudaError_t launch_w4_stream(int format, int group, int which, const W4StreamArg
     }
 }
 
+cudaError_t launch_w4_gemm(int format, int group, int which, const W4GemmArgs& p, const CUtensorMap& a0,
+                           const CUtensorMap& a1, const LayerArgs& a, int bn, cudaStream_t s) {
+    switch (format) {
+        case MOE_W4_INT4: return launch_w4_gemm_int4(group, which, p, a0, a1, a, bn, s);
+        case MOE_W4_INT4_ZP: return launch_w4_gemm_int4_zp(group, which, p, a0, a1, a, bn, s);
+        case MOE_W4_E2M1: return launch_w4_gemm_e2m1(group, which, p, a0, a1, a, bn, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// Tokens from which the linear layer runs on the tensor cores.
+constexpr int kW4GemmTokens = 64;
+
+static cudaError_t w4_linear_gemm(const moe_w4_format& f, const W4LinearArgs& l, cudaStream_t s) {
+    CUtensorMap mx;
+    if (!make_bf16_map(&mx, l.x, l.T, l.K, l.K, 128)) return cudaErrorInvalidValue;
+    W4GemmArgs p = {};
+    p.w[0] = l.w;
+    p.rows[0] = l.N;
+    p.cols[0] = l.K;
+    p.bias = l.bias;
+    p.out = l.out;
+    p.T = l.T;
+    p.err = l.err;
+    p.wait_ns = l.wait_ns;
+    LayerArgs a = {};
+    a.num_sms = l.num_sms;
+    const long long mt = (l.T + 127) / 128;
+    const int bn = mt * ((l.N + 255) / 256) >= l.num_sms ? 256 : 128;
+    return launch_w4_gemm(f.format, f.group, kW4GLinear, p, mx, mx, a, bn, s);
+}
+
+// Gate_up and down of 256 tokens or more on the tensor cores.
+static cudaError_t w4_experts_gemm(const LayerArgs& a, const moe_w4_format& f, cudaStream_t s) {
+    CUtensorMap mx, mh, mhs;  // the h rows are Imax apart; the columns past I (Is) of a row hold nothing
+    if (!make_bf16_map(&mx, a.x, a.T, a.H, a.H, 128) || !make_bf16_map(&mh, a.h, a.P + a.T, a.I, a.Imax, 128) ||
+        !make_bf16_map(&mhs, a.h, a.P + a.T, a.Is, a.Imax, 128))
+        return cudaErrorInvalidValue;
+    W4GemmArgs p = {};
+    p.err = &a.hdr->err;
+    p.wait_ns = a.wait_ns;
+    p.w[0] = reinterpret_cast<const uint8_t*>(a.gate_up);
+    p.w[1] = reinterpret_cast<const uint8_t*>(a.sgu);
+    p.matrix_bytes = w4_matrix_bytes(f.format, f.group, 2 * a.I, a.H);
+    p.rows[0] = 2 * a.I; p.rows[1] = 2 * a.Is;
+    p.cols[0] = p.cols[1] = a.H;
+    cudaError_t e = launch_w4_gemm(f.format, f.group, kW4GUp, p, mx, mx, a, 2 * gemm_up_half(a), s);
+    if (e != cudaSuccess) return e;
+    p.w[0] = reinterpret_cast<const uint8_t*>(a.down);
+    p.w[1] = reinterpret_cast<const uint8_t*>(a.sd);
+    p.matrix_bytes = w4_matrix_bytes(f.format, f.group, a.H, a.I);
+    p.rows[0] = p.rows[1] = a.H;
+    p.cols[0] = a.I; p.cols[1] = a.Is;
+    e = launch_w4_gemm(f.format, f.group, kW4GDown, p, mh, mhs, a, gemm_down_bn(a), s);
+    if (e != cudaSuccess) return e;
+    return launch_combine(a, s);
+}
+
+// Strips of a block, at most: the power of two that still gives every SM four items or more of the
+// call's `strips` (times token tiles). Blocks of one strip let small calls use every SM; full
+// blocks spend less on each stage.
+static int w4_want(long long strips, int num_sms) {
+    int want = 1;
+    while (want < kW4Warps && strips >= 8ll * want * num_sms) want *= 2;
+    return want;
+}
+
 cudaError_t launch_w4_linear(const moe_w4_format& f, const W4LinearArgs& l, cudaStream_t s) {
+    if (l.T >= kW4GemmTokens) return w4_linear_gemm(f, l, s);
     W4StreamArgs p = {};
     p.w = l.w;
     p.x = l.x;
@@ -22,6 +91,8 @@ cudaError_t launch_w4_linear(const moe_w4_format& f, const W4LinearArgs& l, cuda
     p.rows[0] = l.N;
     p.cols[0] = l.K;
     p.T = l.T;
+    const long long strips = (l.N + kW4Strip - 1) / kW4Strip;
+    p.b0 = p.b1 = w4_block(l.N, l.K, w4_want(strips * ((l.T + kW4Tok - 1) / kW4Tok), l.num_sms));
     p.err = l.err;
     p.wait_ns = l.wait_ns;
     p.a.num_sms = l.num_sms;
@@ -30,6 +101,7 @@ cudaError_t launch_w4_linear(const moe_w4_format& f, const W4LinearArgs& l, cuda
 
 // Gate_up and down of the dispatched groups; Y is complete when both have run.
 cudaError_t launch_w4_experts(const LayerArgs& a, const moe_w4_format& f, cudaStream_t s) {
+    if (a.gemm) return w4_experts_gemm(a, f, s);
     W4StreamArgs p = {};
     p.a = a;
     p.T = a.T;
@@ -38,14 +110,22 @@ cudaError_t launch_w4_experts(const LayerArgs& a, const moe_w4_format& f, cudaSt
     p.rows[0] = 2 * a.Is; p.rows[1] = 2 * a.I;
     p.cols[0] = p.cols[1] = a.H;
     p.matrix_bytes = w4_matrix_bytes(f.format, f.group, 2 * a.I, a.H);
+    // token tiles of the shared expert, and of the routed ones about (the routing is on the device)
+    const long long ts = (a.T + kW4Tok - 1) / kW4Tok, tr = a.P < a.E ? a.P : a.E + a.P / kW4Tok;
+    int want = w4_want(ts * (2 * a.Is / kW4Strip) + tr * (2 * a.I / kW4Strip), a.num_sms);
+    p.b0 = w4_block(p.rows[0], a.H, want);
+    p.b1 = w4_block(p.rows[1], a.H, want);
     cudaError_t e = launch_w4_stream(f.format, f.group, kW4Up, p, s);
     if (e != cudaSuccess) return e;
     p.rows[0] = p.rows[1] = a.H;
     p.cols[0] = a.Is; p.cols[1] = a.I;
     p.matrix_bytes = w4_matrix_bytes(f.format, f.group, a.H, a.I);
+    want = w4_want((ts + tr) * (a.H / kW4Strip), a.num_sms);
+    p.b0 = w4_block(a.H, a.Is, want);
+    p.b1 = w4_block(a.H, a.I, want);
     e = launch_w4_stream(f.format, f.group, kW4Down, p, s);
     if (e != cudaSuccess) return e;
-    return a.gemm ? launch_combine(a, s) : launch_combine_pdl(a, s);
+    return launch_combine_pdl(a, s);
 }
 
 }  // namespace moe

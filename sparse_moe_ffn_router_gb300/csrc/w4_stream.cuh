@@ -3,18 +3,19 @@
 //
 // With few tokens each weight is used a handful of times, so the kernels are bound by reading the
 // packed weights once. One persistent CTA per SM: a producer warp walks the CTA's items and copies
-// each item's strips (up to 16 records, 17 to 19 KB, one contiguous 1-D TMA bulk copy) into a ring
-// of shared-memory stages that keeps ~200 KB of copies in flight; eight consumer warps decode the
-// codes in registers into the A operand of warp-level bf16 MMAs (16 weight rows by 8 tokens; a
-// stage's 16 rows are too few for the 64/128-row tcgen05 MMA, and the decoded weights are in
+// each item's strips (up to 32 records, 34 to 39 KB, one contiguous 1-D TMA bulk copy) into a ring
+// of shared-memory stages that keeps ~180 KB of copies in flight; sixteen consumer warps decode
+// the codes in registers into the A operand of warp-level bf16 MMAs (16 weight rows by 8 tokens;
+// a few strips are too few rows for the 64/128-row tcgen05 MMA, and the decoded weights are in
 // registers already), each over its share of a strip's columns with its token rows held in
 // registers; two epilogue warps add the shares in a fixed order and write the results, so the
-// consumers never wait for one another. Decoding, not the MMAs, is the consumers' work: about
-// 1.4 (integer codes) to 1.9 (E2M1) instructions a weight and lane.
+// consumers never wait for one another. Decoding, not the MMAs, is the consumers' work (11 to 14
+// instructions for a word of eight codes), so what a stage costs besides it is kept small: one
+// 16-byte word tells a consumer warp all that a stage needs as long as the token set stays.
 //
-// Item: a block of consecutive strips of one matrix by one tile of 8 tokens. A block is as many
-// strips as fill a stage (a strip of R <= 16 records is shared by W = 1, 2, 4 or 8 warps of two
-// records each, so 8 / W strips to a block); a strip of more than 16 records takes ceil(R / 16)
+// Item: a block of consecutive strips of one matrix by one tile of 8 tokens. A strip of R <= 32
+// records is shared by W warps of one or two records each, so 16 / W strips fill a stage (fewer
+// when that would leave SMs without items); a strip of more than 32 records takes ceil(R / 32)
 // stages, its sums staying in the warps' registers.
 #pragma once
 
@@ -25,6 +26,35 @@ namespace moe {
 
 enum : int { kW4Linear = 0, kW4Up = 1, kW4Down = 2 };
 
+constexpr int kW4Warps = 16;              // consumer warps
+constexpr int kW4StageRecs = 32;          // records of a stage, at most
+constexpr int kW4Tok = 8;                 // tokens per item
+
+// How one matrix is cut into items.
+struct W4Block {
+    int strips, R;    // strips of the matrix, records of a strip
+    int wl, rpw;      // log2 of the warps that share a strip, records of each
+    int ns, blocks;   // strips of a block, blocks of the matrix
+    int nslab;        // stages of a block
+};
+
+// want: strips of a block, at most (a power of two).
+inline W4Block w4_block(int rows, int cols, int want) {
+    W4Block b;
+    b.strips = (rows + kW4Strip - 1) / kW4Strip;
+    b.R = (cols + kW4Cols - 1) / kW4Cols;
+    const int recs = b.R < kW4StageRecs ? b.R : kW4StageRecs;
+    b.wl = 0;
+    while ((2 << b.wl) < recs) ++b.wl;  // two records a warp
+    while (b.wl < 4 && (kW4Warps >> b.wl) > want && (1 << b.wl) < recs) ++b.wl;  // down to one
+    b.rpw = (1 << b.wl) >= recs ? 1 : 2;
+    b.ns = kW4Warps >> b.wl;
+    if (b.ns > want) b.ns = want;
+    b.nslab = (b.R + kW4StageRecs - 1) / kW4StageRecs;
+    b.blocks = (b.strips + b.ns - 1) / b.ns;
+    return b;
+}
+
 // One call's operands. Group 0 is the shared expert (or the linear layer's matrix, taken first),
 // group 1 the routed experts.
 struct W4StreamArgs {
@@ -34,74 +64,83 @@ struct W4StreamArgs {
     const bf16* bias;   // linear: [rows] or NULL
     bf16* out;          // linear: [T, rows]
     int rows[2], cols[2];
+    W4Block b0, b1;
     size_t matrix_bytes;  // of one routed matrix
     uint32_t* err;
     uint64_t wait_ns;
     int T;
 };
 
-struct W4Block {
-    int strips, R, wl, ns, nslab, blocks;  // wl: log2 of the warps of a strip; ns: strips of a block
-};
-
-__host__ __device__ inline W4Block w4_block(int rows, int cols) {
-    W4Block b;
-    b.strips = (rows + kW4Strip - 1) / kW4Strip;
-    b.R = (cols + kW4Cols - 1) / kW4Cols;
-    const int need = ((b.R < 16 ? b.R : 16) + 1) / 2;
-    b.wl = 0;
-    while ((1 << b.wl) < need) ++b.wl;
-    b.ns = 8 >> b.wl;
-    b.nslab = (b.R + 15) / 16;
-    b.blocks = (b.strips + b.ns - 1) / b.ns;
-    return b;
-}
-
 cudaError_t launch_w4_stream(int format, int group, int which, const W4StreamArgs& p, cudaStream_t s);
 
 #ifdef __CUDACC__
 
-constexpr int kW4Tok = 8;                 // tokens per item
 constexpr int kW4RedBufs = 4;             // partial-sum buffers
 constexpr int kW4EpiWarps = 2;
-constexpr int kW4Threads = 32 * (kWarps + 1 + kW4EpiWarps);
-constexpr int kW4SmemMax = 220 * 1024;
+constexpr int kW4Threads = 32 * (kW4Warps + 1 + kW4EpiWarps);
+constexpr int kW4SmemMax = 227 * 1024;
 
+// An item, for the epilogue and for loading token rows.
 struct W4Meta {
     int group;   // 0 shared / linear, 1 routed; -1: no more items
     int mt;      // tokens
     int row0;    // up: first h row written; down: first h row read
     int strip0;  // first strip of the block
-    int key;     // the item's token set: consecutive items with one key use the same rows
+    int n;       // strips of the block
     int tok[kW4Tok], slot[kW4Tok];
     float sc[kW4Tok];
 };
 
+// A stage, for the consumers: the token rows' key (a new one wherever the tokens, the group or the
+// column range change), strips | records << 8 | (last stage of its item) << 16 (0: no more
+// items), the column range, the item's place among the W4Metas.
+struct __align__(16) W4Stage {
+    int key, info, slab, meta;
+};
+
 template <int FMT, int G>
 struct W4Ring {
-    static constexpr int kStage = 16 * W4Rec<FMT, G>::kBytes;
-    static constexpr int kRed = kW4RedBufs * kWarps * 128 * 4;
-    static constexpr int kFixed = 1024 + kRed + 24 * (int)sizeof(W4Meta) + 512 + 258 * 4;
-    static constexpr int kStages = (kW4SmemMax - kFixed) / kStage < 12 ? (kW4SmemMax - kFixed) / kStage : 12;
+    static constexpr int kStage = kW4StageRecs * W4Rec<FMT, G>::kBytes;
+    static constexpr int kRed = kW4RedBufs * kW4Warps * 128 * 4;
+    static constexpr int kMaxMetas = 16, kMaxStages = 6;
+    static constexpr int kFixed = 128 + kRed + kMaxMetas * (int)sizeof(W4Meta) + kMaxStages * (int)sizeof(W4Stage) + 256 + 258 * 4;
+    static constexpr int kFit = (kW4SmemMax - kFixed) / kStage;
+    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+    // an item's metadata is rewritten once its epilogue is done: at most this many items later
     static constexpr int kMetas = kStages + kW4RedBufs + 2;
-    static_assert(kStage % 128 == 0 && kMetas <= 24 && (2 * kStages + 2 * kW4RedBufs) * 8 <= 512, "ring");
+    static_assert(kStage % 128 == 0 && kStages >= 3 && kMetas <= kMaxMetas, "ring");
+    static_assert((2 * kMaxStages + 2 * kW4RedBufs) * 8 <= 256 && sizeof(W4Meta) % 4 == 0, "barriers");
     static constexpr int kBytes = kFixed + kStages * kStage;
 };
 
-// B operands of the warp's two records from its row of the tile: elements k0 + 32 c + 8 t .. + 7 of
-// each, zero past the matrix's columns (the packed weights there have scale 0, but the row's memory
-// may hold anything) and for the tile's missing tokens. L2 loads (an earlier kernel wrote the rows).
-__device__ __forceinline__ void w4_load_frag(uint32_t (&b)[2][1][16], const bf16* row, bool live, int rec0, int nrec, int cols,
-                                             int lane) {
+// B operands of one record from a lane's token row: elements 32 c + 8 t .. + 7 from column k0, zero
+// past the matrix's columns (the packed weights there have scale 0, but the row's memory may hold
+// anything) and for the tile's missing tokens. L2 loads (an earlier kernel wrote the rows).
+__device__ __forceinline__ void w4_load_tokens(uint32_t (&b)[1][16], const bf16* row, bool live, int k0, int cols, int lane) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int k = (rec0 + r) * kW4Cols + 32 * c + 8 * (lane & 3);
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (live && r < nrec && k < cols) v = __ldcg(reinterpret_cast<const uint4*>(row + k));
-            b[r][0][4 * c] = v.x; b[r][0][4 * c + 1] = v.y; b[r][0][4 * c + 2] = v.z; b[r][0][4 * c + 3] = v.w;
+    for (int c = 0; c < 4; ++c) {
+        const int k = k0 + 32 * c + 8 * (lane & 3);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (live && k < cols) v = __ldcg(reinterpret_cast<const uint4*>(row + k));
+        b[0][4 * c] = v.x; b[0][4 * c + 1] = v.y; b[0][4 * c + 2] = v.z; b[0][4 * c + 3] = v.w;
+    }
+}
+
+// A cursor over a ring of N barriers: the slot, and the parity of its current round.
+template <int N>
+struct W4Cursor {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == N) {
+            s = 0;
+            ph ^= 1u;
         }
+    }
+};
+
+__device__ __forceinline__ bool w4_wait(uint64_t* bar, uint32_t parity, uint64_t limit) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit));
 }
 
 template <int WHICH, int FMT, int G>
@@ -112,46 +151,47 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
     uint8_t* base = smem_raw + (((smem_u32(smem_raw) + 127u) & ~127u) - smem_u32(smem_raw));
     uint8_t* stages = base;
     float* red = reinterpret_cast<float*>(base + Ring::kStages * Ring::kStage);
-    W4Meta* metas = reinterpret_cast<W4Meta*>(reinterpret_cast<uint8_t*>(red) + Ring::kRed);
-    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(metas) + 24 * sizeof(W4Meta));
+    W4Stage* sm = reinterpret_cast<W4Stage*>(reinterpret_cast<uint8_t*>(red) + Ring::kRed);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + Ring::kMaxStages);
     uint64_t* empty = full + Ring::kStages;
     uint64_t* rfull = empty + Ring::kStages;
     uint64_t* rempty = rfull + kW4RedBufs;
-    int* tiles = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(full) + 512);
+    W4Meta* metas = reinterpret_cast<W4Meta*>(reinterpret_cast<uint8_t*>(full) + 256);
+    int* tiles = reinterpret_cast<int*>(metas + Ring::kMaxMetas);
     const LayerArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G_ = gridDim.x, c_ = blockIdx.x;
     const uint64_t limit = p.wait_ns;
     if (threadIdx.x == 0) {
         for (int s = 0; s < Ring::kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kWarps);
+            mbar_init(&empty[s], kW4Warps);
         }
         for (int s = 0; s < kW4RedBufs; ++s) {
-            mbar_init(&rfull[s], kWarps);
+            mbar_init(&rfull[s], kW4Warps);
             mbar_init(&rempty[s], 1);
         }
         fence_mbar_init();
     }
     __syncthreads();
-    const W4Block bg[2] = {w4_block(p.rows[0], p.cols[0]),
-                           WHICH == kW4Linear ? W4Block{} : w4_block(p.rows[1], p.cols[1])};
 
-    if (warp == kWarps) {
+    if (warp == kW4Warps) {
         // ---------------- producer
-        int it = 0, item = 0;
+        const int G_ = gridDim.x, c_ = blockIdx.x;
+        W4Cursor<Ring::kStages> cur;
+        int item = 0, issued = 0, key = 0;
         bool ok = true;
-        // one item: its metadata, then its stages (lane 0 copies)
-        auto issue = [&](int group, const uint8_t* W, int row0, int blk, int mt, int key, int tok, int slot, float sc) {
-            const W4Block& b = bg[group];
+        // one item: its metadata, then its stages (lane 0 copies); new_rows: its token rows are not
+        // those of the item before
+        auto issue = [&](const W4Block& b, int group, const uint8_t* W, int row0, int blk, int mt, bool new_rows, int tok,
+                         int slot, float sc) {
             const int strip0 = blk * b.ns, ns = min(b.ns, b.strips - strip0);
-            for (int slab = 0; slab < b.nslab && ok; ++slab, ++it) {
-                const int s = it % Ring::kStages;
-                ok = mbar_wait(&empty[s], (((uint32_t)(it / Ring::kStages)) & 1u) ^ 1u, limit);
-                ok = __all_sync(0xffffffffu, ok);
+            if (new_rows) ++key;
+            for (int slab = 0; slab < b.nslab && ok; ++slab) {
+                ok = w4_wait(&empty[cur.s], cur.ph ^ 1u, limit);
                 if (!ok) break;
+                const int mslot = item % Ring::kMetas;
                 if (slab == 0) {
-                    W4Meta& m = metas[item % Ring::kMetas];
+                    W4Meta& m = metas[mslot];
                     if (lane < kW4Tok) {
                         m.tok[lane] = tok;
                         m.slot[lane] = slot;
@@ -162,33 +202,41 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                         m.mt = mt;
                         m.row0 = row0;
                         m.strip0 = strip0;
-                        m.key = key;
+                        m.n = ns;
                     }
-                    __syncwarp();
-                }
-                if (lane == 0) {
-                    const int recs = b.nslab == 1 ? ns * b.R : min(16, b.R - 16 * slab);
-                    const uint32_t bytes = (uint32_t)(recs * kRec);
-                    mbar_arrive_expect_tx(&full[s], bytes);
-                    bulk_load(stages + (size_t)s * Ring::kStage, W + ((size_t)strip0 * b.R + 16 * slab) * kRec, bytes,
-                              &full[s]);
+                } else {
+                    ++key;
                 }
                 __syncwarp();
+                if (lane == 0) {
+                    const int recs = min(kW4StageRecs, b.R - kW4StageRecs * slab);
+                    sm[cur.s] = W4Stage{key, ns | recs << 8 | (slab == b.nslab - 1 ? 1 << 16 : 0), slab, mslot};
+                    const uint32_t bytes = (uint32_t)((b.nslab == 1 ? ns * recs : recs) * kRec);
+                    mbar_arrive_expect_tx(&full[cur.s], bytes);
+                    bulk_load(stages + (size_t)cur.s * Ring::kStage, W + ((size_t)strip0 * b.R + kW4StageRecs * slab) * kRec,
+                              bytes, &full[cur.s]);
+                }
+                __syncwarp();
+                cur.next();
+                ++issued;
             }
+            if (b.nslab > 1) ++key;  // the next item starts at the first column range again
             ++item;
         };
-        const int n0 = bg[0].blocks * ((p.T + kW4Tok - 1) / kW4Tok);  // group 0: (token tile, block) order
+        const int n0 = p.b0.blocks * ((p.T + kW4Tok - 1) / kW4Tok);  // group 0: (token tile, block) order
         const int i0 = (int)((long long)c_ * n0 / G_), i1 = (int)((long long)(c_ + 1) * n0 / G_);
         if (WHICH == kW4Linear) {
             grid_dep_wait();
             grid_dep_launch();
         }
+        int ptile = -1;
         for (int i = i0; i < i1 && ok; ++i) {
-            const int tile = i / bg[0].blocks, t0 = tile * kW4Tok, mt = min(kW4Tok, p.T - t0);
+            const int tile = i / p.b0.blocks, t0 = tile * kW4Tok, mt = min(kW4Tok, p.T - t0);
             const int tok = t0 + (lane < mt ? lane : 0);
             const uint8_t* W = WHICH == kW4Linear ? p.w : reinterpret_cast<const uint8_t*>(WHICH == kW4Up ? a.sgu : a.sd);
             const float sc = WHICH == kW4Down ? a.sgate[tok] : 0.f;
-            issue(0, W, (WHICH == kW4Linear ? 0 : (int)a.P) + t0, i - tile * bg[0].blocks, mt, -1 - t0, tok, a.K, sc);
+            issue(p.b0, 0, W, (WHICH == kW4Linear ? 0 : (int)a.P) + t0, i - tile * p.b0.blocks, mt, tile != ptile, tok, a.K, sc);
+            ptile = tile;
         }
         if (WHICH != kW4Linear) {
             if (WHICH == kW4Up) {
@@ -196,7 +244,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                 grid_dep_launch();  // the routing is complete: the down kernel may start
             }
             // routed items in (expert, token tile, block) order: tiles[g] = first item of group g
-            const int n_act = a.hdr->n_act, blocks = bg[1].blocks;
+            const int n_act = a.hdr->n_act, blocks = p.b1.blocks;
             int run = 0;
             for (int b0 = 0; b0 < n_act; b0 += 32) {
                 const int g = b0 + lane;
@@ -230,7 +278,8 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                     ctile = -1;
                 }
                 const int local = q - tiles[g], tile = local / blocks, h0 = off + tile * kW4Tok;
-                if (tile != ctile) {
+                const bool fresh = tile != ctile;
+                if (fresh) {
                     ctile = tile;
                     mt = min(kW4Tok, cnt - tile * kW4Tok);
                     const int pv = a.perm[h0 + (lane < mt ? lane : 0)];
@@ -239,58 +288,54 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                     if (WHICH == kW4Down) sc = a.topw[pv];
                 }
                 const uint8_t* W = reinterpret_cast<const uint8_t*>(WHICH == kW4Up ? a.gate_up : a.down);
-                issue(1, W + (size_t)e * p.matrix_bytes, h0, local - tile * blocks, mt, h0, tok, slot, sc);
+                issue(p.b1, 1, W + (size_t)e * p.matrix_bytes, h0, local - tile * blocks, mt, fresh, tok, slot, sc);
             }
         }
         // the end of the items, as one more stage without copies
         if (ok) {
-            const int s = it % Ring::kStages;
-            ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], (((uint32_t)(it / Ring::kStages)) & 1u) ^ 1u, limit));
+            ok = w4_wait(&empty[cur.s], cur.ph ^ 1u, limit);
             if (ok && lane == 0) {
                 for (int j = 0; j < kW4EpiWarps; ++j) metas[(item + j) % Ring::kMetas].group = -1;
-                mbar_arrive(&full[s]);
+                sm[cur.s] = W4Stage{key, 0, 0, 0};
+                mbar_arrive(&full[cur.s]);
             }
         }
         if (!ok && lane == 0) atomicOr(p.err, ERR_TIMEOUT);
         // every copy issued must land before the CTA's shared memory is released (the end mark's stage
         // was free, so its last copy has landed)
         if (lane == 0)
-            for (int k = 0; k < Ring::kStages - (ok ? 1 : 0) && it - 1 - k >= 0; ++k) {
-                const int j = it - 1 - k;
+            for (int k = 0; k < Ring::kStages - (ok ? 1 : 0) && issued - 1 - k >= 0; ++k) {
+                const int j = issued - 1 - k;
                 if (!mbar_wait(&full[j % Ring::kStages], ((uint32_t)(j / Ring::kStages)) & 1u, limit))
                     atomicOr(p.err, ERR_TIMEOUT);
             }
-    } else if (warp < kWarps) {
+    } else if (warp < kW4Warps) {
         // ---------------- consumers
         if (WHICH != kW4Up) grid_dep_wait();  // the token rows (linear) or the h rows (down)
         if (WHICH == kW4Down) grid_dep_launch();
         uint32_t b[2][1][16];
         float acc[1][4] = {};
-        int ckey = 0x7fffffff, cslab = -1, slab = 0, cgroup = -1;
-        int it = 0, item = 0;
-        for (;; ++it) {
-            const int s = it % Ring::kStages;
-            bool ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ((uint32_t)(it / Ring::kStages)) & 1u, limit));
-            const W4Meta& m = metas[item % Ring::kMetas];
-            const int group = ok ? m.group : -1;
-            const int rb = item % kW4RedBufs;
-            if (group < 0) {
-                // the end: passed on to each epilogue warp as one more item
-                for (int j = item; j < item + kW4EpiWarps && ok; ++j) {
-                    ok = mbar_wait(&rempty[j % kW4RedBufs], (((uint32_t)(j / kW4RedBufs)) & 1u) ^ 1u, limit);
-                    if (ok && lane == 0) mbar_arrive(&rfull[j % kW4RedBufs]);
-                }
-                if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicOr(p.err, ERR_TIMEOUT);
-                break;
-            }
-            const W4Block& bk = bg[group];
-            const int wl = bk.wl, sub = warp >> wl, kq = warp & ((1 << wl) - 1);
-            const int Rs = bk.nslab == 1 ? bk.R : min(16, bk.R - 16 * slab);
-            const int nrec = max(0, min(2, Rs - 2 * kq));
-            if (m.key != ckey || slab != cslab || group != cgroup) {
-                ckey = m.key;
-                cslab = slab;
-                cgroup = group;
+        int ckey = -1, sub = 0, nrec = 0;
+        uint32_t at = 0;  // this warp's records within a stage
+        W4Cursor<Ring::kStages> cur;
+        W4Cursor<kW4RedBufs> rcur;
+        const uint32_t st0 = smem_u32(stages);
+        const uint32_t red0 = smem_u32(red) + (uint32_t)(warp * 512 + lane * 16);
+        bool ok;
+        for (;;) {
+            ok = w4_wait(&full[cur.s], cur.ph, limit);
+            if (!ok) break;
+            const W4Stage st = sm[cur.s];
+            if (st.info == 0) break;
+            if (st.key != ckey) {
+                ckey = st.key;
+                const W4Meta& m = metas[st.meta];
+                const bool routed = m.group != 0;
+                const int wl = routed ? p.b1.wl : p.b0.wl, rpw = routed ? p.b1.rpw : p.b0.rpw;
+                const int recs = (st.info >> 8) & 0xff, kq = warp & ((1 << wl) - 1);
+                sub = warp >> wl;
+                nrec = max(0, min(rpw, recs - rpw * kq));
+                at = (uint32_t)((sub * recs + rpw * kq) * kRec);
                 const int n = lane >> 2;
                 const bool live = n < m.mt;
                 const bf16* row;
@@ -300,48 +345,61 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                     row = a.x + (size_t)m.tok[n] * a.H;
                 else
                     row = a.h + (size_t)(m.row0 + (live ? n : 0)) * a.Imax;
-                w4_load_frag(b, row, live, 16 * slab + 2 * kq, nrec, p.cols[group], lane);
+                const int cols = routed ? p.cols[1] : p.cols[0];
+                const int k0 = (st.slab * kW4StageRecs + rpw * kq) * kW4Cols;
+                w4_load_tokens(b[0], row, live && nrec > 0, k0, cols, lane);
+                w4_load_tokens(b[1], row, live && nrec > 1, k0 + kW4Cols, cols, lane);
             }
-            if (sub < min(bk.ns, bk.strips - m.strip0)) {
-                const uint32_t rec = smem_u32(stages + (size_t)s * Ring::kStage) + (uint32_t)((sub * Rs + 2 * kq) * kRec);
-                if (nrec > 0) w4_mma_record<FMT, G, 1>(rec, b[0], acc, lane);
-                if (nrec > 1) w4_mma_record<FMT, G, 1>(rec + kRec, b[1], acc, lane);
+            if (sub < (st.info & 0xff) && nrec > 0) {
+                const uint32_t rec = st0 + (uint32_t)(cur.s * Ring::kStage) + at;
+                W4Frag<FMT, G> f0, f1;
+                w4_load<FMT, G>(rec, lane, f0);
+                if (nrec > 1) w4_load<FMT, G>(rec + kRec, lane, f1);
+                w4_mma_record<FMT, G, 1>(f0, b[0], acc);
+                if (nrec > 1) w4_mma_record<FMT, G, 1>(f1, b[1], acc);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
-            if (++slab == bk.nslab) {
-                slab = 0;
-                const bool free = __all_sync(0xffffffffu, mbar_wait(&rempty[rb], (((uint32_t)(item / kW4RedBufs)) & 1u) ^ 1u, limit));
-                if (!free) {
-                    if (lane == 0) atomicOr(p.err, ERR_TIMEOUT);
-                    break;
-                }
-                *reinterpret_cast<float4*>(red + ((rb * kWarps + warp) * 32 + lane) * 4) =
-                    make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+            if (lane == 0) mbar_arrive(&empty[cur.s]);
+            cur.next();
+            if (st.info >> 16) {
+                ok = w4_wait(&rempty[rcur.s], rcur.ph ^ 1u, limit);
+                if (!ok) break;
+                const uint32_t v[4] = {__float_as_uint(acc[0][0]), __float_as_uint(acc[0][1]), __float_as_uint(acc[0][2]),
+                                       __float_as_uint(acc[0][3])};
+                sts128(red0 + (uint32_t)(rcur.s * kW4Warps * 512), v);
                 acc[0][0] = acc[0][1] = acc[0][2] = acc[0][3] = 0.f;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&rfull[rb]);
-                ++item;
+                if (lane == 0) mbar_arrive(&rfull[rcur.s]);
+                rcur.next();
             }
         }
+        // the end: passed on to each epilogue warp as one more item
+        for (int j = 0; j < kW4EpiWarps && ok; ++j) {
+            ok = w4_wait(&rempty[rcur.s], rcur.ph ^ 1u, limit);
+            if (ok && lane == 0) mbar_arrive(&rfull[rcur.s]);
+            rcur.next();
+        }
+        if (!ok && lane == 0) atomicOr(p.err, ERR_TIMEOUT);
     } else {
         // ---------------- epilogue: warp e takes items e, e + kW4EpiWarps, ...
         const int g8 = lane >> 2, t2 = 2 * (lane & 3);
-        for (int item = warp - kWarps - 1;; item += kW4EpiWarps) {
+        for (int item = warp - kW4Warps - 1;; item += kW4EpiWarps) {
             const int rb = item % kW4RedBufs;
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(&rfull[rb], ((uint32_t)(item / kW4RedBufs)) & 1u, limit));
+            const bool ok = w4_wait(&rfull[rb], ((uint32_t)(item / kW4RedBufs)) & 1u, limit);
             const W4Meta& m = metas[item % Ring::kMetas];
             if (!ok || m.group < 0) {
                 if (!ok && lane == 0) atomicOr(p.err, ERR_TIMEOUT);
                 break;
             }
-            const W4Block& bk = bg[m.group];
-            const int ns = min(bk.ns, bk.strips - m.strip0), mt = m.mt;
+            const int W = 1 << (m.group ? p.b1.wl : p.b0.wl), ns = m.n, mt = m.mt;
+            const uint32_t r0 = smem_u32(red) + (uint32_t)(rb * kW4Warps * 512 + lane * 16);
             for (int sub = 0; sub < ns; ++sub) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int k = 0; k < (1 << bk.wl); ++k) {
-                    const float4 q = *reinterpret_cast<const float4*>(red + ((rb * kWarps + (sub << bk.wl) + k) * 32 + lane) * 4);
-                    v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
+#pragma unroll 4
+                for (int k = 0; k < W; ++k) {
+                    const uint4 q = lds128_smem(r0 + (uint32_t)((sub * W + k) * 512));
+                    v.x += __uint_as_float(q.x); v.y += __uint_as_float(q.y);
+                    v.z += __uint_as_float(q.z); v.w += __uint_as_float(q.w);
                 }
                 const int strip = m.strip0 + sub;
                 if (WHICH == kW4Up) {
@@ -355,13 +413,8 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                         if (t2 + j < mt) {
                             const size_t y = ((size_t)m.tok[t2 + j] * (a.K + 1) + m.slot[t2 + j]) * a.H + row;
                             const float sc = m.sc[t2 + j], y0 = sc * (j ? v.y : v.x), y1 = sc * (j ? v.w : v.z);
-                            if (a.gemm) {
-                                a.Yb[y] = __float2bfloat16_rn(y0);
-                                a.Yb[y + 8] = __float2bfloat16_rn(y1);
-                            } else {
-                                a.Y[y] = y0;
-                                a.Y[y + 8] = y1;
-                            }
+                            a.Y[y] = y0;
+                            a.Y[y + 8] = y1;
                         }
                 } else {
                     const int N = p.rows[0], row = strip * 16 + g8;

@@ -53,11 +53,17 @@ def sum_error(cols: int) -> float:
     return (cols / 16 + cols / 32 + 8) * 2.0 ** -22
 
 
-def linear(x, w, bias):
-    """x . w^T + bias and the bound of a correct result's error. w in 64 bits."""
+GEMM_TOKENS = 64  # tokens from which the linear layer takes the tensor-core path
+
+
+def linear(x, w, bias, rounded=False):
+    """x . w^T + bias and the bound of a correct result's error. w in 64 bits. rounded: the tensor-core
+    path, which rounds each weight w to bf16 once, at most HALF |w| off: HALF sum |x w| on the sum. The
+    error of the sum before the last rounding is itself rounded with it: (1 + HALF)."""
     x = x.double()
     ref = x @ w.T + (0.0 if bias is None else bias.double())
-    return ref, HALF * ref.abs() + sum_error(w.shape[1]) * (x.abs() @ w.abs().T) + 1e-30
+    before = (sum_error(w.shape[1]) + (HALF if rounded else 0.0)) * (x.abs() @ w.abs().T)
+    return ref, HALF * ref.abs() + (1 + HALF) * before + 1e-30
 
 
 def layer(dims, x, router_w, router_b, shared_gate, gu, dn, sgu, sdn, residual, ids=None, weight_half=0.0, y_half=0.0,
