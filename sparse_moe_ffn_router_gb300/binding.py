@@ -25,7 +25,8 @@ EXPORTED = ["moe_workspace_size", "moe_workspace_init", "moe_route", "moe_forwar
 KERNELS = {"router_scores": 0, "router_topk": 1, "dispatch_local": 2, "dispatch_scan": 3, "dispatch_scatter": 4,
            "gate_up": 5, "down": 6, "combine": 7, "rmsnorm": 8, "shared_gate": 9, "gather": 10, "gemm_plan": 11,
            "decode_fused": 12, "router_stats": 13, "fetch_experts": 14,
-           "copy_rows": 15, "w4_pack": 16, "w4_linear": 17}
+           "copy_rows": 15, "w4_pack": 16, "w4_linear": 17,
+           "w4_fused": 18}
 
 
 # moe_dims.flags: router and shared-gate scores rounded to bf16 before ranking and sigmoid

@@ -127,6 +127,7 @@ moe_status prepare(const moe_dims* d, const void* x, const moe_weights* w, void*
     a->uprec = p->T <= kRecTokens ? (UpRec*)(base + p->o_uprec) : nullptr;
     a->dlog = p->T <= kRecTokens ? (uint64_t*)(base + p->o_dlog) : nullptr;
     a->dh = p->T <= kRecTokens ? (uint64_t*)(base + p->o_dh) : nullptr;
+    a->dh4 = p->T == 1 ? (uint64_t*)(base + p->o_dh4) : nullptr;
     a->dx = p->T == 1 ? (uint64_t*)(base + p->o_dx) : nullptr;
     a->gemm = p->gemm;
     a->x_host = false;
@@ -535,6 +536,7 @@ extern "C" moe_status moe_forward_w4(const moe_dims* d, const moe_w4_format* f, 
     a.residual = (const bf16*)residual;
     a.out = (bf16*)out;
     cudaStream_t s = (cudaStream_t)stream;
+    if (w4_one_supported(a, *f)) return cuda_status(launch_w4_one(a, *f, s));
     cudaError_t e = launch_routing(a, s);
     if (e == cudaSuccess) e = launch_w4_experts(a, *f, s);
     return cuda_status(e);

@@ -43,6 +43,7 @@ struct LayerArgs {
     UpRec* uprec;     // routed gate_up records (few-token path), nullptr when not produced
     uint64_t* dlog;   // [T, E+1] router scores tagged with their call (fused few-token kernel)
     uint64_t* dh;     // [P+T, Imax/2] gated activation pairs tagged with their call (same kernel)
+    uint64_t* dh4;    // [K+1, Imax/2] gated activation pairs tagged with their call (4-bit weights, T = 1)
     uint64_t* dx;     // [H/2] the token row's 32-bit words tagged with their call (T = 1, host rows)
     WsHeader* hdr;
     uint64_t wait_ns;   // time limit of the bounded waits of the one-token and streaming kernels
@@ -145,6 +146,9 @@ cudaError_t launch_w4_dequantize(const moe_w4_format& f, int n, int rows, int co
 cudaError_t launch_w4_linear(const moe_w4_format& f, const W4LinearArgs& l, cudaStream_t s);
 // Gate_up, down and combine of a layer whose expert weights are packed (a.gate_up .. a.sd).
 cudaError_t launch_w4_experts(const LayerArgs& a, const moe_w4_format& f, cudaStream_t s);
+// The whole such layer in one kernel (one token).
+bool w4_one_supported(const LayerArgs& a, const moe_w4_format& f);
+cudaError_t launch_w4_one(const LayerArgs& a, const moe_w4_format& f, cudaStream_t s);
 cudaError_t launch_rmsnorm(const bf16* x, const bf16* gamma, float eps, bf16* xn, int T, int H, cudaStream_t s);
 
 }  // namespace moe

@@ -145,16 +145,15 @@ __device__ __forceinline__ void w4_mma_record(const W4Frag<FMT, G>& f, const uin
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int gi = c * 32 / G;
-        if (c * 32 % G == 0) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
-        }
         uint32_t p[4], q[4];
         w4_decode<FMT>(w0[c], w4_bias(f, 0, gi), p);
         w4_decode<FMT>(w1[c], w4_bias(f, 1, gi), q);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            mma16816(d[n], p[0], q[0], p[1], q[1], b[n][4 * c], b[n][4 * c + 1]);
+            if (c * 32 % G == 0)
+                mma16816_first(d[n], p[0], q[0], p[1], q[1], b[n][4 * c], b[n][4 * c + 1]);
+            else
+                mma16816(d[n], p[0], q[0], p[1], q[1], b[n][4 * c], b[n][4 * c + 1]);
             mma16816(d[n], p[2], q[2], p[3], q[3], b[n][4 * c + 2], b[n][4 * c + 3]);
         }
         if ((c + 1) * 32 % G == 0) {

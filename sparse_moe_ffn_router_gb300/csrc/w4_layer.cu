@@ -1,7 +1,7 @@
 // w4_layer.cu -- launch sequences of the products on packed 4-bit weights: the linear layer and
 // the experts of the MoE layer (the routing before and the combine after are the layer's own).
 #include "w4_gemm.cuh"
-#include "w4_stream.cuh"
+#include "w4_one.cuh"
 
 namespace moe {
 
@@ -126,6 +126,36 @@ cudaError_t launch_w4_experts(const LayerArgs& a, const moe_w4_format& f, cudaSt
     e = launch_w4_stream(f.format, f.group, kW4Down, p, s);
     if (e != cudaSuccess) return e;
     return launch_combine_pdl(a, s);
+}
+
+static cudaError_t w4_one(int format, int group, const W4OneArgs* p, cudaStream_t s) {
+    switch (format) {
+        case MOE_W4_INT4: return w4_one_int4(group, p, s);
+        case MOE_W4_INT4_ZP: return w4_one_int4_zp(group, p, s);
+        case MOE_W4_E2M1: return w4_one_e2m1(group, p, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// One token, strips of at most one stage (H <= 4096), sums that fit, one CTA per SM.
+bool w4_one_supported(const LayerArgs& a, const moe_w4_format& f) {
+    return a.T == 1 && a.H <= kW4StageRecs * kW4Cols && a.K <= kOneMaxK && w4_one_strips(a, a.num_sms) <= kOneMaxUp && a.dlog &&
+           a.dh4 && w4_one(f.format, f.group, nullptr, nullptr) == cudaSuccess;
+}
+
+// The whole layer of one token in one kernel.
+cudaError_t launch_w4_one(const LayerArgs& a, const moe_w4_format& f, cudaStream_t s) {
+    W4OneArgs p = {};
+    p.a = a;
+    p.dh = a.dh4;
+    p.gu_bytes = w4_matrix_bytes(f.format, f.group, 2 * a.I, a.H);
+    p.dn_bytes = w4_matrix_bytes(f.format, f.group, a.H, a.I);
+    p.R = (a.H + kW4Cols - 1) / kW4Cols;
+    const W4Block d = w4_block(a.H, a.Imax, kW4Warps);
+    p.dwl = d.wl;
+    p.drpw = d.rpw;
+    p.dR = d.R;
+    return w4_one(f.format, f.group, &p, s);
 }
 
 }  // namespace moe

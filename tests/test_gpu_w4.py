@@ -344,3 +344,40 @@ def test_quantised_stack_of_layers():
         check(out, *ref.layer(dims, xn, router, None, gate, v["gate_up"], v["down"], v["shared_gate_up"][0], v["shared_down"][0], x,
                               ids=ids))
         x = out
+
+
+def test_layer_one_workspace_for_many_calls():
+    """One workspace for calls of several token counts and both kinds of weights, in turn."""
+    dims = lambda T: (T, 512, 32, 4, 128, 128)  # noqa: E731
+    ws = moe.new_workspace(dims(300))
+    layers = {T: W4Layer(dims(T), "int4", 32, seed=70 + T) for T in (1, 3, 8, 20, 300)}
+    dense = {}
+    L = layers[1]
+    for k, rows, cols in (("gate_up", 256, 512), ("down", 512, 128), ("shared_gate_up", 256, 512), ("shared_down", 512, 128)):
+        dense[k] = torch.empty(L.m[k][0].shape[0], rows, cols, dtype=torch.bfloat16, device="cuda")
+        moe.moe_w4_dequantize(ref.fmt("int4", 32), getattr(L.W, k), dense[k], k.endswith("gate_up"))
+    W = moe.Weights(L.router_w, None, dense["gate_up"], dense["down"], dense["shared_gate_up"], dense["shared_down"], L.shared_gate)
+    first = {}
+    for _ in range(4):
+        for T, M in layers.items():
+            out = M.run(ws=ws)
+            if T not in first:
+                check(out, *M.reference())
+                first[T] = out
+            assert torch.equal(out, first[T])
+            moe.moe_forward(dims(1), L.x, W, L.residual, torch.empty_like(L.x), ws)
+    assert moe.moe_last_device_error(ws) == 0
+
+
+def test_layer_wait_timeout_ends_the_call():
+    """A CTA that keeps its router scores back: the call ends with the timeout in the workspace."""
+    L = W4Layer((1, 512, 32, 4, 128, 128), "int4", 32, seed=1)
+    ws, out = moe.new_workspace(L.dims), torch.empty_like(L.x)
+    moe.moe_test_set_wait(20_000_000, moe.TEST_SUPPRESS_SCORE)
+    try:
+        moe.moe_forward_w4(L.dims, ref.fmt("int4", 32), L.x, L.W, L.residual, out, ws)
+        assert moe.moe_last_device_error(ws) == 6
+    finally:
+        moe.moe_test_set_wait()
+    moe.moe_workspace_init(ws)
+    check(L.run(ws=ws), *L.reference())
