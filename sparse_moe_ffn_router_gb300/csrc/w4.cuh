@@ -52,18 +52,26 @@ struct W4Rec {
     static constexpr int kZeros = kW4Codes + 32 * kGroups;
 };
 
-__device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
+// Packed bf16 sums and products, one instruction each (the header functions take more).
+__device__ __forceinline__ uint32_t bf2_add(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
 }
 __device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // The eight values of a word as four bf16 pairs, columns (0, 1), (2, 3), (4, 5), (6, 7); exact.
 // Integer codes: 0x43 in the upper byte of a bf16 and the code in the lower bits is 128 + code;
-// `bias` holds 128 + the zero point in both halves. E2M1: the three magnitude bits put at the
+// `bias` holds -(128 + the zero point) in both halves. E2M1: the three magnitude bits put at the
 // lowest exponent bits and the highest mantissa bit read as the value times 2^-126 (0.5 as a
 // subnormal), so one multiplication by 2^126 gives it; the packed bit order makes that two
 // instructions a pair for three of the four (include/moe.h).
@@ -79,7 +87,30 @@ __device__ __forceinline__ void w4_decode(uint32_t w, uint32_t bias, uint32_t (&
         for (int i = 0; i < 4; ++i) p[i] = bf2_mul(p[i], 0x7e807e80u);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = bf2_sub(((w >> (4 * i)) & 0x000f000fu) | 0x43004300u, bias);
+        for (int i = 0; i < 4; ++i) p[i] = bf2_add(((w >> (4 * i)) & 0x000f000fu) | 0x43004300u, bias);
+    }
+}
+
+// The values as the MMA kernels use them: integer codes a quarter (kUnfold = 4 undoes it on the sums),
+// which takes two shifts a word less than w4_decode. Codes 0 and 2 of a half go through 128 + code,
+// times 1/4. Codes 1 and 3, in bits 4 .. 7, are read as they lie: a bf16 with only its lowest exponent
+// bit and its three highest mantissa bits is linear in them (subnormals and the first binade have one
+// spacing), code * 2^-129; times 2^127 that is code / 4. Every value is exact. b0, b1: -(128 + zero
+// point) / 4 and -(zero point) / 4 in both halves.
+template <int FMT>
+struct W4Fold {
+    static constexpr float kUnfold = FMT == MOE_W4_E2M1 ? 1.f : 4.f;
+};
+template <int FMT>
+__device__ __forceinline__ void w4_decode_fold(uint32_t w, uint32_t b0, uint32_t b1, uint32_t (&p)[4]) {
+    if (FMT == MOE_W4_E2M1) {
+        w4_decode<FMT>(w, 0u, p);
+    } else {
+        const uint32_t h = w >> 8;
+        p[0] = bf2_fma((w & 0x000f000fu) | 0x43004300u, 0x3e803e80u, b0);
+        p[1] = bf2_fma(w & 0x00f000f0u, 0x7f007f00u, b1);
+        p[2] = bf2_fma((h & 0x000f000fu) | 0x43004300u, 0x3e803e80u, b0);
+        p[3] = bf2_fma(h & 0x00f000f0u, 0x7f007f00u, b1);
     }
 }
 
@@ -92,36 +123,56 @@ struct W4Frag {
     uint32_t z[2];
 };
 
-template <int FMT, int G>
-__device__ __forceinline__ void w4_load(uint32_t rec, int lane, W4Frag<FMT, G>& f) {
-    constexpr int N = W4Rec<FMT, G>::kGroups;
-    f.lo = lds128_smem(rec + (uint32_t)lane * 16u);
-    f.hi = lds128_smem(rec + 512u + (uint32_t)lane * 16u);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t row = (uint32_t)(lane >> 2) + 8u * h, at = rec + W4Rec<FMT, G>::kScales + row * (2u * N);
+// Shared-memory loads at a register address and a constant offset (no address arithmetic a load).
+template <int OFF>
+__device__ __forceinline__ uint4 lds128_at(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr), "n"(OFF) : "memory");
+    return v;
+}
+
+// at: of the record + 16 * lane; meta: of the record + 2 * N * (lane / 4) (scales), zmeta: + N * (lane / 4).
+template <int FMT, int G, int OFF>
+__device__ __forceinline__ void w4_load_at(uint32_t at, uint32_t meta, uint32_t zmeta, W4Frag<FMT, G>& f) {
+    constexpr int N = W4Rec<FMT, G>::kGroups, kS = OFF + W4Rec<FMT, G>::kScales, kZ = OFF + W4Rec<FMT, G>::kZeros;
+    f.lo = lds128_at<OFF>(at);
+    f.hi = lds128_at<OFF + 512>(at);
+    if constexpr (N == 4) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];" : "=r"(f.s[0][0]), "=r"(f.s[0][1]) : "r"(meta), "n"(kS));
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];" : "=r"(f.s[1][0]), "=r"(f.s[1][1]) : "r"(meta), "n"(kS + 16 * N));
+    } else if constexpr (N == 2) {
+        asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(f.s[0][0]) : "r"(meta), "n"(kS));
+        asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(f.s[1][0]) : "r"(meta), "n"(kS + 16 * N));
+    } else {
+        uint16_t v0, v1;
+        asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(v0) : "r"(meta), "n"(kS));
+        asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(v1) : "r"(meta), "n"(kS + 16 * N));
+        f.s[0][0] = v0;
+        f.s[1][0] = v1;
+    }
+    f.z[0] = f.z[1] = 0;
+    if constexpr (FMT == MOE_W4_INT4_ZP) {
         if constexpr (N == 4) {
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(f.s[h][0]), "=r"(f.s[h][1]) : "r"(at));
+            asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(f.z[0]) : "r"(zmeta), "n"(kZ));
+            asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(f.z[1]) : "r"(zmeta), "n"(kZ + 8 * N));
         } else if constexpr (N == 2) {
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(f.s[h][0]) : "r"(at));
+            uint16_t v0, v1;
+            asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(v0) : "r"(zmeta), "n"(kZ));
+            asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(v1) : "r"(zmeta), "n"(kZ + 8 * N));
+            f.z[0] = v0;
+            f.z[1] = v1;
         } else {
-            uint16_t v;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-            f.s[h][0] = v;
-        }
-        f.z[h] = 0;
-        if (FMT == MOE_W4_INT4_ZP) {
-            const uint32_t za = rec + W4Rec<FMT, G>::kZeros + row * N;
-            if (N == 4)
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(f.z[h]) : "r"(za));
-            else if (N == 2) {
-                uint16_t v;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(za));
-                f.z[h] = v;
-            } else
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(f.z[h]) : "r"(za));
+            asm volatile("ld.shared.u8 %0, [%1 + %2];" : "=r"(f.z[0]) : "r"(zmeta), "n"(kZ));
+            asm volatile("ld.shared.u8 %0, [%1 + %2];" : "=r"(f.z[1]) : "r"(zmeta), "n"(kZ + 8 * N));
         }
     }
+}
+
+template <int FMT, int G>
+__device__ __forceinline__ void w4_load(uint32_t rec, int lane, W4Frag<FMT, G>& f) {
+    constexpr uint32_t N = W4Rec<FMT, G>::kGroups;
+    const uint32_t row = (uint32_t)lane >> 2;
+    w4_load_at<FMT, G, 0>(rec + 16u * (uint32_t)lane, rec + 2u * N * row, rec + N * row, f);
 }
 
 template <int FMT, int G>
@@ -130,11 +181,37 @@ __device__ __forceinline__ float w4_scale(const W4Frag<FMT, G>& f, int h, int gi
 }
 template <int FMT, int G>
 __device__ __forceinline__ uint32_t w4_bias(const W4Frag<FMT, G>& f, int h, int gi) {
-    if (FMT != MOE_W4_INT4_ZP) return 0x43084308u;
-    return 0x43004300u | (((f.z[h] >> (8 * gi)) & 0xffu) * 0x00010001u);
+    if (FMT != MOE_W4_INT4_ZP) return 0xc308c308u;
+    // 0xc3zz in both halves: byte gi of the zero points below 0xc3
+    return __byte_perm(f.z[h], 0xc3u, 0x4040u | (uint32_t)(gi << 8) | (uint32_t)gi);
 }
 
-// acc += one record (16 rows by 128 columns) times NT tiles of 8 tokens. b[n][4 c + i] are the B
+// m16n8k16 bf16 MMAs, fp32 accumulate (not volatile: the compiler may interleave independent records).
+__device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void w4_mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {  // onto a zero accumulator
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// b0 and b1 of w4_decode_fold.
+template <int FMT, int G>
+__device__ __forceinline__ void w4_bias_fold(const W4Frag<FMT, G>& f, int h, int gi, uint32_t& b0, uint32_t& b1) {
+    b0 = 0xc208c208u;  // -34
+    b1 = 0xc000c000u;  // -2
+    if (FMT == MOE_W4_INT4_ZP) {
+        b0 = __byte_perm(f.z[h], 0xc2u, 0x4040u | (uint32_t)(gi << 8) | (uint32_t)gi);
+        b1 = bf2_add(b0, 0x42004200u);  // + 32
+    }
+}
+
+// acc += one record (16 rows by 128 columns) times NT tiles of 8 tokens, W4Fold::kUnfold times too small. b[n][4 c + i] are the B
 // operands of lane 4g + t: token g of tile n, columns 32 c + 8 t + 2 i, + 1. acc is the m16n8
 // accumulator of each tile: rows g (0, 1) and g + 8 (2, 3), tokens 2t (0, 2) and 2t + 1 (1, 3).
 // Each group's sum starts at zero and is scaled in fp32.
@@ -146,15 +223,18 @@ __device__ __forceinline__ void w4_mma_record(const W4Frag<FMT, G>& f, const uin
     for (int c = 0; c < 4; ++c) {
         const int gi = c * 32 / G;
         uint32_t p[4], q[4];
-        w4_decode<FMT>(w0[c], w4_bias(f, 0, gi), p);
-        w4_decode<FMT>(w1[c], w4_bias(f, 1, gi), q);
+        uint32_t b00, b01, b10, b11;
+        w4_bias_fold(f, 0, gi, b00, b01);
+        w4_bias_fold(f, 1, gi, b10, b11);
+        w4_decode_fold<FMT>(w0[c], b00, b01, p);
+        w4_decode_fold<FMT>(w1[c], b10, b11, q);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (c * 32 % G == 0)
-                mma16816_first(d[n], p[0], q[0], p[1], q[1], b[n][4 * c], b[n][4 * c + 1]);
+                w4_mma_first(d[n], p[0], q[0], p[1], q[1], b[n][4 * c], b[n][4 * c + 1]);
             else
-                mma16816(d[n], p[0], q[0], p[1], q[1], b[n][4 * c], b[n][4 * c + 1]);
-            mma16816(d[n], p[2], q[2], p[3], q[3], b[n][4 * c + 2], b[n][4 * c + 3]);
+                w4_mma(d[n], p[0], q[0], p[1], q[1], b[n][4 * c], b[n][4 * c + 1]);
+            w4_mma(d[n], p[2], q[2], p[3], q[3], b[n][4 * c + 2], b[n][4 * c + 3]);
         }
         if ((c + 1) * 32 % G == 0) {
             const float s0 = w4_scale(f, 0, gi), s1 = w4_scale(f, 1, gi);

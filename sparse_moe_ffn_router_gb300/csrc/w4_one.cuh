@@ -145,6 +145,7 @@ __device__ inline void w4o_route(const LayerArgs& a, W4OneRoute& rt, uint32_t ta
 
 // Between gate_up and down: a warp a gate_up strip adds its sums and publishes its h values, then the h
 // rows of all experts (slots, then the shared one) are gathered into shared memory, a warp a row.
+template <int FMT>
 __device__ __forceinline__ void w4o_exchange(const W4OneArgs& p, const W4OneRoute& rt, const float* part, uint8_t* hs, int hpitch,
                                           uint32_t tag, int n_sh, int n_up, int s0, int q0, uint32_t* err) {
     const LayerArgs& a = p.a;
@@ -158,6 +159,7 @@ __device__ __forceinline__ void w4o_exchange(const W4OneArgs& p, const W4OneRout
         if (lane < 16)
 #pragma unroll
             for (int w = 0; w < kW4Warps; ++w) v += part[(i * kW4Warps + w) * 16 + lane];
+        v *= W4Fold<FMT>::kUnfold;
         const float u = __shfl_down_sync(0xffffffffu, v, 8);
         const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(silu(v) * u));
         const uint32_t h1 = __shfl_down_sync(0xffffffffu, h, 1);
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kOneThreads, 1) k_w4_one(const __grid_constant
             ph ^= 1u;
         }
     }
-    w4o_exchange(p, rt, part, hs, hpitch, tag, n_sh, n_up, s0, q0, err);
+    w4o_exchange<FMT>(p, rt, part, hs, hpitch, tag, n_sh, n_up, s0, q0, err);
 
     // ---- down
     const int sub = warp >> p.dwl, kq = warp & ((1 << p.dwl) - 1), r0 = p.drpw * kq;
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(kOneThreads, 1) k_w4_one(const __grid_constant
                 y[j] = q[0];
                 if (p.dwl > 0) y[j] += q[16];
                 for (int k = 2; k < (1 << p.dwl); ++k) y[j] += q[k * 16];
-                y[j] *= e == K ? rt.sg : rt.w[e];
+                y[j] *= (e == K ? rt.sg : rt.w[e]) * W4Fold<FMT>::kUnfold;
             }
 #pragma unroll
             for (int j = 0; j < kHalf; ++j) {

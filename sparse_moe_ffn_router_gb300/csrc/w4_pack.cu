@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(256) k_w4_unpack(W4PackArgs a, int64_t records
                 if (k0 + 32 * c + 8 * t >= a.cols) continue;
                 const int gi = c * 32 / G;
                 const float s = __bfloat162float(reinterpret_cast<const bf16*>(rec + W4Rec<FMT, G>::kScales)[r * N + gi]);
-                uint32_t bias = 0x43084308u;
-                if (FMT == MOE_W4_INT4_ZP) bias = 0x43004300u | (rec[W4Rec<FMT, G>::kZeros + r * N + gi] * 0x00010001u);
+                uint32_t bias = 0xc308c308u;
+                if (FMT == MOE_W4_INT4_ZP) bias = 0xc300c300u | (rec[W4Rec<FMT, G>::kZeros + r * N + gi] * 0x00010001u);
                 uint32_t p[4];
                 w4_decode<FMT>(words[c], bias, p);
                 uint4 o;  // s * v in fp32 (exact: 8 and at most 5 bits), rounded once to bf16

@@ -103,13 +103,13 @@ struct W4Ring {
     static constexpr int kStage = kW4StageRecs * W4Rec<FMT, G>::kBytes;
     static constexpr int kRed = kW4RedBufs * kW4Warps * 128 * 4;
     static constexpr int kMaxMetas = 16, kMaxStages = 6;
-    static constexpr int kFixed = 128 + kRed + kMaxMetas * (int)sizeof(W4Meta) + kMaxStages * (int)sizeof(W4Stage) + 256 + 258 * 4;
+    static constexpr int kFixed = 128 + kRed + kMaxMetas * (int)sizeof(W4Meta) + kMaxStages * (int)sizeof(W4Stage) + 256 + 260 * 10;
     static constexpr int kFit = (kW4SmemMax - kFixed) / kStage;
     static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
     // an item's metadata is rewritten once its epilogue is done: at most this many items later
     static constexpr int kMetas = kStages + kW4RedBufs + 2;
     static_assert(kStage % 128 == 0 && kStages >= 3 && kMetas <= kMaxMetas, "ring");
-    static_assert((2 * kMaxStages + 2 * kW4RedBufs) * 8 <= 256 && sizeof(W4Meta) % 4 == 0, "barriers");
+    static_assert((2 * kMaxStages + 2 * kW4RedBufs) * 8 <= 256 && kMaxMetas * sizeof(W4Meta) % 8 == 0, "barriers");
     static constexpr int kBytes = kFixed + kStages * kStage;
 };
 
@@ -139,8 +139,28 @@ struct W4Cursor {
     }
 };
 
+// The group of item q: the largest g with tiles[g] <= q, after group `from`.
+__device__ __forceinline__ int w4_find(const int* tiles, int n, int from, int q) {
+    int lo = from < 0 ? 0 : from + 1, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tiles[mid] <= q) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
 __device__ __forceinline__ bool w4_wait(uint64_t* bar, uint32_t parity, uint64_t limit) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit));
+}
+
+// As w4_wait, on a shared-window address.
+__device__ __forceinline__ bool w4_wait32(uint32_t bar, uint32_t parity, uint64_t limit) {
+    if (__all_sync(0xffffffffu, mbar_try_wait32(bar, parity))) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_wait32(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, global_ns() - t0 > limit)) return false;
+    }
 }
 
 template <int WHICH, int FMT, int G>
@@ -158,6 +178,8 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
     uint64_t* rempty = rfull + kW4RedBufs;
     W4Meta* metas = reinterpret_cast<W4Meta*>(reinterpret_cast<uint8_t*>(full) + 256);
     int* tiles = reinterpret_cast<int*>(metas + Ring::kMaxMetas);
+    uint32_t* groups = reinterpret_cast<uint32_t*>(tiles + 260);  // routed groups: expert, first h row
+    uint16_t* counts = reinterpret_cast<uint16_t*>(groups + 260);
     const LayerArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t limit = p.wait_ns;
@@ -180,18 +202,28 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
         W4Cursor<Ring::kStages> cur;
         int item = 0, issued = 0, key = 0;
         bool ok = true;
-        // one item: its metadata, then its stages (lane 0 copies); new_rows: its token rows are not
-        // those of the item before
-        auto issue = [&](const W4Block& b, int group, const uint8_t* W, int row0, int blk, int mt, bool new_rows, int tok,
-                         int slot, float sc) {
+        // one item: for each of its stages the copy, then the metadata (which may still have to come from
+        // memory), then the arrival that lets the consumers in. new_rows: its token rows are not those of
+        // the item before. rows(): the lane's token, slot and scale.
+        auto issue = [&](const W4Block& b, int group, const uint8_t* W, int row0, int blk, int mt, bool new_rows, auto rows) {
             const int strip0 = blk * b.ns, ns = min(b.ns, b.strips - strip0);
             if (new_rows) ++key;
             for (int slab = 0; slab < b.nslab && ok; ++slab) {
                 ok = w4_wait(&empty[cur.s], cur.ph ^ 1u, limit);
                 if (!ok) break;
                 const int mslot = item % Ring::kMetas;
+                const int recs = min(kW4StageRecs, b.R - kW4StageRecs * slab);
+                if (lane == 0) {
+                    const uint32_t bytes = (uint32_t)((b.nslab == 1 ? ns * recs : recs) * kRec);
+                    mbar_expect_tx(&full[cur.s], bytes);
+                    bulk_load(stages + (size_t)cur.s * Ring::kStage, W + ((size_t)strip0 * b.R + kW4StageRecs * slab) * kRec,
+                              bytes, &full[cur.s]);
+                }
                 if (slab == 0) {
                     W4Meta& m = metas[mslot];
+                    int tok, slot;
+                    float sc;
+                    rows(tok, slot, sc);
                     if (lane < kW4Tok) {
                         m.tok[lane] = tok;
                         m.slot[lane] = slot;
@@ -207,16 +239,9 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                 } else {
                     ++key;
                 }
+                if (lane == 0) sm[cur.s] = W4Stage{key, ns | recs << 8 | (slab == b.nslab - 1 ? 1 << 16 : 0), slab, mslot};
                 __syncwarp();
-                if (lane == 0) {
-                    const int recs = min(kW4StageRecs, b.R - kW4StageRecs * slab);
-                    sm[cur.s] = W4Stage{key, ns | recs << 8 | (slab == b.nslab - 1 ? 1 << 16 : 0), slab, mslot};
-                    const uint32_t bytes = (uint32_t)((b.nslab == 1 ? ns * recs : recs) * kRec);
-                    mbar_arrive_expect_tx(&full[cur.s], bytes);
-                    bulk_load(stages + (size_t)cur.s * Ring::kStage, W + ((size_t)strip0 * b.R + kW4StageRecs * slab) * kRec,
-                              bytes, &full[cur.s]);
-                }
-                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[cur.s]);
                 cur.next();
                 ++issued;
             }
@@ -232,10 +257,13 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
         int ptile = -1;
         for (int i = i0; i < i1 && ok; ++i) {
             const int tile = i / p.b0.blocks, t0 = tile * kW4Tok, mt = min(kW4Tok, p.T - t0);
-            const int tok = t0 + (lane < mt ? lane : 0);
             const uint8_t* W = WHICH == kW4Linear ? p.w : reinterpret_cast<const uint8_t*>(WHICH == kW4Up ? a.sgu : a.sd);
-            const float sc = WHICH == kW4Down ? a.sgate[tok] : 0.f;
-            issue(p.b0, 0, W, (WHICH == kW4Linear ? 0 : (int)a.P) + t0, i - tile * p.b0.blocks, mt, tile != ptile, tok, a.K, sc);
+            issue(p.b0, 0, W, (WHICH == kW4Linear ? 0 : (int)a.P) + t0, i - tile * p.b0.blocks, mt, tile != ptile,
+                  [&](int& tok, int& slot, float& sc) {
+                      tok = t0 + (lane < mt ? lane : 0);
+                      slot = a.K;
+                      sc = WHICH == kW4Down ? a.sgate[tok] : 0.f;
+                  });
             ptile = tile;
         }
         if (WHICH != kW4Linear) {
@@ -243,52 +271,65 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                 grid_dep_wait();
                 grid_dep_launch();  // the routing is complete: the down kernel may start
             }
-            // routed items in (expert, token tile, block) order: tiles[g] = first item of group g
+            // routed items in (expert, token tile, block) order: tiles[g] = first item of group g. All the
+            // experts and their counts are read at once (their latencies would come one after another).
             const int n_act = a.hdr->n_act, blocks = p.b1.blocks;
+            int e8[8], o8[8], c8[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e8[j] = 32 * j + lane < n_act ? a.act[32 * j + lane] : 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                o8[j] = a.offsets[e8[j]];
+                c8[j] = a.offsets[e8[j] + 1];
+            }
             int run = 0;
-            for (int b0 = 0; b0 < n_act; b0 += 32) {
-                const int g = b0 + lane;
-                int v = 0;
-                if (g < n_act) v = ((a.offsets[a.act[g] + 1] - a.offsets[a.act[g]] + kW4Tok - 1) / kW4Tok) * blocks;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int g = 32 * j + lane;
+                c8[j] -= o8[j];
+                const int v = g < n_act ? ((c8[j] + kW4Tok - 1) / kW4Tok) * blocks : 0;
                 int incl = v;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int y = __shfl_up_sync(0xffffffffu, incl, o);
                     if (lane >= o) incl += y;
                 }
-                if (g < n_act) tiles[g] = run + incl - v;
+                if (g < n_act) {
+                    tiles[g] = run + incl - v;
+                    groups[g] = (uint32_t)e8[j] << 16 | (uint32_t)o8[j];  // (fewer than 2^16 pairs below 256 tokens)
+                    counts[g] = (uint16_t)c8[j];
+                }
                 run += __shfl_sync(0xffffffffu, incl, 31);
             }
             if (lane == 0) tiles[n_act] = run;
             __syncwarp();
             const int q1 = (int)((long long)(c_ + 1) * run / G_);
-            int g = -1, e = 0, off = 0, cnt = 0, ctile = -1, mt = 0, tok = 0, slot = 0;
+            int g = -1, ctile = -1, mt = 0, pv = 0;
+            uint32_t eo = 0;
             float sc = 0.f;
             for (int q = (int)((long long)c_ * run / G_); q < q1 && ok; ++q) {
                 if (g < 0 || q >= tiles[g + 1]) {
-                    int lo = g < 0 ? 0 : g + 1, hi = n_act - 1;
-                    while (lo < hi) {  // largest g with tiles[g] <= q
-                        const int mid = (lo + hi + 1) >> 1;
-                        if (tiles[mid] <= q) lo = mid; else hi = mid - 1;
-                    }
-                    g = lo;
-                    e = a.act[g];
-                    off = a.offsets[e];
-                    cnt = a.offsets[e + 1] - off;
+                    g = w4_find(tiles, n_act, g, q);
+                    eo = groups[g];
                     ctile = -1;
                 }
-                const int local = q - tiles[g], tile = local / blocks, h0 = off + tile * kW4Tok;
+                const int local = q - tiles[g], tile = local / blocks, h0 = (int)(eo & 0xffffu) + tile * kW4Tok;
                 const bool fresh = tile != ctile;
                 if (fresh) {
                     ctile = tile;
-                    mt = min(kW4Tok, cnt - tile * kW4Tok);
-                    const int pv = a.perm[h0 + (lane < mt ? lane : 0)];
-                    tok = pv / a.K;
-                    slot = pv - tok * a.K;
-                    if (WHICH == kW4Down) sc = a.topw[pv];
+                    mt = min(kW4Tok, counts[g] - tile * kW4Tok);
                 }
                 const uint8_t* W = reinterpret_cast<const uint8_t*>(WHICH == kW4Up ? a.gate_up : a.down);
-                issue(p.b1, 1, W + (size_t)e * p.matrix_bytes, h0, local - tile * blocks, mt, fresh, tok, slot, sc);
+                issue(p.b1, 1, W + (size_t)(eo >> 16) * p.matrix_bytes, h0, local - tile * blocks, mt, fresh,
+                      [&](int& tok, int& slot, float& s) {
+                          if (fresh) {
+                              pv = a.perm[h0 + (lane < mt ? lane : 0)];
+                              if (WHICH == kW4Down) sc = a.topw[pv];
+                          }
+                          tok = pv / a.K;
+                          slot = pv - tok * a.K;
+                          s = sc;
+                      });
             }
         }
         // the end of the items, as one more stage without copies
@@ -319,22 +360,26 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
         uint32_t at = 0;  // this warp's records within a stage
         W4Cursor<Ring::kStages> cur;
         W4Cursor<kW4RedBufs> rcur;
-        const uint32_t st0 = smem_u32(stages);
+        // shared-window addresses: arithmetic on generic pointers costs several instructions a use
+        const uint32_t st0 = smem_u32(stages), sm0 = smem_u32(sm), full0 = smem_u32(full), empty0 = smem_u32(empty),
+                       rfull0 = smem_u32(rfull), rempty0 = smem_u32(rempty);
         const uint32_t red0 = smem_u32(red) + (uint32_t)(warp * 512 + lane * 16);
         bool ok;
         for (;;) {
-            ok = w4_wait(&full[cur.s], cur.ph, limit);
+            ok = w4_wait32(full0 + 8u * cur.s, cur.ph, limit);
             if (!ok) break;
-            const W4Stage st = sm[cur.s];
-            if (st.info == 0) break;
-            if (st.key != ckey) {
-                ckey = st.key;
-                const W4Meta& m = metas[st.meta];
+            const uint4 stv = lds128_smem(sm0 + 16u * cur.s);  // a W4Stage
+            const int key = (int)stv.x, info = (int)stv.y;
+            if (info == 0) break;
+            if (key != ckey) {
+                ckey = key;
+                const W4Meta& m = metas[stv.w];
                 const bool routed = m.group != 0;
                 const int wl = routed ? p.b1.wl : p.b0.wl, rpw = routed ? p.b1.rpw : p.b0.rpw;
-                const int recs = (st.info >> 8) & 0xff, kq = warp & ((1 << wl) - 1);
+                const int recs = (info >> 8) & 0xff, kq = warp & ((1 << wl) - 1);
                 sub = warp >> wl;
                 nrec = max(0, min(rpw, recs - rpw * kq));
+                if (nrec == 0) sub = kW4Warps;  // no share of any stage with these rows
                 at = (uint32_t)((sub * recs + rpw * kq) * kRec);
                 const int n = lane >> 2;
                 const bool live = n < m.mt;
@@ -346,37 +391,40 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                 else
                     row = a.h + (size_t)(m.row0 + (live ? n : 0)) * a.Imax;
                 const int cols = routed ? p.cols[1] : p.cols[0];
-                const int k0 = (st.slab * kW4StageRecs + rpw * kq) * kW4Cols;
+                const int k0 = ((int)stv.z * kW4StageRecs + rpw * kq) * kW4Cols;
                 w4_load_tokens(b[0], row, live && nrec > 0, k0, cols, lane);
                 w4_load_tokens(b[1], row, live && nrec > 1, k0 + kW4Cols, cols, lane);
             }
-            if (sub < (st.info & 0xff) && nrec > 0) {
+            if (sub < (info & 0xff)) {
                 const uint32_t rec = st0 + (uint32_t)(cur.s * Ring::kStage) + at;
                 W4Frag<FMT, G> f0, f1;
-                w4_load<FMT, G>(rec, lane, f0);
-                if (nrec > 1) w4_load<FMT, G>(rec + kRec, lane, f1);
+                constexpr uint32_t N = W4Rec<FMT, G>::kGroups;
+                const uint32_t ra = rec + 16u * (uint32_t)lane, rm = rec + 2u * N * ((uint32_t)lane >> 2),
+                               rz = rec + N * ((uint32_t)lane >> 2);
+                w4_load_at<FMT, G, 0>(ra, rm, rz, f0);
+                if (nrec > 1) w4_load_at<FMT, G, kRec>(ra, rm, rz, f1);
                 w4_mma_record<FMT, G, 1>(f0, b[0], acc);
                 if (nrec > 1) w4_mma_record<FMT, G, 1>(f1, b[1], acc);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[cur.s]);
+            if (lane == 0) mbar_arrive32(empty0 + 8u * cur.s);
             cur.next();
-            if (st.info >> 16) {
-                ok = w4_wait(&rempty[rcur.s], rcur.ph ^ 1u, limit);
+            if (info >> 16) {
+                ok = w4_wait32(rempty0 + 8u * rcur.s, rcur.ph ^ 1u, limit);
                 if (!ok) break;
                 const uint32_t v[4] = {__float_as_uint(acc[0][0]), __float_as_uint(acc[0][1]), __float_as_uint(acc[0][2]),
                                        __float_as_uint(acc[0][3])};
                 sts128(red0 + (uint32_t)(rcur.s * kW4Warps * 512), v);
                 acc[0][0] = acc[0][1] = acc[0][2] = acc[0][3] = 0.f;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&rfull[rcur.s]);
+                if (lane == 0) mbar_arrive32(rfull0 + 8u * rcur.s);
                 rcur.next();
             }
         }
         // the end: passed on to each epilogue warp as one more item
         for (int j = 0; j < kW4EpiWarps && ok; ++j) {
-            ok = w4_wait(&rempty[rcur.s], rcur.ph ^ 1u, limit);
-            if (ok && lane == 0) mbar_arrive(&rfull[rcur.s]);
+            ok = w4_wait32(rempty0 + 8u * rcur.s, rcur.ph ^ 1u, limit);
+            if (ok && lane == 0) mbar_arrive32(rfull0 + 8u * rcur.s);
             rcur.next();
         }
         if (!ok && lane == 0) atomicOr(p.err, ERR_TIMEOUT);
@@ -401,6 +449,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                     v.x += __uint_as_float(q.x); v.y += __uint_as_float(q.y);
                     v.z += __uint_as_float(q.z); v.w += __uint_as_float(q.w);
                 }
+                v.x *= W4Fold<FMT>::kUnfold; v.y *= W4Fold<FMT>::kUnfold; v.z *= W4Fold<FMT>::kUnfold; v.w *= W4Fold<FMT>::kUnfold;
                 const int strip = m.strip0 + sub;
                 if (WHICH == kW4Up) {
                     bf16* h = a.h + (size_t)(m.row0 + t2) * a.Imax + strip * 8 + g8;
