@@ -211,41 +211,67 @@ __device__ __forceinline__ void w4_bias_fold(const W4Frag<FMT, G>& f, int h, int
     }
 }
 
-// acc += one record (16 rows by 128 columns) times NT tiles of 8 tokens, W4Fold::kUnfold times too small. b[n][4 c + i] are the B
-// operands of lane 4g + t: token g of tile n, columns 32 c + 8 t + 2 i, + 1. acc is the m16n8
-// accumulator of each tile: rows g (0, 1) and g + 8 (2, 3), tokens 2t (0, 2) and 2t + 1 (1, 3).
-// Each group's sum starts at zero and is scaled in fp32.
-template <int FMT, int G, int NT>
-__device__ __forceinline__ void w4_mma_record(const W4Frag<FMT, G>& f, const uint32_t (&b)[NT][16], float (&acc)[NT][4]) {
-    const uint32_t w0[4] = {f.lo.x, f.lo.y, f.lo.z, f.lo.w}, w1[4] = {f.hi.x, f.hi.y, f.hi.z, f.hi.w};
-    float d[NT][4];
+// acc += NR records (16 rows by 128 columns each) times a tile of 8 tokens, W4Fold::kUnfold times too
+// small. b[r][4 c + i] are the B operands of lane 4g + t: token g, columns 32 c + 8 t + 2 i, + 1 of record
+// r. acc is the m16n8 accumulator: rows g (0, 1) and g + 8 (2, 3), tokens 2t (0, 2) and 2t + 1 (1, 3).
+// Each group's sum starts at zero and is scaled in fp32. The records' chains of dependent MMAs are
+// interleaved, so that one fills the other's latency.
+template <int FMT, int G, int NR>
+__device__ __forceinline__ void w4_mma_records(const W4Frag<FMT, G> (&f)[NR], const uint32_t (&b)[NR][16], float (&acc)[4]) {
+    float d[NR][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int gi = c * 32 / G;
-        uint32_t p[4], q[4];
-        uint32_t b00, b01, b10, b11;
-        w4_bias_fold(f, 0, gi, b00, b01);
-        w4_bias_fold(f, 1, gi, b10, b11);
-        w4_decode_fold<FMT>(w0[c], b00, b01, p);
-        w4_decode_fold<FMT>(w1[c], b10, b11, q);
+        uint32_t p[NR][4], q[NR][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (c * 32 % G == 0)
-                w4_mma_first(d[n], p[0], q[0], p[1], q[1], b[n][4 * c], b[n][4 * c + 1]);
-            else
-                w4_mma(d[n], p[0], q[0], p[1], q[1], b[n][4 * c], b[n][4 * c + 1]);
-            w4_mma(d[n], p[2], q[2], p[3], q[3], b[n][4 * c + 2], b[n][4 * c + 3]);
+        for (int r = 0; r < NR; ++r) {
+            const uint32_t w0 = c == 0 ? f[r].lo.x : c == 1 ? f[r].lo.y : c == 2 ? f[r].lo.z : f[r].lo.w;
+            const uint32_t w1 = c == 0 ? f[r].hi.x : c == 1 ? f[r].hi.y : c == 2 ? f[r].hi.z : f[r].hi.w;
+            uint32_t b00, b01, b10, b11;
+            w4_bias_fold(f[r], 0, gi, b00, b01);
+            w4_bias_fold(f[r], 1, gi, b10, b11);
+            w4_decode_fold<FMT>(w0, b00, b01, p[r]);
+            w4_decode_fold<FMT>(w1, b10, b11, q[r]);
         }
-        if ((c + 1) * 32 % G == 0) {
-            const float s0 = w4_scale(f, 0, gi), s1 = w4_scale(f, 1, gi);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                acc[n][0] = fmaf(s0, d[n][0], acc[n][0]);
-                acc[n][1] = fmaf(s0, d[n][1], acc[n][1]);
-                acc[n][2] = fmaf(s1, d[n][2], acc[n][2]);
-                acc[n][3] = fmaf(s1, d[n][3], acc[n][3]);
+        for (int r = 0; r < NR; ++r) {
+            if (c * 32 % G == 0)
+                w4_mma_first(d[r], p[r][0], q[r][0], p[r][1], q[r][1], b[r][4 * c], b[r][4 * c + 1]);
+            else
+                w4_mma(d[r], p[r][0], q[r][0], p[r][1], q[r][1], b[r][4 * c], b[r][4 * c + 1]);
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) w4_mma(d[r], p[r][2], q[r][2], p[r][3], q[r][3], b[r][4 * c + 2], b[r][4 * c + 3]);
+        if ((c + 1) * 32 % G == 0) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const float s0 = w4_scale(f[r], 0, gi), s1 = w4_scale(f[r], 1, gi);
+                acc[0] = fmaf(s0, d[r][0], acc[0]);
+                acc[1] = fmaf(s0, d[r][1], acc[1]);
+                acc[2] = fmaf(s1, d[r][2], acc[2]);
+                acc[3] = fmaf(s1, d[r][3], acc[3]);
             }
         }
+    }
+}
+
+// acc += up to two consecutive records in shared memory times a tile.
+template <int FMT, int G>
+__device__ __forceinline__ void w4_records(uint32_t rec, int n, const uint32_t (&b)[2][16], float (&acc)[4], int lane) {
+    constexpr uint32_t N = W4Rec<FMT, G>::kGroups;
+    const uint32_t at = rec + 16u * (uint32_t)lane, row = (uint32_t)lane >> 2, meta = rec + 2u * N * row, zmeta = rec + N * row;
+    if (n > 1) {
+        W4Frag<FMT, G> f[2];
+        w4_load_at<FMT, G, 0>(at, meta, zmeta, f[0]);
+        w4_load_at<FMT, G, W4Rec<FMT, G>::kBytes>(at, meta, zmeta, f[1]);
+        w4_mma_records<FMT, G, 2>(f, b, acc);
+    } else if (n > 0) {
+        W4Frag<FMT, G> f[1];
+        uint32_t b1[1][16];
+        w4_load_at<FMT, G, 0>(at, meta, zmeta, f[0]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) b1[0][i] = b[0][i];
+        w4_mma_records<FMT, G, 1>(f, b1, acc);
     }
 }
 

@@ -418,14 +418,14 @@ __global__ void __launch_bounds__(kOneThreads, 1) k_w4_one(const __grid_constant
     // ---- gate_up: each warp its records of every strip, sums left in shared memory. The B operands (one
     // live column, token 0) are the same for all strips.
     const int n = lane >> 2, rpw = (p.R + kW4Warps - 1) / kW4Warps, unr = max(0, min(rpw, p.R - rpw * warp));
-    uint32_t b[2][1][16];
-    auto load_row = [&](uint32_t (&q)[1][16], uint32_t row, bool live, int k0, int cols) {
+    uint32_t b[2][16];
+    auto load_row = [&](uint32_t (&q)[16], uint32_t row, bool live, int k0, int cols) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int k = k0 + 32 * c + 8 * (lane & 3);
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (n == 0 && live && k < cols) v = lds128_smem(row + 2u * (uint32_t)k);
-            q[0][4 * c] = v.x; q[0][4 * c + 1] = v.y; q[0][4 * c + 2] = v.z; q[0][4 * c + 3] = v.w;
+            q[4 * c] = v.x; q[4 * c + 1] = v.y; q[4 * c + 2] = v.z; q[4 * c + 3] = v.w;
         }
     };
     load_row(b[0], smem_u32(xs), unr > 0, rpw * warp * kW4Cols, a.H);
@@ -435,21 +435,15 @@ __global__ void __launch_bounds__(kOneThreads, 1) k_w4_one(const __grid_constant
     bool ok = true;
     for (int i = 0; i < n_up; ++i) {
         ok = ok && w4_wait(&full[st], ph, 5 * limit);  // (the producer's wait for the routing comes before)
-        float acc[1][4] = {};
+        float acc[4] = {};
         const uint32_t rec = smem_u32(stages) + (uint32_t)(st * Ring::kStage + rpw * warp * kRec);
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-            if (r < unr) {
-                W4Frag<FMT, G> f;
-                w4_load<FMT, G>(rec + (uint32_t)(r * kRec), lane, f);
-                w4_mma_record<FMT, G, 1>(f, b[r], acc);
-            }
+        w4_records<FMT, G>(rec, unr, b, acc, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
         if ((lane & 3) == 0) {
             float* q = part + (i * kW4Warps + warp) * 16 + n;
-            q[0] = acc[0][0];
-            q[8] = acc[0][2];
+            q[0] = acc[0];
+            q[8] = acc[2];
         }
         if (++st == nst) {
             st = 0;
@@ -468,21 +462,15 @@ __global__ void __launch_bounds__(kOneThreads, 1) k_w4_one(const __grid_constant
             load_row(b[0], row, nr > 0, r0 * kW4Cols, cols);
             load_row(b[1], row, nr > 1, (r0 + 1) * kW4Cols, cols);
             ok = ok && w4_wait(&full[st], ph, limit);
-            float acc[1][4] = {};
+            float acc[4] = {};
             const uint32_t rec = smem_u32(stages) + (uint32_t)(st * Ring::kStage + (sub * p.dR + r0) * kRec);
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                if (r < nr) {
-                    W4Frag<FMT, G> f;
-                    w4_load<FMT, G>(rec + (uint32_t)(r * kRec), lane, f);
-                    w4_mma_record<FMT, G, 1>(f, b[r], acc);
-                }
+            w4_records<FMT, G>(rec, nr, b, acc, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
             if ((lane & 3) == 0 && g <= K) {
                 float* q = ys + ((g << p.dwl) + kq) * 16 + n;
-                q[0] = acc[0][0];
-                q[8] = acc[0][2];
+                q[0] = acc[0];
+                q[8] = acc[2];
             }
             if (++st == nst) {
                 st = 0;

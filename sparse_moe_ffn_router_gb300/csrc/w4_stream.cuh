@@ -80,68 +80,63 @@ constexpr int kW4EpiWarps = 2;
 constexpr int kW4Threads = 32 * (kW4Warps + 1 + kW4EpiWarps);
 constexpr int kW4SmemMax = 227 * 1024;
 
-// An item, for the epilogue and for loading token rows.
-struct W4Meta {
-    int group;   // 0 shared / linear, 1 routed; -1: no more items
-    int mt;      // tokens
-    int row0;    // up: first h row written; down: first h row read
-    int strip0;  // first strip of the block
-    int n;       // strips of the block
+// The token rows of an item (consecutive items mostly share them).
+struct __align__(16) W4Set {
+    int group;  // 0 shared / linear, 1 routed
+    int mt;     // tokens
+    int row0;   // up: first h row written; down: first h row read
+    int pad;
     int tok[kW4Tok], slot[kW4Tok];
     float sc[kW4Tok];
 };
 
-// A stage, for the consumers: the token rows' key (a new one wherever the tokens, the group or the
-// column range change), strips | records << 8 | (last stage of its item) << 16 (0: no more
-// items), the column range, the item's place among the W4Metas.
-struct __align__(16) W4Stage {
-    int key, info, slab, meta;
-};
-
+// A stage, as the producer writes it into a ring of entries that the consumers read (an item's last stage
+// into a second ring, by items, for the epilogue):
+//   x  number of the token rows and column range: a new one means new rows to load
+//   y  strips | records << 8 | (last stage of its item) << 16 | column range << 17; 0: no more items
+//   z  first strip of the block          w  the item's W4Set
 template <int FMT, int G>
 struct W4Ring {
     static constexpr int kStage = kW4StageRecs * W4Rec<FMT, G>::kBytes;
     static constexpr int kRed = kW4RedBufs * kW4Warps * 128 * 4;
-    static constexpr int kMaxMetas = 16, kMaxStages = 6;
-    static constexpr int kFixed = 128 + kRed + kMaxMetas * (int)sizeof(W4Meta) + kMaxStages * (int)sizeof(W4Stage) + 256 + 260 * 10;
+    static constexpr int kEnt = 16;  // entries and sets: more than the items between copy and epilogue
+    static constexpr int kMaxStages = 6;
+    static constexpr int oRed = 0, oEnt = oRed + kRed, oItm = oEnt + kEnt * 16, oSet = oItm + kEnt * 16, oBar = oSet + kEnt * (int)sizeof(W4Set),
+                         oTab = oBar + 8 * (2 * kMaxStages + 2 * kW4RedBufs), kFixed = 128 + oTab + 260 * 10;
     static constexpr int kFit = (kW4SmemMax - kFixed) / kStage;
     static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
-    // an item's metadata is rewritten once its epilogue is done: at most this many items later
-    static constexpr int kMetas = kStages + kW4RedBufs + 2;
-    static_assert(kStage % 128 == 0 && kStages >= 3 && kMetas <= kMaxMetas, "ring");
-    static_assert((2 * kMaxStages + 2 * kW4RedBufs) * 8 <= 256 && kMaxMetas * sizeof(W4Meta) % 8 == 0, "barriers");
+    static_assert(kStage % 128 == 0 && kStages >= 3 && kStages + kW4RedBufs + 2 <= kEnt && oBar % 8 == 0, "ring");
     static constexpr int kBytes = kFixed + kStages * kStage;
 };
 
 // B operands of one record from a lane's token row: elements 32 c + 8 t .. + 7 from column k0, zero
 // past the matrix's columns (the packed weights there have scale 0, but the row's memory may hold
 // anything) and for the tile's missing tokens. L2 loads (an earlier kernel wrote the rows).
-__device__ __forceinline__ void w4_load_tokens(uint32_t (&b)[1][16], const bf16* row, bool live, int k0, int cols, int lane) {
+__device__ __forceinline__ void w4_load_tokens(uint32_t (&b)[16], const bf16* row, bool live, int k0, int cols, int lane) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int k = k0 + 32 * c + 8 * (lane & 3);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (live && k < cols) v = __ldcg(reinterpret_cast<const uint4*>(row + k));
-        b[0][4 * c] = v.x; b[0][4 * c + 1] = v.y; b[0][4 * c + 2] = v.z; b[0][4 * c + 3] = v.w;
+        b[4 * c] = v.x; b[4 * c + 1] = v.y; b[4 * c + 2] = v.z; b[4 * c + 3] = v.w;
     }
 }
 
 // A cursor over a ring of N barriers: the slot, and the parity of its current round.
 template <int N>
 struct W4Cursor {
-    int s = 0;
-    uint32_t ph = 0;
+    uint32_t s = 0, ph = 0;
     __device__ __forceinline__ void next() {
-        if (++s == N) {
+        if (++s == (uint32_t)N) {
             s = 0;
             ph ^= 1u;
         }
     }
 };
 
-// The group of item q: the largest g with tiles[g] <= q, after group `from`.
-__device__ __forceinline__ int w4_find(const int* tiles, int n, int from, int q) {
-    int lo = from < 0 ? 0 : from + 1, hi = n - 1;
+// The group of item q: the largest g with tiles[g] <= q.
+__device__ __forceinline__ int w4_find(const int* tiles, int n, int q) {
+    int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (tiles[mid] <= q) lo = mid; else hi = mid - 1;
@@ -168,29 +163,26 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
     using Ring = W4Ring<FMT, G>;
     constexpr int kRec = W4Rec<FMT, G>::kBytes;
     extern __shared__ uint8_t smem_raw[];
+    // shared-window addresses throughout: arithmetic on generic pointers costs several instructions a
+    // use, and a stage's bookkeeping is on every warp's critical path
     uint8_t* base = smem_raw + (((smem_u32(smem_raw) + 127u) & ~127u) - smem_u32(smem_raw));
-    uint8_t* stages = base;
-    float* red = reinterpret_cast<float*>(base + Ring::kStages * Ring::kStage);
-    W4Stage* sm = reinterpret_cast<W4Stage*>(reinterpret_cast<uint8_t*>(red) + Ring::kRed);
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + Ring::kMaxStages);
-    uint64_t* empty = full + Ring::kStages;
-    uint64_t* rfull = empty + Ring::kStages;
-    uint64_t* rempty = rfull + kW4RedBufs;
-    W4Meta* metas = reinterpret_cast<W4Meta*>(reinterpret_cast<uint8_t*>(full) + 256);
-    int* tiles = reinterpret_cast<int*>(metas + Ring::kMaxMetas);
-    uint32_t* groups = reinterpret_cast<uint32_t*>(tiles + 260);  // routed groups: expert, first h row
-    uint16_t* counts = reinterpret_cast<uint16_t*>(groups + 260);
+    const uint32_t st0 = smem_u32(base), x0 = st0 + Ring::kStages * Ring::kStage;
+    const uint32_t red0 = x0 + Ring::oRed, ent0 = x0 + Ring::oEnt, itm0 = x0 + Ring::oItm, full0 = x0 + Ring::oBar, empty0 = full0 + 8 * Ring::kMaxStages,
+                   rfull0 = empty0 + 8 * Ring::kMaxStages, rempty0 = rfull0 + 8 * kW4RedBufs;
+    uint8_t* xp = base + Ring::kStages * Ring::kStage;
+    W4Set* sets = reinterpret_cast<W4Set*>(xp + Ring::oSet);
     const LayerArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t limit = p.wait_ns;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < Ring::kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kW4Warps);
+        uint64_t* bar = reinterpret_cast<uint64_t*>(xp + Ring::oBar);
+        for (int s = 0; s < Ring::kMaxStages; ++s) {
+            mbar_init(&bar[s], 1);
+            mbar_init(&bar[Ring::kMaxStages + s], kW4Warps);
         }
         for (int s = 0; s < kW4RedBufs; ++s) {
-            mbar_init(&rfull[s], kW4Warps);
-            mbar_init(&rempty[s], 1);
+            mbar_init(&bar[2 * Ring::kMaxStages + s], kW4Warps);
+            mbar_init(&bar[2 * Ring::kMaxStages + kW4RedBufs + s], 1);
         }
         fence_mbar_init();
     }
@@ -200,53 +192,41 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
         // ---------------- producer
         const int G_ = gridDim.x, c_ = blockIdx.x;
         W4Cursor<Ring::kStages> cur;
-        int item = 0, issued = 0, key = 0;
+        int it = 0, item = 0, key = 0, nset = -1;
         bool ok = true;
-        // one item: for each of its stages the copy, then the metadata (which may still have to come from
-        // memory), then the arrival that lets the consumers in. new_rows: its token rows are not those of
-        // the item before. rows(): the lane's token, slot and scale.
-        auto issue = [&](const W4Block& b, int group, const uint8_t* W, int row0, int blk, int mt, bool new_rows, auto rows) {
+        // one item: for each of its stages the copy, then (fresh: its token rows are not those of the item
+        // before) the metadata, which may still have to come from memory, then the arrival that lets the
+        // consumers in. rows(set): the lane's token, slot and scale.
+        auto issue = [&](const W4Block& b, const uint8_t* W, int blk, bool fresh, auto rows) {
             const int strip0 = blk * b.ns, ns = min(b.ns, b.strips - strip0);
-            if (new_rows) ++key;
             for (int slab = 0; slab < b.nslab && ok; ++slab) {
-                ok = w4_wait(&empty[cur.s], cur.ph ^ 1u, limit);
+                ok = w4_wait32(empty0 + 8u * cur.s, cur.ph ^ 1u, limit);
                 if (!ok) break;
-                const int mslot = item % Ring::kMetas;
                 const int recs = min(kW4StageRecs, b.R - kW4StageRecs * slab);
+                const uint32_t bytes = (uint32_t)((b.nslab == 1 ? ns * recs : recs) * kRec), bar = full0 + 8u * cur.s;
                 if (lane == 0) {
-                    const uint32_t bytes = (uint32_t)((b.nslab == 1 ? ns * recs : recs) * kRec);
-                    mbar_expect_tx(&full[cur.s], bytes);
-                    bulk_load(stages + (size_t)cur.s * Ring::kStage, W + ((size_t)strip0 * b.R + kW4StageRecs * slab) * kRec,
-                              bytes, &full[cur.s]);
+                    mbar_expect_tx32(bar, bytes);
+                    bulk_load32(st0 + cur.s * (uint32_t)Ring::kStage, W + ((size_t)strip0 * b.R + kW4StageRecs * slab) * kRec, bytes, bar);
                 }
-                if (slab == 0) {
-                    W4Meta& m = metas[mslot];
-                    int tok, slot;
-                    float sc;
-                    rows(tok, slot, sc);
-                    if (lane < kW4Tok) {
-                        m.tok[lane] = tok;
-                        m.slot[lane] = slot;
-                        m.sc[lane] = sc;
-                    }
-                    if (lane == 0) {
-                        m.group = group;
-                        m.mt = mt;
-                        m.row0 = row0;
-                        m.strip0 = strip0;
-                        m.n = ns;
-                    }
-                } else {
-                    ++key;
+                if (slab == 0 && fresh) {
+                    ++nset;
+                    rows(sets[nset & (Ring::kEnt - 1)]);
+                    __syncwarp();
                 }
-                if (lane == 0) sm[cur.s] = W4Stage{key, ns | recs << 8 | (slab == b.nslab - 1 ? 1 << 16 : 0), slab, mslot};
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[cur.s]);
+                if (fresh || slab > 0) ++key;
+                if (lane == 0) {
+                    const uint32_t ent[4] = {(uint32_t)key,
+                                             (uint32_t)(ns | recs << 8 | (slab == b.nslab - 1 ? 1 << 16 : 0) | slab << 17),
+                                             (uint32_t)strip0, (uint32_t)(nset & (Ring::kEnt - 1))};
+                    sts128(ent0 + 16u * (uint32_t)(it & (Ring::kEnt - 1)), ent);
+                    if (slab == b.nslab - 1) sts128(itm0 + 16u * (uint32_t)(item & (Ring::kEnt - 1)), ent);
+                    mbar_arrive32(bar);
+                }
                 cur.next();
-                ++issued;
+                ++it;
             }
-            if (b.nslab > 1) ++key;  // the next item starts at the first column range again
             ++item;
+            if (b.nslab > 1) ++key;  // the next item starts at the first column range again
         };
         const int n0 = p.b0.blocks * ((p.T + kW4Tok - 1) / kW4Tok);  // group 0: (token tile, block) order
         const int i0 = (int)((long long)c_ * n0 / G_), i1 = (int)((long long)(c_ + 1) * n0 / G_);
@@ -254,17 +234,28 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
             grid_dep_wait();
             grid_dep_launch();
         }
-        int ptile = -1;
-        for (int i = i0; i < i1 && ok; ++i) {
-            const int tile = i / p.b0.blocks, t0 = tile * kW4Tok, mt = min(kW4Tok, p.T - t0);
+        {
             const uint8_t* W = WHICH == kW4Linear ? p.w : reinterpret_cast<const uint8_t*>(WHICH == kW4Up ? a.sgu : a.sd);
-            issue(p.b0, 0, W, (WHICH == kW4Linear ? 0 : (int)a.P) + t0, i - tile * p.b0.blocks, mt, tile != ptile,
-                  [&](int& tok, int& slot, float& sc) {
-                      tok = t0 + (lane < mt ? lane : 0);
-                      slot = a.K;
-                      sc = WHICH == kW4Down ? a.sgate[tok] : 0.f;
-                  });
-            ptile = tile;
+            int tile = i0 / p.b0.blocks, blk = i0 - tile * p.b0.blocks;
+            bool fresh = true;
+            for (int i = i0; i < i1 && ok; ++i) {
+                const int t0 = tile * kW4Tok, mt = min(kW4Tok, p.T - t0);
+                issue(p.b0, W, blk, fresh, [&](W4Set& m) {
+                    if (lane < kW4Tok) {
+                        const int tok = t0 + (lane < mt ? lane : 0);
+                        m.tok[lane] = tok;
+                        m.slot[lane] = a.K;
+                        m.sc[lane] = WHICH == kW4Down ? a.sgate[tok] : 0.f;
+                    }
+                    if (lane == 0) *reinterpret_cast<int4*>(&m) = make_int4(0, mt, (WHICH == kW4Linear ? 0 : (int)a.P) + t0, 0);
+                });
+                fresh = false;
+                if (++blk == p.b0.blocks) {
+                    blk = 0;
+                    ++tile;
+                    fresh = true;
+                }
+            }
         }
         if (WHICH != kW4Linear) {
             if (WHICH == kW4Up) {
@@ -273,6 +264,9 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
             }
             // routed items in (expert, token tile, block) order: tiles[g] = first item of group g. All the
             // experts and their counts are read at once (their latencies would come one after another).
+            int* tiles = reinterpret_cast<int*>(xp + Ring::oTab);
+            uint32_t* groups = reinterpret_cast<uint32_t*>(tiles + 260);  // expert << 16 | first h row
+            uint16_t* counts = reinterpret_cast<uint16_t*>(groups + 260);
             const int n_act = a.hdr->n_act, blocks = p.b1.blocks;
             int e8[8], o8[8], c8[8];
 #pragma unroll
@@ -301,86 +295,89 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                 }
                 run += __shfl_sync(0xffffffffu, incl, 31);
             }
-            if (lane == 0) tiles[n_act] = run;
             __syncwarp();
-            const int q1 = (int)((long long)(c_ + 1) * run / G_);
-            int g = -1, ctile = -1, mt = 0, pv = 0;
-            uint32_t eo = 0;
-            float sc = 0.f;
-            for (int q = (int)((long long)c_ * run / G_); q < q1 && ok; ++q) {
-                if (g < 0 || q >= tiles[g + 1]) {
-                    g = w4_find(tiles, n_act, g, q);
-                    eo = groups[g];
-                    ctile = -1;
+            const int q0 = (int)((long long)c_ * run / G_), q1 = (int)((long long)(c_ + 1) * run / G_);
+            if (q0 < q1 && ok) {
+                int g = w4_find(tiles, n_act, q0), tile = (q0 - tiles[g]) / blocks, blk = q0 - tiles[g] - tile * blocks;
+                uint32_t eo = groups[g];
+                int cnt = counts[g];
+                bool fresh = true;
+                const uint8_t* W0 = reinterpret_cast<const uint8_t*>(WHICH == kW4Up ? a.gate_up : a.down);
+                for (int q = q0; q < q1 && ok; ++q) {
+                    issue(p.b1, W0 + (size_t)(eo >> 16) * p.matrix_bytes, blk, fresh, [&](W4Set& m) {
+                        const int h0 = (int)(eo & 0xffffu) + tile * kW4Tok, mt = min(kW4Tok, cnt - tile * kW4Tok);
+                        if (lane < kW4Tok) {
+                            const int pv = a.perm[h0 + (lane < mt ? lane : 0)], tok = pv / a.K;
+                            m.tok[lane] = tok;
+                            m.slot[lane] = pv - tok * a.K;
+                            m.sc[lane] = WHICH == kW4Down ? a.topw[pv] : 0.f;
+                        }
+                        if (lane == 0) *reinterpret_cast<int4*>(&m) = make_int4(1, mt, h0, 0);
+                    });
+                    fresh = false;
+                    if (++blk == blocks) {
+                        blk = 0;
+                        ++tile;
+                        fresh = true;
+                        if (tile * kW4Tok >= cnt && q + 1 < q1) {
+                            ++g;
+                            tile = 0;
+                            eo = groups[g];
+                            cnt = counts[g];
+                        }
+                    }
                 }
-                const int local = q - tiles[g], tile = local / blocks, h0 = (int)(eo & 0xffffu) + tile * kW4Tok;
-                const bool fresh = tile != ctile;
-                if (fresh) {
-                    ctile = tile;
-                    mt = min(kW4Tok, counts[g] - tile * kW4Tok);
-                }
-                const uint8_t* W = reinterpret_cast<const uint8_t*>(WHICH == kW4Up ? a.gate_up : a.down);
-                issue(p.b1, 1, W + (size_t)(eo >> 16) * p.matrix_bytes, h0, local - tile * blocks, mt, fresh,
-                      [&](int& tok, int& slot, float& s) {
-                          if (fresh) {
-                              pv = a.perm[h0 + (lane < mt ? lane : 0)];
-                              if (WHICH == kW4Down) sc = a.topw[pv];
-                          }
-                          tok = pv / a.K;
-                          slot = pv - tok * a.K;
-                          s = sc;
-                      });
             }
         }
         // the end of the items, as one more stage without copies
+        const int issued = it;
         if (ok) {
-            ok = w4_wait(&empty[cur.s], cur.ph ^ 1u, limit);
+            ok = w4_wait32(empty0 + 8u * cur.s, cur.ph ^ 1u, limit);
             if (ok && lane == 0) {
-                for (int j = 0; j < kW4EpiWarps; ++j) metas[(item + j) % Ring::kMetas].group = -1;
-                sm[cur.s] = W4Stage{key, 0, 0, 0};
-                mbar_arrive(&full[cur.s]);
+                const uint32_t ent[4] = {(uint32_t)key, 0u, 0u, 0u};
+                sts128(ent0 + 16u * (uint32_t)(it & (Ring::kEnt - 1)), ent);
+                for (int j = 0; j < kW4EpiWarps; ++j) sts128(itm0 + 16u * (uint32_t)((item + j) & (Ring::kEnt - 1)), ent);
+                mbar_arrive32(full0 + 8u * cur.s);
             }
         }
         if (!ok && lane == 0) atomicOr(p.err, ERR_TIMEOUT);
         // every copy issued must land before the CTA's shared memory is released (the end mark's stage
         // was free, so its last copy has landed)
+        uint64_t* bar = reinterpret_cast<uint64_t*>(xp + Ring::oBar);
         if (lane == 0)
             for (int k = 0; k < Ring::kStages - (ok ? 1 : 0) && issued - 1 - k >= 0; ++k) {
                 const int j = issued - 1 - k;
-                if (!mbar_wait(&full[j % Ring::kStages], ((uint32_t)(j / Ring::kStages)) & 1u, limit))
-                    atomicOr(p.err, ERR_TIMEOUT);
+                if (!mbar_wait(&bar[j % Ring::kStages], ((uint32_t)(j / Ring::kStages)) & 1u, limit)) atomicOr(p.err, ERR_TIMEOUT);
             }
     } else if (warp < kW4Warps) {
         // ---------------- consumers
         if (WHICH != kW4Up) grid_dep_wait();  // the token rows (linear) or the h rows (down)
         if (WHICH == kW4Down) grid_dep_launch();
-        uint32_t b[2][1][16];
-        float acc[1][4] = {};
-        int ckey = -1, sub = 0, nrec = 0;
-        uint32_t at = 0;  // this warp's records within a stage
+        uint32_t b[2][16];
+        float acc[4] = {};
+        int ckey = 0, sub = 0, nrec = 0;
+        uint32_t at = 0, ent = 0;  // this warp's records within a stage; the entry
         W4Cursor<Ring::kStages> cur;
         W4Cursor<kW4RedBufs> rcur;
-        // shared-window addresses: arithmetic on generic pointers costs several instructions a use
-        const uint32_t st0 = smem_u32(stages), sm0 = smem_u32(sm), full0 = smem_u32(full), empty0 = smem_u32(empty),
-                       rfull0 = smem_u32(rfull), rempty0 = smem_u32(rempty);
-        const uint32_t red0 = smem_u32(red) + (uint32_t)(warp * 512 + lane * 16);
+        const uint32_t red = red0 + (uint32_t)(warp * 512 + lane * 16);
         bool ok;
         for (;;) {
             ok = w4_wait32(full0 + 8u * cur.s, cur.ph, limit);
             if (!ok) break;
-            const uint4 stv = lds128_smem(sm0 + 16u * cur.s);  // a W4Stage
-            const int key = (int)stv.x, info = (int)stv.y;
+            const uint4 e = lds128_smem(ent0 + ent);
+            ent = (ent + 16u) & (16u * Ring::kEnt - 1u);
+            const int info = (int)e.y;
             if (info == 0) break;
-            if (key != ckey) {
-                ckey = key;
-                const W4Meta& m = metas[stv.w];
+            if ((int)e.x != ckey) {
+                ckey = (int)e.x;
+                const W4Set& m = sets[e.w];
                 const bool routed = m.group != 0;
                 const int wl = routed ? p.b1.wl : p.b0.wl, rpw = routed ? p.b1.rpw : p.b0.rpw;
                 const int recs = (info >> 8) & 0xff, kq = warp & ((1 << wl) - 1);
                 sub = warp >> wl;
                 nrec = max(0, min(rpw, recs - rpw * kq));
-                if (nrec == 0) sub = kW4Warps;  // no share of any stage with these rows
                 at = (uint32_t)((sub * recs + rpw * kq) * kRec);
+                if (nrec == 0) sub = kW4StageRecs;  // no share of any stage with these rows
                 const int n = lane >> 2;
                 const bool live = n < m.mt;
                 const bf16* row;
@@ -391,31 +388,24 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
                 else
                     row = a.h + (size_t)(m.row0 + (live ? n : 0)) * a.Imax;
                 const int cols = routed ? p.cols[1] : p.cols[0];
-                const int k0 = ((int)stv.z * kW4StageRecs + rpw * kq) * kW4Cols;
+                const int k0 = ((info >> 17) * kW4StageRecs + rpw * kq) * kW4Cols;
                 w4_load_tokens(b[0], row, live && nrec > 0, k0, cols, lane);
                 w4_load_tokens(b[1], row, live && nrec > 1, k0 + kW4Cols, cols, lane);
             }
             if (sub < (info & 0xff)) {
-                const uint32_t rec = st0 + (uint32_t)(cur.s * Ring::kStage) + at;
-                W4Frag<FMT, G> f0, f1;
-                constexpr uint32_t N = W4Rec<FMT, G>::kGroups;
-                const uint32_t ra = rec + 16u * (uint32_t)lane, rm = rec + 2u * N * ((uint32_t)lane >> 2),
-                               rz = rec + N * ((uint32_t)lane >> 2);
-                w4_load_at<FMT, G, 0>(ra, rm, rz, f0);
-                if (nrec > 1) w4_load_at<FMT, G, kRec>(ra, rm, rz, f1);
-                w4_mma_record<FMT, G, 1>(f0, b[0], acc);
-                if (nrec > 1) w4_mma_record<FMT, G, 1>(f1, b[1], acc);
+                const uint32_t rec = st0 + cur.s * (uint32_t)Ring::kStage + at;
+                w4_records<FMT, G>(rec, nrec, b, acc, lane);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive32(empty0 + 8u * cur.s);
             cur.next();
-            if (info >> 16) {
+            if (info & (1 << 16)) {
                 ok = w4_wait32(rempty0 + 8u * rcur.s, rcur.ph ^ 1u, limit);
                 if (!ok) break;
-                const uint32_t v[4] = {__float_as_uint(acc[0][0]), __float_as_uint(acc[0][1]), __float_as_uint(acc[0][2]),
-                                       __float_as_uint(acc[0][3])};
-                sts128(red0 + (uint32_t)(rcur.s * kW4Warps * 512), v);
-                acc[0][0] = acc[0][1] = acc[0][2] = acc[0][3] = 0.f;
+                const uint32_t v[4] = {__float_as_uint(acc[0]), __float_as_uint(acc[1]), __float_as_uint(acc[2]),
+                                       __float_as_uint(acc[3])};
+                sts128(red + rcur.s * (uint32_t)(kW4Warps * 512), v);
+                acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
                 __syncwarp();
                 if (lane == 0) mbar_arrive32(rfull0 + 8u * rcur.s);
                 rcur.next();
@@ -431,57 +421,84 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
     } else {
         // ---------------- epilogue: warp e takes items e, e + kW4EpiWarps, ...
         const int g8 = lane >> 2, t2 = 2 * (lane & 3);
-        for (int item = warp - kW4Warps - 1;; item += kW4EpiWarps) {
-            const int rb = item % kW4RedBufs;
-            const bool ok = w4_wait(&rfull[rb], ((uint32_t)(item / kW4RedBufs)) & 1u, limit);
-            const W4Meta& m = metas[item % Ring::kMetas];
-            if (!ok || m.group < 0) {
+        int item = warp - kW4Warps - 1, cset = -1, wl = 0, row0 = 0;
+        bool live0 = false, live1 = false;  // the lane's two tokens
+        size_t o0 = 0, o1 = 0;              // their output rows
+        float sc0 = 0.f, sc1 = 0.f;
+        for (;; item += kW4EpiWarps) {
+            const uint32_t rb = (uint32_t)item % kW4RedBufs;
+            const bool ok = w4_wait32(rfull0 + 8u * rb, ((uint32_t)item / kW4RedBufs) & 1u, limit);
+            const uint4 e = lds128_smem(itm0 + 16u * ((uint32_t)item & (Ring::kEnt - 1)));
+            if (!ok || e.y == 0) {
                 if (!ok && lane == 0) atomicOr(p.err, ERR_TIMEOUT);
                 break;
             }
-            const int W = 1 << (m.group ? p.b1.wl : p.b0.wl), ns = m.n, mt = m.mt;
-            const uint32_t r0 = smem_u32(red) + (uint32_t)(rb * kW4Warps * 512 + lane * 16);
+            const int ns = (int)(e.y & 0xffu), strip0 = (int)e.z;
+            if ((int)e.w != cset) {
+                cset = (int)e.w;
+                const W4Set& m = sets[cset];
+                wl = m.group ? p.b1.wl : p.b0.wl;
+                row0 = m.row0;
+                live0 = t2 < m.mt;
+                live1 = t2 + 1 < m.mt;
+                const int k0 = m.tok[t2], k1 = m.tok[t2 + 1];
+                if (WHICH == kW4Up) {
+                    o0 = (size_t)(row0 + t2) * a.Imax;
+                    o1 = o0 + a.Imax;
+                } else if (WHICH == kW4Down) {
+                    o0 = ((size_t)k0 * (a.K + 1) + m.slot[t2]) * a.H;
+                    o1 = ((size_t)k1 * (a.K + 1) + m.slot[t2 + 1]) * a.H;
+                    sc0 = m.sc[t2] * W4Fold<FMT>::kUnfold;
+                    sc1 = m.sc[t2 + 1] * W4Fold<FMT>::kUnfold;
+                } else {
+                    o0 = (size_t)k0 * p.rows[0];
+                    o1 = (size_t)k1 * p.rows[0];
+                }
+            }
+            const uint32_t r0 = red0 + rb * (uint32_t)(kW4Warps * 512) + (uint32_t)(lane * 16);
             for (int sub = 0; sub < ns; ++sub) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                for (int k = 0; k < W; ++k) {
-                    const uint4 q = lds128_smem(r0 + (uint32_t)((sub * W + k) * 512));
+                const uint32_t rs = r0 + (uint32_t)((sub << wl) * 512);
+                for (int k = 0; k < (1 << wl); k += 2) {  // (at least two warps share a strip, or one)
+                    const uint4 q = lds128_smem(rs + (uint32_t)(k * 512));
+                    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+                    if (wl > 0) r = lds128_smem(rs + (uint32_t)(k * 512 + 512));
                     v.x += __uint_as_float(q.x); v.y += __uint_as_float(q.y);
                     v.z += __uint_as_float(q.z); v.w += __uint_as_float(q.w);
+                    v.x += __uint_as_float(r.x); v.y += __uint_as_float(r.y);
+                    v.z += __uint_as_float(r.z); v.w += __uint_as_float(r.w);
                 }
-                v.x *= W4Fold<FMT>::kUnfold; v.y *= W4Fold<FMT>::kUnfold; v.z *= W4Fold<FMT>::kUnfold; v.w *= W4Fold<FMT>::kUnfold;
-                const int strip = m.strip0 + sub;
+                if (WHICH != kW4Down) {
+                    v.x *= W4Fold<FMT>::kUnfold; v.y *= W4Fold<FMT>::kUnfold;
+                    v.z *= W4Fold<FMT>::kUnfold; v.w *= W4Fold<FMT>::kUnfold;
+                }
+                const int strip = strip0 + sub;
                 if (WHICH == kW4Up) {
-                    bf16* h = a.h + (size_t)(m.row0 + t2) * a.Imax + strip * 8 + g8;
-                    if (t2 < mt) h[0] = __float2bfloat16_rn(silu(v.x) * v.z);
-                    if (t2 + 1 < mt) h[a.Imax] = __float2bfloat16_rn(silu(v.y) * v.w);
+                    const int f = strip * 8 + g8;
+                    if (live0) a.h[o0 + f] = __float2bfloat16_rn(silu(v.x) * v.z);
+                    if (live1) a.h[o1 + f] = __float2bfloat16_rn(silu(v.y) * v.w);
                 } else if (WHICH == kW4Down) {
                     const int row = strip * 16 + g8;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (t2 + j < mt) {
-                            const size_t y = ((size_t)m.tok[t2 + j] * (a.K + 1) + m.slot[t2 + j]) * a.H + row;
-                            const float sc = m.sc[t2 + j], y0 = sc * (j ? v.y : v.x), y1 = sc * (j ? v.w : v.z);
-                            a.Y[y] = y0;
-                            a.Y[y + 8] = y1;
-                        }
-                } else {
-                    const int N = p.rows[0], row = strip * 16 + g8;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int n = row + 8 * i;
-                        if (n >= N) continue;
-                        const float bias = p.bias ? __bfloat162float(p.bias[n]) : 0.f;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            if (t2 + j < mt)
-                                p.out[(size_t)m.tok[t2 + j] * N + n] =
-                                    __float2bfloat16_rn((i ? (j ? v.w : v.z) : (j ? v.y : v.x)) + bias);
+                    if (live0) {
+                        a.Y[o0 + row] = sc0 * v.x;
+                        a.Y[o0 + row + 8] = sc0 * v.z;
                     }
+                    if (live1) {
+                        a.Y[o1 + row] = sc1 * v.y;
+                        a.Y[o1 + row + 8] = sc1 * v.w;
+                    }
+                } else {
+                    const int N = p.rows[0], n0 = strip * 16 + g8, n1 = n0 + 8;
+                    const float bias0 = p.bias && n0 < N ? __bfloat162float(p.bias[n0]) : 0.f;
+                    const float bias1 = p.bias && n1 < N ? __bfloat162float(p.bias[n1]) : 0.f;
+                    if (live0 && n0 < N) p.out[o0 + n0] = __float2bfloat16_rn(v.x + bias0);
+                    if (live1 && n0 < N) p.out[o1 + n0] = __float2bfloat16_rn(v.y + bias0);
+                    if (live0 && n1 < N) p.out[o0 + n1] = __float2bfloat16_rn(v.z + bias1);
+                    if (live1 && n1 < N) p.out[o1 + n1] = __float2bfloat16_rn(v.w + bias1);
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&rempty[rb]);
+            if (lane == 0) mbar_arrive32(rempty0 + 8u * rb);
         }
     }
     if (WHICH == kW4Up) grid_dep_launch();
