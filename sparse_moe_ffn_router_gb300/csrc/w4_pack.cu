@@ -42,11 +42,29 @@ __device__ __forceinline__ uint32_t w4_place(uint32_t code, int i) {
     return (s << 14) | ((m >> 2) << 13) | (((m >> 1) & 1u) << 10) | ((m & 1u) << 11);
 }
 
-// E2M1 code of a value: nearest, halfway cases to the even code, at most 6.
-__device__ __forceinline__ uint32_t e2m1_code(float v) {
-    const float m = fabsf(v);
-    const uint32_t c = (m > 0.25f) + (m >= 0.75f) + (m > 1.25f) + (m >= 1.75f) + (m > 2.5f) + (m >= 3.5f) + (m > 5.0f);
-    return c | (v < 0.f ? 8u : 0u);
+// Four codes of each half of a word, code i in bits 4i .. 4i+3, moved to the E2M1 packed order.
+__device__ __forceinline__ uint32_t e2m1_planes(uint32_t w) {
+    return ((w << 12) & 0x80008000u) | ((w << 6) & 0x01c001c0u) | ((w << 5) & 0x10001000u) | ((w >> 1) & 0x68386838u) |
+           ((w >> 2) & 0x02000200u) | ((w >> 8) & 0x00070007u) | ((w >> 3) & 0x04000400u);
+}
+
+// Two E2M1 codes (nearest, halfway cases to the even code, at most 6) in a byte, lo in its low half.
+__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Maximum and minimum of packed bf16; a NaN in either operand gives NaN.
+__device__ __forceinline__ uint32_t bf2_max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf2_min(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 __device__ __forceinline__ void st_record(uint8_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
@@ -64,70 +82,107 @@ __device__ __forceinline__ void st_meta(uint8_t* rec, int row, const bf16 (&s)[W
     }
 }
 
+// w / s for bf16 w and s, r = 1 / s rounded to nearest, as far as rounding the quotient to a code needs
+// it. A quotient of two 8-bit mantissas is either exactly halfway between two codes or at least 1/2040
+// away from that (codes are multiples of 1/2, |w / s| < 32), so an error of a few fp32 steps decides no
+// code; a quotient that is exactly halfway is representable, and one correction step of the product
+// w * r finds it: the remainder w - t * s is then exact, and t + remainder * r rounds to the quotient.
+__device__ __forceinline__ float w4_quotient(float w, float s, float r) {
+    const float t = w * r;
+    return fmaf(fmaf(-t, s, w), r, t);
+}
+
 // One row of a record quantised by its four lanes. Per group: scale s = bf16(max|w| / 7) for
 // INT4 (/ 6 for E2M1), or bf16(max / 15 - min / 15) over the values and 0 for INT4_ZP with zero
-// point rint(-min / s); codes are the nearest value of w / s (halfway to even). All divisions are
-// fp32, correctly rounded. A group of zeros has scale 0; one with a NaN or an infinity has scale
-// NaN and codes of value 0, so every product with it is NaN.
+// point rint(-min / s); codes are the nearest value of w / s (halfway to even). A group of zeros has
+// scale 0; one with a NaN or an infinity has scale NaN and codes of value 0, so every product with it
+// is NaN.
 template <int FMT, int G>
 __device__ __forceinline__ void quantize_row(const W4PackArgs& a, const bf16* src, int k0, int t, bool live, uint32_t (&words)[4],
-                             bf16 (&sc)[W4Rec<FMT, G>::kGroups], uint32_t (&zp)[W4Rec<FMT, G>::kGroups]) {
+                                             bf16 (&sc)[W4Rec<FMT, G>::kGroups], uint32_t (&zp)[W4Rec<FMT, G>::kGroups]) {
     constexpr int P = G / 32;  // 32-column pieces of a group
-    float v[4][8];
+    uint4 v[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int k = k0 + 32 * c + 8 * t;
-        if (live && k < a.cols)
-            unpack8(ld_stream(src + k), v[c]);
-        else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[c][e] = 0.f;
+        v[c] = live && k < a.cols ? ld_stream(src + k) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int gi = 0; gi < 4 / P; ++gi) {
-        float hi = 0.f, lo = 0.f;
-        bool bad = false;
+        // largest magnitude, or largest and smallest value with 0, of packed pairs
+        uint32_t hi2 = 0u, lo2 = 0u;
 #pragma unroll
-        for (int c = gi * P; c < (gi + 1) * P; ++c)
+        for (int c = gi * P; c < (gi + 1) * P; ++c) {
+            const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = v[c][e];
-                bad |= !(fabsf(x) < INFINITY);
+            for (int j = 0; j < 4; ++j) {
                 if (FMT == MOE_W4_INT4_ZP) {
-                    hi = fmaxf(hi, x);
-                    lo = fminf(lo, x);
+                    hi2 = bf2_max(hi2, x[j]);
+                    lo2 = bf2_min(lo2, x[j]);
                 } else {
-                    hi = fmaxf(hi, fabsf(x));
+                    hi2 = bf2_max(hi2, x[j] & 0x7fff7fffu);
                 }
             }
+        }
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            bad |= __shfl_xor_sync(0xffffffffu, (int)bad, o) != 0;
+            hi2 = bf2_max(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
+            if (FMT == MOE_W4_INT4_ZP) lo2 = bf2_min(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
         }
+        hi2 = bf2_max(hi2, hi2 >> 16);
+        lo2 = bf2_min(lo2, lo2 >> 16);
+        const float hi = bf_lo(hi2), lo = bf_lo(lo2);
+        const bool bad = !(hi < INFINITY) || !(lo > -INFINITY);
         const float raw = FMT == MOE_W4_INT4_ZP ? __fsub_rn(__fdiv_rn(hi, 15.f), __fdiv_rn(lo, 15.f))
                                                 : __fdiv_rn(hi, FMT == MOE_W4_INT4 ? 7.f : 6.f);
         const bf16 sb = __float2bfloat16_rn(raw);
         const float s = __bfloat162float(sb);
         const bool use = s > 0.f && !bad;
-        const float z = FMT == MOE_W4_INT4_ZP && use ? fminf(rintf(__fdiv_rn(-lo, s)), 15.f) : 0.f;
+        // (1 / s overflows below 2^-127, and a subnormal scale is too coarse for the quotients' bounds:
+        // such groups are divided, and clamped to the codes)
+        const bool tiny = s < 0x1p-120f;
+        const float r = use && !tiny ? __frcp_rn(s) : 0.f;
+        float zf = 0.f;
+        if (FMT == MOE_W4_INT4_ZP && use) zf = fminf(rintf(tiny ? __fdiv_rn(-lo, s) : w4_quotient(-lo, s, r)), 15.f);
         sc[gi] = bad ? __ushort_as_bfloat16(0x7fffu) : sb;
-        zp[gi] = (uint32_t)z;
+        zp[gi] = (uint32_t)zf;
 #pragma unroll
         for (int c = gi * P; c < (gi + 1) * P; ++c) {
-            uint32_t w = 0;
+            const uint32_t x[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+            float q[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float q = use ? __fdiv_rn(v[c][e], s) : 0.f;
-                uint32_t code;
-                if (FMT == MOE_W4_E2M1)
-                    code = e2m1_code(q);
-                else if (FMT == MOE_W4_INT4)
-                    code = (uint32_t)(int)(fminf(fmaxf(rintf(q), -8.f), 7.f) + 8.f);
-                else
-                    code = (uint32_t)(int)fminf(fmaxf(rintf(q) + z, 0.f), 15.f);
-                w |= w4_place<FMT>(code, e >> 1) << (16 * (e & 1));
+                const float w = (e & 1) ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1]);
+                q[e] = w4_quotient(w, s, r);
+            }
+            if (!use || tiny) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float w = (e & 1) ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1]);
+                    q[e] = use ? __fdiv_rn(w, s) : 0.f;
+                    if (FMT == MOE_W4_INT4) q[e] = fminf(fmaxf(q[e], -8.f), 7.f);
+                    if (FMT == MOE_W4_INT4_ZP) q[e] = fminf(fmaxf(q[e], -zf), 15.f - zf);
+                }
+            }
+            // code i of the low half is column 2i, of the high half column 2i + 1
+            uint32_t w = 0;
+            if (FMT == MOE_W4_E2M1) {
+                w = e2m1_pair(q[0], q[2]) | e2m1_pair(q[4], q[6]) << 8 | e2m1_pair(q[1], q[3]) << 16 | e2m1_pair(q[5], q[7]) << 24;
+                w = e2m1_planes(w);
+            } else {
+                // q + 1.5 * 2^23 rounds q to an integer (halfway to even) in the low mantissa bits
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t m0 = __float_as_uint(q[2 * i] + 12582912.f), m1 = __float_as_uint(q[2 * i + 1] + 12582912.f);
+                    if (FMT == MOE_W4_INT4) {
+                        w |= ((__byte_perm(m0, m1, 0x5410) & 0x000f000fu) ^ 0x00080008u) << (4 * i);
+                    } else {
+                        const int z = (int)zf, b = 0x4b400000;
+                        m0 = (uint32_t)min((int)m0 - b + z, 15);
+                        m1 = (uint32_t)min((int)m1 - b + z, 15);
+                        w |= (m0 | m1 << 16) << (4 * i);
+                    }
+                }
             }
             words[c] = w;
         }
