@@ -1,25 +1,31 @@
 // w4_gemm.cuh -- the products of packed 4-bit weights with many tokens, on the 5th-generation
 // tensor cores (tcgen05 + TMEM + TMA).
 //
-// D[128 token rows, BN weight rows] = A . B^T, both operands K-major bf16 in shared memory. A (the
-// token rows, or the h rows of down) comes by TMA, or is gathered from x for a routed expert's
-// gate_up. B does not exist in memory: sixteen warps read the packed records (16 rows by 128
-// columns each, straight from global memory into registers, one stage ahead), decode them,
-// multiply by the group scale and write bf16 into the 128-byte swizzled layout the tensor core
-// reads. A weight is rounded once, to bf16(s * v): the tensor core takes bf16 operands and its
-// accumulator spans all of K, so a scale per 32 to 128 columns cannot be applied behind it; the
+// D[128 weight rows, N tokens] = A . B^T with the weights as the A operand in tensor memory. The bf16
+// weights do not exist in memory: decoder warps read the packed records (a thread owns a weight row
+// of a record: 64 bytes of codes, the columns in order), decode them, multiply by the group's scale
+// and store bf16 pairs straight into TMEM (tcgen05.st, lane = weight row, column = pair of columns).
+// So a weight passes through no shared memory at all: with the weights staged there as the B operand
+// (the other way round) the stores, the token tiles and the MMAs' reads together came to more than the
+// 128 bytes a cycle of shared memory, and the tensor cores ran at half rate. B, the token rows (h rows
+// for down), K-major bf16 tiles in shared memory, comes by TMA, or is gathered from x for a routed
+// expert's gate_up. A weight is rounded once, to bf16(s * v): the tensor core takes bf16 operands and
+// its accumulator spans all of K, so a scale per 32 to 128 columns cannot be applied behind it; the
 // error is at most half a bf16 step a weight (2^-8), of the size of the roundings of h and Y.
 //
-// One persistent CTA per SM walks the tiles (group, N tile, M tile; the M tiles that share weights
-// run back to back). A stage is 128 columns (one record): 32 KB of A, 64 KB of B at BN = 256; two
-// stages, so the decoding of one overlaps the MMAs of the other: 8 MMAs of 128 x 256 x 16 are
-// ~1300 cycles, the 16 records of a stage ~2400 issue slots over four schedulers. Two accumulators
-// in TMEM let the epilogue of a tile overlap the next tile's MMAs. Roles:
-//   warp 0     TMA producer (one lane)            warps 2-5   epilogue (TMEM lane quadrants)
-//   warp 1     TMEM owner and MMA issuer           warps 6-21  decoders, and gatherers of A rows
-// Decoder stores: lane 4g + t writes 16 bytes (8 columns) of row g; odd rows take the two 32-column
-// pieces of a 64-column tile in the other order, which spreads the eight lanes of a store phase
-// (two rows) over all banks.
+// A tile is 256 weight rows (16 strips; for gate_up 128 features) by at most 128 tokens, as two MMAs of
+// 128 rows that share a stage's token rows (with 128-row tiles the token rows came from L2 twice as
+// often, ~8 TB/s, and bound the kernel). The tokens of a group are split evenly over its token tiles and N
+// is rounded up to 16, so a group of few tokens costs little tensor time. One persistent CTA per SM walks
+// the tiles (group, row tile, token tile; the token tiles that share weights run back to back). TMEM: an
+// accumulator of 128 columns for each row half, handed to the epilogue one after the other (the next
+// tile's first half starts while the second is written out), and four A stages of 128 columns of K (64
+// TMEM columns each). Roles:
+//   warp 0      TMA producer (one lane)           warps 2-5    epilogue (TMEM lane quadrants) of row half 0;
+//   warp 1      TMEM owner and MMA issuer                       gate_up: of both halves
+//   warps 6-9   gate_up: gatherers of token rows; else epilogue of row half 1
+//   warps 10-25 decoders: four groups of four warps, group j takes every fourth A stage, warp w lanes
+//               32 (w % 4) .. + 31
 #pragma once
 
 #include "launch.h"
@@ -29,184 +35,207 @@ namespace moe {
 
 enum : int { kW4GLinear = 0, kW4GUp = 1, kW4GDown = 2 };
 
+constexpr int kW4gRows = 256;    // weight rows of a tile: two halves of 128
+constexpr int kW4gTok = 128;     // tokens of a tile, at most
+constexpr int kW4gGroups = 257;  // routed experts and the shared one, at most
+
 struct W4GemmArgs {
     const uint8_t* w[2];   // packed matrices: routed (or linear), shared
     size_t matrix_bytes;   // of one routed matrix
     int rows[2], cols[2];  // of one matrix
     const bf16* bias;      // linear
     bf16* out;             // linear [T, rows]
-    int T;                 // linear: token rows
+    int T, tok_tiles;      // linear: token rows and their tiles
     uint32_t* err;
     uint64_t wait_ns;
 };
 
+// a0, a1: tensor maps of the token rows (linear, routed down; shared), boxes of 64 columns by 32 rows.
 cudaError_t launch_w4_gemm(int format, int group, int which, const W4GemmArgs& p, const CUtensorMap& a0,
-                           const CUtensorMap& a1, const LayerArgs& a, int bn, cudaStream_t s);
+                           const CUtensorMap& a1, const LayerArgs& a, cudaStream_t s);
 
 #ifdef __CUDACC__
 
-constexpr int kW4gM = 128, kW4gK = 128;          // token rows of a tile, columns of a stage
-constexpr int kW4gStages = 2;
-constexpr int kW4gDec = 16;                      // decoder warps
-constexpr int kW4gThreads = 32 * (6 + kW4gDec);
-constexpr uint32_t kW4gA = kW4gM * kW4gK * 2;    // bytes of a stage's A: two 64-column tiles
+constexpr int kW4gK = 128;                       // columns of a stage
+constexpr int kW4gAStages = 4, kW4gBStages = 6;
+constexpr int kW4gGather = 4, kW4gDec = 16;      // warps (the gatherers of gate_up are epilogue warps elsewhere)
+constexpr int kW4gIssuer1 = 6 + kW4gGather + kW4gDec;
+constexpr int kW4gThreads = 32 * (kW4gIssuer1 + 1);
+constexpr uint32_t kW4gB = kW4gTok * kW4gK * 2;  // bytes of a B stage: two 64-column tiles
+constexpr uint32_t kW4gACol = 2 * kW4gTok;       // first TMEM column of the A stages
+static_assert(kW4gACol + kW4gAStages * (kW4gK / 2) <= 512, "TMEM columns");
 
-template <int BN>
 struct W4GSmem {
-    static constexpr uint32_t kB = BN * kW4gK * 2;
-    static constexpr uint32_t kTiles = kW4gStages * (kW4gA + kB);
-    static constexpr uint32_t kScratch = 4 * 2048;  // epilogue: per warp 32 rows of 64 bytes
-    static constexpr uint32_t kBytes = 1024 + kTiles + 128 + kScratch;
+    static constexpr uint32_t kTiles = kW4gBStages * kW4gB;
+    static constexpr uint32_t kTokens = 8 * kW4gTok * 8;  // down: output row and scale of each token, per epilogue warp
+    static constexpr uint32_t kTable = (kW4gGroups + 1) * 4 + kW4gGroups * (uint32_t)sizeof(GemmGroup) + 12;
+    static constexpr uint32_t kBytes = 1024 + kTiles + 256 + kTokens + kTable;
+    static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
 struct W4Tile {
-    int m0, n_idx, rows, a_row, src, nk;
+    int m0, mt, n;       // first token of the tile in its group, tokens, tokens rounded up to 16
+    int row0, halves;    // first weight row, row halves (1 when the second lies past the matrix)
+    int b_row, src, nk;  // first B row of the group, 1: shared, stages
     int out_row0;        // up: first h row of the group
     const uint8_t* w;    // the group's matrix
 };
 
+// The groups and their first tiles, in shared memory (up, down).
+struct W4Table {
+    const int* start;
+    const GemmGroup* groups;
+    int n, total;
+};
+
+__host__ __device__ __forceinline__ int w4_row_tiles(int rows) { return (rows + kW4gRows - 1) / kW4gRows; }
+__host__ __device__ __forceinline__ int w4_tok_tiles(int rows) { return (rows + kW4gTok - 1) / kW4gTok; }
+
 // Tile t (tiles are visited in increasing order, so the group cursor g only advances).
 template <int WHICH>
-__device__ __forceinline__ bool w4_find_tile(const W4GemmArgs& p, const LayerArgs& a, int t, int& g, W4Tile& ti) {
-    if (WHICH == kW4GLinear) {
-        const int mt = (p.T + kW4gM - 1) / kW4gM;
-        ti.n_idx = t / mt;
-        ti.m0 = (t - ti.n_idx * mt) * kW4gM;
-        ti.rows = p.T;
-        ti.a_row = 0;
-        ti.src = 0;
-        ti.w = p.w[0];
-    } else {
-        const int32_t* start = WHICH == kW4GUp ? a.up_tiles : a.dn_tiles;
-        const int ng = *a.n_groups;
-        while (g < ng && t >= start[g + 1]) ++g;
-        if (g >= ng) return false;
-        const GemmGroup G = WHICH == kW4GUp ? a.up_groups[g] : a.dn_groups[g];
-        const int mt = (G.rows + kW4gM - 1) / kW4gM, local = t - start[g];
-        ti.n_idx = local / mt;
-        ti.m0 = (local - ti.n_idx * mt) * kW4gM;
-        ti.rows = G.rows;
-        ti.a_row = G.a_row0;
+__device__ __forceinline__ bool w4_find_tile(const W4GemmArgs& p, const W4Table& tab, int t, int& g, W4Tile& ti) {
+    if (t >= tab.total) return false;
+    int rows = p.T, local = t;
+    ti.b_row = ti.src = ti.out_row0 = 0;
+    ti.w = p.w[0];
+    if (WHICH != kW4GLinear) {
+        while (t >= tab.start[g + 1]) ++g;
+        const GemmGroup G = tab.groups[g];
+        rows = G.rows;
+        local = t - tab.start[g];
+        ti.b_row = G.a_row0;
         ti.src = G.src;
         ti.out_row0 = G.out_row0;
         ti.w = G.src ? p.w[1] : p.w[0] + (size_t)(G.b_row0 / p.rows[0]) * p.matrix_bytes;
     }
+    const int tiles = WHICH == kW4GLinear ? p.tok_tiles : w4_tok_tiles(rows);
+    int idx = local, per = rows;
+    ti.m0 = 0;
+    if (tiles > 1) {
+        per = (rows + tiles - 1) / tiles;
+        idx = local / tiles;
+        ti.m0 = (local - idx * tiles) * per;
+    }
+    ti.mt = min(per, rows - ti.m0);  // (at least 1: per is at least 65 when there are several tiles)
+    ti.n = (ti.mt + 15) & ~15;
+    ti.row0 = idx * kW4gRows;
+    ti.halves = (ti.src ? p.rows[1] : p.rows[0]) - ti.row0 > kW4gRows / 2 ? 2 : 1;
     ti.nk = ((ti.src ? p.cols[1] : p.cols[0]) + kW4gK - 1) / kW4gK;
     return true;
 }
 
-// One record's share of a lane, from global memory.
+// A thread's row of one record: codes [t][c], scales and zero points of its groups.
 template <int FMT, int G>
-__device__ __forceinline__ void w4_load_global(const uint8_t* rec, int lane, W4Frag<FMT, G>& f) {
+struct W4Row {
+    uint4 w[4];
+    uint32_t s[W4Rec<FMT, G>::kGroups == 4 ? 2 : 1];
+    uint32_t z;
+};
+template <int FMT, int G>
+__device__ __forceinline__ void w4_load_row(const uint8_t* rec, int r, W4Row<FMT, G>& f) {
     constexpr int N = W4Rec<FMT, G>::kGroups;
-    f.lo = ld_stream(rec + lane * 16);
-    f.hi = ld_stream(rec + 512 + lane * 16);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int row = (lane >> 2) + 8 * h;
-        const uint8_t* at = rec + W4Rec<FMT, G>::kScales + row * (2 * N);
-        if constexpr (N == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
-            f.s[h][0] = v.x;
-            f.s[h][1] = v.y;
-        } else if constexpr (N == 2) {
-            f.s[h][0] = __ldg(reinterpret_cast<const unsigned int*>(at));
-        } else {
-            f.s[h][0] = __ldg(reinterpret_cast<const unsigned short*>(at));
-        }
-        f.z[h] = 0;
-        if (FMT == MOE_W4_INT4_ZP) {
-            const uint8_t* za = rec + W4Rec<FMT, G>::kZeros + row * N;
-            f.z[h] = N == 4   ? __ldg(reinterpret_cast<const unsigned int*>(za))
-                     : N == 2 ? __ldg(reinterpret_cast<const unsigned short*>(za))
-                              : __ldg(za);
-        }
+    for (int t = 0; t < 4; ++t) f.w[t] = ld_ro(rec + r * 64 + t * 16);
+    const uint8_t* at = rec + W4Rec<FMT, G>::kScales + r * (2 * N);
+    if constexpr (N == 4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+        f.s[0] = v.x;
+        f.s[1] = v.y;
+    } else if constexpr (N == 2) {
+        f.s[0] = __ldg(reinterpret_cast<const unsigned int*>(at));
+    } else {
+        f.s[0] = __ldg(reinterpret_cast<const unsigned short*>(at));
+    }
+    f.z = 0;
+    if (FMT == MOE_W4_INT4_ZP) {
+        const uint8_t* za = rec + W4Rec<FMT, G>::kZeros + r * N;
+        f.z = N == 4   ? __ldg(reinterpret_cast<const unsigned int*>(za))
+              : N == 2 ? __ldg(reinterpret_cast<const unsigned short*>(za))
+                       : __ldg(za);
     }
 }
 
-// The group's scale in both halves of a word.
+// Decodes a row's 128 weights into 64 TMEM columns of this thread's lane.
 template <int FMT, int G>
-__device__ __forceinline__ uint32_t w4_scale2(const W4Frag<FMT, G>& f, int h, int gi) {
-    return __byte_perm(f.s[h][gi >> 1], 0u, (gi & 1) ? 0x3232 : 0x1010);
+__device__ __forceinline__ void w4_row_to_tmem(const W4Row<FMT, G>& f, uint32_t taddr) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int gi = c * 32 / G;
+        const uint32_t s = __byte_perm(f.s[gi >> 1], 0u, (gi & 1) ? 0x3232 : 0x1010);
+        uint32_t bias = 0xc308c308u;
+        if (FMT == MOE_W4_INT4_ZP) bias = __byte_perm(f.z, 0xc3u, 0x4040u | (uint32_t)(gi << 8) | (uint32_t)gi);
+        uint32_t v[16];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t word = c == 0 ? f.w[t].x : c == 1 ? f.w[t].y : c == 2 ? f.w[t].z : f.w[t].w;
+            uint32_t q[4];
+            w4_decode<FMT>(word, bias, q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * t + i] = bf2_mul(q[i], s);
+        }
+        tmem_st16(taddr + 16u * (uint32_t)c, v);
+    }
+    tmem_st_wait();
 }
 
-// Writes one record as bf16 into a stage's two 64-column tiles: rows r0 + g and r1 + g (multiples
-// of 8), tile stride `tile`.
-template <int FMT, int G>
-__device__ __forceinline__ void w4_expand(const W4Frag<FMT, G>& f, uint32_t sb, uint32_t tile, int r0, int r1, int lane) {
-    const uint32_t g = (uint32_t)lane >> 2, t = (uint32_t)lane & 3u;
-    const bool odd = g & 1u;
-    const uint32_t w[2][4] = {{f.lo.x, f.lo.y, f.lo.z, f.lo.w}, {f.hi.x, f.hi.y, f.hi.z, f.hi.w}};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t row = sb + ((uint32_t)(h ? r1 : r0) + g) * 128u;
-#pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                // even rows: piece c + i; odd rows: the other one
-                const uint32_t word = odd ? w[h][c + 1 - i] : w[h][c + i];
-                const int ge = (c + i) * 32 / G, go = (c + 1 - i) * 32 / G;
-                const uint32_t s = ge == go ? w4_scale2(f, h, ge) : odd ? w4_scale2(f, h, go) : w4_scale2(f, h, ge);
-                const uint32_t bias = ge == go ? w4_bias(f, h, ge) : odd ? w4_bias(f, h, go) : w4_bias(f, h, ge);
-                uint32_t v[4];
-                w4_decode<FMT>(word, bias, v);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = bf2_mul(v[j], s);
-                const uint32_t chunk = (odd ? (uint32_t)(1 - i) : (uint32_t)i) * 4u + t;
-                sts128(row + (uint32_t)(c >> 1) * tile + ((chunk ^ g) << 4), v);
-            }
-        }
-    }
-}
+// g / (1 + e^-g) by CUDA's fast exponential and division: at most ~100 fp32 steps off, far below the bf16
+// step of h; where e^-g passes 2^126 it is 0 (the exact value is below 2^-119).
+__device__ __forceinline__ float w4_silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 __device__ __forceinline__ void w4g_timeout(uint32_t* err, volatile int* abort_flag) {
     atomicOr(err, ERR_TIMEOUT);
     *abort_flag = 1;
 }
 
-template <int WHICH, int FMT, int G, int BN>
+template <int WHICH, int FMT, int G>
 __global__ void __launch_bounds__(kW4gThreads, 1)
-    k_w4_gemm(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
+    k_w4_gemm(const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
               const __grid_constant__ W4GemmArgs p, const __grid_constant__ LayerArgs a) {
     constexpr int kRec = W4Rec<FMT, G>::kBytes;
-    constexpr int kStrips = BN / 16;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-    uint8_t* sA = smem;
-    uint8_t* sB = smem + kW4gStages * kW4gA;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W4GSmem<BN>::kTiles);
-    uint64_t* full = bars;
-    uint64_t* empty = bars + kW4gStages;
-    uint64_t* fullA = bars + 2 * kW4gStages;  // gathered A rows
-    uint64_t* accf = bars + 3 * kW4gStages;
-    uint64_t* acce = accf + 2;
+    uint8_t* sB = smem;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W4GSmem::kTiles);
+    uint64_t* fullB = bars;                       // TMA (or the arrival in its place)
+    uint64_t* emptyB = fullB + kW4gBStages;
+    uint64_t* fullG = emptyB + kW4gBStages;       // gathered token rows
+    uint64_t* fullA = fullG + kW4gBStages;
+    uint64_t* emptyA = fullA + kW4gAStages;
+    uint64_t* accf = emptyA + kW4gAStages;
+    uint64_t* acce = accf + 2;  // (an accumulator for each row half)
     uint64_t* mma_done = acce + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    uint8_t* scratch = smem + W4GSmem<BN>::kTiles + 128;
+    static_assert((3 * kW4gBStages + 2 * kW4gAStages + 5) * 8 + 8 <= 256, "barriers");
+    uint2* tokens = reinterpret_cast<uint2*>(smem + W4GSmem::kTiles + 256);
+    int* tstart = reinterpret_cast<int*>(smem + W4GSmem::kTiles + 256 + W4GSmem::kTokens);
+    GemmGroup* tgroups = reinterpret_cast<GemmGroup*>(tstart + kW4gGroups + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t limit = p.wait_ns;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kW4gStages; ++s) {
-            mbar_init(&full[s], 1 + kW4gDec);
-            mbar_init(&empty[s], 1);
-            mbar_init(&fullA[s], 32 * kW4gDec);
+        for (int s = 0; s < kW4gBStages; ++s) {
+            mbar_init(&fullB[s], 1);
+            mbar_init(&emptyB[s], 2);
+            mbar_init(&fullG[s], 32 * kW4gGather);
+        }
+        for (int s = 0; s < kW4gAStages; ++s) {
+            mbar_init(&fullA[s], 4);
+            mbar_init(&emptyA[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf[b], 1);
             mbar_init(&acce[b], 4);
         }
-        mbar_init(mma_done, 1);
+        mbar_init(mma_done, 2);
         *abort_flag = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&tmA0);
-        tma_prefetch_desc(&tmA1);
+        tma_prefetch_desc(&tmB0);
+        tma_prefetch_desc(&tmB1);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, 2 * BN <= 256 ? 256 : 512);
+        tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -215,299 +244,375 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
     const uint32_t tmem = *tmem_slot;
     grid_dep_wait();  // the set-up above overlaps the previous kernel's end
     grid_dep_launch();
-    const int total = WHICH == kW4GLinear ? ((p.T + kW4gM - 1) / kW4gM) * ((p.rows[0] + BN - 1) / BN)
-                                          : (WHICH == kW4GUp ? a.up_tiles : a.dn_tiles)[*a.n_groups];
+    W4Table tab;
+    tab.start = tstart;
+    tab.groups = tgroups;
+    if (WHICH == kW4GLinear) {
+        tab.n = 1;
+        tab.total = p.tok_tiles * w4_row_tiles(p.rows[0]);
+    } else {
+        // the dispatch's groups and a prefix of their tiles
+        tab.n = *a.n_groups;
+        const GemmGroup* src = WHICH == kW4GUp ? a.up_groups : a.dn_groups;
+        if ((int)threadIdx.x < tab.n) {
+            const GemmGroup G = src[threadIdx.x];
+            tgroups[threadIdx.x] = G;
+            tstart[threadIdx.x + 1] = w4_tok_tiles(G.rows) * w4_row_tiles(G.src ? p.rows[1] : p.rows[0]);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int run = 0;
+            for (int i0 = 0; i0 < tab.n; i0 += 32) {
+                int v = i0 + lane < tab.n ? tstart[i0 + lane + 1] : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += y;
+                }
+                if (i0 + lane < tab.n) tstart[i0 + lane + 1] = run + v;
+                run += __shfl_sync(0xffffffffu, v, 31);
+            }
+            if (lane == 0) tstart[0] = 0;
+        }
+        __syncthreads();
+        tab.total = tstart[tab.n];
+    }
+    const int total = tab.total;
 
     if (warp == 0 && lane == 0) {
-        // ---------------- TMA producer: A, except a routed expert's token rows
+        // ---------------- TMA producer: B, except a routed expert's token rows
         int g = 0, it = 0;
-        bool issued[kW4gStages] = {};
-        uint32_t par[kW4gStages] = {};
+        bool issued[kW4gBStages] = {};
+        uint32_t par[kW4gBStages] = {};
         for (int t = blockIdx.x; t < total && !*abort_flag; t += gridDim.x) {
             W4Tile ti;
-            if (!w4_find_tile<WHICH>(p, a, t, g, ti)) break;
-            const CUtensorMap* mA = ti.src ? &tmA1 : &tmA0;
+            if (!w4_find_tile<WHICH>(p, tab, t, g, ti)) break;
+            const CUtensorMap* mB = ti.src ? &tmB1 : &tmB0;
+            const bool gathered = WHICH == kW4GUp && !ti.src;
+            const int boxes = (ti.n + 31) / 32;
             for (int kb = 0; kb < ti.nk; ++kb, ++it) {
-                const int s = it % kW4gStages;
-                const uint32_t ph = (uint32_t)(it / kW4gStages) & 1u;
-                if (!mbar_wait(&empty[s], ph ^ 1u, limit)) {
+                const int s = it % kW4gBStages;
+                const uint32_t ph = (uint32_t)(it / kW4gBStages) & 1u;
+                if (!mbar_wait(&emptyB[s], ph ^ 1u, limit)) {
                     w4g_timeout(p.err, abort_flag);
                     break;
-                }
-                const bool gathered = WHICH == kW4GUp && !ti.src;
-                mbar_arrive_expect_tx(&full[s], gathered ? 0u : kW4gA);
-                if (!gathered) {
-                    tma_load_2d(sA + s * kW4gA, mA, &full[s], kb * kW4gK, ti.a_row + ti.m0);
-                    tma_load_2d(sA + s * kW4gA + kW4gA / 2, mA, &full[s], kb * kW4gK + 64, ti.a_row + ti.m0);
                 }
                 issued[s] = true;
                 par[s] = ph;
+                if (gathered) {
+                    mbar_arrive(&fullB[s]);
+                    continue;
+                }
+                mbar_arrive_expect_tx(&fullB[s], (uint32_t)boxes * 8192u);
+                for (int i = 0; i < boxes; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        tma_load_2d(sB + s * kW4gB + j * (kW4gB / 2) + i * 4096, mB, &fullB[s], kb * kW4gK + 64 * j,
+                                    ti.b_row + ti.m0 + 32 * i);
             }
         }
         // every copy issued must land before shared memory is released
-        for (int s = 0; s < kW4gStages; ++s)
-            if (issued[s] && !mbar_wait(&full[s], par[s], limit)) w4g_timeout(p.err, abort_flag);
-    } else if (warp == 1 && lane == 0) {
-        // ---------------- MMA issuer
-        constexpr uint32_t idesc = idesc_bf16_f32(kW4gM, BN);
-        int g = 0, it = 0, local = 0;
-        for (int t = blockIdx.x; t < total && !*abort_flag; t += gridDim.x, ++local) {
-            W4Tile ti;
-            if (!w4_find_tile<WHICH>(p, a, t, g, ti)) break;
-            const int b = local & 1;
-            if (!mbar_wait(&acce[b], ((uint32_t)(local >> 1) & 1u) ^ 1u, limit)) {
-                w4g_timeout(p.err, abort_flag);
-                break;
-            }
-            tc_fence_after();
-            const uint32_t d = tmem + (uint32_t)(b * BN);
+        for (int s = 0; s < kW4gBStages; ++s)
+            if (issued[s] && !mbar_wait(&fullB[s], par[s], limit)) w4g_timeout(p.err, abort_flag);
+    } else if (warp == 1 || warp == kW4gIssuer1) {
+        // ---------------- MMA issuers: warp 1 the tiles' first row halves, kW4gIssuer1 the second ones
+        if (lane == 0) {
+            const int h = warp == 1 ? 0 : 1;
+            const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(sB));
+            const uint32_t d = tmem + (uint32_t)(h * kW4gTok);
+            int g = 0;
+            uint32_t sb = 0, pb = 0, ia = 0, pacc = 1;  // B stage and its phase, A stages passed, accumulator phase
             bool ok = true;
-            for (int kb = 0; kb < ti.nk; ++kb, ++it) {
-                const int s = it % kW4gStages;
-                const uint32_t ph = (uint32_t)(it / kW4gStages) & 1u;
-                if (!mbar_wait(&full[s], ph, limit) || (WHICH == kW4GUp && !mbar_wait(&fullA[s], ph, limit))) {
-                    w4g_timeout(p.err, abort_flag);
-                    ok = false;
-                    break;
+            for (int t = blockIdx.x; t < total && ok && !*abort_flag; t += gridDim.x) {
+                W4Tile ti;
+                if (!w4_find_tile<WHICH>(p, tab, t, g, ti)) break;
+                const uint32_t idesc = idesc_bf16_f32(kW4gRows / 2, ti.n);
+                const bool gathered = WHICH == kW4GUp && !ti.src, mine = h < ti.halves;
+                if (mine) {
+                    ok = mbar_wait(&acce[h], pacc, limit);
+                    pacc ^= 1u;
                 }
-                if (WHICH == kW4GUp) fence_proxy_async_smem();  // the gathered rows
-                tc_fence_after();
-                const uint32_t a_addr = smem_u32(sA + s * kW4gA), b_addr = smem_u32(sB + s * W4GSmem<BN>::kB);
+                for (int kb = 0; kb < ti.nk && ok; ++kb, ia += (uint32_t)ti.halves) {
+                    ok = mbar_wait(&fullB[sb], pb, limit);
+                    if (mine) {
+                        const uint32_t i = ia + (uint32_t)h, sa = i % kW4gAStages;
+                        if (WHICH == kW4GUp) ok = ok && mbar_wait(&fullG[sb], pb, limit);
+                        ok = ok && mbar_wait(&fullA[sa], i / kW4gAStages & 1u, limit);
+                        if (!ok) break;
+                        if (gathered) fence_proxy_async_smem();  // the gathered rows came through the generic proxy
+                        tc_fence_after();
+                        const uint64_t db = desc0 + (uint64_t)(sb * (kW4gB >> 4));
+                        const uint32_t acol = tmem + kW4gACol + sa * (uint32_t)(kW4gK / 2);
+                        mma_bf16_ta(d, acol, db, idesc, kb != 0);
 #pragma unroll
-                for (int kk = 0; kk < kW4gK / 16; ++kk) {
-                    const uint32_t o = (uint32_t)(kk & 3) * 32u;
-                    mma_bf16(d, sdesc_kmajor_sw128(a_addr + (uint32_t)(kk >> 2) * (kW4gA / 2) + o),
-                             sdesc_kmajor_sw128(b_addr + (uint32_t)(kk >> 2) * (W4GSmem<BN>::kB / 2) + o), idesc, (kb | kk) != 0);
+                        for (int kk = 1; kk < kW4gK / 16; ++kk)
+                            mma_bf16_ta(d, acol + (uint32_t)(kk * 8), db + (uint64_t)((kk >> 2) * (kW4gB >> 5) + (kk & 3) * 2), idesc, 1u);
+                        mma_commit(&emptyA[sa]);
+                        mma_commit(&emptyB[sb]);
+                    } else if (ok) {
+                        mbar_arrive(&emptyB[sb]);
+                    }
+                    if (++sb == kW4gBStages) {
+                        sb = 0;
+                        pb ^= 1u;
+                    }
                 }
-                mma_commit(&empty[s]);
+                if (!ok)
+                    w4g_timeout(p.err, abort_flag);
+                else if (mine)
+                    mma_commit(&accf[h]);
             }
-            if (!ok) break;
-            mma_commit(&accf[b]);
+            mma_commit(mma_done);
+            if (!mbar_wait(mma_done, 0, limit)) w4g_timeout(p.err, abort_flag);
         }
-        mma_commit(mma_done);
-        if (!mbar_wait(mma_done, 0, limit)) w4g_timeout(p.err, abort_flag);
-    } else if (warp >= 6) {
-        // ---------------- decoders: warp w takes strip w of the tile; gatherers: 8 lanes to a row's
-        // 128-byte piece, rows tid / 8 and tid / 8 + 64
-        const int dw = warp - 6, tid = threadIdx.x - 6 * 32;
-        const uint32_t c8 = (uint32_t)(lane & 7);
-        const uint64_t pol = l2_evict_last();  // each token row is read by K experts
-        const int r0 = WHICH == kW4GUp ? dw * 8 : dw * 16, r1 = WHICH == kW4GUp ? BN / 2 + dw * 8 : dw * 16 + 8;
-        int g = 0, it = 0, t = blockIdx.x, kb = 0;
-        W4Tile ti;
-        const uint8_t* rec = nullptr;  // this warp's records of the tile (NULL: none)
+    } else if (warp >= 6 + kW4gGather) {
+        // ---------------- decoders
+        const int dw = warp - 6 - kW4gGather, grp = dw >> 2, quad = warp & 3;
+        const uint32_t a0 = tmem + kW4gACol + (uint32_t)(grp * (kW4gK / 2)) + ((uint32_t)(quad * 32) << 16);
+        // A stages of a tile: (column block, row half); this group takes every fourth
+        int g = 0, t = blockIdx.x, pos = grp, n_pos = 0, halves = 1;
+        const uint8_t* strip[2] = {nullptr, nullptr};  // this thread's strips of the row halves (NULL: past the matrix)
         auto locate = [&]() -> bool {
-            if (t >= total || !w4_find_tile<WHICH>(p, a, t, g, ti)) return false;
-            const int strip = ti.n_idx * kStrips + dw, strips = ((ti.src ? p.rows[1] : p.rows[0]) + 15) / 16;
-            rec = dw < kStrips && strip < strips ? ti.w + (size_t)strip * ti.nk * kRec : nullptr;
+            W4Tile ti;
+            for (;;) {
+                if (!w4_find_tile<WHICH>(p, tab, t, g, ti)) return false;
+                if (pos < ti.nk * ti.halves) break;
+                pos -= ti.nk * ti.halves;
+                t += gridDim.x;
+            }
+            halves = ti.halves;
+            n_pos = ti.nk * ti.halves;
+            const int i = ti.row0 / 16 + 2 * quad + (lane >> 4), strips = ((ti.src ? p.rows[1] : p.rows[0]) + 15) / 16;
+            strip[0] = i < strips ? ti.w + (size_t)i * ti.nk * kRec : nullptr;
+            strip[1] = i + 8 < strips ? ti.w + (size_t)(i + 8) * ti.nk * kRec : nullptr;
             return true;
         };
+        W4Row<FMT, G> nxt = {};
+        auto load = [&]() {
+            const int kb = halves == 2 ? pos >> 1 : pos;
+            const uint8_t* q = halves == 2 && (pos & 1) ? strip[1] : strip[0];
+            if (q) w4_load_row<FMT, G>(q + kb * kRec, lane & 15, nxt);
+        };
         bool more = locate();
-        W4Frag<FMT, G> nxt = {};
-        if (more && rec) w4_load_global<FMT, G>(rec, lane, nxt);
-        const bf16* arow[2] = {nullptr, nullptr};
-        uint32_t live = 0;
-        while (more && !*abort_flag) {
-            const W4Frag<FMT, G> cur = nxt;
-            const bool have = rec != nullptr, gathered = WHICH == kW4GUp && !ti.src;
-            const int kcur = kb;
-            if (WHICH == kW4GUp && kb == 0 && gathered) {
-                live = 0;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int m = ti.m0 + (tid >> 3) + 64 * i;
-                    arow[i] = a.x + c8 * 8;
-                    if (m < ti.rows) {
-                        arow[i] += (size_t)(a.perm[ti.a_row + m] / a.K) * a.H;
-                        live |= 1u << i;
-                    }
-                }
-            }
-            if (++kb == ti.nk) {
-                kb = 0;
-                t += gridDim.x;
-                more = locate();
-            }
-            if (more && rec) w4_load_global<FMT, G>(rec + (size_t)kb * kRec, lane, nxt);
-            const int s = it % kW4gStages;
-            const uint32_t ph = (uint32_t)(it / kW4gStages) & 1u;
-            ++it;
-            if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, limit))) {
-                if (lane == 0) w4g_timeout(p.err, abort_flag);
-                break;
-            }
-            if (WHICH == kW4GUp) {
-                if (gathered) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t r = (uint32_t)(tid >> 3) + 64u * i;
-                            cp_async16(smem_u32(sA + s * kW4gA) + (uint32_t)j * (kW4gA / 2) + r * 128u + ((c8 ^ (r & 7u)) << 4),
-                                       arow[i] + kcur * kW4gK + 64 * j, ((live >> i) & 1u) * 16u, pol);
-                        }
-                    cp_async_arrive(&fullA[s]);
-                } else {
-                    mbar_arrive(&fullA[s]);
-                }
-            }
-            if (have)
-                w4_expand<FMT, G>(cur, smem_u32(sB + s * W4GSmem<BN>::kB), W4GSmem<BN>::kB / 2, r0, r1, lane);
-            fence_proxy_async_smem();  // the tensor core reads these rows through the async proxy
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
-        }
-        cp_async_wait_all();  // no copy may be in flight when the CTA exits
-    } else if (warp >= 2) {
-        // ---------------- epilogue: TMEM lanes 32 * (warp % 4) .. + 31, one accumulator row each
-        const int q = warp & 3, r = q * 32 + lane;
-        const uint32_t scr = smem_u32(scratch) + (uint32_t)q * 2048u;
-        int g = 0, local = 0;
-        for (int t = blockIdx.x; t < total && !*abort_flag; t += gridDim.x, ++local) {
-            W4Tile ti;
-            if (!w4_find_tile<WHICH>(p, a, t, g, ti)) break;
-            const int b = local & 1, m = ti.m0 + r;
-            const bool row_live = m < ti.rows;
-            // the row's destination, read before the accumulator wait
-            int tok = m, slot = a.K;
-            float sc = 0.f;
-            if (WHICH == kW4GDown && row_live) {
-                if (ti.src) {
-                    sc = a.sgate[m];
-                } else {
-                    const int pv = a.perm[ti.a_row + m];
-                    tok = pv / a.K;
-                    slot = pv - tok * a.K;
-                    sc = a.topw[pv];
-                }
-            }
-            if (!__all_sync(0xffffffffu, mbar_wait(&accf[b], (uint32_t)(local >> 1) & 1u, limit))) {
+        if (more) load();
+        for (int round = 0; more && !*abort_flag; ++round) {
+            const W4Row<FMT, G> cur = nxt;
+            pos += kW4gDec / 4;
+            if (pos >= n_pos) more = locate();
+            if (more) load();
+            if (!__all_sync(0xffffffffu, mbar_wait(&emptyA[grp], ((uint32_t)round & 1u) ^ 1u, limit))) {
                 if (lane == 0) w4g_timeout(p.err, abort_flag);
                 break;
             }
             tc_fence_after();
-            const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * BN);
-            if (WHICH == kW4GUp) {
-                constexpr int FH = BN / 2;
-                bf16* hrow = a.h + (size_t)(ti.out_row0 + m) * a.Imax + ti.n_idx * FH;
-#pragma unroll 1
-                for (int c = 0; c < FH / 16; ++c) {
-                    uint32_t gv[16], uv[16];
-                    tmem_ld16(tb + c * 16, gv);
-                    tmem_ld16(tb + FH + c * 16, uv);
-                    tmem_ld_wait();
-                    if (row_live) {
+            w4_row_to_tmem<FMT, G>(cur, a0);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&fullA[grp]);
+        }
+    } else if (WHICH == kW4GUp && warp >= 6) {
+        // ---------------- gatherers: token rows of x, 8 lanes to a row's 128-byte piece, 16 rows a round
+        {
+            const int tid = threadIdx.x - 6 * 32;
+            const uint32_t c8 = (uint32_t)(lane & 7);
+            const uint64_t pol = l2_evict_last();  // each token row is read by K experts
+            int g = 0, it = 0;
+            W4Tile ti;
+            int pv[8];  // the tile's pairs, read a tile ahead
+            auto pairs = [&](int t, W4Tile& q) -> bool {
+                if (!w4_find_tile<WHICH>(p, tab, t, g, q)) return false;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int k = j * 8 + i * 2;
-                                o[i] = pack_bf16x2(silu(__uint_as_float(gv[k])) * __uint_as_float(uv[k]),
-                                                   silu(__uint_as_float(gv[k + 1])) * __uint_as_float(uv[k + 1]));
-                            }
-                            reinterpret_cast<uint4*>(hrow + c * 16)[j] = make_uint4(o[0], o[1], o[2], o[3]);
-                        }
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const int m = (tid >> 3) + 16 * i;
+                    pv[i] = !q.src && m < q.mt ? a.perm[q.b_row + q.m0 + m] : 0;
                 }
-            } else {
-                // 32 columns of the warp's 32 rows at a time through shared memory (16-byte pieces
-                // swizzled by row), so that a store instruction writes 8 rows x 64 contiguous bytes
-                const int N = WHICH == kW4GLinear ? p.rows[0] : a.H;
-                bf16* orow = WHICH == kW4GLinear ? p.out + (size_t)m * N
-                                                 : a.Yb + ((size_t)tok * (a.K + 1) + slot) * a.H;
-                const bool whole = (N & 7) == 0;
+                return true;
+            };
+            bool more = pairs(blockIdx.x, ti);
+            for (int t = blockIdx.x; more && !*abort_flag;) {
+                const bf16* row[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) row[i] = a.x + c8 * 8 + (size_t)(pv[i] / a.K) * a.H;
+                const W4Tile cur = ti;
+                t += gridDim.x;
+                more = pairs(t, ti);
+                bool ok = true;
+                for (int kb = 0; kb < cur.nk; ++kb, ++it) {
+                    const int s = it % kW4gBStages;
+                    if (!__all_sync(0xffffffffu, mbar_wait(&emptyB[s], ((uint32_t)(it / kW4gBStages) & 1u) ^ 1u, limit))) {
+                        if (lane == 0) w4g_timeout(p.err, abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    if (cur.src) {
+                        mbar_arrive(&fullG[s]);
+                        continue;
+                    }
+                    const uint32_t st = smem_u32(sB + s * kW4gB);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t r = (uint32_t)(tid >> 3) + 16u * i;
+                        if (16 * i < cur.n)  // (rows between the tokens and N read a token row that exists)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                cp_async16(st + (uint32_t)j * (kW4gB / 2) + r * 128u + ((c8 ^ (r & 7u)) << 4),
+                                           row[i] + kb * kW4gK + 64 * j, 16u, pol);
+                    }
+                    cp_async_arrive(&fullG[s]);
+                }
+                if (!ok) break;
+            }
+            cp_async_wait_all();  // no copy may be in flight when the CTA exits
+        }
+    } else if (warp >= 2) {
+        // ---------------- epilogue: TMEM lanes 32 * (warp % 4) .. + 31, one weight row each
+        const int q = warp & 3;
+        int g = 0;
+        uint32_t used[2] = {0u, 0u};
+        bool dead = false;
+        for (int t = blockIdx.x; t < total && !dead && !*abort_flag; t += gridDim.x) {
+            W4Tile ti;
+            if (!w4_find_tile<WHICH>(p, tab, t, g, ti)) break;
+            uint2* tk = tokens + (warp - 2) * kW4gTok;
+            const uint32_t tks = smem_u32(tk);
+            if (WHICH == kW4GDown) {
+                // output row (token, slot) and scale of each token of the tile, read before the accumulator wait
+                for (int m = lane; m < ti.mt; m += 32) {
+                    int tok = ti.m0 + m, slot = a.K;
+                    float sc;
+                    if (ti.src) {
+                        sc = a.sgate[tok];
+                    } else {
+                        const int pv = a.perm[ti.b_row + ti.m0 + m];
+                        tok = pv / a.K;
+                        slot = pv - tok * a.K;
+                        sc = a.topw[pv];
+                    }
+                    tk[m] = make_uint2((uint32_t)(tok * (a.K + 1) + slot), __float_as_uint(sc));
+                }
+                __syncwarp();
+            }
+            for (int h = 0; h < ti.halves; ++h) {
+            if (WHICH != kW4GUp && h != (warp >= 6)) continue;  // the other warps' half
+            if (!__all_sync(0xffffffffu, mbar_wait(&accf[h], used[h] & 1u, limit))) {
+                if (lane == 0) w4g_timeout(p.err, abort_flag);
+                dead = true;
+                break;
+            }
+            ++used[h];
+            tc_fence_after();
+            const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kW4gTok);
+            const int row = ti.row0 + h * (kW4gRows / 2) + q * 32 + lane, rows = ti.src ? p.rows[1] : p.rows[0];
+            const float bias = WHICH == kW4GLinear && p.bias && row < rows ? __bfloat162float(p.bias[row]) : 0.f;
+            // (a lane stores 2 bytes a token, a warp 64 or, for gate_up, 32 contiguous ones: pairing rows or
+            // tokens for wider stores took more instructions than it saved)
+            const bool up = (lane >> 3) & 1;  // gate_up: a strip's rows 8 .. 15 are the up rows
+            const int ldo = WHICH == kW4GUp ? a.Imax : WHICH == kW4GDown ? a.H : rows;
+            bf16* out;
+            if (WHICH == kW4GUp)
+                out = a.h + (size_t)(ti.out_row0 + ti.m0 + up) * ldo + (row >> 4) * 8 + (row & 7);
+            else if (WHICH == kW4GDown)
+                out = a.Yb + row;
+            else
+                out = p.out + (size_t)ti.m0 * ldo + row;
+            const int live = row < rows ? ti.mt : 0;  // (rows past the matrix: a half of few strips)
+            uint32_t nx[16];
+            tmem_ld16(tb, nx);
 #pragma unroll 1
-                for (int c = 0; c < BN / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(tb + c * 32, v);
-                    tmem_ld_wait();
-                    const int n0 = ti.n_idx * BN + c * 32;
-                    if (n0 >= N) break;
+            for (int c0 = 0; c0 < ti.mt; c0 += 16) {  // 16 tokens at a time, read from TMEM one ahead
+                float v[16];
+                tmem_ld_wait16(nx);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t o[4];
+                for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(nx[c]);
+                if (c0 + 16 < ti.mt) tmem_ld16(tb + (uint32_t)c0 + 16u, nx);
+                if (WHICH == kW4GUp) {
+                    // lane pairs 8 apart hold gate and up of one feature: the gate lane forms h of the even
+                    // token, the up lane of the odd one
+                    bf16 y[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int k = j * 8 + i * 2;
-                            float x0 = __uint_as_float(v[k]), x1 = __uint_as_float(v[k + 1]);
-                            if (WHICH == kW4GDown) {
-                                x0 *= sc;
-                                x1 *= sc;
-                            } else if (p.bias) {
-                                x0 += n0 + k < N ? __bfloat162float(p.bias[n0 + k]) : 0.f;
-                                x1 += n0 + k + 1 < N ? __bfloat162float(p.bias[n0 + k + 1]) : 0.f;
-                            }
-                            o[i] = pack_bf16x2(x0, x1);
-                        }
-                        sts128(scr + (uint32_t)lane * 64u + (((uint32_t)j ^ (((uint32_t)lane >> 1) & 3u)) << 4), o);
+                    for (int c = 0; c < 8; ++c) {
+                        const float o = __shfl_xor_sync(0xffffffffu, up ? v[2 * c] : v[2 * c + 1], 8);
+                        y[c] = __float2bfloat16_rn(w4_silu(up ? o : v[2 * c]) * (up ? v[2 * c + 1] : o));
                     }
-                    __syncwarp();
-                    if (whole) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t rr = (uint32_t)(lane >> 2) + 8u * i, pc = (uint32_t)(lane & 3);
-                            const uint4 o = lds128_smem(scr + rr * 64u + ((pc ^ ((rr >> 1) & 3u)) << 4));
-                            bf16* dst = reinterpret_cast<bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(orow), (int)rr));
-                            if (__shfl_sync(0xffffffffu, (int)row_live, (int)rr) && n0 + (int)pc * 8 < N)
-                                *reinterpret_cast<uint4*>(dst + n0 + pc * 8) = o;
-                        }
-                    } else {  // rows that are not 16-byte aligned: one element a lane
-                        for (int rr = 0; rr < 32; ++rr) {
-                            const uint32_t at = scr + (uint32_t)rr * 64u + ((((uint32_t)lane >> 3) ^ (((uint32_t)rr >> 1) & 3u)) << 4) + ((uint32_t)lane & 7u) * 2u;
-                            uint16_t e;
-                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(at) : "memory");
-                            bf16* dst = reinterpret_cast<bf16*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(orow), rr));
-                            if (__shfl_sync(0xffffffffu, (int)row_live, rr) && n0 + lane < N) dst[n0 + lane] = __ushort_as_bfloat16(e);
-                        }
+                    for (int c = 0; c < 8; ++c) {
+                        if (c0 + 2 * c + up < live) *out = y[c];
+                        out += 2 * ldo;
                     }
-                    __syncwarp();
+                } else if (WHICH == kW4GDown) {
+#pragma unroll
+                    for (int b = 0; b < 16; b += 4) {  // (the rows are read before any store: the compiler keeps their order)
+                        const uint4 t0 = lds128_smem(tks + (uint32_t)(c0 + b) * 8u), t1 = lds128_smem(tks + (uint32_t)(c0 + b) * 8u + 16u);
+                        const uint32_t o[4] = {t0.x, t0.z, t1.x, t1.z};
+                        const float sc[4] = {__uint_as_float(t0.y), __uint_as_float(t0.w), __uint_as_float(t1.y), __uint_as_float(t1.w)};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (c0 + b + c < live) out[(uint64_t)o[c] * (uint32_t)ldo] = __float2bfloat16_rn(v[b + c] * sc[c]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        if (c0 + c < live) *out = __float2bfloat16_rn(v[c] + bias);
+                        out += ldo;
+                    }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acce[b]);
+            if (lane == 0) mbar_arrive(&acce[h]);
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * BN <= 256 ? 256 : 512);
+        tmem_dealloc(tmem, 512);
     }
 }
 
-template <int WHICH, int FMT, int G, int BN>
-cudaError_t launch_w4_gemm_t(const W4GemmArgs& p, const CUtensorMap& a0, const CUtensorMap& a1, const LayerArgs& a, cudaStream_t s) {
+template <int WHICH, int FMT, int G>
+cudaError_t launch_w4_gemm_t(const W4GemmArgs& args, const CUtensorMap& b0, const CUtensorMap& b1, const LayerArgs& a, cudaStream_t s) {
     static bool configured[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) dev = 0;
-    constexpr int bytes = (int)W4GSmem<BN>::kBytes;
+    constexpr int bytes = (int)W4GSmem::kBytes;
     if (!configured[dev]) {
         const cudaError_t e =
-            cudaFuncSetAttribute(k_w4_gemm<WHICH, FMT, G, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            cudaFuncSetAttribute(k_w4_gemm<WHICH, FMT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
+    W4GemmArgs p = args;
     int grid = a.num_sms;
     if (WHICH == kW4GLinear) {
-        const long long tiles = (long long)((p.T + kW4gM - 1) / kW4gM) * ((p.rows[0] + BN - 1) / BN);
-        if (tiles < grid) grid = (int)tiles;
+        // A tile's time is about that of its tokens, rounded up to 16, and of 32 more (the handshakes of a
+        // stage), so more and smaller token tiles are taken where they fill the waves of CTAs better.
+        const int rt = w4_row_tiles(p.rows[0]), least = w4_tok_tiles(p.T);
+        long long best = 0;
+        for (int n = least; n <= least + least / 2 + 1; ++n) {
+            const int per = (p.T + n - 1) / n, tiles = (p.T + per - 1) / per;
+            const long long cost = (((long long)tiles * rt + a.num_sms - 1) / a.num_sms) * (((per + 15) & ~15) + 32);
+            if (best == 0 || cost < best) {
+                best = cost;
+                p.tok_tiles = tiles;
+            }
+        }
+        if ((long long)p.tok_tiles * rt < grid) grid = p.tok_tiles * rt;
     }
     cudaError_t e;
     const int kernel = WHICH == kW4GLinear ? MOE_KERNEL_W4_LINEAR : WHICH == kW4GUp ? MOE_KERNEL_GATE_UP : MOE_KERNEL_DOWN;
     MOE_LAUNCH(kernel, s,
-               (e = launch_pdl(k_w4_gemm<WHICH, FMT, G, BN>, dim3(grid), dim3(kW4gThreads), (size_t)bytes, s, a0, a1, p, a)));
+               (e = launch_pdl(k_w4_gemm<WHICH, FMT, G>, dim3(grid), dim3(kW4gThreads), (size_t)bytes, s, b0, b1, p, a)));
     return e;
 }
 
 template <int FMT>
-cudaError_t launch_w4_gemm_f(int group, int which, const W4GemmArgs& p, const CUtensorMap& a0, const CUtensorMap& a1,
-                             const LayerArgs& a, int bn, cudaStream_t s) {
+cudaError_t launch_w4_gemm_f(int group, int which, const W4GemmArgs& p, const CUtensorMap& b0, const CUtensorMap& b1,
+                             const LayerArgs& a, cudaStream_t s) {
 #define MOE_W4_CASE(W, G) \
-    if (which == W && group == G) \
-        return bn == 256 ? launch_w4_gemm_t<W, FMT, G, 256>(p, a0, a1, a, s) : launch_w4_gemm_t<W, FMT, G, 128>(p, a0, a1, a, s)
+    if (which == W && group == G) return launch_w4_gemm_t<W, FMT, G>(p, b0, b1, a, s)
     MOE_W4_CASE(kW4GLinear, 32); MOE_W4_CASE(kW4GLinear, 64); MOE_W4_CASE(kW4GLinear, 128);
     MOE_W4_CASE(kW4GUp, 32); MOE_W4_CASE(kW4GUp, 64); MOE_W4_CASE(kW4GUp, 128);
     MOE_W4_CASE(kW4GDown, 32); MOE_W4_CASE(kW4GDown, 64); MOE_W4_CASE(kW4GDown, 128);
@@ -516,12 +621,12 @@ cudaError_t launch_w4_gemm_f(int group, int which, const W4GemmArgs& p, const CU
 }
 
 // One translation unit per format (compiled in parallel).
-cudaError_t launch_w4_gemm_int4(int group, int which, const W4GemmArgs& p, const CUtensorMap& a0, const CUtensorMap& a1,
-                                const LayerArgs& a, int bn, cudaStream_t s);
-cudaError_t launch_w4_gemm_int4_zp(int group, int which, const W4GemmArgs& p, const CUtensorMap& a0, const CUtensorMap& a1,
-                                   const LayerArgs& a, int bn, cudaStream_t s);
-cudaError_t launch_w4_gemm_e2m1(int group, int which, const W4GemmArgs& p, const CUtensorMap& a0, const CUtensorMap& a1,
-                                const LayerArgs& a, int bn, cudaStream_t s);
+cudaError_t launch_w4_gemm_int4(int group, int which, const W4GemmArgs& p, const CUtensorMap& b0, const CUtensorMap& b1,
+                                const LayerArgs& a, cudaStream_t s);
+cudaError_t launch_w4_gemm_int4_zp(int group, int which, const W4GemmArgs& p, const CUtensorMap& b0, const CUtensorMap& b1,
+                                   const LayerArgs& a, cudaStream_t s);
+cudaError_t launch_w4_gemm_e2m1(int group, int which, const W4GemmArgs& p, const CUtensorMap& b0, const CUtensorMap& b1,
+                                const LayerArgs& a, cudaStream_t s);
 
 #endif
 

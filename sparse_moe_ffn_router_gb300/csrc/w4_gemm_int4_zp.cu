@@ -3,9 +3,9 @@
 
 namespace moe {
 
-cudaError_t launch_w4_gemm_int4_zp(int group, int which, const W4GemmArgs& p, const CUtensorMap& a0, const CUtensorMap& a1,
-                              const LayerArgs& a, int bn, cudaStream_t s) {
-    return launch_w4_gemm_f<MOE_W4_INT4_ZP>(group, which, p, a0, a1, a, bn, s);
+cudaError_t launch_w4_gemm_int4_zp(int group, int which, const W4GemmArgs& p, const CUtensorMap& b0, const CUtensorMap& b1,
+                              const LayerArgs& a, cudaStream_t s) {
+    return launch_w4_gemm_f<MOE_W4_INT4_ZP>(group, which, p, b0, b1, a, s);
 }
 
 }  // namespace moe

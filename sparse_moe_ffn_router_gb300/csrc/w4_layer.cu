@@ -15,11 +15,11 @@ cudaError_t launch_w4_stream(int format, int group, int which, const W4StreamArg
 }
 
 cudaError_t launch_w4_gemm(int format, int group, int which, const W4GemmArgs& p, const CUtensorMap& a0,
-                           const CUtensorMap& a1, const LayerArgs& a, int bn, cudaStream_t s) {
+                           const CUtensorMap& a1, const LayerArgs& a, cudaStream_t s) {
     switch (format) {
-        case MOE_W4_INT4: return launch_w4_gemm_int4(group, which, p, a0, a1, a, bn, s);
-        case MOE_W4_INT4_ZP: return launch_w4_gemm_int4_zp(group, which, p, a0, a1, a, bn, s);
-        case MOE_W4_E2M1: return launch_w4_gemm_e2m1(group, which, p, a0, a1, a, bn, s);
+        case MOE_W4_INT4: return launch_w4_gemm_int4(group, which, p, a0, a1, a, s);
+        case MOE_W4_INT4_ZP: return launch_w4_gemm_int4_zp(group, which, p, a0, a1, a, s);
+        case MOE_W4_E2M1: return launch_w4_gemm_e2m1(group, which, p, a0, a1, a, s);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -29,7 +29,7 @@ constexpr int kW4GemmTokens = 64;
 
 static cudaError_t w4_linear_gemm(const moe_w4_format& f, const W4LinearArgs& l, cudaStream_t s) {
     CUtensorMap mx;
-    if (!make_bf16_map(&mx, l.x, l.T, l.K, l.K, 128)) return cudaErrorInvalidValue;
+    if (!make_bf16_map(&mx, l.x, l.T, l.K, l.K, 32)) return cudaErrorInvalidValue;
     W4GemmArgs p = {};
     p.w[0] = l.w;
     p.rows[0] = l.N;
@@ -41,16 +41,14 @@ static cudaError_t w4_linear_gemm(const moe_w4_format& f, const W4LinearArgs& l,
     p.wait_ns = l.wait_ns;
     LayerArgs a = {};
     a.num_sms = l.num_sms;
-    const long long mt = (l.T + 127) / 128;
-    const int bn = mt * ((l.N + 255) / 256) >= l.num_sms ? 256 : 128;
-    return launch_w4_gemm(f.format, f.group, kW4GLinear, p, mx, mx, a, bn, s);
+    return launch_w4_gemm(f.format, f.group, kW4GLinear, p, mx, mx, a, s);
 }
 
 // Gate_up and down of 256 tokens or more on the tensor cores.
 static cudaError_t w4_experts_gemm(const LayerArgs& a, const moe_w4_format& f, cudaStream_t s) {
     CUtensorMap mx, mh, mhs;  // the h rows are Imax apart; the columns past I (Is) of a row hold nothing
-    if (!make_bf16_map(&mx, a.x, a.T, a.H, a.H, 128) || !make_bf16_map(&mh, a.h, a.P + a.T, a.I, a.Imax, 128) ||
-        !make_bf16_map(&mhs, a.h, a.P + a.T, a.Is, a.Imax, 128))
+    if (!make_bf16_map(&mx, a.x, a.T, a.H, a.H, 32) || !make_bf16_map(&mh, a.h, a.P + a.T, a.I, a.Imax, 32) ||
+        !make_bf16_map(&mhs, a.h, a.P + a.T, a.Is, a.Imax, 32))
         return cudaErrorInvalidValue;
     W4GemmArgs p = {};
     p.err = &a.hdr->err;
@@ -60,14 +58,14 @@ static cudaError_t w4_experts_gemm(const LayerArgs& a, const moe_w4_format& f, c
     p.matrix_bytes = w4_matrix_bytes(f.format, f.group, 2 * a.I, a.H);
     p.rows[0] = 2 * a.I; p.rows[1] = 2 * a.Is;
     p.cols[0] = p.cols[1] = a.H;
-    cudaError_t e = launch_w4_gemm(f.format, f.group, kW4GUp, p, mx, mx, a, 2 * gemm_up_half(a), s);
+    cudaError_t e = launch_w4_gemm(f.format, f.group, kW4GUp, p, mx, mx, a, s);
     if (e != cudaSuccess) return e;
     p.w[0] = reinterpret_cast<const uint8_t*>(a.down);
     p.w[1] = reinterpret_cast<const uint8_t*>(a.sd);
     p.matrix_bytes = w4_matrix_bytes(f.format, f.group, a.H, a.I);
     p.rows[0] = p.rows[1] = a.H;
     p.cols[0] = a.I; p.cols[1] = a.Is;
-    e = launch_w4_gemm(f.format, f.group, kW4GDown, p, mh, mhs, a, gemm_down_bn(a), s);
+    e = launch_w4_gemm(f.format, f.group, kW4GDown, p, mh, mhs, a, s);
     if (e != cudaSuccess) return e;
     return launch_combine(a, s);
 }
