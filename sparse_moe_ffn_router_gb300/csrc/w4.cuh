@@ -201,12 +201,12 @@ __device__ __forceinline__ void w4_mma_first(float (&d)[4], uint32_t a0, uint32_
 }
 
 // b0 and b1 of w4_decode_fold.
-template <int FMT, int G>
-__device__ __forceinline__ void w4_bias_fold(const W4Frag<FMT, G>& f, int h, int gi, uint32_t& b0, uint32_t& b1) {
+template <int FMT>
+__device__ __forceinline__ void w4_bias_fold(uint32_t z, int gi, uint32_t& b0, uint32_t& b1) {
     b0 = 0xc208c208u;  // -34
     b1 = 0xc000c000u;  // -2
     if (FMT == MOE_W4_INT4_ZP) {
-        b0 = __byte_perm(f.z[h], 0xc2u, 0x4040u | (uint32_t)(gi << 8) | (uint32_t)gi);
+        b0 = __byte_perm(z, 0xc2u, 0x4040u | (uint32_t)(gi << 8) | (uint32_t)gi);
         b1 = bf2_add(b0, 0x42004200u);  // + 32
     }
 }
@@ -228,8 +228,8 @@ __device__ __forceinline__ void w4_mma_records(const W4Frag<FMT, G> (&f)[NR], co
             const uint32_t w0 = c == 0 ? f[r].lo.x : c == 1 ? f[r].lo.y : c == 2 ? f[r].lo.z : f[r].lo.w;
             const uint32_t w1 = c == 0 ? f[r].hi.x : c == 1 ? f[r].hi.y : c == 2 ? f[r].hi.z : f[r].hi.w;
             uint32_t b00, b01, b10, b11;
-            w4_bias_fold(f[r], 0, gi, b00, b01);
-            w4_bias_fold(f[r], 1, gi, b10, b11);
+            w4_bias_fold<FMT>(f[r].z[0], gi, b00, b01);
+            w4_bias_fold<FMT>(f[r].z[1], gi, b10, b11);
             w4_decode_fold<FMT>(w0, b00, b01, p[r]);
             w4_decode_fold<FMT>(w1, b10, b11, q[r]);
         }

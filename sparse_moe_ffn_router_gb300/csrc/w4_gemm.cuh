@@ -62,14 +62,17 @@ constexpr int kW4gGather = 4, kW4gDec = 16;      // warps (the gatherers of gate
 constexpr int kW4gIssuer1 = 6 + kW4gGather + kW4gDec;
 constexpr int kW4gThreads = 32 * (kW4gIssuer1 + 1);
 constexpr uint32_t kW4gB = kW4gTok * kW4gK * 2;  // bytes of a B stage: two 64-column tiles
+constexpr uint32_t kW4gChunk = 16 * 256;         // epilogue: 16 tokens of 128 bf16 rows
 constexpr uint32_t kW4gACol = 2 * kW4gTok;       // first TMEM column of the A stages
 static_assert(kW4gACol + kW4gAStages * (kW4gK / 2) <= 512, "TMEM columns");
 
 struct W4GSmem {
     static constexpr uint32_t kTiles = kW4gBStages * kW4gB;
-    static constexpr uint32_t kTokens = 8 * kW4gTok * 8;  // down: output row and scale of each token, per epilogue warp
-    static constexpr uint32_t kTable = (kW4gGroups + 1) * 4 + kW4gGroups * (uint32_t)sizeof(GemmGroup) + 12;
-    static constexpr uint32_t kBytes = 1024 + kTiles + 256 + kTokens + kTable;
+    static constexpr uint32_t kStage = kTiles;                   // epilogue: two chunks for each team
+    static constexpr uint32_t kTok = kStage + 4 * kW4gChunk;     // down: output row and scale of each token, per epilogue warp
+    static constexpr uint32_t kBars = kTok + 8 * kW4gTok * 8;
+    static constexpr uint32_t kTab = kBars + 256;
+    static constexpr uint32_t kBytes = 1024 + kTab + (kW4gGroups + 1) * 4 + kW4gGroups * (uint32_t)sizeof(GemmGroup) + 12;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -155,21 +158,22 @@ __device__ __forceinline__ void w4_load_row(const uint8_t* rec, int r, W4Row<FMT
     }
 }
 
-// Decodes a row's 128 weights into 64 TMEM columns of this thread's lane.
+// Decodes a row's 128 weights into 64 TMEM columns of this thread's lane: bf16(s * v / kUnfold), the factor (a
+// power of two) undone on the sums.
 template <int FMT, int G>
 __device__ __forceinline__ void w4_row_to_tmem(const W4Row<FMT, G>& f, uint32_t taddr) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int gi = c * 32 / G;
         const uint32_t s = __byte_perm(f.s[gi >> 1], 0u, (gi & 1) ? 0x3232 : 0x1010);
-        uint32_t bias = 0xc308c308u;
-        if (FMT == MOE_W4_INT4_ZP) bias = __byte_perm(f.z, 0xc3u, 0x4040u | (uint32_t)(gi << 8) | (uint32_t)gi);
+        uint32_t b0, b1;
+        w4_bias_fold<FMT>(f.z, gi, b0, b1);
         uint32_t v[16];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const uint32_t word = c == 0 ? f.w[t].x : c == 1 ? f.w[t].y : c == 2 ? f.w[t].z : f.w[t].w;
             uint32_t q[4];
-            w4_decode<FMT>(word, bias, q);
+            w4_decode_fold<FMT>(word, b0, b1, q);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[4 * t + i] = bf2_mul(q[i], s);
         }
@@ -187,16 +191,35 @@ __device__ __forceinline__ void w4g_timeout(uint32_t* err, volatile int* abort_f
     *abort_flag = 1;
 }
 
+// Barriers of an epilogue team (four warps).
+__device__ __forceinline__ void w4g_team_sync(int team) { asm volatile("bar.sync %0, 128;" ::"r"(team + 1) : "memory"); }
+__device__ __forceinline__ bool w4g_team_any(int team, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(team + 1)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void sts_bf16(uint32_t at, float v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(v))) : "memory");
+}
+
 template <int WHICH, int FMT, int G>
 __global__ void __launch_bounds__(kW4gThreads, 1)
     k_w4_gemm(const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
               const __grid_constant__ W4GemmArgs p, const __grid_constant__ LayerArgs a) {
     constexpr int kRec = W4Rec<FMT, G>::kBytes;
+    constexpr float kUnfold = W4Fold<FMT>::kUnfold;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     uint8_t* sB = smem;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W4GSmem::kTiles);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W4GSmem::kBars);
     uint64_t* fullB = bars;                       // TMA (or the arrival in its place)
     uint64_t* emptyB = fullB + kW4gBStages;
     uint64_t* fullG = emptyB + kW4gBStages;       // gathered token rows
@@ -208,8 +231,7 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     static_assert((3 * kW4gBStages + 2 * kW4gAStages + 5) * 8 + 8 <= 256, "barriers");
-    uint2* tokens = reinterpret_cast<uint2*>(smem + W4GSmem::kTiles + 256);
-    int* tstart = reinterpret_cast<int*>(smem + W4GSmem::kTiles + 256 + W4GSmem::kTokens);
+    int* tstart = reinterpret_cast<int*>(smem + W4GSmem::kTab);
     GemmGroup* tgroups = reinterpret_cast<GemmGroup*>(tstart + kW4gGroups + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t limit = p.wait_ns;
@@ -465,101 +487,136 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
             cp_async_wait_all();  // no copy may be in flight when the CTA exits
         }
     } else if (warp >= 2) {
-        // ---------------- epilogue: TMEM lanes 32 * (warp % 4) .. + 31, one weight row each
-        const int q = warp & 3;
-        int g = 0;
-        uint32_t used[2] = {0u, 0u};
-        bool dead = false;
-        for (int t = blockIdx.x; t < total && !dead && !*abort_flag; t += gridDim.x) {
-            W4Tile ti;
-            if (!w4_find_tile<WHICH>(p, tab, t, g, ti)) break;
-            uint2* tk = tokens + (warp - 2) * kW4gTok;
-            const uint32_t tks = smem_u32(tk);
+        // ---------------- epilogue: TMEM lanes 32 * (warp % 4) .. + 31, one weight row each; four warps to a
+        // row half (gate_up: one team of four for both). 16 tokens at a time pass through shared memory, where
+        // a token's 128 rows (64 h values) lie together, and leave in pieces of 16 bytes: stored from
+        // registers, 64 bytes a warp and token, the scattered rows of Y took longer than down's products.
+        const int q = warp & 3, team = warp >= 6;
+        constexpr int kPitch = WHICH == kW4GUp ? 128 : 256;  // bytes of a token
+        const uint32_t stage = smem_u32(smem + W4GSmem::kStage) + (uint32_t)team * 2u * kW4gChunk;
+        uint2* tk = reinterpret_cast<uint2*>(smem + W4GSmem::kTok) + (warp - 2) * kW4gTok;
+        const uint32_t tks = smem_u32(tk);
+        const bool up = (lane >> 3) & 1;  // gate_up: a strip's rows 8 .. 15 are the up rows
+        const uint32_t put = stage + (WHICH == kW4GUp ? (uint32_t)(up * kPitch + (q * 16 + (lane >> 4) * 8 + (lane & 7)) * 2)
+                                                      : (uint32_t)(q * 32 + lane) * 2u);
+        const int ldo = WHICH == kW4GUp ? a.Imax : WHICH == kW4GDown ? a.H : p.rows[0];
+        bf16* const out = WHICH == kW4GUp ? a.h : WHICH == kW4GDown ? a.Yb : p.out;
+        const bool bulk = WHICH != kW4GLinear || ((ldo & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0);
+        int g = 0, t = blockIdx.x;
+        uint32_t used[2] = {0u, 0u}, buf = 0;
+        W4Tile ti = {}, nx_ti = {};
+        int pv[kW4gTok / 32] = {};
+        // the next tile, and down's pairs of its tokens: read a tile ahead
+        auto find = [&]() -> bool {
+            if (!w4_find_tile<WHICH>(p, tab, t, g, nx_ti)) return false;
+            if (WHICH == kW4GDown && !nx_ti.src) {
+#pragma unroll
+                for (int i = 0; i < kW4gTok / 32; ++i) {
+                    const int m = lane + 32 * i;
+                    pv[i] = m < nx_ti.mt ? a.perm[nx_ti.b_row + nx_ti.m0 + m] : 0;
+                }
+            }
+            return true;
+        };
+        bool more = find(), dead = false;
+        while (more && !dead) {
+            ti = nx_ti;
             if (WHICH == kW4GDown) {
-                // output row (token, slot) and scale of each token of the tile, read before the accumulator wait
-                for (int m = lane; m < ti.mt; m += 32) {
-                    int tok = ti.m0 + m, slot = a.K;
-                    float sc;
-                    if (ti.src) {
-                        sc = a.sgate[tok];
-                    } else {
-                        const int pv = a.perm[ti.b_row + ti.m0 + m];
-                        tok = pv / a.K;
-                        slot = pv - tok * a.K;
-                        sc = a.topw[pv];
+                // output row (token, slot) and scale of each token of the tile
+#pragma unroll
+                for (int i = 0; i < kW4gTok / 32; ++i) {
+                    const int m = lane + 32 * i;
+                    if (m < ti.mt) {
+                        int tok = ti.m0 + m, slot = a.K;
+                        float sc;
+                        if (ti.src) {
+                            sc = a.sgate[tok];
+                        } else {
+                            tok = pv[i] / a.K;
+                            slot = pv[i] - tok * a.K;
+                            sc = a.topw[pv[i]];
+                        }
+                        tk[m] = make_uint2((uint32_t)(tok * (a.K + 1) + slot), __float_as_uint(kUnfold * sc));
                     }
-                    tk[m] = make_uint2((uint32_t)(tok * (a.K + 1) + slot), __float_as_uint(sc));
                 }
                 __syncwarp();
             }
+            t += gridDim.x;
+            more = find();
+            const int rows = ti.src ? p.rows[1] : p.rows[0];
             for (int h = 0; h < ti.halves; ++h) {
-            if (WHICH != kW4GUp && h != (warp >= 6)) continue;  // the other warps' half
-            if (!__all_sync(0xffffffffu, mbar_wait(&accf[h], used[h] & 1u, limit))) {
-                if (lane == 0) w4g_timeout(p.err, abort_flag);
-                dead = true;
-                break;
-            }
-            ++used[h];
-            tc_fence_after();
-            const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kW4gTok);
-            const int row = ti.row0 + h * (kW4gRows / 2) + q * 32 + lane, rows = ti.src ? p.rows[1] : p.rows[0];
-            const float bias = WHICH == kW4GLinear && p.bias && row < rows ? __bfloat162float(p.bias[row]) : 0.f;
-            // (a lane stores 2 bytes a token, a warp 64 or, for gate_up, 32 contiguous ones: pairing rows or
-            // tokens for wider stores took more instructions than it saved)
-            const bool up = (lane >> 3) & 1;  // gate_up: a strip's rows 8 .. 15 are the up rows
-            const int ldo = WHICH == kW4GUp ? a.Imax : WHICH == kW4GDown ? a.H : rows;
-            bf16* out;
-            if (WHICH == kW4GUp)
-                out = a.h + (size_t)(ti.out_row0 + ti.m0 + up) * ldo + (row >> 4) * 8 + (row & 7);
-            else if (WHICH == kW4GDown)
-                out = a.Yb + row;
-            else
-                out = p.out + (size_t)ti.m0 * ldo + row;
-            const int live = row < rows ? ti.mt : 0;  // (rows past the matrix: a half of few strips)
-            uint32_t nx[16];
-            tmem_ld16(tb, nx);
+                if (WHICH != kW4GUp && h != team) continue;  // the other warps' half
+                const int row0 = ti.row0 + h * (kW4gRows / 2), row = row0 + q * 32 + lane;
+                const float bias = WHICH == kW4GLinear && p.bias && row < rows ? __bfloat162float(p.bias[row]) : 0.f;
+                const int bytes = min(rows - row0, kW4gRows / 2) * (WHICH == kW4GUp ? 1 : 2);  // of a token
+                if (!__all_sync(0xffffffffu, mbar_wait(&accf[h], used[h] & 1u, limit))) {
+                    if (lane == 0) w4g_timeout(p.err, abort_flag);
+                    dead = true;
+                }
+                // the four warps of a team leave together, as they meet at its barrier
+                dead = w4g_team_any(team, dead || *abort_flag);
+                if (dead) break;
+                ++used[h];
+                tc_fence_after();
+                const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kW4gTok);
+                uint32_t nx[16];
+                tmem_ld16(tb, nx);
 #pragma unroll 1
-            for (int c0 = 0; c0 < ti.mt; c0 += 16) {  // 16 tokens at a time, read from TMEM one ahead
-                float v[16];
-                tmem_ld_wait16(nx);
+                for (int c0 = 0; c0 < ti.mt; c0 += 16, buf ^= 1u) {
+                    float v[16];
+                    tmem_ld_wait16(nx);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(nx[c]);
-                if (c0 + 16 < ti.mt) tmem_ld16(tb + (uint32_t)c0 + 16u, nx);
-                if (WHICH == kW4GUp) {
-                    // lane pairs 8 apart hold gate and up of one feature: the gate lane forms h of the even
-                    // token, the up lane of the odd one
-                    bf16 y[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float o = __shfl_xor_sync(0xffffffffu, up ? v[2 * c] : v[2 * c + 1], 8);
-                        y[c] = __float2bfloat16_rn(w4_silu(up ? o : v[2 * c]) * (up ? v[2 * c + 1] : o));
+                    for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(nx[c]);
+                    if (c0 + 16 < ti.mt) {  // the next 16 tokens
+                        tmem_ld16(tb + (uint32_t)c0 + 16u, nx);
+                    } else {  // the accumulator is read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acce[h]);
                     }
+                    if (!bulk) {  // rows that are not 16-byte aligned
+                        bf16* o = out + (size_t)(ti.m0 + c0) * ldo + row;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        if (c0 + 2 * c + up < live) *out = y[c];
-                        out += 2 * ldo;
+                        for (int c = 0; c < 16; ++c, o += ldo)
+                            if (c0 + c < ti.mt && row < rows) *o = __float2bfloat16_rn(fmaf(v[c], kUnfold, bias));
+                        continue;
                     }
-                } else if (WHICH == kW4GDown) {
+                    const uint32_t at = put + buf * kW4gChunk;
+                    if (WHICH == kW4GUp) {
+                        // lane pairs 8 apart hold gate and up of one feature: the gate lane forms h of the even
+                        // token, the up lane of the odd one
 #pragma unroll
-                    for (int b = 0; b < 16; b += 4) {  // (the rows are read before any store: the compiler keeps their order)
-                        const uint4 t0 = lds128_smem(tks + (uint32_t)(c0 + b) * 8u), t1 = lds128_smem(tks + (uint32_t)(c0 + b) * 8u + 16u);
-                        const uint32_t o[4] = {t0.x, t0.z, t1.x, t1.z};
-                        const float sc[4] = {__uint_as_float(t0.y), __uint_as_float(t0.w), __uint_as_float(t1.y), __uint_as_float(t1.w)};
+                        for (int c = 0; c < 8; ++c) {
+                            const float o = __shfl_xor_sync(0xffffffffu, up ? v[2 * c] : v[2 * c + 1], 8);
+                            sts_bf16(at + (uint32_t)(2 * c * kPitch), w4_silu(kUnfold * (up ? o : v[2 * c])) * (kUnfold * (up ? v[2 * c + 1] : o)));
+                        }
+                    } else {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (c0 + b + c < live) out[(uint64_t)o[c] * (uint32_t)ldo] = __float2bfloat16_rn(v[b + c] * sc[c]);
+                        for (int c = 0; c < 16; c += 2) {
+                            float s0 = 1.f, s1 = 1.f;
+                            if (WHICH == kW4GDown) {
+                                const uint4 e = lds128_smem(tks + (uint32_t)(c0 + c) * 8u);
+                                s0 = __uint_as_float(e.y);
+                                s1 = __uint_as_float(e.w);
+                            }
+                            sts_bf16(at + (uint32_t)(c * kPitch), WHICH == kW4GDown ? v[c] * s0 : fmaf(v[c], kUnfold, bias));
+                            sts_bf16(at + (uint32_t)((c + 1) * kPitch), WHICH == kW4GDown ? v[c + 1] * s1 : fmaf(v[c + 1], kUnfold, bias));
+                        }
                     }
-                } else {
+                    w4g_team_sync(team);  // (chunks alternate: the buffer is written again after the next chunk's)
+                    constexpr int kLanes = kPitch / 16;  // lanes to a token, 16 bytes each
+                    const int piece = lane % kLanes;
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        if (c0 + c < live) *out = __float2bfloat16_rn(v[c] + bias);
-                        out += ldo;
+                    for (int i = 0; i < kLanes / 8; ++i) {
+                        const int j = (q * (kLanes / 8) + i) * (32 / kLanes) + lane / kLanes, m = c0 + j;
+                        if (m < ti.mt && piece * 16 < bytes) {
+                            const uint4 o = lds128_smem(stage + buf * kW4gChunk + (uint32_t)(j * kPitch + piece * 16));
+                            const size_t r = WHICH == kW4GUp ? (size_t)(ti.out_row0 + ti.m0 + m)
+                                             : WHICH == kW4GDown ? (size_t)tk[m].x : (size_t)(ti.m0 + m);
+                            *reinterpret_cast<uint4*>(out + r * ldo + (WHICH == kW4GUp ? row0 / 2 : row0) + piece * 8) = o;
+                        }
                     }
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acce[h]);
             }
         }
     }
