@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
     }
     const int total = tab.total;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
+        if (elect_one()) {
         // ---------------- TMA producer: B, except a routed expert's token rows
         int g = 0, it = 0;
         bool issued[kW4gBStages] = {};
@@ -336,9 +337,10 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
         // every copy issued must land before shared memory is released
         for (int s = 0; s < kW4gBStages; ++s)
             if (issued[s] && !mbar_wait(&fullB[s], par[s], limit)) w4g_timeout(p.err, abort_flag);
+        }
     } else if (warp == 1 || warp == kW4gIssuer1) {
         // ---------------- MMA issuers: warp 1 the tiles' first row halves, kW4gIssuer1 the second ones
-        if (lane == 0) {
+        if (elect_one()) {
             const int h = warp == 1 ? 0 : 1;
             const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(sB));
             const uint32_t d = tmem + (uint32_t)(h * kW4gTok);
