@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
         const int q = warp & 3, team = warp >= 6;
         constexpr int kPitch = WHICH == kW4GUp ? 128 : 256;  // bytes of a token
         const uint32_t stage = smem_u32(smem + W4GSmem::kStage) + (uint32_t)team * 2u * kW4gChunk;
-        uint2* tk = reinterpret_cast<uint2*>(smem + W4GSmem::kTok) + (warp - 2) * kW4gTok;
+        uint32_t* tk = reinterpret_cast<uint32_t*>(smem + W4GSmem::kTok) + (warp - 2) * 2 * kW4gTok;  // rows, scales
         const uint32_t tks = smem_u32(tk);
         const bool up = (lane >> 3) & 1;  // gate_up: a strip's rows 8 .. 15 are the up rows
         const uint32_t put = stage + (WHICH == kW4GUp ? (uint32_t)(up * kPitch + (q * 16 + (lane >> 4) * 8 + (lane & 7)) * 2)
@@ -538,7 +538,8 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
                             slot = pv[i] - tok * a.K;
                             sc = a.topw[pv[i]];
                         }
-                        tk[m] = make_uint2((uint32_t)(tok * (a.K + 1) + slot), __float_as_uint(kUnfold * sc));
+                        tk[m] = (uint32_t)(tok * (a.K + 1) + slot);
+                        tk[kW4gTok + m] = __float_as_uint(kUnfold * sc);
                     }
                 }
                 __syncwarp();
@@ -584,40 +585,55 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
                         continue;
                     }
                     const uint32_t at = put + buf * kW4gChunk;
+                    // (reads, shuffles and stores of shared memory keep their order, so each kind comes in a block)
                     if (WHICH == kW4GUp) {
                         // lane pairs 8 apart hold gate and up of one feature: the gate lane forms h of the even
                         // token, the up lane of the odd one
+                        float o[8];
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float o = __shfl_xor_sync(0xffffffffu, up ? v[2 * c] : v[2 * c + 1], 8);
-                            sts_bf16(at + (uint32_t)(2 * c * kPitch), w4_silu(kUnfold * (up ? o : v[2 * c])) * (kUnfold * (up ? v[2 * c + 1] : o)));
-                        }
+                        for (int c = 0; c < 8; ++c) o[c] = __shfl_xor_sync(0xffffffffu, up ? v[2 * c] : v[2 * c + 1], 8);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            o[c] = w4_silu(kUnfold * (up ? o[c] : v[2 * c])) * (kUnfold * (up ? v[2 * c + 1] : o[c]));
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) sts_bf16(at + (uint32_t)(2 * c * kPitch), o[c]);
                     } else {
+                        if (WHICH == kW4GDown) {
+                            uint4 e[4];
 #pragma unroll
-                        for (int c = 0; c < 16; c += 2) {
-                            float s0 = 1.f, s1 = 1.f;
-                            if (WHICH == kW4GDown) {
-                                const uint4 e = lds128_smem(tks + (uint32_t)(c0 + c) * 8u);
-                                s0 = __uint_as_float(e.y);
-                                s1 = __uint_as_float(e.w);
+                            for (int c = 0; c < 4; ++c) e[c] = lds128_smem(tks + (uint32_t)(kW4gTok + c0 + 4 * c) * 4u);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                v[4 * c] *= __uint_as_float(e[c].x);
+                                v[4 * c + 1] *= __uint_as_float(e[c].y);
+                                v[4 * c + 2] *= __uint_as_float(e[c].z);
+                                v[4 * c + 3] *= __uint_as_float(e[c].w);
                             }
-                            sts_bf16(at + (uint32_t)(c * kPitch), WHICH == kW4GDown ? v[c] * s0 : fmaf(v[c], kUnfold, bias));
-                            sts_bf16(at + (uint32_t)((c + 1) * kPitch), WHICH == kW4GDown ? v[c + 1] * s1 : fmaf(v[c + 1], kUnfold, bias));
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) v[c] = fmaf(v[c], kUnfold, bias);
                         }
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) sts_bf16(at + (uint32_t)(c * kPitch), v[c]);
+                    }
+                    constexpr int kLanes = kPitch / 16, kPieces = kLanes / 8;  // lanes to a token, 16 bytes each
+                    const int piece = lane % kLanes;
+                    bf16* dst[kPieces];
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int m = c0 + (q * kPieces + i) * (32 / kLanes) + lane / kLanes;
+                        const size_t r = WHICH == kW4GUp ? (size_t)(ti.out_row0 + ti.m0 + m)
+                                         : WHICH == kW4GDown ? (size_t)tk[m] : (size_t)(ti.m0 + m);
+                        dst[i] = m < ti.mt && piece * 16 < bytes ? out + r * ldo + (WHICH == kW4GUp ? row0 / 2 : row0) + piece * 8 : nullptr;
                     }
                     w4g_team_sync(team);  // (chunks alternate: the buffer is written again after the next chunk's)
-                    constexpr int kLanes = kPitch / 16;  // lanes to a token, 16 bytes each
-                    const int piece = lane % kLanes;
+                    uint4 o[kPieces];
 #pragma unroll
-                    for (int i = 0; i < kLanes / 8; ++i) {
-                        const int j = (q * (kLanes / 8) + i) * (32 / kLanes) + lane / kLanes, m = c0 + j;
-                        if (m < ti.mt && piece * 16 < bytes) {
-                            const uint4 o = lds128_smem(stage + buf * kW4gChunk + (uint32_t)(j * kPitch + piece * 16));
-                            const size_t r = WHICH == kW4GUp ? (size_t)(ti.out_row0 + ti.m0 + m)
-                                             : WHICH == kW4GDown ? (size_t)tk[m].x : (size_t)(ti.m0 + m);
-                            *reinterpret_cast<uint4*>(out + r * ldo + (WHICH == kW4GUp ? row0 / 2 : row0) + piece * 8) = o;
-                        }
-                    }
+                    for (int i = 0; i < kPieces; ++i)
+                        o[i] = lds128_smem(stage + buf * kW4gChunk + (uint32_t)(((q * kPieces + i) * (32 / kLanes) + lane / kLanes) * kPitch + piece * 16));
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i)
+                        if (dst[i]) *reinterpret_cast<uint4*>(dst[i]) = o[i];
                 }
             }
         }
