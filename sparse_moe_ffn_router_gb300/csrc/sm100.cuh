@@ -281,6 +281,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 16 columns of the warp's TMEM lanes l .. l + 15 (l in taddr: 0 or 16 of its quadrant) as accumulator
+// fragments of 8 columns: thread 4g + t holds of block b lane g, columns 8b + 2t, 8b + 2t + 1 in r[4b], r[4b + 1]
+// and lane g + 8 in r[4b + 2], r[4b + 3].
+__device__ __forceinline__ void tmem_ld_frag2(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit elements to shared memory, transposed: register j's fragment (lane 4g + t: row g,
+// columns 2t, 2t + 1) goes to the eight 16-byte rows that lanes 8j .. 8j + 7 point to, one matrix column each.
+__device__ __forceinline__ void stmatrix4_trans(uint32_t at, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r0), "r"(r1), "r"(r2),
+                 "r"(r3)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // The same, tied to the registers of a tmem_ld16 that was issued earlier, so that no use of them moves

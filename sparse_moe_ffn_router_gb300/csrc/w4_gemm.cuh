@@ -62,7 +62,7 @@ constexpr int kW4gGather = 4, kW4gDec = 16;      // warps (the gatherers of gate
 constexpr int kW4gIssuer1 = 6 + kW4gGather + kW4gDec;
 constexpr int kW4gThreads = 32 * (kW4gIssuer1 + 1);
 constexpr uint32_t kW4gB = kW4gTok * kW4gK * 2;  // bytes of a B stage: two 64-column tiles
-constexpr uint32_t kW4gChunk = 16 * 256;         // epilogue: 16 tokens of 128 bf16 rows
+constexpr uint32_t kW4gChunk = 16 * 272;         // epilogue: 16 tokens of 128 bf16 rows
 constexpr uint32_t kW4gACol = 2 * kW4gTok;       // first TMEM column of the A stages
 static_assert(kW4gACol + kW4gAStages * (kW4gK / 2) <= 512, "TMEM columns");
 
@@ -205,8 +205,10 @@ __device__ __forceinline__ bool w4g_team_any(int team, bool v) {
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void sts_bf16(uint32_t at, float v) {
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(v))) : "memory");
+__device__ __forceinline__ uint2 lds64_smem(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
 }
 
 template <int WHICH, int FMT, int G>
@@ -494,13 +496,13 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
         // a token's 128 rows (64 h values) lie together, and leave in pieces of 16 bytes: stored from
         // registers, 64 bytes a warp and token, the scattered rows of Y took longer than down's products.
         const int q = warp & 3, team = warp >= 6;
-        constexpr int kPitch = WHICH == kW4GUp ? 128 : 256;  // bytes of a token
+        constexpr int kPitch = WHICH == kW4GUp ? 144 : 272;  // bytes of a token: 64 or 128 values, and 16 to spread the banks
         const uint32_t stage = smem_u32(smem + W4GSmem::kStage) + (uint32_t)team * 2u * kW4gChunk;
         uint32_t* tk = reinterpret_cast<uint32_t*>(smem + W4GSmem::kTok) + (warp - 2) * 2 * kW4gTok;  // rows, scales
         const uint32_t tks = smem_u32(tk);
-        const bool up = (lane >> 3) & 1;  // gate_up: a strip's rows 8 .. 15 are the up rows
-        const uint32_t put = stage + (WHICH == kW4GUp ? (uint32_t)(up * kPitch + (q * 16 + (lane >> 4) * 8 + (lane & 7)) * 2)
-                                                      : (uint32_t)(q * 32 + lane) * 2u);
+        // this lane's 16-byte row of a transposed store: matrix lane / 8, token lane % 8 of its block
+        const uint32_t put = stage + (WHICH == kW4GUp ? (uint32_t)((((lane >> 3) & 1) * 8 + (lane & 7)) * kPitch + (q * 2 + (lane >> 4)) * 16)
+                                                      : (uint32_t)(((lane >> 4) * 8 + (lane & 7)) * kPitch + q * 64 + ((lane >> 3) & 1) * 16));
         const int ldo = WHICH == kW4GUp ? a.Imax : WHICH == kW4GDown ? a.H : p.rows[0];
         bf16* const out = WHICH == kW4GUp ? a.h : WHICH == kW4GDown ? a.Yb : p.out;
         const bool bulk = WHICH != kW4GLinear || ((ldo & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0);
@@ -549,8 +551,11 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
             const int rows = ti.src ? p.rows[1] : p.rows[0];
             for (int h = 0; h < ti.halves; ++h) {
                 if (WHICH != kW4GUp && h != team) continue;  // the other warps' half
-                const int row0 = ti.row0 + h * (kW4gRows / 2), row = row0 + q * 32 + lane;
-                const float bias = WHICH == kW4GLinear && p.bias && row < rows ? __bfloat162float(p.bias[row]) : 0.f;
+                const int row0 = ti.row0 + h * (kW4gRows / 2), row = row0 + q * 32 + (lane >> 2);
+                float bias[4];  // of rows row + 8 j
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    bias[j] = WHICH == kW4GLinear && p.bias && row + 8 * j < rows ? __bfloat162float(p.bias[row + 8 * j]) : 0.f;
                 const int bytes = min(rows - row0, kW4gRows / 2) * (WHICH == kW4GUp ? 1 : 2);  // of a token
                 if (!__all_sync(0xffffffffu, mbar_wait(&accf[h], used[h] & 1u, limit))) {
                     if (lane == 0) w4g_timeout(p.err, abort_flag);
@@ -563,60 +568,63 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
                 tc_fence_after();
                 const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kW4gTok);
                 uint32_t nx[16];
-                tmem_ld16(tb, nx);
+                tmem_ld_frag2(tb, nx);
+                tmem_ld_frag2(tb + (16u << 16), nx + 8);
 #pragma unroll 1
                 for (int c0 = 0; c0 < ti.mt; c0 += 16, buf ^= 1u) {
-                    float v[16];
+                    float v[16];  // [8 i + 4 b + 2 k + e]: row 16 i + 8 k + lane / 4 of the warp's 32, token 8 b + 2 (lane % 4) + e
                     tmem_ld_wait16(nx);
 #pragma unroll
                     for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(nx[c]);
                     if (c0 + 16 < ti.mt) {  // the next 16 tokens
-                        tmem_ld16(tb + (uint32_t)c0 + 16u, nx);
+                        tmem_ld_frag2(tb + (uint32_t)c0 + 16u, nx);
+                        tmem_ld_frag2(tb + (16u << 16) + (uint32_t)c0 + 16u, nx + 8);
                     } else {  // the accumulator is read
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&acce[h]);
                     }
-                    if (!bulk) {  // rows that are not 16-byte aligned
-                        bf16* o = out + (size_t)(ti.m0 + c0) * ldo + row;
+                    if (WHICH == kW4GDown) {
 #pragma unroll
-                        for (int c = 0; c < 16; ++c, o += ldo)
-                            if (c0 + c < ti.mt && row < rows) *o = __float2bfloat16_rn(fmaf(v[c], kUnfold, bias));
+                        for (int b = 0; b < 2; ++b) {
+                            const uint2 e = lds64_smem(tks + (uint32_t)(kW4gTok + c0 + 8 * b + 2 * (lane & 3)) * 4u);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                v[8 * (j >> 1) + 4 * b + 2 * (j & 1)] *= __uint_as_float(e.x);
+                                v[8 * (j >> 1) + 4 * b + 2 * (j & 1) + 1] *= __uint_as_float(e.y);
+                            }
+                        }
+                    } else if (WHICH == kW4GLinear) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = fmaf(v[j], kUnfold, bias[2 * (j >> 3) + ((j >> 1) & 1)]);
+                    }
+                    if (!bulk) {  // rows that are not 16-byte aligned
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int m = c0 + 8 * ((j >> 2) & 1) + 2 * (lane & 3) + (j & 1), r = row + 16 * (j >> 3) + 8 * ((j >> 1) & 1);
+                            if (m < ti.mt && r < rows) out[(size_t)(ti.m0 + m) * ldo + r] = __float2bfloat16_rn(v[j]);
+                        }
                         continue;
                     }
                     const uint32_t at = put + buf * kW4gChunk;
-                    // (reads, shuffles and stores of shared memory keep their order, so each kind comes in a block)
                     if (WHICH == kW4GUp) {
-                        // lane pairs 8 apart hold gate and up of one feature: the gate lane forms h of the even
-                        // token, the up lane of the odd one
-                        float o[8];
+                        // rows 0 .. 7 of a strip are gate, 8 .. 15 up: a thread holds both of a feature
+                        uint32_t hv[4];
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) o[c] = __shfl_xor_sync(0xffffffffu, up ? v[2 * c] : v[2 * c + 1], 8);
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            o[c] = w4_silu(kUnfold * (up ? o[c] : v[2 * c])) * (kUnfold * (up ? v[2 * c + 1] : o[c]));
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) sts_bf16(at + (uint32_t)(2 * c * kPitch), o[c]);
-                    } else {
-                        if (WHICH == kW4GDown) {
-                            uint4 e[4];
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) e[c] = lds128_smem(tks + (uint32_t)(kW4gTok + c0 + 4 * c) * 4u);
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                v[4 * c] *= __uint_as_float(e[c].x);
-                                v[4 * c + 1] *= __uint_as_float(e[c].y);
-                                v[4 * c + 2] *= __uint_as_float(e[c].z);
-                                v[4 * c + 3] *= __uint_as_float(e[c].w);
-                            }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) v[c] = fmaf(v[c], kUnfold, bias);
+                        for (int j = 0; j < 4; ++j) {  // strip j / 2, tokens of block j % 2
+                            const float* f = v + 4 * j;
+                            hv[j] = pack_bf16x2(w4_silu(kUnfold * f[0]) * (kUnfold * f[2]), w4_silu(kUnfold * f[1]) * (kUnfold * f[3]));
                         }
+                        stmatrix4_trans(at, hv[0], hv[1], hv[2], hv[3]);
+                    } else {
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) sts_bf16(at + (uint32_t)(c * kPitch), v[c]);
+                        for (int i = 0; i < 2; ++i) {
+                            const float* f = v + 8 * i;
+                            stmatrix4_trans(at + 32u * i, pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                            pack_bf16x2(f[6], f[7]));
+                        }
                     }
-                    constexpr int kLanes = kPitch / 16, kPieces = kLanes / 8;  // lanes to a token, 16 bytes each
+                    constexpr int kLanes = (kPitch - 16) / 16, kPieces = kLanes / 8;  // lanes to a token, 16 bytes each
                     const int piece = lane % kLanes;
                     bf16* dst[kPieces];
 #pragma unroll
