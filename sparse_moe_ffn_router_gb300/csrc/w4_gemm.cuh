@@ -57,7 +57,7 @@ cudaError_t launch_w4_gemm(int format, int group, int which, const W4GemmArgs& p
 #ifdef __CUDACC__
 
 constexpr int kW4gK = 128;                       // columns of a stage
-constexpr int kW4gAStages = 4, kW4gBStages = 6;
+constexpr int kW4gAStages = 4, kW4gBStages = 6;  // (A: two for each row half)
 constexpr int kW4gGather = 4, kW4gDec = 16;      // warps (the gatherers of gate_up are epilogue warps elsewhere)
 constexpr int kW4gIssuer1 = 6 + kW4gGather + kW4gDec;
 constexpr int kW4gThreads = 32 * (kW4gIssuer1 + 1);
@@ -72,7 +72,7 @@ struct W4GSmem {
     static constexpr uint32_t kTok = kStage + 4 * kW4gChunk;     // down: output row and scale of each token, per epilogue warp
     static constexpr uint32_t kBars = kTok + 8 * kW4gTok * 8;
     static constexpr uint32_t kTab = kBars + 256;
-    static constexpr uint32_t kBytes = 1024 + kTab + (kW4gGroups + 1) * 4 + kW4gGroups * (uint32_t)sizeof(GemmGroup) + 12;
+    static constexpr uint32_t kBytes = 1024 + kTab + (kW4gGroups + 1) * 4 + kW4gGroups * 20 + 12;
     static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -84,48 +84,92 @@ struct W4Tile {
     const uint8_t* w;    // the group's matrix
 };
 
-// The groups and their first tiles, in shared memory (up, down).
-struct W4Table {
-    const int* start;
-    const GemmGroup* groups;
-    int n, total;
+// A group as the tiles need it (in shared memory for up and down).
+struct W4Group {
+    int rows, b_row, out_row;
+    int matrix;      // of the routed weights; -1: the shared ones
+    uint32_t tiles;  // token tiles << 8 | tokens of one
 };
 
 __host__ __device__ __forceinline__ int w4_row_tiles(int rows) { return (rows + kW4gRows - 1) / kW4gRows; }
 __host__ __device__ __forceinline__ int w4_tok_tiles(int rows) { return (rows + kW4gTok - 1) / kW4gTok; }
-
-// Tile t (tiles are visited in increasing order, so the group cursor g only advances).
-template <int WHICH>
-__device__ __forceinline__ bool w4_find_tile(const W4GemmArgs& p, const W4Table& tab, int t, int& g, W4Tile& ti) {
-    if (t >= tab.total) return false;
-    int rows = p.T, local = t;
-    ti.b_row = ti.src = ti.out_row0 = 0;
-    ti.w = p.w[0];
-    if (WHICH != kW4GLinear) {
-        while (t >= tab.start[g + 1]) ++g;
-        const GemmGroup G = tab.groups[g];
-        rows = G.rows;
-        local = t - tab.start[g];
-        ti.b_row = G.a_row0;
-        ti.src = G.src;
-        ti.out_row0 = G.out_row0;
-        ti.w = G.src ? p.w[1] : p.w[0] + (size_t)(G.b_row0 / p.rows[0]) * p.matrix_bytes;
-    }
-    const int tiles = WHICH == kW4GLinear ? p.tok_tiles : w4_tok_tiles(rows);
-    int idx = local, per = rows;
-    ti.m0 = 0;
-    if (tiles > 1) {
-        per = (rows + tiles - 1) / tiles;
-        idx = local / tiles;
-        ti.m0 = (local - idx * tiles) * per;
-    }
-    ti.mt = min(per, rows - ti.m0);  // (at least 1: per is at least 65 when there are several tiles)
-    ti.n = (ti.mt + 15) & ~15;
-    ti.row0 = idx * kW4gRows;
-    ti.halves = (ti.src ? p.rows[1] : p.rows[0]) - ti.row0 > kW4gRows / 2 ? 2 : 1;
-    ti.nk = ((ti.src ? p.cols[1] : p.cols[0]) + kW4gK - 1) / kW4gK;
-    return true;
+// A tile's time, in arbitrary units: its stages, each about as long as 160 tokens' MMAs and those of its tokens.
+__device__ __forceinline__ uint32_t w4_tile_cost(int cols, int per) {
+    return (uint32_t)((cols + 127) / 128) * (uint32_t)(10 + (per + 15) / 16);
 }
+
+// A CTA's tiles: a run of (group, row tile, token tile), cut where the running cost passes the CTA's share of
+// the whole. Every role walks the same tiles; with tiles taken in turn by all CTAs instead, finding the next
+// one (a search over the groups and two divisions) was as long as a stage.
+template <int WHICH>
+struct W4Walk {
+    const W4GemmArgs& p;
+    const W4Group* groups;
+    int g, i, r, tok_tiles, row_tiles, per, rows;
+    uint32_t pos, hi, cost;
+    W4Tile ti;
+
+    // cost: prefix of the groups' costs (n_groups + 1); linear: none, one group of p.tok_tiles
+    __device__ __forceinline__ W4Walk(const W4GemmArgs& args, const W4Group* gr, const uint32_t* prefix, int n) : p(args), groups(gr) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t total = WHICH == kW4GLinear ? (uint32_t)(p.tok_tiles * w4_row_tiles(p.rows[0])) : prefix[n];
+        pos = (uint32_t)((uint64_t)total * blockIdx.x / gridDim.x);
+        hi = (uint32_t)((uint64_t)total * (blockIdx.x + 1) / gridDim.x);
+        g = 0;
+        if (WHICH != kW4GLinear) {
+            for (int g0 = 0; g0 < n; g0 += 32)
+                g += __popc(__ballot_sync(0xffffffffu, g0 + lane < n && prefix[g0 + lane + 1] <= pos));
+        }
+        const uint32_t first = WHICH == kW4GLinear ? 0u : prefix[g];
+        group();
+        const uint32_t local = (pos - first + cost - 1) / cost;  // the first tile that starts in the share
+        pos = first + local * cost;
+        r = (int)(local / (uint32_t)tok_tiles);
+        i = (int)local - r * tok_tiles;
+    }
+    __device__ __forceinline__ void group() {
+        if (WHICH == kW4GLinear) {
+            tok_tiles = p.tok_tiles;
+            rows = p.T;
+            per = (rows + tok_tiles - 1) / tok_tiles;
+            ti.b_row = ti.src = ti.out_row0 = 0;
+            ti.w = p.w[0];
+            cost = 1;
+        } else {
+            const W4Group G = groups[g];
+            tok_tiles = (int)(G.tiles >> 8);
+            per = (int)(G.tiles & 0xffu);
+            rows = G.rows;
+            ti.b_row = G.b_row;
+            ti.out_row0 = G.out_row;
+            ti.src = G.matrix < 0;
+            ti.w = G.matrix < 0 ? p.w[1] : p.w[0] + (size_t)G.matrix * p.matrix_bytes;
+            cost = w4_tile_cost(p.cols[ti.src], per);
+        }
+        row_tiles = w4_row_tiles(p.rows[ti.src]);
+        ti.nk = (p.cols[ti.src] + kW4gK - 1) / kW4gK;
+    }
+    // The next tile into ti.
+    __device__ __forceinline__ bool next() {
+        if (pos >= hi) return false;
+        if (r == row_tiles) {
+            i = r = 0;
+            ++g;
+            group();
+        }
+        ti.m0 = i * per;
+        ti.mt = min(per, rows - ti.m0);
+        ti.n = (ti.mt + 15) & ~15;
+        ti.row0 = r * kW4gRows;
+        ti.halves = p.rows[ti.src] - ti.row0 > kW4gRows / 2 ? 2 : 1;
+        pos += cost;
+        if (++i == tok_tiles) {
+            i = 0;
+            ++r;
+        }
+        return true;
+    }
+};
 
 // A thread's row of one record: codes [t][c], scales and zero points of its groups.
 template <int FMT, int G>
@@ -233,8 +277,8 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     static_assert((3 * kW4gBStages + 2 * kW4gAStages + 5) * 8 + 8 <= 256, "barriers");
-    int* tstart = reinterpret_cast<int*>(smem + W4GSmem::kTab);
-    GemmGroup* tgroups = reinterpret_cast<GemmGroup*>(tstart + kW4gGroups + 1);
+    uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + W4GSmem::kTab);  // of the groups' costs
+    W4Group* groups = reinterpret_cast<W4Group*>(prefix + kW4gGroups + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t limit = p.wait_ns;
 
@@ -268,50 +312,43 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
     const uint32_t tmem = *tmem_slot;
     grid_dep_wait();  // the set-up above overlaps the previous kernel's end
     grid_dep_launch();
-    W4Table tab;
-    tab.start = tstart;
-    tab.groups = tgroups;
-    if (WHICH == kW4GLinear) {
-        tab.n = 1;
-        tab.total = p.tok_tiles * w4_row_tiles(p.rows[0]);
-    } else {
-        // the dispatch's groups and a prefix of their tiles
-        tab.n = *a.n_groups;
-        const GemmGroup* src = WHICH == kW4GUp ? a.up_groups : a.dn_groups;
-        if ((int)threadIdx.x < tab.n) {
-            const GemmGroup G = src[threadIdx.x];
-            tgroups[threadIdx.x] = G;
-            tstart[threadIdx.x + 1] = w4_tok_tiles(G.rows) * w4_row_tiles(G.src ? p.rows[1] : p.rows[0]);
+    int n_groups = 1;
+    if (WHICH != kW4GLinear) {
+        // the dispatch's groups and the prefix of their costs
+        n_groups = *a.n_groups;
+        if ((int)threadIdx.x < n_groups) {
+            const GemmGroup G = (WHICH == kW4GUp ? a.up_groups : a.dn_groups)[threadIdx.x];
+            const int tiles = w4_tok_tiles(G.rows), per = (G.rows + tiles - 1) / tiles;  // (at least 65 of several: none is empty)
+            groups[threadIdx.x] = {G.rows, G.a_row0, G.out_row0, G.src ? -1 : G.b_row0 / p.rows[0], (uint32_t)tiles << 8 | (uint32_t)per};
+            prefix[threadIdx.x + 1] = (uint32_t)(tiles * w4_row_tiles(p.rows[G.src ? 1 : 0])) * w4_tile_cost(p.cols[G.src ? 1 : 0], per);
         }
         __syncthreads();
         if (warp == 0) {
-            int run = 0;
-            for (int i0 = 0; i0 < tab.n; i0 += 32) {
-                int v = i0 + lane < tab.n ? tstart[i0 + lane + 1] : 0;
+            uint32_t run = 0;
+            for (int i0 = 0; i0 < n_groups; i0 += 32) {
+                uint32_t v = i0 + lane < n_groups ? prefix[i0 + lane + 1] : 0;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, v, o);
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
                     if (lane >= o) v += y;
                 }
-                if (i0 + lane < tab.n) tstart[i0 + lane + 1] = run + v;
+                if (i0 + lane < n_groups) prefix[i0 + lane + 1] = run + v;
                 run += __shfl_sync(0xffffffffu, v, 31);
             }
-            if (lane == 0) tstart[0] = 0;
+            if (lane == 0) prefix[0] = 0;
         }
         __syncthreads();
-        tab.total = tstart[tab.n];
     }
-    const int total = tab.total;
+    W4Walk<WHICH> walk(p, groups, prefix, n_groups);
 
     if (warp == 0) {
         if (elect_one()) {
         // ---------------- TMA producer: B, except a routed expert's token rows
-        int g = 0, it = 0;
+        int it = 0;
         bool issued[kW4gBStages] = {};
         uint32_t par[kW4gBStages] = {};
-        for (int t = blockIdx.x; t < total && !*abort_flag; t += gridDim.x) {
-            W4Tile ti;
-            if (!w4_find_tile<WHICH>(p, tab, t, g, ti)) break;
+        while (walk.next() && !*abort_flag) {
+            const W4Tile& ti = walk.ti;
             const CUtensorMap* mB = ti.src ? &tmB1 : &tmB0;
             const bool gathered = WHICH == kW4GUp && !ti.src;
             const int boxes = (ti.n + 31) / 32;
@@ -346,24 +383,23 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
             const int h = warp == 1 ? 0 : 1;
             const uint64_t desc0 = sdesc_kmajor_sw128(smem_u32(sB));
             const uint32_t d = tmem + (uint32_t)(h * kW4gTok);
-            int g = 0;
-            uint32_t sb = 0, pb = 0, ia = 0, pacc = 1;  // B stage and its phase, A stages passed, accumulator phase
+            uint32_t sb = 0, pb = 0, ia = 0, pacc = 1;  // B stage and its phase, this half's A stages passed, accumulator phase
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok && !*abort_flag; t += gridDim.x) {
-                W4Tile ti;
-                if (!w4_find_tile<WHICH>(p, tab, t, g, ti)) break;
+            while (ok && walk.next() && !*abort_flag) {
+                const W4Tile& ti = walk.ti;
                 const uint32_t idesc = idesc_bf16_f32(kW4gRows / 2, ti.n);
                 const bool gathered = WHICH == kW4GUp && !ti.src, mine = h < ti.halves;
                 if (mine) {
                     ok = mbar_wait(&acce[h], pacc, limit);
                     pacc ^= 1u;
                 }
-                for (int kb = 0; kb < ti.nk && ok; ++kb, ia += (uint32_t)ti.halves) {
+                for (int kb = 0; kb < ti.nk && ok; ++kb) {
                     ok = mbar_wait(&fullB[sb], pb, limit);
                     if (mine) {
-                        const uint32_t i = ia + (uint32_t)h, sa = i % kW4gAStages;
+                        const uint32_t sa = (uint32_t)h + 2u * (ia & 1u);
                         if (WHICH == kW4GUp) ok = ok && mbar_wait(&fullG[sb], pb, limit);
-                        ok = ok && mbar_wait(&fullA[sa], i / kW4gAStages & 1u, limit);
+                        ok = ok && mbar_wait(&fullA[sa], (ia >> 1) & 1u, limit);
+                        ++ia;
                         if (!ok) break;
                         if (gathered) fence_proxy_async_smem();  // the gathered rows came through the generic proxy
                         tc_fence_after();
@@ -395,36 +431,34 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
         // ---------------- decoders
         const int dw = warp - 6 - kW4gGather, grp = dw >> 2, quad = warp & 3;
         const uint32_t a0 = tmem + kW4gACol + (uint32_t)(grp * (kW4gK / 2)) + ((uint32_t)(quad * 32) << 16);
-        // A stages of a tile: (column block, row half); this group takes every fourth
-        int g = 0, t = blockIdx.x, pos = grp, n_pos = 0, halves = 1;
-        const uint8_t* strip[2] = {nullptr, nullptr};  // this thread's strips of the row halves (NULL: past the matrix)
+        // Group j writes A stage j: every second column block of row half j % 2. (A stage belongs to one half, so
+        // that its issuer sees every phase of its barrier: tiles of one half only would let the other issuer
+        // fall two phases behind.)
+        const int half = grp & 1;
+        int kb = grp >> 1, nk = 0;
+        const uint8_t* strip = nullptr;  // this thread's strip of the tile (NULL: past the matrix)
         auto locate = [&]() -> bool {
-            W4Tile ti;
+            const W4Tile& ti = walk.ti;
             for (;;) {
-                if (!w4_find_tile<WHICH>(p, tab, t, g, ti)) return false;
-                if (pos < ti.nk * ti.halves) break;
-                pos -= ti.nk * ti.halves;
-                t += gridDim.x;
+                kb -= nk;
+                if (!walk.next()) return false;
+                nk = half < ti.halves ? ti.nk : 0;
+                if (kb < nk) break;
             }
-            halves = ti.halves;
-            n_pos = ti.nk * ti.halves;
-            const int i = ti.row0 / 16 + 2 * quad + (lane >> 4), strips = ((ti.src ? p.rows[1] : p.rows[0]) + 15) / 16;
-            strip[0] = i < strips ? ti.w + (size_t)i * ti.nk * kRec : nullptr;
-            strip[1] = i + 8 < strips ? ti.w + (size_t)(i + 8) * ti.nk * kRec : nullptr;
+            const int i = ti.row0 / 16 + 8 * half + 2 * quad + (lane >> 4), strips = (p.rows[ti.src] + 15) / 16;
+            strip = i < strips ? ti.w + (size_t)i * ti.nk * kRec : nullptr;
             return true;
         };
         W4Row<FMT, G> nxt = {};
         auto load = [&]() {
-            const int kb = halves == 2 ? pos >> 1 : pos;
-            const uint8_t* q = halves == 2 && (pos & 1) ? strip[1] : strip[0];
-            if (q) w4_load_row<FMT, G>(q + kb * kRec, lane & 15, nxt);
+            if (strip) w4_load_row<FMT, G>(strip + kb * kRec, lane & 15, nxt);
         };
         bool more = locate();
         if (more) load();
         for (int round = 0; more && !*abort_flag; ++round) {
             const W4Row<FMT, G> cur = nxt;
-            pos += kW4gDec / 4;
-            if (pos >= n_pos) more = locate();
+            kb += 2;
+            if (kb >= nk) more = locate();
             if (more) load();
             if (!__all_sync(0xffffffffu, mbar_wait(&emptyA[grp], ((uint32_t)round & 1u) ^ 1u, limit))) {
                 if (lane == 0) w4g_timeout(p.err, abort_flag);
@@ -442,11 +476,11 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
             const int tid = threadIdx.x - 6 * 32;
             const uint32_t c8 = (uint32_t)(lane & 7);
             const uint64_t pol = l2_evict_last();  // each token row is read by K experts
-            int g = 0, it = 0;
-            W4Tile ti;
+            int it = 0;
             int pv[8];  // the tile's pairs, read a tile ahead
-            auto pairs = [&](int t, W4Tile& q) -> bool {
-                if (!w4_find_tile<WHICH>(p, tab, t, g, q)) return false;
+            auto pairs = [&]() -> bool {
+                if (!walk.next()) return false;
+                const W4Tile& q = walk.ti;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int m = (tid >> 3) + 16 * i;
@@ -454,14 +488,13 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
                 }
                 return true;
             };
-            bool more = pairs(blockIdx.x, ti);
-            for (int t = blockIdx.x; more && !*abort_flag;) {
+            bool more = pairs();
+            while (more && !*abort_flag) {
                 const bf16* row[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) row[i] = a.x + c8 * 8 + (size_t)(pv[i] / a.K) * a.H;
-                const W4Tile cur = ti;
-                t += gridDim.x;
-                more = pairs(t, ti);
+                const W4Tile cur = walk.ti;
+                more = pairs();
                 bool ok = true;
                 for (int kb = 0; kb < cur.nk; ++kb, ++it) {
                     const int s = it % kW4gBStages;
@@ -506,13 +539,13 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
         const int ldo = WHICH == kW4GUp ? a.Imax : WHICH == kW4GDown ? a.H : p.rows[0];
         bf16* const out = WHICH == kW4GUp ? a.h : WHICH == kW4GDown ? a.Yb : p.out;
         const bool bulk = WHICH != kW4GLinear || ((ldo & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0);
-        int g = 0, t = blockIdx.x;
         uint32_t used[2] = {0u, 0u}, buf = 0;
-        W4Tile ti = {}, nx_ti = {};
+        W4Tile ti;
+        const W4Tile& nx_ti = walk.ti;
         int pv[kW4gTok / 32] = {};
         // the next tile, and down's pairs of its tokens: read a tile ahead
         auto find = [&]() -> bool {
-            if (!w4_find_tile<WHICH>(p, tab, t, g, nx_ti)) return false;
+            if (!walk.next()) return false;
             if (WHICH == kW4GDown && !nx_ti.src) {
 #pragma unroll
                 for (int i = 0; i < kW4gTok / 32; ++i) {
@@ -546,7 +579,6 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
                 }
                 __syncwarp();
             }
-            t += gridDim.x;
             more = find();
             const int rows = ti.src ? p.rows[1] : p.rows[0];
             for (int h = 0; h < ti.halves; ++h) {
