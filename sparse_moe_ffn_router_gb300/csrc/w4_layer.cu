@@ -24,8 +24,17 @@ cudaError_t launch_w4_gemm(int format, int group, int which, const W4GemmArgs& p
     }
 }
 
-// Tokens from which the linear layer runs on the tensor cores.
-constexpr int kW4GemmTokens = 64;
+// The linear layer's path. The streaming kernel passes over the weights once for 8 tokens: about 0.04 us for
+// each record of a CTA. The tensor-core kernel takes about 0.55 us for 256 rows of one column block by at most
+// 128 tokens, a wave of CTAs at a time. In both the column blocks are a factor, so what decides are a CTA's
+// strips: measured (2048 x 2048) 10.8 against 12.9 us at 128 tokens and 14.8 against 12.5 at 192;
+// (4096 x 2048) 10.7 against 12.2 at 64 and 14.8 against 12.5 at 96; (24576 x 4096) 14.7 against 20.2 at 8 and
+// 25.2 against 20.2 at 16.
+static bool w4_linear_on_tensor_cores(long long T, long long N, int num_sms) {
+    const long long strips = (N + kW4Strip - 1) / kW4Strip * ((T + kW4Tok - 1) / kW4Tok);
+    const long long tiles = (N + kW4gRows - 1) / kW4gRows * ((T + kW4gTok - 1) / kW4gTok);
+    return strips > 14 * num_sms * ((tiles + num_sms - 1) / num_sms);
+}
 
 static cudaError_t w4_linear_gemm(const moe_w4_format& f, const W4LinearArgs& l, cudaStream_t s) {
     CUtensorMap mx;
@@ -80,7 +89,7 @@ static int w4_want(long long strips, int num_sms) {
 }
 
 cudaError_t launch_w4_linear(const moe_w4_format& f, const W4LinearArgs& l, cudaStream_t s) {
-    if (l.T >= kW4GemmTokens) return w4_linear_gemm(f, l, s);
+    if (w4_linear_on_tensor_cores(l.T, l.N, l.num_sms)) return w4_linear_gemm(f, l, s);
     W4StreamArgs p = {};
     p.w = l.w;
     p.x = l.x;

@@ -145,6 +145,40 @@ def test_linear_many_tokens(name, group, T, N, K):
     check(out, *ref.linear(x, w, b, rounded=T >= ref.GEMM_TOKENS))
 
 
+@pytest.mark.parametrize("name,group", [("int4", 64), ("int4_zp", 32), ("e2m1", 128)])
+@pytest.mark.parametrize("T,N,K", [(9, 20000, 128), (17, 16393, 256), (65, 8200, 384), (1500, 520, 640), (2100, 257, 1152), (4200, 129, 128),
+                                   (5000, 640, 896), (10000, 32, 128)])
+def test_linear_on_tensor_cores(name, group, T, N, K):
+    """Tiles of one row half and of two, several to a CTA, rows past the matrix, ragged token tiles; NaN around the
+    result stays."""
+    assert ref.linear_rounds(T, N, torch.cuda.get_device_properties(0).multi_processor_count)
+    x, w, b, out = run_linear(name, group, T, N, K, bias=N % 2 == 0)
+    check(out, *ref.linear(x, w, b, rounded=True))
+
+
+@pytest.mark.parametrize("T,N,K", [(3000, 640, 384), (5000, 384, 640), (9, 24000, 1152), (777, 5000, 128), (2500, 1000, 2048)])
+def test_linear_on_tensor_cores_is_exact_on_integers(T, N, K):
+    """Codes -8 .. 7 and tokens with 0, 1 and -1 in at most 32 columns, scales 1: every product, sum and result (at
+    most 256) is exact in bf16 and fp32, so the results are equal, whatever the order; and again on every repeat."""
+    f = ref.fmt("int4", 128)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    codes = torch.randint(0, 16, (1, N, K), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.ones(1, N, K // 128, dtype=torch.bfloat16, device="cuda")
+    packed = ref.pack("int4", 128, (codes, scales, None))
+    w = ref.values("int4", 128, (codes, scales, None))[0]
+    x = torch.zeros(T, K, device="cuda")
+    cols = torch.randint(0, K, (T, 32), device="cuda", generator=g)
+    x.scatter_(1, cols, torch.randint(0, 2, (T, 32), device="cuda", generator=g) * 2.0 - 1)
+    want = x.double() @ w.T
+    assert float(want.abs().max()) <= 256
+    ws = moe.new_w4_linear_workspace(f, T, N, K)
+    for _ in range(20):
+        out = torch.full((T, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+        moe.moe_w4_linear(f, x.to(torch.bfloat16), packed, None, out, ws)
+        assert torch.equal(out.double(), want)
+    assert moe.moe_last_device_error(ws) == 0
+
+
 @pytest.mark.parametrize("T", [1, 8, 40, 300])
 def test_linear_nonfinite_rows_stay_apart(T):
     """NaN and infinities in one token's row reach that row's results only."""
@@ -256,6 +290,22 @@ def test_layer_tiny(name, group, T):
 def test_layer_shapes(dims, name, group):
     L = W4Layer(dims, name, group, seed=sum(dims), bias=dims[2] % 2 == 1)
     check(L.run(), *L.reference())
+
+
+@pytest.mark.parametrize("dims", [(777, 640, 11, 3, 192, 320), (300, 384, 7, 7, 64, 64), (2000, 640, 64, 2, 64, 192), (1024, 1408, 40, 4, 704, 128)],
+                         ids=lambda v: "x".join(map(str, v)))
+def test_layer_repeats_bit_for_bit_with_skewed_experts(dims):
+    """Experts of a few tokens next to experts of nearly all, row tiles of one half and of two, several tiles to a
+    CTA: the same result every time, also where every intermediate held NaN before."""
+    L = W4Layer(dims, "int4_zp", 64, seed=sum(dims), bias=True)
+    ws = moe.new_workspace(L.dims)
+    first = L.run(ws=ws)
+    check(first, *L.reference())
+    for _ in range(25):
+        for tap in (0, 1):
+            at, n = moe.moe_workspace_tap(L.dims, tap)
+            ws.view(torch.uint8)[at:at + n] = 255
+        assert torch.equal(L.run(ws=ws), first)
 
 
 @pytest.mark.parametrize("T", [1, 8, 40, 256])

@@ -53,7 +53,13 @@ def sum_error(cols: int) -> float:
     return (cols / 16 + cols / 32 + 8) * 2.0 ** -22
 
 
-GEMM_TOKENS = 64  # tokens from which the linear layer takes the tensor-core path
+GEMM_TOKENS = 64  # the linear layer rounds its weights to bf16 at most from here on in matrices of a few thousand rows
+
+
+def linear_rounds(T, N, sms):
+    """Whether the linear layer takes the tensor-core path, which rounds each weight once to bf16."""
+    waves = -(-(-(-N // 256) * -(-T // 128)) // sms)
+    return -(-N // 16) * -(-T // 8) > 14 * sms * waves
 
 
 def linear(x, w, bias, rounded=False):
