@@ -7,6 +7,7 @@ library returns a status other than MOE_OK. Nothing here computes any part of th
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass, fields
@@ -416,24 +417,27 @@ def moe_w4_linear(fmt: W4Format, x, packed, bias, out, workspace, stream=None):
                                         _stream(stream)), "moe_w4_linear")
 
 
-# (format, group) -> bytes of a packed record (16 rows by 128 columns)
-_W4_RECORD = {(f, g): 1024 + 16 * (128 // g) * (3 if f == W4_INT4_ZP else 2)
-              for f in (W4_INT4, W4_INT4_ZP, W4_E2M1) for g in (32, 64, 128)}
+@functools.lru_cache(maxsize=256)
+def _w4_layer(dims: tuple, fmt: int, group: int):
+    """The dims as passed to C, and the bytes of the layer's packed gate_up, down, shared_gate_up and shared_down."""
+    d = Dims(*[int(v) for v in dims])
+    record = 1024 + 16 * (128 // group) * (3 if fmt == W4_INT4_ZP else 2) if group in (32, 64, 128) else 0
+    h = (d.H + 127) // 128
+    return d, (d.E * ((2 * d.I + 15) // 16) * h * record, d.E * ((d.H + 15) // 16) * ((d.I + 127) // 128) * record,
+               ((2 * d.Is + 15) // 16) * h * record, ((d.H + 15) // 16) * ((d.Is + 127) // 128) * record)
 
 
 def moe_forward_w4(dims, fmt: W4Format, x, weights: Weights, residual, out, workspace, stream=None):
     """moe_forward with weights.gate_up, down, shared_gate_up and shared_down in packed 4-bit form
     (uint8 tensors of moe_w4_size bytes; gate_up layouts W4_GATE_UP, down layouts W4_ROWS)."""
-    d = _dims(dims)
-    H, I, Is = d.H, d.I, d.Is
-    record = _W4_RECORD.get((fmt.format, fmt.group), 0)
-    h_recs, up, down, sup, sdown = (H + 127) // 128, weights.gate_up, weights.down, weights.shared_gate_up, weights.shared_down
-    for t, need in ((up, d.E * ((2 * I + 15) // 16) * h_recs), (down, d.E * ((H + 15) // 16) * ((I + 127) // 128)),
-                    (sup, ((2 * Is + 15) // 16) * h_recs), (sdown, ((H + 15) // 16) * ((Is + 127) // 128))):
+    if isinstance(dims, Dims):
+        dims = tuple(getattr(dims, f) for f, _ in Dims._fields_)
+    d, needs = _w4_layer(tuple(dims), fmt.format, fmt.group)
+    for t, need in zip((weights.gate_up, weights.down, weights.shared_gate_up, weights.shared_down), needs):
         if t.dtype != torch.uint8:
             raise TypeError("the experts' weights must be packed 4-bit weights (uint8)")
-        if t.numel() < need * record:
-            raise ValueError(f"packed weights of {t.numel()} bytes, the layer's dims need {need * record}")
+        if t.numel() < need:
+            raise ValueError(f"packed weights of {t.numel()} bytes, the layer's dims need {need}")
     w = weights.to_c()
     _check(load_library().moe_forward_w4(ctypes.byref(d), ctypes.byref(fmt), _ptr(x), ctypes.byref(w), _ptr(residual),
                                          _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
