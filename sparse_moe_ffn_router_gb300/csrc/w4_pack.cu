@@ -82,7 +82,7 @@ __device__ __forceinline__ void st_meta(uint8_t* rec, int row, const bf16 (&s)[W
     }
 }
 
-// w / s for bf16 w and s, r = 1 / s rounded to nearest, as far as rounding the quotient to a code needs
+// w / s for bf16 w and s, r = 1 / s to a few fp32 steps, as far as rounding the quotient to a code needs
 // it. A quotient of two 8-bit mantissas is either exactly halfway between two codes or at least 1/2040
 // away from that (codes are multiples of 1/2, |w / s| < 32), so an error of a few fp32 steps decides no
 // code; a quotient that is exactly halfway is representable, and one correction step of the product
@@ -90,6 +90,20 @@ __device__ __forceinline__ void st_meta(uint8_t* rec, int row, const bf16 (&s)[W
 __device__ __forceinline__ float w4_quotient(float w, float s, float r) {
     const float t = w * r;
     return fmaf(fmaf(-t, s, w), r, t);
+}
+
+// x / D for a bf16 x >= 0, correctly rounded: the product with 1 / D and one correction step. (For D = 6, 7
+// and 15 checked in exact arithmetic for every bf16; an infinity gives NaN.)
+template <int D>
+__device__ __forceinline__ float w4_div_const(float x) {
+    constexpr float r = 1.f / D;
+    const float t = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-t, (float)D, x), r, t);
+}
+__device__ __forceinline__ float w4_rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // One row of a record quantised by its four lanes. Per group: scale s = bf16(max|w| / 7) for
@@ -133,15 +147,15 @@ __device__ __forceinline__ void quantize_row(const W4PackArgs& a, const bf16* sr
         lo2 = bf2_min(lo2, lo2 >> 16);
         const float hi = bf_lo(hi2), lo = bf_lo(lo2);
         const bool bad = !(hi < INFINITY) || !(lo > -INFINITY);
-        const float raw = FMT == MOE_W4_INT4_ZP ? __fsub_rn(__fdiv_rn(hi, 15.f), __fdiv_rn(lo, 15.f))
-                                                : __fdiv_rn(hi, FMT == MOE_W4_INT4 ? 7.f : 6.f);
+        const float raw = FMT == MOE_W4_INT4_ZP ? __fadd_rn(w4_div_const<15>(hi), w4_div_const<15>(-lo))
+                                                : w4_div_const<FMT == MOE_W4_INT4 ? 7 : 6>(hi);
         const bf16 sb = __float2bfloat16_rn(raw);
         const float s = __bfloat162float(sb);
         const bool use = s > 0.f && !bad;
-        // (1 / s overflows below 2^-127, and a subnormal scale is too coarse for the quotients' bounds:
-        // such groups are divided, and clamped to the codes)
-        const bool tiny = s < 0x1p-120f;
-        const float r = use && !tiny ? __frcp_rn(s) : 0.f;
+        // (1 / s leaves the normal range below 2^-126 and above 2^126, and a subnormal scale is too coarse for
+        // the quotients' bounds: such groups are divided, and clamped to the codes)
+        const bool tiny = !(s >= 0x1p-120f && s <= 0x1p120f);
+        const float r = use && !tiny ? w4_rcp(s) : 0.f;
         float zf = 0.f;
         if (FMT == MOE_W4_INT4_ZP && use) zf = fminf(rintf(tiny ? __fdiv_rn(-lo, s) : w4_quotient(-lo, s, r)), 15.f);
         sc[gi] = bad ? __ushort_as_bfloat16(0x7fffu) : sb;

@@ -80,6 +80,20 @@ def test_quantize(name, group, rows, cols, layout):
 
 
 @pytest.mark.parametrize("name", list(ref.FORMATS))
+def test_quantize_every_magnitude(name):
+    """Every positive normal bf16 as a group's largest value, from the smallest whose scale is normal to 2^126, with
+    other values of the group at and between the codes: scales and codes as the definition's divisions give them."""
+    bits = torch.arange(0x0200, 0x7e80, dtype=torch.int32)  # 2^-123 .. 2^126
+    b = (bits << 16).view(torch.float32)
+    n = b.numel() // 16 * 16
+    part = torch.tensor([1.0, -1.0, 0.5, 0.25, -0.75, 0.125, 0.375, -0.0625] * 4)
+    w = (b[:n, None] * part).to(torch.bfloat16).view(1, n // 4, 128).cuda()
+    packed = moe.new_w4(ref.fmt(name, 32), n // 4, 128)
+    moe.moe_w4_quantize(ref.fmt(name, 32), w[0], packed)
+    assert torch.equal(packed, ref.pack(name, 32, ref.quantize(name, 32, w)))
+
+
+@pytest.mark.parametrize("name", list(ref.FORMATS))
 def test_quantize_extreme_values(name):
     """The largest and smallest finite weights, and a group with an infinity or a NaN."""
     w = torch.zeros(1, 16, 128, dtype=torch.bfloat16, device="cuda")
