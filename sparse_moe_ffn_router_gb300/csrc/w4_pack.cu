@@ -74,11 +74,22 @@ template <int FMT, int G>
 __device__ __forceinline__ void st_meta(uint8_t* rec, int row, const bf16 (&s)[W4Rec<FMT, G>::kGroups],
                                         const uint32_t (&z)[W4Rec<FMT, G>::kGroups]) {
     constexpr int N = W4Rec<FMT, G>::kGroups;
-    bf16* sp = reinterpret_cast<bf16*>(rec + W4Rec<FMT, G>::kScales) + row * N;
+    uint8_t* sp = rec + W4Rec<FMT, G>::kScales + row * (2 * N);
+    uint32_t b[N], zw = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        sp[i] = s[i];
-        if (FMT == MOE_W4_INT4_ZP) rec[W4Rec<FMT, G>::kZeros + row * N + i] = (uint8_t)z[i];
+        b[i] = __bfloat16_as_ushort(s[i]);
+        zw |= z[i] << (8 * i);
+    }
+    if constexpr (N == 4) {
+        *reinterpret_cast<uint2*>(sp) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+        if (FMT == MOE_W4_INT4_ZP) *reinterpret_cast<uint32_t*>(rec + W4Rec<FMT, G>::kZeros + row * N) = zw;
+    } else if constexpr (N == 2) {
+        *reinterpret_cast<uint32_t*>(sp) = b[0] | b[1] << 16;
+        if (FMT == MOE_W4_INT4_ZP) *reinterpret_cast<uint16_t*>(rec + W4Rec<FMT, G>::kZeros + row * N) = (uint16_t)zw;
+    } else {
+        *reinterpret_cast<uint16_t*>(sp) = (uint16_t)b[0];
+        if (FMT == MOE_W4_INT4_ZP) rec[W4Rec<FMT, G>::kZeros + row * N] = (uint8_t)zw;
     }
 }
 
@@ -106,21 +117,51 @@ __device__ __forceinline__ float w4_rcp(float x) {
     return r;
 }
 
+// Walks the records of a warp: i, its 128 columns k, strip and matrix m (two divisions for all of them).
+struct W4RecordWalk {
+    int64_t i, m;
+    int stride, k, strip, dk, ds, dm, R, S;
+    __device__ __forceinline__ W4RecordWalk(const W4PackArgs& a) {
+        R = (a.cols + kW4Cols - 1) / kW4Cols;
+        S = (a.rows + kW4Strip - 1) / kW4Strip;
+        const int first = (int)blockIdx.x * 8 + (int)(threadIdx.x >> 5);
+        int m0;
+        stride = (int)gridDim.x * 8;
+        split(first, k, strip, m0);
+        split(stride, dk, ds, dm);
+        i = first;
+        m = m0;
+    }
+    __device__ __forceinline__ void split(int n, int& k_, int& s_, int& m_) const {
+        const int sg = (int)((unsigned)n / (unsigned)R);
+        k_ = n - sg * R;
+        m_ = (int)((unsigned)sg / (unsigned)S);
+        s_ = sg - m_ * S;
+    }
+    __device__ __forceinline__ void next() {
+        i += stride;
+        m += dm;
+        k += dk;
+        strip += ds;
+        if (k >= R) {
+            k -= R;
+            ++strip;
+        }
+        if (strip >= S) {
+            strip -= S;
+            ++m;
+        }
+    }
+};
+
 // One row of a record quantised by its four lanes. Per group: scale s = bf16(max|w| / 7) for
 // INT4 (/ 6 for E2M1), or bf16(max / 15 - min / 15) over the values and 0 for INT4_ZP with zero
 // point rint(-min / s); codes are the nearest value of w / s (halfway to even). A group of zeros has
 // scale 0; one with a NaN or an infinity has scale NaN and codes of value 0, so every product with it
 // is NaN.
 template <int FMT, int G>
-__device__ __forceinline__ void quantize_row(const W4PackArgs& a, const bf16* src, int k0, int t, bool live, uint32_t (&words)[4],
-                                             bf16 (&sc)[W4Rec<FMT, G>::kGroups], uint32_t (&zp)[W4Rec<FMT, G>::kGroups]) {
+__device__ __forceinline__ void quantize_row(const uint4 (&v)[4], uint32_t (&words)[4], bf16 (&sc)[W4Rec<FMT, G>::kGroups], uint32_t (&zp)[W4Rec<FMT, G>::kGroups]) {
     constexpr int P = G / 32;  // 32-column pieces of a group
-    uint4 v[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int k = k0 + 32 * c + 8 * t;
-        v[c] = live && k < a.cols ? ld_stream(src + k) : make_uint4(0u, 0u, 0u, 0u);
-    }
 #pragma unroll
     for (int gi = 0; gi < 4 / P; ++gi) {
         // largest magnitude, or largest and smallest value with 0, of packed pairs
@@ -232,26 +273,30 @@ __device__ __forceinline__ void pack_row(const W4PackArgs& a, int64_t row, int k
 template <int FMT, int G, bool QUANT>
 __global__ void __launch_bounds__(256) k_w4_pack(W4PackArgs a, int64_t records) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int R = (a.cols + kW4Cols - 1) / kW4Cols, S = (a.rows + kW4Strip - 1) / kW4Strip;
-    const int64_t stride = (int64_t)gridDim.x * 8;
-    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < records; i += stride) {
-        const int64_t sg = i / R;
-        const int k0 = (int)(i - sg * R) * kW4Cols;
-        const int64_t m = sg / S;
-        const int strip = (int)(sg - m * S);
-        uint8_t* rec = a.packed + (size_t)i * W4Rec<FMT, G>::kBytes;
+    for (W4RecordWalk at(a); at.i < records; at.next()) {
+        const int k0 = at.k * kW4Cols;
+        uint8_t* rec = a.packed + (size_t)at.i * W4Rec<FMT, G>::kBytes;
+        uint4 v[2][4];  // both rows' weights: all loads of a record are on their way before its first shuffle
+        if (QUANT) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = w4_row(a, at.strip, g + 8 * h);
+                const bf16* src = a.w + (at.m * a.rows + row) * a.cols + k0 + 8 * t;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    v[h][c] = row < a.rows && k0 + 32 * c + 8 * t < a.cols ? ld_stream(src + 32 * c) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int row = w4_row(a, strip, g + 8 * h);
-            const bool live = row < a.rows;
-            const int64_t grow = m * a.rows + row;
+            const int row = w4_row(a, at.strip, g + 8 * h);
             uint32_t words[4];
             bf16 sc[W4Rec<FMT, G>::kGroups];
             uint32_t zp[W4Rec<FMT, G>::kGroups];
             if (QUANT)
-                quantize_row<FMT, G>(a, a.w + grow * a.cols, k0, t, live, words, sc, zp);
+                quantize_row<FMT, G>(v[h], words, sc, zp);
             else
-                pack_row<FMT, G>(a, grow, k0, t, live, words, sc, zp);
+                pack_row<FMT, G>(a, at.m * a.rows + row, k0, t, row < a.rows, words, sc, zp);
             st_record(rec + 512 * h + lane * 16, make_uint4(words[0], words[1], words[2], words[3]));
             if (t == 0) st_meta<FMT, G>(rec, g + 8 * h, sc, zp);
         }
@@ -262,14 +307,10 @@ template <int FMT, int G>
 __global__ void __launch_bounds__(256) k_w4_unpack(W4PackArgs a, int64_t records) {
     constexpr int N = W4Rec<FMT, G>::kGroups;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int R = (a.cols + kW4Cols - 1) / kW4Cols, S = (a.rows + kW4Strip - 1) / kW4Strip;
-    const int64_t stride = (int64_t)gridDim.x * 8;
-    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < records; i += stride) {
-        const int64_t sg = i / R;
-        const int k0 = (int)(i - sg * R) * kW4Cols;
-        const int64_t m = sg / S;
-        const int strip = (int)(sg - m * S);
-        const uint8_t* rec = a.packed + (size_t)i * W4Rec<FMT, G>::kBytes;
+    for (W4RecordWalk at(a); at.i < records; at.next()) {
+        const int k0 = at.k * kW4Cols, strip = at.strip;
+        const int64_t m = at.m;
+        const uint8_t* rec = a.packed + (size_t)at.i * W4Rec<FMT, G>::kBytes;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = g + 8 * h, row = w4_row(a, strip, r);
