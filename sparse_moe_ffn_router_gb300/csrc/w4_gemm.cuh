@@ -17,15 +17,21 @@
 // 128 rows that share a stage's token rows (with 128-row tiles the token rows came from L2 twice as
 // often, ~8 TB/s, and bound the kernel). The tokens of a group are split evenly over its token tiles and N
 // is rounded up to 16, so a group of few tokens costs little tensor time. One persistent CTA per SM walks
-// the tiles (group, row tile, token tile; the token tiles that share weights run back to back). TMEM: an
-// accumulator of 128 columns for each row half, handed to the epilogue one after the other (the next
-// tile's first half starts while the second is written out), and four A stages of 128 columns of K (64
-// TMEM columns each). Roles:
-//   warp 0      TMA producer (one lane)           warps 2-5    epilogue (TMEM lane quadrants) of row half 0;
-//   warp 1      TMEM owner and MMA issuer                       gate_up: of both halves
+// a run of tiles (group, row tile, token tile; the token tiles that share weights run back to back). TMEM:
+// an accumulator of 128 columns for each row half and four A stages of 128 columns of K (64 TMEM columns
+// each), two to a half. Each half has an issuer of its own: with one thread for both, its waits and commits
+// were as long as the MMAs. Roles:
+//   warp 0      TMA producer                      warps 2-5    epilogue (TMEM lane quadrants) of row half 0;
+//   warps 1, 26 MMA issuers of the row halves                   gate_up: of both halves
 //   warps 6-9   gate_up: gatherers of token rows; else epilogue of row half 1
-//   warps 10-25 decoders: four groups of four warps, group j takes every fourth A stage, warp w lanes
+//   warps 10-25 decoders: four groups of four warps, group j writes A stage j, warp w lanes
 //               32 (w % 4) .. + 31
+//
+// Measured: linear 4096 x 2048 by 4096 tokens 52 us (1.31 PFLOP/s, 0.70 of the measured cuBLAS rate; the
+// tensor pipe is active 63 % of the time), the MoE layer of 4096 tokens and 256 experts 182 us in gate_up
+// and 138 us in down of 390. What is left is the decoders' and the epilogue's share of the issue slots (68 %)
+// and the four A stages' hand-over: a stage in two halves (finer hand-over) took 434 us for that layer, a
+// second accumulator for tiles of up to 64 tokens 414.
 #pragma once
 
 #include "launch.h"

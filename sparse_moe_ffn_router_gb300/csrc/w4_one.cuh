@@ -12,6 +12,9 @@
 //   down     output strips c, c + G, ... of the shared and every routed expert: the h rows are gathered
 //            into shared memory (a warp a row), 16 / W experts' strips fill a stage, W warps to each;
 //            then residual, gated shared expert and slots 0 .. K-1 are added in that order.
+// Measured at the pages' shape (INT4 per 32): 15.3 to 16.2 us a layer back to back, against 28 us for the
+// chain of routing, gate_up, down and combine. What bounds it is the chain of dependent steps: scores, their
+// exchange, routing, the first routed weights, the h exchange, output; the weights alone are 2.5 us.
 // The products are warp MMAs with one live column of eight: the weights are decoded to the A operand
 // anyway, and an MMA step replaces 64 multiply-adds a lane would do on unpacked values.
 // Exchanges carry a tag of the call instead of a flag or fence: 64-bit words (32-bit tag, fp32 score)

@@ -13,6 +13,11 @@
 // instructions for a word of eight codes), so what a stage costs besides it is kept small: one
 // 16-byte word tells a consumer warp all that a stage needs as long as the token set stays.
 //
+// Measured: linear, one token, 24576 x 4096 E2M1 with scales per 32 columns (57 MB) 22 us from HBM, 18 from
+// L2; the layer of 64 tokens (221 experts touched, INT4_ZP per 128) gate_up 60 us (235 MB, 3.9 TB/s) and
+// down 43 us. Issue slots (55 to 63 % active) and the stages' hand-over bound them together: without any
+// decoding gate_up takes 50 us, and a record is 165 (INT4 per 128) to 220 (E2M1 per 32) instructions.
+//
 // Item: a block of consecutive strips of one matrix by one tile of 8 tokens. A strip of R <= 32
 // records is shared by W warps of one or two records each, so 16 / W strips fill a stage (fewer
 // when that would leave SMs without items); a strip of more than 32 records takes ceil(R / 32)
