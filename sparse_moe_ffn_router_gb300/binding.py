@@ -343,12 +343,6 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
-def _bf16(t, what: str):
-    if t is not None and t.dtype != torch.bfloat16:
-        raise TypeError(f"{what} must be bfloat16, got {t.dtype}")
-    return _ptr(t)
-
-
 def moe_w4_size(fmt: W4Format, rows: int, cols: int, n: int = 1) -> int:
     """Bytes of n packed 4-bit matrices [rows, cols] (0 when the format or shape is not supported)."""
     return int(load_library().moe_w4_size(ctypes.byref(fmt), int(n), int(rows), int(cols)))
@@ -368,11 +362,37 @@ def _matrices(t) -> tuple[int, int, int]:
     return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
 
 
+def _device(t, dtype=None, what: str = "") -> int:
+    """The current CUDA device, where the kernels will run; t: the first tensor of the call."""
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        _ptr(t)
+    return torch.cuda.current_device()
+
+
+def _here(t, device: int, dtype=None, what: str = "") -> int | None:
+    """_ptr of a tensor that must be on the given device (and of the given type)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or not t.is_contiguous():
+        _ptr(t)
+        raise ValueError(f"tensors must be on the current CUDA device ({device})")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _stream_of(stream, device: int) -> int:
+    return _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
+
+
 def moe_w4_quantize(fmt: W4Format, w, packed, layout: int = W4_ROWS, stream=None):
     """packed = the 4-bit form of the bf16 weights w [rows, cols] or [n, rows, cols]."""
     n, rows, cols = _matrices(w)
-    _check(load_library().moe_w4_quantize(ctypes.byref(fmt), n, rows, cols, int(layout), _bf16(w, "w"), _ptr(packed),
-                                          _nbytes(packed), _stream(stream)), "moe_w4_quantize")
+    dev = _device(w, torch.bfloat16, "w")
+    _check(load_library().moe_w4_quantize(ctypes.byref(fmt), n, rows, cols, int(layout), _here(w, dev),
+                                          _here(packed, dev), _nbytes(packed), _stream_of(stream, dev)), "moe_w4_quantize")
 
 
 def moe_w4_pack(fmt: W4Format, codes, scales, zeros, packed, layout: int = W4_ROWS, stream=None):
@@ -384,16 +404,18 @@ def moe_w4_pack(fmt: W4Format, codes, scales, zeros, packed, layout: int = W4_RO
         raise TypeError("codes and zeros must be uint8")
     if tuple(scales.shape) != groups or (zeros is not None and tuple(zeros.shape) != groups):
         raise ValueError(f"scales and zeros must be {list(groups)}")
-    _check(load_library().moe_w4_pack(ctypes.byref(fmt), n, rows, 2 * half, int(layout), _ptr(codes),
-                                      _bf16(scales, "scales"), _ptr(zeros), _ptr(packed), _nbytes(packed),
-                                      _stream(stream)), "moe_w4_pack")
+    dev = _device(codes)
+    _check(load_library().moe_w4_pack(ctypes.byref(fmt), n, rows, 2 * half, int(layout), _here(codes, dev),
+                                      _here(scales, dev, torch.bfloat16, "scales"), _here(zeros, dev), _here(packed, dev),
+                                      _nbytes(packed), _stream_of(stream, dev)), "moe_w4_pack")
 
 
 def moe_w4_dequantize(fmt: W4Format, packed, w, layout: int = W4_ROWS, stream=None):
     """w [rows, cols] or [n, rows, cols] = the bf16 weights the packed form stands for."""
     n, rows, cols = _matrices(w)
-    _check(load_library().moe_w4_dequantize(ctypes.byref(fmt), n, rows, cols, int(layout), _ptr(packed),
-                                            _nbytes(packed), _bf16(w, "w"), _stream(stream)), "moe_w4_dequantize")
+    dev = _device(w, torch.bfloat16, "w")
+    _check(load_library().moe_w4_dequantize(ctypes.byref(fmt), n, rows, cols, int(layout), _here(packed, dev), _nbytes(packed),
+                                            _here(w, dev), _stream_of(stream, dev)), "moe_w4_dequantize")
 
 
 def new_w4_linear_workspace(fmt: W4Format, T: int, N: int, K: int, device="cuda") -> torch.Tensor:
@@ -412,15 +434,17 @@ def moe_w4_linear(fmt: W4Format, x, packed, bias, out, workspace, stream=None):
     N = out.shape[1]
     if bias is not None and tuple(bias.shape) != (N,):
         raise ValueError(f"bias must be [{N}]")
-    _check(load_library().moe_w4_linear(ctypes.byref(fmt), T, N, K, _bf16(x, "x"), _ptr(packed), _nbytes(packed),
-                                        _bf16(bias, "bias"), _bf16(out, "out"), _ptr(workspace), _nbytes(workspace),
-                                        _stream(stream)), "moe_w4_linear")
+    bf16 = torch.bfloat16
+    dev = _device(x, bf16, "x")
+    _check(load_library().moe_w4_linear(ctypes.byref(fmt), T, N, K, _here(x, dev), _here(packed, dev), _nbytes(packed),
+                                        _here(bias, dev, bf16, "bias"), _here(out, dev, bf16, "out"), _here(workspace, dev),
+                                        _nbytes(workspace), _stream_of(stream, dev)), "moe_w4_linear")
 
 
 @functools.lru_cache(maxsize=256)
 def _w4_layer(dims: tuple, fmt: int, group: int):
-    """The dims as passed to C, and the bytes of the layer's packed gate_up, down, shared_gate_up and shared_down."""
-    d = Dims(*[int(v) for v in dims])
+    """The dims (whole numbers) as passed to C, and the bytes of the layer's packed gate_up, down, shared_gate_up and shared_down."""
+    d = Dims(*dims)
     record = 1024 + 16 * (128 // group) * (3 if fmt == W4_INT4_ZP else 2) if group in (32, 64, 128) else 0
     h = (d.H + 127) // 128
     return d, (d.E * ((2 * d.I + 15) // 16) * h * record, d.E * ((d.H + 15) // 16) * ((d.I + 127) // 128) * record,
@@ -432,15 +456,18 @@ def moe_forward_w4(dims, fmt: W4Format, x, weights: Weights, residual, out, work
     (uint8 tensors of moe_w4_size bytes; gate_up layouts W4_GATE_UP, down layouts W4_ROWS)."""
     if isinstance(dims, Dims):
         dims = tuple(getattr(dims, f) for f, _ in Dims._fields_)
-    d, needs = _w4_layer(tuple(dims), fmt.format, fmt.group)
-    for t, need in zip((weights.gate_up, weights.down, weights.shared_gate_up, weights.shared_down), needs):
+    d, needs = _w4_layer(tuple(map(int, dims)), fmt.format, fmt.group)
+    packed = (weights.gate_up, weights.down, weights.shared_gate_up, weights.shared_down)
+    for t, need in zip(packed, needs):
         if t.dtype != torch.uint8:
             raise TypeError("the experts' weights must be packed 4-bit weights (uint8)")
         if t.numel() < need:
             raise ValueError(f"packed weights of {t.numel()} bytes, the layer's dims need {need}")
-    w = weights.to_c()
-    _check(load_library().moe_forward_w4(ctypes.byref(d), ctypes.byref(fmt), _ptr(x), ctypes.byref(w), _ptr(residual),
-                                         _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
+    dev = _device(x)
+    w = CWeights(_here(weights.router_w, dev), _here(weights.router_b, dev), *[_here(t, dev) for t in packed],
+                 _here(weights.shared_gate, dev))
+    _check(load_library().moe_forward_w4(ctypes.byref(d), ctypes.byref(fmt), _here(x, dev), ctypes.byref(w), _here(residual, dev),
+                                         _here(out, dev), _here(workspace, dev), _nbytes(workspace), _stream_of(stream, dev)),
            "moe_forward_w4")
 
 

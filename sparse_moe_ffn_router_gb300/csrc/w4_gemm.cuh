@@ -712,7 +712,9 @@ cudaError_t launch_w4_gemm_t(const W4GemmArgs& args, const CUtensorMap& b0, cons
         // stage), so more and smaller token tiles are taken where they fill the waves of CTAs better.
         const int rt = w4_row_tiles(p.rows[0]), least = w4_tok_tiles(p.T);
         long long best = 0;
-        for (int n = least; n <= least + least / 2 + 1; ++n) {
+        // (with many waves there is little to fill)
+        const int most = (long long)least * rt <= 8LL * a.num_sms ? least + least / 2 + 1 : least;
+        for (int n = least; n <= most; ++n) {
             const int per = (p.T + n - 1) / n, tiles = (p.T + per - 1) / per;
             const long long cost = (((long long)tiles * rt + a.num_sms - 1) / a.num_sms) * (((per + 15) & ~15) + 32);
             if (best == 0 || cost < best) {

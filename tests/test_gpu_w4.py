@@ -204,6 +204,42 @@ def test_linear_nonfinite_rows_stay_apart(T):
     check(out[keep], *ref.linear(x[keep], w, b, rounded=T >= ref.GEMM_TOKENS))
 
 
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    f = ref.fmt("int4", 32)
+    w = torch.zeros(16, 128, dtype=torch.bfloat16, device="cuda")
+    packed, ws = moe.new_w4(f, 16, 128), moe.new_w4_linear_workspace(f, 1, 16, 128)
+    x, out = torch.zeros(1, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 16, dtype=torch.bfloat16, device="cuda")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: moe.moe_w4_quantize(f, w, packed), lambda: moe.moe_w4_dequantize(f, packed, w),
+                 lambda: moe.moe_w4_linear(f, x, packed, None, out, ws)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+
+
+def test_linear_on_two_streams_at_once():
+    """Two layers in flight together, each with its own workspace and output, on the streaming and the tensor-core path."""
+    f = ref.fmt("int4", 64)
+    cases = []
+    for T, N, K in ((5, 4096, 2048), (40, 24000, 512), (1000, 2048, 1024), (3000, 640, 512)):
+        packed = ref.pack("int4", 64, ref.matrices("int4", 64, 1, N, K, seed=N))
+        x = torch.randn(T, K, device="cuda").to(torch.bfloat16)
+        ws = [moe.new_w4_linear_workspace(f, T, N, K) for _ in range(2)]
+        out = [torch.empty(T, N, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        alone = torch.empty_like(out[0])
+        moe.moe_w4_linear(f, x, packed, None, alone, ws[0])
+        cases.append((packed, x, ws, out, alone))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            for packed, x, ws, out, _ in (cases if i == 0 else cases[::-1]):
+                moe.moe_w4_linear(f, x, packed, None, out[i], ws[i], s)
+    torch.cuda.synchronize()
+    for packed, x, ws, out, alone in cases:
+        assert torch.equal(out[0], alone) and torch.equal(out[1], alone)
+        assert all(moe.moe_last_device_error(w) == 0 for w in ws)
+
+
 def test_linear_repeats_bit_for_bit_and_in_graphs():
     f = ref.fmt("int4", 64)
     for T in (1, 7, 33, 260):
