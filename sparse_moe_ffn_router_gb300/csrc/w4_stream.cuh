@@ -275,7 +275,9 @@ __global__ void __launch_bounds__(kW4Threads, 1) k_w4_stream(const __grid_consta
             const int n_act = a.hdr->n_act, blocks = p.b1.blocks;
             int e8[8], o8[8], c8[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) e8[j] = 32 * j + lane < n_act ? a.act[32 * j + lane] : 0;
+            for (int j = 0; j < 8; ++j) e8[j] = 32 * j + lane < a.E ? a.act[32 * j + lane] : 0;  // (not waiting for n_act)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e8[j] = 32 * j + lane < n_act ? e8[j] : 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 o8[j] = a.offsets[e8[j]];
