@@ -371,16 +371,16 @@ def _device(t, dtype=None, what: str = "") -> int:
     return torch.cuda.current_device()
 
 
-def _here(t, device: int, dtype=None, what: str = "") -> int | None:
-    """_ptr of a tensor that must be on the given device (and of the given type)."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.get_device() != device or not t.is_contiguous():
-        _ptr(t)
+def _here(device: int, *tensors) -> list:
+    """_ptr of each tensor; all must be on the given device."""
+    try:
+        ptrs = [None if t is None else t.data_ptr() if t.get_device() == device and t.is_contiguous() else -1 for t in tensors]
+    except AttributeError:
+        raise TypeError("expected a torch.Tensor") from None
+    if -1 in ptrs:
+        _ptr(tensors[ptrs.index(-1)])
         raise ValueError(f"tensors must be on the current CUDA device ({device})")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    return t.data_ptr()
+    return ptrs
 
 
 def _stream_of(stream, device: int) -> int:
@@ -391,8 +391,9 @@ def moe_w4_quantize(fmt: W4Format, w, packed, layout: int = W4_ROWS, stream=None
     """packed = the 4-bit form of the bf16 weights w [rows, cols] or [n, rows, cols]."""
     n, rows, cols = _matrices(w)
     dev = _device(w, torch.bfloat16, "w")
-    _check(load_library().moe_w4_quantize(ctypes.byref(fmt), n, rows, cols, int(layout), _here(w, dev),
-                                          _here(packed, dev), _nbytes(packed), _stream_of(stream, dev)), "moe_w4_quantize")
+    src, dst = _here(dev, w, packed)
+    _check(load_library().moe_w4_quantize(ctypes.byref(fmt), n, rows, cols, int(layout), src, dst, _nbytes(packed),
+                                          _stream_of(stream, dev)), "moe_w4_quantize")
 
 
 def moe_w4_pack(fmt: W4Format, codes, scales, zeros, packed, layout: int = W4_ROWS, stream=None):
@@ -404,18 +405,19 @@ def moe_w4_pack(fmt: W4Format, codes, scales, zeros, packed, layout: int = W4_RO
         raise TypeError("codes and zeros must be uint8")
     if tuple(scales.shape) != groups or (zeros is not None and tuple(zeros.shape) != groups):
         raise ValueError(f"scales and zeros must be {list(groups)}")
-    dev = _device(codes)
-    _check(load_library().moe_w4_pack(ctypes.byref(fmt), n, rows, 2 * half, int(layout), _here(codes, dev),
-                                      _here(scales, dev, torch.bfloat16, "scales"), _here(zeros, dev), _here(packed, dev),
-                                      _nbytes(packed), _stream_of(stream, dev)), "moe_w4_pack")
+    dev = _device(scales, torch.bfloat16, "scales")
+    c, s, z, dst = _here(dev, codes, scales, zeros, packed)
+    _check(load_library().moe_w4_pack(ctypes.byref(fmt), n, rows, 2 * half, int(layout), c, s, z, dst, _nbytes(packed),
+                                      _stream_of(stream, dev)), "moe_w4_pack")
 
 
 def moe_w4_dequantize(fmt: W4Format, packed, w, layout: int = W4_ROWS, stream=None):
     """w [rows, cols] or [n, rows, cols] = the bf16 weights the packed form stands for."""
     n, rows, cols = _matrices(w)
     dev = _device(w, torch.bfloat16, "w")
-    _check(load_library().moe_w4_dequantize(ctypes.byref(fmt), n, rows, cols, int(layout), _here(packed, dev), _nbytes(packed),
-                                            _here(w, dev), _stream_of(stream, dev)), "moe_w4_dequantize")
+    src, dst = _here(dev, packed, w)
+    _check(load_library().moe_w4_dequantize(ctypes.byref(fmt), n, rows, cols, int(layout), src, _nbytes(packed), dst,
+                                            _stream_of(stream, dev)), "moe_w4_dequantize")
 
 
 def new_w4_linear_workspace(fmt: W4Format, T: int, N: int, K: int, device="cuda") -> torch.Tensor:
@@ -428,17 +430,19 @@ def new_w4_linear_workspace(fmt: W4Format, T: int, N: int, K: int, device="cuda"
 
 def moe_w4_linear(fmt: W4Format, x, packed, bias, out, workspace, stream=None):
     """out [T, N] = x [T, K] . W^T + bias, with W [N, K] packed (layout W4_ROWS)."""
-    if x.dim() != 2 or out.dim() != 2 or x.shape[0] != out.shape[0]:
+    xs, os = x.shape, out.shape
+    if len(xs) != 2 or len(os) != 2 or xs[0] != os[0]:
         raise ValueError("x is [T, K] and out [T, N]")
-    T, K = x.shape
-    N = out.shape[1]
-    if bias is not None and tuple(bias.shape) != (N,):
-        raise ValueError(f"bias must be [{N}]")
-    bf16 = torch.bfloat16
-    dev = _device(x, bf16, "x")
-    _check(load_library().moe_w4_linear(ctypes.byref(fmt), T, N, K, _here(x, dev), _here(packed, dev), _nbytes(packed),
-                                        _here(bias, dev, bf16, "bias"), _here(out, dev, bf16, "out"), _here(workspace, dev),
-                                        _nbytes(workspace), _stream_of(stream, dev)), "moe_w4_linear")
+    T, K = xs
+    N = os[1]
+    if bias is not None and (bias.dtype != torch.bfloat16 or tuple(bias.shape) != (N,)):
+        raise (TypeError if bias.dtype != torch.bfloat16 else ValueError)(f"bias must be bfloat16 [{N}]")
+    if out.dtype != torch.bfloat16:
+        raise TypeError(f"out must be {torch.bfloat16}, got {out.dtype}")
+    dev = _device(x, torch.bfloat16, "x")
+    px, pw, pb, po, ws = _here(dev, x, packed, bias, out, workspace)
+    _check(load_library().moe_w4_linear(ctypes.byref(fmt), T, N, K, px, pw, _nbytes(packed), pb, po, ws, _nbytes(workspace),
+                                        _stream_of(stream, dev)), "moe_w4_linear")
 
 
 @functools.lru_cache(maxsize=256)
@@ -464,11 +468,11 @@ def moe_forward_w4(dims, fmt: W4Format, x, weights: Weights, residual, out, work
         if t.numel() < need:
             raise ValueError(f"packed weights of {t.numel()} bytes, the layer's dims need {need}")
     dev = _device(x)
-    w = CWeights(_here(weights.router_w, dev), _here(weights.router_b, dev), *[_here(t, dev) for t in packed],
-                 _here(weights.shared_gate, dev))
-    _check(load_library().moe_forward_w4(ctypes.byref(d), ctypes.byref(fmt), _here(x, dev), ctypes.byref(w), _here(residual, dev),
-                                         _here(out, dev), _here(workspace, dev), _nbytes(workspace), _stream_of(stream, dev)),
-           "moe_forward_w4")
+    px, res, po, ws, router_w, router_b, gu, dn, sgu, sdn, gate = _here(
+        dev, x, residual, out, workspace, weights.router_w, weights.router_b, *packed, weights.shared_gate)
+    w = CWeights(router_w, router_b, gu, dn, sgu, sdn, gate)
+    _check(load_library().moe_forward_w4(ctypes.byref(d), ctypes.byref(fmt), px, ctypes.byref(w), res, po, ws, _nbytes(workspace),
+                                         _stream_of(stream, dev)), "moe_forward_w4")
 
 
 def moe_rmsnorm(dims, x, gamma, eps: float, xn, stream=None):
