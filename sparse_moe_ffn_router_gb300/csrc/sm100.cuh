@@ -203,6 +203,16 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const void* map, uin
         : "memory");
 }
 
+// Four rows r0 .. r3 of a map whose box is one row high, 64 bf16 columns from c0, one after another in shared
+// memory (the 128-byte swizzle goes by address, as in a tile).
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* map, uint64_t* bar, int c0, int r0, int r1, int r2, int r3) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, "
+        "%7}], [%2];" ::"r"(dst),
+        "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+        : "memory");
+}
+
 // ---------------------------------------------------------------------------------------
 // tcgen05
 

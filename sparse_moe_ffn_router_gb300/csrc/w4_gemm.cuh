@@ -8,8 +8,8 @@
 // So a weight passes through no shared memory at all: with the weights staged there as the B operand
 // (the other way round) the stores, the token tiles and the MMAs' reads together came to more than the
 // 128 bytes a cycle of shared memory, and the tensor cores ran at half rate. B, the token rows (h rows
-// for down), K-major bf16 tiles in shared memory, comes by TMA, or is gathered from x for a routed
-// expert's gate_up. A weight is rounded once, to bf16(s * v): the tensor core takes bf16 operands and
+// for down), K-major bf16 tiles in shared memory, comes by TMA, gathered from x four rows a copy for a
+// routed expert's gate_up. A weight is rounded once, to bf16(s * v): the tensor core takes bf16 operands and
 // its accumulator spans all of K, so a scale per 32 to 128 columns cannot be applied behind it; the
 // error is at most half a bf16 step a weight (2^-8), of the size of the roundings of h and Y.
 //
@@ -21,9 +21,8 @@
 // an accumulator of 128 columns for each row half and four A stages of 128 columns of K (64 TMEM columns
 // each), two to a half. Each half has an issuer of its own: with one thread for both, its waits and commits
 // were as long as the MMAs. Roles:
-//   warp 0      TMA producer                      warps 2-5    epilogue (TMEM lane quadrants) of row half 0;
-//   warps 1, 26 MMA issuers of the row halves                   gate_up: of both halves
-//   warps 6-9   gate_up: gatherers of token rows; else epilogue of row half 1
+//   warps 0, 27 TMA producers                     warps 2-5, 6-9  epilogue (TMEM lane quadrants) of row half 0, 1
+//   warps 1, 26 MMA issuers of the row halves
 //   warps 10-25 decoders: four groups of four warps, group j writes A stage j, warp w lanes
 //               32 (w % 4) .. + 31
 //
@@ -64,9 +63,10 @@ cudaError_t launch_w4_gemm(int format, int group, int which, const W4GemmArgs& p
 
 constexpr int kW4gK = 128;                       // columns of a stage
 constexpr int kW4gAStages = 4, kW4gBStages = 6;  // (A: two for each row half)
-constexpr int kW4gGather = 4, kW4gDec = 16;      // warps (the gatherers of gate_up are epilogue warps elsewhere)
-constexpr int kW4gIssuer1 = 6 + kW4gGather + kW4gDec;
-constexpr int kW4gThreads = 32 * (kW4gIssuer1 + 1);
+constexpr int kW4gEpi = 8, kW4gDec = 16;         // epilogue and decoder warps
+constexpr int kW4gIssuer1 = 2 + kW4gEpi + kW4gDec;
+constexpr int kW4gProducer1 = kW4gIssuer1 + 1;
+constexpr int kW4gThreads = 32 * (kW4gProducer1 + 1);
 constexpr uint32_t kW4gB = kW4gTok * kW4gK * 2;  // bytes of a B stage: two 64-column tiles
 constexpr uint32_t kW4gChunk = 16 * 272;         // epilogue: 16 tokens of 128 bf16 rows
 constexpr uint32_t kW4gACol = 2 * kW4gTok;       // first TMEM column of the A stages
@@ -272,17 +272,16 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     uint8_t* sB = smem;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W4GSmem::kBars);
-    uint64_t* fullB = bars;                       // TMA (or the arrival in its place)
+    uint64_t* fullB = bars;
     uint64_t* emptyB = fullB + kW4gBStages;
-    uint64_t* fullG = emptyB + kW4gBStages;       // gathered token rows
-    uint64_t* fullA = fullG + kW4gBStages;
+    uint64_t* fullA = emptyB + kW4gBStages;
     uint64_t* emptyA = fullA + kW4gAStages;
     uint64_t* accf = emptyA + kW4gAStages;
     uint64_t* acce = accf + 2;  // (an accumulator for each row half)
     uint64_t* mma_done = acce + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((3 * kW4gBStages + 2 * kW4gAStages + 5) * 8 + 8 <= 256, "barriers");
+    static_assert((2 * kW4gBStages + 2 * kW4gAStages + 5) * 8 + 8 <= 256, "barriers");
     uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + W4GSmem::kTab);  // of the groups' costs
     W4Group* groups = reinterpret_cast<W4Group*>(prefix + kW4gGroups + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -290,9 +289,8 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kW4gBStages; ++s) {
-            mbar_init(&fullB[s], 1);
+            mbar_init(&fullB[s], 2);
             mbar_init(&emptyB[s], 2);
-            mbar_init(&fullG[s], 32 * kW4gGather);
         }
         for (int s = 0; s < kW4gAStages; ++s) {
             mbar_init(&fullA[s], 4);
@@ -347,42 +345,69 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
     }
     W4Walk<WHICH> walk(p, groups, prefix, n_groups);
 
-    if (warp == 0) {
-        if (elect_one()) {
-        // ---------------- TMA producer: B, except a routed expert's token rows
-        int it = 0;
-        bool issued[kW4gBStages] = {};
-        uint32_t par[kW4gBStages] = {};
-        while (walk.next() && !*abort_flag) {
-            const W4Tile& ti = walk.ti;
-            const CUtensorMap* mB = ti.src ? &tmB1 : &tmB0;
-            const bool gathered = WHICH == kW4GUp && !ti.src;
-            const int boxes = (ti.n + 31) / 32;
-            for (int kb = 0; kb < ti.nk; ++kb, ++it) {
-                const int s = it % kW4gBStages;
-                const uint32_t ph = (uint32_t)(it / kW4gBStages) & 1u;
-                if (!mbar_wait(&emptyB[s], ph ^ 1u, limit)) {
-                    w4g_timeout(p.err, abort_flag);
-                    break;
-                }
-                issued[s] = true;
-                par[s] = ph;
-                if (gathered) {
-                    mbar_arrive(&fullB[s]);
-                    continue;
-                }
-                mbar_arrive_expect_tx(&fullB[s], (uint32_t)boxes * 8192u);
-                for (int i = 0; i < boxes; ++i)
+    if (warp == 0 || warp == kW4gProducer1) {
+        // ---------------- TMA producers: B, 64 columns of a stage each. A routed expert's gate_up gathers its token
+        // rows from x, four a copy; a warp reads the tokens of a tile ahead, one lane issues (up to 32 copies a
+        // stage: one producer for all 128 columns was as long as a stage).
+        const int j = warp == 0 ? 0 : 1;
+        int* tok = reinterpret_cast<int*>(smem + W4GSmem::kTok) + j * kW4gTok;
+        const uint32_t toks = smem_u32(tok);
+        int it = 0, pv[kW4gTok / 32] = {};
+        auto find = [&]() -> bool {
+            if (!walk.next()) return false;
+            if (WHICH == kW4GUp && !walk.ti.src) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        tma_load_2d(sB + s * kW4gB + j * (kW4gB / 2) + i * 4096, mB, &fullB[s], kb * kW4gK + 64 * j,
-                                    ti.b_row + ti.m0 + 32 * i);
+                for (int i = 0; i < kW4gTok / 32; ++i)  // (rows between the tokens and N read the last token's)
+                    pv[i] = a.perm[walk.ti.b_row + walk.ti.m0 + min(lane + 32 * i, walk.ti.mt - 1)];
             }
+            return true;
+        };
+        bool more = find(), ok = true;
+        while (more && ok) {
+            const W4Tile ti = walk.ti;
+            const bool gathered = WHICH == kW4GUp && !ti.src;
+            if (gathered) {
+#pragma unroll
+                for (int i = 0; i < kW4gTok / 32; ++i) tok[lane + 32 * i] = pv[i] / a.K;
+                __syncwarp();
+            }
+            more = find();
+            if (elect_one()) {
+                const int boxes = (ti.n + 31) / 32;
+                for (int kb = 0; kb < ti.nk && !*abort_flag; ++kb, ++it) {
+                    const int s = it % kW4gBStages;
+                    if (!mbar_wait(&emptyB[s], ((uint32_t)(it / kW4gBStages) & 1u) ^ 1u, limit)) {
+                        w4g_timeout(p.err, abort_flag);
+                        break;
+                    }
+                    uint8_t* st = sB + s * kW4gB + j * (kW4gB / 2);
+                    if (gathered) {
+                        mbar_arrive_expect_tx(&fullB[s], (uint32_t)ti.n * 128u);
+                        for (int r = 0; r < ti.n; r += 16) {
+                            uint4 q[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) q[i] = lds128_smem(toks + 4u * (uint32_t)(r + 4 * i));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                tma_gather4(smem_u32(st) + (uint32_t)(r + 4 * i) * 128u, &tmB0, &fullB[s], kb * kW4gK + 64 * j, (int)q[i].x,
+                                            (int)q[i].y, (int)q[i].z, (int)q[i].w);
+                        }
+                    } else {
+                        const CUtensorMap* mB = ti.src ? &tmB1 : &tmB0;
+                        mbar_arrive_expect_tx(&fullB[s], (uint32_t)boxes * 4096u);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(st + i * 4096, mB, &fullB[s], kb * kW4gK + 64 * j, ti.b_row + ti.m0 + 32 * i);
+                    }
+                }
+            }
+            __syncwarp();
+            it = (int)__reduce_max_sync(0xffffffffu, (unsigned)it);
+            ok = !__any_sync(0xffffffffu, *abort_flag != 0);
         }
         // every copy issued must land before shared memory is released
-        for (int s = 0; s < kW4gBStages; ++s)
-            if (issued[s] && !mbar_wait(&fullB[s], par[s], limit)) w4g_timeout(p.err, abort_flag);
-        }
+        if (elect_one())
+            for (int j = max(0, it - kW4gBStages); j < it; ++j)
+                if (!mbar_wait(&fullB[j % kW4gBStages], (uint32_t)(j / kW4gBStages) & 1u, limit)) w4g_timeout(p.err, abort_flag);
     } else if (warp == 1 || warp == kW4gIssuer1) {
         // ---------------- MMA issuers: warp 1 the tiles' first row halves, kW4gIssuer1 the second ones
         if (elect_one()) {
@@ -394,7 +419,7 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
             while (ok && walk.next() && !*abort_flag) {
                 const W4Tile& ti = walk.ti;
                 const uint32_t idesc = idesc_bf16_f32(kW4gRows / 2, ti.n);
-                const bool gathered = WHICH == kW4GUp && !ti.src, mine = h < ti.halves;
+                const bool mine = h < ti.halves;
                 if (mine) {
                     ok = mbar_wait(&acce[h], pacc, limit);
                     pacc ^= 1u;
@@ -403,11 +428,9 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
                     ok = mbar_wait(&fullB[sb], pb, limit);
                     if (mine) {
                         const uint32_t sa = (uint32_t)h + 2u * (ia & 1u);
-                        if (WHICH == kW4GUp) ok = ok && mbar_wait(&fullG[sb], pb, limit);
                         ok = ok && mbar_wait(&fullA[sa], (ia >> 1) & 1u, limit);
                         ++ia;
                         if (!ok) break;
-                        if (gathered) fence_proxy_async_smem();  // the gathered rows came through the generic proxy
                         tc_fence_after();
                         const uint64_t db = desc0 + (uint64_t)(sb * (kW4gB >> 4));
                         const uint32_t acol = tmem + kW4gACol + sa * (uint32_t)(kW4gK / 2);
@@ -433,9 +456,9 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
             mma_commit(mma_done);
             if (!mbar_wait(mma_done, 0, limit)) w4g_timeout(p.err, abort_flag);
         }
-    } else if (warp >= 6 + kW4gGather) {
+    } else if (warp >= 2 + kW4gEpi) {
         // ---------------- decoders
-        const int dw = warp - 6 - kW4gGather, grp = dw >> 2, quad = warp & 3;
+        const int dw = warp - 2 - kW4gEpi, grp = dw >> 2, quad = warp & 3;
         const uint32_t a0 = tmem + kW4gACol + (uint32_t)(grp * (kW4gK / 2)) + ((uint32_t)(quad * 32) << 16);
         // Group j writes A stage j: every second column block of row half j % 2. (A stage belongs to one half, so
         // that its issuer sees every phase of its barrier: tiles of one half only would let the other issuer
@@ -476,62 +499,9 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&fullA[grp]);
         }
-    } else if (WHICH == kW4GUp && warp >= 6) {
-        // ---------------- gatherers: token rows of x, 8 lanes to a row's 128-byte piece, 16 rows a round
-        {
-            const int tid = threadIdx.x - 6 * 32;
-            const uint32_t c8 = (uint32_t)(lane & 7);
-            const uint64_t pol = l2_evict_last();  // each token row is read by K experts
-            int it = 0;
-            int pv[8];  // the tile's pairs, read a tile ahead
-            auto pairs = [&]() -> bool {
-                if (!walk.next()) return false;
-                const W4Tile& q = walk.ti;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int m = (tid >> 3) + 16 * i;
-                    pv[i] = !q.src && m < q.mt ? a.perm[q.b_row + q.m0 + m] : 0;
-                }
-                return true;
-            };
-            bool more = pairs();
-            while (more && !*abort_flag) {
-                const bf16* row[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) row[i] = a.x + c8 * 8 + (size_t)(pv[i] / a.K) * a.H;
-                const W4Tile cur = walk.ti;
-                more = pairs();
-                bool ok = true;
-                for (int kb = 0; kb < cur.nk; ++kb, ++it) {
-                    const int s = it % kW4gBStages;
-                    if (!__all_sync(0xffffffffu, mbar_wait(&emptyB[s], ((uint32_t)(it / kW4gBStages) & 1u) ^ 1u, limit))) {
-                        if (lane == 0) w4g_timeout(p.err, abort_flag);
-                        ok = false;
-                        break;
-                    }
-                    if (cur.src) {
-                        mbar_arrive(&fullG[s]);
-                        continue;
-                    }
-                    const uint32_t st = smem_u32(sB + s * kW4gB);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t r = (uint32_t)(tid >> 3) + 16u * i;
-                        if (16 * i < cur.n)  // (rows between the tokens and N read a token row that exists)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                cp_async16(st + (uint32_t)j * (kW4gB / 2) + r * 128u + ((c8 ^ (r & 7u)) << 4),
-                                           row[i] + kb * kW4gK + 64 * j, 16u, pol);
-                    }
-                    cp_async_arrive(&fullG[s]);
-                }
-                if (!ok) break;
-            }
-            cp_async_wait_all();  // no copy may be in flight when the CTA exits
-        }
-    } else if (warp >= 2) {
-        // ---------------- epilogue: TMEM lanes 32 * (warp % 4) .. + 31, one weight row each; four warps to a
-        // row half (gate_up: one team of four for both). 16 tokens at a time pass through shared memory, where
+    } else {
+        // ---------------- epilogue: TMEM lanes 32 * (warp % 4) .. + 31, one weight row each; a team of
+        // four warps to a row half. 16 tokens at a time pass through shared memory, where
         // a token's 128 rows (64 h values) lie together, and leave in pieces of 16 bytes: stored from
         // registers, 64 bytes a warp and token, the scattered rows of Y took longer than down's products.
         const int q = warp & 3, team = warp >= 6;
@@ -545,7 +515,7 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
         const int ldo = WHICH == kW4GUp ? a.Imax : WHICH == kW4GDown ? a.H : p.rows[0];
         bf16* const out = WHICH == kW4GUp ? a.h : WHICH == kW4GDown ? a.Yb : p.out;
         const bool bulk = WHICH != kW4GLinear || ((ldo & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0);
-        uint32_t used[2] = {0u, 0u}, buf = 0;
+        uint32_t used = 0, buf = 0;
         W4Tile ti;
         const W4Tile& nx_ti = walk.ti;
         int pv[kW4gTok / 32] = {};
@@ -587,22 +557,22 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
             }
             more = find();
             const int rows = ti.src ? p.rows[1] : p.rows[0];
-            for (int h = 0; h < ti.halves; ++h) {
-                if (WHICH != kW4GUp && h != team) continue;  // the other warps' half
+            if (team < ti.halves) {
+                const int h = team;
                 const int row0 = ti.row0 + h * (kW4gRows / 2), row = row0 + q * 32 + (lane >> 2);
                 float bias[4];  // of rows row + 8 j
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     bias[j] = WHICH == kW4GLinear && p.bias && row + 8 * j < rows ? __bfloat162float(p.bias[row + 8 * j]) : 0.f;
                 const int bytes = min(rows - row0, kW4gRows / 2) * (WHICH == kW4GUp ? 1 : 2);  // of a token
-                if (!__all_sync(0xffffffffu, mbar_wait(&accf[h], used[h] & 1u, limit))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&accf[h], used & 1u, limit))) {
                     if (lane == 0) w4g_timeout(p.err, abort_flag);
                     dead = true;
                 }
                 // the four warps of a team leave together, as they meet at its barrier
                 dead = w4g_team_any(team, dead || *abort_flag);
                 if (dead) break;
-                ++used[h];
+                ++used;
                 tc_fence_after();
                 const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kW4gTok);
                 uint32_t nx[16];

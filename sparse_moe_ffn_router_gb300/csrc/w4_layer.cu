@@ -55,8 +55,8 @@ static cudaError_t w4_linear_gemm(const moe_w4_format& f, const W4LinearArgs& l,
 
 // Gate_up and down of 256 tokens or more on the tensor cores.
 static cudaError_t w4_experts_gemm(const LayerArgs& a, const moe_w4_format& f, cudaStream_t s) {
-    CUtensorMap mx, mh, mhs;  // the h rows are Imax apart; the columns past I (Is) of a row hold nothing
-    if (!make_bf16_map(&mx, a.x, a.T, a.H, a.H, 32) || !make_bf16_map(&mh, a.h, a.P + a.T, a.I, a.Imax, 32) ||
+    CUtensorMap mx, mg, mh, mhs;  // the h rows are Imax apart; the columns past I (Is) of a row hold nothing
+    if (!make_bf16_map(&mx, a.x, a.T, a.H, a.H, 32) || !make_bf16_map(&mg, a.x, a.T, a.H, a.H, 1) || !make_bf16_map(&mh, a.h, a.P + a.T, a.I, a.Imax, 32) ||
         !make_bf16_map(&mhs, a.h, a.P + a.T, a.Is, a.Imax, 32))
         return cudaErrorInvalidValue;
     W4GemmArgs p = {};
@@ -67,7 +67,7 @@ static cudaError_t w4_experts_gemm(const LayerArgs& a, const moe_w4_format& f, c
     p.matrix_bytes = w4_matrix_bytes(f.format, f.group, 2 * a.I, a.H);
     p.rows[0] = 2 * a.I; p.rows[1] = 2 * a.Is;
     p.cols[0] = p.cols[1] = a.H;
-    cudaError_t e = launch_w4_gemm(f.format, f.group, kW4GUp, p, mx, mx, a, s);
+    cudaError_t e = launch_w4_gemm(f.format, f.group, kW4GUp, p, mg, mx, a, s);  // (gathered rows: boxes of one)
     if (e != cudaSuccess) return e;
     p.w[0] = reinterpret_cast<const uint8_t*>(a.down);
     p.w[1] = reinterpret_cast<const uint8_t*>(a.sd);
