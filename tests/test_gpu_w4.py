@@ -342,7 +342,8 @@ def test_layer_shapes(dims, name, group):
     check(L.run(), *L.reference())
 
 
-@pytest.mark.parametrize("dims", [(777, 640, 11, 3, 192, 320), (300, 384, 7, 7, 64, 64), (2000, 640, 64, 2, 64, 192), (1024, 1408, 40, 4, 704, 128)],
+@pytest.mark.parametrize("dims", [(777, 640, 11, 3, 192, 320), (300, 384, 7, 7, 64, 64), (2000, 640, 64, 2, 64, 192), (1024, 1408, 40, 4, 704, 128),
+                                  (1500, 256, 24, 3, 64, 704), (900, 1280, 11, 4, 192, 320)],
                          ids=lambda v: "x".join(map(str, v)))
 def test_layer_repeats_bit_for_bit_with_skewed_experts(dims):
     """Experts of a few tokens next to experts of nearly all, row tiles of one half and of two, several tiles to a
