@@ -204,6 +204,27 @@ def test_linear_nonfinite_rows_stay_apart(T):
     check(out[keep], *ref.linear(x[keep], w, b, rounded=T >= ref.GEMM_TOKENS))
 
 
+def test_linear_on_tensor_cores_keeps_nonfinite_rows_apart():
+    """NaN and infinities in some token rows, those next to tile borders among them, and in one weight row's scale
+    reach their own rows and column only."""
+    T, N, K = 3000, 640, 256
+    f = ref.fmt("e2m1", 64)
+    codes, scales, _ = ref.matrices("e2m1", 64, 1, N, K, seed=5)
+    x = torch.randn(T, K, device="cuda").to(torch.bfloat16)
+    bad = torch.tensor([0, 93, 94, 95, 96, 127, 128, 1500, 2999], device="cuda")
+    x[bad, 7] = torch.tensor([float("nan"), float("inf"), float("-inf")] * 3, dtype=torch.bfloat16, device="cuda")
+    scales[0, 130, 1] = float("nan")
+    ws, out = moe.new_w4_linear_workspace(f, T, N, K), torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    moe.moe_w4_linear(f, x, ref.pack("e2m1", 64, (codes, scales, None)), None, out, ws)
+    row, col = torch.ones(T, dtype=torch.bool, device="cuda"), torch.ones(N, dtype=torch.bool, device="cuda")
+    row[bad], col[130] = False, False
+    assert bool(out[:, 130].isnan().all()) and bool((codes[0, :, 7] % 8 == 0).any())
+    assert not bool(out[bad][:, codes[0, :, 7] % 8 != 0].isfinite().any())
+    w = ref.values("e2m1", 64, (codes, scales, None))[0]
+    want, bound = ref.linear(x[row], w[col], None, rounded=True)
+    check(out[row][:, col], want, bound)
+
+
 def test_tensors_of_another_device_are_refused(monkeypatch):
     f = ref.fmt("int4", 32)
     w = torch.zeros(16, 128, dtype=torch.bfloat16, device="cuda")
