@@ -173,9 +173,10 @@ moe_status moe_forward_host_experts(const moe_dims* d, const void* x, const moe_
  *                                    v = sign * {0, 0.5, 1, 1.5, 2, 3, 4, 6}[code & 7]  MOE_W4_E2M1
  *                                                       (sign: bit 3 of the code)
  * group is 32, 64 or 128 and divides cols.
- * Products use v exactly and apply the scale to each group's fp32 sum in fp32. The
- * tensor-core paths (the layer from 256 tokens; the linear layer where ceil(T / 8) * ceil(N / 16)
- * is more than 14 for each SM, in whole waves of their tiles) multiply by s * v rounded once to bf16.
+ * Products use v exactly and apply the scale to each group's fp32 sum in fp32. The tensor-core
+ * paths multiply by s * v rounded once to bf16: the layer from 256 tokens; the linear layer where
+ * ceil(T / 8) * ceil(N / 16) is more than 14 times the SMs times the waves (tiles of 128 tokens by
+ * 256 rows, an SM each).
  * Packed form (moe_w4_size bytes, 16-byte aligned): matrices one after another, each a sequence
  * of strips of 16 rows (layout MOE_W4_ROWS: rows 16j .. 16j+15; MOE_W4_GATE_UP, for the merged
  * [2I, H] tensors: gate rows 8j .. 8j+7, then the matching up rows I+8j .. I+8j+7); a strip is a

@@ -169,23 +169,9 @@ __device__ __forceinline__ void w4_load_at(uint32_t at, uint32_t meta, uint32_t 
 }
 
 template <int FMT, int G>
-__device__ __forceinline__ void w4_load(uint32_t rec, int lane, W4Frag<FMT, G>& f) {
-    constexpr uint32_t N = W4Rec<FMT, G>::kGroups;
-    const uint32_t row = (uint32_t)lane >> 2;
-    w4_load_at<FMT, G, 0>(rec + 16u * (uint32_t)lane, rec + 2u * N * row, rec + N * row, f);
-}
-
-template <int FMT, int G>
 __device__ __forceinline__ float w4_scale(const W4Frag<FMT, G>& f, int h, int gi) {
     return (gi & 1) ? bf_hi(f.s[h][gi >> 1]) : bf_lo(f.s[h][gi >> 1]);
 }
-template <int FMT, int G>
-__device__ __forceinline__ uint32_t w4_bias(const W4Frag<FMT, G>& f, int h, int gi) {
-    if (FMT != MOE_W4_INT4_ZP) return 0xc308c308u;
-    // 0xc3zz in both halves: byte gi of the zero points below 0xc3
-    return __byte_perm(f.z[h], 0xc3u, 0x4040u | (uint32_t)(gi << 8) | (uint32_t)gi);
-}
-
 // m16n8k16 bf16 MMAs, fp32 accumulate (not volatile: the compiler may interleave independent records).
 __device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {

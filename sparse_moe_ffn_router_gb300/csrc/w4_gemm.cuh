@@ -26,11 +26,12 @@
 //   warps 10-25 decoders: four groups of four warps, group j writes A stage j, warp w lanes
 //               32 (w % 4) .. + 31
 //
-// Measured: linear 4096 x 2048 by 4096 tokens 52 us (1.31 PFLOP/s, 0.70 of the measured cuBLAS rate; the
+// Measured: linear 4096 x 2048 by 4096 tokens 53 us (1.30 PFLOP/s, 0.70 of the measured cuBLAS rate; the
 // tensor pipe is active 63 % of the time), the MoE layer of 4096 tokens and 256 experts 182 us in gate_up
-// and 138 us in down of 390. What is left is the decoders' and the epilogue's share of the issue slots (68 %)
-// and the four A stages' hand-over: a stage in two halves (finer hand-over) took 434 us for that layer, a
-// second accumulator for tiles of up to 64 tokens 414.
+// and 133 us in down of 380. What is left is the decoders' and the epilogue's share of the issue slots (68 %)
+// and the A stages' hand-over. Neither alone gives much: a stage handed over in two halves took that layer from
+// 390 to 434 us, a second accumulator for tiles of up to 64 tokens to 414; a third one for down in the place of its
+// second A stages 382 against 380; accumulators read whole before anything is stored 418 (registers).
 #pragma once
 
 #include "launch.h"
@@ -62,7 +63,8 @@ cudaError_t launch_w4_gemm(int format, int group, int which, const W4GemmArgs& p
 #ifdef __CUDACC__
 
 constexpr int kW4gK = 128;                       // columns of a stage
-constexpr int kW4gAStages = 4, kW4gBStages = 5;  // (A: two for each row half; a sixth B stage takes the L1 that the records pass through: layer T=4096 388 against 380 us)
+constexpr int kW4gAStages = 4, kW4gBStages = 5;  // (two A stages to a row half; a sixth B stage would take the L1 that
+                                                 // the records pass through: layer of 4096 tokens 388 against 380 us)
 constexpr int kW4gEpi = 8, kW4gDec = 16;         // epilogue and decoder warps
 constexpr int kW4gIssuer1 = 2 + kW4gEpi + kW4gDec;
 constexpr int kW4gProducer1 = kW4gIssuer1 + 1;
