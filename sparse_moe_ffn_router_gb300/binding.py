@@ -348,9 +348,14 @@ def moe_w4_size(fmt: W4Format, rows: int, cols: int, n: int = 1) -> int:
     return int(load_library().moe_w4_size(ctypes.byref(fmt), int(n), int(rows), int(cols)))
 
 
+@functools.lru_cache(maxsize=1024)
+def _w4_bytes(fmt: int, group: int, rows: int, cols: int) -> int:
+    return moe_w4_size(W4Format(fmt, group), rows, cols)
+
+
 def new_w4(fmt: W4Format, rows: int, cols: int, n: int = 1, device="cuda") -> torch.Tensor:
     """An uninitialised uint8 CUDA tensor [n, bytes of one packed matrix]."""
-    b = moe_w4_size(fmt, rows, cols, 1)
+    b = _w4_bytes(fmt.format, fmt.group, int(rows), int(cols))
     if b == 0 or n < 0:
         raise MoEError(2, "moe_w4_size")
     return torch.empty(int(n), b, dtype=torch.uint8, device=device)
