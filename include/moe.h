@@ -241,7 +241,7 @@ moe_status moe_w4_linear(const moe_w4_format* f, int32_t T, int32_t N, int32_t K
  * w->shared_gate_up in layout MOE_W4_GATE_UP, w->down (E matrices [H, I]) and w->shared_down in
  * layout MOE_W4_ROWS, all in format f; router_w, router_b and shared_gate are bf16 as ever. Same
  * dims (with I and Is multiples of f->group), flags, workspace (moe_workspace_size), taps and
- * errors as moe_forward. One token (H <= 4096) runs as one grid of one CTA per SM whose CTAs
+ * errors as moe_forward (but with K = 1 and T >= 256 tap 1 holds fp32, twice the bytes stated). One token (H <= 4096) runs as one grid of one CTA per SM whose CTAs
  * exchange values, with the needs stated above for that. */
 moe_status moe_forward_w4(const moe_dims* d, const moe_w4_format* f, const void* x, const moe_weights* w,
                           const void* residual, void* out, void* workspace, size_t ws_bytes, void* stream);

@@ -108,7 +108,8 @@ inline bool make_plan(const moe_dims& d, Plan* p) {
     p->o_h = take((P + T) * p->Imax * 2);
     p->gemm = d.T >= kGemmMinTokens;
     // Y, which a statistics call borrows for its per-block partial sums (fp32 + int per expert)
-    const size_t ybytes = T * (d.K + 1) * d.H * (p->gemm ? 2 : 4);
+    // (K = 1: the 4-bit layer keeps Y in fp32 for any T)
+    const size_t ybytes = T * (d.K + 1) * d.H * (p->gemm && d.K > 1 ? 2 : 4);
     const size_t sbytes = (size_t)((d.T + kStatsTokens - 1) / kStatsTokens) * d.E * 8;
     p->o_y = take(ybytes > sbytes ? ybytes : sbytes);
     p->o_upg = take((size_t)(d.E + 1) * sizeof(GemmGroup));

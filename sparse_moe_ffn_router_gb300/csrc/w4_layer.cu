@@ -76,7 +76,7 @@ static cudaError_t w4_experts_gemm(const LayerArgs& a, const moe_w4_format& f, c
     p.cols[0] = a.I; p.cols[1] = a.Is;
     e = launch_w4_gemm(f.format, f.group, kW4GDown, p, mh, mhs, a, s);
     if (e != cudaSuccess) return e;
-    return launch_combine(a, s);
+    return a.K == 1 ? launch_combine_pdl(a, s) : launch_combine(a, s);  // (Y in fp32, in bf16)
 }
 
 // Strips of a block, at most: the power of two that still gives every SM four items or more of the

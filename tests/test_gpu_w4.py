@@ -363,6 +363,20 @@ def test_layer_shapes(dims, name, group):
     check(L.run(), *L.reference())
 
 
+@pytest.mark.parametrize("dims", [(300, 512, 4, 1, 128, 64), (700, 640, 5, 1, 64, 192), (1000, 2048, 16, 1, 512, 512), (256, 128, 1, 1, 64, 64)],
+                         ids=lambda v: "x".join(map(str, v)))
+def test_layer_of_one_expert_a_token(dims):
+    """On the tensor cores Y is not rounded where K is 1: the bound without those roundings holds."""
+    L = W4Layer(dims, "e2m1", 64, seed=sum(dims), bias=True)
+    want, bound = ref.layer(L.dims, L.x, L.router_w, L.router_b, L.shared_gate, L.v["gate_up"], L.v["down"], L.v["shared_gate_up"][0],
+                            L.v["shared_down"][0], L.residual, weight_half=ref.HALF, y_half=0.0)
+    ws = moe.new_workspace(L.dims)
+    first = L.run(ws=ws)
+    check(first, want, bound)
+    for _ in range(5):
+        assert torch.equal(L.run(ws=ws), first)
+
+
 @pytest.mark.parametrize("dims", [(777, 640, 11, 3, 192, 320), (300, 384, 7, 7, 64, 64), (2000, 640, 64, 2, 64, 192), (1024, 1408, 40, 4, 704, 128),
                                   (1500, 256, 24, 3, 64, 704), (900, 1280, 11, 4, 192, 320)],
                          ids=lambda v: "x".join(map(str, v)))
