@@ -225,6 +225,40 @@ def test_linear_on_tensor_cores_keeps_nonfinite_rows_apart():
     check(out[row][:, col], want, bound)
 
 
+def test_tensor_core_paths_in_one_graph():
+    """A linear layer and a layer of many tokens captured together, replayed on new inputs, and between eager calls on the
+    same workspaces."""
+    f, T, N, K = ref.fmt("int4", 64), 3000, 640, 512
+    packed = ref.pack("int4", 64, ref.matrices("int4", 64, 1, N, K, seed=3))
+    x = torch.randn(T, K, device="cuda").to(torch.bfloat16)
+    ws, out = moe.new_w4_linear_workspace(f, T, N, K), torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    L = W4Layer((400, 640, 9, 2, 192, 64), "int4", 64, seed=11, bias=True)
+    lws, lout = moe.new_workspace(L.dims), torch.empty_like(L.x)
+
+    def both(o, lo):
+        moe.moe_w4_linear(f, x, packed, None, o, ws)
+        moe.moe_forward_w4(L.dims, f, L.x, L.W, L.residual, lo, lws)
+
+    both(out, lout)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for _ in range(2):
+            both(out, lout)
+    for seed in range(3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x.copy_(torch.randn(T, K, generator=g, device="cuda"))
+        L.residual.copy_(torch.randn(L.residual.shape, generator=g, device="cuda"))
+        out.fill_(float("nan"))
+        lout.fill_(float("nan"))
+        graph.replay()
+        want, lwant = torch.empty_like(out), torch.empty_like(lout)
+        both(want, lwant)
+        assert torch.equal(out, want) and torch.equal(lout, lwant)
+    assert moe.moe_last_device_error(ws) == 0 and moe.moe_last_device_error(lws) == 0
+
+
 def test_tensors_of_another_device_are_refused(monkeypatch):
     f = ref.fmt("int4", 32)
     w = torch.zeros(16, 128, dtype=torch.bfloat16, device="cuda")
