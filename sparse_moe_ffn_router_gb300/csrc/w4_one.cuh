@@ -198,16 +198,18 @@ __device__ __forceinline__ void w4o_exchange(const W4OneArgs& p, const W4OneRout
             }
             ok = __all_sync(0xffffffffu, ok);
         }
-        if (blockIdx.x == 0) {  // tap 0: rows in dispatch order, the shared expert's last
-            int pos = 0;
-            for (int j = 0; j < K; ++j) pos += g < K && rt.ids[j] < rt.ids[g];
-            __syncwarp();
-            for (int c = lane; c < pairs; c += 32)
-                reinterpret_cast<uint32_t*>(a.h + (size_t)(g == K ? K : pos) * a.Imax)[c] = *reinterpret_cast<uint32_t*>(dst + 4 * c);
-        }
     }
     if (!ok && lane == 0) atomicOr(err, ERR_TIMEOUT);
-    asm volatile("bar.sync 2, %0;" ::"n"(32 * (kW4Warps + 1)) : "memory");  // h rows in place; the router's weights too
+    asm volatile("bar.sync 2, %0;" ::"n"(32 * (kW4Warps + 1)) : "memory");  // h rows in place; the routing complete
+    // tap 0: rows in dispatch order, the shared expert's last. Not before the barrier: a CTA without a routed
+    // gate_up strip of its own (K * I / 8 below the CTAs) waits for nothing else of its router.
+    if (blockIdx.x == 0)
+        for (int g = warp; g <= K; g += kW4Warps) {
+            int pos = 0;
+            for (int j = 0; j < K; ++j) pos += g < K && rt.ids[j] < rt.ids[g];
+            for (int c = lane; c < (g == K ? a.Is : a.I) / 2; c += 32)
+                reinterpret_cast<uint32_t*>(a.h + (size_t)(g == K ? K : pos) * a.Imax)[c] = *reinterpret_cast<const uint32_t*>(hs + g * hpitch + 4 * c);
+        }
 }
 
 template <int FMT, int G>

@@ -1,0 +1,61 @@
+"""What the 4-bit layer leaves in the workspace, stage by stage against 64 bits (w4_stages.py)."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import sparse_moe_ffn_router_gb300 as moe
+from tests import w4_reference as ref
+from tests import w4_stages as st
+from tests.test_gpu_w4 import W4Layer, check
+
+pytestmark = pytest.mark.gpu
+
+
+def tap(ws, dims, which, dtype, shape):
+    at, n = moe.moe_workspace_tap(dims, which)
+    t = ws[at:at + n].view(dtype)
+    assert t.numel() == torch.Size(shape).numel()
+    return t.view(shape)
+
+
+def check_routing(L, ws):
+    T, H, E, K, I, Is = L.dims
+    ids, topw, sgate = st.routing(L.x, L.router_w, L.router_b, L.shared_gate, K)
+    got = tap(ws, L.dims, 3, torch.int32, (T, K))
+    assert torch.equal(got.long(), ids)
+    w, g = tap(ws, L.dims, 4, torch.float32, (T, K)), tap(ws, L.dims, 2, torch.float32, (T,))
+    check(w, topw, torch.full_like(topw, 5e-4), "routing weights")
+    check(g, sgate, torch.full_like(sgate, 5e-4), "shared gate")
+    return got, w, g
+
+
+def check_activations(L, ws, ids, rounded=False):
+    T, H, E, K, I, Is = L.dims
+    W = {k: st.weights(L.name, L.group, L.m[k], rounded) for k in ("gate_up", "shared_gate_up")}
+    want, bound = st.activations(L.dims, L.x, ids, W["gate_up"], W["shared_gate_up"][0])
+    h = tap(ws, L.dims, 0, torch.bfloat16, want.shape)
+    live = ~want.isnan()
+    check(h[live], want[live], bound[live], "h")
+    return h
+
+
+@pytest.mark.parametrize("dims,name,group", [((1, 512, 32, 4, 128, 128), "int4", 32), ((1, 1024, 64, 2, 512, 64), "e2m1", 64),
+                                             ((1, 128, 8, 1, 64, 64), "int4_zp", 64), ((1, 640, 200, 8, 64, 320), "int4", 64),
+                                             ((1, 2048, 256, 8, 512, 512), "int4", 32), ((1, 4096, 16, 8, 192, 2048), "e2m1", 32)],
+                         ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else str(v))
+def test_one_token_leaves_its_activations(dims, name, group):
+    """Tap 0 of the one-kernel layer holds the experts' rows in dispatch order, every time; with fewer routed gate_up
+    strips (K * I / 8) than SMs, the CTA that writes it has none of its own."""
+    for seed in range(4):  # other experts, in other orders
+        L = W4Layer(dims, name, group, seed=seed + sum(dims), bias=True)
+        ws = moe.new_workspace(L.dims)
+        at, n = moe.moe_workspace_tap(L.dims, 0)
+        first = None
+        for _ in range(40):
+            ws[at:at + n] = 255
+            L.run(ws=ws)
+            if first is None:
+                check_activations(L, ws, check_routing(L, ws)[0])
+                first = ws[at:at + n].clone()
+            assert torch.equal(ws[at:at + n], first)
