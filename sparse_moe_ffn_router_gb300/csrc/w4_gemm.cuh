@@ -542,6 +542,7 @@ __global__ void __launch_bounds__(kW4gThreads, 1)
             ti = nx_ti;
             if (WHICH == kW4GDown) {
                 // output row (token, slot) and scale of each token of the tile
+                __syncwarp();  // (stores of fp32 Y may still read the last tile's)
 #pragma unroll
                 for (int i = 0; i < kW4gTok / 32; ++i) {
                     const int m = lane + 32 * i;

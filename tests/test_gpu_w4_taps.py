@@ -59,3 +59,26 @@ def test_one_token_leaves_its_activations(dims, name, group):
                 check_activations(L, ws, check_routing(L, ws)[0])
                 first = ws[at:at + n].clone()
             assert torch.equal(ws[at:at + n], first)
+
+
+@pytest.mark.parametrize("dims", [(4000, 256, 6, 1, 64, 64), (700, 1280, 5, 1, 64, 192), (3001, 2048, 40, 1, 128, 256)],
+                         ids=lambda v: "x".join(map(str, v)))
+def test_one_expert_a_token_leaves_its_outputs(dims):
+    """With one expert a token Y is fp32 from 256 tokens too; several tiles to a CTA, every value written by its own
+    token and scale, every time, also where Y held NaN before."""
+    L = W4Layer(dims, "int4", 64, seed=sum(dims), bias=True)
+    T, H, E, K, I, Is = dims
+    ws = moe.new_workspace(L.dims)
+    at = moe.moe_workspace_tap(L.dims, 1)[0]
+    y = ws[at:at + T * 2 * H * 4].view(torch.float32).view(T, 2, H)
+    first = None
+    for _ in range(30):
+        y.fill_(float("nan"))
+        L.run(ws=ws)
+        if first is None:
+            ids, w, g = check_routing(L, ws)
+            h = check_activations(L, ws, ids, rounded=True)
+            W = {k: st.weights(L.name, L.group, L.m[k], True) for k in ("down", "shared_down")}
+            check(y, *st.outputs(L.dims, h, ids, w, g, W["down"], W["shared_down"][0], 0.0), "Y")
+            first = y.clone()
+        assert torch.equal(y, first)
