@@ -197,7 +197,7 @@ typedef struct {
 } moe_w4_format;
 
 /* Bytes of n packed matrices [rows, cols]; 0 when the format or shape is not supported:
- * n >= 0, rows >= 1, 32 <= cols <= 65536, cols % group == 0, rows * cols < 2^40 / max(n, 1). */
+ * n >= 0, 1 <= rows <= 2^31 - 256, 32 <= cols <= 65536, cols % group == 0, rows * cols < 2^40 / max(n, 1). */
 size_t moe_w4_size(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols);
 
 /* Quantises n bf16 matrices w [n, rows, cols] into packed form. Per group, in fp32 with correctly
@@ -228,7 +228,7 @@ moe_status moe_w4_dequantize(const moe_w4_format* f, int32_t n, int32_t rows, in
 /* Linear layer on packed weights (layout MOE_W4_ROWS, one matrix [N, K]):
  *   out[t, n] = bf16( sum_k x[t, k] * w[n, k] + bias[n] )      fp32 sums in a fixed order
  *   x [T, K], bias [N] or NULL, out [T, N], all bf16 (bias 2-byte aligned); out must not overlap x.
- * T = 0 is a no-op; T * N and T * K < 2^40. The workspace (moe_w4_linear_workspace_size bytes,
+ * T = 0 is a no-op; T <= 2^31 - 256, T * N and T * K < 2^40. The workspace (moe_w4_linear_workspace_size bytes,
  * zero-filled once by moe_workspace_init) holds the error word of moe_last_device_error; calls
  * that may overlap in time need one each. x, bias, the weights and the workspace are read after
  * the previous kernel on `stream` is complete. */

@@ -426,7 +426,7 @@ bool w4_format_known(const moe_w4_format* f) {
 }
 
 bool w4_shape(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols) {
-    if (n < 0 || rows < 1 || cols < 32 || cols > 65536 || cols % f->group) return false;
+    if (n < 0 || rows < 1 || rows > kW4MaxRows || cols < 32 || cols > 65536 || cols % f->group) return false;
     return (int64_t)rows * cols < ((int64_t)1 << 40) / (n > 0 ? n : 1);
 }
 
@@ -491,7 +491,7 @@ extern "C" moe_status moe_w4_dequantize(const moe_w4_format* f, int32_t n, int32
 }
 
 extern "C" size_t moe_w4_linear_workspace_size(const moe_w4_format* f, int32_t T, int32_t N, int32_t K) {
-    if (!w4_format_known(f) || T < 0 || !w4_shape(f, 1, N, K)) return 0;
+    if (!w4_format_known(f) || T < 0 || T > kW4MaxRows || !w4_shape(f, 1, N, K)) return 0;
     return align256(sizeof(WsHeader));
 }
 
@@ -499,7 +499,7 @@ extern "C" moe_status moe_w4_linear(const moe_w4_format* f, int32_t T, int32_t N
                                     const void* packed, size_t packed_bytes, const void* bias, void* out, void* workspace,
                                     size_t ws_bytes, void* stream) {
     if (!w4_format_known(f) || T < 0) return MOE_ERR_INVALID_ARG;
-    if (!w4_shape(f, 1, N, K) || (int64_t)T * N >= (int64_t)1 << 40 || (int64_t)T * K >= (int64_t)1 << 40)
+    if (!w4_shape(f, 1, N, K) || T > kW4MaxRows || (int64_t)T * N >= (int64_t)1 << 40 || (int64_t)T * K >= (int64_t)1 << 40)
         return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return MOE_OK;
     if (!x || !packed || !out || !workspace) return MOE_ERR_INVALID_ARG;

@@ -31,6 +31,8 @@ namespace moe {
 constexpr int kW4Strip = 16;    // rows of a strip
 constexpr int kW4Cols = 128;    // columns of a record
 constexpr int kW4Codes = 1024;  // bytes of codes in a record
+// Weight rows and token rows, at most: a row index rounded up to a tile (256 rows at most) still fits an int.
+constexpr int kW4MaxRows = 0x7fffffff - 255;
 
 __host__ __device__ constexpr int w4_record_bytes(int format, int group) {
     return kW4Codes + 16 * (kW4Cols / group) * (format == MOE_W4_INT4_ZP ? 3 : 2);

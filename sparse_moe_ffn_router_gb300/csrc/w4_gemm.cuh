@@ -139,7 +139,7 @@ struct W4Walk {
         if (WHICH == kW4GLinear) {
             tok_tiles = p.tok_tiles;
             rows = p.T;
-            per = (rows + tok_tiles - 1) / tok_tiles;
+            per = (int)(((unsigned)rows + (unsigned)tok_tiles - 1u) / (unsigned)tok_tiles);  // (the sum may pass 2^31)
             ti.b_row = ti.src = ti.out_row0 = 0;
             ti.w = p.w[0];
             cost = 1;
@@ -700,7 +700,7 @@ cudaError_t launch_w4_gemm_t(const W4GemmArgs& args, const CUtensorMap& b0, cons
         // (with many waves there is little to fill)
         const int most = (long long)least * rt <= 8LL * a.num_sms ? least + least / 2 + 1 : least;
         for (int n = least; n <= most; ++n) {
-            const int per = (p.T + n - 1) / n, tiles = (p.T + per - 1) / per;
+            const int per = (int)(((long long)p.T + n - 1) / n), tiles = (p.T + per - 1) / per;
             const long long cost = (((long long)tiles * rt + a.num_sms - 1) / a.num_sms) * (((per + 15) & ~15) + 32);
             if (best == 0 || cost < best) {
                 best = cost;

@@ -82,3 +82,21 @@ def test_one_expert_a_token_leaves_its_outputs(dims):
             check(y, *st.outputs(L.dims, h, ids, w, g, W["down"], W["shared_down"][0], 0.0), "Y")
             first = y.clone()
         assert torch.equal(y, first)
+
+
+def test_linear_offsets_past_32_bits():
+    """More than 2^32 elements of token rows and of results, on the tensor-core path: rows spread over the whole range."""
+    T, N, K = (1 << 26) + 77, 66, 64
+    assert T * N > 1 << 32 and T * K > 1 << 32 and torch.cuda.mem_get_info()[0] > 24 << 30
+    m = ref.matrices("int4", 64, 1, N, K, seed=7)
+    w, f = st.weights("int4", 64, m, True)[0], ref.fmt("int4", 64)
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    rows = torch.cat([torch.arange(0, 300), torch.randint(0, T, (3000,)), torch.arange(T - 300, T)]).unique().cuda()
+    x[rows] = torch.randn(rows.numel(), K, device="cuda").to(torch.bfloat16)
+    out = torch.full((T, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    ws = moe.new_w4_linear_workspace(f, T, N, K)
+    moe.moe_w4_linear(f, x, ref.pack("int4", 64, m), None, out, ws)
+    assert moe.moe_last_device_error(ws) == 0
+    check(out[rows], *ref.linear(x[rows], w, None))
+    out[rows] = 0
+    assert all(not bool(part.any()) for part in out.split(1 << 24))

@@ -42,6 +42,26 @@ def test_size_refuses(lib):
         assert lib.moe_w4_linear_workspace_size(f, 1, r, c) == 0 or n != 1
 
 
+def test_largest_row_counts(lib):
+    """The largest counts whose roundings to strips and tiles fit 32 bits, and one more."""
+    most = 2 ** 31 - 256
+    for rows in (most, most - 1, most - 15, most - 16):
+        assert lib.moe_w4_size(F(), 1, rows, 32) == -(-rows // 16) * 1152
+    for rows in (most + 1, 2 ** 31 - 16, 2 ** 31 - 1):
+        assert lib.moe_w4_size(F(), 1, rows, 32) == 0
+        assert _quantize(lib, n=1, rows=rows, cols=32) == 2 and _dequantize(lib, n=1, rows=rows, cols=32) == 2
+        assert lib.moe_w4_pack(F(), 1, rows, 32, 0, A, A, None, A + 0x1000000, 1 << 60, None) == 2
+    ws = lib.moe_w4_linear_workspace_size(F(), most, 16, 32)
+    assert ws > 0 and lib.moe_w4_linear_workspace_size(F(), most + 1, 16, 32) == 0
+
+    def linear(T, N):
+        return lib.moe_w4_linear(F(), T, N, 32, None, A, 1 << 60, None, A + 0x200000, A + 0x300000, ws, None)
+
+    assert linear(most, 16) == 1 and linear(16, most) == 1  # past the sizes, refused for the missing x
+    for big in (most + 1, 2 ** 31 - 128, 2 ** 31 - 1):
+        assert linear(big, 16) == 2 and linear(16, big) == 2
+
+
 def _quantize(lib, f=None, n=2, rows=32, cols=256, layout=0, w=A, packed=A + 0x1000000, nbytes=1 << 20):
     return lib.moe_w4_quantize(f or F(), n, rows, cols, layout, w, packed, nbytes, None)
 
