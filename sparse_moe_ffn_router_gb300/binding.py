@@ -452,12 +452,36 @@ def moe_w4_linear(fmt: W4Format, x, packed, bias, out, workspace, stream=None):
 
 @functools.lru_cache(maxsize=256)
 def _w4_layer(dims: tuple, fmt: int, group: int):
-    """The dims (whole numbers) as passed to C, and the bytes of the layer's packed gate_up, down, shared_gate_up and shared_down."""
+    """The dims (whole numbers) as passed to C, the bytes of the layer's packed gate_up, down, shared_gate_up and shared_down, and
+    the elements of its bf16 tensors."""
     d = Dims(*dims)
     record = 1024 + 16 * (128 // group) * (3 if fmt == W4_INT4_ZP else 2) if group in (32, 64, 128) else 0
     h = (d.H + 127) // 128
     return d, (d.E * ((2 * d.I + 15) // 16) * h * record, d.E * ((d.H + 15) // 16) * ((d.I + 127) // 128) * record,
-               ((2 * d.Is + 15) // 16) * h * record, ((d.H + 15) // 16) * ((d.Is + 127) // 128) * record)
+               ((2 * d.Is + 15) // 16) * h * record, ((d.H + 15) // 16) * ((d.Is + 127) // 128) * record), \
+        (d.T * d.H, d.T * d.H, d.T * d.H, d.E * d.H, d.E, d.H)
+
+
+_BF16, _U8 = torch.bfloat16, torch.uint8
+
+
+def _w4_refuse(packed, needs, plain, counts):
+    """Raises what is wrong with the tensors of moe_forward_w4."""
+    for t, need in zip(packed, needs):
+        if t is None or t.dtype != _U8:
+            raise TypeError("the experts' weights must be packed 4-bit weights (uint8)")
+        if t.numel() < need:
+            raise ValueError(f"packed weights of {t.numel()} bytes, the layer's dims need {need}")
+    for name, t, need in zip(("x", "out", "residual", "router_w", "router_b", "shared_gate"), plain, counts):
+        if t is None:
+            if name in ("residual", "router_b"):
+                continue
+            raise TypeError(f"{name} is missing")
+        if t.dtype != _BF16:
+            raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
+        if t.numel() < need:
+            raise ValueError(f"{name} holds {t.numel()} elements, the layer's dims need {need}")
+    raise TypeError("expected torch.Tensors")
 
 
 def moe_forward_w4(dims, fmt: W4Format, x, weights: Weights, residual, out, workspace, stream=None):
@@ -465,17 +489,23 @@ def moe_forward_w4(dims, fmt: W4Format, x, weights: Weights, residual, out, work
     (uint8 tensors of moe_w4_size bytes; gate_up layouts W4_GATE_UP, down layouts W4_ROWS)."""
     if isinstance(dims, Dims):
         dims = tuple(getattr(dims, f) for f, _ in Dims._fields_)
-    d, needs = _w4_layer(tuple(map(int, dims)), fmt.format, fmt.group)
-    packed = (weights.gate_up, weights.down, weights.shared_gate_up, weights.shared_down)
-    for t, need in zip(packed, needs):
-        if t.dtype != torch.uint8:
-            raise TypeError("the experts' weights must be packed 4-bit weights (uint8)")
-        if t.numel() < need:
-            raise ValueError(f"packed weights of {t.numel()} bytes, the layer's dims need {need}")
+    d, needs, counts = _w4_layer(tuple(map(int, dims)), fmt.format, fmt.group)
+    rw, rb, gu, dn, sgu, sdn, sg = (weights.router_w, weights.router_b, weights.gate_up, weights.down, weights.shared_gate_up,
+                                    weights.shared_down, weights.shared_gate)
+    rows, er, eb, hs = counts[0], counts[3], counts[4], counts[5]
+    try:
+        fits = (gu.dtype is dn.dtype is sgu.dtype is sdn.dtype is _U8 and x.dtype is out.dtype is rw.dtype is sg.dtype is _BF16
+                and gu.numel() >= needs[0] and dn.numel() >= needs[1] and sgu.numel() >= needs[2] and sdn.numel() >= needs[3]
+                and x.numel() >= rows and out.numel() >= rows and rw.numel() >= er and sg.numel() >= hs
+                and (residual is None or residual.dtype is _BF16 and residual.numel() >= rows)
+                and (rb is None or rb.dtype is _BF16 and rb.numel() >= eb))
+    except AttributeError:
+        fits = False
+    if not fits:
+        _w4_refuse((gu, dn, sgu, sdn), needs, (x, out, residual, rw, rb, sg), counts)
     dev = _device(x)
-    px, res, po, ws, router_w, router_b, gu, dn, sgu, sdn, gate = _here(
-        dev, x, residual, out, workspace, weights.router_w, weights.router_b, *packed, weights.shared_gate)
-    w = CWeights(router_w, router_b, gu, dn, sgu, sdn, gate)
+    px, po, res, router_w, router_b, gate, ws, *packed = _here(dev, x, out, residual, rw, rb, sg, workspace, gu, dn, sgu, sdn)
+    w = CWeights(router_w, router_b, *packed, gate)
     _check(load_library().moe_forward_w4(ctypes.byref(d), ctypes.byref(fmt), px, ctypes.byref(w), res, po, ws, _nbytes(workspace),
                                          _stream_of(stream, dev)), "moe_forward_w4")
 

@@ -148,3 +148,39 @@ def test_binding_checks():
         binding.moe_forward_w4((1, 128, 8, 2, 64, 64), f, w, binding.Weights(*[w] * 7), None, w, w)
     with pytest.raises(ValueError):  # packed tensors too small for the dims
         binding.moe_forward_w4((1, 128, 8, 2, 64, 64), f, w, binding.Weights(*[torch.zeros(16, dtype=torch.uint8)] * 7), None, w, w)
+
+
+def test_forward_binding_checks_every_tensor():
+    """Rows, types and sizes that do not fit the dims are refused before the library sees a pointer."""
+    f, dims = W4Format(0, 32), (5, 128, 8, 2, 64, 64)
+    T, H, E, K, I, Is = dims
+
+    def bf16(*shape):
+        return torch.zeros(*shape, dtype=torch.bfloat16)
+
+    def packed(n, rows, cols):
+        return torch.zeros(n, binding.moe_w4_size(f, rows, cols), dtype=torch.uint8)
+
+    def call(residual=None, dims=dims, **over):
+        t = dict(x=bf16(T, H), out=bf16(T, H), router_w=bf16(E, H), router_b=bf16(E), shared_gate=bf16(1, H),
+                 gate_up=packed(E, 2 * I, H), down=packed(E, H, I), shared_gate_up=packed(1, 2 * Is, H), shared_down=packed(1, H, Is))
+        t.update(over)
+        x, out = t.pop("x"), t.pop("out")
+        binding.moe_forward_w4(dims, f, x, binding.Weights(**t), residual, out, torch.zeros(1 << 20, dtype=torch.uint8))
+
+    for name, t in (("x", bf16(T - 1, H)), ("out", bf16(T, H - 1)), ("residual", bf16(T * H - 1)), ("router_w", bf16(E - 1, H)),
+                    ("router_b", bf16(E - 1)), ("shared_gate", bf16(H - 1))):
+        with pytest.raises(ValueError, match=f"{name} holds"):
+            call(**{name: t})
+    for name, t in (("x", bf16(T, H).float()), ("out", bf16(T, H).half()), ("residual", bf16(T, H).float()), ("router_w", bf16(E, H).float()),
+                    ("router_b", bf16(E).float()), ("shared_gate", bf16(1, H).float())):
+        with pytest.raises(TypeError, match=f"{name} must be"):
+            call(**{name: t})
+    for name in ("x", "out", "router_w", "shared_gate"):
+        with pytest.raises(TypeError, match=f"{name} is missing"):
+            call(**{name: None})
+    for name in ("gate_up", "down", "shared_gate_up", "shared_down"):
+        with pytest.raises(ValueError, match="packed weights of"):
+            call(**{name: torch.zeros(1000, dtype=torch.uint8)})
+    with pytest.raises(ValueError, match="GPU only"):  # everything fits: only the device is wrong
+        call(router_b=None)
