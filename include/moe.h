@@ -91,8 +91,9 @@ typedef enum {
     MOE_ERR_DEVICE = 7               /* a kernel flagged bad data (e.g. a non-finite score) */
 } moe_status;
 
-/* Bytes of device workspace that moe_route / moe_forward need for dims d (0 if d is
- * unsupported). Host-only; never fails otherwise. */
+/* Bytes of device workspace that moe_route / moe_forward / moe_forward_w4 need for dims d (0 if
+ * d is unsupported). Host-only; never fails otherwise. (At T = 1, and at K = 1 from 256 tokens,
+ * the last part is used by moe_forward_w4 alone: the other calls accept a workspace without it.) */
 size_t moe_workspace_size(const moe_dims* d);
 
 /* Zero-fill a workspace on `stream` (cudaMemsetAsync). Needed once after allocation. */
@@ -240,9 +241,10 @@ moe_status moe_w4_linear(const moe_w4_format* f, int32_t T, int32_t N, int32_t K
 /* moe_forward with the experts' weights packed: w->gate_up (E matrices [2I, H]) and
  * w->shared_gate_up in layout MOE_W4_GATE_UP, w->down (E matrices [H, I]) and w->shared_down in
  * layout MOE_W4_ROWS, all in format f; router_w, router_b and shared_gate are bf16 as ever. Same
- * dims (with I and Is multiples of f->group), flags, workspace (moe_workspace_size), taps and
- * errors as moe_forward (but with K = 1 and T >= 256 tap 1 holds fp32, twice the bytes stated). One token (H <= 4096) runs as one grid of one CTA per SM whose CTAs
- * exchange values, with the needs stated above for that. */
+ * dims (with I and Is multiples of f->group), flags, workspace (moe_workspace_size), taps
+ * (moe_w4_workspace_tap: tap 1 is fp32 for any T where K = 1) and errors as moe_forward. One token
+ * (H <= 4096) runs as one grid of one CTA per SM whose CTAs exchange values, with the needs stated
+ * above for that. */
 moe_status moe_forward_w4(const moe_dims* d, const moe_w4_format* f, const void* x, const moe_weights* w,
                           const void* residual, void* out, void* workspace, size_t ws_bytes, void* stream);
 
@@ -266,6 +268,10 @@ moe_status moe_last_device_error(void* workspace, void* stream);
  *   tap 3  ids    [T, K] int32      tap 4  topk_w [T, K] fp32
  * Row strides are the widths given. Returns MOE_ERR_INVALID_ARG for an unknown tap. */
 moe_status moe_workspace_tap(const moe_dims* d, int tap, size_t* offset, size_t* bytes);
+
+/* The same after moe_forward_w4. Only tap 1 differs, and only where K = 1 and T >= 256: fp32, with
+ * the bytes of that. */
+moe_status moe_w4_workspace_tap(const moe_dims* d, int tap, size_t* offset, size_t* bytes);
 
 /* Load-balancing statistics of one routing call ("Qwen3.6-35B-A3B -- Architecture Overview",
  * MoE FFN: 256 Experts, Load Balancing: an auxiliary loss, coefficient 0.001, penalises uneven

@@ -40,6 +40,7 @@ from .binding import (  # noqa: F401
     moe_w4_pack,
     moe_w4_quantize,
     moe_w4_size,
+    moe_w4_workspace_tap,
     moe_workspace_init,
     moe_workspace_size,
     moe_workspace_tap,

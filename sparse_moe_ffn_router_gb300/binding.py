@@ -22,7 +22,7 @@ EXPORTED = ["moe_workspace_size", "moe_workspace_init", "moe_route", "moe_forwar
             "moe_last_device_error", "moe_workspace_tap", "moe_set_trace", "moe_launch_count", "moe_route_noalloc", "moe_status_string",
             "moe_router_stats", "moe_expert_shadow_size", "moe_forward_host_experts", "moe_forward_host_io",
             "moe_test_set_wait", "moe_w4_size", "moe_w4_quantize", "moe_w4_pack", "moe_w4_dequantize",
-            "moe_w4_linear_workspace_size", "moe_w4_linear", "moe_forward_w4"]
+            "moe_w4_linear_workspace_size", "moe_w4_linear", "moe_forward_w4", "moe_w4_workspace_tap"]
 KERNELS = {"router_scores": 0, "router_topk": 1, "dispatch_local": 2, "dispatch_scan": 3, "dispatch_scatter": 4,
            "gate_up": 5, "down": 6, "combine": 7, "rmsnorm": 8, "shared_gate": 9, "gather": 10, "gemm_plan": 11,
            "decode_fused": 12, "router_stats": 13, "fetch_experts": 14,
@@ -124,6 +124,8 @@ def load_library(build_if_missing: bool = True):
             lib.moe_last_device_error.argtypes = [P, P]
             lib.moe_workspace_tap.restype = st
             lib.moe_workspace_tap.argtypes = [D, ctypes.c_int, ctypes.POINTER(S), ctypes.POINTER(S)]
+            lib.moe_w4_workspace_tap.restype = st
+            lib.moe_w4_workspace_tap.argtypes = [D, ctypes.c_int, ctypes.POINTER(S), ctypes.POINTER(S)]
             lib.moe_set_trace.restype = st
             lib.moe_set_trace.argtypes = [ctypes.c_int, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.c_int]
             lib.moe_launch_count.restype = ctypes.c_uint64
@@ -548,4 +550,12 @@ def moe_workspace_tap(dims, tap: int) -> tuple[int, int]:
     off, nb = ctypes.c_size_t(), ctypes.c_size_t()
     _check(load_library().moe_workspace_tap(ctypes.byref(_dims(dims)), int(tap), ctypes.byref(off), ctypes.byref(nb)),
            "moe_workspace_tap")
+    return off.value, nb.value
+
+
+def moe_w4_workspace_tap(dims, tap: int) -> tuple[int, int]:
+    """moe_workspace_tap after moe_forward_w4 (tap 1 is fp32 for any T where K = 1)."""
+    off, nb = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load_library().moe_w4_workspace_tap(ctypes.byref(_dims(dims)), int(tap), ctypes.byref(off), ctypes.byref(nb)),
+           "moe_w4_workspace_tap")
     return off.value, nb.value

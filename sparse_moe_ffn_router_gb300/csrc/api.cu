@@ -77,10 +77,10 @@ int sm_count() {
     return cache[dev];
 }
 
-// Common validation of moe_route / moe_forward. On success fills the plan and the
-// workspace-backed fields of the argument block.
+// Common validation of moe_route / moe_forward / moe_forward_w4 (w4). On success fills the plan and
+// the workspace-backed fields of the argument block.
 moe_status prepare(const moe_dims* d, const void* x, const moe_weights* w, void* ws, size_t ws_bytes, Plan* p,
-                   LayerArgs* a) {
+                   LayerArgs* a, bool w4 = false) {
     if (!d || (d->flags & ~MOE_FLAG_BF16_SCORES)) return MOE_ERR_INVALID_ARG;
     if (!make_plan(*d, p)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (d->T == 0) return MOE_OK;
@@ -91,7 +91,7 @@ moe_status prepare(const moe_dims* d, const void* x, const moe_weights* w, void*
         !aligned16(w->down) || !aligned16(w->shared_gate_up) || !aligned16(w->shared_down) ||
         !aligned16(w->shared_gate) || (w->router_b && !aligned16(w->router_b)))
         return MOE_ERR_MISALIGNED;
-    if (ws_bytes < p->total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < (w4 ? p->total : p->need)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     memset(a, 0, sizeof *a);
     char* base = (char*)ws;
     a->flags = d->flags;
@@ -527,7 +527,7 @@ extern "C" moe_status moe_forward_w4(const moe_dims* d, const moe_w4_format* f, 
     if (!w4_format_known(f)) return MOE_ERR_INVALID_ARG;
     Plan p;
     LayerArgs a;
-    moe_status st = prepare(d, x, w, workspace, ws_bytes, &p, &a);
+    moe_status st = prepare(d, x, w, workspace, ws_bytes, &p, &a, true);
     if (st != MOE_OK) return st;
     if (d->I % f->group || d->Is % f->group) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (d->T == 0) return MOE_OK;
@@ -570,19 +570,27 @@ extern "C" moe_status moe_last_device_error(void* workspace, void* stream) {
     return (err & ERR_TIMEOUT) ? MOE_ERR_TIMEOUT : MOE_ERR_DEVICE;
 }
 
-extern "C" moe_status moe_workspace_tap(const moe_dims* d, int tap, size_t* offset, size_t* bytes) {
+static moe_status workspace_tap(const moe_dims* d, int tap, size_t* offset, size_t* bytes, bool w4) {
     Plan p;
     if (!d || !offset || !bytes) return MOE_ERR_INVALID_ARG;
     if (!make_plan(*d, &p)) return MOE_ERR_UNSUPPORTED_SHAPE;
     const size_t T = (size_t)d->T, P = (size_t)p.P;
     switch (tap) {
         case 0: *offset = p.o_h; *bytes = (P + T) * p.Imax * 2; return MOE_OK;
-        case 1: *offset = p.o_y; *bytes = T * (d->K + 1) * d->H * (p.gemm ? 2 : 4); return MOE_OK;
+        case 1: *offset = p.o_y; *bytes = w4 ? p.ybytes4 : p.ybytes; return MOE_OK;
         case 2: *offset = p.o_sgate; *bytes = T * 4; return MOE_OK;
         case 3: *offset = p.o_ids; *bytes = P * 4; return MOE_OK;
         case 4: *offset = p.o_topw; *bytes = P * 4; return MOE_OK;
         default: return MOE_ERR_INVALID_ARG;
     }
+}
+
+extern "C" moe_status moe_workspace_tap(const moe_dims* d, int tap, size_t* offset, size_t* bytes) {
+    return workspace_tap(d, tap, offset, bytes, false);
+}
+
+extern "C" moe_status moe_w4_workspace_tap(const moe_dims* d, int tap, size_t* offset, size_t* bytes) {
+    return workspace_tap(d, tap, offset, bytes, true);
 }
 
 extern "C" moe_status moe_set_trace(int kernel, void* const* start_events, void* const* stop_events, int n_events) {

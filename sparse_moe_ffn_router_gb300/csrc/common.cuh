@@ -70,7 +70,11 @@ struct Plan {
     int nb;          // token blocks of the dispatch
     bool gemm;       // many-token path (tensor-core GEMMs, bf16 Y) instead of weight streaming
     size_t o_hdr, o_logits, o_ids, o_topw, o_sgate, o_counts, o_offsets, o_perm, o_inv, o_lr, o_cntb, o_base,
-        o_act, o_h, o_y, o_upg, o_dng, o_upt, o_dnt, o_uprec, o_dlog, o_dh, o_dx, o_dh4, total;
+        o_act, o_h, o_y, o_upg, o_dng, o_upt, o_dnt, o_uprec, o_dlog, o_dh, o_dx, o_dh4,
+        total,    // bytes of the workspace
+        ybytes,   // of Y as the layer on bf16 weights writes it
+        ybytes4;  // of Y as the layer on 4-bit weights does (one expert a token: fp32 for any T)
+    size_t need;  // what the calls on bf16 weights use of total: the rest is the 4-bit layer's alone
 };
 
 constexpr int kStatsTokens = 32;     // tokens per block of the load-balancing statistics
@@ -108,10 +112,12 @@ inline bool make_plan(const moe_dims& d, Plan* p) {
     p->o_h = take((P + T) * p->Imax * 2);
     p->gemm = d.T >= kGemmMinTokens;
     // Y, which a statistics call borrows for its per-block partial sums (fp32 + int per expert)
-    // (K = 1: the 4-bit layer keeps Y in fp32 for any T)
-    const size_t ybytes = T * (d.K + 1) * d.H * (p->gemm && d.K > 1 ? 2 : 4);
+    p->ybytes = T * (d.K + 1) * d.H * (p->gemm ? 2 : 4);
+    p->ybytes4 = d.K == 1 ? T * 2 * d.H * 4 : p->ybytes;
     const size_t sbytes = (size_t)((d.T + kStatsTokens - 1) / kStatsTokens) * d.E * 8;
-    p->o_y = take(ybytes > sbytes ? ybytes : sbytes);
+    const size_t yneed = p->ybytes > sbytes ? p->ybytes : sbytes;
+    const bool grows = p->ybytes4 > yneed;  // (then Y lies last)
+    if (!grows) p->o_y = take(yneed);
     p->o_upg = take((size_t)(d.E + 1) * sizeof(GemmGroup));
     p->o_dng = take((size_t)(d.E + 1) * sizeof(GemmGroup));
     p->o_upt = take((size_t)(d.E + 2) * 4);
@@ -120,6 +126,13 @@ inline bool make_plan(const moe_dims& d, Plan* p) {
     p->o_dlog = take(d.T <= kRecTokens ? T * (size_t)(d.E + 1) * 8 : 0);
     p->o_dh = take(d.T <= kRecTokens ? (P + T) * (size_t)(p->Imax / 2) * 8 : 0);
     p->o_dx = take(d.T == 1 ? (size_t)(d.H / 2) * 8 : 0);  // the token row as tagged words (host rows)
+    if (grows) {
+        p->o_y = take(0);
+        p->need = align256(p->o_y + yneed);
+        take(p->ybytes4);
+    } else {
+        p->need = o;
+    }
     p->o_dh4 = take(d.T == 1 ? (P + T) * (size_t)(p->Imax / 2) * 8 : 0);  // h pairs (4-bit weights)
     p->total = o;
     return true;

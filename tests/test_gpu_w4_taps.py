@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 
 def tap(ws, dims, which, dtype, shape):
-    at, n = moe.moe_workspace_tap(dims, which)
+    at, n = moe.moe_w4_workspace_tap(dims, which)
     t = ws[at:at + n].view(dtype)
     assert t.numel() == torch.Size(shape).numel()
     return t.view(shape)
@@ -69,8 +69,7 @@ def test_one_expert_a_token_leaves_its_outputs(dims):
     L = W4Layer(dims, "int4", 64, seed=sum(dims), bias=True)
     T, H, E, K, I, Is = dims
     ws = moe.new_workspace(L.dims)
-    at = moe.moe_workspace_tap(L.dims, 1)[0]
-    y = ws[at:at + T * 2 * H * 4].view(torch.float32).view(T, 2, H)
+    y = tap(ws, L.dims, 1, torch.float32, (T, 2, H))
     first = None
     for _ in range(30):
         y.fill_(float("nan"))
@@ -82,6 +81,26 @@ def test_one_expert_a_token_leaves_its_outputs(dims):
             check(y, *st.outputs(L.dims, h, ids, w, g, W["down"], W["shared_down"][0], 0.0), "Y")
             first = y.clone()
         assert torch.equal(y, first)
+
+
+@pytest.mark.parametrize("dims", [(300, 512, 4, 1, 128, 64), (1, 2048, 64, 8, 512, 512)], ids=lambda v: "x".join(map(str, v)))
+def test_bf16_layer_leaves_the_rest_of_a_shorter_workspace_alone(dims):
+    """moe_forward on a workspace without the 4-bit layer's own part: same result, nothing behind it touched."""
+    T, H, E, K, I, Is = dims
+    L = W4Layer(dims, "int4", 64, seed=5, bias=True)
+    dense = [torch.empty(m[0].shape, dtype=torch.bfloat16, device="cuda") for m in L.m.values()]
+    for (k, w) in zip(L.m, dense):
+        moe.moe_w4_dequantize(ref.fmt("int4", 64), getattr(L.W, k), w, k.endswith("gate_up"))
+    W = moe.Weights(L.router_w, L.router_b, *dense, L.shared_gate)
+    torch.cuda.synchronize()
+    full = moe.new_workspace(dims)
+    want, out = torch.empty_like(L.x), torch.empty_like(L.x)
+    moe.moe_forward(dims, L.x, W, L.residual, want, full)
+    extra = T * 2 * H * 2 if T > 1 else (K + 1) * max(I, Is) // 2 * 8
+    ws = torch.zeros_like(full)
+    ws[-extra:] = 77
+    moe.moe_forward(dims, L.x, W, L.residual, out, ws[:-extra])
+    assert moe.moe_last_device_error(ws) == 0 and torch.equal(out, want) and bool((ws[-extra:] == 77).all())
 
 
 def test_linear_offsets_past_32_bits():

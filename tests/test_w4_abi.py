@@ -184,3 +184,33 @@ def test_forward_binding_checks_every_tensor():
             call(**{name: torch.zeros(1000, dtype=torch.uint8)})
     with pytest.raises(ValueError, match="GPU only"):  # everything fits: only the device is wrong
         call(router_b=None)
+
+
+@pytest.mark.parametrize("dims,extra", [((300, 512, 4, 1, 128, 64), 300 * 2 * 512 * 2), ((256, 2048, 8, 1, 64, 512), 256 * 2 * 2048 * 2),
+                                        ((1, 2048, 256, 8, 512, 512), 9 * 256 * 8), ((64, 2048, 256, 8, 512, 512), 0),
+                                        ((1000, 2048, 256, 8, 512, 512), 0), ((255, 512, 4, 1, 128, 64), 0)])
+def test_workspace_of_both_layers(lib, dims, extra):
+    """The 4-bit layer's own part of the workspace (fp32 Y of one expert a token, exchanged h pairs of one token) lies last and
+    is asked of that layer only; its tap 1 has the bytes that it writes."""
+    T, H, E, K, I, Is = dims
+    d, size = Dims(*dims), lib.moe_workspace_size(ctypes.byref(Dims(*dims)))
+    w = CWeights(*[None if f[0] == "router_b" else A for f in CWeights._fields_])
+
+    def bf16(nbytes):  # refused for the missing out once the workspace is large enough
+        return lib.moe_forward(ctypes.byref(d), A, ctypes.byref(w), None, None, A + 0x1000000, nbytes, None)
+
+    def w4(nbytes):
+        return lib.moe_forward_w4(ctypes.byref(d), F(), A, ctypes.byref(w), None, None, A + 0x1000000, nbytes, None)
+
+    assert bf16(size - extra) == 1 and bf16(size - extra - 1) == 4
+    assert w4(size) == 1 and w4(size - 1) == 4
+    for tap in (0, 2, 3, 4):
+        assert binding.moe_w4_workspace_tap(dims, tap) == binding.moe_workspace_tap(dims, tap)
+    (at, nb), (at4, nb4) = binding.moe_workspace_tap(dims, 1), binding.moe_w4_workspace_tap(dims, 1)
+    assert at == at4 and at % 256 == 0 and nb == T * (K + 1) * H * (4 if T < 256 else 2)
+    assert nb4 == T * (K + 1) * H * (4 if T < 256 or K == 1 else 2) and at4 + nb4 <= size
+    assert at + nb <= size - extra
+    with pytest.raises(binding.MoEError):
+        binding.moe_w4_workspace_tap(dims, 5)
+    with pytest.raises(binding.MoEError):
+        binding.moe_w4_workspace_tap((T, 100, E, K, I, Is), 1)
