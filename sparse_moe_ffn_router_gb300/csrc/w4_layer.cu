@@ -144,10 +144,12 @@ static cudaError_t w4_one(int format, int group, const W4OneArgs* p, cudaStream_
     }
 }
 
-// One token, strips of at most one stage (H <= 4096), sums that fit, one CTA per SM.
+// One token, strips of at most one stage (H <= 4096), h rows and sums that fit (then at least three stages do),
+// one CTA per SM.
 bool w4_one_supported(const LayerArgs& a, const moe_w4_format& f) {
-    return a.T == 1 && a.H <= kW4StageRecs * kW4Cols && a.K <= kOneMaxK && w4_one_strips(a, a.num_sms) <= kOneMaxUp && a.dlog &&
-           a.dh4 && w4_one(f.format, f.group, nullptr, nullptr) == cudaSuccess;
+    return a.T == 1 && a.H <= kW4StageRecs * kW4Cols && a.K <= kOneMaxK && a.Imax <= kOneMaxInner &&
+           w4_one_strips(a, a.num_sms) <= kOneMaxUp && a.dlog && a.dh4 &&
+           w4_one(f.format, f.group, nullptr, nullptr) == cudaSuccess;
 }
 
 // The whole layer of one token in one kernel.

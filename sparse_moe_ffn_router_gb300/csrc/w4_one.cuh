@@ -55,7 +55,6 @@ struct W4OneRoute {
     int ids[kOneMaxK];
     float w[kOneMaxK];
     float sg;
-    int ready;  // 1: complete (0 after a timeout: the indices are then those of expert 0)
 };
 
 template <int FMT, int G>
@@ -66,9 +65,11 @@ struct W4OneRing {
     static constexpr int kFixed = 128 + kPart + kYs + 256 + 256;
 };
 // Shared memory: stages, h rows [K + 1][Imax] bf16 (64 bytes apart modulo 128), the token row, sums.
-inline int w4_one_rows(int K, int Imax, int H) { return (K + 1) * (2 * Imax + 64) + 2 * H; }
+constexpr int w4_one_rows(int K, int Imax, int H) { return (K + 1) * (2 * Imax + 64) + 2 * H; }
 template <int FMT, int G>
 inline int w4_one_stages(int K, int Imax, int H) {
+    static_assert((kW4SmemMax - W4OneRing<FMT, G>::kFixed - w4_one_rows(kOneMaxK, kOneMaxInner, kW4StageRecs * kW4Cols)) / W4OneRing<FMT, G>::kStage >= 3,
+                  "stages beside the largest rows");
     const int n = (kW4SmemMax - W4OneRing<FMT, G>::kFixed - w4_one_rows(K, Imax, H)) / W4OneRing<FMT, G>::kStage;
     return n < 6 ? n : 6;
 }
@@ -248,7 +249,8 @@ __global__ void __launch_bounds__(kOneThreads, 1) k_w4_one(const __grid_constant
         mbar_init(routed, 1);
         fence_mbar_init();
     }
-    // every index read from the routing is in range even when a wait runs out before it is complete
+    // every index read from the routing is in range even when a wait runs out before it is complete (a routing
+    // whose own wait ran out ranks scores of 0 in the missing places)
     if (threadIdx.x < sizeof(W4OneRoute) / 4) reinterpret_cast<int*>(&rt)[threadIdx.x] = 0;
     __syncthreads();
     grid_dep_launch();  // the next kernel may be scheduled as this one's CTAs finish
@@ -343,8 +345,6 @@ __global__ void __launch_bounds__(kOneThreads, 1) k_w4_one(const __grid_constant
         __syncthreads();  // every thread has read the call's number
         if (lane == 0) red_release_add(&a.hdr->dec_start, 1u);
         w4o_route(a, rt, tag, lane, routed);
-        if (lane == 0) rt.ready = 1;
-        __syncwarp();
         asm volatile("bar.arrive 2, %0;" ::"n"(32 * (kW4Warps + 1)) : "memory");  // the weights and the gate are known
         if (cta == 0) {
             // the routing's results, for the workspace's taps
