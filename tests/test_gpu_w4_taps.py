@@ -7,7 +7,7 @@ import torch
 import sparse_moe_ffn_router_gb300 as moe
 from tests import w4_reference as ref
 from tests import w4_stages as st
-from tests.test_gpu_w4 import W4Layer, check
+from tests.test_gpu_w4 import W4Layer, check, run_linear
 
 pytestmark = pytest.mark.gpu
 
@@ -38,6 +38,67 @@ def check_activations(L, ws, ids, rounded=False):
     live = ~want.isnan()
     check(h[live], want[live], bound[live], "h")
     return h
+
+
+def check_stages(L, ws, out, residual):
+    """Every stage of the call that left ws and out: routing, h, Y and the sum."""
+    T, H, E, K, I, Is = L.dims
+    big = T >= 256
+    ids, w, g = check_routing(L, ws)
+    h = check_activations(L, ws, ids, rounded=big)
+    W = {k: st.weights(L.name, L.group, L.m[k], big) for k in ("down", "shared_down")}
+    half = big and K > 1
+    Y = tap(ws, L.dims, 1, torch.bfloat16 if half else torch.float32, (T, K + 1, H))
+    check(Y, *st.outputs(L.dims, h, ids, w, g, W["down"], W["shared_down"][0], ref.HALF if half else 0.0), "Y")
+    check(out, *st.combined(Y, L.residual if residual else None), "out")
+
+
+@pytest.mark.parametrize("dims,name,group", [
+    ((1, 2048, 64, 8, 512, 512), "int4", 64), ((1, 512, 4, 1, 128, 64), "e2m1", 32), ((1, 5120, 16, 4, 128, 128), "int4_zp", 128),
+    ((2, 512, 32, 4, 128, 128), "int4_zp", 64), ((7, 2048, 256, 8, 512, 512), "e2m1", 64), ((8, 8192, 8, 2, 64, 192), "int4", 32),
+    ((9, 640, 21, 5, 192, 448), "int4", 64), ((64, 2048, 64, 8, 512, 512), "int4_zp", 128), ((130, 384, 3, 3, 2048, 64), "e2m1", 32),
+    ((255, 512, 16, 2, 128, 2048), "int4", 64), ((255, 128, 1, 1, 64, 64), "int4", 32),
+    ((256, 512, 32, 4, 128, 128), "int4", 32), ((300, 2048, 32, 8, 512, 512), "e2m1", 64), ((777, 640, 11, 3, 192, 320), "int4_zp", 64),
+    ((1000, 128, 8, 2, 64, 64), "int4", 32), ((512, 2304, 9, 8, 576, 128), "e2m1", 32), ((300, 512, 4, 1, 128, 64), "e2m1", 64),
+    ((2000, 640, 64, 2, 64, 192), "int4_zp", 64), ((1500, 256, 24, 3, 64, 704), "int4", 64), ((260, 8192, 6, 2, 2048, 1024), "int4_zp", 128),
+    ((4096, 2048, 256, 8, 512, 512), "int4", 64)],
+    ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else str(v))
+def test_layer_stage_by_stage(dims, name, group):
+    L = W4Layer(dims, name, group, seed=sum(dims) + 1, bias=dims[0] % 2 == 0)
+    ws = moe.new_workspace(L.dims)
+    for residual in (True, False):
+        for which in (0, 1):
+            at, n = moe.moe_w4_workspace_tap(L.dims, which)
+            ws[at:at + n] = 255
+        check_stages(L, ws, L.run(residual=residual, ws=ws), residual)
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("name,group", [("int4", 128), ("int4_zp", 32), ("e2m1", 64)])
+@pytest.mark.parametrize("T,N,K", [(64, 1000, 1024), (70, 129, 128), (129, 257, 640), (190, 512, 2048), (300, 384, 512), (1000, 130, 256)])
+def test_linear_that_does_not_round_its_weights(name, group, T, N, K):
+    """The streaming path's larger token counts, by the bound without a rounding of the weights."""
+    assert not ref.linear_rounds(T, N, sms())
+    x, w, b, out = run_linear(name, group, T, N, K, bias=N % 2 == 0, seed=3)
+    check(out, *ref.linear(x, w, b))
+
+
+@pytest.mark.parametrize("name,group,cols", [(f, 32, c) for f in ref.FORMATS for c in (32, 96, 160)] + [("int4", 64, 64), ("int4_zp", 64, 1984), ("e2m1", 128, 2048)])
+@pytest.mark.parametrize("T,N", [(3000, 640), (9, 24001)])
+def test_linear_on_rounded_weights(name, group, cols, T, N):
+    """The tensor-core path's weights are s * v rounded to bf16: by the bound of the sums alone, also with columns that
+    are no whole record or half of one."""
+    assert ref.linear_rounds(T, N, sms())
+    m = ref.matrices(name, group, 1, N, cols, seed=cols)
+    x = torch.randn(T, cols, device="cuda").to(torch.bfloat16)
+    f = ref.fmt(name, group)
+    ws, out = moe.new_w4_linear_workspace(f, T, N, cols), torch.full((T, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    moe.moe_w4_linear(f, x, ref.pack(name, group, m), None, out, ws)
+    assert moe.moe_last_device_error(ws) == 0
+    check(out, *ref.linear(x, st.weights(name, group, m, True)[0], None))
 
 
 @pytest.mark.parametrize("dims,name,group", [((1, 512, 32, 4, 128, 128), "int4", 32), ((1, 1024, 64, 2, 512, 64), "e2m1", 64),
