@@ -211,7 +211,7 @@ __device__ __forceinline__ void w4_load_row(const uint8_t* rec, int r, W4Row<FMT
 }
 
 // Decodes a row's 128 weights into 64 TMEM columns of this thread's lane: bf16(s * v / kUnfold), the factor (a
-// power of two) undone on the sums.
+// power of two) undone on the sums. (A quarter of a weight below 2^-124 is subnormal and keeps fewer bits.)
 template <int FMT, int G>
 __device__ __forceinline__ void w4_row_to_tmem(const W4Row<FMT, G>& f, uint32_t taddr) {
 #pragma unroll

@@ -180,3 +180,26 @@ def test_linear_offsets_past_32_bits():
     check(out[rows], *ref.linear(x[rows], w, None))
     out[rows] = 0
     assert all(not bool(part.any()) for part in out.split(1 << 24))
+
+
+@pytest.mark.parametrize("name,group", [("int4", 32), ("int4_zp", 64), ("e2m1", 128)])
+@pytest.mark.parametrize("T", [3, 3000])
+def test_linear_smallest_scales(name, group, T):
+    """Scales from the smallest subnormal bf16 to 2^-118 by token rows of 2^110: the streaming path multiplies by s * v, the
+    tensor-core path by s * v rounded to bf16, which for integer codes is rounded at a quarter of its size."""
+    N, K = 640, 256
+    codes, _, zeros = ref.matrices(name, group, 1, N, K, seed=2)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    bits = torch.randint(1, 9 << 7, (1, N, K // group), generator=g, device="cuda")  # 2^-133 .. 2^-118
+    m = codes, bits.to(torch.int16).view(torch.bfloat16), zeros
+    x = (torch.randn(T, K, generator=g, device="cuda") * 2.0 ** 110).to(torch.bfloat16)
+    f = ref.fmt(name, group)
+    ws, out = moe.new_w4_linear_workspace(f, T, N, K), torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    moe.moe_w4_linear(f, x, ref.pack(name, group, m), None, out, ws)
+    assert moe.moe_last_device_error(ws) == 0
+    w = ref.values(name, group, m)[0]
+    if ref.linear_rounds(T, N, sms()):
+        part = 1.0 if name == "e2m1" else 4.0
+        w = (w / part).float().to(torch.bfloat16).double() * part
+    assert ref.linear_rounds(T, N, sms()) == (T == 3000)
+    check(out, *ref.linear(x, w, None))
