@@ -35,7 +35,8 @@
  * One token at the pages' layer shape (H = 2048, I = Is = 512, T = 1) runs as one grid of one
  * CTA per SM whose CTAs exchange values with one another, so it needs every SM at once:
  * kernels on other streams that hold SMs longer than the wait limit (about 1 s) make the
- * call end with MOE_ERR_TIMEOUT in the workspace's error word rather than wait for them.
+ * call end with MOE_ERR_TIMEOUT in the workspace's error word rather than wait for them (two such
+ * calls in flight on two streams can each hold SMs that the other needs: put them on one stream).
  * Results are deterministic: the same inputs give bit-identical outputs on every call.
  */
 #ifndef MOE_GB300_H
@@ -175,7 +176,8 @@ moe_status moe_forward_host_experts(const moe_dims* d, const void* x, const moe_
  *                                                       (sign: bit 3 of the code)
  * group is 32, 64 or 128 and divides cols.
  * Products use v exactly and apply the scale to each group's fp32 sum in fp32. The tensor-core
- * paths multiply by s * v rounded once to bf16: the layer from 256 tokens; the linear layer where
+ * paths multiply by s * v rounded once to bf16 (INT4, INT4_ZP: below 2^-124 to a multiple of 2^-131,
+ * as the rounding is of a quarter of it): the layer from 256 tokens; the linear layer where
  * ceil(T / 8) * ceil(N / 16) is more than 14 times the SMs times the waves (tiles of 128 tokens by
  * 256 rows, an SM each).
  * Packed form (moe_w4_size bytes, 16-byte aligned): matrices one after another, each a sequence
@@ -222,7 +224,8 @@ moe_status moe_w4_quantize(const moe_w4_format* f, int32_t n, int32_t rows, int3
 moe_status moe_w4_pack(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols, int32_t layout, const void* codes,
                        const void* scales, const void* zeros, void* packed, size_t packed_bytes, void* stream);
 
-/* The weights a packed form stands for: w [n, rows, cols] bf16, s * v rounded once. */
+/* The weights a packed form stands for: w [n, rows, cols] bf16, s * v rounded once. (moe_forward on
+ * w: after other work, as the ordering rule above asks of any kernel that writes weights.) */
 moe_status moe_w4_dequantize(const moe_w4_format* f, int32_t n, int32_t rows, int32_t cols, int32_t layout,
                              const void* packed, size_t packed_bytes, void* w, void* stream);
 
@@ -325,16 +328,16 @@ uint64_t moe_launch_count(void);
 
 /* Testing aid for the bounded-wait path (the paper has no counterpart). Every wait of the
  * one-token kernel (moe_forward with T = 1 at the page's layer shape) and of the streaming
- * expert kernels (2 <= T < 256) gives up after a time limit, sets MOE_ERR_TIMEOUT in the
+ * expert kernels (2 <= T < 256), and every wait of the kernels on 4-bit weights, gives up after a time limit, sets MOE_ERR_TIMEOUT in the
  * workspace's error word and lets the kernel run to its end with in-range indices; the calls
  * after a timeout need moe_workspace_init on that workspace. This sets, process-wide and for
  * the calls made after it returns:
  *   wait_ns   the time limit of those waits in nanoseconds; 0 restores the default (~1 s);
  *             at most 10 s;
  *   suppress  0 in normal use, or one signal to hold back so that a wait runs out:
- *             MOE_TEST_SUPPRESS_SCORE  CTA 1 of the one-token kernel does not publish its
+ *             MOE_TEST_SUPPRESS_SCORE  CTA 1 of the one-token kernels does not publish its
  *                                      router scores (every CTA's wait for the scores runs out);
- *             MOE_TEST_SUPPRESS_STAGE  CTA 0 of the streaming gate_up kernel (9 <= T < 256)
+ *             MOE_TEST_SUPPRESS_STAGE  CTA 0 of moe_forward's streaming gate_up kernel (9 <= T < 256)
  *                                      never loads its first ring stage (its consumers' wait
  *                                      on the stage's mbarrier runs out).
  * Results of calls made while a signal is held back are meaningless; no call faults, traps or

@@ -3,11 +3,11 @@
 //
 // All three pass over the data once: quantising reads 2 bytes and writes 0.52 to 0.59 bytes a weight,
 // dequantising the reverse. Writing out is bound by HBM (256 matrices of 1024 x 2048: 233 us, 5.7 TB/s);
-// quantising (the same bank: 275 us, 4.8 TB/s) by its ~14 instructions a weight, so each is counted: quotients
-// by a reciprocal and one correction step instead of a division, packed maxima, the hardware's E2M1
-// rounding, no division to find a record. A warp takes one record (16 rows by 128
-// columns): lane 4g + t holds, of rows g and g + 8, the columns 32 c + 8 t + 0 .. 7 of every
-// 32-column piece c -- the order of the packed words, so its codes leave as two 16-byte stores
+// quantising (the same bank with E2M1 codes per 32: 280 us, 4.8 TB/s; INT4 per 64: 226 us) by its ~13
+// instructions a weight, so each is counted: quotients by a reciprocal and one correction step instead of
+// a division, packed maxima, the hardware's E2M1 rounding, no division to find a record. A warp takes one
+// record (16 rows by 128 columns): lane 4g + t holds, of rows g and g + 8, the columns 32 c + 8 t + 0 .. 7
+// of every 32-column piece c -- the order of the packed words, so its codes leave as two 16-byte stores
 // that the warp makes contiguous, and its weights come in 16 bytes a piece, four lanes to a
 // 64-byte run of a row. A group's largest weight is a maximum over the lane's 8 values and the
 // four lanes of a row (two shuffles).
