@@ -203,3 +203,65 @@ def test_linear_smallest_scales(name, group, T):
         w = (w / part).float().to(torch.bfloat16).double() * part
     assert ref.linear_rounds(T, N, sms()) == (T == 3000)
     check(out, *ref.linear(x, w, None))
+
+
+@pytest.mark.parametrize("flags", [0, moe.FLAG_BF16_SCORES])
+@pytest.mark.parametrize("T", [1, 5, 8, 40, 300])
+def test_layer_routing_with_equal_scores(T, flags):
+    """Scores that are exact in fp32 (sums of sixteenths), many of them equal, more so when rounded to bf16: the lower
+    expert comes first, and every stage follows."""
+    dims = (T, 512, 32, 4, 128, 64)
+    L = W4Layer(dims, "int4", 32, seed=T, bias=True)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    draw = lambda low, high, *shape: torch.randint(low, high, shape, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    L.x, L.router_w, L.router_b = draw(-1, 2, T, 512), draw(-8, 9, 32, 512) / 16, draw(-2, 3, 32)
+    L.W = moe.Weights(L.router_w, L.router_b, L.W.gate_up, L.W.down, L.W.shared_gate_up, L.W.shared_down, L.shared_gate)
+    score = L.x.double() @ L.router_w.double().T + L.router_b.double()
+    assert float(score.abs().max()) * 16 < 1 << 24
+    if flags:
+        score = score.float().to(torch.bfloat16).double()
+    top = score.sort(dim=1, descending=True, stable=True)
+    assert T < 40 or bool((top.values[:, :4] == top.values[:, 1:5]).any())
+    ws, out = moe.new_workspace(dims), torch.empty_like(L.x)
+    moe.moe_forward_w4((*dims, flags), ref.fmt("int4", 32), L.x, L.W, L.residual, out, ws)
+    assert moe.moe_last_device_error(ws) == 0
+    ids, w = tap(ws, dims, 3, torch.int32, (T, 4)), tap(ws, dims, 4, torch.float32, (T, 4))
+    assert torch.equal(ids.long(), top.indices[:, :4])
+    want = torch.softmax(top.values[:, :4], 1)
+    # exact differences of scores; expf, three additions and the division: a few fp32 steps
+    check(w, want, 2.0 ** -20 * want + 1e-30, "routing weights")
+    check_activations(L, ws, ids, rounded=T >= 256)
+
+
+@pytest.mark.parametrize("T", [1, 8, 40, 300])
+def test_layer_of_large_activations(T):
+    """Gate values far into both tails of the sigmoid, where its exponential overflows."""
+    L = W4Layer((T, 512, 16, 2, 128, 128), "int4", 32, seed=T)
+    L.x = (L.x.float() * 96).to(torch.bfloat16)
+    ids = st.routing(L.x, L.router_w, L.router_b, L.shared_gate, 2)[0]
+    gate = L.x.double() @ st.weights("int4", 32, L.m["shared_gate_up"], False)[0, :128].T
+    assert float(gate.min()) < -90 and float(gate.max()) > 90
+    ws = moe.new_workspace(L.dims)
+    out = L.run(ws=ws)
+    assert torch.equal(tap(ws, L.dims, 3, torch.int32, (T, 2)).long(), ids) and bool(out.isfinite().all())
+    check_activations(L, ws, ids, rounded=T >= 256)
+
+
+def test_layers_on_two_streams_at_once():
+    """Layers of two tokens and more in flight together, each with its own workspace and output."""
+    layers = [W4Layer((T, 2048, 32, 8, 512, 512), "int4", 64, seed=T) for T in (2, 8, 40, 300)]
+    f = ref.fmt("int4", 64)
+    spaces = [[moe.new_workspace(L.dims) for L in layers] for _ in range(2)]
+    outs = [[torch.empty_like(L.x) for L in layers] for _ in range(2)]
+    alone = [L.run() for L in layers]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            for j in (range(4) if i == 0 else reversed(range(4))):
+                L = layers[j]
+                moe.moe_forward_w4(L.dims, f, L.x, L.W, L.residual, outs[i][j], spaces[i][j], s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for j in range(4):
+            assert moe.moe_last_device_error(spaces[i][j]) == 0 and torch.equal(outs[i][j], alone[j])
