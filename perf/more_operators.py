@@ -238,14 +238,13 @@ def prepare(case, seed):
     if own:  # what a program makes once: sizes as one object, workspaces
         import sparse_moe_ffn_router_gb300 as moe
         types = {"bf16": moe.BF16, "fp16": moe.FP16, "fp32": moe.FP32}
-        if c["kind"] == "dispatch":
-            s["workspace"] = moe.new_sort_workspace(T, c["top"], c["E"])
         if c["kind"] in ("norm", "norm_backward"):
             s["dims"] = moe.NormDims(T, c["H"], dtype=types[c["dtype"]], post=c["post"],
                                      gate={"none": moe.GATE_NONE, "token": moe.GATE_TOKEN, "channel": moe.GATE_CHANNEL, "full": moe.GATE_FULL}[c["gate"]],
                                      gate_act={"none": moe.ACT_NONE, "sigmoid": moe.ACT_SIGMOID, "silu": moe.ACT_SILU}[c["gate_act"]],
                                      eps=EPS, branch_scale=c["branch"], residual_scale=c["keep"])
-            s["workspace"] = moe.new_norm_workspace(s["dims"])
+            if c["kind"] == "norm_backward":
+                s["workspace"] = moe.new_norm_workspace(s["dims"])
         if c["kind"] in ("linear", "linear_backward"):
             act = {"none": moe.ACT_NONE, "relu": moe.ACT_RELU, "silu": moe.ACT_SILU, "gelu": moe.ACT_GELU, "swiglu": moe.ACT_SWIGLU}[c["act"]]
             s["dims"] = moe.LinearDims(_rows(c), c["N"], c["K"], E=max(1, c["E"]), act=act, dtype=types[c["dtype"]])
@@ -268,7 +267,7 @@ def _dispatch(s):
         import sparse_moe_ffn_router_gb300 as moe
         counts, offsets = (torch.empty(n, dtype=torch.int32, device=DEV) for n in (c["E"], c["E"] + 1))
         perm, inv = (torch.empty(P, dtype=torch.int32, device=DEV) for _ in range(2))
-        moe.moe_sort_pairs(c["E"], s["ids"], counts, offsets, perm, inv, s["workspace"])
+        moe.moe_sort_pairs(c["E"], s["ids"], counts, offsets, perm, inv)
         moe.moe_dispatch(x, inv, w, s["filled"])
         return {"counts": counts, "offsets": offsets, "perm": perm, "inv": inv, "rows": s["filled"]}
     counts, offsets, perm, inv = _order(s["ids"], c["E"])
