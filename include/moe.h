@@ -257,6 +257,115 @@ moe_status moe_forward_w4(const moe_dims* d, const moe_w4_format* f, const void*
  * Uses d->T and d->H only. gamma [H] bf16 may be NULL (all ones). xn must not overlap x. */
 moe_status moe_rmsnorm(const moe_dims* d, const void* x, const void* gamma, float eps, void* xn, void* stream);
 
+/* ---- Parts of the layer, with gradients -----------------------------------------------------
+ * The same layer put together from parts, for training and for experts of another kind: rows to
+ * their experts and back, the experts' products, and the norms around the block (the pages describe
+ * the forward layer alone; these have no counterpart there). All of them are asynchronous on
+ * `stream`, read every argument after the previous kernel on it is complete, allocate nothing, and
+ * give the same bits on every call. Tensors are contiguous, 16-byte aligned unless stated otherwise.
+ * Results that a call does not name as optional are written in full; inputs are only read. */
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype;
+/* Activations. GELU is z * Phi(z), Phi the normal distribution function; SWIGLU is silu(gate) * up. */
+typedef enum {
+    MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_SIGMOID = 4, MOE_ACT_SWIGLU = 5
+} moe_act;
+
+/* The dispatch of given expert ids [T, K] (moe_route's, or any other router's): a stable sort of the pairs
+ * p = t*K + k by expert. An id outside [0, E) drops its slot.
+ *   counts [E], offsets [E+1]  pairs of each expert and their exclusive prefix sum
+ *   perm [T*K]                 pairs in order of (expert, t, k); -1 from offsets[E] on
+ *   inv [T*K]                  place of pair p in perm; -1 for a dropped slot
+ * For ids of moe_route, counts, offsets and perm are moe_route's. 1 <= K <= 8, 1 <= E <= 256, T * K < 2^31;
+ * T = 0 gives zeros. A token may name an expert twice. Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE,
+ * MOE_ERR_MISALIGNED. */
+moe_status moe_sort_pairs(int32_t T, int32_t K, int32_t E, const int32_t* ids, int32_t* counts, int32_t* offsets,
+                          int32_t* perm, int32_t* inv, void* stream);
+
+/* Token rows to their experts and back, weights applied on either way, and the gradients. x, out, dout, dx,
+ * residual are [T, H]; rows, drows [T*K, H] in the order of perm; topk_w, dtopk_w [T, K] fp32; inv of moe_sort_pairs.
+ *   moe_dispatch           rows[inv[p]] = topk_w[p] * x[t]        (topk_w NULL: the rows as they are)
+ *   moe_dispatch_backward  dx[t] = sum_k topk_w[p] * drows[inv[p]];  dtopk_w[p] = x[t] . drows[inv[p]]
+ *   moe_combine            out[t] = residual[t] + sum_k topk_w[p] * rows[inv[p]]   (residual, topk_w optional)
+ *   moe_combine_backward   drows[inv[p]] = topk_w[p] * dout[t];      dtopk_w[p] = dout[t] . rows[inv[p]]
+ * (the gradient of residual is dout). dtopk_w is optional, and x and rows of the backward calls are read for it
+ * alone (NULL without it). Dropped slots give and receive nothing: their dtopk_w is 0, and rows that no pair has as
+ * its place are left as they were. Sums are in fp32 in slot order, dots in fp32, each result rounded once.
+ * out may be the same buffer as residual; otherwise results overlap no input. An entry of inv that is no place
+ * in [0, T*K) counts as dropped. dtype: bf16, fp16 or fp32; 1 <= K <= 8, 1 <= H <= 65536, T * K < 2^31;
+ * rows move fastest where H elements are a multiple of 16 bytes. T = 0 is a no-op. */
+moe_status moe_dispatch(int32_t dtype, int32_t T, int32_t K, int32_t H, const void* x, const int32_t* inv,
+                        const float* topk_w, void* rows, void* stream);
+moe_status moe_dispatch_backward(int32_t dtype, int32_t T, int32_t K, int32_t H, const void* drows, const int32_t* inv,
+                                 const float* topk_w, const void* x, void* dx, float* dtopk_w, void* stream);
+moe_status moe_combine(int32_t dtype, int32_t T, int32_t K, int32_t H, const void* rows, const int32_t* inv,
+                       const float* topk_w, const void* residual, void* out, void* stream);
+moe_status moe_combine_backward(int32_t dtype, int32_t T, int32_t K, int32_t H, const void* dout, const int32_t* inv,
+                                const float* topk_w, const void* rows, void* drows, float* dtopk_w, void* stream);
+
+/* Linear layers with bias, activation and residual: one matrix for all T rows (E = 1, offsets NULL), or the
+ * experts' products (offsets [E+1] of moe_route or moe_sort_pairs, on the device): rows offsets[e] ..
+ * offsets[e+1] - 1 of x go through matrix e.
+ *   z   = x . W_e^T + bias_e           x [T, K], w [E, N, K], bias [E, N] or NULL
+ *   out = act(z) + residual            out, residual [T, No]: No = N, or N/2 for SWIGLU, whose W has the gate
+ *                                      rows [0, N/2) and the up rows [N/2, N) of moe_weights' gate_up
+ *   z [T, N] is stored too when z is not NULL (what the backward pass reads).
+ * Backward, for dout [T, No] and the z of the forward pass (NULL when act is NONE):
+ *   dz = act'(z) * dout;  dx = dz . W_e;  dw_e = dz^T . x and dbias_e = sum of dz, over expert e's rows
+ * (zeros for an expert without rows); the gradient of residual is dout. Each of dx, dw, dbias is optional (NULL);
+ * w is read for dx alone, x for dw alone. Rows from offsets[E] on are not read into any result and are left as they were
+ * in out, z and dx.
+ * dtype: bf16 or fp16, all tensors. Products accumulate in fp32, bias, activation and residual are applied in fp32,
+ * results are rounded once; dz is rounded to dtype before the products of the backward pass (dbias sums it before).
+ * Bounds: 1 <= N <= 2^20, 8 <= K <= 2^20 with K % 8 == 0, N % 32 == 0 for SWIGLU, 1 <= E <= 256, 0 <= T <= 2^31 - 256,
+ * T*N, T*K, E*N*K < 2^40. bias and dbias are 2-byte aligned. out may be the same buffer as residual; otherwise results
+ * overlap nothing. The workspace (moe_linear_workspace_size bytes; backward: nonzero for moe_linear_backward) is
+ * zero-filled once (moe_workspace_init); calls that may overlap in time need one each. Offsets that
+ * fall or leave [0, T] are cut to that range and set MOE_ERR_DEVICE for moe_last_device_error; waits that run out set
+ * MOE_ERR_TIMEOUT. T = 0 is a no-op for moe_linear; moe_linear_backward then writes zeros to dw and dbias. */
+typedef struct {
+    int32_t T, N, K, E;
+    int32_t act;   /* moe_act */
+    int32_t dtype; /* moe_dtype: MOE_BF16 or MOE_FP16 */
+} moe_linear_dims;
+size_t moe_linear_workspace_size(const moe_linear_dims* d, int32_t backward);
+moe_status moe_linear(const moe_linear_dims* d, const void* x, const void* w, const void* bias, const int32_t* offsets,
+                      const void* residual, void* out, void* z, void* workspace, size_t ws_bytes, void* stream);
+moe_status moe_linear_backward(const moe_linear_dims* d, const void* x, const void* w, const int32_t* offsets,
+                               const void* z, const void* dout, void* dx, void* dw, void* dbias, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/* The norms before and after a block with its gate and residual scale: y is a block's output, residual the stream
+ * it is added to, s the stream after it, xn what the next block reads. N(v; g) = v / sqrt(mean(v^2) + eps) * g.
+ *   s  = residual_scale * residual + branch_scale * act(gate) * n,   n = N(y; gamma_post) with MOE_NORM_POST, else y
+ *   xn = N(s; gamma_pre)                                             (of s before its rounding)
+ * y, residual, s, xn [T, H]; gamma_post, gamma_pre [H] or NULL (ones); residual may be NULL (none), and s or xn,
+ * not both. gate: none, one number a token [T], one a channel [H], or one an element [T, H]; gate_act NONE,
+ * SIGMOID or SILU (of the gate).
+ * Backward: ds and dxn are the gradients of s and xn (either may be NULL: none), s and y the forward pass's (s is read
+ * for dxn alone). Results, each optional: dresidual, dy [T, H], dgate (as gate), dgamma_post, dgamma_pre [H].
+ * dgamma_pre needs dxn, dgamma_post MOE_NORM_POST, dgate a gate.
+ * dtype: bf16, fp16 or fp32, all tensors; arithmetic and sums in fp32, one rounding a result. 1 <= H <= 8192, T >= 0.
+ * s and xn may be the buffers of y or residual (and dresidual and dy those of ds, dxn, s or y), each as a whole; results
+ * overlap nothing else. The backward workspace (moe_norm_workspace_size bytes) need not be zero-filled; calls
+ * that may overlap in time need one each. T = 0 is a no-op, or writes zeros to the [H] gradients. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2, MOE_GATE_FULL = 3 } moe_gate;
+#define MOE_NORM_POST 1
+typedef struct {
+    int32_t T, H;
+    int32_t dtype;    /* moe_dtype */
+    int32_t gate;     /* moe_gate */
+    int32_t gate_act; /* moe_act */
+    int32_t flags;    /* 0 or MOE_NORM_POST */
+    float eps, branch_scale, residual_scale;
+} moe_norm_dims;
+size_t moe_norm_workspace_size(const moe_norm_dims* d);
+moe_status moe_norm_residual(const moe_norm_dims* d, const void* y, const void* residual, const void* gate,
+                             const void* gamma_post, const void* gamma_pre, void* s, void* xn, void* stream);
+moe_status moe_norm_residual_backward(const moe_norm_dims* d, const void* ds, const void* dxn, const void* s,
+                                      const void* y, const void* gate, const void* gamma_post, const void* gamma_pre,
+                                      void* dresidual, void* dy, void* dgate, void* dgamma_post, void* dgamma_pre,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, then read and clear the device error word kept in `workspace`:
  * MOE_OK, MOE_ERR_DEVICE (a kernel saw a non-finite router score) or MOE_ERR_TIMEOUT. */
 moe_status moe_last_device_error(void* workspace, void* stream);
@@ -313,7 +422,14 @@ enum {
     MOE_KERNEL_W4_PACK = 16,        /* quantising, packing, dequantising 4-bit weights */
     MOE_KERNEL_W4_LINEAR = 17,      /* moe_w4_linear                                */
     MOE_KERNEL_W4_FUSED = 18,       /* whole layer on 4-bit weights in one kernel (T = 1) */
-    MOE_KERNEL_COUNT = 19
+    MOE_KERNEL_SORT_PAIRS = 19,     /* moe_sort_pairs                               */
+    MOE_KERNEL_SPREAD_ROWS = 20,    /* moe_dispatch, moe_combine_backward           */
+    MOE_KERNEL_GATHER_ROWS = 21,    /* moe_combine, moe_dispatch_backward           */
+    MOE_KERNEL_LINEAR = 22,         /* moe_linear                                   */
+    MOE_KERNEL_LINEAR_BACKWARD = 23,/* moe_linear_backward, all of its kernels      */
+    MOE_KERNEL_NORM = 24,           /* moe_norm_residual                            */
+    MOE_KERNEL_NORM_BACKWARD = 25,  /* moe_norm_residual_backward, both its kernels */
+    MOE_KERNEL_COUNT = 26
 };
 
 /* Benchmarking aid. While set, every launch of `kernel` made by this library records
@@ -328,7 +444,7 @@ uint64_t moe_launch_count(void);
 
 /* Testing aid for the bounded-wait path (the paper has no counterpart). Every wait of the
  * one-token kernel (moe_forward with T = 1 at the page's layer shape) and of the streaming
- * expert kernels (2 <= T < 256), and every wait of the kernels on 4-bit weights, gives up after a time limit, sets MOE_ERR_TIMEOUT in the
+ * expert kernels (2 <= T < 256), and every wait of the kernels on 4-bit weights and of moe_linear's, gives up after a time limit, sets MOE_ERR_TIMEOUT in the
  * workspace's error word and lets the kernel run to its end with in-range indices; the calls
  * after a timeout need moe_workspace_init on that workspace. This sets, process-wide and for
  * the calls made after it returns:
@@ -339,7 +455,8 @@ uint64_t moe_launch_count(void);
  *                                      router scores (every CTA's wait for the scores runs out);
  *             MOE_TEST_SUPPRESS_STAGE  CTA 0 of moe_forward's streaming gate_up kernel (9 <= T < 256)
  *                                      never loads its first ring stage (its consumers' wait
- *                                      on the stage's mbarrier runs out).
+ *                                      on the stage's mbarrier runs out); nor does that of
+ *                                      moe_linear's kernel.
  * Results of calls made while a signal is held back are meaningless; no call faults, traps or
  * hangs. Returns MOE_ERR_INVALID_ARG for another suppress value or wait_ns above 10 s. Not
  * thread-safe with concurrent calls of the library. */

@@ -22,12 +22,15 @@ EXPORTED = ["moe_workspace_size", "moe_workspace_init", "moe_route", "moe_forwar
             "moe_last_device_error", "moe_workspace_tap", "moe_set_trace", "moe_launch_count", "moe_route_noalloc", "moe_status_string",
             "moe_router_stats", "moe_expert_shadow_size", "moe_forward_host_experts", "moe_forward_host_io",
             "moe_test_set_wait", "moe_w4_size", "moe_w4_quantize", "moe_w4_pack", "moe_w4_dequantize",
-            "moe_w4_linear_workspace_size", "moe_w4_linear", "moe_forward_w4", "moe_w4_workspace_tap"]
+            "moe_w4_linear_workspace_size", "moe_w4_linear", "moe_forward_w4", "moe_w4_workspace_tap", "moe_sort_pairs",
+            "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward", "moe_linear_workspace_size", "moe_linear",
+            "moe_linear_backward", "moe_norm_workspace_size", "moe_norm_residual", "moe_norm_residual_backward"]
 KERNELS = {"router_scores": 0, "router_topk": 1, "dispatch_local": 2, "dispatch_scan": 3, "dispatch_scatter": 4,
            "gate_up": 5, "down": 6, "combine": 7, "rmsnorm": 8, "shared_gate": 9, "gather": 10, "gemm_plan": 11,
            "decode_fused": 12, "router_stats": 13, "fetch_experts": 14,
            "copy_rows": 15, "w4_pack": 16, "w4_linear": 17,
-           "w4_fused": 18}
+           "w4_fused": 18, "sort_pairs": 19, "spread_rows": 20, "gather_rows": 21, "linear": 22, "linear_backward": 23,
+           "norm": 24, "norm_backward": 25}
 
 
 # moe_dims.flags: router and shared-gate scores rounded to bf16 before ranking and sigmoid
@@ -54,6 +57,33 @@ class Dims(ctypes.Structure):
     """moe_dims; a dims tuple is (T, H, E, K, I, Is) or (T, H, E, K, I, Is, flags)."""
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("E", ctypes.c_int32),
                 ("K", ctypes.c_int32), ("I", ctypes.c_int32), ("Is", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+# moe_dtype, moe_act and moe_gate
+BF16, FP16, FP32 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_SIGMOID, ACT_SWIGLU = range(6)
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_FULL = range(4)
+NORM_POST = 1
+_TORCH = {BF16: torch.bfloat16, FP16: torch.float16, FP32: torch.float32}
+_DTYPE = {v: k for k, v in _TORCH.items()}
+
+
+class LinearDims(ctypes.Structure):
+    """moe_linear_dims: T rows of K columns through one matrix [N, K], or through E of them by the rows' expert."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "N", "K", "E", "act", "dtype")]
+
+    def __init__(self, T, N, K, E=1, act=ACT_NONE, dtype=BF16):
+        super().__init__(int(T), int(N), int(K), int(E), int(act), int(dtype))
+
+
+class NormDims(ctypes.Structure):
+    """moe_norm_dims: T rows of H columns; gate: GATE_*, gate_act: ACT_NONE, ACT_SIGMOID or ACT_SILU of it."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "dtype", "gate", "gate_act", "flags")] + [
+        (n, ctypes.c_float) for n in ("eps", "branch_scale", "residual_scale")]
+
+    def __init__(self, T, H, dtype=BF16, post=True, gate=GATE_NONE, gate_act=ACT_NONE, eps=1e-6, branch_scale=1.0, residual_scale=1.0):
+        super().__init__(int(T), int(H), int(dtype), int(gate), int(gate_act), NORM_POST if post else 0, float(eps), float(branch_scale),
+                         float(residual_scale))
 
 
 class CWeights(ctypes.Structure):
@@ -155,6 +185,28 @@ def load_library(build_if_missing: bool = True):
             lib.moe_w4_linear.argtypes = [F, I32, I32, I32, P, P, S, P, P, P, S, P]
             lib.moe_forward_w4.restype = st
             lib.moe_forward_w4.argtypes = [D, F, P, W, P, P, P, S, P]
+            L, N = ctypes.POINTER(LinearDims), ctypes.POINTER(NormDims)
+            lib.moe_sort_pairs.restype = st
+            lib.moe_sort_pairs.argtypes = [I32, I32, I32, P, P, P, P, P, P]
+            for name in ("moe_dispatch", "moe_combine"):
+                getattr(lib, name).restype = st
+            lib.moe_dispatch.argtypes = [I32, I32, I32, I32, P, P, P, P, P]
+            lib.moe_combine.argtypes = [I32, I32, I32, I32, P, P, P, P, P, P]
+            for name in ("moe_dispatch_backward", "moe_combine_backward"):
+                getattr(lib, name).restype = st
+                getattr(lib, name).argtypes = [I32, I32, I32, I32, P, P, P, P, P, P, P]
+            lib.moe_linear_workspace_size.restype = S
+            lib.moe_linear_workspace_size.argtypes = [L, I32]
+            lib.moe_linear.restype = st
+            lib.moe_linear.argtypes = [L, P, P, P, P, P, P, P, P, S, P]
+            lib.moe_linear_backward.restype = st
+            lib.moe_linear_backward.argtypes = [L, P, P, P, P, P, P, P, P, P, S, P]
+            lib.moe_norm_workspace_size.restype = S
+            lib.moe_norm_workspace_size.argtypes = [N]
+            lib.moe_norm_residual.restype = st
+            lib.moe_norm_residual.argtypes = [N, P, P, P, P, P, P, P, P]
+            lib.moe_norm_residual_backward.restype = st
+            lib.moe_norm_residual_backward.argtypes = [N, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P]
             lib.moe_test_set_wait.restype = st
             lib.moe_test_set_wait.argtypes = [ctypes.c_uint64, ctypes.c_int]
             lib.moe_status_string.restype = ctypes.c_char_p
@@ -510,6 +562,178 @@ def moe_forward_w4(dims, fmt: W4Format, x, weights: Weights, residual, out, work
     w = CWeights(router_w, router_b, *packed, gate)
     _check(load_library().moe_forward_w4(ctypes.byref(d), ctypes.byref(fmt), px, ctypes.byref(w), res, po, ws, _nbytes(workspace),
                                          _stream_of(stream, dev)), "moe_forward_w4")
+
+
+def _shaped(what: str, t, dtype, *shape):
+    """Raises unless t is of this type and shape."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _pairs(what: str, t, dtype, T: int, K: int):
+    """Raises unless t holds one number for each pair: [T, K] or [T * K]."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.numel() != T * K or t.dim() not in (1, 2) or (t.dim() == 2 and tuple(t.shape) != (T, K)):
+        raise ValueError(f"{what} must be [{T}, {K}], got {list(t.shape)}")
+
+
+def moe_sort_pairs(E: int, ids, counts, offsets, perm, inv, stream=None):
+    """Dispatch of the expert ids [T, K] int32: counts [E], offsets [E + 1], perm [T * K] (pairs t * K + k by expert,
+    -1 behind the last) and inv [T * K] (each pair's place, -1 for an id outside [0, E))."""
+    if ids.dim() != 2 or ids.dtype is not torch.int32:
+        raise TypeError("ids must be int32 [T, K]")
+    T, K = ids.shape
+    _shaped("counts", counts, torch.int32, E)
+    _shaped("offsets", offsets, torch.int32, E + 1)
+    _pairs("perm", perm, torch.int32, T, K)
+    _pairs("inv", inv, torch.int32, T, K)
+    dev = _device(ids)
+    _check(load_library().moe_sort_pairs(T, K, int(E), *_here(dev, ids, counts, offsets, perm, inv), _stream_of(stream, dev)), "moe_sort_pairs")
+
+
+def _exchange(name: str, token, token_what: str, rows, rows_what: str, inv, topk_w, dtopk_w=None):
+    """Sizes and type of a call on token [T, H] and rows [T * K, H]."""
+    if token.dim() != 2 or rows.dim() != 2:
+        raise ValueError(f"{token_what} is [T, H], {rows_what} [T * K, H]")
+    T, H = token.shape
+    if T and rows.shape[0] % T:
+        raise ValueError(f"{rows_what} must have T * K rows, T = {T}")
+    K = rows.shape[0] // T if T else 1
+    dtype = _DTYPE.get(token.dtype)
+    if dtype is None:
+        raise TypeError(f"{token_what} must be bfloat16, float16 or float32, got {token.dtype}")
+    _shaped(rows_what, rows, token.dtype, T * K, H)
+    _pairs("inv", inv, torch.int32, T, K)
+    if topk_w is not None:
+        _pairs("topk_w", topk_w, torch.float32, T, K)
+    if dtopk_w is not None:
+        _pairs("dtopk_w", dtopk_w, torch.float32, T, K)
+    return dtype, T, K, H
+
+
+def moe_dispatch(x, inv, topk_w, rows, stream=None):
+    """rows [T * K, H]: rows[inv[t, k]] = topk_w[t, k] * x[t] (topk_w None: the rows as they are)."""
+    sizes = _exchange("moe_dispatch", x, "x", rows, "rows", inv, topk_w)
+    dev = _device(x)
+    _check(load_library().moe_dispatch(*sizes, *_here(dev, x, inv, topk_w, rows), _stream_of(stream, dev)), "moe_dispatch")
+
+
+def moe_dispatch_backward(drows, inv, topk_w, x, dx, dtopk_w=None, stream=None):
+    """dx [T, H] = sum_k topk_w[t, k] * drows[inv[t, k]]; dtopk_w [T, K] (optional; x is read for it) = x[t] . drows[inv[t, k]]."""
+    sizes = _exchange("moe_dispatch_backward", dx, "dx", drows, "drows", inv, topk_w, dtopk_w)
+    if x is not None:
+        _shaped("x", x, dx.dtype, *dx.shape)
+    dev = _device(dx)
+    _check(load_library().moe_dispatch_backward(*sizes, *_here(dev, drows, inv, topk_w, x, dx, dtopk_w), _stream_of(stream, dev)),
+           "moe_dispatch_backward")
+
+
+def moe_combine(rows, inv, topk_w, residual, out, stream=None):
+    """out [T, H] = residual + sum_k topk_w[t, k] * rows[inv[t, k]] (topk_w and residual may be None)."""
+    sizes = _exchange("moe_combine", out, "out", rows, "rows", inv, topk_w)
+    if residual is not None:
+        _shaped("residual", residual, out.dtype, *out.shape)
+    dev = _device(out)
+    _check(load_library().moe_combine(*sizes, *_here(dev, rows, inv, topk_w, residual, out), _stream_of(stream, dev)), "moe_combine")
+
+
+def moe_combine_backward(dout, inv, topk_w, rows, drows, dtopk_w=None, stream=None):
+    """drows[inv[t, k]] = topk_w[t, k] * dout[t]; dtopk_w [T, K] (optional; rows are read for it) = dout[t] . rows[inv[t, k]]."""
+    sizes = _exchange("moe_combine_backward", dout, "dout", drows, "drows", inv, topk_w, dtopk_w)
+    if rows is not None:
+        _shaped("rows", rows, drows.dtype, *drows.shape)
+    dev = _device(dout)
+    _check(load_library().moe_combine_backward(*sizes, *_here(dev, dout, inv, topk_w, rows, drows, dtopk_w), _stream_of(stream, dev)),
+           "moe_combine_backward")
+
+
+def new_linear_workspace(dims: LinearDims, backward: bool = False, device="cuda") -> torch.Tensor:
+    """A zero-filled uint8 device workspace for moe_linear, or for moe_linear_backward, at these sizes."""
+    n = int(load_library().moe_linear_workspace_size(ctypes.byref(dims), int(backward)))
+    if n == 0:
+        raise MoEError(2, "moe_linear_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _linear(d: LinearDims, wide, **tensors):
+    """Checks the tensors of a call by name; wide: the columns of act's result."""
+    dt = _TORCH.get(d.dtype)
+    shapes = {"x": (d.T, d.K), "dx": (d.T, d.K), "w": (d.E, d.N, d.K), "dw": (d.E, d.N, d.K), "bias": (d.E, d.N), "dbias": (d.E, d.N),
+              "residual": (d.T, wide), "out": (d.T, wide), "dout": (d.T, wide), "z": (d.T, d.N)}
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.dtype is not dt:
+            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+        shape = shapes[name]
+        if t.shape != shape and not (d.E == 1 and name in ("w", "dw", "bias", "dbias") and t.shape == shape[1:]):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _offsets(d: LinearDims, offsets):
+    if offsets is not None:
+        _shaped("offsets", offsets, torch.int32, d.E + 1)
+
+
+def moe_linear(dims: LinearDims, x, w, bias, offsets, residual, out, z, workspace, stream=None):
+    """out = act(x . W_e^T + bias_e) + residual, e the expert whose rows [offsets[e], offsets[e + 1]) hold x's row
+    (offsets None: the one matrix); z (or None) receives the pre-activations for moe_linear_backward."""
+    wide = dims.N // 2 if dims.act == ACT_SWIGLU else dims.N
+    _linear(dims, wide, x=x, w=w, bias=bias, residual=residual, out=out, z=z)
+    _offsets(dims, offsets)
+    dev = _device(x)
+    px, pw, pb, of, pr, po, pz, ws = _here(dev, x, w, bias, offsets, residual, out, z, workspace)
+    _check(load_library().moe_linear(ctypes.byref(dims), px, pw, pb, of, pr, po, pz, ws, _nbytes(workspace), _stream_of(stream, dev)), "moe_linear")
+
+
+def moe_linear_backward(dims: LinearDims, x, w, offsets, z, dout, dx, dw, dbias, workspace, stream=None):
+    """Gradients of moe_linear's x, w and bias (each may be None) for the gradient dout of its result; the residual's is dout."""
+    wide = dims.N // 2 if dims.act == ACT_SWIGLU else dims.N
+    _linear(dims, wide, x=x, w=w, z=z, dout=dout, dx=dx, dw=dw, dbias=dbias)
+    _offsets(dims, offsets)
+    dev = _device(dout)
+    px, pw, of, pz, pd, gx, gw, gb, ws = _here(dev, x, w, offsets, z, dout, dx, dw, dbias, workspace)
+    _check(load_library().moe_linear_backward(ctypes.byref(dims), px, pw, of, pz, pd, gx, gw, gb, ws, _nbytes(workspace), _stream_of(stream, dev)),
+           "moe_linear_backward")
+
+
+def new_norm_workspace(dims: NormDims, device="cuda") -> torch.Tensor:
+    """A uint8 device workspace for moe_norm_residual_backward at these sizes."""
+    n = int(load_library().moe_norm_workspace_size(ctypes.byref(dims)))
+    if n == 0:
+        raise MoEError(2, "moe_norm_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _norm(d: NormDims, gate, dgate, rows, columns):
+    dt = _TORCH.get(d.dtype)
+    gate_shape = {GATE_TOKEN: (d.T,), GATE_CHANNEL: (d.H,), GATE_FULL: (d.T, d.H)}.get(d.gate, ())
+    for what, tensors, shape in (("rows", rows, (d.T, d.H)), ("gamma", columns, (d.H,)), ("gate", (gate, dgate), gate_shape)):
+        for t in tensors:
+            if t is not None and (t.dtype is not dt or t.shape != shape):
+                raise (TypeError if t.dtype is not dt else ValueError)(f"{what} tensors must be {dt} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def moe_norm_residual(dims: NormDims, y, residual, gate, gamma_post, gamma_pre, s, xn, stream=None):
+    """s = residual_scale * residual + branch_scale * act(gate) * N(y; gamma_post), xn = N(s; gamma_pre); residual, the
+    gammas and either result may be None, and N(y) is y for dims without post."""
+    _norm(dims, gate, None, (y, residual, s, xn), (gamma_post, gamma_pre))
+    dev = _device(y)
+    _check(load_library().moe_norm_residual(ctypes.byref(dims), *_here(dev, y, residual, gate, gamma_post, gamma_pre, s, xn), _stream_of(stream, dev)),
+           "moe_norm_residual")
+
+
+def moe_norm_residual_backward(dims: NormDims, ds, dxn, s, y, gate, gamma_post, gamma_pre, dresidual, dy, dgate, dgamma_post, dgamma_pre, workspace,
+                               stream=None):
+    """Gradients of moe_norm_residual's inputs (each may be None) for the gradients ds and dxn of its results (either may be None)."""
+    _norm(dims, gate, dgate, (ds, dxn, s, y, dresidual, dy), (gamma_post, gamma_pre, dgamma_post, dgamma_pre))
+    dev = _device(y)
+    *ptrs, ws = _here(dev, ds, dxn, s, y, gate, gamma_post, gamma_pre, dresidual, dy, dgate, dgamma_post, dgamma_pre, workspace)
+    _check(load_library().moe_norm_residual_backward(ctypes.byref(dims), *ptrs, ws, _nbytes(workspace), _stream_of(stream, dev)),
+           "moe_norm_residual_backward")
 
 
 def moe_rmsnorm(dims, x, gamma, eps: float, xn, stream=None):

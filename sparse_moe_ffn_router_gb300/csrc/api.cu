@@ -9,7 +9,7 @@
 #include <cuda.h>
 #include <vector>
 
-#include "launch.h"
+#include "ops.cuh"
 #include "w4.cuh"
 
 namespace moe {
@@ -251,6 +251,12 @@ cudaError_t launch_layer(const LayerArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+namespace moe {
+int device_sms() { return sm_count(); }
+uint64_t device_wait_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
+int device_suppress() { return g_suppress.load(std::memory_order_relaxed); }
+}  // namespace moe
 
 extern "C" size_t moe_workspace_size(const moe_dims* d) {
     Plan p;

@@ -1,0 +1,289 @@
+// exchange.cu -- token rows to their experts and back.
+//
+//   sort      a stable counting sort of the pairs p = t * K + k by expert: counts, offsets, perm
+//             (pairs in order, -1 behind the last) and inv (each pair's place, -1 for a dropped slot)
+//   spread    rows[inv[p]] = (w[p]) * tok[t]            dispatch, and the backward pass of combine
+//   gather    out[t] = (res[t]) + sum_k (w[p]) * rows[inv[p]]   combine, and the backward pass of dispatch
+// with, on request, dots[p] = tok[t] . rows[inv[p]]: the gradient of w in either direction.
+//
+// All of it is bound by HBM: a token row is read once and kept in registers while its K copies are
+// written, and a token's K rows are read once, side by side, and summed in fp32 in slot order.
+// Sums and dots run in a fixed order, so results are the same bits on every call.
+#include <cooperative_groups.h>
+
+#include "ops.cuh"
+
+namespace moe {
+
+namespace cg = cooperative_groups;
+
+// ---------------------------------------------------------------------------------------
+// sort: one thread-block cluster of up to 8 CTAs. A CTA takes a run of pairs, each of its 32 warps a
+// piece of the run. Pass one counts each warp's pairs per expert (match_any: equal ids of 32 lanes at
+// once, no atomics), the counts are scanned over warps, over CTAs (read through distributed shared
+// memory) and over experts, pass two ranks the same pairs again and writes their places. One launch
+// and no workspace: the 8 CTAs' two passes over 32768 ids cost less than a second launch would.
+constexpr int kSortWarps = 32, kSortMaxE = 256, kSortCtas = 8;
+
+__global__ void __launch_bounds__(32 * kSortWarps, 1)
+    k_sort_pairs(const int32_t* __restrict__ ids, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
+                 int32_t* __restrict__ perm, int32_t* __restrict__ inv, int P, int E, int seg) {
+    __shared__ int cnt[kSortWarps][kSortMaxE];  // a warp's pairs of each expert, then its first place among them
+    __shared__ int tot[kSortMaxE];              // this CTA's pairs of each expert
+    __shared__ int base[kSortMaxE];             // first place of this CTA's pairs of each expert
+    __shared__ int wsum[kSortMaxE / 32];
+    __shared__ int total_s;
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = (int)cl.block_rank(), n = (int)cl.num_blocks();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned below = (1u << lane) - 1u;
+    grid_dep_wait();
+    grid_dep_launch();
+    for (int e = lane; e < E; e += 32) cnt[warp][e] = 0;
+    __syncwarp();
+    const int64_t p0 = ((int64_t)rank * kSortWarps + warp) * seg;
+    const int64_t p1 = p0 + seg < P ? p0 + seg : P;
+    constexpr int kAhead = 4;  // ids loaded together
+    for (int64_t i0 = p0; i0 < p1; i0 += 32 * kAhead) {
+        int e[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t i = i0 + 32 * j + lane;
+            e[j] = i < p1 ? ids[i] : -1;
+            if ((unsigned)e[j] >= (unsigned)E) e[j] = -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const unsigned m = __match_any_sync(0xffffffffu, e[j]);
+            if (e[j] >= 0 && (m & below) == 0) cnt[warp][e[j]] += __popc(m);
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    const int e = threadIdx.x;
+    if (e < E) {
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int c = cnt[w][e];
+            cnt[w][e] = sum;
+            sum += c;
+        }
+        tot[e] = sum;
+    }
+    cl.sync();
+    int all = 0, before = 0;
+    if (e < E)
+        for (int r = 0; r < n; ++r) {
+            const int c = cl.map_shared_rank(tot, r)[e];
+            all += c;
+            before += r < rank ? c : 0;
+        }
+    if (e < kSortMaxE) {  // exclusive scan over the experts
+        int v = all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        if (lane == 31) wsum[warp] = v;
+        base[e] = v - all;
+    }
+    __syncthreads();
+    if (e < kSortMaxE) {
+        int add = 0;
+        for (int w = 0; w < warp; ++w) add += wsum[w];
+        const int first = base[e] + add;
+        base[e] = first + before;
+        if (e == kSortMaxE - 1) total_s = first + all;
+        if (rank == 0 && e < E) {
+            counts[e] = all;
+            offsets[e] = first;
+            if (e == E - 1) offsets[E] = first + all;
+        }
+    }
+    __syncthreads();
+    const int total = total_s;
+    for (int64_t i0 = p0; i0 < p1; i0 += 32 * kAhead) {
+        int e[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t i = i0 + 32 * j + lane;
+            e[j] = i < p1 ? ids[i] : -1;
+            if ((unsigned)e[j] >= (unsigned)E) e[j] = -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t i = i0 + 32 * j + lane;
+            const unsigned m = __match_any_sync(0xffffffffu, e[j]);
+            int at = -1;
+            if (e[j] >= 0) at = base[e[j]] + cnt[warp][e[j]] + __popc(m & below);
+            __syncwarp();
+            if (e[j] >= 0 && (m & below) == 0) cnt[warp][e[j]] += __popc(m);
+            __syncwarp();
+            if (i < p1) {
+                inv[i] = at;
+                if (at >= 0) perm[at] = (int32_t)i;
+                if (i >= total) perm[i] = -1;
+            }
+        }
+    }
+    cl.sync();  // no CTA leaves while another may still read its counts
+}
+
+cudaError_t launch_sort_pairs(const int32_t* ids, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, int P,
+                              int E, cudaStream_t s) {
+    int n = 1;
+    while (n < kSortCtas && P > 1024 * n) n *= 2;
+    const int64_t per = ((int64_t)P + n * kSortWarps - 1) / (n * kSortWarps);
+    const int seg = (int)((per + 31) / 32 * 32);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(32 * kSortWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e;
+    MOE_LAUNCH(MOE_KERNEL_SORT_PAIRS, s, (e = cudaLaunchKernelEx(&cfg, k_sort_pairs, ids, counts, offsets, perm, inv, P, E, seg)));
+    return e;
+}
+
+// ---------------------------------------------------------------------------------------
+// spread and gather. TPT threads take a token: a warp where there are tokens enough to fill the GPU,
+// a CTA of 256 where there are few and the latency of one row's loads is what counts.
+
+constexpr int kSlots = 8;  // K, at most
+
+// Sum over the TPT threads of a token of v[k]; thread 0 .. K - 1 of the token stores it.
+template <int TPT>
+__device__ __forceinline__ void store_dots(float (&v)[kSlots], float* dst, int K) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k)
+        if (k < K) v[k] = warp_sum(v[k]);
+    if (TPT == 32) {
+#pragma unroll
+        for (int k = 0; k < kSlots; ++k)
+            if (k < K && lane == k) dst[k] = v[k];
+    } else {
+        __shared__ float part[TPT / 32][kSlots];
+        if (lane == 0)
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k) part[warp][k] = v[k];
+        __syncthreads();
+        if ((int)threadIdx.x < K) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < TPT / 32; ++w) sum += part[w][threadIdx.x];
+            dst[threadIdx.x] = sum;
+        }
+    }
+}
+
+template <typename T, int VE, int TPT, bool GATHER, bool DOTS>
+__global__ void __launch_bounds__(256) k_exchange(const ExchangeArgs a) {
+    typedef Vec<T, VE> V;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int t = (int)(blockIdx.x * (256 / TPT) + threadIdx.x / TPT);
+    if (t >= a.T) return;  // (a whole token's threads)
+    const int lane = threadIdx.x % TPT;
+    const int K = a.K, nv = a.H / VE;
+    const int64_t P = (int64_t)a.T * K, p = (int64_t)t * K;
+    int at[kSlots];
+    float w[kSlots], dot[kSlots];
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+        at[k] = -1;
+        w[k] = 1.f;
+        dot[k] = 0.f;
+        if (k < K) {
+            at[k] = a.inv[p + k];
+            if (at[k] >= P) at[k] = -1;  // (no place: as a dropped slot)
+            if (a.w) w[k] = a.w[p + k];
+        }
+    }
+    const V* tok = reinterpret_cast<const V*>(a.tok) + (int64_t)t * nv;
+    const V* rows = reinterpret_cast<const V*>(a.rows);
+    V* out = reinterpret_cast<V*>(a.out);
+    const bool scaled = a.w != nullptr;
+    for (int j = lane; j < nv; j += TPT) {
+        V x = {}, r[kSlots];
+        if (!GATHER || a.tok) x = tok[j];
+        if (GATHER || DOTS) {
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k)
+                if (at[k] >= 0) r[k] = rows[(int64_t)at[k] * nv + j];
+        }
+        if (GATHER) {
+            float sum[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i) sum[i] = DOTS || !a.tok ? 0.f : to_f(x.v[i]);
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k)
+                if (at[k] >= 0) {
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) sum[i] = scaled ? fmaf(w[k], to_f(r[k].v[i]), sum[i]) : sum[i] + to_f(r[k].v[i]);
+                }
+            V o;
+#pragma unroll
+            for (int i = 0; i < VE; ++i) o.v[i] = from_f<T>(sum[i]);
+            out[(int64_t)t * nv + j] = o;
+        } else {
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k)
+                if (at[k] >= 0) {
+                    V o = x;
+                    if (scaled) {
+#pragma unroll
+                        for (int i = 0; i < VE; ++i) o.v[i] = from_f<T>(w[k] * to_f(x.v[i]));
+                    }
+                    out[(int64_t)at[k] * nv + j] = o;
+                }
+        }
+        if (DOTS) {
+#pragma unroll
+            for (int k = 0; k < kSlots; ++k)
+                if (at[k] >= 0) {
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) dot[k] = fmaf(to_f(x.v[i]), to_f(r[k].v[i]), dot[k]);
+                }
+        }
+    }
+    if (DOTS) store_dots<TPT>(dot, a.dots + p, K);
+}
+
+template <typename T, int VE, bool GATHER, bool DOTS>
+static cudaError_t launch_exchange_t(const ExchangeArgs& a, cudaStream_t s) {
+    cudaError_t e;
+    const int id = GATHER ? MOE_KERNEL_GATHER_ROWS : MOE_KERNEL_SPREAD_ROWS;
+    // a warp for each token from 16 tokens an SM, where the warps fill the GPU; a CTA below
+    if (a.T >= 16 * a.num_sms)
+        MOE_LAUNCH(id, s, (e = launch_pdl(k_exchange<T, VE, 32, GATHER, DOTS>, dim3((a.T + 7) / 8), dim3(256), 0, s, a)));
+    else
+        MOE_LAUNCH(id, s, (e = launch_pdl(k_exchange<T, VE, 256, GATHER, DOTS>, dim3(a.T), dim3(256), 0, s, a)));
+    return e;
+}
+
+template <typename T, bool GATHER>
+static cudaError_t launch_exchange(const ExchangeArgs& a, cudaStream_t s) {
+    constexpr int VE = 16 / (int)sizeof(T);
+    if (a.H % VE == 0)
+        return a.dots ? launch_exchange_t<T, VE, GATHER, true>(a, s) : launch_exchange_t<T, VE, GATHER, false>(a, s);
+    return a.dots ? launch_exchange_t<T, 1, GATHER, true>(a, s) : launch_exchange_t<T, 1, GATHER, false>(a, s);
+}
+
+cudaError_t launch_spread(int32_t dtype, const ExchangeArgs& a, cudaStream_t s) {
+    return dtype == MOE_BF16 ? launch_exchange<bf16, false>(a, s) : dtype == MOE_FP16 ? launch_exchange<fp16, false>(a, s) : launch_exchange<float, false>(a, s);
+}
+cudaError_t launch_gather(int32_t dtype, const ExchangeArgs& a, cudaStream_t s) {
+    return dtype == MOE_BF16 ? launch_exchange<bf16, true>(a, s) : dtype == MOE_FP16 ? launch_exchange<fp16, true>(a, s) : launch_exchange<float, true>(a, s);
+}
+
+}  // namespace moe

@@ -30,7 +30,7 @@
 //             the group's end are zero-filled. x rows are kept in L2 (evict-last) across the K
 //             experts that read them, and no dispatched copy of x is written or read. The
 //             shared expert's A rows are x itself, loaded by TMA.
-#include "launch.h"
+#include "ops.cuh"
 #include "sm100.cuh"
 
 namespace moe {
@@ -472,6 +472,23 @@ cudaError_t launch_gemm(const CUtensorMap& A0, const CUtensorMap& A1, const CUte
 
 bool make_bf16_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch, uint32_t box_rows) {
     return make_map(m, base, rows, cols, pitch, box_rows);
+}
+
+bool encode_map(CUtensorMap* m, int32_t dtype, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box) {
+    auto fn = encode_fn();
+    if (!fn || rank < 1 || rank > 5) return false;
+    cuuint64_t d[5], st[5];
+    cuuint32_t b[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        es[i] = 1;
+        if (i) st[i - 1] = strides[i - 1];
+    }
+    return fn(m, dtype == MOE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+              const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Router scores of all T tokens on the tensor cores: logits[:, 0:E] = x . Wr^T (+ br).

@@ -1,0 +1,830 @@
+// linear.cu -- linear layers with bias, activation and residual in the epilogue, and their gradients, for
+// one weight matrix or for one to each expert's rows, on the 5th-generation tensor cores.
+//
+//   kFwd   out = act(x . W_e^T + b_e) + residual      D[n, t] = sum_k W_e[n, k] x[t, k]
+//   kDx    dx  = dz . W_e                             D[k, t] = sum_n W_e[n, k] dz[t, n]
+//   kDw    dW_e = dz_e^T . x_e                        D[k, n] = sum_t x[t, k] dz[t, n], t over expert e's rows
+// with dz = act'(z) * dout from an elementwise kernel that also leaves the bias' column sums.
+//
+// In all three the 128 lanes of the accumulator are what is contiguous in the result, and its columns are
+// the result's rows: token rows (kFwd, kDx), of which a tile takes as many as there are, in steps of
+// 16, so that experts with few rows cost few columns; or W's rows (kDw). Operands are read as they
+// lie in memory: K-major where the contraction is contiguous, else MN-major (W in kDx, both in kDw), so
+// nothing is transposed beforehand. For swiglu a tile's 128 weight rows are 64 gate rows and the 64
+// matching up rows in turns of 16, by a five-dimensional tensor map: gate and up of a feature are
+// then 16 lanes apart, in one warp's reach.
+//
+// One CTA an SM walks its share of the tiles (expert by expert, then 128 features, then columns, so tiles
+// that share weights run side by side and meet in L2). Warp 0 loads by TMA into a ring of 64-deep stages,
+// warp 1 issues the MMAs into one of two accumulators in tensor memory, warps 4 - 11 write the other out.
+// With few tiles (decode) a cluster of up to 8 CTAs takes one tile's contraction in parts; the parts are added
+// in rank order through distributed shared memory. Sums are fp32 in a fixed order throughout.
+#include <type_traits>
+
+#include "ops.cuh"
+#include "sm100.cuh"
+
+namespace moe {
+
+enum { kFwd = 0, kDx = 1, kDw = 2 };
+
+constexpr int kLinThreads = 384, kLinEpiWarp0 = 4, kLinEpiWarps = 8;
+constexpr int kLinMaxE = 256;
+constexpr uint32_t kLinA = 128 * 64 * 2;  // a stage's feature side
+constexpr int kLinBoxRows = 32;           // token rows of one TMA box
+constexpr int kPartPitch = 132;           // floats of a column of the cluster's partial tile (4 mod 32: no bank conflicts)
+constexpr int kStagePitch = 36;           // floats of a column of a warp's transposition buffer (the same)
+
+// NB: columns of a tile, at most. 256 for many rows; 64 for few, with a deeper ring and the split contraction.
+template <int NB>
+struct LinSmem {
+    static constexpr uint32_t kB = NB * 64 * 2;
+    static constexpr int kStages = NB == 256 ? 4 : 7;
+    static constexpr uint32_t kRing = kStages * (kLinA + kB);
+    static constexpr uint32_t kScratch = NB == 256 ? kLinEpiWarps * 16 * kStagePitch * 4 : NB * kPartPitch * 4;
+    static constexpr uint32_t kTables = 2 * (kLinMaxE + 4) * 4;
+    static constexpr uint32_t kBytes = 1024 + kRing + kScratch + kTables + 256;
+    static constexpr uint32_t kTmem = 2 * NB;
+};
+
+// One launch's view of the operands.
+struct LinView {
+    const int32_t* offsets;
+    const void *bias, *residual;
+    void *out, *z;
+    int T, E, N;      // token rows, experts, W's rows
+    int F;            // features: contiguous extent of out
+    int C;            // contraction (kFwd, kDx)
+    int colw;         // columns of a tile, at most (a multiple of 16)
+    int ftiles;
+    int act;
+    int vec;          // rows of out, residual and z start on 8 bytes
+    int suppress;     // testing aid: CTA 0 never loads its first stage
+    uint32_t* err;
+    uint64_t wait_ns;
+};
+
+struct LinTile {
+    int e, f, c0, cols, row0, blocks, rows;  // expert, feature tile, first column, columns, first token row, 64-deep blocks, the expert's rows
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes at the same shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float lin_sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+__device__ __forceinline__ float lin_act(int act, float z) {
+    switch (act) {
+        case MOE_ACT_SIGMOID: return lin_sigmoid(z);
+        case MOE_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
+        case MOE_ACT_SILU: return z * lin_sigmoid(z);
+        case MOE_ACT_GELU: return 0.5f * z * erfcf(-0.70710678f * z);
+        default: return z;
+    }
+}
+__device__ __forceinline__ float lin_slope(int act, float z) {
+    switch (act) {
+        case MOE_ACT_SIGMOID: { const float p = lin_sigmoid(z); return p * (1.f - p); }
+        case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+        case MOE_ACT_SILU: { const float p = lin_sigmoid(z); return p * (1.f + z * (1.f - p)); }
+        case MOE_ACT_GELU: return 0.5f * erfcf(-0.70710678f * z) + z * 0.39894228f * expf(-0.5f * z * z);
+        default: return 1.f;
+    }
+}
+
+// Columns of each of an expert's tiles: as even as steps of 16 allow.
+__device__ __forceinline__ int lin_width(int cols, int tiles) { return ((cols + tiles - 1) / tiles + 15) / 16 * 16; }
+
+// Row boundaries of the experts and first tile of each, in shared memory; every bound is within [0, T].
+template <int MODE>
+__device__ void lin_tables(const LinView& a, int* off, int* start) {
+    const int e = threadIdx.x;
+    if (e <= a.E) {
+        const int o = a.offsets ? a.offsets[e] : e ? a.T : 0;
+        const int c = min(max(o, 0), a.T);
+        if (c != o) atomicOr(a.err, ERR_BAD_ROUTE);
+        off[e] = c;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int run = 0;
+        for (int b = 0; b < a.E; b += 32) {
+            const int i = b + lane;
+            int n = 0;
+            if (i < a.E) {
+                const int rows = off[i + 1] - off[i];
+                if (rows < 0) atomicOr(a.err, ERR_BAD_ROUTE);
+                const int cols = MODE == kDw ? a.N : max(rows, 0);
+                n = (cols + a.colw - 1) / a.colw * a.ftiles;
+            }
+            int v = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += y;
+            }
+            if (i < a.E) start[i] = run + v - n;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) start[a.E] = run;
+    }
+    __syncthreads();
+}
+
+template <int MODE>
+__device__ __forceinline__ LinTile lin_tile(const LinView& a, const int* off, const int* start, int t) {
+    int lo = 0, hi = a.E;  // start[lo] <= t < start[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= t) lo = mid; else hi = mid;
+    }
+    LinTile r;
+    r.e = lo;
+    r.row0 = off[lo];
+    r.rows = max(off[lo + 1] - r.row0, 0);
+    const int cols = MODE == kDw ? a.N : r.rows;
+    const int n = (cols + a.colw - 1) / a.colw, local = t - start[lo], width = lin_width(cols, n);
+    r.f = local / n;
+    r.c0 = (local - r.f * n) * width;
+    r.cols = min(width, cols - r.c0);
+    r.blocks = ((MODE == kDw ? r.rows : a.C) + 63) / 64;
+    return r;
+}
+
+// Four consecutive features of one row of the result, from their sums v (and the up sums u).
+template <typename T, bool GATED>
+__device__ __forceinline__ void lin_finish(const LinView& a, int64_t row, int f, float (&v)[4], float (&u)[4], const float (&bv)[4],
+                                           const float (&bu)[4]) {
+    typedef Vec<T, 4> V;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] += bv[i];
+        if (GATED) u[i] += bu[i];
+    }
+    T* out = reinterpret_cast<T*>(a.out) + row * a.F + f;
+    const T* res = a.residual ? reinterpret_cast<const T*>(a.residual) + row * a.F + f : nullptr;
+    T* z = a.z ? reinterpret_cast<T*>(a.z) + row * a.N + f : nullptr;
+    float o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = GATED ? v[i] * lin_sigmoid(v[i]) * u[i] : lin_act(a.act, v[i]);
+    if (a.vec && f + 4 <= a.F) {
+        if (res) {
+            const V r = *reinterpret_cast<const V*>(res);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] += to_f(r.v[i]);
+        }
+        V w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.v[i] = from_f<T>(o[i]);
+        *reinterpret_cast<V*>(out) = w;
+        if (z) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w.v[i] = from_f<T>(v[i]);
+            *reinterpret_cast<V*>(z) = w;
+            if (GATED) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w.v[i] = from_f<T>(u[i]);
+                *reinterpret_cast<V*>(z + a.F) = w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (f + i < a.F) {
+                out[i] = from_f<T>(o[i] + (res ? to_f(res[i]) : 0.f));
+                if (z) {
+                    z[i] = from_f<T>(v[i]);
+                    if (GATED) z[a.F + i] = from_f<T>(u[i]);
+                }
+            }
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void lin_bias(const LinView& a, int e, int f, float (&b)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = a.bias && f + i < a.F ? to_f(reinterpret_cast<const T*>(a.bias)[(int64_t)e * a.N + f + i]) : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void lin_bias_up(const LinView& a, int e, int f, float (&b)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = a.bias && f + i < a.F ? to_f(reinterpret_cast<const T*>(a.bias)[(int64_t)e * a.N + a.F + f + i]) : 0.f;
+}
+
+template <typename T, int MODE, bool GATED, int NB>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    k_linear(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB, const LinView a) {
+    typedef LinSmem<NB> S;
+    constexpr int kStages = S::kStages;
+    constexpr bool kCanSplit = NB == 64;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + kStages * kLinA;
+    float* scratch = reinterpret_cast<float*>(smem + S::kRing);
+    int* off = reinterpret_cast<int*>(smem + S::kRing + S::kScratch);
+    int* start = off + kLinMaxE + 4;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kRing + S::kScratch + S::kTables);
+    uint64_t* empty = full + kStages;
+    uint64_t* accf = empty + kStages;
+    uint64_t* acce = accf + 2;
+    uint64_t* mma_done = acce + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((2 * kStages + 5) * 8 + 8 <= 256, "barrier area");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = kCanSplit ? cluster_rank() : 0, split = kCanSplit ? cluster_size() : 1;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf[b], 1);
+            mbar_init(&acce[b], kLinEpiWarps);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&mA);
+        tma_prefetch_desc(&mB);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, S::kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dep_wait();  // everything is read from here on: operands, offsets and workspace may be the previous kernel's
+    grid_dep_launch();
+    lin_tables<MODE>(a, off, start);
+    const int total = start[a.E];
+    const int step = gridDim.x / split, first = blockIdx.x / split;
+
+    if (warp == 0) {
+        // ---------------- TMA producer (one lane; the warp stays together for the cluster's barriers)
+        int it = 0;
+        uint32_t last_par[kStages];
+        bool issued[kStages];
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) issued[s] = false;
+        for (int t = first; t < total; t += step) {
+            if (lane == 0 && !*abort_flag) {
+                const LinTile ti = lin_tile<MODE>(a, off, start, t);
+                const int kb0 = (int)((int64_t)ti.blocks * rank / split), kb1 = (int)((int64_t)ti.blocks * (rank + 1) / split);
+                const int boxes = MODE == kDw ? (ti.cols + 63) / 64 : (ti.cols + kLinBoxRows - 1) / kLinBoxRows;
+                const uint32_t bytes = kLinA + (uint32_t)boxes * (MODE == kDw ? 64 : kLinBoxRows) * 128u;
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t ph = (uint32_t)(it / kStages) & 1u;
+                    if (!mbar_wait(&empty[s], ph ^ 1u, a.wait_ns)) {
+                        atomicOr(a.err, ERR_TIMEOUT);
+                        *abort_flag = 1;
+                        break;
+                    }
+                    if (a.suppress && blockIdx.x == 0 && it == 0) continue;
+                    mbar_arrive_expect_tx(&full[s], bytes);
+                    uint8_t* da = sA + s * kLinA;
+                    uint8_t* db = sB + s * S::kB;
+                    if (MODE == kFwd) {
+                        if (GATED)
+                            tma_load_5d(da, &mA, &full[s], kb * 64, 0, 0, ti.f * 4, ti.e);
+                        else
+                            tma_load_3d(da, &mA, &full[s], kb * 64, ti.f * 128, ti.e);
+                    } else if (MODE == kDx) {
+                        for (int p = 0; p < 2; ++p) tma_load_3d(da + p * 8192, &mA, &full[s], ti.f * 128 + p * 64, kb * 64, ti.e);
+                    } else {
+                        for (int p = 0; p < 2; ++p) tma_load_2d(da + p * 8192, &mA, &full[s], ti.f * 128 + p * 64, ti.row0 + kb * 64);
+                    }
+                    if (MODE == kDw)
+                        for (int p = 0; p < boxes; ++p) tma_load_2d(db + p * 8192, &mB, &full[s], ti.c0 + p * 64, ti.row0 + kb * 64);
+                    else
+                        for (int p = 0; p < boxes; ++p)
+                            tma_load_2d(db + p * (kLinBoxRows * 128), &mB, &full[s], kb * 64, ti.row0 + ti.c0 + p * kLinBoxRows);
+                    issued[s] = true;
+                    last_par[s] = ph;
+                }
+            }
+            __syncwarp();
+            if (kCanSplit && split > 1) {
+                cluster_sync_all();
+                cluster_sync_all();
+            }
+        }
+        // every copy this CTA issued must land before shared memory is released
+        if (lane == 0)
+#pragma unroll
+            for (int s = 0; s < kStages; ++s)
+                if (issued[s] && !mbar_wait(&full[s], last_par[s], a.wait_ns)) atomicOr(a.err, ERR_TIMEOUT);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA issuer
+        int it = 0, local = 0;
+        for (int t = first; t < total; t += step, ++local) {
+            bool ok = !*abort_flag;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (ok) {
+                const LinTile ti = lin_tile<MODE>(a, off, start, t);
+                const int kb0 = (int)((int64_t)ti.blocks * rank / split), kb1 = (int)((int64_t)ti.blocks * (rank + 1) / split);
+                const int n16 = (ti.cols + 15) / 16 * 16;
+                const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 128, n16, MODE != kFwd, MODE == kDw);
+                const int b = local & 1;
+                const uint32_t use = (uint32_t)(local >> 1) & 1u;
+                const uint32_t d = tmem + (uint32_t)(b * NB);
+                ok = mbar_wait(&acce[b], use ^ 1u, a.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t ph = (uint32_t)(it / kStages) & 1u;
+                    ok = mbar_wait(&full[s], ph, a.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t aa = smem_u32(sA + s * kLinA), bb = smem_u32(sB + s * S::kB);
+                    int steps = 4;
+                    if (MODE == kDw) {
+                        // the expert's last block: 16 rows at a time, rows of the next expert in the last 16 set
+                        // to zero in both operands (whatever they hold: 0 x infinity would stay)
+                        const int left = ti.rows - kb * 64;
+                        if (left < 64) {
+                            steps = (left + 15) / 16;
+                            if (left & 15) {
+                                const int panels = 2 + (ti.cols + 63) / 64, rows = steps * 16 - left;
+                                const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+                                for (int i = lane; i < panels * rows * 8; i += 32) {
+                                    const int p = i / (rows * 8), r = i - p * (rows * 8);
+                                    sts128((p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)(left * 128 + r * 16), zero);
+                                }
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                            }
+                        }
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        for (int kk = 0; kk < steps; ++kk) {
+                            const uint64_t da = MODE == kFwd ? sdesc_kmajor_sw128(aa + kk * 32) : sdesc_mnmajor_sw128(aa + kk * 2048, 8192);
+                            const uint64_t db = MODE == kDw ? sdesc_mnmajor_sw128(bb + kk * 2048, 8192) : sdesc_kmajor_sw128(bb + kk * 32);
+                            mma_bf16(d, da, db, idesc, kb != kb0 || kk != 0);
+                        }
+                        mma_commit(&empty[s]);
+                        if (kb + 1 == kb1) mma_commit(&accf[b]);
+                    }
+                    __syncwarp();
+                }
+                if (ok && kb0 == kb1 && lane == 0) mbar_arrive(&accf[b]);  // (no rows: zeros are written)
+                if (!ok && lane == 0) {
+                    atomicOr(a.err, ERR_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                __syncwarp();
+            }
+            if (kCanSplit && split > 1) {
+                cluster_sync_all();
+                cluster_sync_all();
+            }
+        }
+        if (elect_one()) mma_commit(mma_done);
+        __syncwarp();
+        if (!mbar_wait(mma_done, 0, a.wait_ns) && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
+        __syncwarp();
+    } else if (warp >= kLinEpiWarp0) {
+        // ---------------- epilogue: lanes 32 q .. of the accumulator, every other 16 columns
+        const int q = warp & 3, h = (warp - kLinEpiWarp0) >> 2;
+        const int g = lane >> 2, tt = lane & 3;
+        float* mine = scratch + (warp - kLinEpiWarp0) * 16 * kStagePitch;
+        int local = 0;
+        for (int t = first; t < total; t += step, ++local) {
+            const LinTile ti = lin_tile<MODE>(a, off, start, t);
+            const int kb0 = (int)((int64_t)ti.blocks * rank / split), kb1 = (int)((int64_t)ti.blocks * (rank + 1) / split);
+            const int b = local & 1;
+            const uint32_t use = (uint32_t)(local >> 1) & 1u;
+            const int64_t row0 = MODE == kDw ? (int64_t)ti.e * a.N + ti.c0 : (int64_t)ti.row0 + ti.c0;
+            // a lane's four features: those of chunk lane % 8 (gated: lane % 4) of the warp's 32 lanes
+            const int f = GATED ? ti.f * 64 + q * 16 + (lane & 3) * 4 : ti.f * 128 + q * 32 + (lane & 7) * 4;
+            float bv[4], bu[4];
+            if (!(kCanSplit && split > 1)) {
+                lin_bias<T>(a, ti.e, f, bv);
+                if (GATED) lin_bias_up<T>(a, ti.e, f, bu);
+            }
+            bool ready = false;
+            if (!*abort_flag) ready = mbar_wait(&accf[b], use, a.wait_ns);
+            ready = __all_sync(0xffffffffu, ready);
+            if (!ready && lane == 0) {
+                if (!*abort_flag) atomicOr(a.err, ERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            if (ready) {
+                tc_fence_after();
+                const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NB);
+                for (int c = h * 16; c < ti.cols; c += 32) {
+                    uint32_t r[16];
+                    if (kb0 < kb1) {
+                        tmem_ld_frag2(tb + c, r);
+                        tmem_ld_frag2(tb + (16u << 16) + c, r + 8);
+                        tmem_ld_wait16(r);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) r[i] = 0u;
+                    }
+                    if (kCanSplit && split > 1) {
+                        float* p = scratch + c * kPartPitch + q * 32;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)  // register i: lane g + 8 (i / 2 % 2) + 16 (i / 8), column 8 (i / 4 % 2) + 2 tt + i % 2
+                            p[(8 * ((i >> 2) & 1) + 2 * tt + (i & 1)) * kPartPitch + g + 8 * ((i >> 1) & 1) + 16 * (i >> 3)] = __uint_as_float(r[i]);
+                        continue;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        mine[(8 * ((i >> 2) & 1) + 2 * tt + (i & 1)) * kStagePitch + g + 8 * ((i >> 1) & 1) + 16 * (i >> 3)] = __uint_as_float(r[i]);
+                    __syncwarp();
+                    constexpr int kPer = GATED ? 8 : 4;  // columns of one round
+#pragma unroll
+                    for (int i = 0; i < 16 / kPer; ++i) {
+                        const int col = i * kPer + lane / (32 / kPer);
+                        float v[4], u[4] = {0.f, 0.f, 0.f, 0.f};
+                        const float4 x = *reinterpret_cast<const float4*>(mine + col * kStagePitch + (lane & (32 / kPer - 1)) * 4);
+                        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+                        if (GATED) {
+                            const float4 y = *reinterpret_cast<const float4*>(mine + col * kStagePitch + 16 + (lane & 3) * 4);
+                            u[0] = y.x; u[1] = y.y; u[2] = y.z; u[3] = y.w;
+                        }
+                        if (c + col < ti.cols) lin_finish<T, GATED>(a, row0 + c + col, f, v, u, bv, bu);
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acce[b]);
+            }
+            if (kCanSplit && split > 1) {
+                __syncwarp();
+                cluster_sync_all();
+                if (ready) {
+                    // the tile's (column, four features) in rows of the cluster's threads; the parts in rank order
+                    constexpr int kChunks = GATED ? 16 : 32;
+                    const int me = (int)rank * (kLinEpiWarps * 32) + (int)threadIdx.x - kLinEpiWarp0 * 32;
+                    for (int i = me; i < ti.cols * kChunks; i += (int)split * kLinEpiWarps * 32) {
+                        const int col = i / kChunks, ch = i % kChunks;
+                        const int at = GATED ? (ch >> 2) * 32 + (ch & 3) * 4 : ch * 4;
+                        const int ff = GATED ? ti.f * 64 + ch * 4 : ti.f * 128 + ch * 4;
+                        const uint32_t addr = smem_u32(scratch + col * kPartPitch + at);
+                        float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+                        lin_bias<T>(a, ti.e, ff, bv);
+                        if (GATED) lin_bias_up<T>(a, ti.e, ff, bu);
+                        for (uint32_t r = 0; r < split; ++r) {
+                            const float4 x = ld_peer(addr, r);
+                            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                            if (GATED) {
+                                const float4 y = ld_peer(addr + 64, r);
+                                u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+                            }
+                        }
+                        if (ff < a.F) lin_finish<T, GATED>(a, row0 + col, ff, v, u, bv, bu);
+                    }
+                }
+                __syncwarp();
+                cluster_sync_all();
+            }
+        }
+    } else if (kCanSplit && split > 1) {
+        for (int t = first; t < total; t += step) {
+            cluster_sync_all();
+            cluster_sync_all();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::kTmem);
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// dz = act'(z) * dout, and the column sums of it for the bias. A CTA takes a chunk of 64 rows and 128
+// columns (for swiglu 128 gate columns and the matching up columns); 16 threads side by side hold 8 columns
+// each, 16 rows at a time. Sums are of dz before its rounding, row block by row block: those of the rows of
+// expert e in chunk c go to part[c + e], a place of their own as chunks and experts follow one another.
+
+template <typename T, int VE>
+__device__ __forceinline__ void ld_cols(const T* p, int n, float (&v)[8]) {
+    if (VE == 8) {
+        const Vec<T, 8> x = *reinterpret_cast<const Vec<T, 8>*>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f(x.v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f(p[i]) : 0.f;
+    }
+}
+
+template <typename T, int VE, bool GATED>
+__global__ void __launch_bounds__(256) k_dz(const LinearArgs a, int pitch) {
+    __shared__ int off[kLinMaxE + 1];
+    __shared__ float sums[GATED ? 2 : 1][16][128];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int N = a.d.N, E = a.d.E, wide = GATED ? N / 2 : N;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int r0 = blockIdx.x * kDzRows, r1 = min(r0 + kDzRows, a.d.T);
+    const int f = blockIdx.y * 128 + tx * 8, n = min(8, wide - f);  // columns of this thread (none: n <= 0)
+    for (int e = threadIdx.x; e <= E; e += 256) off[e] = a.offsets ? min(max(a.offsets[e], 0), a.d.T) : e ? a.d.T : 0;
+    __syncthreads();
+    int lo = 0, hi = E;  // the last expert whose rows begin at or before r0
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= r0) lo = mid; else hi = mid;
+    }
+    T* dz = reinterpret_cast<T*>(a.dz);
+    const T *z = reinterpret_cast<const T*>(a.z_in), *dout = reinterpret_cast<const T*>(a.dout);
+    for (int e = lo; e < E && off[e] < r1; ++e) {
+        const int b0 = max(off[e], r0), b1 = min(off[e + 1], r1);
+        if (b0 >= b1) continue;
+        float sv[8], su[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sv[i] = su[i] = 0.f;
+        if (n > 0) {
+#pragma unroll 4
+            for (int r = b0 + ty; r < b1; r += 16) {
+                float d[8], v[8], u[8];
+                ld_cols<T, VE>(dout + (int64_t)r * wide + f, n, d);
+                if (GATED || a.d.act != MOE_ACT_NONE) ld_cols<T, VE>(z + (int64_t)r * N + f, n, v);
+                if (GATED) {
+                    ld_cols<T, VE>(z + (int64_t)r * N + wide + f, n, u);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float p = lin_sigmoid(v[i]), dd = d[i];
+                        d[i] = dd * u[i] * (p * (1.f + v[i] * (1.f - p)));
+                        u[i] = dd * (v[i] * p);
+                    }
+                } else if (a.d.act != MOE_ACT_NONE) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) d[i] *= lin_slope(a.d.act, v[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    sv[i] += d[i];
+                    if (GATED) su[i] += u[i];
+                }
+                if (dz) {
+                    Vec<T, 8> o;  // (columns up to the pitch are zeros)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o.v[i] = from_f<T>(i < n ? d[i] : 0.f);
+                    *reinterpret_cast<Vec<T, 8>*>(dz + (int64_t)r * pitch + f) = o;
+                    if (GATED) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o.v[i] = from_f<T>(u[i]);
+                        *reinterpret_cast<Vec<T, 8>*>(dz + (int64_t)r * pitch + wide + f) = o;
+                    }
+                }
+            }
+        }
+        if (a.dbias) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sums[0][ty][tx * 8 + i] = sv[i];
+                if (GATED) sums[GATED ? 1 : 0][ty][tx * 8 + i] = su[i];
+            }
+            __syncthreads();
+            const int half = threadIdx.x >> 7, col = threadIdx.x & 127;
+            if (half < (GATED ? 2 : 1) && (int)blockIdx.y * 128 + col < wide) {
+                float s = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s += sums[half][i][col];
+                a.part[(int64_t)((int)blockIdx.x + e) * N + half * wide + blockIdx.y * 128 + col] = s;
+            }
+        }
+    }
+}
+
+// db[e, n]: an expert's chunks in order. 64 columns a CTA, four threads a column.
+template <typename T>
+__global__ void __launch_bounds__(256) k_dbias(const LinearArgs a) {
+    __shared__ float sm[4][64];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int e = blockIdx.y, n = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+    const int b0 = a.offsets ? min(max(a.offsets[e], 0), a.d.T) : 0, b1 = a.offsets ? min(max(a.offsets[e + 1], 0), a.d.T) : a.d.T;
+    float s = 0.f;
+    if (b0 < b1 && n < a.d.N) {
+        const int c0 = b0 / kDzRows, c1 = (b1 - 1) / kDzRows + 1, per = (c1 - c0 + 3) / 4;
+#pragma unroll 4
+        for (int c = c0 + q * per; c < min(c1, c0 + (q + 1) * per); ++c) s += a.part[(int64_t)(c + e) * a.d.N + n];
+    }
+    sm[q][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (q == 0 && n < a.d.N) {
+        const int i = threadIdx.x;
+        reinterpret_cast<T*>(a.dbias)[(int64_t)e * a.d.N + n] = from_f<T>((sm[0][i] + sm[1][i]) + (sm[2][i] + sm[3][i]));
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// host side
+
+namespace {
+
+template <typename T, int MODE, bool GATED, int NB>
+cudaError_t launch_k(const CUtensorMap& A, const CUtensorMap& B, const LinView& v, int grid, int split, cudaStream_t s) {
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(k_linear<T, MODE, GATED, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LinSmem<NB>::kBytes);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = LinSmem<NB>::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_linear<T, MODE, GATED, NB>, A, B, v);
+}
+
+struct LinPlan {
+    int nb, colw, grid, split;
+};
+
+// Columns of a tile, CTAs, and CTAs to one tile's contraction. groups: how many experts have rows, about; cols:
+// columns of one of them, about; blocks: 64-deep steps of the contraction, about. A tile costs its
+// columns (64 at least: below, its weights' 128 rows bound the step), and the GPU takes num_sms tiles at a
+// time; among equal costs the wider tile reads less. Where even 64-column tiles leave half the SMs idle, clusters split the contraction.
+LinPlan lin_plan(int64_t groups, int64_t cols, int ftiles, int blocks, int num_sms) {
+    LinPlan p = {256, 256, num_sms, 1};
+    int64_t best = INT64_MAX;
+    for (int w = 256; w >= 64; w /= 2) {
+        const int64_t tiles = groups * ftiles * ((cols + w - 1) / w), cost = (tiles + num_sms - 1) / num_sms * w;
+        if (cost < best) {
+            best = cost;
+            p.colw = w;
+        }
+    }
+    if (cols <= 64) p.colw = 64;
+    p.nb = p.colw > 64 ? 256 : 64;
+    const int64_t tiles = groups * ftiles * ((cols + p.colw - 1) / p.colw);
+    if (p.nb == 64)
+        while (p.split < 8 && tiles * p.split * 2 <= num_sms && p.split * 2 <= blocks) p.split *= 2;
+    p.grid = (int)(tiles * p.split < num_sms ? tiles * p.split : num_sms) / p.split * p.split;
+    return p;
+}
+
+template <typename T, int MODE, bool GATED>
+cudaError_t launch_nb(const LinPlan& p, const CUtensorMap& A, const CUtensorMap& B, LinView v, cudaStream_t s) {
+    v.colw = p.colw;
+    return p.nb == 256 ? launch_k<T, MODE, GATED, 256>(A, B, v, p.grid, p.split, s) : launch_k<T, MODE, GATED, 64>(A, B, v, p.grid, p.split, s);
+}
+
+// Row-major [rows, cols] with `pitch` elements between rows.
+bool map_2d(CUtensorMap* m, int32_t dt, const void* p, uint64_t rows, uint64_t cols, uint64_t pitch, uint32_t box_rows) {
+    const uint64_t d[2] = {cols, rows}, st[1] = {pitch * 2};
+    const uint32_t b[2] = {64, box_rows};
+    return encode_map(m, dt, p, 2, d, st, b);
+}
+// W [E, N, K].
+bool map_w(CUtensorMap* m, const moe_linear_dims& d, const void* w, uint32_t box_rows) {
+    const uint64_t dim[3] = {(uint64_t)d.K, (uint64_t)d.N, (uint64_t)d.E}, st[2] = {(uint64_t)d.K * 2, (uint64_t)d.N * d.K * 2};
+    const uint32_t b[3] = {64, box_rows, 1};
+    return encode_map(m, d.dtype, w, 3, dim, st, b);
+}
+// W [E, 2, I / 16, 16, K] as tiles of 64 gate and 64 up rows in turns of 16.
+bool map_w_gated(CUtensorMap* m, const moe_linear_dims& d, const void* w) {
+    const uint64_t K = d.K, I = d.N / 2;
+    const uint64_t dim[5] = {K, 16, 2, I / 16, (uint64_t)d.E}, st[4] = {K * 2, I * K * 2, 16 * K * 2, 2 * I * K * 2};
+    const uint32_t b[5] = {64, 16, 2, 4, 1};
+    return encode_map(m, d.dtype, w, 5, dim, st, b);
+}
+
+LinView view_of(const LinearArgs& a) {
+    LinView v = {};
+    v.offsets = a.offsets;
+    v.T = a.d.T;
+    v.E = a.d.E;
+    v.N = a.d.N;
+    v.err = a.err;
+    v.wait_ns = a.wait_ns;
+    return v;
+}
+
+// Experts with rows, about, and the rows of one, about.
+int64_t groups_of(const LinearArgs& a) { return a.offsets ? (a.d.E < a.d.T ? a.d.E : a.d.T) : 1; }
+
+template <typename T>
+cudaError_t linear_t(const LinearArgs& a, cudaStream_t s) {
+    const bool gated = a.d.act == MOE_ACT_SWIGLU;
+    CUtensorMap A, B;
+    if (!(gated ? map_w_gated(&A, a.d, a.w) : map_w(&A, a.d, a.w, 128)) || !map_2d(&B, a.d.dtype, a.x, a.d.T, a.d.K, a.d.K, kLinBoxRows))
+        return cudaErrorInvalidValue;
+    LinView v = view_of(a);
+    v.bias = a.bias;
+    v.residual = a.residual;
+    v.out = a.out;
+    v.z = a.z;
+    v.F = gated ? a.d.N / 2 : a.d.N;
+    v.C = a.d.K;
+    v.act = a.d.act;
+    v.vec = a.d.N % 4 == 0;
+    v.ftiles = gated ? (v.F + 63) / 64 : (v.F + 127) / 128;
+    v.suppress = a.suppress;
+    const int64_t g = groups_of(a);
+    const LinPlan p = lin_plan(g, (a.d.T + g - 1) / g, v.ftiles, (v.C + 63) / 64, a.num_sms);
+    cudaError_t e;
+    MOE_LAUNCH(MOE_KERNEL_LINEAR, s, (e = gated ? launch_nb<T, kFwd, true>(p, A, B, v, s) : launch_nb<T, kFwd, false>(p, A, B, v, s)));
+    return e;
+}
+
+template <typename T, int VE, bool GATED>
+cudaError_t launch_dz(const LinearArgs& a, int pitch, cudaStream_t s) {
+    const int wide = GATED ? a.d.N / 2 : a.d.N;
+    return launch_pdl(k_dz<T, VE, GATED>, dim3((a.d.T + kDzRows - 1) / kDzRows, (wide + 127) / 128), dim3(256), 0, s, a, pitch);
+}
+
+template <typename T>
+cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
+    LinearArgs a = in;
+    const moe_linear_dims& d = a.d;
+    const bool gated = d.act == MOE_ACT_SWIGLU, vec = d.N % 8 == 0 && (!gated || d.N % 16 == 0);
+    int pitch = (d.N + 7) / 8 * 8;
+    const bool plain = d.act == MOE_ACT_NONE && vec;  // dz is dout itself
+    if (plain || (!a.dx && !a.dw)) a.dz = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (a.dz || a.dbias) {
+        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s,
+                   (e = gated ? launch_dz<T, 8, true>(a, pitch, s) : vec ? launch_dz<T, 8, false>(a, pitch, s) : launch_dz<T, 1, false>(a, pitch, s)));
+        if (e == cudaSuccess && a.dbias)
+            MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_pdl(k_dbias<T>, dim3((d.N + 63) / 64, d.E), dim3(256), 0, s, a)));
+        if (e != cudaSuccess) return e;
+    }
+    const void* dz = plain ? a.dout : a.dz;
+    const int64_t g = groups_of(a);
+    CUtensorMap A, B;
+    LinView v = view_of(a);
+    v.vec = d.K % 4 == 0;
+    v.F = d.K;
+    v.ftiles = (d.K + 127) / 128;
+    if (a.dx) {
+        if (!map_w(&A, d, a.w, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, kLinBoxRows)) return cudaErrorInvalidValue;
+        v.out = a.dx;
+        v.C = d.N;
+        const LinPlan p = lin_plan(g, (d.T + g - 1) / g, v.ftiles, (v.C + 63) / 64, a.num_sms);
+        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_nb<T, kDx, false>(p, A, B, v, s)));
+        if (e != cudaSuccess) return e;
+    }
+    if (a.dw) {
+        if (!map_2d(&A, d.dtype, a.x, d.T, d.K, d.K, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, 64)) return cudaErrorInvalidValue;
+        v.out = a.dw;
+        v.C = 0;
+        const LinPlan p = lin_plan(d.E, d.N, v.ftiles, (int)(((d.T + g - 1) / g + 63) / 64), a.num_sms);
+        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_nb<T, kDw, false>(p, A, B, v, s)));
+    }
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+    return a.d.dtype == MOE_FP16 ? linear_t<fp16>(a, s) : linear_t<bf16>(a, s);
+}
+cudaError_t launch_linear_backward(const LinearArgs& a, cudaStream_t s) {
+    return a.d.dtype == MOE_FP16 ? linear_backward_t<fp16>(a, s) : linear_backward_t<bf16>(a, s);
+}
+
+}  // namespace moe

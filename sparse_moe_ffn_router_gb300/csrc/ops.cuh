@@ -1,0 +1,96 @@
+// ops.cuh -- what the exchange, norm and linear operators share: element types, vectors of them, and
+// the argument blocks passed from the C-ABI entry points to the launches.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "launch.h"
+
+namespace moe {
+
+typedef __half fp16;
+
+// Bytes of an element of moe_dtype, 0 for an unknown one.
+inline int elem_size(int32_t dtype) { return dtype == MOE_BF16 || dtype == MOE_FP16 ? 2 : dtype == MOE_FP32 ? 4 : 0; }
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(bf16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(fp16 v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ bf16 from_f<bf16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ fp16 from_f<fp16>(float v) { return __float2half_rn(v); }
+
+// VE elements moved by one load or store: 16 bytes where every row starts on 16 bytes, else one element.
+template <typename T, int VE>
+struct alignas(sizeof(T) * VE) Vec {
+    T v[VE];
+};
+#endif
+
+// ---- exchange (exchange.cu): tokens [T, H], rows [T * K, H], inv [T * K]
+struct ExchangeArgs {
+    const void* tok;       // token side, read: x, the residual, or the other factor of the dots
+    const void* rows;      // row side, read
+    const int32_t* inv;
+    const float* w;        // [T, K] or NULL
+    void* out;             // rows (spread) or tokens (gather)
+    float* dots;           // [T, K] or NULL
+    int T, K, H;
+    int num_sms;
+};
+cudaError_t launch_sort_pairs(const int32_t* ids, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, int P,
+                              int E, cudaStream_t s);
+// out[inv[t, k]] = (w) * tok[t]; dots[t, k] = tok[t] . rows[inv[t, k]]
+cudaError_t launch_spread(int32_t dtype, const ExchangeArgs& a, cudaStream_t s);
+// out[t] = (residual = tok when there are no dots) + sum_k (w) * rows[inv[t, k]]; dots as above
+cudaError_t launch_gather(int32_t dtype, const ExchangeArgs& a, cudaStream_t s);
+
+// ---- norm (norm.cu)
+struct NormArgs {
+    moe_norm_dims d;
+    const void *y, *residual, *gate, *gamma_post, *gamma_pre;
+    void *s, *xn;  // forward results
+    const void *s_in, *ds, *dxn;
+    void *dresidual, *dy, *dgate, *dgamma_post, *dgamma_pre;
+    float* part;  // [blocks, 3, H]
+    int num_sms;
+};
+constexpr int kNormBlocks = 304;  // row blocks of the backward pass, at most (two for each SM)
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t s);
+
+// ---- linear (linear.cu)
+struct LinearArgs {
+    moe_linear_dims d;
+    const void *x, *w, *bias, *residual;
+    const int32_t* offsets;  // [E + 1], or NULL: all T rows are the one matrix's
+    void *out, *z;           // forward results
+    const void *z_in, *dout;
+    void *dx, *dw, *dbias;
+    void* dz;                // [T, N rounded up to 8]: gradient of the pre-activation
+    float* part;             // [ceil(T / kDzRows) + E, N]: column sums of a chunk's rows of one expert
+    uint32_t* err;
+    uint64_t wait_ns;
+    int num_sms;
+    int suppress;            // testing aid: CTA 0 of the forward kernel never loads its first stage
+};
+constexpr int kDzRows = 64;  // rows of a chunk
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_linear_backward(const LinearArgs& a, cudaStream_t s);
+// A tensor map for TMA with 128-byte swizzle and zeros outside: dims and box innermost first, strides in
+// bytes of dims 1 .. rank - 1.
+bool encode_map(CUtensorMap* m, int32_t dtype, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box);
+
+// SMs of the current device, the time limit of bounded device waits, the signal held back in tests (api.cu).
+int device_sms();
+uint64_t device_wait_ns();
+int device_suppress();
+
+}  // namespace moe

@@ -184,6 +184,21 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, uint64_t
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t* bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* map, uint64_t* bar, int c0, int c1, int c2, int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, "
+        "%7}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
+
 // The same with an L2 cache policy (l2_evict_first / l2_evict_last).
 __device__ __forceinline__ void tma_load_2d_hint(void* dst, const void* map, uint64_t* bar, int c0, int c1,
                                                  uint64_t policy) {
@@ -309,6 +324,25 @@ __device__ __forceinline__ uint64_t sdesc_kmajor_sw128(uint32_t smem_addr) {
     d |= (uint64_t)1 << 46;                         // descriptor version of this tensor-core generation
     d |= (uint64_t)2 << 61;                         // 128-byte swizzle
     return d;
+}
+
+// Descriptor of an MN-major 16-bit tile written by TMA with 128-byte swizzling: panels of 64 M (or N) elements
+// (128 B) by K rows, one row after another; 8 K rows 1024 B apart, panels panel_bytes apart. A K offset of
+// 16 rows is added to the start address.
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t smem_addr, uint32_t panel_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(panel_bytes >> 4) << 16;  // leading byte offset: the next 64 M (or N) elements
+    d |= (uint64_t)(1024 >> 4) << 32;         // stride byte offset: the next 8 K rows
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Instruction descriptor: kind::f16 with bf16 (or fp16) A and B, fp32 D; an operand is K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(bool is_bf16, int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | (is_bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // Instruction descriptor: kind::f16 with bf16 A and B, fp32 D, both operands K-major.
