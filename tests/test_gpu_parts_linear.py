@@ -1,0 +1,223 @@
+"""Linear layers with bias, activation and residual, dense and by expert, and their gradients, against plain forms."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import sparse_moe_ffn_router_gb300 as moe
+from tests import parts_reference as ref
+
+pytestmark = pytest.mark.gpu
+DT = {moe.BF16: torch.bfloat16, moe.FP16: torch.float16}
+NAN = float("nan")
+
+
+def offsets_of(counts):
+    o = [0]
+    for c in counts:
+        o.append(o[-1] + c)
+    return torch.tensor(o, dtype=torch.int32, device="cuda")
+
+
+def inputs(d, bias=True, residual=True, seed=0):
+    dt, wide = DT[d.dtype], d.N // 2 if d.act == moe.ACT_SWIGLU else d.N
+    x, w = ref.randn(seed + 1, dt, d.T, d.K), ref.randn(seed + 2, dt, d.E, d.N, d.K, scale=d.K ** -0.5)
+    return x, w, ref.randn(seed + 3, dt, d.E, d.N) if bias else None, ref.randn(seed + 4, dt, d.T, wide) if residual else None
+
+
+def forward(d, x, w, bias, offsets, residual, fill=7.0, keep=True):
+    wide = d.N // 2 if d.act == moe.ACT_SWIGLU else d.N
+    out = torch.full((d.T, wide), fill, dtype=x.dtype, device="cuda")
+    z = torch.full((d.T, d.N), fill, dtype=x.dtype, device="cuda") if keep else None
+    ws = moe.new_linear_workspace(d)
+    moe.moe_linear(d, x, w, bias, offsets, residual, out, z, ws)
+    assert moe.moe_last_device_error(ws) == 0
+    return out, z
+
+
+def check_forward(d, x, w, bias, offsets, residual):
+    out, z = forward(d, x, w, bias, offsets, residual)
+    o64, z64, mo, mz = ref.linear(d, x, w, bias, offsets, residual)
+    n = d.T if offsets is None else int(offsets[-1])
+    ref.check(out[:n], o64[:n], mo[:n], d.K + 2, "out")
+    ref.check(z[:n], z64[:n], mz[:n], d.K + 2, "z")
+    assert bool((out[n:] == 7).all()) and bool((z[n:] == 7).all())
+    return z
+
+
+def check_backward(d, x, w, offsets, z, seed=9):
+    wide = d.N // 2 if d.act == moe.ACT_SWIGLU else d.N
+    dout = ref.randn(seed, x.dtype, d.T, wide)
+    n = d.T if offsets is None else int(offsets[-1])
+    dout[n:] = NAN  # rows of no expert are read into nothing
+    dx, dw, db = torch.full_like(x, 7.0), torch.full_like(w, 7.0), torch.full((d.E, d.N), 7.0, dtype=x.dtype, device="cuda")
+    ws = moe.new_linear_workspace(d, backward=True)
+    ws[512:] = 255  # the error word's line apart, it holds nothing yet: NaN in both types
+    moe.moe_linear_backward(d, x, w, offsets, z if d.act != moe.ACT_NONE else None, dout, dx, dw, db, ws)
+    assert moe.moe_last_device_error(ws) == 0
+    clean = torch.nan_to_num(dout)
+    want, bound = ref.linear_backward(d, x.nan_to_num(), w, offsets, z.nan_to_num() if d.act != moe.ACT_NONE else None, clean)
+    for name, g, r, b in zip(("dx", "dw", "db"), (dx[:n], dw, db), (want[0][:n], *want[1:]), (bound[0][:n], *bound[1:])):
+        off = (g.double() - r).abs()
+        assert not bool((~(off <= b)).any()), f"{name}: worst {float((off / b).max()):.2f} x the bound"
+    assert bool((dx[n:] == 7).all())
+    for keep in range(3):  # each gradient alone has the same bits
+        some = [torch.empty_like(t) if i == keep else None for i, t in enumerate((dx, dw, db))]
+        if keep == 0:
+            some[0].fill_(7.0)
+        moe.moe_linear_backward(d, x if keep == 1 else None, w if keep == 0 else None, offsets, z if d.act != moe.ACT_NONE else None, dout, *some, ws)
+        assert torch.equal(some[keep], (dx, dw, db)[keep])
+
+
+DENSE = [(1, 2048, 2048), (1, 1, 8), (2, 7, 16), (3, 130, 72), (15, 64, 64), (16, 257, 512), (17, 5003, 144), (31, 128, 1032), (33, 256, 200), (64, 1024, 2048), (65, 96, 88),
+         (100, 1000, 264), (129, 40, 1544), (255, 513, 96), (257, 2048, 512), (700, 1003, 1544), (1021, 2056, 72), (2500, 384, 640)]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("T,N,K", DENSE)
+def test_dense(dtype, T, N, K):
+    act = (moe.ACT_NONE, moe.ACT_RELU, moe.ACT_SILU, moe.ACT_GELU, moe.ACT_SIGMOID)[(T + N + K) % 5]
+    d = moe.LinearDims(T, N, K, act=act, dtype=dtype)
+    x, w, b, r = inputs(d, bias=T % 3 != 0, residual=T % 2 == 0)
+    check_backward(d, x, w, None, check_forward(d, x, w, b, None, r))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("act", range(6))
+@pytest.mark.parametrize("T", [5, 300])
+def test_activations(dtype, act, T):
+    d = moe.LinearDims(T, 160, 128, act=act, dtype=dtype)
+    x, w, b, r = inputs(d)
+    check_backward(d, x, w, None, check_forward(d, x, w, b, None, r))
+
+
+COUNTS = [[0, 1], [3, 0, 0, 5], [0, 0, 0], [1] * 40, [64, 65, 0, 63, 1], [16, 0, 17, 15, 256, 257, 100], [700, 1, 0, 2], [0, 0, 1000], [33] * 256]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("counts", COUNTS)
+@pytest.mark.parametrize("N,K,act", [(128, 64, moe.ACT_NONE), (96, 200, moe.ACT_SWIGLU), (77, 136, moe.ACT_SILU), (352, 72, moe.ACT_SWIGLU)])
+@pytest.mark.parametrize("spare", [0, 29])
+def test_experts(dtype, counts, N, K, act, spare):
+    """Experts without rows, with one, around 16, 64 and 256; rows behind the last expert's that hold NaN."""
+    off = offsets_of(counts)
+    T = int(off[-1]) + spare
+    if T == 0:
+        T = 4
+    d = moe.LinearDims(T, N, K, E=len(counts), act=act, dtype=dtype)
+    x, w, b, r = inputs(d)
+    n = int(off[-1])
+    x[n:] = NAN
+    z = check_forward(d, x, w, b, off, r)
+    z[n:] = NAN
+    check_backward(d, x, w, off, z)
+
+
+def test_one_expert_with_offsets_takes_a_part():
+    d = moe.LinearDims(90, 64, 64, act=moe.ACT_SILU)
+    x, w, b, r = inputs(d)
+    off = torch.tensor([7, 50], dtype=torch.int32, device="cuda")
+    out, z = forward(d, x, w, b, off, r)
+    whole, _ = forward(d, x, w, b, None, r)
+    assert torch.equal(out[7:50], whole[7:50]) and bool((out[:7] == 7).all()) and bool((out[50:] == 7).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_experts_do_not_reach_one_another(bad):
+    """Non-finite weights and rows of one expert stay in that expert's results: tiles read past its rows and columns."""
+    counts = [5, 70, 0, 33, 1]
+    off = offsets_of(counts)
+    d = moe.LinearDims(int(off[-1]), 100, 136, E=5)
+    x, w, b, _ = inputs(d, residual=False)
+    dout = ref.randn(5, x.dtype, d.T, d.N)
+    ws = moe.new_linear_workspace(d, backward=True)
+
+    def grads(x, w, dout):
+        dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+        moe.moe_linear_backward(d, x, w, off, None, dout, dx, dw, db, ws)
+        return dx, dw, db
+
+    out, _ = forward(d, x, w, b, off, None)
+    clean = grads(x, w, dout)
+    for e in (1, 3):
+        xb, wb, db_ = x.clone(), w.clone(), dout.clone()
+        a, c = int(off[e]), int(off[e + 1])
+        xb[a:c], wb[e], db_[a:c] = bad, bad, bad
+        rows = torch.ones(d.T, dtype=torch.bool, device="cuda")
+        rows[a:c] = False
+        others = [i for i in range(5) if i != e]
+        got, _ = forward(d, xb, wb, b, off, None)
+        assert torch.equal(got[rows], out[rows])
+        g = grads(xb, wb, db_)
+        assert torch.equal(g[0][rows], clean[0][rows]) and torch.equal(g[1][others], clean[1][others]) and torch.equal(g[2][others], clean[2][others])
+
+
+def test_residual_may_be_the_result():
+    for T in (3, 300):
+        d = moe.LinearDims(T, 200, 64, act=moe.ACT_GELU)
+        x, w, b, r = inputs(d)
+        out, _ = forward(d, x, w, b, None, r)
+        moe.moe_linear(d, x, w, b, None, r, r, None, moe.new_linear_workspace(d))
+        assert torch.equal(r, out)
+
+
+def test_offsets_out_of_order_are_flagged():
+    d = moe.LinearDims(64, 64, 64, E=3)
+    x, w, b, _ = inputs(d, residual=False)
+    ws = moe.new_linear_workspace(d)
+    out = torch.zeros(64, 64, dtype=x.dtype, device="cuda")
+    for off in ([0, 40, 20, 64], [0, 10, 20, 65], [-1, 10, 20, 64], [2 ** 31 - 1, -2 ** 31, 5, 6]):
+        moe.moe_linear(d, x, w, b, torch.tensor(off, dtype=torch.int32, device="cuda"), None, out, None, ws)
+        assert moe.moe_last_device_error(ws) == 7 and moe.moe_last_device_error(ws) == 0
+    moe.moe_linear(d, x, w, b, torch.tensor([0, 10, 20, 64], dtype=torch.int32, device="cuda"), None, out, None, ws)
+    assert moe.moe_last_device_error(ws) == 0
+
+
+def test_no_rows():
+    d = moe.LinearDims(0, 64, 64)
+    z, w = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(64, 64, dtype=torch.bfloat16, device="cuda")
+    moe.moe_linear(d, z, w, None, None, None, z, None, moe.new_linear_workspace(d))
+    dw, db = w.clone(), w[0].clone()
+    moe.moe_linear_backward(d, z, w, None, None, z, z, dw, db, moe.new_linear_workspace(d, backward=True))
+    assert not bool(dw.any()) and not bool(db.any())
+
+
+def test_gradients_against_differences():
+    """Central differences of the plain forward pass in 64 bits along random directions. Their error is h^2 / 6 of the third
+    derivative (below 2 for these functions of arguments of unit size: 1e-6 of the magnitudes with h = 1e-3 is ample); the
+    kernel's side carries the bounds of its rounding."""
+    d = moe.LinearDims(70, 64, 40, E=3, act=moe.ACT_SWIGLU, dtype=moe.FP16)
+    off = offsets_of([20, 0, 50])
+    x, w, b, _ = inputs(d, residual=False)
+    _, z = forward(d, x, w, b, off, None)
+    dout = ref.randn(8, x.dtype, 70, 32)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+    moe.moe_linear_backward(d, x, w, off, z, dout, dx, dw, db, moe.new_linear_workspace(d, backward=True))
+    _, bounds = ref.linear_backward(d, x, w, off, z, dout)
+    loss = lambda x, w, b: float((ref.linear(d, x, w, b, off, None)[0] * dout.double()).sum())  # noqa: E731
+    h, wide = 1e-3, [t.double() for t in (x, w, b)]
+    for i, (g, bound) in enumerate(zip((dx, dw, db), bounds)):
+        v = ref.randn(20 + i, torch.float64, *g.shape)
+        up, down = ([t + s * h * v if j == i else t for j, t in enumerate(wide)] for s in (1, -1))
+        diff = (loss(*up) - loss(*down)) / (2 * h)
+        # the z that the pass kept is rounded: its slopes are off by half a step of z times the second derivative (below 1.2)
+        kept = 2 * ref.unit(x.dtype) * float((g.double().abs() * v.abs()).sum()) * 4
+        assert abs(diff - float((g.double() * v).sum())) <= float((bound * v.abs()).sum()) + kept + 1e-6 * float((g.double() * v).abs().sum())
+
+
+def test_a_held_back_load_ends_in_an_error():
+    """A stage that never fills: the kernel gives up after the limit and says so, and the next call is whole."""
+    for T in (1, 300):
+        d = moe.LinearDims(T, 2048, 1024)
+        x, w, b, r = inputs(d)
+        out, _ = forward(d, x, w, b, None, r, keep=False)
+        ws = moe.new_linear_workspace(d)
+        again = torch.empty_like(out)
+        try:
+            moe.moe_test_set_wait(2_000_000, moe.TEST_SUPPRESS_STAGE)
+            moe.moe_linear(d, x, w, b, None, r, again, None, ws)
+            assert moe.moe_last_device_error(ws) == 6
+        finally:
+            moe.moe_test_set_wait()
+        moe.moe_linear(d, x, w, b, None, r, again, None, ws)
+        assert moe.moe_last_device_error(ws) == 0 and torch.equal(again, out)
