@@ -19,160 +19,22 @@
 // warp 1 issues the MMAs into one of two accumulators in tensor memory, warps 4 - 11 write the other out.
 // With few tiles (decode) a cluster of up to 8 CTAs takes one tile's contraction in parts; the parts are added
 // in rank order through distributed shared memory. Sums are fp32 in a fixed order throughout.
-#include <type_traits>
-
-#include "ops.cuh"
-#include "sm100.cuh"
+#include "linear.cuh"
 
 namespace moe {
 
-enum { kFwd = 0, kDx = 1, kDw = 2 };
-
-constexpr int kLinThreads = 384, kLinEpiWarp0 = 4, kLinEpiWarps = 8;
-constexpr int kLinMaxE = 256;
-constexpr uint32_t kLinA = 128 * 64 * 2;  // a stage's feature side
-constexpr int kLinBoxRows = 32;           // token rows of one TMA box
 constexpr int kPartPitch = 132;           // floats of a column of the cluster's partial tile (4 mod 32: no bank conflicts)
 constexpr int kStagePitch = 36;           // floats of a column of a warp's transposition buffer (the same)
 
-// NB: columns of a tile, at most. 256 for many rows; 64 for few, with a deeper ring and the split contraction.
-template <int NB>
-struct LinSmem {
-    static constexpr uint32_t kB = NB * 64 * 2;
-    static constexpr int kStages = NB == 256 ? 4 : 7;
-    static constexpr uint32_t kRing = kStages * (kLinA + kB);
-    static constexpr uint32_t kScratch = NB == 256 ? kLinEpiWarps * 16 * kStagePitch * 4 : NB * kPartPitch * 4;
-    static constexpr uint32_t kTables = 2 * (kLinMaxE + 4) * 4;
-    static constexpr uint32_t kBytes = 1024 + kRing + kScratch + kTables + 256;
-    static constexpr uint32_t kTmem = 2 * NB;
-};
-
-// One launch's view of the operands.
-struct LinView {
-    const int32_t* offsets;
-    const void *bias, *residual;
-    void *out, *z;
-    int T, E, N;      // token rows, experts, W's rows
-    int F;            // features: contiguous extent of out
-    int C;            // contraction (kFwd, kDx)
-    int colw;         // columns of a tile, at most (a multiple of 16)
-    int ftiles;
-    int act;
-    int vec;          // rows of out, residual and z start on 8 bytes
-    int suppress;     // testing aid: CTA 0 never loads its first stage
-    uint32_t* err;
-    uint64_t wait_ns;
-};
-
-struct LinTile {
-    int e, f, c0, cols, row0, blocks, rows;  // expert, feature tile, first column, columns, first token row, 64-deep blocks, the expert's rows
-};
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// 16 bytes at the same shared-memory address in CTA `rank` of the cluster.
-__device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
-    float4 v;
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\t"
-        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
-        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-        : "r"(addr), "r"(rank)
-        : "memory");
-    return v;
-}
-
-__device__ __forceinline__ float lin_sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
-__device__ __forceinline__ float lin_act(int act, float z) {
-    switch (act) {
-        case MOE_ACT_SIGMOID: return lin_sigmoid(z);
-        case MOE_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
-        case MOE_ACT_SILU: return z * lin_sigmoid(z);
-        case MOE_ACT_GELU: return 0.5f * z * erfcf(-0.70710678f * z);
-        default: return z;
-    }
-}
-__device__ __forceinline__ float lin_slope(int act, float z) {
-    switch (act) {
-        case MOE_ACT_SIGMOID: { const float p = lin_sigmoid(z); return p * (1.f - p); }
-        case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-        case MOE_ACT_SILU: { const float p = lin_sigmoid(z); return p * (1.f + z * (1.f - p)); }
-        case MOE_ACT_GELU: return 0.5f * erfcf(-0.70710678f * z) + z * 0.39894228f * expf(-0.5f * z * z);
-        default: return 1.f;
-    }
-}
-
-// Columns of each of an expert's tiles: as even as steps of 16 allow.
-__device__ __forceinline__ int lin_width(int cols, int tiles) { return ((cols + tiles - 1) / tiles + 15) / 16 * 16; }
-
-// Row boundaries of the experts and first tile of each, in shared memory; every bound is within [0, T].
-template <int MODE>
-__device__ void lin_tables(const LinView& a, int* off, int* start) {
-    const int e = threadIdx.x;
-    if (e <= a.E) {
-        const int o = a.offsets ? a.offsets[e] : e ? a.T : 0;
-        const int c = min(max(o, 0), a.T);
-        if (c != o) atomicOr(a.err, ERR_BAD_ROUTE);
-        off[e] = c;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int run = 0;
-        for (int b = 0; b < a.E; b += 32) {
-            const int i = b + lane;
-            int n = 0;
-            if (i < a.E) {
-                const int rows = off[i + 1] - off[i];
-                if (rows < 0) atomicOr(a.err, ERR_BAD_ROUTE);
-                const int cols = MODE == kDw ? a.N : max(rows, 0);
-                n = (cols + a.colw - 1) / a.colw * a.ftiles;
-            }
-            int v = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += y;
-            }
-            if (i < a.E) start[i] = run + v - n;
-            run += __shfl_sync(0xffffffffu, v, 31);
-        }
-        if (lane == 0) start[a.E] = run;
-    }
-    __syncthreads();
-}
-
-template <int MODE>
-__device__ __forceinline__ LinTile lin_tile(const LinView& a, const int* off, const int* start, int t) {
-    int lo = 0, hi = a.E;  // start[lo] <= t < start[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= t) lo = mid; else hi = mid;
-    }
-    LinTile r;
-    r.e = lo;
-    r.row0 = off[lo];
-    r.rows = max(off[lo + 1] - r.row0, 0);
-    const int cols = MODE == kDw ? a.N : r.rows;
-    const int n = (cols + a.colw - 1) / a.colw, local = t - start[lo], width = lin_width(cols, n);
-    r.f = local / n;
-    r.c0 = (local - r.f * n) * width;
-    r.cols = min(width, cols - r.c0);
-    r.blocks = ((MODE == kDw ? r.rows : a.C) + 63) / 64;
-    return r;
-}
+// Columns of a tile, at most, and the ring: 16 KB of weights a stage, 112 KB on their way.
+constexpr int kLinCols = 64, kLinStages = 7;
+constexpr uint32_t kLinB = kLinCols * 64 * 2;
+constexpr uint32_t kLinRing = kLinStages * (kLinA + kLinB);
+constexpr uint32_t kLinScratch = kLinCols * kPartPitch * 4;
+constexpr uint32_t kLinTables = 2 * (kLinMaxE + 4) * 4;
+constexpr uint32_t kLinBytes = 1024 + kLinRing + kLinScratch + kLinTables + 256;
+constexpr uint32_t kLinTmem = 2 * kLinCols;
+static_assert(kLinEpiWarps * 16 * kStagePitch * 4 <= kLinScratch, "transposition buffers");
 
 // Four consecutive features of one row of the result, from their sums v (and the up sums u).
 template <typename T, bool GATED>
@@ -235,21 +97,19 @@ __device__ __forceinline__ void lin_bias_up(const LinView& a, int e, int f, floa
     for (int i = 0; i < 4; ++i) b[i] = a.bias && f + i < a.F ? to_f(reinterpret_cast<const T*>(a.bias)[(int64_t)e * a.N + a.F + f + i]) : 0.f;
 }
 
-template <typename T, int MODE, bool GATED, int NB>
+template <typename T, int MODE, bool GATED>
 __global__ void __launch_bounds__(kLinThreads, 1)
     k_linear(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB, const LinView a) {
-    typedef LinSmem<NB> S;
-    constexpr int kStages = S::kStages;
-    constexpr bool kCanSplit = NB == 64;
+    constexpr int kStages = kLinStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     uint8_t* sA = smem;
     uint8_t* sB = smem + kStages * kLinA;
-    float* scratch = reinterpret_cast<float*>(smem + S::kRing);
-    int* off = reinterpret_cast<int*>(smem + S::kRing + S::kScratch);
+    float* scratch = reinterpret_cast<float*>(smem + kLinRing);
+    int* off = reinterpret_cast<int*>(smem + kLinRing + kLinScratch);
     int* start = off + kLinMaxE + 4;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kRing + S::kScratch + S::kTables);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kLinRing + kLinScratch + kLinTables);
     uint64_t* empty = full + kStages;
     uint64_t* accf = empty + kStages;
     uint64_t* acce = accf + 2;
@@ -259,7 +119,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     static_assert((2 * kStages + 5) * 8 + 8 <= 256, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = kCanSplit ? cluster_rank() : 0, split = kCanSplit ? cluster_size() : 1;
+    const uint32_t rank = cluster_rank(), split = cluster_size();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -276,7 +136,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         tma_prefetch_desc(&mB);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, S::kTmem);
+        tmem_alloc(tmem_slot, kLinTmem);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -298,7 +158,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int s = 0; s < kStages; ++s) issued[s] = false;
         for (int t = first; t < total; t += step) {
             if (lane == 0 && !*abort_flag) {
-                const LinTile ti = lin_tile<MODE>(a, off, start, t);
+                const LinTile ti = lin_tile<MODE, 16>(a, off, start, t);
                 const int kb0 = (int)((int64_t)ti.blocks * rank / split), kb1 = (int)((int64_t)ti.blocks * (rank + 1) / split);
                 const int boxes = MODE == kDw ? (ti.cols + 63) / 64 : (ti.cols + kLinBoxRows - 1) / kLinBoxRows;
                 const uint32_t bytes = kLinA + (uint32_t)boxes * (MODE == kDw ? 64 : kLinBoxRows) * 128u;
@@ -313,7 +173,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     if (a.suppress && blockIdx.x == 0 && it == 0) continue;
                     mbar_arrive_expect_tx(&full[s], bytes);
                     uint8_t* da = sA + s * kLinA;
-                    uint8_t* db = sB + s * S::kB;
+                    uint8_t* db = sB + s * kLinB;
                     if (MODE == kFwd) {
                         if (GATED)
                             tma_load_5d(da, &mA, &full[s], kb * 64, 0, 0, ti.f * 4, ti.e);
@@ -334,7 +194,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 }
             }
             __syncwarp();
-            if (kCanSplit && split > 1) {
+            if (split > 1) {
                 cluster_sync_all();
                 cluster_sync_all();
             }
@@ -352,13 +212,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             bool ok = !*abort_flag;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (ok) {
-                const LinTile ti = lin_tile<MODE>(a, off, start, t);
+                const LinTile ti = lin_tile<MODE, 16>(a, off, start, t);
                 const int kb0 = (int)((int64_t)ti.blocks * rank / split), kb1 = (int)((int64_t)ti.blocks * (rank + 1) / split);
                 const int n16 = (ti.cols + 15) / 16 * 16;
                 const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 128, n16, MODE != kFwd, MODE == kDw);
                 const int b = local & 1;
                 const uint32_t use = (uint32_t)(local >> 1) & 1u;
-                const uint32_t d = tmem + (uint32_t)(b * NB);
+                const uint32_t d = tmem + (uint32_t)(b * kLinCols);
                 ok = mbar_wait(&acce[b], use ^ 1u, a.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
@@ -368,7 +228,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     ok = mbar_wait(&full[s], ph, a.wait_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    const uint32_t aa = smem_u32(sA + s * kLinA), bb = smem_u32(sB + s * S::kB);
+                    const uint32_t aa = smem_u32(sA + s * kLinA), bb = smem_u32(sB + s * kLinB);
                     int steps = 4;
                     if (MODE == kDw) {
                         // the expert's last block: 16 rows at a time, rows of the next expert in the last 16 set
@@ -407,7 +267,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 }
                 __syncwarp();
             }
-            if (kCanSplit && split > 1) {
+            if (split > 1) {
                 cluster_sync_all();
                 cluster_sync_all();
             }
@@ -423,7 +283,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         float* mine = scratch + (warp - kLinEpiWarp0) * 16 * kStagePitch;
         int local = 0;
         for (int t = first; t < total; t += step, ++local) {
-            const LinTile ti = lin_tile<MODE>(a, off, start, t);
+            const LinTile ti = lin_tile<MODE, 16>(a, off, start, t);
             const int kb0 = (int)((int64_t)ti.blocks * rank / split), kb1 = (int)((int64_t)ti.blocks * (rank + 1) / split);
             const int b = local & 1;
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
@@ -431,7 +291,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             // a lane's four features: those of chunk lane % 8 (gated: lane % 4) of the warp's 32 lanes
             const int f = GATED ? ti.f * 64 + q * 16 + (lane & 3) * 4 : ti.f * 128 + q * 32 + (lane & 7) * 4;
             float bv[4], bu[4];
-            if (!(kCanSplit && split > 1)) {
+            if (split == 1) {
                 lin_bias<T>(a, ti.e, f, bv);
                 if (GATED) lin_bias_up<T>(a, ti.e, f, bu);
             }
@@ -444,7 +304,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             if (ready) {
                 tc_fence_after();
-                const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NB);
+                const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kLinCols);
                 for (int c = h * 16; c < ti.cols; c += 32) {
                     uint32_t r[16];
                     if (kb0 < kb1) {
@@ -455,7 +315,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) r[i] = 0u;
                     }
-                    if (kCanSplit && split > 1) {
+                    if (split > 1) {
                         float* p = scratch + c * kPartPitch + q * 32;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)  // register i: lane g + 8 (i / 2 % 2) + 16 (i / 8), column 8 (i / 4 % 2) + 2 tt + i % 2
@@ -485,7 +345,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acce[b]);
             }
-            if (kCanSplit && split > 1) {
+            if (split > 1) {
                 __syncwarp();
                 cluster_sync_all();
                 if (ready) {
@@ -515,7 +375,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 cluster_sync_all();
             }
         }
-    } else if (kCanSplit && split > 1) {
+    } else if (split > 1) {
         for (int t = first; t < total; t += step) {
             cluster_sync_all();
             cluster_sync_all();
@@ -525,7 +385,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, S::kTmem);
+        tmem_dealloc(tmem, kLinTmem);
     }
 }
 
@@ -654,20 +514,20 @@ __global__ void __launch_bounds__(256) k_dbias(const LinearArgs a) {
 
 namespace {
 
-template <typename T, int MODE, bool GATED, int NB>
+template <typename T, int MODE, bool GATED>
 cudaError_t launch_k(const CUtensorMap& A, const CUtensorMap& B, const LinView& v, int grid, int split, cudaStream_t s) {
     static bool configured[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(k_linear<T, MODE, GATED, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LinSmem<NB>::kBytes);
+        cudaError_t e = cudaFuncSetAttribute(k_linear<T, MODE, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinBytes);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = LinSmem<NB>::kBytes;
+    cfg.dynamicSmemBytes = kLinBytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -677,40 +537,49 @@ cudaError_t launch_k(const CUtensorMap& A, const CUtensorMap& B, const LinView& 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_linear<T, MODE, GATED, NB>, A, B, v);
+    return cudaLaunchKernelEx(&cfg, k_linear<T, MODE, GATED>, A, B, v);
 }
 
 struct LinPlan {
-    int nb, colw, grid, split;
+    bool pair;
+    int colw, grid, split, width;  // columns of a tile, at most; CTAs; CTAs to a tile's contraction; columns of a tile as they are cut
 };
 
-// Columns of a tile, CTAs, and CTAs to one tile's contraction. groups: how many experts have rows, about; cols:
-// columns of one of them, about; blocks: 64-deep steps of the contraction, about. A tile costs its
-// columns (64 at least: below, its weights' 128 rows bound the step), and the GPU takes num_sms tiles at a
-// time; among equal costs the wider tile reads less. Where even 64-column tiles leave half the SMs idle, clusters split the contraction.
-LinPlan lin_plan(int64_t groups, int64_t cols, int ftiles, int blocks, int num_sms) {
-    LinPlan p = {256, 256, num_sms, 1};
-    int64_t best = INT64_MAX;
+// Which kernel, and its tiles. groups: experts with rows, about; cols: columns of one of them, about; F: features
+// (lanes) in weight rows; blocks: 64-deep steps of the contraction, about.
+// Time of a 16-deep step, in clocks: on a pair, 256 features by w columns take w / 2 on the tensor cores and
+// (8 KB + 32 w B) / 128 B through each SM's shared memory (TMA's writes and the tensor core's reads of
+// its half), which measured times follow as 64 + w / 4; one SM's 128 x 64 take 96. A wave of tiles costs its widest. With
+// 64 columns or fewer the weights' way from HBM is what counts: one SM a tile, and clusters that split the contraction while SMs are idle.
+LinPlan lin_plan(int64_t groups, int64_t cols, int64_t F, int blocks, int num_sms) {
+    LinPlan p = {false, kLinCols, 0, 1, 0};
+    const int64_t f1 = (F + 127) / 128, f2 = (F + 255) / 256;
+    const int64_t tiles = groups * f1 * ((cols + kLinCols - 1) / kLinCols);
+    while (p.split < 8 && tiles * p.split * 2 <= num_sms && p.split * 2 <= blocks) p.split *= 2;
+    p.grid = (int)(tiles * p.split < num_sms ? tiles * p.split : num_sms) / p.split * p.split;
+    if (cols <= kLinCols || num_sms < 2) return p;
+    int64_t best = (tiles * p.split + num_sms - 1) / num_sms * 96 / p.split;
     for (int w = 256; w >= 64; w /= 2) {
-        const int64_t tiles = groups * ftiles * ((cols + w - 1) / w), cost = (tiles + num_sms - 1) / num_sms * w;
+        const int64_t n = (cols + w - 1) / w, width = ((cols + n - 1) / n + 31) / 32 * 32, all = groups * f2 * n;
+        const int64_t cost = (all + num_sms / 2 - 1) / (num_sms / 2) * (64 + width / 4);
         if (cost < best) {
             best = cost;
-            p.colw = w;
+            p = {true, w, 2 * (int)(all < num_sms / 2 ? all : num_sms / 2), 1, (int)width};
         }
     }
-    if (cols <= 64) p.colw = 64;
-    p.nb = p.colw > 64 ? 256 : 64;
-    const int64_t tiles = groups * ftiles * ((cols + p.colw - 1) / p.colw);
-    if (p.nb == 64)
-        while (p.split < 8 && tiles * p.split * 2 <= num_sms && p.split * 2 <= blocks) p.split *= 2;
-    p.grid = (int)(tiles * p.split < num_sms ? tiles * p.split : num_sms) / p.split * p.split;
     return p;
 }
 
+// Rows of the pair kernel's column-side box: a CTA's half of a tile where all tiles are alike, else 32.
+int pair_boxes(const LinPlan& p, bool one_group) { return one_group && p.pair ? p.width / 2 : kLinBoxRows; }
+
 template <typename T, int MODE, bool GATED>
-cudaError_t launch_nb(const LinPlan& p, const CUtensorMap& A, const CUtensorMap& B, LinView v, cudaStream_t s) {
+cudaError_t launch_plan(int32_t dtype, const LinPlan& p, const CUtensorMap& A, const CUtensorMap& B, LinView v, cudaStream_t s) {
     v.colw = p.colw;
-    return p.nb == 256 ? launch_k<T, MODE, GATED, 256>(A, B, v, p.grid, p.split, s) : launch_k<T, MODE, GATED, 64>(A, B, v, p.grid, p.split, s);
+    const int per = (p.pair ? 256 : 128) / (GATED ? 2 : 1);
+    v.ftiles = (v.F + per - 1) / per;
+    v.vec = v.F % (p.pair ? 8 : 4) == 0;
+    return p.pair ? launch_pair(dtype, MODE, GATED, A, B, v, p.grid, s) : launch_k<T, MODE, GATED>(A, B, v, p.grid, p.split, s);
 }
 
 // Row-major [rows, cols] with `pitch` elements between rows.
@@ -750,9 +619,6 @@ int64_t groups_of(const LinearArgs& a) { return a.offsets ? (a.d.E < a.d.T ? a.d
 template <typename T>
 cudaError_t linear_t(const LinearArgs& a, cudaStream_t s) {
     const bool gated = a.d.act == MOE_ACT_SWIGLU;
-    CUtensorMap A, B;
-    if (!(gated ? map_w_gated(&A, a.d, a.w) : map_w(&A, a.d, a.w, 128)) || !map_2d(&B, a.d.dtype, a.x, a.d.T, a.d.K, a.d.K, kLinBoxRows))
-        return cudaErrorInvalidValue;
     LinView v = view_of(a);
     v.bias = a.bias;
     v.residual = a.residual;
@@ -761,13 +627,15 @@ cudaError_t linear_t(const LinearArgs& a, cudaStream_t s) {
     v.F = gated ? a.d.N / 2 : a.d.N;
     v.C = a.d.K;
     v.act = a.d.act;
-    v.vec = a.d.N % 4 == 0;
-    v.ftiles = gated ? (v.F + 63) / 64 : (v.F + 127) / 128;
     v.suppress = a.suppress;
     const int64_t g = groups_of(a);
-    const LinPlan p = lin_plan(g, (a.d.T + g - 1) / g, v.ftiles, (v.C + 63) / 64, a.num_sms);
+    const LinPlan p = lin_plan(g, (a.d.T + g - 1) / g, a.d.N, (v.C + 63) / 64, a.num_sms);
+    v.boxes = pair_boxes(p, !a.offsets);
+    CUtensorMap A, B;
+    if (!(gated ? map_w_gated(&A, a.d, a.w) : map_w(&A, a.d, a.w, 128)) || !map_2d(&B, a.d.dtype, a.x, a.d.T, a.d.K, a.d.K, v.boxes))
+        return cudaErrorInvalidValue;
     cudaError_t e;
-    MOE_LAUNCH(MOE_KERNEL_LINEAR, s, (e = gated ? launch_nb<T, kFwd, true>(p, A, B, v, s) : launch_nb<T, kFwd, false>(p, A, B, v, s)));
+    MOE_LAUNCH(MOE_KERNEL_LINEAR, s, (e = gated ? launch_plan<T, kFwd, true>(a.d.dtype, p, A, B, v, s) : launch_plan<T, kFwd, false>(a.d.dtype, p, A, B, v, s)));
     return e;
 }
 
@@ -797,23 +665,22 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
     const int64_t g = groups_of(a);
     CUtensorMap A, B;
     LinView v = view_of(a);
-    v.vec = d.K % 4 == 0;
     v.F = d.K;
-    v.ftiles = (d.K + 127) / 128;
     if (a.dx) {
-        if (!map_w(&A, d, a.w, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, kLinBoxRows)) return cudaErrorInvalidValue;
         v.out = a.dx;
         v.C = d.N;
-        const LinPlan p = lin_plan(g, (d.T + g - 1) / g, v.ftiles, (v.C + 63) / 64, a.num_sms);
-        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_nb<T, kDx, false>(p, A, B, v, s)));
+        const LinPlan p = lin_plan(g, (d.T + g - 1) / g, d.K, (v.C + 63) / 64, a.num_sms);
+        v.boxes = pair_boxes(p, !a.offsets);
+        if (!map_w(&A, d, a.w, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, v.boxes)) return cudaErrorInvalidValue;
+        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_plan<T, kDx, false>(d.dtype, p, A, B, v, s)));
         if (e != cudaSuccess) return e;
     }
     if (a.dw) {
         if (!map_2d(&A, d.dtype, a.x, d.T, d.K, d.K, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, 64)) return cudaErrorInvalidValue;
         v.out = a.dw;
         v.C = 0;
-        const LinPlan p = lin_plan(d.E, d.N, v.ftiles, (int)(((d.T + g - 1) / g + 63) / 64), a.num_sms);
-        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_nb<T, kDw, false>(p, A, B, v, s)));
+        const LinPlan p = lin_plan(d.E, d.N, d.K, (int)(((d.T + g - 1) / g + 63) / 64), a.num_sms);
+        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_plan<T, kDw, false>(d.dtype, p, A, B, v, s)));
     }
     return e;
 }

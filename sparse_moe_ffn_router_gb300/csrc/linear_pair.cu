@@ -1,0 +1,454 @@
+// linear_pair.cu -- the linear layers' products where there are rows enough: tiles of 256 features by up to 256
+// columns on pairs of SMs.
+//
+// The roles and operands are those of linear.cu; here two CTAs share a tile (tcgen05 cta_group::2). Each loads
+// its own 128 feature rows and half of the columns, so a 64-deep stage is 32 KB for 256 x 256 of the product's
+// tile: a tensor core reads 8 KB of shared memory for 128 cycles of work and TMA writes as much, which one SM
+// alone (16 KB of A and 32 KB of B a stage) cannot keep up with. The CTA of even rank issues the
+// MMAs of both; the other's warp 1 passes on that its half of a stage has landed.
+//
+// The epilogue reads accumulator fragments (a thread: two columns of one feature side by side), applies bias,
+// activation and residual in fp32 and transposes by stmatrix, 32 columns at a time, so that what is stored is
+// 16 bytes of features a lane; residual comes the same way back by ldmatrix. A warp's buffer is 2 KB, its 16-byte
+// chunks swizzled so that both sides go without bank conflicts.
+#include "linear.cuh"
+
+namespace moe {
+
+constexpr int kPairStages = 6;
+constexpr uint32_t kPairB = 128 * 64 * 2;  // half of the columns
+constexpr uint32_t kPairRing = kPairStages * (kLinA + kPairB);
+constexpr uint32_t kPairScratch = kLinEpiWarps * 2048;
+constexpr uint32_t kPairTables = 2 * (kLinMaxE + 4) * 4;
+constexpr uint32_t kPairBytes = 1024 + kPairRing + kPairScratch + kPairTables + 256;
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, bf16) { return pack_bf16x2(a, b); }
+__device__ __forceinline__ uint32_t pack2(float a, float b, fp16) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t u, bf16) { return make_float2(bf_lo(u), bf_hi(u)); }
+__device__ __forceinline__ float2 unpack2(uint32_t u, fp16) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+
+// Byte of 16-byte chunk `chunk` of row `row` in a warp's buffer: rows of 64 bytes (32 features), of 32 (16 features).
+__device__ __forceinline__ uint32_t at64(int row, int chunk) { return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4)); }
+__device__ __forceinline__ uint32_t at32(int row, int chunk) { return (uint32_t)(row * 32 + ((chunk ^ ((row >> 2) & 1)) << 4)); }
+
+// Eight features (16 bytes) to p, of which `left` exist.
+template <typename T>
+__device__ __forceinline__ void put8(T* p, const uint4& v, int left, bool vec) {
+    if (vec) {
+        if (left > 0) *reinterpret_cast<uint4*>(p) = v;
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+}
+template <typename T>
+__device__ __forceinline__ uint4 get8(const T* p, int left, bool vec) {
+    uint4 v = {0u, 0u, 0u, 0u};
+    if (vec) {
+        if (left > 0) v = *reinterpret_cast<const uint4*>(p);
+        return v;
+    }
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+    v.x = w[0]; v.y = w[1]; v.z = w[2]; v.w = w[3];
+    return v;
+}
+
+// A warp's part of a tile: 32 accumulator lanes (q), 32 columns at a time. row0: the result's row of the tile's
+// first column; fl: the CTA's first feature.
+template <typename T, int MODE, bool GATED>
+__device__ __forceinline__ void pair_epilogue(const LinView& a, uint32_t tmem, uint32_t buf, int q, int h, int e, int64_t row0, int fl, int cols,
+                                              bool any) {
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    constexpr bool kFull = MODE == kFwd;
+    constexpr int kWide = GATED ? 16 : 32;  // features of the warp
+    const int f0 = fl + q * kWide;
+    const bool vec = a.vec != 0;
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};  // of features g, g + 8 and g + 16, g + 24 (gated: the up rows of g, g + 8)
+    if (kFull && a.bias) {
+        const T* b = reinterpret_cast<const T*>(a.bias) + (int64_t)e * a.N;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int f = f0 + g + 8 * (GATED ? i & 1 : i);
+            if (f < a.F) bias[i] = to_f(b[f + (GATED && i >= 2 ? a.F : 0)]);
+        }
+    }
+    const int crow = GATED ? lane >> 1 : lane >> 2, cch = GATED ? lane & 1 : lane & 3;  // the lane's row and chunk of the result
+    const int left = a.F - f0 - cch * 8;                                                // features from its chunk on
+    constexpr int kRows = GATED ? 16 : 8, kRounds = 32 / kRows;
+    T* out = reinterpret_cast<T*>(a.out) + (row0 + crow) * a.F + f0 + cch * 8;
+    const T* res = kFull && a.residual ? reinterpret_cast<const T*>(a.residual) + (row0 + crow) * a.F + f0 + cch * 8 : nullptr;
+    T* z = nullptr;
+    int zleft = 0;
+    if (kFull && a.z) {  // rows of z hold 32 features of the warp: gated, 16 gate and the 16 up of the same features
+        const int zc = lane & 3, zf = GATED ? f0 + (zc & 1) * 8 + (zc >> 1) * a.F : f0 + zc * 8;
+        z = reinterpret_cast<T*>(a.z) + (row0 + (lane >> 2)) * a.N + zf;
+        zleft = a.F - f0 - (GATED ? zc & 1 : zc) * 8;
+    }
+    for (int c = h * 32; c < cols; c += 64) {
+        uint32_t r[32];  // 16 features (lanes) from 0 in r[0 .. 15], from 16 in r[16 .. 31]; each: column block b in [4 b ..]
+        uint4 rv[kRounds];
+        if (kFull && res) {
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i)
+                if (c + crow + i * kRows < cols) rv[i] = get8(res + (int64_t)(c + i * kRows) * a.F, left, vec);
+        }
+        if (any) {
+            tmem_ld_frag4(tmem + c, r);
+            tmem_ld_frag4(tmem + (16u << 16) + c, r + 16);
+            asm volatile("tcgen05.wait::ld.sync.aligned;"
+                         : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
+                           "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                           "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                           "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0u;
+        }
+        if (kFull && a.bias) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + bias[(i >> 4) * 2 + ((i >> 1) & 1)]);
+        }
+        if (kFull && z) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t p[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int i = (m >> 1) * 16 + b * 4 + (m & 1) * 2;
+                    p[m] = pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]), T());
+                }
+                stmatrix4_trans(buf + at64(8 * b + (lane & 7), lane >> 3), p[0], p[1], p[2], p[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = (lane >> 2) + 8 * i;
+                const uint4 v = lds128_smem(buf + at64(row, lane & 3));
+                if (c + row < cols) put8(z + (int64_t)(c + 8 * i) * a.N, v, zleft, vec);
+            }
+            __syncwarp();
+        }
+        if (kFull && res) {
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i) {
+                const uint32_t w[4] = {rv[i].x, rv[i].y, rv[i].z, rv[i].w};
+                if (c + crow + i * kRows < cols) sts128(buf + (GATED ? at32(crow + i * kRows, cch) : at64(crow + i * kRows, cch)), w);
+            }
+            __syncwarp();
+        }
+        // activation, residual, rounding: pairs of columns of a feature
+        uint32_t p[GATED ? 8 : 16];
+#pragma unroll
+        for (int k = 0; k < (GATED ? 2 : 4); ++k) {  // matrices of one ldmatrix / stmatrix: gated two blocks of 16 features, else one of 32
+            uint32_t rr[4];
+            const uint32_t at = GATED ? at32(16 * k + 8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1) : at64(8 * k + (lane & 7), lane >> 3);
+            if (kFull && res) ldmatrix4_trans(buf + at, rr);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                float v0, v1;
+                if (GATED) {
+                    const int i = (2 * k + (m >> 1)) * 4 + (m & 1) * 2;
+                    v0 = __uint_as_float(r[i]);
+                    v1 = __uint_as_float(r[i + 1]);
+                    v0 = v0 * lin_sigmoid(v0) * __uint_as_float(r[i + 16]);
+                    v1 = v1 * lin_sigmoid(v1) * __uint_as_float(r[i + 17]);
+                } else {
+                    const int i = (m >> 1) * 16 + k * 4 + (m & 1) * 2;
+                    v0 = __uint_as_float(r[i]);
+                    v1 = __uint_as_float(r[i + 1]);
+                    if (kFull) {
+                        v0 = lin_act(a.act, v0);
+                        v1 = lin_act(a.act, v1);
+                    }
+                }
+                if (kFull && res) {
+                    const float2 x = unpack2(rr[m], T());
+                    v0 += x.x;
+                    v1 += x.y;
+                }
+                p[k * 4 + m] = pack2(v0, v1, T());
+            }
+        }
+        if (kFull && res) __syncwarp();
+#pragma unroll
+        for (int k = 0; k < (GATED ? 2 : 4); ++k) {
+            const uint32_t at = GATED ? at32(16 * k + 8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1) : at64(8 * k + (lane & 7), lane >> 3);
+            stmatrix4_trans(buf + at, p[k * 4], p[k * 4 + 1], p[k * 4 + 2], p[k * 4 + 3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            const int row = crow + i * kRows;
+            const uint4 v = lds128_smem(buf + (GATED ? at32(row, cch) : at64(row, cch)));
+            if (c + row < cols) put8(out + (int64_t)(c + i * kRows) * a.F, v, left, vec);
+        }
+        __syncwarp();
+    }
+}
+
+template <typename T, int MODE, bool GATED>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    k_linear_pair(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB, const LinView a) {
+    constexpr int kStages = kPairStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + kStages * kLinA;
+    uint8_t* scratch = smem + kPairRing;
+    int* off = reinterpret_cast<int*>(scratch + kPairScratch);
+    int* start = off + kLinMaxE + 4;
+    uint64_t* full = reinterpret_cast<uint64_t*>(scratch + kPairScratch + kPairTables);  // this CTA's half of a stage has landed
+    uint64_t* other = full + kStages;   // even rank: so has the other's
+    uint64_t* empty = other + kStages;  // both CTAs' MMAs have read it
+    uint64_t* accf = empty + kStages;
+    uint64_t* acce = accf + 2;          // even rank: both CTAs' epilogues have read the accumulator
+    uint64_t* mma_done = acce + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((3 * kStages + 5) * 8 + 8 <= 256, "barrier area");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&other[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf[b], 1);
+            mbar_init(&acce[b], 2 * kLinEpiWarps);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&mA);
+        tma_prefetch_desc(&mB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // barriers of both CTAs are ready
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dep_wait();
+    grid_dep_launch();
+    lin_tables<MODE>(a, off, start);
+    const int total = start[a.E];
+    const int step = gridDim.x / 2, first = blockIdx.x / 2;
+
+    if (warp == 0) {
+        // ---------------- TMA producer of this CTA's halves
+        if (lane == 0) {
+            int it = 0;
+            uint32_t last_par[kStages];
+            bool issued[kStages];
+#pragma unroll
+            for (int s = 0; s < kStages; ++s) issued[s] = false;
+            for (int t = first; t < total && !*abort_flag; t += step) {
+                const LinTile ti = lin_tile<MODE, 32>(a, off, start, t);
+                const int half = (ti.cols + 31) / 32 * 16;  // columns of this CTA
+                const int c0 = ti.c0 + (int)rank * half, f = ti.f * 2 + (int)rank;
+                const int boxes = MODE == kDw ? (half + 63) / 64 : (half + a.boxes - 1) / a.boxes;
+                const uint32_t bytes = kLinA + (uint32_t)boxes * (MODE == kDw ? 64 : a.boxes) * 128u;
+                for (int kb = 0; kb < ti.blocks; ++kb, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t ph = (uint32_t)(it / kStages) & 1u;
+                    if (!mbar_wait(&empty[s], ph ^ 1u, a.wait_ns)) {
+                        atomicOr(a.err, ERR_TIMEOUT);
+                        *abort_flag = 1;
+                        break;
+                    }
+                    if (a.suppress && blockIdx.x == 0 && it == 0) continue;
+                    mbar_arrive_expect_tx(&full[s], bytes);
+                    uint8_t* da = sA + s * kLinA;
+                    uint8_t* db = sB + s * kPairB;
+                    if (MODE == kFwd) {
+                        if (GATED)
+                            tma_load_5d(da, &mA, &full[s], kb * 64, 0, 0, f * 4, ti.e);
+                        else
+                            tma_load_3d(da, &mA, &full[s], kb * 64, f * 128, ti.e);
+                    } else if (MODE == kDx) {
+                        for (int p = 0; p < 2; ++p) tma_load_3d(da + p * 8192, &mA, &full[s], f * 128 + p * 64, kb * 64, ti.e);
+                    } else {
+                        for (int p = 0; p < 2; ++p) tma_load_2d(da + p * 8192, &mA, &full[s], f * 128 + p * 64, ti.row0 + kb * 64);
+                    }
+                    if (MODE == kDw)
+                        for (int p = 0; p < boxes; ++p) tma_load_2d(db + p * 8192, &mB, &full[s], c0 + p * 64, ti.row0 + kb * 64);
+                    else
+                        for (int p = 0; p < boxes; ++p) tma_load_2d(db + p * a.boxes * 128, &mB, &full[s], kb * 64, ti.row0 + c0 + p * a.boxes);
+                    issued[s] = true;
+                    last_par[s] = ph;
+                }
+            }
+            // every copy this CTA issued must land before shared memory is released
+#pragma unroll
+            for (int s = 0; s < kStages; ++s)
+                if (issued[s] && !mbar_wait(&full[s], last_par[s], a.wait_ns)) atomicOr(a.err, ERR_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (even rank), or its counterpart that reports the other half of each stage
+        int it = 0, local = 0;
+        bool ok = true;
+        for (int t = first; t < total && ok; t += step, ++local) {
+            ok = __shfl_sync(0xffffffffu, (int)!*abort_flag, 0) != 0;
+            if (!ok) break;
+            const LinTile ti = lin_tile<MODE, 32>(a, off, start, t);
+            const int n32 = (ti.cols + 31) / 32 * 32;
+            const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 256, n32, MODE != kFwd, MODE == kDw);
+            const int b = local & 1;
+            const uint32_t use = (uint32_t)(local >> 1) & 1u;
+            const uint32_t d = tmem + (uint32_t)(b * 256);
+            if (rank == 0) {
+                ok = mbar_wait(&acce[b], use ^ 1u, a.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+            }
+            for (int kb = 0; ok && kb < ti.blocks; ++kb, ++it) {
+                const int s = it % kStages;
+                const uint32_t ph = (uint32_t)(it / kStages) & 1u;
+                ok = mbar_wait(&full[s], ph, a.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t aa = smem_u32(sA + s * kLinA), bb = smem_u32(sB + s * kPairB);
+                int steps = 4;
+                if (MODE == kDw) {
+                    // the expert's last block: 16 rows at a time, rows of the next expert in the last 16 set to zero in
+                    // both operands (whatever they hold: 0 x infinity would stay)
+                    const int left = ti.rows - kb * 64;
+                    if (left < 64) {
+                        steps = (left + 15) / 16;
+                        if (left & 15) {
+                            const int panels = 2 + (n32 / 2 + 63) / 64, rows = steps * 16 - left;
+                            const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+                            for (int i = lane; i < panels * rows * 8; i += 32) {
+                                const int p = i / (rows * 8), r = i - p * (rows * 8);
+                                sts128((p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)(left * 128 + r * 16), zero);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                }
+                if (rank != 0) {
+                    if (lane == 0) mbar_arrive_cluster(&other[s], 0);
+                    continue;
+                }
+                ok = mbar_wait(&other[s], ph, a.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    for (int kk = 0; kk < steps; ++kk) {
+                        const uint64_t da = MODE == kFwd ? sdesc_kmajor_sw128(aa + kk * 32) : sdesc_mnmajor_sw128(aa + kk * 2048, 8192);
+                        const uint64_t db = MODE == kDw ? sdesc_mnmajor_sw128(bb + kk * 2048, 8192) : sdesc_kmajor_sw128(bb + kk * 32);
+                        mma_f16_pair(d, da, db, idesc, (kb | kk) != 0);
+                    }
+                    mma_commit_pair(&empty[s]);
+                    if (kb + 1 == ti.blocks) mma_commit_pair(&accf[b]);
+                }
+                __syncwarp();
+            }
+            if (ok && ti.blocks == 0 && rank == 0 && lane < 2) mbar_arrive_cluster(&accf[b], lane);  // (no rows: zeros are written)
+            if (!ok && lane == 0) {
+                atomicOr(a.err, ERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            __syncwarp();
+        }
+        if (rank == 0) {
+            if (elect_one()) mma_commit_pair(mma_done);
+            __syncwarp();
+        }
+        if (!mbar_wait(mma_done, 0, a.wait_ns) && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
+        __syncwarp();
+    } else if (warp >= kLinEpiWarp0) {
+        // ---------------- epilogue of this CTA's features: lanes 32 q .. of the accumulator, every other 32 columns
+        const int q = warp & 3, h = (warp - kLinEpiWarp0) >> 2;
+        const uint32_t buf = smem_u32(scratch + (warp - kLinEpiWarp0) * 2048);
+        int local = 0;
+        for (int t = first; t < total; t += step, ++local) {
+            const LinTile ti = lin_tile<MODE, 32>(a, off, start, t);
+            const int b = local & 1;
+            const uint32_t use = (uint32_t)(local >> 1) & 1u;
+            const int64_t row0 = MODE == kDw ? (int64_t)ti.e * a.N + ti.c0 : (int64_t)ti.row0 + ti.c0;
+            bool ready = false;
+            if (!*abort_flag) ready = mbar_wait(&accf[b], use, a.wait_ns);
+            ready = __all_sync(0xffffffffu, ready);
+            if (!ready) {
+                if (lane == 0) {
+                    if (!*abort_flag) atomicOr(a.err, ERR_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            tc_fence_after();
+            pair_epilogue<T, MODE, GATED>(a, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 256), buf, q, h, ti.e, row0,
+                                          (ti.f * 2 + (int)rank) * (GATED ? 64 : 128), ti.cols, ti.blocks > 0);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(&acce[b], 0);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // neither CTA leaves while the other may still arrive on its barriers or read its tiles
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+template <typename T, int MODE, bool GATED>
+static cudaError_t launch_pair_k(const CUtensorMap& A, const CUtensorMap& B, const LinView& v, int grid, cudaStream_t s) {
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(k_linear_pair<T, MODE, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairBytes);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = kPairBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_linear_pair<T, MODE, GATED>, A, B, v);
+}
+
+template <typename T>
+static cudaError_t launch_pair_t(int mode, bool gated, const CUtensorMap& A, const CUtensorMap& B, const LinView& v, int grid, cudaStream_t s) {
+    if (mode == kDx) return launch_pair_k<T, kDx, false>(A, B, v, grid, s);
+    if (mode == kDw) return launch_pair_k<T, kDw, false>(A, B, v, grid, s);
+    return gated ? launch_pair_k<T, kFwd, true>(A, B, v, grid, s) : launch_pair_k<T, kFwd, false>(A, B, v, grid, s);
+}
+
+cudaError_t launch_pair(int32_t dtype, int mode, bool gated, const CUtensorMap& A, const CUtensorMap& B, const LinView& v, int grid,
+                        cudaStream_t s) {
+    return dtype == MOE_FP16 ? launch_pair_t<fp16>(mode, gated, A, B, v, grid, s) : launch_pair_t<bf16>(mode, gated, A, B, v, grid, s);
+}
+
+}  // namespace moe
