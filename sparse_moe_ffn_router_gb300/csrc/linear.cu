@@ -51,7 +51,8 @@ __device__ __forceinline__ void lin_finish(const LinView& a, int64_t row, int f,
     T* z = a.z ? reinterpret_cast<T*>(a.z) + row * a.N + f : nullptr;
     float o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = GATED ? v[i] * lin_sigmoid(v[i]) * u[i] : lin_act(a.act, v[i]);
+    for (int i = 0; i < 4; ++i) o[i] = GATED ? v[i] * lin_sigmoid(v[i]) * u[i] : v[i];
+    if (!GATED) lin_act<4>(a.act, o);
     if (a.vec && f + 4 <= a.F) {
         if (res) {
             const V r = *reinterpret_cast<const V*>(res);
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     lin_tables<MODE>(a, off, start);
     const int total = start[a.E];
     const int step = gridDim.x / split, first = blockIdx.x / split;
+    LinWalk<MODE, 16> walk;
 
     if (warp == 0) {
         // ---------------- TMA producer (one lane; the warp stays together for the cluster's barriers)
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int s = 0; s < kStages; ++s) issued[s] = false;
         for (int t = first; t < total; t += step) {
             if (lane == 0 && !*abort_flag) {
-                const LinTile ti = lin_tile<MODE, 16>(a, off, start, t);
+                const LinTile ti = walk.to(a, off, start, t);
                 const int kb0 = (int)((int64_t)ti.blocks * rank / split), kb1 = (int)((int64_t)ti.blocks * (rank + 1) / split);
                 const int boxes = MODE == kDw ? (ti.cols + 63) / 64 : (ti.cols + kLinBoxRows - 1) / kLinBoxRows;
                 const uint32_t bytes = kLinA + (uint32_t)boxes * (MODE == kDw ? 64 : kLinBoxRows) * 128u;
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             bool ok = !*abort_flag;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (ok) {
-                const LinTile ti = lin_tile<MODE, 16>(a, off, start, t);
+                const LinTile ti = walk.to(a, off, start, t);
                 const int kb0 = (int)((int64_t)ti.blocks * rank / split), kb1 = (int)((int64_t)ti.blocks * (rank + 1) / split);
                 const int n16 = (ti.cols + 15) / 16 * 16;
                 const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 128, n16, MODE != kFwd, MODE == kDw);
@@ -239,9 +241,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                             if (left & 15) {
                                 const int panels = 2 + (ti.cols + 63) / 64, rows = steps * 16 - left;
                                 const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-                                for (int i = lane; i < panels * rows * 8; i += 32) {
-                                    const int p = i / (rows * 8), r = i - p * (rows * 8);
-                                    sts128((p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)(left * 128 + r * 16), zero);
+                                for (int p = 0; p < panels; ++p) {
+                                    const uint32_t at = (p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)left * 128u;
+                                    for (int i = lane; i < rows * 8; i += 32) sts128(at + (uint32_t)i * 16u, zero);
                                 }
                                 fence_proxy_async_smem();
                                 __syncwarp();
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         float* mine = scratch + (warp - kLinEpiWarp0) * 16 * kStagePitch;
         int local = 0;
         for (int t = first; t < total; t += step, ++local) {
-            const LinTile ti = lin_tile<MODE, 16>(a, off, start, t);
+            const LinTile ti = walk.to(a, off, start, t);
             const int kb0 = (int)((int64_t)ti.blocks * rank / split), kb1 = (int)((int64_t)ti.blocks * (rank + 1) / split);
             const int b = local & 1;
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
@@ -395,28 +397,44 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // each, 16 rows at a time. Sums are of dz before its rounding, row block by row block: those of the rows of
 // expert e in chunk c go to part[c + e], a place of their own as chunks and experts follow one another.
 
+// Eight columns of a row, of which n exist.
 template <typename T, int VE>
-__device__ __forceinline__ void ld_cols(const T* p, int n, float (&v)[8]) {
+__device__ __forceinline__ Vec<T, 8> ld_cols(const T* p, int n) {
+    Vec<T, 8> x;
     if (VE == 8) {
-        const Vec<T, 8> x = *reinterpret_cast<const Vec<T, 8>*>(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f(x.v[i]);
+        x = *reinterpret_cast<const Vec<T, 8>*>(p);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f(p[i]) : 0.f;
+        for (int i = 0; i < 8; ++i) x.v[i] = i < n ? p[i] : from_f<T>(0.f);
     }
+    return x;
 }
 
 template <typename T, int VE, bool GATED>
 __global__ void __launch_bounds__(256) k_dz(const LinearArgs a, int pitch) {
     __shared__ int off[kLinMaxE + 1];
     __shared__ float sums[GATED ? 2 : 1][16][128];
+    constexpr int kMore = kDzRows / 16;  // rows of a thread, all loaded before the first is used
+    typedef Vec<T, 8> V;
     grid_dep_wait();
     grid_dep_launch();
     const int N = a.d.N, E = a.d.E, wide = GATED ? N / 2 : N;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int r0 = blockIdx.x * kDzRows, r1 = min(r0 + kDzRows, a.d.T);
     const int f = blockIdx.y * 128 + tx * 8, n = min(8, wide - f);  // columns of this thread (none: n <= 0)
+    const bool need_z = GATED || a.d.act != MOE_ACT_NONE;
+    T* dz = reinterpret_cast<T*>(a.dz);
+    const T *z = reinterpret_cast<const T*>(a.z_in), *dout = reinterpret_cast<const T*>(a.dout);
+    V dv[kMore], zv[kMore], uv[kMore];
+#pragma unroll
+    for (int k = 0; k < kMore; ++k) {
+        const int r = r0 + ty + 16 * k;
+        if (r < r1 && n > 0) {
+            dv[k] = ld_cols<T, VE>(dout + (int64_t)r * wide + f, n);
+            if (need_z) zv[k] = ld_cols<T, VE>(z + (int64_t)r * N + f, n);
+            if (GATED) uv[k] = ld_cols<T, VE>(z + (int64_t)r * N + wide + f, n);
+        }
+    }
     for (int e = threadIdx.x; e <= E; e += 256) off[e] = a.offsets ? min(max(a.offsets[e], 0), a.d.T) : e ? a.d.T : 0;
     __syncthreads();
     int lo = 0, hi = E;  // the last expert whose rows begin at or before r0
@@ -424,47 +442,46 @@ __global__ void __launch_bounds__(256) k_dz(const LinearArgs a, int pitch) {
         const int mid = (lo + hi) >> 1;
         if (off[mid] <= r0) lo = mid; else hi = mid;
     }
-    T* dz = reinterpret_cast<T*>(a.dz);
-    const T *z = reinterpret_cast<const T*>(a.z_in), *dout = reinterpret_cast<const T*>(a.dout);
     for (int e = lo; e < E && off[e] < r1; ++e) {
         const int b0 = max(off[e], r0), b1 = min(off[e + 1], r1);
         if (b0 >= b1) continue;
         float sv[8], su[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) sv[i] = su[i] = 0.f;
-        if (n > 0) {
-#pragma unroll 4
-            for (int r = b0 + ty; r < b1; r += 16) {
-                float d[8], v[8], u[8];
-                ld_cols<T, VE>(dout + (int64_t)r * wide + f, n, d);
-                if (GATED || a.d.act != MOE_ACT_NONE) ld_cols<T, VE>(z + (int64_t)r * N + f, n, v);
-                if (GATED) {
-                    ld_cols<T, VE>(z + (int64_t)r * N + wide + f, n, u);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float p = lin_sigmoid(v[i]), dd = d[i];
-                        d[i] = dd * u[i] * (p * (1.f + v[i] * (1.f - p)));
-                        u[i] = dd * (v[i] * p);
-                    }
-                } else if (a.d.act != MOE_ACT_NONE) {
+        for (int k = 0; k < kMore; ++k) {
+            const int r = r0 + ty + 16 * k;
+            if (r < b0 || r >= b1 || n <= 0) continue;
+            float d[8], v[8], u[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) d[i] *= lin_slope(a.d.act, v[i]);
-                }
+            for (int i = 0; i < 8; ++i) {
+                d[i] = to_f(dv[k].v[i]);
+                if (need_z) v[i] = to_f(zv[k].v[i]);
+            }
+            if (GATED) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    sv[i] += d[i];
-                    if (GATED) su[i] += u[i];
+                    const float p = lin_sigmoid(v[i]), dd = d[i];
+                    d[i] = dd * to_f(uv[k].v[i]) * (p * (1.f + v[i] * (1.f - p)));
+                    u[i] = dd * (v[i] * p);
                 }
-                if (dz) {
-                    Vec<T, 8> o;  // (columns up to the pitch are zeros)
+            } else {
+                lin_slope<8>(a.d.act, v, d);
+            }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o.v[i] = from_f<T>(i < n ? d[i] : 0.f);
-                    *reinterpret_cast<Vec<T, 8>*>(dz + (int64_t)r * pitch + f) = o;
-                    if (GATED) {
+            for (int i = 0; i < 8; ++i) {
+                sv[i] += d[i];
+                if (GATED) su[i] += u[i];
+            }
+            if (dz) {
+                V o;  // (columns up to the pitch are zeros)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) o.v[i] = from_f<T>(u[i]);
-                        *reinterpret_cast<Vec<T, 8>*>(dz + (int64_t)r * pitch + wide + f) = o;
-                    }
+                for (int i = 0; i < 8; ++i) o.v[i] = from_f<T>(i < n ? d[i] : 0.f);
+                *reinterpret_cast<V*>(dz + (int64_t)r * pitch + f) = o;
+                if (GATED) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o.v[i] = from_f<T>(u[i]);
+                    *reinterpret_cast<V*>(dz + (int64_t)r * pitch + wide + f) = o;
                 }
             }
         }

@@ -145,6 +145,13 @@ __device__ __forceinline__ void pair_epilogue(const LinView& a, uint32_t tmem, u
             __syncwarp();
         }
         // activation, residual, rounding: pairs of columns of a feature
+        float v[GATED ? 16 : 32];
+#pragma unroll
+        for (int i = 0; i < (GATED ? 16 : 32); ++i) {
+            v[i] = __uint_as_float(r[i]);
+            if (GATED) v[i] *= lin_sigmoid(v[i]) * __uint_as_float(r[i + 16]);
+        }
+        if (kFull && !GATED) lin_act<GATED ? 16 : 32>(a.act, v);
         uint32_t p[GATED ? 8 : 16];
 #pragma unroll
         for (int k = 0; k < (GATED ? 2 : 4); ++k) {  // matrices of one ldmatrix / stmatrix: gated two blocks of 16 features, else one of 32
@@ -153,22 +160,8 @@ __device__ __forceinline__ void pair_epilogue(const LinView& a, uint32_t tmem, u
             if (kFull && res) ldmatrix4_trans(buf + at, rr);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                float v0, v1;
-                if (GATED) {
-                    const int i = (2 * k + (m >> 1)) * 4 + (m & 1) * 2;
-                    v0 = __uint_as_float(r[i]);
-                    v1 = __uint_as_float(r[i + 1]);
-                    v0 = v0 * lin_sigmoid(v0) * __uint_as_float(r[i + 16]);
-                    v1 = v1 * lin_sigmoid(v1) * __uint_as_float(r[i + 17]);
-                } else {
-                    const int i = (m >> 1) * 16 + k * 4 + (m & 1) * 2;
-                    v0 = __uint_as_float(r[i]);
-                    v1 = __uint_as_float(r[i + 1]);
-                    if (kFull) {
-                        v0 = lin_act(a.act, v0);
-                        v1 = lin_act(a.act, v1);
-                    }
-                }
+                const int i = GATED ? (2 * k + (m >> 1)) * 4 + (m & 1) * 2 : (m >> 1) * 16 + k * 4 + (m & 1) * 2;
+                float v0 = v[i], v1 = v[i + 1];
                 if (kFull && res) {
                     const float2 x = unpack2(rr[m], T());
                     v0 += x.x;
@@ -248,6 +241,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     lin_tables<MODE>(a, off, start);
     const int total = start[a.E];
     const int step = gridDim.x / 2, first = blockIdx.x / 2;
+    LinWalk<MODE, 32> walk;
 
     if (warp == 0) {
         // ---------------- TMA producer of this CTA's halves
@@ -258,7 +252,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
             for (int s = 0; s < kStages; ++s) issued[s] = false;
             for (int t = first; t < total && !*abort_flag; t += step) {
-                const LinTile ti = lin_tile<MODE, 32>(a, off, start, t);
+                const LinTile ti = walk.to(a, off, start, t);
                 const int half = (ti.cols + 31) / 32 * 16;  // columns of this CTA
                 const int c0 = ti.c0 + (int)rank * half, f = ti.f * 2 + (int)rank;
                 const int boxes = MODE == kDw ? (half + 63) / 64 : (half + a.boxes - 1) / a.boxes;
@@ -306,7 +300,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int t = first; t < total && ok; t += step, ++local) {
             ok = __shfl_sync(0xffffffffu, (int)!*abort_flag, 0) != 0;
             if (!ok) break;
-            const LinTile ti = lin_tile<MODE, 32>(a, off, start, t);
+            const LinTile ti = walk.to(a, off, start, t);
             const int n32 = (ti.cols + 31) / 32 * 32;
             const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 256, n32, MODE != kFwd, MODE == kDw);
             const int b = local & 1;
@@ -334,9 +328,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         if (left & 15) {
                             const int panels = 2 + (n32 / 2 + 63) / 64, rows = steps * 16 - left;
                             const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-                            for (int i = lane; i < panels * rows * 8; i += 32) {
-                                const int p = i / (rows * 8), r = i - p * (rows * 8);
-                                sts128((p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)(left * 128 + r * 16), zero);
+                            for (int p = 0; p < panels; ++p) {
+                                const uint32_t at = (p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)left * 128u;
+                                for (int i = lane; i < rows * 8; i += 32) sts128(at + (uint32_t)i * 16u, zero);
                             }
                             fence_proxy_async_smem();
                             __syncwarp();
@@ -381,7 +375,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const uint32_t buf = smem_u32(scratch + (warp - kLinEpiWarp0) * 2048);
         int local = 0;
         for (int t = first; t < total; t += step, ++local) {
-            const LinTile ti = lin_tile<MODE, 32>(a, off, start, t);
+            const LinTile ti = walk.to(a, off, start, t);
             const int b = local & 1;
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
             const int64_t row0 = MODE == kDw ? (int64_t)ti.e * a.N + ti.c0 : (int64_t)ti.row0 + ti.c0;
