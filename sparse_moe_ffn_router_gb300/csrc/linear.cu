@@ -19,6 +19,8 @@
 // warp 1 issues the MMAs into one of two accumulators in tensor memory, warps 4 - 11 write the other out.
 // With few tiles (decode) a cluster of up to 8 CTAs takes one tile's contraction in parts; the parts are added
 // in rank order through distributed shared memory. Sums are fp32 in a fixed order throughout.
+#include <atomic>
+
 #include "linear.cuh"
 
 namespace moe {
@@ -362,14 +364,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
                         lin_bias<T>(a, ti.e, ff, bv);
                         if (GATED) lin_bias_up<T>(a, ti.e, ff, bu);
-                        for (uint32_t r = 0; r < split; ++r) {
-                            const float4 x = ld_peer(addr, r);
-                            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-                            if (GATED) {
-                                const float4 y = ld_peer(addr + 64, r);
-                                u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+                        float4 x[8], y[8];  // all on their way at once
+#pragma unroll
+                        for (uint32_t r = 0; r < 8; ++r)
+                            if (r < split) {
+                                x[r] = ld_peer(addr, r);
+                                if (GATED) y[r] = ld_peer(addr + 64, r);
                             }
-                        }
+#pragma unroll
+                        for (uint32_t r = 0; r < 8; ++r)
+                            if (r < split) {
+                                v[0] += x[r].x; v[1] += x[r].y; v[2] += x[r].z; v[3] += x[r].w;
+                                if (GATED) {
+                                    u[0] += y[r].x; u[1] += y[r].y; u[2] += y[r].z; u[3] += y[r].w;
+                                }
+                            }
                         if (ff < a.F) lin_finish<T, GATED>(a, row0 + col, ff, v, u, bv, bu);
                     }
                 }
@@ -392,7 +401,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------------
-// dz = act'(z) * dout, and the column sums of it for the bias. A CTA takes a chunk of 64 rows and 128
+// dz = act'(z) * dout, and the column sums of it for the bias. A CTA takes a chunk of 32 rows and 128
 // columns (for swiglu 128 gate columns and the matching up columns); 16 threads side by side hold 8 columns
 // each, 16 rows at a time. Sums are of dz before its rounding, row block by row block: those of the rows of
 // expert e in chunk c go to part[c + e], a place of their own as chunks and experts follow one another.
@@ -562,17 +571,49 @@ struct LinPlan {
     int colw, grid, split, width;  // columns of a tile, at most; CTAs; CTAs to a tile's contraction; columns of a tile as they are cut
 };
 
+// Clusters of `split` CTAs of the split kernel that the device holds at once (clusters lie within a GPC, so there are
+// fewer than its SMs divided by their size).
+template <typename T, int MODE, bool GATED>
+int resident_clusters(int split, int num_sms) {
+    static std::atomic<int> cache[64][4];
+    int dev = 0, slot = split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3;
+    cudaGetDevice(&dev);
+    if (split == 1) return num_sms;
+    if (dev < 0 || dev >= 64) return num_sms / split / 2;
+    int n = cache[dev][slot].load(std::memory_order_relaxed);
+    if (n) return n - 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms / split * split);
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = kLinBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(k_linear<T, MODE, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, k_linear<T, MODE, GATED>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    cache[dev][slot].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 // Which kernel, and its tiles. groups: experts with rows, about; cols: columns of one of them, about; F: features
 // (lanes) in weight rows; blocks: 64-deep steps of the contraction, about.
 // Time of a 16-deep step, in clocks: on a pair, 256 features by w columns take w / 2 on the tensor cores and
 // (8 KB + 32 w B) / 128 B through each SM's shared memory (TMA's writes and the tensor core's reads of
 // its half), which measured times follow as 64 + w / 4; one SM's 128 x 64 take 96. A wave of tiles costs its widest. With
-// 64 columns or fewer the weights' way from HBM is what counts: one SM a tile, and clusters that split the contraction while SMs are idle.
+// 64 columns or fewer the weights' way from HBM is what counts: one SM a tile, and clusters that split the contraction as long as all of them are
+// resident at once (2048 x 2048, 16 tokens: clusters of 4 take 9.2 us, of 8 in two turns 15.0, one CTA a tile 12.9).
+template <typename T, int MODE, bool GATED>
 LinPlan lin_plan(int64_t groups, int64_t cols, int64_t F, int blocks, int num_sms) {
     LinPlan p = {false, kLinCols, 0, 1, 0};
     const int64_t f1 = (F + 127) / 128, f2 = (F + 255) / 256;
     const int64_t tiles = groups * f1 * ((cols + kLinCols - 1) / kLinCols);
-    while (p.split < 8 && tiles * p.split * 2 <= num_sms && p.split * 2 <= blocks) p.split *= 2;
+    while (p.split < 8 && p.split * 2 <= blocks && tiles <= resident_clusters<T, MODE, GATED>(p.split * 2, num_sms)) p.split *= 2;
     p.grid = (int)(tiles * p.split < num_sms ? tiles * p.split : num_sms) / p.split * p.split;
     if (cols <= kLinCols || num_sms < 2) return p;
     int64_t best = (tiles * p.split + num_sms - 1) / num_sms * 96 / p.split;
@@ -630,8 +671,20 @@ LinView view_of(const LinearArgs& a) {
     return v;
 }
 
-// Experts with rows, about, and the rows of one, about.
+// Experts with rows, about.
 int64_t groups_of(const LinearArgs& a) { return a.offsets ? (a.d.E < a.d.T ? a.d.E : a.d.T) : 1; }
+
+// Whether the streaming kernel takes the call. One matrix: a single row always (2048 x 2048: 3.6 against 9 us, 8192 x 4096:
+// 12.3 against 16.5); up to 8 while their sums, which grow with the rows, stay below the other kernel's start (2048 x 2048 by 4 rows 5.7
+// against 9 us, by 8 rows 10.8 against 9.0; 8192 x 4096 by 4 rows 23 against 17). Rows of experts: each reads a matrix of
+// its own, mostly, while they are no more than twice the experts (256 experts of 1024 x 2048 by 8 rows 7.2 against 17.5 us, by 64
+// rows 39 against 46, by 128 rows 79 against 77; 8 experts of 2048 x 512 by 64 rows 15.7 against 7).
+// (A test that holds back a stage needs a kernel that has stages.)
+bool few_rows(const LinearArgs& a) {
+    if (a.suppress) return false;
+    if (a.offsets) return a.d.T <= kFewRows && a.d.T <= 2 * a.d.E;
+    return a.d.T == 1 || (a.d.T <= 8 && (int64_t)a.d.T * a.d.N * a.d.K < 1 << 25);
+}
 
 template <typename T>
 cudaError_t linear_t(const LinearArgs& a, cudaStream_t s) {
@@ -645,13 +698,18 @@ cudaError_t linear_t(const LinearArgs& a, cudaStream_t s) {
     v.C = a.d.K;
     v.act = a.d.act;
     v.suppress = a.suppress;
-    const int64_t g = groups_of(a);
-    const LinPlan p = lin_plan(g, (a.d.T + g - 1) / g, a.d.N, (v.C + 63) / 64, a.num_sms);
+    cudaError_t e;
+    if (few_rows(a)) {
+        MOE_LAUNCH(MOE_KERNEL_LINEAR, s, (e = launch_few(a.d.dtype, gated, a.x, a.w, v, a.num_sms, s)));
+        return e;
+    }
+    const int64_t g = groups_of(a), rows = (a.d.T + g - 1) / g;
+    const int blocks = (v.C + 63) / 64;
+    const LinPlan p = gated ? lin_plan<T, kFwd, true>(g, rows, a.d.N, blocks, a.num_sms) : lin_plan<T, kFwd, false>(g, rows, a.d.N, blocks, a.num_sms);
     v.boxes = pair_boxes(p, !a.offsets);
     CUtensorMap A, B;
     if (!(gated ? map_w_gated(&A, a.d, a.w) : map_w(&A, a.d, a.w, 128)) || !map_2d(&B, a.d.dtype, a.x, a.d.T, a.d.K, a.d.K, v.boxes))
         return cudaErrorInvalidValue;
-    cudaError_t e;
     MOE_LAUNCH(MOE_KERNEL_LINEAR, s, (e = gated ? launch_plan<T, kFwd, true>(a.d.dtype, p, A, B, v, s) : launch_plan<T, kFwd, false>(a.d.dtype, p, A, B, v, s)));
     return e;
 }
@@ -686,7 +744,7 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
     if (a.dx) {
         v.out = a.dx;
         v.C = d.N;
-        const LinPlan p = lin_plan(g, (d.T + g - 1) / g, d.K, (v.C + 63) / 64, a.num_sms);
+        const LinPlan p = lin_plan<T, kDx, false>(g, (d.T + g - 1) / g, d.K, (v.C + 63) / 64, a.num_sms);
         v.boxes = pair_boxes(p, !a.offsets);
         if (!map_w(&A, d, a.w, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, v.boxes)) return cudaErrorInvalidValue;
         MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_plan<T, kDx, false>(d.dtype, p, A, B, v, s)));
@@ -696,7 +754,7 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
         if (!map_2d(&A, d.dtype, a.x, d.T, d.K, d.K, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, 64)) return cudaErrorInvalidValue;
         v.out = a.dw;
         v.C = 0;
-        const LinPlan p = lin_plan(d.E, d.N, d.K, (int)(((d.T + g - 1) / g + 63) / 64), a.num_sms);
+        const LinPlan p = lin_plan<T, kDw, false>(d.E, d.N, d.K, (int)(((d.T + g - 1) / g + 63) / 64), a.num_sms);
         MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_plan<T, kDw, false>(d.dtype, p, A, B, v, s)));
     }
     return e;

@@ -59,8 +59,7 @@ __device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
         "mapa.shared::cluster.u32 a, %4, %5;\n\t"
         "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-        : "r"(addr), "r"(rank)
-        : "memory");
+        : "r"(addr), "r"(rank));
     return v;
 }
 
@@ -202,6 +201,10 @@ struct LinWalk {
         return ti;
     }
 };
+
+// The forward pass of at most 8 rows of one matrix, or kFewRows of several (linear_few.cu).
+constexpr int kFewRows = 64;
+cudaError_t launch_few(int32_t dtype, bool gated, const void* x, const void* w, const LinView& v, int num_sms, cudaStream_t s);
 
 // Launches of the pair kernel (linear_pair.cu); grid: CTAs, an even number.
 cudaError_t launch_pair(int32_t dtype, int mode, bool gated, const CUtensorMap& A, const CUtensorMap& B, const LinView& v, int grid,

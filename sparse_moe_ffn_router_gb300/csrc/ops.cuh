@@ -80,7 +80,7 @@ struct LinearArgs {
     int num_sms;
     int suppress;            // testing aid: CTA 0 of the forward kernel never loads its first stage
 };
-constexpr int kDzRows = 64;  // rows of a chunk
+constexpr int kDzRows = 32;  // rows of a chunk
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_backward(const LinearArgs& a, cudaStream_t s);
 // A tensor map for TMA with 128-byte swizzle and zeros outside: dims and box innermost first, strides in
