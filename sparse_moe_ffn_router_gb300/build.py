@@ -19,7 +19,7 @@ SOURCES = ["api.cu", "router.cu", "route_small.cu", "dispatch.cu", "experts.cu",
            "noalloc.cu", "stats.cu", "host_experts.cu", "host_io.cu", "w4_pack.cu", "w4_layer.cu", "w4_stream_int4.cu",
            "w4_stream_int4_zp.cu", "w4_stream_e2m1.cu", "w4_gemm_int4.cu", "w4_gemm_int4_zp.cu", "w4_gemm_e2m1.cu",
            "w4_one_int4.cu", "w4_one_int4_zp.cu", "w4_one_e2m1.cu",
-           "ops_api.cu", "exchange.cu", "norm.cu", "linear.cu", "linear_pair.cu", "linear_few.cu"]
+           "ops_api.cu", "exchange.cu", "norm_bf16.cu", "norm_fp16.cu", "norm_fp32.cu", "linear.cu", "linear_pair.cu", "linear_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v", "--expt-relaxed-constexpr"]
 

@@ -51,7 +51,7 @@ cudaError_t launch_spread(int32_t dtype, const ExchangeArgs& a, cudaStream_t s);
 // out[t] = (residual = tok when there are no dots) + sum_k (w) * rows[inv[t, k]]; dots as above
 cudaError_t launch_gather(int32_t dtype, const ExchangeArgs& a, cudaStream_t s);
 
-// ---- norm (norm.cu)
+// ---- norm (norm.cuh)
 struct NormArgs {
     moe_norm_dims d;
     const void *y, *residual, *gate, *gamma_post, *gamma_pre;
@@ -61,9 +61,13 @@ struct NormArgs {
     float* part;  // [blocks, 3, H]
     int num_sms;
 };
-constexpr int kNormBlocks = 304;  // row blocks of the backward pass, at most (two for each SM)
-cudaError_t launch_norm(const NormArgs& a, cudaStream_t s);
-cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t s);
+constexpr int kNormBlocks = 304;  // CTAs of the backward pass, at most
+cudaError_t launch_norm_bf16(const NormArgs& a, cudaStream_t s, bool backward);
+cudaError_t launch_norm_fp16(const NormArgs& a, cudaStream_t s, bool backward);
+cudaError_t launch_norm_fp32(const NormArgs& a, cudaStream_t s, bool backward);
+inline cudaError_t launch_norm(const NormArgs& a, cudaStream_t s, bool backward) {
+    return a.d.dtype == MOE_BF16 ? launch_norm_bf16(a, s, backward) : a.d.dtype == MOE_FP16 ? launch_norm_fp16(a, s, backward) : launch_norm_fp32(a, s, backward);
+}
 
 // ---- linear (linear.cu)
 struct LinearArgs {

@@ -228,7 +228,7 @@ extern "C" moe_status moe_norm_residual(const moe_norm_dims* d, const void* y, c
     a.y = y; a.residual = residual; a.gate = gate; a.gamma_post = gamma_post; a.gamma_pre = gamma_pre;
     a.s = s; a.xn = xn;
     a.num_sms = device_sms();
-    return to_status(launch_norm(a, (cudaStream_t)stream));
+    return to_status(launch_norm(a, (cudaStream_t)stream, false));
 }
 
 extern "C" moe_status moe_norm_residual_backward(const moe_norm_dims* d, const void* ds, const void* dxn, const void* s,
@@ -261,5 +261,5 @@ extern "C" moe_status moe_norm_residual_backward(const moe_norm_dims* d, const v
     a.dresidual = dresidual; a.dy = dy; a.dgate = dgate; a.dgamma_post = dgamma_post; a.dgamma_pre = dgamma_pre;
     a.part = (float*)workspace;
     a.num_sms = device_sms();
-    return to_status(launch_norm_backward(a, (cudaStream_t)stream));
+    return to_status(launch_norm(a, (cudaStream_t)stream, true));
 }
