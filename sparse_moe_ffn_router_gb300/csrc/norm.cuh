@@ -29,21 +29,41 @@ namespace moe {
 constexpr int kNormThreads = 512;
 enum { kGateRow = 0, kGateColumn = 1, kGateAll = 2 };  // none or one number a row; a channel; an element
 
-__device__ __forceinline__ float norm_sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
-
-// act(gate) and its slope.
-__device__ __forceinline__ float gate_value(int act, float g) {
-    if (act == MOE_ACT_NONE) return g;
-    const float p = norm_sigmoid(g);
-    return act == MOE_ACT_SIGMOID ? p : g * p;
+// Of 16-bit tensors the hardware's exp and quotient do: a few 2^-22 relative against half a step of 2^-12 and up.
+template <typename T>
+__device__ __forceinline__ float norm_sigmoid(float v) {
+    if constexpr (sizeof(T) == 2) return __fdividef(1.0f, 1.0f + __expf(-v));
+    else return 1.0f / (1.0f + expf(-v));
 }
-__device__ __forceinline__ void gate_both(int act, float g, float& a, float& slope) {
-    a = g;
-    slope = 1.f;
-    if (act != MOE_ACT_NONE) {
-        const float p = norm_sigmoid(g);
-        a = act == MOE_ACT_SIGMOID ? p : g * p;
-        slope = act == MOE_ACT_SIGMOID ? p * (1.f - p) : p * (1.f + g * (1.f - p));
+// g = act(g) of N values, and their slopes.
+template <typename T, int N>
+__device__ __forceinline__ void gate_values(int act, float (&g)[N]) {
+    if (act == MOE_ACT_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] = norm_sigmoid<T>(g[i]);
+    } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] *= norm_sigmoid<T>(g[i]);
+    }
+}
+template <typename T, int N>
+__device__ __forceinline__ void gate_slopes(int act, float (&g)[N], float (&slope)[N]) {
+    if (act == MOE_ACT_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            g[i] = norm_sigmoid<T>(g[i]);
+            slope[i] = g[i] * (1.f - g[i]);
+        }
+    } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float p = norm_sigmoid<T>(g[i]);
+            slope[i] = p * (1.f + g[i] * (1.f - p));
+            g[i] *= p;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) slope[i] = 1.f;
     }
 }
 
@@ -206,13 +226,17 @@ __global__ void __launch_bounds__(kNormThreads, VPT == 1 ? 2 : 1) k_norm(const N
     if (first < d.T) load(first);
     // tensors [H]: in vectors where rows are aligned, else by elements
     const bool aligned = mis == 0 && H % VE == 0;
-    Raw gp[VPT], gq[VPT], gc[VPT];
+    Raw gp[VPT], gq[VPT];
+    float gc[VPT][VE];  // act(gate) of a channel gate
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
         if (live[i]) {
             if (post && a.gamma_post) gp[i] = row_get<T, VE>((const T*)a.gamma_post, col[i], H, aligned);
             if (a.xn && a.gamma_pre) gq[i] = row_get<T, VE>((const T*)a.gamma_pre, col[i], H, aligned);
-            if (channel) gc[i] = row_get<T, VE>((const T*)a.gate, col[i], H, aligned);
+            if (channel) {
+                R::values(row_get<T, VE>((const T*)a.gate, col[i], H, aligned), gc[i]);
+                gate_values<T, VE>(d.gate_act, gc[i]);
+            }
         }
     for (int i = g.tid; i < 80; i += g.threads) (&bufs[g.id][0][0][0])[i] = 0.f;  // (read past the last warp)
     if (g.threads > 32) asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(g.threads) : "memory");
@@ -221,7 +245,11 @@ __global__ void __launch_bounds__(kNormThreads, VPT == 1 ? 2 : 1) k_norm(const N
     for (int t = first; t < d.T; t += step, turn ^= 1) {
         const int64_t row = (int64_t)t * H;
         float scale = d.branch_scale;  // of the whole row's branch
-        if (GATE == kGateRow && d.gate == MOE_GATE_TOKEN) scale *= gate_value(d.gate_act, to_f(tg));
+        if (GATE == kGateRow && d.gate == MOE_GATE_TOKEN) {
+            float v[1] = {to_f(tg)};
+            gate_values<T, 1>(d.gate_act, v);
+            scale *= v[0];
+        }
         float s[VPT][VE];  // the branch without the norm's factor, then s
         float sq[1] = {0.f};
         Raw rr[VPT];
@@ -240,10 +268,15 @@ __global__ void __launch_bounds__(kNormThreads, VPT == 1 ? 2 : 1) k_norm(const N
                         for (int e = 0; e < VE; ++e) s[i][e] *= f[e];
                     }
                 }
-                if (full || channel) {
-                    R::values(full ? ga[i] : gc[i], f);
+                if (full) {
+                    R::values(ga[i], f);
+                    gate_values<T, VE>(d.gate_act, f);
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) s[i][e] *= gate_value(d.gate_act, f[e]);
+                    for (int e = 0; e < VE; ++e) s[i][e] *= f[e];
+                }
+                if (channel) {
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) s[i][e] *= gc[i][e];
                 }
             }
         if (t + step < d.T) load(t + step);
@@ -330,7 +363,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_backward(const NormArg
     if (first < d.T) load(first);
     const bool aligned = mis == 0 && H % VE == 0;
     float acc_post[VPT][VE], acc_pre[VPT][VE], acc_gate[VPT][VE];
-    Raw gp[VPT], gq[VPT], gc[VPT];
+    Raw gp[VPT], gq[VPT];
+    float gc[VPT][VE];  // act(gate) of a channel gate
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         float one[VE];
@@ -343,7 +377,10 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_backward(const NormArg
         if (live[i]) {
             if (post && a.gamma_post) gp[i] = row_get<T, VE>((const T*)a.gamma_post, col[i], H, aligned);
             if (pre && a.gamma_pre) gq[i] = row_get<T, VE>((const T*)a.gamma_pre, col[i], H, aligned);
-            if (channel) gc[i] = row_get<T, VE>((const T*)a.gate, col[i], H, aligned);
+            if (channel) {
+                R::values(row_get<T, VE>((const T*)a.gate, col[i], H, aligned), gc[i]);
+                gate_values<T, VE>(d.gate_act, gc[i]);
+            }
         }
     }
     for (int i = g.tid; i < 200; i += g.threads) (&bufs[g.id][0][0][0])[i] = 0.f;
@@ -372,8 +409,12 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_backward(const NormArg
         const float rs = pre ? rsqrtf(sm[0] * inv_h + d.eps) : 0.f;
         const float ry = post ? rsqrtf(sm[1] * inv_h + d.eps) : 1.f;
         const float cs = pre ? rs * rs * rs * (sm[2] * inv_h) : 0.f;
-        float tval = 1.f, tslope = 0.f;
-        if (token) gate_both(d.gate_act, to_f(tg), tval, tslope);
+        float tval[1] = {1.f}, tslope[1] = {0.f};
+        if (token) {
+            tval[0] = to_f(tg);
+            gate_slopes<T, 1>(d.gate_act, tval, tslope);
+        }
+        const float branch = d.branch_scale * tval[0];
         float gs[VPT][VE];  // dn gamma_post
         Raw yy[VPT];
         float more[2] = {0.f, 0.f};  // dn gamma_post y, g_s n
@@ -395,18 +436,19 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_backward(const NormArg
                 if (a.dresidual) row_put<T, VE>((T*)a.dresidual + row, col[i], H, whole[i], R::pack(o));
                 R::values(y[i], yv);
                 R::values(gp[i], gm);
-                float ge[VE];
-                if (full || channel) R::values(full ? ga[i] : gc[i], ge);
+                float ge[VE], slope[VE];
+                if (full) {
+                    R::values(ga[i], ge);
+                    gate_slopes<T, VE>(d.gate_act, ge, slope);
+                }
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    const float n = yv[e] * ry * gm[e];  // (gamma_post is 1 and r_y is 1 without the norm)
-                    float av = tval, slope = 0.f;
-                    if (full || channel) gate_both(d.gate_act, ge[e], av, slope);
-                    const float dn = d.branch_scale * av * v[e];
-                    if (channel) acc_gate[i][e] = fmaf(d.branch_scale * v[e] * n, slope, acc_gate[i][e]);
-                    if (full) o[e] = d.branch_scale * v[e] * n * slope;
+                    const float yn = yv[e] * ry, n = yn * gm[e];  // (gamma_post is 1 and r_y is 1 without the norm)
+                    const float dn = (full ? branch * ge[e] : channel ? branch * gc[i][e] : branch) * v[e];
+                    if (channel) acc_gate[i][e] = fmaf(v[e], n, acc_gate[i][e]);  // (branch and slope: once, at the end)
+                    if (full) o[e] = branch * v[e] * n * slope[e];
                     if (token) more[1] = fmaf(v[e], n, more[1]);
-                    acc_post[i][e] = fmaf(dn * yv[e], ry, acc_post[i][e]);
+                    acc_post[i][e] = fmaf(dn, yn, acc_post[i][e]);
                     gs[i][e] = dn * gm[e];
                     more[0] = fmaf(gs[i][e], yv[e], more[0]);
                 }
@@ -414,7 +456,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_backward(const NormArg
             }
         if (t + step < d.T) load(t + step);
         if (post || token) group_sum<2>(more, &bufs[g.id][turn][3], g);
-        if (token && a.dgate && g.tid == 0) ((T*)a.dgate)[t] = from_f<T>(d.branch_scale * more[1] * tslope);
+        if (token && a.dgate && g.tid == 0) ((T*)a.dgate)[t] = from_f<T>(d.branch_scale * more[1] * tslope[0]);
         const float cy = post ? ry * ry * ry * (more[0] * inv_h) : 0.f;
         if (a.dy)
 #pragma unroll
@@ -428,6 +470,17 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_backward(const NormArg
                 }
     }
     if (!a.part) return;
+    if (channel) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (live[i]) {
+                float ge[VE], slope[VE];
+                R::values(row_get<T, VE>((const T*)a.gate, col[i], H, aligned), ge);
+                gate_slopes<T, VE>(d.gate_act, ge, slope);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) acc_gate[i][e] *= d.branch_scale * slope[e];
+            }
+    }
     float* part = a.part + (int64_t)blockIdx.x * 3 * H;
     if (VPT > 1 || g.groups == 1) {
 #pragma unroll
