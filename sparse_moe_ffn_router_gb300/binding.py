@@ -564,90 +564,97 @@ def moe_forward_w4(dims, fmt: W4Format, x, weights: Weights, residual, out, work
                                          _stream_of(stream, dev)), "moe_forward_w4")
 
 
-def _shaped(what: str, t, dtype, *shape):
-    """Raises unless t is of this type and shape."""
+def _refuse(name: str, t, dtype, shapes, device: int):
+    """Raises what is wrong with an argument that _ptr_of does not take."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype is not dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape not in shapes:
+        raise ValueError(f"{name} must be {' or '.join(str(list(s)) for s in shapes)}, got {list(t.shape)}")
+    _ptr(t)
+    raise ValueError(f"{name} must be on the current CUDA device ({device}), got {t.device}")
 
 
-def _pairs(what: str, t, dtype, T: int, K: int):
-    """Raises unless t holds one number for each pair: [T, K] or [T * K]."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.numel() != T * K or t.dim() not in (1, 2) or (t.dim() == 2 and tuple(t.shape) != (T, K)):
-        raise ValueError(f"{what} must be [{T}, {K}], got {list(t.shape)}")
+def _ptr_of(device: int, dtype, shape: tuple, name: str, t, other: tuple | None = None):
+    """Address of an argument (None: none) once its type, shape (or other), layout and device are checked."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and (t.shape == shape or t.shape == other) and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(name, t, dtype, (shape,) if other is None else (shape, other), device)
+
+
+_I32, _F32 = torch.int32, torch.float32
 
 
 def moe_sort_pairs(E: int, ids, counts, offsets, perm, inv, stream=None):
     """Dispatch of the expert ids [T, K] int32: counts [E], offsets [E + 1], perm [T * K] (pairs t * K + k by expert,
     -1 behind the last) and inv [T * K] (each pair's place, -1 for an id outside [0, E))."""
-    if ids.dim() != 2 or ids.dtype is not torch.int32:
-        raise TypeError("ids must be int32 [T, K]")
-    T, K = ids.shape
-    _shaped("counts", counts, torch.int32, E)
-    _shaped("offsets", offsets, torch.int32, E + 1)
-    _pairs("perm", perm, torch.int32, T, K)
-    _pairs("inv", inv, torch.int32, T, K)
-    dev = _device(ids)
-    _check(load_library().moe_sort_pairs(T, K, int(E), *_here(dev, ids, counts, offsets, perm, inv), _stream_of(stream, dev)), "moe_sort_pairs")
+    if ids.dim() != 2:
+        raise ValueError("ids must be int32 [T, K]")
+    shape = ids.shape
+    T, K = shape
+    dev, flat = torch.cuda.current_device() if ids.is_cuda else -2, (T * K,)
+    _check(load_library().moe_sort_pairs(T, K, E, _ptr_of(dev, _I32, shape, "ids", ids), _ptr_of(dev, _I32, (E,), "counts", counts),
+                                         _ptr_of(dev, _I32, (E + 1,), "offsets", offsets), _ptr_of(dev, _I32, flat, "perm", perm, shape),
+                                         _ptr_of(dev, _I32, flat, "inv", inv, shape), _stream_of(stream, dev)), "moe_sort_pairs")
 
 
-def _exchange(name: str, token, token_what: str, rows, rows_what: str, inv, topk_w, dtopk_w=None):
-    """Sizes and type of a call on token [T, H] and rows [T * K, H]."""
+def _exchange(token, rows):
+    """Device, type, T, K and H of a call on token rows [T, H] and experts' rows [T * K, H]."""
     if token.dim() != 2 or rows.dim() != 2:
-        raise ValueError(f"{token_what} is [T, H], {rows_what} [T * K, H]")
+        raise ValueError("token rows are [T, H], experts' rows [T * K, H]")
     T, H = token.shape
-    if T and rows.shape[0] % T:
-        raise ValueError(f"{rows_what} must have T * K rows, T = {T}")
-    K = rows.shape[0] // T if T else 1
-    dtype = _DTYPE.get(token.dtype)
-    if dtype is None:
-        raise TypeError(f"{token_what} must be bfloat16, float16 or float32, got {token.dtype}")
-    _shaped(rows_what, rows, token.dtype, T * K, H)
-    _pairs("inv", inv, torch.int32, T, K)
-    if topk_w is not None:
-        _pairs("topk_w", topk_w, torch.float32, T, K)
-    if dtopk_w is not None:
-        _pairs("dtopk_w", dtopk_w, torch.float32, T, K)
-    return dtype, T, K, H
+    n = rows.shape[0]
+    K = n // T if T else 1
+    if n != T * K:
+        raise ValueError(f"experts' rows must be T * K, T = {T}: got {n}")
+    code = _DTYPE.get(token.dtype)
+    if code is None:
+        raise TypeError(f"token rows must be bfloat16, float16 or float32, got {token.dtype}")
+    return torch.cuda.current_device() if token.is_cuda else -2, token.dtype, code, T, K, H
 
 
 def moe_dispatch(x, inv, topk_w, rows, stream=None):
     """rows [T * K, H]: rows[inv[t, k]] = topk_w[t, k] * x[t] (topk_w None: the rows as they are)."""
-    sizes = _exchange("moe_dispatch", x, "x", rows, "rows", inv, topk_w)
-    dev = _device(x)
-    _check(load_library().moe_dispatch(*sizes, *_here(dev, x, inv, topk_w, rows), _stream_of(stream, dev)), "moe_dispatch")
+    dev, dt, code, T, K, H = _exchange(x, rows)
+    n = T * K
+    _check(load_library().moe_dispatch(code, T, K, H, _ptr_of(dev, dt, (T, H), "x", x), _ptr_of(dev, _I32, (n,), "inv", inv, (T, K)),
+                                       _ptr_of(dev, _F32, (T, K), "topk_w", topk_w, (n,)), _ptr_of(dev, dt, (n, H), "rows", rows),
+                                       _stream_of(stream, dev)), "moe_dispatch")
 
 
 def moe_dispatch_backward(drows, inv, topk_w, x, dx, dtopk_w=None, stream=None):
     """dx [T, H] = sum_k topk_w[t, k] * drows[inv[t, k]]; dtopk_w [T, K] (optional; x is read for it) = x[t] . drows[inv[t, k]]."""
-    sizes = _exchange("moe_dispatch_backward", dx, "dx", drows, "drows", inv, topk_w, dtopk_w)
-    if x is not None:
-        _shaped("x", x, dx.dtype, *dx.shape)
-    dev = _device(dx)
-    _check(load_library().moe_dispatch_backward(*sizes, *_here(dev, drows, inv, topk_w, x, dx, dtopk_w), _stream_of(stream, dev)),
-           "moe_dispatch_backward")
+    dev, dt, code, T, K, H = _exchange(dx, drows)
+    n = T * K
+    _check(load_library().moe_dispatch_backward(code, T, K, H, _ptr_of(dev, dt, (n, H), "drows", drows), _ptr_of(dev, _I32, (n,), "inv", inv, (T, K)),
+                                                _ptr_of(dev, _F32, (T, K), "topk_w", topk_w, (n,)), _ptr_of(dev, dt, (T, H), "x", x),
+                                                _ptr_of(dev, dt, (T, H), "dx", dx), _ptr_of(dev, _F32, (T, K), "dtopk_w", dtopk_w, (n,)),
+                                                _stream_of(stream, dev)), "moe_dispatch_backward")
 
 
 def moe_combine(rows, inv, topk_w, residual, out, stream=None):
     """out [T, H] = residual + sum_k topk_w[t, k] * rows[inv[t, k]] (topk_w and residual may be None)."""
-    sizes = _exchange("moe_combine", out, "out", rows, "rows", inv, topk_w)
-    if residual is not None:
-        _shaped("residual", residual, out.dtype, *out.shape)
-    dev = _device(out)
-    _check(load_library().moe_combine(*sizes, *_here(dev, rows, inv, topk_w, residual, out), _stream_of(stream, dev)), "moe_combine")
+    dev, dt, code, T, K, H = _exchange(out, rows)
+    n = T * K
+    _check(load_library().moe_combine(code, T, K, H, _ptr_of(dev, dt, (n, H), "rows", rows), _ptr_of(dev, _I32, (n,), "inv", inv, (T, K)),
+                                      _ptr_of(dev, _F32, (T, K), "topk_w", topk_w, (n,)), _ptr_of(dev, dt, (T, H), "residual", residual),
+                                      _ptr_of(dev, dt, (T, H), "out", out), _stream_of(stream, dev)), "moe_combine")
 
 
 def moe_combine_backward(dout, inv, topk_w, rows, drows, dtopk_w=None, stream=None):
     """drows[inv[t, k]] = topk_w[t, k] * dout[t]; dtopk_w [T, K] (optional; rows are read for it) = dout[t] . rows[inv[t, k]]."""
-    sizes = _exchange("moe_combine_backward", dout, "dout", drows, "drows", inv, topk_w, dtopk_w)
-    if rows is not None:
-        _shaped("rows", rows, drows.dtype, *drows.shape)
-    dev = _device(dout)
-    _check(load_library().moe_combine_backward(*sizes, *_here(dev, dout, inv, topk_w, rows, drows, dtopk_w), _stream_of(stream, dev)),
-           "moe_combine_backward")
+    dev, dt, code, T, K, H = _exchange(dout, drows)
+    n = T * K
+    _check(load_library().moe_combine_backward(code, T, K, H, _ptr_of(dev, dt, (T, H), "dout", dout), _ptr_of(dev, _I32, (n,), "inv", inv, (T, K)),
+                                               _ptr_of(dev, _F32, (T, K), "topk_w", topk_w, (n,)), _ptr_of(dev, dt, (n, H), "rows", rows),
+                                               _ptr_of(dev, dt, (n, H), "drows", drows), _ptr_of(dev, _F32, (T, K), "dtopk_w", dtopk_w, (n,)),
+                                               _stream_of(stream, dev)), "moe_combine_backward")
 
 
 def new_linear_workspace(dims: LinearDims, backward: bool = False, device="cuda") -> torch.Tensor:
@@ -658,46 +665,41 @@ def new_linear_workspace(dims: LinearDims, backward: bool = False, device="cuda"
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _linear(d: LinearDims, wide, **tensors):
-    """Checks the tensors of a call by name; wide: the columns of act's result."""
+def _linear(d: LinearDims, t):
+    """Device, type and sizes of a call, t: one of its tensors. The one matrix of E = 1 may come without its first dimension."""
+    T, N, K, E = d.T, d.N, d.K, d.E
     dt = _TORCH.get(d.dtype)
-    shapes = {"x": (d.T, d.K), "dx": (d.T, d.K), "w": (d.E, d.N, d.K), "dw": (d.E, d.N, d.K), "bias": (d.E, d.N), "dbias": (d.E, d.N),
-              "residual": (d.T, wide), "out": (d.T, wide), "dout": (d.T, wide), "z": (d.T, d.N)}
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.dtype is not dt:
-            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-        shape = shapes[name]
-        if t.shape != shape and not (d.E == 1 and name in ("w", "dw", "bias", "dbias") and t.shape == shape[1:]):
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if dt is None:
+        raise MoEError(1, "moe_linear_dims")
+    return torch.cuda.current_device() if t.is_cuda else -2, dt, T, N, K, E, N // 2 if d.act == ACT_SWIGLU else N
 
 
-def _offsets(d: LinearDims, offsets):
-    if offsets is not None:
-        _shaped("offsets", offsets, torch.int32, d.E + 1)
+def _workspace(device: int, t):
+    if t is None or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on the current CUDA device ({device})")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def moe_linear(dims: LinearDims, x, w, bias, offsets, residual, out, z, workspace, stream=None):
     """out = act(x . W_e^T + bias_e) + residual, e the expert whose rows [offsets[e], offsets[e + 1]) hold x's row
     (offsets None: the one matrix); z (or None) receives the pre-activations for moe_linear_backward."""
-    wide = dims.N // 2 if dims.act == ACT_SWIGLU else dims.N
-    _linear(dims, wide, x=x, w=w, bias=bias, residual=residual, out=out, z=z)
-    _offsets(dims, offsets)
-    dev = _device(x)
-    px, pw, pb, of, pr, po, pz, ws = _here(dev, x, w, bias, offsets, residual, out, z, workspace)
-    _check(load_library().moe_linear(ctypes.byref(dims), px, pw, pb, of, pr, po, pz, ws, _nbytes(workspace), _stream_of(stream, dev)), "moe_linear")
+    dev, dt, T, N, K, E, wide = _linear(dims, x)
+    one = E == 1
+    _check(load_library().moe_linear(ctypes.byref(dims), _ptr_of(dev, dt, (T, K), "x", x), _ptr_of(dev, dt, (E, N, K), "w", w, (N, K) if one else None),
+                                     _ptr_of(dev, dt, (E, N), "bias", bias, (N,) if one else None), _ptr_of(dev, _I32, (E + 1,), "offsets", offsets),
+                                     _ptr_of(dev, dt, (T, wide), "residual", residual), _ptr_of(dev, dt, (T, wide), "out", out),
+                                     _ptr_of(dev, dt, (T, N), "z", z), *_workspace(dev, workspace), _stream_of(stream, dev)), "moe_linear")
 
 
 def moe_linear_backward(dims: LinearDims, x, w, offsets, z, dout, dx, dw, dbias, workspace, stream=None):
     """Gradients of moe_linear's x, w and bias (each may be None) for the gradient dout of its result; the residual's is dout."""
-    wide = dims.N // 2 if dims.act == ACT_SWIGLU else dims.N
-    _linear(dims, wide, x=x, w=w, z=z, dout=dout, dx=dx, dw=dw, dbias=dbias)
-    _offsets(dims, offsets)
-    dev = _device(dout)
-    px, pw, of, pz, pd, gx, gw, gb, ws = _here(dev, x, w, offsets, z, dout, dx, dw, dbias, workspace)
-    _check(load_library().moe_linear_backward(ctypes.byref(dims), px, pw, of, pz, pd, gx, gw, gb, ws, _nbytes(workspace), _stream_of(stream, dev)),
-           "moe_linear_backward")
+    dev, dt, T, N, K, E, wide = _linear(dims, dout)
+    flat, line = ((N, K), (N,)) if E == 1 else (None, None)
+    _check(load_library().moe_linear_backward(
+        ctypes.byref(dims), _ptr_of(dev, dt, (T, K), "x", x), _ptr_of(dev, dt, (E, N, K), "w", w, flat), _ptr_of(dev, _I32, (E + 1,), "offsets", offsets),
+        _ptr_of(dev, dt, (T, N), "z", z), _ptr_of(dev, dt, (T, wide), "dout", dout), _ptr_of(dev, dt, (T, K), "dx", dx),
+        _ptr_of(dev, dt, (E, N, K), "dw", dw, flat), _ptr_of(dev, dt, (E, N), "dbias", dbias, line), *_workspace(dev, workspace),
+        _stream_of(stream, dev)), "moe_linear_backward")
 
 
 def new_norm_workspace(dims: NormDims, device="cuda") -> torch.Tensor:
@@ -708,32 +710,36 @@ def new_norm_workspace(dims: NormDims, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _norm(d: NormDims, gate, dgate, rows, columns):
+def _norm(d: NormDims, t):
+    """Device, type, shapes [T, H] and [H], and the gate's shape."""
+    T, H, gate = d.T, d.H, d.gate
     dt = _TORCH.get(d.dtype)
-    gate_shape = {GATE_TOKEN: (d.T,), GATE_CHANNEL: (d.H,), GATE_FULL: (d.T, d.H)}.get(d.gate, ())
-    for what, tensors, shape in (("rows", rows, (d.T, d.H)), ("gamma", columns, (d.H,)), ("gate", (gate, dgate), gate_shape)):
-        for t in tensors:
-            if t is not None and (t.dtype is not dt or t.shape != shape):
-                raise (TypeError if t.dtype is not dt else ValueError)(f"{what} tensors must be {dt} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if dt is None:
+        raise MoEError(1, "moe_norm_dims")
+    return (torch.cuda.current_device() if t.is_cuda else -2, dt, (T, H), (H,),
+            (T,) if gate == GATE_TOKEN else (H,) if gate == GATE_CHANNEL else (T, H) if gate == GATE_FULL else ())
 
 
 def moe_norm_residual(dims: NormDims, y, residual, gate, gamma_post, gamma_pre, s, xn, stream=None):
     """s = residual_scale * residual + branch_scale * act(gate) * N(y; gamma_post), xn = N(s; gamma_pre); residual, the
     gammas and either result may be None, and N(y) is y for dims without post."""
-    _norm(dims, gate, None, (y, residual, s, xn), (gamma_post, gamma_pre))
-    dev = _device(y)
-    _check(load_library().moe_norm_residual(ctypes.byref(dims), *_here(dev, y, residual, gate, gamma_post, gamma_pre, s, xn), _stream_of(stream, dev)),
-           "moe_norm_residual")
+    dev, dt, rows, cols, gs = _norm(dims, y)
+    _check(load_library().moe_norm_residual(
+        ctypes.byref(dims), _ptr_of(dev, dt, rows, "y", y), _ptr_of(dev, dt, rows, "residual", residual), _ptr_of(dev, dt, gs, "gate", gate),
+        _ptr_of(dev, dt, cols, "gamma_post", gamma_post), _ptr_of(dev, dt, cols, "gamma_pre", gamma_pre), _ptr_of(dev, dt, rows, "s", s),
+        _ptr_of(dev, dt, rows, "xn", xn), _stream_of(stream, dev)), "moe_norm_residual")
 
 
 def moe_norm_residual_backward(dims: NormDims, ds, dxn, s, y, gate, gamma_post, gamma_pre, dresidual, dy, dgate, dgamma_post, dgamma_pre, workspace,
                                stream=None):
     """Gradients of moe_norm_residual's inputs (each may be None) for the gradients ds and dxn of its results (either may be None)."""
-    _norm(dims, gate, dgate, (ds, dxn, s, y, dresidual, dy), (gamma_post, gamma_pre, dgamma_post, dgamma_pre))
-    dev = _device(y)
-    *ptrs, ws = _here(dev, ds, dxn, s, y, gate, gamma_post, gamma_pre, dresidual, dy, dgate, dgamma_post, dgamma_pre, workspace)
-    _check(load_library().moe_norm_residual_backward(ctypes.byref(dims), *ptrs, ws, _nbytes(workspace), _stream_of(stream, dev)),
-           "moe_norm_residual_backward")
+    dev, dt, rows, cols, gs = _norm(dims, y)
+    _check(load_library().moe_norm_residual_backward(
+        ctypes.byref(dims), _ptr_of(dev, dt, rows, "ds", ds), _ptr_of(dev, dt, rows, "dxn", dxn), _ptr_of(dev, dt, rows, "s", s),
+        _ptr_of(dev, dt, rows, "y", y), _ptr_of(dev, dt, gs, "gate", gate), _ptr_of(dev, dt, cols, "gamma_post", gamma_post),
+        _ptr_of(dev, dt, cols, "gamma_pre", gamma_pre), _ptr_of(dev, dt, rows, "dresidual", dresidual), _ptr_of(dev, dt, rows, "dy", dy),
+        _ptr_of(dev, dt, gs, "dgate", dgate), _ptr_of(dev, dt, cols, "dgamma_post", dgamma_post), _ptr_of(dev, dt, cols, "dgamma_pre", dgamma_pre),
+        *_workspace(dev, workspace), _stream_of(stream, dev)), "moe_norm_residual_backward")
 
 
 def moe_rmsnorm(dims, x, gamma, eps: float, xn, stream=None):

@@ -43,42 +43,50 @@ __global__ void __launch_bounds__(32 * kSortWarps, 1)
     __syncwarp();
     const int64_t p0 = ((int64_t)rank * kSortWarps + warp) * seg;
     const int64_t p1 = p0 + seg < P ? p0 + seg : P;
-    constexpr int kAhead = 4;  // ids loaded together
+    constexpr int kAhead = 4;  // ids loaded together; a piece of no more is ranked once and for all in the first pass
+    int held[kAhead], ahead[kAhead];  // expert, pairs of the warp before it with the same one
     for (int64_t i0 = p0; i0 < p1; i0 += 32 * kAhead) {
-        int e[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int64_t i = i0 + 32 * j + lane;
-            e[j] = i < p1 ? ids[i] : -1;
-            if ((unsigned)e[j] >= (unsigned)E) e[j] = -1;
+            held[j] = i < p1 ? ids[i] : -1;
+            if ((unsigned)held[j] >= (unsigned)E) held[j] = -1;
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const unsigned m = __match_any_sync(0xffffffffu, e[j]);
-            if (e[j] >= 0 && (m & below) == 0) cnt[warp][e[j]] += __popc(m);
+            const unsigned m = __match_any_sync(0xffffffffu, held[j]);
+            const int before = held[j] >= 0 ? cnt[warp][held[j]] : 0;
+            ahead[j] = before + __popc(m & below);
+            __syncwarp();
+            if (held[j] >= 0 && (m & below) == 0) cnt[warp][held[j]] = before + __popc(m);
             __syncwarp();
         }
     }
     __syncthreads();
     const int e = threadIdx.x;
     if (e < E) {
-        int sum = 0;
+        int c[kSortWarps], sum = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) c[w] = cnt[w][e];
 #pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
-            const int c = cnt[w][e];
             cnt[w][e] = sum;
-            sum += c;
+            sum += c[w];
         }
         tot[e] = sum;
     }
     cl.sync();
     int all = 0, before = 0;
-    if (e < E)
-        for (int r = 0; r < n; ++r) {
-            const int c = cl.map_shared_rank(tot, r)[e];
-            all += c;
-            before += r < rank ? c : 0;
+    if (e < E) {
+        int c[kSortCtas];  // all on their way at once
+#pragma unroll
+        for (int r = 0; r < kSortCtas; ++r) c[r] = r < n ? cl.map_shared_rank(tot, r)[e] : 0;
+#pragma unroll
+        for (int r = 0; r < kSortCtas; ++r) {
+            all += c[r];
+            before += r < rank ? c[r] : 0;
         }
+    }
     if (e < kSortMaxE) {  // exclusive scan over the experts
         int v = all;
 #pragma unroll
@@ -92,7 +100,8 @@ __global__ void __launch_bounds__(32 * kSortWarps, 1)
     __syncthreads();
     if (e < kSortMaxE) {
         int add = 0;
-        for (int w = 0; w < warp; ++w) add += wsum[w];
+#pragma unroll
+        for (int w = 0; w < kSortMaxE / 32; ++w) add += w < warp ? wsum[w] : 0;
         const int first = base[e] + add;
         base[e] = first + before;
         if (e == kSortMaxE - 1) total_s = first + all;
@@ -105,22 +114,28 @@ __global__ void __launch_bounds__(32 * kSortWarps, 1)
     __syncthreads();
     const int total = total_s;
     for (int64_t i0 = p0; i0 < p1; i0 += 32 * kAhead) {
-        int e[kAhead];
+        if (seg > 32 * kAhead) {  // ranked again, from the warp's first places on
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int64_t i = i0 + 32 * j + lane;
-            e[j] = i < p1 ? ids[i] : -1;
-            if ((unsigned)e[j] >= (unsigned)E) e[j] = -1;
+            for (int j = 0; j < kAhead; ++j) {
+                const int64_t i = i0 + 32 * j + lane;
+                held[j] = i < p1 ? ids[i] : -1;
+                if ((unsigned)held[j] >= (unsigned)E) held[j] = -1;
+            }
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int64_t i = i0 + 32 * j + lane;
-            const unsigned m = __match_any_sync(0xffffffffu, e[j]);
             int at = -1;
-            if (e[j] >= 0) at = base[e[j]] + cnt[warp][e[j]] + __popc(m & below);
-            __syncwarp();
-            if (e[j] >= 0 && (m & below) == 0) cnt[warp][e[j]] += __popc(m);
-            __syncwarp();
+            if (seg > 32 * kAhead) {
+                const unsigned m = __match_any_sync(0xffffffffu, held[j]);
+                const int first = held[j] >= 0 ? cnt[warp][held[j]] : 0;
+                if (held[j] >= 0) at = base[held[j]] + first + __popc(m & below);
+                __syncwarp();
+                if (held[j] >= 0 && (m & below) == 0) cnt[warp][held[j]] = first + __popc(m);
+                __syncwarp();
+            } else if (held[j] >= 0) {
+                at = base[held[j]] + cnt[warp][held[j]] + ahead[j];
+            }
             if (i < p1) {
                 inv[i] = at;
                 if (at >= 0) perm[at] = (int32_t)i;
@@ -186,16 +201,38 @@ __device__ __forceinline__ void store_dots(float (&v)[kSlots], float* dst, int K
     }
 }
 
+// What a thread moves at once: 16 bytes, or one element where rows do not start on 16 bytes.
+template <typename T, int VE>
+struct Piece {
+    typedef Raw type;
+    static __device__ __forceinline__ Raw get(const T* p) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        return Raw{{v.x, v.y, v.z, v.w}};
+    }
+    static __device__ __forceinline__ void put(T* p, const Raw& r) { *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]); }
+    static __device__ __forceinline__ void values(const Raw& r, float (&f)[VE]) { RawOf<T>::values(r, f); }
+    static __device__ __forceinline__ Raw pack(const float (&f)[VE]) { return RawOf<T>::pack(f); }
+};
+template <typename T>
+struct Piece<T, 1> {
+    typedef T type;
+    static __device__ __forceinline__ T get(const T* p) { return *p; }
+    static __device__ __forceinline__ void put(T* p, const T& r) { *p = r; }
+    static __device__ __forceinline__ void values(const T& r, float (&f)[1]) { f[0] = to_f(r); }
+    static __device__ __forceinline__ T pack(const float (&f)[1]) { return from_f<T>(f[0]); }
+};
+
 template <typename T, int VE, int TPT, bool GATHER, bool DOTS>
 __global__ void __launch_bounds__(256) k_exchange(const ExchangeArgs a) {
-    typedef Vec<T, VE> V;
+    typedef Piece<T, VE> P;
+    typedef typename P::type V;
     grid_dep_wait();
     grid_dep_launch();
     const int t = (int)(blockIdx.x * (256 / TPT) + threadIdx.x / TPT);
     if (t >= a.T) return;  // (a whole token's threads)
     const int lane = threadIdx.x % TPT;
     const int K = a.K, nv = a.H / VE;
-    const int64_t P = (int64_t)a.T * K, p = (int64_t)t * K;
+    const int64_t pairs = (int64_t)a.T * K, p = (int64_t)t * K;
     int at[kSlots];
     float w[kSlots], dot[kSlots];
 #pragma unroll
@@ -205,56 +242,58 @@ __global__ void __launch_bounds__(256) k_exchange(const ExchangeArgs a) {
         dot[k] = 0.f;
         if (k < K) {
             at[k] = a.inv[p + k];
-            if (at[k] >= P) at[k] = -1;  // (no place: as a dropped slot)
+            if (at[k] >= pairs) at[k] = -1;  // (no place: as a dropped slot)
             if (a.w) w[k] = a.w[p + k];
         }
     }
-    const V* tok = reinterpret_cast<const V*>(a.tok) + (int64_t)t * nv;
-    const V* rows = reinterpret_cast<const V*>(a.rows);
-    V* out = reinterpret_cast<V*>(a.out);
+    const T* tok = (const T*)a.tok + (int64_t)t * a.H;
+    const T* rows = (const T*)a.rows;
+    T* out = (T*)a.out;
     const bool scaled = a.w != nullptr;
-    for (int j = lane; j < nv; j += TPT) {
-        V x = {}, r[kSlots];
-        if (!GATHER || a.tok) x = tok[j];
+    for (int j = lane * VE; j < nv * VE; j += TPT * VE) {
+        V x, r[kSlots];
+        float xf[VE];
+        if (!GATHER || a.tok) {
+            x = P::get(tok + j);
+            P::values(x, xf);
+        }
         if (GATHER || DOTS) {
 #pragma unroll
             for (int k = 0; k < kSlots; ++k)
-                if (at[k] >= 0) r[k] = rows[(int64_t)at[k] * nv + j];
+                if (at[k] >= 0) r[k] = P::get(rows + (int64_t)at[k] * a.H + j);
         }
+        float sum[VE];
         if (GATHER) {
-            float sum[VE];
 #pragma unroll
-            for (int i = 0; i < VE; ++i) sum[i] = DOTS || !a.tok ? 0.f : to_f(x.v[i]);
+            for (int i = 0; i < VE; ++i) sum[i] = DOTS || !a.tok ? 0.f : xf[i];
+        }
 #pragma unroll
-            for (int k = 0; k < kSlots; ++k)
-                if (at[k] >= 0) {
+        for (int k = 0; k < kSlots; ++k)
+            if (at[k] >= 0) {
+                if (GATHER || DOTS) {
+                    float f[VE];
+                    P::values(r[k], f);
+                    if (DOTS) {
 #pragma unroll
-                    for (int i = 0; i < VE; ++i) sum[i] = scaled ? fmaf(w[k], to_f(r[k].v[i]), sum[i]) : sum[i] + to_f(r[k].v[i]);
+                        for (int i = 0; i < VE; ++i) dot[k] = fmaf(xf[i], f[i], dot[k]);
+                    }
+                    if (GATHER) {
+#pragma unroll
+                        for (int i = 0; i < VE; ++i) sum[i] = fmaf(w[k], f[i], sum[i]);  // (without weights exact: times one)
+                    }
                 }
-            V o;
-#pragma unroll
-            for (int i = 0; i < VE; ++i) o.v[i] = from_f<T>(sum[i]);
-            out[(int64_t)t * nv + j] = o;
-        } else {
-#pragma unroll
-            for (int k = 0; k < kSlots; ++k)
-                if (at[k] >= 0) {
+                if (!GATHER) {
                     V o = x;
                     if (scaled) {
+                        float y[VE];
 #pragma unroll
-                        for (int i = 0; i < VE; ++i) o.v[i] = from_f<T>(w[k] * to_f(x.v[i]));
+                        for (int i = 0; i < VE; ++i) y[i] = w[k] * xf[i];
+                        o = P::pack(y);
                     }
-                    out[(int64_t)at[k] * nv + j] = o;
+                    P::put(out + (int64_t)at[k] * a.H + j, o);
                 }
-        }
-        if (DOTS) {
-#pragma unroll
-            for (int k = 0; k < kSlots; ++k)
-                if (at[k] >= 0) {
-#pragma unroll
-                    for (int i = 0; i < VE; ++i) dot[k] = fmaf(to_f(x.v[i]), to_f(r[k].v[i]), dot[k]);
-                }
-        }
+            }
+        if (GATHER) P::put(out + (int64_t)t * a.H + j, P::pack(sum));
     }
     if (DOTS) store_dots<TPT>(dot, a.dots + p, K);
 }

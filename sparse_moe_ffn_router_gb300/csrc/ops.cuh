@@ -31,6 +31,56 @@ template <typename T, int VE>
 struct alignas(sizeof(T) * VE) Vec {
     T v[VE];
 };
+// 16 bytes of a row as they lie in memory, and their values. (Held as words: as 16-bit elements they would take twice
+// the registers between the two ways of loading them.)
+struct Raw {
+    uint32_t w[4];
+};
+template <typename T>
+struct RawOf;
+template <>
+struct RawOf<float> {
+    static __device__ __forceinline__ void values(const Raw& r, float (&f)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(r.w[i]);
+    }
+    static __device__ __forceinline__ Raw pack(const float (&f)[4]) {
+        return Raw{{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])}};
+    }
+};
+template <>
+struct RawOf<bf16> {
+    static __device__ __forceinline__ void values(const Raw& r, float (&f)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = bf_lo(r.w[i]);
+            f[2 * i + 1] = bf_hi(r.w[i]);
+        }
+    }
+    static __device__ __forceinline__ Raw pack(const float (&f)[8]) {
+        return Raw{{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])}};
+    }
+};
+template <>
+struct RawOf<fp16> {
+    static __device__ __forceinline__ void values(const Raw& r, float (&f)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
+            f[2 * i] = v.x;
+            f[2 * i + 1] = v.y;
+        }
+    }
+    static __device__ __forceinline__ Raw pack(const float (&f)[8]) {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            r.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        return r;
+    }
+};
 #endif
 
 // ---- exchange (exchange.cu): tokens [T, H], rows [T * K, H], inv [T * K]
