@@ -475,7 +475,7 @@ bool make_bf16_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
 }
 
 bool encode_map(CUtensorMap* m, int32_t dtype, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-                const uint32_t* box) {
+                const uint32_t* box, bool swizzle64) {
     auto fn = encode_fn();
     if (!fn || rank < 1 || rank > 5) return false;
     cuuint64_t d[5], st[5];
@@ -487,8 +487,9 @@ bool encode_map(CUtensorMap* m, int32_t dtype, const void* base, int rank, const
         if (i) st[i - 1] = strides[i - 1];
     }
     return fn(m, dtype == MOE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
-              const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Router scores of all T tokens on the tensor cores: logits[:, 0:E] = x . Wr^T (+ br).

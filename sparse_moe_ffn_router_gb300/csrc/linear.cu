@@ -632,12 +632,12 @@ LinPlan lin_plan(int64_t groups, int64_t cols, int64_t F, int blocks, int num_sm
 int pair_boxes(const LinPlan& p, bool one_group) { return one_group && p.pair ? p.width / 2 : kLinBoxRows; }
 
 template <typename T, int MODE, bool GATED>
-cudaError_t launch_plan(int32_t dtype, const LinPlan& p, const CUtensorMap& A, const CUtensorMap& B, LinView v, cudaStream_t s) {
+cudaError_t launch_plan(int32_t dtype, const LinPlan& p, const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& C, LinView v, cudaStream_t s) {
     v.colw = p.colw;
     const int per = (p.pair ? 256 : 128) / (GATED ? 2 : 1);
     v.ftiles = (v.F + per - 1) / per;
     v.vec = v.F % (p.pair ? 8 : 4) == 0;
-    return p.pair ? launch_pair(dtype, MODE, GATED, A, B, v, p.grid, s) : launch_k<T, MODE, GATED>(A, B, v, p.grid, p.split, s);
+    return p.pair ? launch_pair(dtype, MODE, GATED, A, B, C, v, p.grid, s) : launch_k<T, MODE, GATED>(A, B, v, p.grid, p.split, s);
 }
 
 // Row-major [rows, cols] with `pitch` elements between rows.
@@ -710,7 +710,7 @@ cudaError_t linear_t(const LinearArgs& a, cudaStream_t s) {
     CUtensorMap A, B;
     if (!(gated ? map_w_gated(&A, a.d, a.w) : map_w(&A, a.d, a.w, 128)) || !map_2d(&B, a.d.dtype, a.x, a.d.T, a.d.K, a.d.K, v.boxes))
         return cudaErrorInvalidValue;
-    MOE_LAUNCH(MOE_KERNEL_LINEAR, s, (e = gated ? launch_plan<T, kFwd, true>(a.d.dtype, p, A, B, v, s) : launch_plan<T, kFwd, false>(a.d.dtype, p, A, B, v, s)));
+    MOE_LAUNCH(MOE_KERNEL_LINEAR, s, (e = gated ? launch_plan<T, kFwd, true>(a.d.dtype, p, A, B, A, v, s) : launch_plan<T, kFwd, false>(a.d.dtype, p, A, B, A, v, s)));
     return e;
 }
 
@@ -747,7 +747,7 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
         const LinPlan p = lin_plan<T, kDx, false>(g, (d.T + g - 1) / g, d.K, (v.C + 63) / 64, a.num_sms);
         v.boxes = pair_boxes(p, !a.offsets);
         if (!map_w(&A, d, a.w, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, v.boxes)) return cudaErrorInvalidValue;
-        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_plan<T, kDx, false>(d.dtype, p, A, B, v, s)));
+        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_plan<T, kDx, false>(d.dtype, p, A, B, A, v, s)));
         if (e != cudaSuccess) return e;
     }
     if (a.dw) {
@@ -755,7 +755,13 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
         v.out = a.dw;
         v.C = 0;
         const LinPlan p = lin_plan<T, kDw, false>(d.E, d.N, d.K, (int)(((d.T + g - 1) / g + 63) / 64), a.num_sms);
-        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_plan<T, kDw, false>(d.dtype, p, A, B, v, s)));
+        CUtensorMap C = A;
+        if (p.pair) {
+            const uint64_t dim[3] = {(uint64_t)d.K, (uint64_t)d.N, (uint64_t)d.E}, st[2] = {(uint64_t)d.K * 2, (uint64_t)d.N * d.K * 2};
+            const uint32_t box[3] = {32, 32, 1};
+            if (!encode_map(&C, d.dtype, a.dw, 3, dim, st, box, true)) return cudaErrorInvalidValue;
+        }
+        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_plan<T, kDw, false>(d.dtype, p, A, B, C, v, s)));
     }
     return e;
 }

@@ -67,24 +67,50 @@ __device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
 // good to a few 2^-22 relative at the arguments that matter, far below half a step of bf16 (2^-9 and up) or fp16 (2^-12).
 __device__ __forceinline__ float lin_sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
-// Phi(z), the normal distribution function, and e = exp(-z^2 / 2). Phi(-|z|) = e * R(t), t = 1 / (1 + 0.3 |z|): the scaled tail
-// exp(z^2 / 2) * Phi(-|z|) falls smoothly from 1/2 like 1 / |z|, so it is close to a polynomial in t. R is of degree 8,
+// Two fp32 operations in one instruction.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void f2_split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_both(float x) { return f2(x, x); }
+
+// Phi(z), the normal distribution function, and e = exp(-z^2 / 2), of two values. Phi(-|z|) = e * R(t), t = 1 / (1 + 0.3 |z|): the scaled
+// tail exp(z^2 / 2) * Phi(-|z|) falls smoothly from 1/2 like 1 / |z|, so it is close to a polynomial in t. R is of degree 8,
 // fitted here by reweighted least squares at Chebyshev nodes for the least relative error up to |z| = 14: 6e-8, evaluated in fp32
 // 4e-7. (0.5 erfc(-z / sqrt 2) by the library's erfcf: 40 us more over 4096 x 8192.)
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-    const float a = fabsf(z), t = __fdividef(1.0f, fmaf(0.3f, a, 1.0f));
-    float p = 0.0383782946f;
-    p = fmaf(p, t, -0.169166133f);
-    p = fmaf(p, t, 0.228660107f);
-    p = fmaf(p, t, -0.0765065104f);
-    p = fmaf(p, t, 0.142535552f);
-    p = fmaf(p, t, 0.0946835130f);
-    p = fmaf(p, t, 0.121920347f);
-    p = fmaf(p, t, 0.119487688f);
-    p = fmaf(p, t, 7.16889144e-06f);
-    e = __expf(-0.5f * z * z);
-    p *= e;
-    return z < 0.f ? p : 1.0f - p;
+__device__ __forceinline__ void normal_cdf(float z0, float z1, F2& cdf, F2& e) {
+    const F2 z = f2(z0, z1), d = f2_fma(f2_both(0.3f), f2(fabsf(z0), fabsf(z1)), f2_both(1.0f));
+    float d0, d1, x0, x1;
+    f2_split(d, d0, d1);
+    const F2 t = f2(__fdividef(1.0f, d0), __fdividef(1.0f, d1));
+    F2 p = f2_fma(f2_both(0.0383782946f), t, f2_both(-0.169166133f));
+    p = f2_fma(p, t, f2_both(0.228660107f));
+    p = f2_fma(p, t, f2_both(-0.0765065104f));
+    p = f2_fma(p, t, f2_both(0.142535552f));
+    p = f2_fma(p, t, f2_both(0.0946835130f));
+    p = f2_fma(p, t, f2_both(0.121920347f));
+    p = f2_fma(p, t, f2_both(0.119487688f));
+    p = f2_fma(p, t, f2_both(7.16889144e-06f));
+    f2_split(f2_mul(f2_mul(z, z), f2_both(-0.5f)), x0, x1);
+    e = f2(__expf(x0), __expf(x1));
+    p = f2_mul(p, e);
+    f2_split(p, x0, x1);
+    cdf = f2(z0 < 0.f ? x0 : 1.0f - x0, z1 < 0.f ? x1 : 1.0f - x1);
 }
 
 // v = act(v) of N values: one branch, then N independent chains.
@@ -94,10 +120,19 @@ __device__ __forceinline__ void lin_act(int act, float (&v)[N]) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] *= lin_sigmoid(v[i]);
     } else if (act == MOE_ACT_GELU) {
+        if constexpr (N == 1) {
+            F2 c, e;
+            float p, unused;
+            normal_cdf(v[0], v[0], c, e);
+            f2_split(c, p, unused);
+            v[0] *= p;
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float e;
-            v[i] *= normal_cdf(v[i], e);
+            for (int i = 0; i + 1 < N; i += 2) {
+                F2 c, e;
+                normal_cdf(v[i], v[i + 1], c, e);
+                f2_split(f2_mul(f2(v[i], v[i + 1]), c), v[i], v[i + 1]);
+            }
         }
     } else if (act == MOE_ACT_RELU) {
 #pragma unroll
@@ -118,10 +153,11 @@ __device__ __forceinline__ void lin_slope(int act, const float (&z)[N], float (&
         }
     } else if (act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float e;
-            const float p = normal_cdf(z[i], e);
-            d[i] *= fmaf(z[i] * 0.39894228f, e, p);  // Phi + z phi
+        for (int i = 0; i + 1 < N; i += 2) {
+            F2 c, e;
+            normal_cdf(z[i], z[i + 1], c, e);
+            const F2 slope = f2_fma(f2_mul(f2(z[i], z[i + 1]), f2_both(0.39894228f)), e, c);  // Phi + z phi
+            f2_split(f2_mul(f2(d[i], d[i + 1]), slope), d[i], d[i + 1]);
         }
     } else if (act == MOE_ACT_RELU) {
 #pragma unroll
@@ -207,7 +243,8 @@ constexpr int kFewRows = 64;
 cudaError_t launch_few(int32_t dtype, bool gated, const void* x, const void* w, const LinView& v, int num_sms, cudaStream_t s);
 
 // Launches of the pair kernel (linear_pair.cu); grid: CTAs, an even number.
-cudaError_t launch_pair(int32_t dtype, int mode, bool gated, const CUtensorMap& A, const CUtensorMap& B, const LinView& v, int grid,
-                        cudaStream_t s);
+// C: kDw, the map of its result.
+cudaError_t launch_pair(int32_t dtype, int mode, bool gated, const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& C, const LinView& v,
+                        int grid, cudaStream_t s);
 
 }  // namespace moe

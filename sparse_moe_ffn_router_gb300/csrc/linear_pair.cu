@@ -15,12 +15,13 @@
 
 namespace moe {
 
-constexpr int kPairStages = 6;
 constexpr uint32_t kPairB = 128 * 64 * 2;  // half of the columns
-constexpr uint32_t kPairRing = kPairStages * (kLinA + kPairB);
-constexpr uint32_t kPairScratch = kLinEpiWarps * 2048;
+// Stages of 32 KB, and the epilogue warps' buffers: one of 2 KB each; kDw has two, and a stage less.
+constexpr int pair_stages(int mode) { return mode == kDw ? 5 : 6; }
+constexpr uint32_t pair_ring(int mode) { return (uint32_t)pair_stages(mode) * (kLinA + kPairB); }
+constexpr uint32_t pair_scratch(int mode) { return kLinEpiWarps * (mode == kDw ? 4096u : 2048u); }
 constexpr uint32_t kPairTables = 2 * (kLinMaxE + 4) * 4;
-constexpr uint32_t kPairBytes = 1024 + kPairRing + kPairScratch + kPairTables + 256;
+constexpr uint32_t pair_bytes(int mode) { return 1024 + pair_ring(mode) + pair_scratch(mode) + kPairTables + 256; }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b, bf16) { return pack_bf16x2(a, b); }
 __device__ __forceinline__ uint32_t pack2(float a, float b, fp16) {
@@ -187,10 +188,53 @@ __device__ __forceinline__ void pair_epilogue(const LinView& a, uint32_t tmem, u
     }
 }
 
+// The same of kDw: nothing is added, and a tile's rows are W's own, so a warp's 32 x 32 go out by TMA (rows and
+// columns past W's are left out there), from two buffers in turn.
+template <typename T>
+__device__ __forceinline__ void pair_epilogue_dw(const CUtensorMap* mC, uint32_t tmem, uint32_t buf, int q, int h, int e, int c0, int fl, int cols,
+                                                 bool any, int& turn) {
+    const int lane = threadIdx.x & 31;
+    for (int c = h * 32; c < cols; c += 64, turn ^= 1) {
+        uint32_t r[32];
+        if (any) {
+            tmem_ld_frag4(tmem + c, r);
+            tmem_ld_frag4(tmem + (16u << 16) + c, r + 16);
+            asm volatile("tcgen05.wait::ld.sync.aligned;"
+                         : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
+                           "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                           "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                           "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0u;
+        }
+        const uint32_t at = buf + (uint32_t)turn * 2048u;
+        if (lane == 0) tma_store_wait_read<1>();  // the store before the last has read this buffer
+        __syncwarp();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            uint32_t p[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int i = (m >> 1) * 16 + b * 4 + (m & 1) * 2;
+                p[m] = pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]), T());
+            }
+            stmatrix4_trans(at + at64(8 * b + (lane & 7), lane >> 3), p[0], p[1], p[2], p[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(mC, at, fl + q * 32, c0 + c, e);
+            tma_store_commit();
+        }
+    }
+}
+
 template <typename T, int MODE, bool GATED>
 __global__ void __launch_bounds__(kLinThreads, 1)
-    k_linear_pair(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB, const LinView a) {
-    constexpr int kStages = kPairStages;
+    k_linear_pair(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mC, const LinView a) {
+    constexpr int kStages = pair_stages(MODE);
+    constexpr uint32_t kPairRing = pair_ring(MODE), kPairScratch = pair_scratch(MODE);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -372,13 +416,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     } else if (warp >= kLinEpiWarp0) {
         // ---------------- epilogue of this CTA's features: lanes 32 q .. of the accumulator, every other 32 columns
         const int q = warp & 3, h = (warp - kLinEpiWarp0) >> 2;
-        const uint32_t buf = smem_u32(scratch + (warp - kLinEpiWarp0) * 2048);
-        int local = 0;
+        const uint32_t buf = smem_u32(scratch + (warp - kLinEpiWarp0) * (kPairScratch / kLinEpiWarps));
+        int local = 0, turn = 0;
         for (int t = first; t < total; t += step, ++local) {
             const LinTile ti = walk.to(a, off, start, t);
             const int b = local & 1;
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
-            const int64_t row0 = MODE == kDw ? (int64_t)ti.e * a.N + ti.c0 : (int64_t)ti.row0 + ti.c0;
             bool ready = false;
             if (!*abort_flag) ready = mbar_wait(&accf[b], use, a.wait_ns);
             ready = __all_sync(0xffffffffu, ready);
@@ -390,12 +433,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 break;
             }
             tc_fence_after();
-            pair_epilogue<T, MODE, GATED>(a, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 256), buf, q, h, ti.e, row0,
-                                          (ti.f * 2 + (int)rank) * (GATED ? 64 : 128), ti.cols, ti.blocks > 0);
+            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 256);
+            const int fl = (ti.f * 2 + (int)rank) * (GATED ? 64 : 128);
+            if constexpr (MODE == kDw)
+                pair_epilogue_dw<T>(&mC, acc, buf, q, h, ti.e, ti.c0, fl, ti.cols, ti.blocks > 0, turn);
+            else
+                pair_epilogue<T, MODE, GATED>(a, acc, buf, q, h, ti.e, (int64_t)ti.row0 + ti.c0, fl, ti.cols, ti.blocks > 0);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(&acce[b], 0);
         }
+        if (MODE == kDw && lane == 0) tma_store_wait_all();
         __syncwarp();
     }
     tc_fence_before();
@@ -408,19 +456,19 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 }
 
 template <typename T, int MODE, bool GATED>
-static cudaError_t launch_pair_k(const CUtensorMap& A, const CUtensorMap& B, const LinView& v, int grid, cudaStream_t s) {
+static cudaError_t launch_pair_k(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& C, const LinView& v, int grid, cudaStream_t s) {
     static bool configured[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(k_linear_pair<T, MODE, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairBytes);
+        cudaError_t e = cudaFuncSetAttribute(k_linear_pair<T, MODE, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_bytes(MODE));
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = kPairBytes;
+    cfg.dynamicSmemBytes = pair_bytes(MODE);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -430,19 +478,19 @@ static cudaError_t launch_pair_k(const CUtensorMap& A, const CUtensorMap& B, con
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_linear_pair<T, MODE, GATED>, A, B, v);
+    return cudaLaunchKernelEx(&cfg, k_linear_pair<T, MODE, GATED>, A, B, C, v);
 }
 
 template <typename T>
-static cudaError_t launch_pair_t(int mode, bool gated, const CUtensorMap& A, const CUtensorMap& B, const LinView& v, int grid, cudaStream_t s) {
-    if (mode == kDx) return launch_pair_k<T, kDx, false>(A, B, v, grid, s);
-    if (mode == kDw) return launch_pair_k<T, kDw, false>(A, B, v, grid, s);
-    return gated ? launch_pair_k<T, kFwd, true>(A, B, v, grid, s) : launch_pair_k<T, kFwd, false>(A, B, v, grid, s);
+static cudaError_t launch_pair_t(int mode, bool gated, const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& C, const LinView& v, int grid, cudaStream_t s) {
+    if (mode == kDx) return launch_pair_k<T, kDx, false>(A, B, C, v, grid, s);
+    if (mode == kDw) return launch_pair_k<T, kDw, false>(A, B, C, v, grid, s);
+    return gated ? launch_pair_k<T, kFwd, true>(A, B, C, v, grid, s) : launch_pair_k<T, kFwd, false>(A, B, C, v, grid, s);
 }
 
-cudaError_t launch_pair(int32_t dtype, int mode, bool gated, const CUtensorMap& A, const CUtensorMap& B, const LinView& v, int grid,
+cudaError_t launch_pair(int32_t dtype, int mode, bool gated, const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& C, const LinView& v, int grid,
                         cudaStream_t s) {
-    return dtype == MOE_FP16 ? launch_pair_t<fp16>(mode, gated, A, B, v, grid, s) : launch_pair_t<bf16>(mode, gated, A, B, v, grid, s);
+    return dtype == MOE_FP16 ? launch_pair_t<fp16>(mode, gated, A, B, C, v, grid, s) : launch_pair_t<bf16>(mode, gated, A, B, C, v, grid, s);
 }
 
 }  // namespace moe

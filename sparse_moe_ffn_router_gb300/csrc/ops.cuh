@@ -137,10 +137,10 @@ struct LinearArgs {
 constexpr int kDzRows = 32;  // rows of a chunk
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_backward(const LinearArgs& a, cudaStream_t s);
-// A tensor map for TMA with 128-byte swizzle and zeros outside: dims and box innermost first, strides in
+// A tensor map for TMA with 128-byte (or 64-byte) swizzle and zeros outside: dims and box innermost first, strides in
 // bytes of dims 1 .. rank - 1.
 bool encode_map(CUtensorMap* m, int32_t dtype, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-                const uint32_t* box);
+                const uint32_t* box, bool swizzle64 = false);
 
 // SMs of the current device, the time limit of bounded device waits, the signal held back in tests (api.cu).
 int device_sms();

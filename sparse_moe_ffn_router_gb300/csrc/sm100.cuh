@@ -199,6 +199,19 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const void* map, uint64_t
         : "memory");
 }
 
+// A box from shared to global memory (what lies outside the tensor is left out); the stores of a thread are waited for in
+// groups. Writes to shared memory that it reads are fenced by fence_proxy_async_smem first.
+__device__ __forceinline__ void tma_store_3d(const void* map, uint32_t src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map), "r"(src), "r"(c0), "r"(c1),
+                 "r"(c2)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// At most N groups of this thread's stores have shared memory left to read.
+template <int N>
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // The same with an L2 cache policy (l2_evict_first / l2_evict_last).
 __device__ __forceinline__ void tma_load_2d_hint(void* dst, const void* map, uint64_t* bar, int c0, int c1,
                                                  uint64_t policy) {
