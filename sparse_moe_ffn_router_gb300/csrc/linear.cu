@@ -408,23 +408,29 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
 // Eight columns of a row, of which n exist.
 template <typename T, int VE>
-__device__ __forceinline__ Vec<T, 8> ld_cols(const T* p, int n) {
-    Vec<T, 8> x;
+__device__ __forceinline__ Raw ld_cols(const T* p, int n) {
+    Raw r;
     if (VE == 8) {
-        x = *reinterpret_cast<const Vec<T, 8>*>(p);
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
     } else {
+        r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x.v[i] = i < n ? p[i] : from_f<T>(0.f);
+        for (int i = 0; i < 8; ++i)
+            if (i < n) r.w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
     }
-    return x;
+    return r;
 }
 
+template <typename T>
+__device__ __forceinline__ void st_cols(T* p, const Raw& r) { *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]); }
+
 template <typename T, int VE, bool GATED>
-__global__ void __launch_bounds__(256) k_dz(const LinearArgs a, int pitch) {
+__global__ void __launch_bounds__(256, 3) k_dz(const LinearArgs a, int pitch) {
     __shared__ int off[kLinMaxE + 1];
     __shared__ float sums[GATED ? 2 : 1][16][128];
     constexpr int kMore = kDzRows / 16;  // rows of a thread, all loaded before the first is used
-    typedef Vec<T, 8> V;
+    typedef RawOf<T> R;
     grid_dep_wait();
     grid_dep_launch();
     const int N = a.d.N, E = a.d.E, wide = GATED ? N / 2 : N;
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(256) k_dz(const LinearArgs a, int pitch) {
     const bool need_z = GATED || a.d.act != MOE_ACT_NONE;
     T* dz = reinterpret_cast<T*>(a.dz);
     const T *z = reinterpret_cast<const T*>(a.z_in), *dout = reinterpret_cast<const T*>(a.dout);
-    V dv[kMore], zv[kMore], uv[kMore];
+    Raw dv[kMore], zv[kMore], uv[kMore];
 #pragma unroll
     for (int k = 0; k < kMore; ++k) {
         const int r = r0 + ty + 16 * k;
@@ -444,15 +450,21 @@ __global__ void __launch_bounds__(256) k_dz(const LinearArgs a, int pitch) {
             if (GATED) uv[k] = ld_cols<T, VE>(z + (int64_t)r * N + wide + f, n);
         }
     }
-    for (int e = threadIdx.x; e <= E; e += 256) off[e] = a.offsets ? min(max(a.offsets[e], 0), a.d.T) : e ? a.d.T : 0;
-    __syncthreads();
-    int lo = 0, hi = E;  // the last expert whose rows begin at or before r0
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (off[mid] <= r0) lo = mid; else hi = mid;
+    // whose rows they are matters to the column sums alone (rows behind the last expert's are read into nothing)
+    const bool split = a.offsets && a.dbias;
+    int lo = 0, hi = split ? E : 1;
+    if (split) {
+        for (int e = threadIdx.x; e <= E; e += 256) off[e] = min(max(a.offsets[e], 0), a.d.T);
+        __syncthreads();
+        while (hi - lo > 1) {  // the last expert whose rows begin at or before r0
+            const int mid = (lo + hi) >> 1;
+            if (off[mid] <= r0) lo = mid; else hi = mid;
+        }
+        hi = E;
     }
-    for (int e = lo; e < E && off[e] < r1; ++e) {
-        const int b0 = max(off[e], r0), b1 = min(off[e + 1], r1);
+    for (int e = lo; e < hi; ++e) {
+        const int b0 = split ? max(off[e], r0) : r0, b1 = split ? min(off[e + 1], r1) : r1;
+        if (split && off[e] >= r1) break;
         if (b0 >= b1) continue;
         float sv[8], su[8];
 #pragma unroll
@@ -461,38 +473,30 @@ __global__ void __launch_bounds__(256) k_dz(const LinearArgs a, int pitch) {
         for (int k = 0; k < kMore; ++k) {
             const int r = r0 + ty + 16 * k;
             if (r < b0 || r >= b1 || n <= 0) continue;
-            float d[8], v[8], u[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                d[i] = to_f(dv[k].v[i]);
-                if (need_z) v[i] = to_f(zv[k].v[i]);
-            }
+            float d[8], v[8];
+            R::values(dv[k], d);
+            if (need_z) R::values(zv[k], v);
+            const int64_t at = (int64_t)r * pitch + f;
             if (GATED) {
+                float u[8];
+                R::values(uv[k], u);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float p = lin_sigmoid(v[i]), dd = d[i];
-                    d[i] = dd * to_f(uv[k].v[i]) * (p * (1.f + v[i] * (1.f - p)));
+                    d[i] = dd * u[i] * (p * (1.f + v[i] * (1.f - p)));
                     u[i] = dd * (v[i] * p);
+                    su[i] += u[i];
                 }
+                if (dz) st_cols(dz + at + wide, R::pack(u));
             } else {
                 lin_slope<8>(a.d.act, v, d);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+                if (VE == 1 && i >= n) d[i] = 0.f;  // (columns up to the pitch are zeros)
                 sv[i] += d[i];
-                if (GATED) su[i] += u[i];
             }
-            if (dz) {
-                V o;  // (columns up to the pitch are zeros)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o.v[i] = from_f<T>(i < n ? d[i] : 0.f);
-                *reinterpret_cast<V*>(dz + (int64_t)r * pitch + f) = o;
-                if (GATED) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o.v[i] = from_f<T>(u[i]);
-                    *reinterpret_cast<V*>(dz + (int64_t)r * pitch + wide + f) = o;
-                }
-            }
+            if (dz) st_cols(dz + at, R::pack(d));
         }
         if (a.dbias) {
             __syncthreads();
