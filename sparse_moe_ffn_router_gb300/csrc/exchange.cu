@@ -9,6 +9,8 @@
 // All of it is bound by HBM: a token row is read once and kept in registers while its K copies are
 // written, and a token's K rows are read once, side by side, and summed in fp32 in slot order.
 // Sums and dots run in a fixed order, so results are the same bits on every call.
+#include <atomic>
+
 #include <cooperative_groups.h>
 
 #include "ops.cuh"
@@ -18,12 +20,12 @@ namespace moe {
 namespace cg = cooperative_groups;
 
 // ---------------------------------------------------------------------------------------
-// sort: one thread-block cluster of up to 8 CTAs. A CTA takes a run of pairs, each of its 32 warps a
-// piece of the run. Pass one counts each warp's pairs per expert (equal ids of 32 lanes at once, by votes,
+// sort: one thread-block cluster of up to 16 CTAs (8 where the device has no room for 16). A CTA takes a run of pairs, each
+// of its 32 warps a piece of the run. Pass one counts each warp's pairs per expert (equal ids of 32 lanes at once, by votes,
 // no atomics), the counts are scanned over warps, over CTAs (read through distributed shared
-// memory) and over experts, pass two ranks the same pairs again and writes their places. One launch
-// and no workspace: the 8 CTAs' two passes over 32768 ids cost less than a second launch would.
-constexpr int kSortWarps = 32, kSortMaxE = 256, kSortCtas = 8;
+// memory) and over experts, pass two writes the pairs' places. One launch and no workspace: 8 pairs 3.0 us, 32768
+// pairs 7.1 (8.0 by 8 CTAs), 131072 pairs 14.4 (23.5).
+constexpr int kSortWarps = 32, kSortMaxE = 256, kSortCtas = 16;
 
 // The lanes whose expert (0 .. 255, or -1: none) is this lane's. One vote a bit: the match instruction takes one turn for each
 // distinct value, and 32 lanes of 256 experts mostly are: 32768 ids took 12 us with it.
@@ -87,9 +89,10 @@ __global__ void __launch_bounds__(32 * kSortWarps, 1)
         }
         tot[e] = sum;
     }
-    cl.sync();
-    int all = 0, before = 0;
-    if (e < E) {
+    if (n > 1) cl.sync();
+    int all = e < E ? tot[e] : 0, before = 0;
+    if (n > 1 && e < E) {
+        all = 0;
         int c[kSortCtas];  // all on their way at once
 #pragma unroll
         for (int r = 0; r < kSortCtas; ++r) c[r] = r < n ? cl.map_shared_rank(tot, r)[e] : 0;
@@ -155,13 +158,41 @@ __global__ void __launch_bounds__(32 * kSortWarps, 1)
             }
         }
     }
-    cl.sync();  // no CTA leaves while another may still read its counts
+    if (n > 1) cl.sync();  // no CTA leaves while another may still read its counts
+}
+
+// CTAs of the largest sorting cluster that the current device holds.
+static int sort_ctas() {
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 8;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSortCtas);
+    cfg.blockDim = dim3(32 * kSortWarps);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSortCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int fits = 0;
+    if (cudaFuncSetAttribute(k_sort_pairs, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&fits, k_sort_pairs, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        fits = 0;
+    }
+    n = fits > 0 ? kSortCtas : 8;
+    cache[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 cudaError_t launch_sort_pairs(const int32_t* ids, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* inv, int P,
                               int E, cudaStream_t s) {
     int n = 1;
     while (n < kSortCtas && P > 1024 * n) n *= 2;
+    if (n > 8) n = sort_ctas();
     const int64_t per = ((int64_t)P + n * kSortWarps - 1) / (n * kSortWarps);
     const int seg = (int)((per + 31) / 32 * 32);
     cudaLaunchConfig_t cfg = {};

@@ -386,11 +386,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 cluster_sync_all();
             }
         }
-    } else if (split > 1) {
-        for (int t = first; t < total; t += step) {
-            cluster_sync_all();
-            cluster_sync_all();
+    } else {
+        if (MODE != kFwd && a.dbias) {
+            lin_dbias<T>(a, off, blockIdx.x * 2 + warp - 2, gridDim.x * 2);
+            __syncwarp();
         }
+        if (split > 1)
+            for (int t = first; t < total; t += step) {
+                cluster_sync_all();
+                cluster_sync_all();
+            }
     }
     tc_fence_before();
     __syncthreads();
@@ -517,26 +522,15 @@ __global__ void __launch_bounds__(256, 3) k_dz(const LinearArgs a, int pitch) {
     }
 }
 
-// db[e, n]: an expert's chunks in order. 64 columns a CTA, four threads a column.
+// db alone, where no product is asked for.
 template <typename T>
-__global__ void __launch_bounds__(256) k_dbias(const LinearArgs a) {
-    __shared__ float sm[4][64];
+__global__ void __launch_bounds__(256) k_dbias(const LinView a) {
+    __shared__ int off[kLinMaxE + 1];
     grid_dep_wait();
     grid_dep_launch();
-    const int e = blockIdx.y, n = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
-    const int b0 = a.offsets ? min(max(a.offsets[e], 0), a.d.T) : 0, b1 = a.offsets ? min(max(a.offsets[e + 1], 0), a.d.T) : a.d.T;
-    float s = 0.f;
-    if (b0 < b1 && n < a.d.N) {
-        const int c0 = b0 / kDzRows, c1 = (b1 - 1) / kDzRows + 1, per = (c1 - c0 + 3) / 4;
-#pragma unroll 4
-        for (int c = c0 + q * per; c < min(c1, c0 + (q + 1) * per); ++c) s += a.part[(int64_t)(c + e) * a.d.N + n];
-    }
-    sm[q][threadIdx.x & 63] = s;
+    for (int e = threadIdx.x; e <= a.E; e += 256) off[e] = a.offsets ? min(max(a.offsets[e], 0), a.T) : e ? a.T : 0;
     __syncthreads();
-    if (q == 0 && n < a.d.N) {
-        const int i = threadIdx.x;
-        reinterpret_cast<T*>(a.dbias)[(int64_t)e * a.d.N + n] = from_f<T>((sm[0][i] + sm[1][i]) + (sm[2][i] + sm[3][i]));
-    }
+    lin_dbias<T>(a, off, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -736,8 +730,6 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
     if (a.dz || a.dbias) {
         MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s,
                    (e = gated ? launch_dz<T, 8, true>(a, pitch, s) : vec ? launch_dz<T, 8, false>(a, pitch, s) : launch_dz<T, 1, false>(a, pitch, s)));
-        if (e == cudaSuccess && a.dbias)
-            MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_pdl(k_dbias<T>, dim3((d.N + 63) / 64, d.E), dim3(256), 0, s, a)));
         if (e != cudaSuccess) return e;
     }
     const void* dz = plain ? a.dout : a.dz;
@@ -745,6 +737,12 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
     CUtensorMap A, B;
     LinView v = view_of(a);
     v.F = d.K;
+    v.part = a.part;
+    v.dbias = a.dbias;  // (the first of the products adds it up)
+    if (a.dbias && !a.dx && !a.dw) {
+        MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_pdl(k_dbias<T>, dim3(a.num_sms), dim3(256), 0, s, v)));
+        return e;
+    }
     if (a.dx) {
         v.out = a.dx;
         v.C = d.N;
@@ -753,6 +751,7 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
         if (!map_w(&A, d, a.w, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, v.boxes)) return cudaErrorInvalidValue;
         MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_plan<T, kDx, false>(d.dtype, p, A, B, A, v, s)));
         if (e != cudaSuccess) return e;
+        v.dbias = nullptr;
     }
     if (a.dw) {
         if (!map_2d(&A, d.dtype, a.x, d.T, d.K, d.K, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, 64)) return cudaErrorInvalidValue;

@@ -30,6 +30,8 @@ struct LinView {
     int vec;          // rows of out, residual and z start on 8 bytes (pair kernel: on 16)
     int boxes;        // rows of a K-major column-side TMA box
     int suppress;     // testing aid: CTA 0 never loads its first stage
+    const float* part;  // kDx, kDw: column sums to add up beside the products, or NULL
+    void* dbias;
     uint32_t* err;
     uint64_t wait_ns;
 };
@@ -241,6 +243,33 @@ struct LinWalk {
 // The forward pass of at most 8 rows of one matrix, or kFewRows of several (linear_few.cu).
 constexpr int kFewRows = 64;
 cudaError_t launch_few(int32_t dtype, bool gated, const void* x, const void* w, const LinView& v, int num_sms, cudaStream_t s);
+
+// db[e, n] of the chunks' column sums, a warp to 32 columns of an expert: the chunks of its rows in order. For `warps`
+// warps, of which this is number `w`: the products' kernels have two warps to spare in every CTA.
+template <typename T>
+__device__ void lin_dbias(const LinView& a, const int* off, int w, int warps) {
+    const int lane = threadIdx.x & 31, strips = (a.N + 31) / 32;
+    for (int64_t i = w; i < (int64_t)a.E * strips; i += warps) {
+        const int e = (int)(i / strips), n = (int)(i - (int64_t)e * strips) * 32 + lane;
+        if (n >= a.N) continue;
+        const int b0 = off[e], b1 = off[e + 1];
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        if (b0 < b1) {
+            const int c0 = b0 / kDzRows, c1 = (b1 - 1) / kDzRows + 1;
+            const float* p = a.part + (int64_t)(c0 + e) * a.N + n;
+            int c = c0;
+            for (; c + 4 <= c1; c += 4, p += (int64_t)4 * a.N) {
+                float v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = p[(int64_t)k * a.N];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[k] += v[k];
+            }
+            for (; c < c1; ++c, p += a.N) s[0] += *p;
+        }
+        reinterpret_cast<T*>(a.dbias)[(int64_t)e * a.N + n] = from_f<T>((s[0] + s[1]) + (s[2] + s[3]));
+    }
+}
 
 // Launches of the pair kernel (linear_pair.cu); grid: CTAs, an even number.
 // C: kDw, the map of its result.

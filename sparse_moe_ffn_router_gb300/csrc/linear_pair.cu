@@ -445,6 +445,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         if (MODE == kDw && lane == 0) tma_store_wait_all();
         __syncwarp();
+    } else if (MODE != kFwd && a.dbias) {
+        lin_dbias<T>(a, off, blockIdx.x * 2 + warp - 2, gridDim.x * 2);
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
