@@ -68,15 +68,38 @@ _TORCH = {BF16: torch.bfloat16, FP16: torch.float16, FP32: torch.float32}
 _DTYPE = {v: k for k, v in _TORCH.items()}
 
 
-class LinearDims(ctypes.Structure):
+class _Dims(ctypes.Structure):
+    """Sizes of a call, with what the checks of its tensors need worked out once (again after a field is set)."""
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        self.__dict__.pop("checked", None)
+
+    def __getattr__(self, name):
+        if name != "checked":
+            raise AttributeError(name)
+        c = self.__dict__["checked"] = self._checked()
+        return c
+
+
+class LinearDims(_Dims):
     """moe_linear_dims: T rows of K columns through one matrix [N, K], or through E of them by the rows' expert."""
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "N", "K", "E", "act", "dtype")]
 
     def __init__(self, T, N, K, E=1, act=ACT_NONE, dtype=BF16):
         super().__init__(int(T), int(N), int(K), int(E), int(act), int(dtype))
 
+    def _checked(self):
+        """Type, and the shapes of x, out, z, w, bias and offsets; the one matrix of E = 1 may come without its first dimension."""
+        dt = _TORCH.get(self.dtype)
+        if dt is None:
+            raise MoEError(1, "moe_linear_dims")
+        T, N, K, E = self.T, self.N, self.K, self.E
+        return (dt, (T, K), (T, N // 2 if self.act == ACT_SWIGLU else N), (T, N), (E, N, K), (N, K) if E == 1 else None, (E, N),
+                (N,) if E == 1 else None, (E + 1,))
 
-class NormDims(ctypes.Structure):
+
+class NormDims(_Dims):
     """moe_norm_dims: T rows of H columns; gate: GATE_*, gate_act: ACT_NONE, ACT_SIGMOID or ACT_SILU of it."""
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "dtype", "gate", "gate_act", "flags")] + [
         (n, ctypes.c_float) for n in ("eps", "branch_scale", "residual_scale")]
@@ -84,6 +107,13 @@ class NormDims(ctypes.Structure):
     def __init__(self, T, H, dtype=BF16, post=True, gate=GATE_NONE, gate_act=ACT_NONE, eps=1e-6, branch_scale=1.0, residual_scale=1.0):
         super().__init__(int(T), int(H), int(dtype), int(gate), int(gate_act), NORM_POST if post else 0, float(eps), float(branch_scale),
                          float(residual_scale))
+
+    def _checked(self):
+        """Type, and the shapes of rows, gammas and gate."""
+        dt, T, H = _TORCH.get(self.dtype), self.T, self.H
+        if dt is None:
+            raise MoEError(1, "moe_norm_dims")
+        return dt, (T, H), (H,), {GATE_TOKEN: (T,), GATE_CHANNEL: (H,), GATE_FULL: (T, H)}.get(self.gate, ())
 
 
 class CWeights(ctypes.Structure):
@@ -598,7 +628,7 @@ def moe_sort_pairs(E: int, ids, counts, offsets, perm, inv, stream=None):
         raise ValueError("ids must be int32 [T, K]")
     shape = ids.shape
     T, K = shape
-    dev, flat = torch.cuda.current_device() if ids.is_cuda else -2, (T * K,)
+    dev, flat = _current(ids), (T * K,)
     _check(load_library().moe_sort_pairs(T, K, E, _ptr_of(dev, _I32, shape, "ids", ids), _ptr_of(dev, _I32, (E,), "counts", counts),
                                          _ptr_of(dev, _I32, (E + 1,), "offsets", offsets), _ptr_of(dev, _I32, flat, "perm", perm, shape),
                                          _ptr_of(dev, _I32, flat, "inv", inv, shape), _stream_of(stream, dev)), "moe_sort_pairs")
@@ -616,7 +646,7 @@ def _exchange(token, rows):
     code = _DTYPE.get(token.dtype)
     if code is None:
         raise TypeError(f"token rows must be bfloat16, float16 or float32, got {token.dtype}")
-    return torch.cuda.current_device() if token.is_cuda else -2, token.dtype, code, T, K, H
+    return _current(token), token.dtype, code, T, K, H
 
 
 def moe_dispatch(x, inv, topk_w, rows, stream=None):
@@ -665,13 +695,9 @@ def new_linear_workspace(dims: LinearDims, backward: bool = False, device="cuda"
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _linear(d: LinearDims, t):
-    """Device, type and sizes of a call, t: one of its tensors. The one matrix of E = 1 may come without its first dimension."""
-    T, N, K, E = d.T, d.N, d.K, d.E
-    dt = _TORCH.get(d.dtype)
-    if dt is None:
-        raise MoEError(1, "moe_linear_dims")
-    return torch.cuda.current_device() if t.is_cuda else -2, dt, T, N, K, E, N // 2 if d.act == ACT_SWIGLU else N
+def _current(t) -> int:
+    """The current CUDA device, where the kernels will run; t: the first tensor of the call."""
+    return torch.cuda.current_device() if t.is_cuda else -2
 
 
 def _workspace(device: int, t):
@@ -683,22 +709,22 @@ def _workspace(device: int, t):
 def moe_linear(dims: LinearDims, x, w, bias, offsets, residual, out, z, workspace, stream=None):
     """out = act(x . W_e^T + bias_e) + residual, e the expert whose rows [offsets[e], offsets[e + 1]) hold x's row
     (offsets None: the one matrix); z (or None) receives the pre-activations for moe_linear_backward."""
-    dev, dt, T, N, K, E, wide = _linear(dims, x)
-    one = E == 1
-    _check(load_library().moe_linear(ctypes.byref(dims), _ptr_of(dev, dt, (T, K), "x", x), _ptr_of(dev, dt, (E, N, K), "w", w, (N, K) if one else None),
-                                     _ptr_of(dev, dt, (E, N), "bias", bias, (N,) if one else None), _ptr_of(dev, _I32, (E + 1,), "offsets", offsets),
-                                     _ptr_of(dev, dt, (T, wide), "residual", residual), _ptr_of(dev, dt, (T, wide), "out", out),
-                                     _ptr_of(dev, dt, (T, N), "z", z), *_workspace(dev, workspace), _stream_of(stream, dev)), "moe_linear")
+    dev = _current(x)
+    dt, rows, wide, pre, mat, mat1, vec, vec1, ends = dims.checked
+    _check(load_library().moe_linear(ctypes.byref(dims), _ptr_of(dev, dt, rows, "x", x), _ptr_of(dev, dt, mat, "w", w, mat1),
+                                     _ptr_of(dev, dt, vec, "bias", bias, vec1), _ptr_of(dev, _I32, ends, "offsets", offsets),
+                                     _ptr_of(dev, dt, wide, "residual", residual), _ptr_of(dev, dt, wide, "out", out),
+                                     _ptr_of(dev, dt, pre, "z", z), *_workspace(dev, workspace), _stream_of(stream, dev)), "moe_linear")
 
 
 def moe_linear_backward(dims: LinearDims, x, w, offsets, z, dout, dx, dw, dbias, workspace, stream=None):
     """Gradients of moe_linear's x, w and bias (each may be None) for the gradient dout of its result; the residual's is dout."""
-    dev, dt, T, N, K, E, wide = _linear(dims, dout)
-    flat, line = ((N, K), (N,)) if E == 1 else (None, None)
+    dev = _current(dout)
+    dt, rows, wide, pre, mat, mat1, vec, vec1, ends = dims.checked
     _check(load_library().moe_linear_backward(
-        ctypes.byref(dims), _ptr_of(dev, dt, (T, K), "x", x), _ptr_of(dev, dt, (E, N, K), "w", w, flat), _ptr_of(dev, _I32, (E + 1,), "offsets", offsets),
-        _ptr_of(dev, dt, (T, N), "z", z), _ptr_of(dev, dt, (T, wide), "dout", dout), _ptr_of(dev, dt, (T, K), "dx", dx),
-        _ptr_of(dev, dt, (E, N, K), "dw", dw, flat), _ptr_of(dev, dt, (E, N), "dbias", dbias, line), *_workspace(dev, workspace),
+        ctypes.byref(dims), _ptr_of(dev, dt, rows, "x", x), _ptr_of(dev, dt, mat, "w", w, mat1), _ptr_of(dev, _I32, ends, "offsets", offsets),
+        _ptr_of(dev, dt, pre, "z", z), _ptr_of(dev, dt, wide, "dout", dout), _ptr_of(dev, dt, rows, "dx", dx),
+        _ptr_of(dev, dt, mat, "dw", dw, mat1), _ptr_of(dev, dt, vec, "dbias", dbias, vec1), *_workspace(dev, workspace),
         _stream_of(stream, dev)), "moe_linear_backward")
 
 
@@ -710,20 +736,11 @@ def new_norm_workspace(dims: NormDims, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _norm(d: NormDims, t):
-    """Device, type, shapes [T, H] and [H], and the gate's shape."""
-    T, H, gate = d.T, d.H, d.gate
-    dt = _TORCH.get(d.dtype)
-    if dt is None:
-        raise MoEError(1, "moe_norm_dims")
-    return (torch.cuda.current_device() if t.is_cuda else -2, dt, (T, H), (H,),
-            (T,) if gate == GATE_TOKEN else (H,) if gate == GATE_CHANNEL else (T, H) if gate == GATE_FULL else ())
-
-
 def moe_norm_residual(dims: NormDims, y, residual, gate, gamma_post, gamma_pre, s, xn, stream=None):
     """s = residual_scale * residual + branch_scale * act(gate) * N(y; gamma_post), xn = N(s; gamma_pre); residual, the
     gammas and either result may be None, and N(y) is y for dims without post."""
-    dev, dt, rows, cols, gs = _norm(dims, y)
+    dev = _current(y)
+    dt, rows, cols, gs = dims.checked
     _check(load_library().moe_norm_residual(
         ctypes.byref(dims), _ptr_of(dev, dt, rows, "y", y), _ptr_of(dev, dt, rows, "residual", residual), _ptr_of(dev, dt, gs, "gate", gate),
         _ptr_of(dev, dt, cols, "gamma_post", gamma_post), _ptr_of(dev, dt, cols, "gamma_pre", gamma_pre), _ptr_of(dev, dt, rows, "s", s),
@@ -733,7 +750,8 @@ def moe_norm_residual(dims: NormDims, y, residual, gate, gamma_post, gamma_pre, 
 def moe_norm_residual_backward(dims: NormDims, ds, dxn, s, y, gate, gamma_post, gamma_pre, dresidual, dy, dgate, dgamma_post, dgamma_pre, workspace,
                                stream=None):
     """Gradients of moe_norm_residual's inputs (each may be None) for the gradients ds and dxn of its results (either may be None)."""
-    dev, dt, rows, cols, gs = _norm(dims, y)
+    dev = _current(y)
+    dt, rows, cols, gs = dims.checked
     _check(load_library().moe_norm_residual_backward(
         ctypes.byref(dims), _ptr_of(dev, dt, rows, "ds", ds), _ptr_of(dev, dt, rows, "dxn", dxn), _ptr_of(dev, dt, rows, "s", s),
         _ptr_of(dev, dt, rows, "y", y), _ptr_of(dev, dt, gs, "gate", gate), _ptr_of(dev, dt, cols, "gamma_post", gamma_post),

@@ -69,28 +69,6 @@ __device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
 // good to a few 2^-22 relative at the arguments that matter, far below half a step of bf16 (2^-9 and up) or fp16 (2^-12).
 __device__ __forceinline__ float lin_sigmoid(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
 
-// Two fp32 operations in one instruction.
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float x, float y) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void f2_split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
-__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 f2_both(float x) { return f2(x, x); }
-
 // Phi(z), the normal distribution function, and e = exp(-z^2 / 2), of two values. Phi(-|z|) = e * R(t), t = 1 / (1 + 0.3 |z|): the scaled
 // tail exp(z^2 / 2) * Phi(-|z|) falls smoothly from 1/2 like 1 / |z|, so it is close to a polynomial in t. R is of degree 8,
 // fitted here by reweighted least squares at Chebyshev nodes for the least relative error up to |z| = 14: 6e-8, evaluated in fp32

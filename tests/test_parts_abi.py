@@ -185,3 +185,20 @@ def test_binding_refuses():
             size(moe.LinearDims(4, 33, 64, act=moe.ACT_SWIGLU), device="cpu")
     with pytest.raises(moe.MoEError):
         moe.new_norm_workspace(moe.NormDims(4, 9000), device="cpu")
+
+
+def test_dims_may_be_changed():
+    """What the checks work out of the dims once is worked out again when a field is set."""
+    d = moe.LinearDims(4, 32, 64)
+    assert d.checked[1] == (4, 64) and d.checked[2] == (4, 32)
+    d.T, d.act = 6, moe.ACT_SWIGLU
+    assert d.checked[1] == (6, 64) and d.checked[2] == (6, 16)
+    n = moe.NormDims(4, 64, gate=moe.GATE_TOKEN)
+    assert n.checked[3] == (4,)
+    n.gate = moe.GATE_FULL
+    assert n.checked[3] == (4, 64)
+    with pytest.raises(AttributeError):
+        d.nothing
+    d.dtype = 9
+    with pytest.raises(moe.MoEError):
+        d.checked
