@@ -411,22 +411,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // each, 16 rows at a time. Sums are of dz before its rounding, row block by row block: those of the rows of
 // expert e in chunk c go to part[c + e], a place of their own as chunks and experts follow one another.
 
-// Eight columns of a row, of which n exist.
-template <typename T, int VE>
-__device__ __forceinline__ Raw ld_cols(const T* p, int n) {
-    Raw r;
-    if (VE == 8) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p);
-        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
-    } else {
-        r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) r.w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-    }
-    return r;
-}
-
 template <typename T>
 __device__ __forceinline__ void st_cols(T* p, const Raw& r) { *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]); }
 
@@ -450,9 +434,9 @@ __global__ void __launch_bounds__(256, 3) k_dz(const LinearArgs a, int pitch) {
     for (int k = 0; k < kMore; ++k) {
         const int r = r0 + ty + 16 * k;
         if (r < r1 && n > 0) {
-            dv[k] = ld_cols<T, VE>(dout + (int64_t)r * wide + f, n);
-            if (need_z) zv[k] = ld_cols<T, VE>(z + (int64_t)r * N + f, n);
-            if (GATED) uv[k] = ld_cols<T, VE>(z + (int64_t)r * N + wide + f, n);
+            dv[k] = ld_cols<T, VE>(dout, (int64_t)r * wide + f, (int64_t)a.d.T * wide, n);
+            if (need_z) zv[k] = ld_cols<T, VE>(z, (int64_t)r * N + f, (int64_t)a.d.T * N, n);
+            if (GATED) uv[k] = ld_cols<T, VE>(z, (int64_t)r * N + wide + f, (int64_t)a.d.T * N, n);
         }
     }
     // whose rows they are matters to the column sums alone (rows behind the last expert's are read into nothing)
@@ -599,28 +583,31 @@ int resident_clusters(int split, int num_sms) {
     return n;
 }
 
-// Which kernel, and its tiles. groups: experts with rows, about; cols: columns of one of them, about; F: features
-// (lanes) in weight rows; blocks: 64-deep steps of the contraction, about.
+// Which kernel, and its tiles. groups: experts with rows, about; cols: columns of one of them, about (ragged: they are
+// experts' rows); F: features (lanes) in weight rows; blocks: 64-deep steps of the contraction, about.
 // Time of a 16-deep step, in clocks: on a pair, 256 features by w columns take w / 2 on the tensor cores and
 // (8 KB + 32 w B) / 128 B through each SM's shared memory (TMA's writes and the tensor core's reads of
 // its half), which measured times follow as 64 + w / 4; one SM's 128 x 64 take 96. A wave of tiles costs its widest. With
 // 64 columns or fewer the weights' way from HBM is what counts: one SM a tile, and clusters that split the contraction as long as all of them are
 // resident at once (2048 x 2048, 16 tokens: clusters of 4 take 9.2 us, of 8 in two turns 15.0, one CTA a tile 12.9).
 template <typename T, int MODE, bool GATED>
-LinPlan lin_plan(int64_t groups, int64_t cols, int64_t F, int blocks, int num_sms) {
+LinPlan lin_plan(int64_t groups, int64_t cols, bool ragged, int64_t F, int blocks, int num_sms) {
     LinPlan p = {false, kLinCols, 0, 1, 0};
     const int64_t f1 = (F + 127) / 128, f2 = (F + 255) / 256;
     const int64_t tiles = groups * f1 * ((cols + kLinCols - 1) / kLinCols);
     while (p.split < 8 && p.split * 2 <= blocks && tiles <= resident_clusters<T, MODE, GATED>(p.split * 2, num_sms)) p.split *= 2;
-    p.grid = (int)(tiles * p.split < num_sms ? tiles * p.split : num_sms) / p.split * p.split;
+    // (experts' tiles are more or fewer than thought: CTAs for all that can be)
+    p.grid = (int)(!ragged && tiles * p.split < num_sms ? tiles * p.split : num_sms) / p.split * p.split;
     if (cols <= kLinCols || num_sms < 2) return p;
     int64_t best = (tiles * p.split + num_sms - 1) / num_sms * 96 / p.split;
     for (int w = 256; w >= 64; w /= 2) {
-        const int64_t n = (cols + w - 1) / w, width = ((cols + n - 1) / n + 31) / 32 * 32, all = groups * f2 * n;
+        // tiles of a group's columns, twice: of experts' rows half a tile more than they fill, on average
+        const int64_t n2 = ragged ? (2 * cols > w ? 2 * cols / w + 1 : 2) : 2 * ((cols + w - 1) / w);
+        const int64_t width = ((2 * cols + n2 - 1) / n2 + 31) / 32 * 32, all = (groups * f2 * n2 + 1) / 2;
         const int64_t cost = (all + num_sms / 2 - 1) / (num_sms / 2) * (64 + width / 4);
         if (cost < best) {
             best = cost;
-            p = {true, w, 2 * (int)(all < num_sms / 2 ? all : num_sms / 2), 1, (int)width};
+            p = {true, w, 2 * (int)(!ragged && all < num_sms / 2 ? all : num_sms / 2), 1, (int)width};
         }
     }
     return p;
@@ -703,7 +690,8 @@ cudaError_t linear_t(const LinearArgs& a, cudaStream_t s) {
     }
     const int64_t g = groups_of(a), rows = (a.d.T + g - 1) / g;
     const int blocks = (v.C + 63) / 64;
-    const LinPlan p = gated ? lin_plan<T, kFwd, true>(g, rows, a.d.N, blocks, a.num_sms) : lin_plan<T, kFwd, false>(g, rows, a.d.N, blocks, a.num_sms);
+    const bool ragged = a.offsets != nullptr;
+    const LinPlan p = gated ? lin_plan<T, kFwd, true>(g, rows, ragged, a.d.N, blocks, a.num_sms) : lin_plan<T, kFwd, false>(g, rows, ragged, a.d.N, blocks, a.num_sms);
     v.boxes = pair_boxes(p, !a.offsets);
     CUtensorMap A, B;
     if (!(gated ? map_w_gated(&A, a.d, a.w) : map_w(&A, a.d, a.w, 128)) || !map_2d(&B, a.d.dtype, a.x, a.d.T, a.d.K, a.d.K, v.boxes))
@@ -746,7 +734,7 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
     if (a.dx) {
         v.out = a.dx;
         v.C = d.N;
-        const LinPlan p = lin_plan<T, kDx, false>(g, (d.T + g - 1) / g, d.K, (v.C + 63) / 64, a.num_sms);
+        const LinPlan p = lin_plan<T, kDx, false>(g, (d.T + g - 1) / g, a.offsets != nullptr, d.K, (v.C + 63) / 64, a.num_sms);
         v.boxes = pair_boxes(p, !a.offsets);
         if (!map_w(&A, d, a.w, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, v.boxes)) return cudaErrorInvalidValue;
         MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_plan<T, kDx, false>(d.dtype, p, A, B, A, v, s)));
@@ -757,7 +745,7 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
         if (!map_2d(&A, d.dtype, a.x, d.T, d.K, d.K, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, 64)) return cudaErrorInvalidValue;
         v.out = a.dw;
         v.C = 0;
-        const LinPlan p = lin_plan<T, kDw, false>(d.E, d.N, d.K, (int)(((d.T + g - 1) / g + 63) / 64), a.num_sms);
+        const LinPlan p = lin_plan<T, kDw, false>(d.E, d.N, false, d.K, (int)(((d.T + g - 1) / g + 63) / 64), a.num_sms);
         CUtensorMap C = A;
         if (p.pair) {
             const uint64_t dim[3] = {(uint64_t)d.K, (uint64_t)d.N, (uint64_t)d.E}, st[2] = {(uint64_t)d.K * 2, (uint64_t)d.N * d.K * 2};

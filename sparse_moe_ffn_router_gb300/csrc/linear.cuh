@@ -222,6 +222,40 @@ struct LinWalk {
 constexpr int kFewRows = 64;
 cudaError_t launch_few(int32_t dtype, bool gated, const void* x, const void* w, const LinView& v, int num_sms, cudaStream_t s);
 
+// Eight columns from element `at` of a tensor of `total` elements, of which n belong to the row. Where rows do not
+// start on 16 bytes (VE = 1) they come as the two aligned vectors around them and are shifted into place.
+template <typename T, int VE>
+__device__ __forceinline__ Raw ld_cols(const T* p, int64_t at, int64_t total, int n) {
+    Raw r;
+    if (VE == 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p + at);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+        return r;
+    }
+    const int64_t lo = at & ~(int64_t)7;
+    const int m = (int)(at - lo);
+    if (lo + 16 <= total) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p + lo), y = *reinterpret_cast<const uint4*>(p + lo + 8);
+        uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        if (m & 4) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (m & 2) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = __funnelshift_r(w[i], w[i + 1], 16 * (m & 1));
+    } else {
+        r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) r.w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[at + i] << (16 * (i & 1));
+    }
+    return r;
+}
+
 // db[e, n] of the chunks' column sums, a warp to 32 columns of an expert: the chunks of its rows in order. For `warps`
 // warps, of which this is number `w`: the products' kernels have two warps to spare in every CTA.
 template <typename T>

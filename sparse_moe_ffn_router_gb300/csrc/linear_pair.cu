@@ -35,33 +35,21 @@ __device__ __forceinline__ float2 unpack2(uint32_t u, fp16) { return __half22flo
 __device__ __forceinline__ uint32_t at64(int row, int chunk) { return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4)); }
 __device__ __forceinline__ uint32_t at32(int row, int chunk) { return (uint32_t)(row * 32 + ((chunk ^ ((row >> 2) & 1)) << 4)); }
 
-// Eight features (16 bytes) to p, of which `left` exist.
-template <typename T>
-__device__ __forceinline__ void put8(T* p, const uint4& v, int left, bool vec) {
-    if (vec) {
-        if (left > 0) *reinterpret_cast<uint4*>(p) = v;
-        return;
+// Rows that do not start on 16 bytes: a warp's buffer of 32 rows of kWide features to memory, a row (two of
+// 16 features) at a time, lanes side by side. row0, ld: of the first row, between rows; f0: its first feature, of F; rows: how many exist.
+template <int kWide>
+__device__ __forceinline__ uint32_t feature_at(int row, int f) { return (kWide == 16 ? at32(row, f >> 3) : at64(row, f >> 3)) + 2 * (f & 7); }
+template <int kWide>
+__device__ __forceinline__ void rows_out(uint32_t buf, uint16_t* p, int64_t ld, int f0, int F, int rows) {
+    const int lane = threadIdx.x & 31, f = lane & (kWide - 1);
+    constexpr int kAtOnce = 32 / kWide;
+#pragma unroll 4
+    for (int r = lane / kWide; r < rows; r += kAtOnce) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(buf + feature_at<kWide>(r, f)) : "memory");
+        if (f0 + f < F) p[(int64_t)r * ld + f] = v;
     }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < left) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
 }
-template <typename T>
-__device__ __forceinline__ uint4 get8(const T* p, int left, bool vec) {
-    uint4 v = {0u, 0u, 0u, 0u};
-    if (vec) {
-        if (left > 0) v = *reinterpret_cast<const uint4*>(p);
-        return v;
-    }
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < left) w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-    v.x = w[0]; v.y = w[1]; v.z = w[2]; v.w = w[3];
-    return v;
-}
-
 // A warp's part of a tile: 32 accumulator lanes (q), 32 columns at a time. row0: the result's row of the tile's
 // first column; fl: the CTA's first feature.
 template <typename T, int MODE, bool GATED>
@@ -85,7 +73,7 @@ __device__ __forceinline__ void pair_epilogue(const LinView& a, uint32_t tmem, u
     const int left = a.F - f0 - cch * 8;                                                // features from its chunk on
     constexpr int kRows = GATED ? 16 : 8, kRounds = 32 / kRows;
     T* out = reinterpret_cast<T*>(a.out) + (row0 + crow) * a.F + f0 + cch * 8;
-    const T* res = kFull && a.residual ? reinterpret_cast<const T*>(a.residual) + (row0 + crow) * a.F + f0 + cch * 8 : nullptr;
+    const T* res = kFull ? reinterpret_cast<const T*>(a.residual) : nullptr;
     T* z = nullptr;
     int zleft = 0;
     if (kFull && a.z) {  // rows of z hold 32 features of the warp: gated, 16 gate and the 16 up of the same features
@@ -95,11 +83,14 @@ __device__ __forceinline__ void pair_epilogue(const LinView& a, uint32_t tmem, u
     }
     for (int c = h * 32; c < cols; c += 64) {
         uint32_t r[32];  // 16 features (lanes) from 0 in r[0 .. 15], from 16 in r[16 .. 31]; each: column block b in [4 b ..]
-        uint4 rv[kRounds];
+        Raw rv[kRounds];
         if (kFull && res) {
 #pragma unroll
             for (int i = 0; i < kRounds; ++i)
-                if (c + crow + i * kRows < cols) rv[i] = get8(res + (int64_t)(c + i * kRows) * a.F, left, vec);
+                if (c + crow + i * kRows < cols && left > 0) {
+                    const int64_t at = (row0 + c + crow + i * kRows) * a.F + f0 + cch * 8;
+                    rv[i] = vec ? ld_cols<T, 8>(res, at, 0, 8) : ld_cols<T, 1>(res, at, (int64_t)a.T * a.F, left);
+                }
         }
         if (any) {
             tmem_ld_frag4(tmem + c, r);
@@ -129,20 +120,22 @@ __device__ __forceinline__ void pair_epilogue(const LinView& a, uint32_t tmem, u
                 stmatrix4_trans(buf + at64(8 * b + (lane & 7), lane >> 3), p[0], p[1], p[2], p[3]);
             }
             __syncwarp();
+            if (vec) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = (lane >> 2) + 8 * i;
-                const uint4 v = lds128_smem(buf + at64(row, lane & 3));
-                if (c + row < cols) put8(z + (int64_t)(c + 8 * i) * a.N, v, zleft, vec);
+                for (int i = 0; i < 4; ++i) {
+                    const int row = (lane >> 2) + 8 * i;
+                    const uint4 v = lds128_smem(buf + at64(row, lane & 3));
+                    if (c + row < cols && zleft > 0) *reinterpret_cast<uint4*>(z + (int64_t)(c + 8 * i) * a.N) = v;
+                }
+            } else {  // (not gated: its rows are a multiple of 16 bytes)
+                rows_out<32>(buf, reinterpret_cast<uint16_t*>(a.z) + (row0 + c) * a.N + f0, a.N, f0, a.F, min(32, cols - c));
             }
             __syncwarp();
         }
         if (kFull && res) {
 #pragma unroll
-            for (int i = 0; i < kRounds; ++i) {
-                const uint32_t w[4] = {rv[i].x, rv[i].y, rv[i].z, rv[i].w};
-                if (c + crow + i * kRows < cols) sts128(buf + (GATED ? at32(crow + i * kRows, cch) : at64(crow + i * kRows, cch)), w);
-            }
+            for (int i = 0; i < kRounds; ++i)
+                if (c + crow + i * kRows < cols) sts128(buf + (GATED ? at32(crow + i * kRows, cch) : at64(crow + i * kRows, cch)), rv[i].w);
             __syncwarp();
         }
         // activation, residual, rounding: pairs of columns of a feature
@@ -178,11 +171,15 @@ __device__ __forceinline__ void pair_epilogue(const LinView& a, uint32_t tmem, u
             stmatrix4_trans(buf + at, p[k * 4], p[k * 4 + 1], p[k * 4 + 2], p[k * 4 + 3]);
         }
         __syncwarp();
+        if (vec) {
 #pragma unroll
-        for (int i = 0; i < kRounds; ++i) {
-            const int row = crow + i * kRows;
-            const uint4 v = lds128_smem(buf + (GATED ? at32(row, cch) : at64(row, cch)));
-            if (c + row < cols) put8(out + (int64_t)(c + i * kRows) * a.F, v, left, vec);
+            for (int i = 0; i < kRounds; ++i) {
+                const int row = crow + i * kRows;
+                const uint4 v = lds128_smem(buf + (GATED ? at32(row, cch) : at64(row, cch)));
+                if (c + row < cols && left > 0) *reinterpret_cast<uint4*>(out + (int64_t)(c + i * kRows) * a.F) = v;
+            }
+        } else {
+            rows_out<kWide>(buf, reinterpret_cast<uint16_t*>(a.out) + (row0 + c) * a.F + f0, a.F, f0, a.F, min(32, cols - c));
         }
         __syncwarp();
     }
