@@ -89,7 +89,7 @@ typedef enum {
     MOE_ERR_WORKSPACE_TOO_SMALL = 4, /* ws_bytes < moe_workspace_size(d)                    */
     MOE_ERR_CUDA = 5,                /* a CUDA launch or runtime call failed                */
     MOE_ERR_TIMEOUT = 6,             /* a bounded device-side wait gave up                  */
-    MOE_ERR_DEVICE = 7               /* a kernel flagged bad data (e.g. a non-finite score) */
+    MOE_ERR_DEVICE = 7               /* a kernel flagged bad data (a non-finite score, expert offsets out of order) */
 } moe_status;
 
 /* Bytes of device workspace that moe_route / moe_forward / moe_forward_w4 need for dims d (0 if
@@ -275,7 +275,7 @@ typedef enum {
  *   counts [E], offsets [E+1]  pairs of each expert and their exclusive prefix sum
  *   perm [T*K]                 pairs in order of (expert, t, k); -1 from offsets[E] on
  *   inv [T*K]                  place of pair p in perm; -1 for a dropped slot
- * For ids of moe_route, counts, offsets and perm are moe_route's. 1 <= K <= 8, 1 <= E <= 256, T * K < 2^31;
+ * For ids of moe_route, counts, offsets and perm are moe_route's. 1 <= K <= 8, 1 <= E <= 256, T * K <= 2^31 - 2^16;
  * T = 0 gives zeros. A token may name an expert twice. Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE,
  * MOE_ERR_MISALIGNED. */
 moe_status moe_sort_pairs(int32_t T, int32_t K, int32_t E, const int32_t* ids, int32_t* counts, int32_t* offsets,
@@ -291,7 +291,7 @@ moe_status moe_sort_pairs(int32_t T, int32_t K, int32_t E, const int32_t* ids, i
  * alone (NULL without it). Dropped slots give and receive nothing: their dtopk_w is 0, and rows that no pair has as
  * its place are left as they were. Sums are in fp32 in slot order, dots in fp32, each result rounded once.
  * out may be the same buffer as residual; otherwise results overlap no input. An entry of inv that is no place
- * in [0, T*K) counts as dropped. dtype: bf16, fp16 or fp32; 1 <= K <= 8, 1 <= H <= 65536, T * K < 2^31;
+ * in [0, T*K) counts as dropped. dtype: bf16, fp16 or fp32; 1 <= K <= 8, 1 <= H <= 65536, T * K <= 2^31 - 2^16;
  * rows move fastest where H elements are a multiple of 16 bytes. T = 0 is a no-op. */
 moe_status moe_dispatch(int32_t dtype, int32_t T, int32_t K, int32_t H, const void* x, const int32_t* inv,
                         const float* topk_w, void* rows, void* stream);
@@ -316,7 +316,7 @@ moe_status moe_combine_backward(int32_t dtype, int32_t T, int32_t K, int32_t H, 
  * in out, z and dx.
  * dtype: bf16 or fp16, all tensors. Products accumulate in fp32, bias, activation and residual are applied in fp32,
  * results are rounded once; dz is rounded to dtype before the products of the backward pass (dbias sums it before).
- * Bounds: 1 <= N <= 2^20, 8 <= K <= 2^20 with K % 8 == 0, N % 32 == 0 for SWIGLU, 1 <= E <= 256, 0 <= T <= 2^31 - 256,
+ * Bounds: 1 <= N <= 2^20, 8 <= K <= 2^20 with K % 8 == 0, N % 32 == 0 for SWIGLU, 1 <= E <= 256, 0 <= T <= 2^31 - 2^16,
  * T*N, T*K, E*N*K < 2^40. bias and dbias are 2-byte aligned. out may be the same buffer as residual; otherwise results
  * overlap nothing. The workspace (moe_linear_workspace_size bytes; backward: nonzero for moe_linear_backward) is
  * zero-filled once (moe_workspace_init); calls that may overlap in time need one each. Offsets that
@@ -344,7 +344,8 @@ moe_status moe_linear_backward(const moe_linear_dims* d, const void* x, const vo
  * Backward: ds and dxn are the gradients of s and xn (either may be NULL: none), s and y the forward pass's (s is read
  * for dxn alone). Results, each optional: dresidual, dy [T, H], dgate (as gate), dgamma_post, dgamma_pre [H].
  * dgamma_pre needs dxn, dgamma_post MOE_NORM_POST, dgate a gate.
- * dtype: bf16, fp16 or fp32, all tensors; arithmetic and sums in fp32, one rounding a result. 1 <= H <= 8192, T >= 0.
+ * dtype: bf16, fp16 or fp32, all tensors; arithmetic and sums in fp32, one rounding a result. 1 <= H <= 8192,
+ * 0 <= T <= 2^31 - 2^16.
  * s and xn may be the buffers of y or residual (and dresidual and dy those of ds, dxn, s or y), each as a whole; results
  * overlap nothing else. The backward workspace (moe_norm_workspace_size bytes) need not be zero-filled; calls
  * that may overlap in time need one each. T = 0 is a no-op, or writes zeros to the [H] gradients. */
@@ -367,7 +368,7 @@ moe_status moe_norm_residual_backward(const moe_norm_dims* d, const void* ds, co
                                       void* workspace, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then read and clear the device error word kept in `workspace`:
- * MOE_OK, MOE_ERR_DEVICE (a kernel saw a non-finite router score) or MOE_ERR_TIMEOUT. */
+ * MOE_OK, MOE_ERR_DEVICE (a kernel saw a non-finite router score, or expert offsets out of order) or MOE_ERR_TIMEOUT. */
 moe_status moe_last_device_error(void* workspace, void* stream);
 
 /* Where an intermediate lives in the workspace after moe_forward (for inspection):

@@ -633,7 +633,7 @@ extern "C" const char* moe_status_string(moe_status s) {
         case MOE_ERR_WORKSPACE_TOO_SMALL: return "MOE_ERR_WORKSPACE_TOO_SMALL: workspace smaller than moe_workspace_size()";
         case MOE_ERR_CUDA: return "MOE_ERR_CUDA: a CUDA launch or runtime call failed";
         case MOE_ERR_TIMEOUT: return "MOE_ERR_TIMEOUT: a bounded device-side wait gave up";
-        case MOE_ERR_DEVICE: return "MOE_ERR_DEVICE: a kernel flagged a non-finite router score";
+        case MOE_ERR_DEVICE: return "MOE_ERR_DEVICE: a kernel flagged bad data (a non-finite router score, expert offsets out of order)";
         default: return "unknown moe_status";
     }
 }

@@ -8,6 +8,8 @@ using namespace moe;
 
 namespace {
 
+constexpr int32_t kMaxRows = 0x7fff0000;  // 2^31 - 2^16
+
 bool misaligned(const void* p) { return ((uintptr_t)p & 15u) != 0; }
 
 moe_status to_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -60,7 +62,7 @@ struct ExchangeCall {
 moe_status exchange(const ExchangeCall& c, void* stream) {
     const int b = elem_size(c.dtype);
     if (!b || c.T < 0) return MOE_ERR_INVALID_ARG;
-    if (c.K < 1 || c.K > 8 || c.H < 1 || c.H > 65536 || (int64_t)c.T * c.K >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (c.K < 1 || c.K > 8 || c.H < 1 || c.H > 65536 || (int64_t)c.T * c.K > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (c.T == 0) return MOE_OK;
     if ((c.needs_tok && !c.tok) || (c.needs_rows && !c.rows) || !c.inv || !c.out) return MOE_ERR_INVALID_ARG;
     if (any_misaligned({c.tok, c.rows, c.inv, c.w, c.out, c.dots})) return MOE_ERR_MISALIGNED;
@@ -87,7 +89,7 @@ bool linear_known(const moe_linear_dims* d) {
 }
 bool linear_shape(const moe_linear_dims& d) {
     const int64_t most = (int64_t)1 << 40;
-    return d.T <= 0x7fffff00 && d.N >= 1 && d.N <= 1 << 20 && d.K >= 8 && d.K <= 1 << 20 && d.K % 8 == 0 && d.E >= 1 && d.E <= 256 &&
+    return d.T <= kMaxRows && d.N >= 1 && d.N <= 1 << 20 && d.K >= 8 && d.K <= 1 << 20 && d.K % 8 == 0 && d.E >= 1 && d.E <= 256 &&
            !(d.act == MOE_ACT_SWIGLU && d.N % 32) && (int64_t)d.T * d.N < most && (int64_t)d.T * d.K < most && (int64_t)d.N * d.K < most / d.E;
 }
 size_t dz_bytes(const moe_linear_dims& d) { return align256((size_t)d.T * ((d.N + 7) / 8 * 8) * 2); }
@@ -98,7 +100,7 @@ size_t part_bytes(const moe_linear_dims& d) { return align256(((size_t)(d.T + kD
 extern "C" moe_status moe_sort_pairs(int32_t T, int32_t K, int32_t E, const int32_t* ids, int32_t* counts, int32_t* offsets,
                                      int32_t* perm, int32_t* inv, void* stream) {
     if (T < 0) return MOE_ERR_INVALID_ARG;
-    if (K < 1 || K > 8 || E < 1 || E > 256 || (int64_t)T * K >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (K < 1 || K > 8 || E < 1 || E > 256 || (int64_t)T * K > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (!counts || !offsets || (T && (!ids || !perm || !inv))) return MOE_ERR_INVALID_ARG;
     if (any_misaligned({ids, counts, offsets, perm, inv})) return MOE_ERR_MISALIGNED;
     const size_t pairs = (size_t)T * K * 4;
@@ -196,7 +198,8 @@ bool norm_known(const moe_norm_dims* d) {
            (d->gate_act == MOE_ACT_NONE || ((d->gate_act == MOE_ACT_SIGMOID || d->gate_act == MOE_ACT_SILU) && d->gate != MOE_GATE_NONE)) &&
            !(d->flags & ~MOE_NORM_POST) && d->T >= 0 && d->eps >= 0.f && d->eps < 3.4e38f;
 }
-bool norm_shape(const moe_norm_dims& d) { return d.H >= 1 && d.H <= 8192; }
+// (T + a step of the kernels' rows stays within 32 bits)
+bool norm_shape(const moe_norm_dims& d) { return d.H >= 1 && d.H <= 8192 && d.T <= kMaxRows; }
 size_t gate_bytes(const moe_norm_dims& d) {
     const size_t b = elem_size(d.dtype);
     return d.gate == MOE_GATE_TOKEN ? d.T * b : d.gate == MOE_GATE_CHANNEL ? d.H * b : d.gate == MOE_GATE_FULL ? (size_t)d.T * d.H * b : 0;

@@ -168,3 +168,34 @@ def test_tensors_of_another_kind_are_refused():
         moe.moe_linear(d, x, w.cpu(), None, None, None, out, None, ws)
     with pytest.raises(moe.MoEError):
         moe.moe_linear(d, x, w, None, None, None, x, None, ws)
+
+
+FIRST = """
+import torch, sparse_moe_ffn_router_gb300 as moe
+from tests.test_gpu_parts_block import Block
+moe.load_library()
+b = Block(130)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    b.forward()
+    b.backward()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in b.results()]
+b.forward()
+b.backward()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(got, b.results()))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]

@@ -221,3 +221,68 @@ def test_a_held_back_load_ends_in_an_error():
             moe.moe_test_set_wait()
         moe.moe_linear(d, x, w, b, None, r, again, None, ws)
         assert moe.moe_last_device_error(ws) == 0 and torch.equal(again, out)
+
+
+def test_offsets_out_of_order_are_flagged_for_few_rows():
+    d = moe.LinearDims(6, 64, 64, E=3)
+    x, w, b, _ = inputs(d, residual=False)
+    ws, out = moe.new_linear_workspace(d), torch.zeros(6, 64, dtype=x.dtype, device="cuda")
+    for off in ([0, 4, 2, 6], [0, 1, 2, 7], [-1, 1, 2, 6], [2 ** 31 - 1, -2 ** 31, 5, 6], [0, 6, 0, 6]):
+        moe.moe_linear(d, x, w, b, torch.tensor(off, dtype=torch.int32, device="cuda"), None, out, None, ws)
+        assert moe.moe_last_device_error(ws) == 7 and moe.moe_last_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("T", [1, 2, 8, 9, 40, 64, 65])
+def test_residual_may_be_the_result_of_every_kernel(T):
+    for act, N in ((moe.ACT_NONE, 2048), (moe.ACT_SWIGLU, 1024)):
+        d = moe.LinearDims(T, N, 2048, act=act)
+        x, w, b, r = inputs(d)
+        out, _ = forward(d, x, w, b, None, r)
+        moe.moe_linear(d, x, w, b, None, r, r, None, moe.new_linear_workspace(d))
+        assert torch.equal(r, out)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("T,N,K,E", [(2, 2048, 512, 0), (3, 1003, 1024, 0), (4, 96, 2048, 0), (8, 130, 4104, 0), (5, 64, 64, 40), (64, 224, 520, 32), (64, 32, 1032, 256), (17, 77, 8, 9)])
+def test_few_rows(dtype, T, N, K, E):
+    """One to four features a warp, rows in batches of four and eight, rows of experts one at a time; with every part of the epilogue."""
+    for act in (moe.ACT_GELU, moe.ACT_SWIGLU):
+        n = N // 32 * 32 if act == moe.ACT_SWIGLU else N
+        d = moe.LinearDims(T, n, K, E=max(E, 1), act=act, dtype=dtype)
+        off = None
+        if E:
+            g = torch.Generator().manual_seed(T)
+            off = offsets_of(torch.bincount(torch.randint(0, E, (T,), generator=g), minlength=E).tolist())
+        x, w, b, r = inputs(d)
+        check_forward(d, x, w, b, off, r)
+
+
+@pytest.mark.parametrize("T,N,K", [(300, 1001, 64), (513, 259, 72), (700, 1004, 136)])
+def test_rows_that_do_not_start_on_16_bytes(T, N, K):
+    """The whole epilogue and the way back where a row of the result begins anywhere: nothing beside the rows is touched."""
+    for act in (moe.ACT_NONE, moe.ACT_SILU):
+        d = moe.LinearDims(T, N, K, act=act)
+        x, w, b, r = inputs(d)
+        room = torch.full((T * N + 64,), 7.0, dtype=x.dtype, device="cuda")
+        out = room[:T * N].view(T, N)
+        moe.moe_linear(d, x, w, b, None, r, out, None, moe.new_linear_workspace(d))
+        o64, _, mo, _ = ref.linear(d, x, w, b, None, r)
+        ref.check(out, o64, mo, K + 2, "out")
+        assert bool((room[T * N:] == 7).all())
+        check_backward(d, x, w, None, check_forward(d, x, w, b, None, r))
+
+
+@pytest.mark.parametrize("keep", [(True, False, False), (False, True, False), (False, False, True), (False, True, True)])
+def test_bias_gradient_beside_any_product(keep):
+    """The bias' sums are added up by whichever kernel runs, or one of its own."""
+    for counts in ([500, 0, 33, 1], [130] * 7):
+        off = offsets_of(counts)
+        d = moe.LinearDims(int(off[-1]) + 5, 264, 136, E=len(counts), act=moe.ACT_SILU)
+        x, w, b, _ = inputs(d)
+        _, z = forward(d, x, w, b, off, None)
+        dout, ws = ref.randn(5, x.dtype, d.T, d.N), moe.new_linear_workspace(d, backward=True)
+        full = [torch.zeros_like(x), torch.zeros_like(w), torch.zeros_like(b)]
+        moe.moe_linear_backward(d, x, w, off, z, dout, *full, ws)
+        some = [torch.zeros_like(t) if k else None for t, k in zip(full, keep)]
+        moe.moe_linear_backward(d, x, w, off, z, dout, *some, ws)
+        assert all(s is None or torch.equal(s, t) for s, t in zip(some, full))

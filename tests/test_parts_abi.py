@@ -37,7 +37,7 @@ def test_sort_refuses(lib):
         assert call(K=k) == 2
     for e in (0, 257, -3):
         assert call(E=e) == 2
-    assert call(T=2 ** 30, K=2) == 2 and call(T=2 ** 28, K=8) == 2
+    assert call(T=2 ** 30, K=2) == 2 and call(T=2 ** 28, K=8) == 2 and call(T=2 ** 31 - 2 ** 16 + 1, K=1) == 2
     for name in ("ids", "counts", "offsets", "perm", "inv"):
         assert call(**{name: None}) == 1
         assert call(**{name: at(9) + 4}) == 3
@@ -83,7 +83,7 @@ def test_linear_sizes(lib):
               LinearDims(2 ** 31 - 1, 64, 64), LinearDims(2 ** 30, 1024, 64), LinearDims(2 ** 30, 64, 1024), LinearDims(4, 2 ** 20, 2 ** 20)):
         assert size(d, 0) == 0 and size(d, 1) == 0
     assert lib.moe_linear_workspace_size(None, 0) == 0
-    most = 2 ** 31 - 256
+    most = 2 ** 31 - 2 ** 16
     assert size(LinearDims(most, 256, 256), 0) > 0 and size(LinearDims(most + 1, 256, 256), 0) == 0
 
 
@@ -151,6 +151,7 @@ def test_norm_refuses(lib):
     for name in ("ds", "dxn", "s", "y", "gp", "gq", "dres", "dy", "dgp", "dgq", "ws"):
         assert backward(**{name: at(13) + 4}) == 3
     assert backward(dres=at(8)) == 1 and backward(dy=at(3) + 64) == 1 and backward(dgp=at(5)) == 1 and backward(ws=at(1)) == 1
+    assert forward(d=NormDims(2 ** 31 - 2 ** 16 + 1, 1)) == 2 and lib.moe_norm_workspace_size(R(NormDims(2 ** 31 - 1, 1))) == 0
     assert lib.moe_norm_workspace_size(R(NormDims(10 ** 6, 2048))) == lib.moe_norm_workspace_size(R(NormDims(304, 2048))) > 0
 
 
