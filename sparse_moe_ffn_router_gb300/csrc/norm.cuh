@@ -503,6 +503,7 @@ static cudaError_t launch_norm_t(const NormArgs& a, cudaStream_t s, bool backwar
         const int up = (blocks + VE - 1) / VE * VE;
         blocks = blocks < a.d.T && up <= kNormBlocks ? up : max(VE, blocks / VE * VE);
     }
+    if (backward && blocks > norm_blocks(a.d.T)) return cudaErrorInvalidValue;  // (never: what the workspace holds)
     cudaError_t e;
     if (!backward) {
         MOE_LAUNCH(MOE_KERNEL_NORM, s, (e = launch_pdl(k_norm<T, VE, VPT, GATE>, dim3(blocks), dim3(tpr * groups), 0, s, a, tpr)));

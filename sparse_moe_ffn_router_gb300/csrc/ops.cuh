@@ -133,7 +133,10 @@ struct NormArgs {
     float* part;  // [blocks, 3, H]
     int num_sms;
 };
-constexpr int kNormBlocks = 304;  // CTAs of the backward pass, at most
+// CTAs of the backward pass over T rows, at most: one for each row or few, rounded up to 8 so that the rows of a CTA can
+// begin at the same place within a vector.
+constexpr int kNormBlocks = 304;
+inline int64_t norm_blocks(int64_t T) { return T > kNormBlocks - 8 ? kNormBlocks : (T + 7) / 8 * 8; }
 cudaError_t launch_norm_bf16(const NormArgs& a, cudaStream_t s, bool backward);
 cudaError_t launch_norm_fp16(const NormArgs& a, cudaStream_t s, bool backward);
 cudaError_t launch_norm_fp32(const NormArgs& a, cudaStream_t s, bool backward);

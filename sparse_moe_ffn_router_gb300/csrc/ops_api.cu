@@ -209,8 +209,7 @@ size_t gate_bytes(const moe_norm_dims& d) {
 
 extern "C" size_t moe_norm_workspace_size(const moe_norm_dims* d) {
     if (!norm_known(d) || !norm_shape(*d)) return 0;
-    const size_t blocks = d->T < kNormBlocks ? (d->T > 0 ? d->T : 1) : kNormBlocks;
-    return align256(blocks * 3 * d->H * 4);
+    return align256((size_t)norm_blocks(d->T > 0 ? d->T : 1) * 3 * d->H * 4);
 }
 
 extern "C" moe_status moe_norm_residual(const moe_norm_dims* d, const void* y, const void* residual, const void* gate,

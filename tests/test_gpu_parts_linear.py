@@ -286,3 +286,16 @@ def test_bias_gradient_beside_any_product(keep):
         some = [torch.zeros_like(t) if k else None for t, k in zip(full, keep)]
         moe.moe_linear_backward(d, x, w, off, z, dout, *some, ws)
         assert all(s is None or torch.equal(s, t) for s, t in zip(some, full))
+
+
+@pytest.mark.parametrize("T,N,K,counts", [(1, 7, 16, None), (33, 1003, 72, None), (700, 130, 64, None), (45, 77, 40, [0, 33, 0, 7, 5]), (600, 96, 64, [33] * 18 + [6])])
+def test_nothing_is_written_behind_the_workspace(T, N, K, counts):
+    off = None if counts is None else offsets_of(counts)
+    d = moe.LinearDims(T, N, K, E=1 if counts is None else len(counts), act=moe.ACT_SILU)
+    x, w, b, _ = inputs(d, residual=False)
+    z, dout = ref.randn(5, x.dtype, T, N), ref.randn(6, x.dtype, T, N)
+    size = moe.new_linear_workspace(d, backward=True).numel()
+    room = torch.full((size + (1 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    room[:512] = 0
+    moe.moe_linear_backward(d, x, w, off, z, dout, torch.empty_like(x), torch.empty_like(w), torch.empty_like(b), room[:size])
+    assert moe.moe_last_device_error(room[:size]) == 0 and bool((room[size:] == 0x5A).all())

@@ -168,3 +168,17 @@ def test_no_rows():
     grads = [h.clone() for _ in range(3)]
     moe.moe_norm_residual_backward(d, z, z, z, z, h, h, h, z, z, *grads, moe.new_norm_workspace(d))
     assert all(bool((t == 0).all()) for t in grads)
+
+
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 150, 153, 290, 297, 305, 700])
+@pytest.mark.parametrize("H", [64, 65, 1003, 2048, 8191])
+def test_nothing_is_written_behind_the_workspace(T, H):
+    """Row counts around the CTAs' and rows of any length, with the workspace at the end of what may be written."""
+    d = dims(T, H, moe.BF16, (moe.GATE_CHANNEL, moe.ACT_NONE))
+    y, r, g, gp, gq = inputs(d)
+    s, ds, dxn = ref.randn(5, y.dtype, T, H), ref.randn(6, y.dtype, T, H), ref.randn(7, y.dtype, T, H)
+    size = moe.new_norm_workspace(d).numel()
+    room = torch.full((size + (4 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    new = lambda t: torch.empty_like(t)  # noqa: E731
+    moe.moe_norm_residual_backward(d, ds, dxn, s, y, g, gp, gq, new(y), new(y), new(g), new(gp), new(gq), room[:size])
+    assert bool((room[size:] == 0x5A).all())

@@ -153,6 +153,7 @@ def test_norm_refuses(lib):
     assert backward(dres=at(8)) == 1 and backward(dy=at(3) + 64) == 1 and backward(dgp=at(5)) == 1 and backward(ws=at(1)) == 1
     assert forward(d=NormDims(2 ** 31 - 2 ** 16 + 1, 1)) == 2 and lib.moe_norm_workspace_size(R(NormDims(2 ** 31 - 1, 1))) == 0
     assert lib.moe_norm_workspace_size(R(NormDims(10 ** 6, 2048))) == lib.moe_norm_workspace_size(R(NormDims(304, 2048))) > 0
+    assert lib.moe_norm_workspace_size(R(NormDims(2, 8191))) >= 8 * 3 * 8191 * 4  # eight CTAs, whatever the rows
 
 
 def test_binding_refuses():
