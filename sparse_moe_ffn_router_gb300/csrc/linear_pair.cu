@@ -5,7 +5,8 @@
 // its own 128 feature rows and half of the columns, so a 64-deep stage is 32 KB for 256 x 256 of the product's
 // tile: a tensor core reads 8 KB of shared memory for 128 cycles of work and TMA writes as much, which one SM
 // alone (16 KB of A and 32 KB of B a stage) cannot keep up with. The CTA of even rank issues the
-// MMAs of both; the other's warp 1 passes on that its half of a stage has landed.
+// MMAs of both; its barrier of a stage counts both CTAs' copies. (kDw: each CTA waits for its own half, so that it
+// can clear the rows of another expert in it, and the odd one then reports it.)
 //
 // The epilogue reads accumulator fragments (a thread: two columns of one feature side by side), applies bias,
 // activation and residual in fp32 and transposes by stmatrix, 32 columns at a time, so that what is stored is
@@ -307,106 +308,152 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         break;
                     }
                     if (a.suppress && blockIdx.x == 0 && it == 0) continue;
-                    mbar_arrive_expect_tx(&full[s], bytes);
                     uint8_t* da = sA + s * kLinA;
                     uint8_t* db = sB + s * kPairB;
-                    if (MODE == kFwd) {
-                        if (GATED)
-                            tma_load_5d(da, &mA, &full[s], kb * 64, 0, 0, f * 4, ti.e);
-                        else
-                            tma_load_3d(da, &mA, &full[s], kb * 64, f * 128, ti.e);
-                    } else if (MODE == kDx) {
-                        for (int p = 0; p < 2; ++p) tma_load_3d(da + p * 8192, &mA, &full[s], f * 128 + p * 64, kb * 64, ti.e);
-                    } else {
+                    if (MODE == kDw) {
+                        mbar_arrive_expect_tx(&full[s], bytes);
                         for (int p = 0; p < 2; ++p) tma_load_2d(da + p * 8192, &mA, &full[s], f * 128 + p * 64, ti.row0 + kb * 64);
-                    }
-                    if (MODE == kDw)
                         for (int p = 0; p < boxes; ++p) tma_load_2d(db + p * 8192, &mB, &full[s], c0 + p * 64, ti.row0 + kb * 64);
-                    else
-                        for (int p = 0; p < boxes; ++p) tma_load_2d(db + p * a.boxes * 128, &mB, &full[s], kb * 64, ti.row0 + c0 + p * a.boxes);
+                    } else {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                        const uint32_t bar = mbar_of_even(&full[s]);
+                        if (MODE == kDx) {
+                            for (int p = 0; p < 2; ++p) tma_load_3d_pair(da + p * 8192, &mA, bar, f * 128 + p * 64, kb * 64, ti.e);
+                        } else if (GATED) {
+                            tma_load_5d_pair(da, &mA, bar, kb * 64, 0, 0, f * 4, ti.e);
+                        } else {
+                            tma_load_3d_pair(da, &mA, bar, kb * 64, f * 128, ti.e);
+                        }
+                        for (int p = 0; p < boxes; ++p) tma_load_2d_pair(db + p * a.boxes * 128, &mB, bar, kb * 64, ti.row0 + c0 + p * a.boxes);
+                    }
                     issued[s] = true;
                     last_par[s] = ph;
                 }
             }
-            // every copy this CTA issued must land before shared memory is released
+            // every copy this CTA issued must land before shared memory is released. (Those of the odd CTA count in the other:
+            // the last product has read them by the end; where a wait ran out, a millisecond is ample.)
+            if (MODE == kDw || rank == 0) {
 #pragma unroll
-            for (int s = 0; s < kStages; ++s)
-                if (issued[s] && !mbar_wait(&full[s], last_par[s], a.wait_ns)) atomicOr(a.err, ERR_TIMEOUT);
+                for (int s = 0; s < kStages; ++s)
+                    if (issued[s] && !mbar_wait(&full[s], last_par[s], a.wait_ns)) atomicOr(a.err, ERR_TIMEOUT);
+            }
+            if (*abort_flag) {
+                const uint64_t t0 = global_ns();
+                while (global_ns() - t0 < 1000000u) {}
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ---------------- MMA issuer (even rank), or its counterpart that reports the other half of each stage
-        int it = 0, local = 0;
-        bool ok = true;
-        for (int t = first; t < total && ok; t += step, ++local) {
-            ok = __shfl_sync(0xffffffffu, (int)!*abort_flag, 0) != 0;
-            if (!ok) break;
-            const LinTile ti = walk.to(a, off, start, t);
-            const int n32 = (ti.cols + 31) / 32 * 32;
-            const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 256, n32, MODE != kFwd, MODE == kDw);
-            const int b = local & 1;
-            const uint32_t use = (uint32_t)(local >> 1) & 1u;
-            const uint32_t d = tmem + (uint32_t)(b * 256);
-            if (rank == 0) {
-                ok = mbar_wait(&acce[b], use ^ 1u, a.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
-                tc_fence_after();
+        // ---------------- MMA issuer (even rank)
+        if (MODE != kDw) {
+            // one lane does it all: what it spends on a stage besides the products' 512 clocks is time of narrow tiles
+            if (rank == 0 && elect_one()) {
+                int it = 0, local = 0;
+                bool ok = true;
+                const uint64_t descA = MODE == kFwd ? sdesc_kmajor_sw128(smem_u32(sA)) : sdesc_mnmajor_sw128(smem_u32(sA), 8192);
+                const uint64_t descB = sdesc_kmajor_sw128(smem_u32(sB));
+                for (int t = first; t < total && ok; t += step, ++local) {
+                    if (*abort_flag) break;
+                    const LinTile ti = walk.to(a, off, start, t);
+                    const int n32 = (ti.cols + 31) / 32 * 32;
+                    const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 256, n32, MODE != kFwd, false);
+                    const int b = local & 1;
+                    const uint32_t d = tmem + (uint32_t)(b * 256);
+                    ok = mbar_wait(&acce[b], ((uint32_t)(local >> 1) & 1u) ^ 1u, a.wait_ns);
+                    tc_fence_after();
+                    for (int kb = 0; ok && kb < ti.blocks; ++kb, ++it) {
+                        const int s = it % kStages;
+                        ok = mbar_wait(&full[s], (uint32_t)(it / kStages) & 1u, a.wait_ns);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t da = descA + (uint64_t)(s * (kLinA >> 4)), db = descB + (uint64_t)(s * (kPairB >> 4));
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f16_pair(d, da + (MODE == kFwd ? kk * 2 : kk * 128), db + kk * 2, idesc, (kb | kk) != 0);
+                        mma_commit_pair(&empty[s]);
+                    }
+                    if (ok) mma_commit_pair(&accf[b]);
+                }
+                if (!ok) {
+                    atomicOr(a.err, ERR_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                mma_commit_pair(mma_done);
             }
-            for (int kb = 0; ok && kb < ti.blocks; ++kb, ++it) {
-                const int s = it % kStages;
-                const uint32_t ph = (uint32_t)(it / kStages) & 1u;
-                ok = mbar_wait(&full[s], ph, a.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
+            __syncwarp();
+        } else {
+            int it = 0, local = 0;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += step, ++local) {
+                ok = __shfl_sync(0xffffffffu, (int)!*abort_flag, 0) != 0;
                 if (!ok) break;
-                const uint32_t aa = smem_u32(sA + s * kLinA), bb = smem_u32(sB + s * kPairB);
-                int steps = 4;
-                if (MODE == kDw) {
-                    // the expert's last block: 16 rows at a time, rows of the next expert in the last 16 set to zero in
-                    // both operands (whatever they hold: 0 x infinity would stay)
-                    const int left = ti.rows - kb * 64;
-                    if (left < 64) {
-                        steps = (left + 15) / 16;
-                        if (left & 15) {
-                            const int panels = 2 + (n32 / 2 + 63) / 64, rows = steps * 16 - left;
-                            const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-                            for (int p = 0; p < panels; ++p) {
-                                const uint32_t at = (p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)left * 128u;
-                                for (int i = lane; i < rows * 8; i += 32) sts128(at + (uint32_t)i * 16u, zero);
+                const LinTile ti = walk.to(a, off, start, t);
+                const int n32 = (ti.cols + 31) / 32 * 32;
+                const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 256, n32, MODE != kFwd, MODE == kDw);
+                const int b = local & 1;
+                const uint32_t use = (uint32_t)(local >> 1) & 1u;
+                const uint32_t d = tmem + (uint32_t)(b * 256);
+                if (rank == 0) {
+                    ok = mbar_wait(&acce[b], use ^ 1u, a.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    tc_fence_after();
+                }
+                for (int kb = 0; ok && kb < ti.blocks; ++kb, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t ph = (uint32_t)(it / kStages) & 1u;
+                    ok = mbar_wait(&full[s], ph, a.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t aa = smem_u32(sA + s * kLinA), bb = smem_u32(sB + s * kPairB);
+                    int steps = 4;
+                    if (MODE == kDw) {
+                        // the expert's last block: 16 rows at a time, rows of the next expert in the last 16 set to zero in
+                        // both operands (whatever they hold: 0 x infinity would stay)
+                        const int left = ti.rows - kb * 64;
+                        if (left < 64) {
+                            steps = (left + 15) / 16;
+                            if (left & 15) {
+                                const int panels = 2 + (n32 / 2 + 63) / 64, rows = steps * 16 - left;
+                                const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+                                for (int p = 0; p < panels; ++p) {
+                                    const uint32_t at = (p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)left * 128u;
+                                    for (int i = lane; i < rows * 8; i += 32) sts128(at + (uint32_t)i * 16u, zero);
+                                }
+                                fence_proxy_async_smem();
+                                __syncwarp();
                             }
-                            fence_proxy_async_smem();
-                            __syncwarp();
                         }
                     }
-                }
-                if (rank != 0) {
-                    if (lane == 0) mbar_arrive_cluster(&other[s], 0);
-                    continue;
-                }
-                ok = mbar_wait(&other[s], ph, a.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    for (int kk = 0; kk < steps; ++kk) {
-                        const uint64_t da = MODE == kFwd ? sdesc_kmajor_sw128(aa + kk * 32) : sdesc_mnmajor_sw128(aa + kk * 2048, 8192);
-                        const uint64_t db = MODE == kDw ? sdesc_mnmajor_sw128(bb + kk * 2048, 8192) : sdesc_kmajor_sw128(bb + kk * 32);
-                        mma_f16_pair(d, da, db, idesc, (kb | kk) != 0);
+                    if (rank != 0) {
+                        if (lane == 0) mbar_arrive_cluster(&other[s], 0);
+                        continue;
                     }
-                    mma_commit_pair(&empty[s]);
-                    if (kb + 1 == ti.blocks) mma_commit_pair(&accf[b]);
+                    ok = mbar_wait(&other[s], ph, a.wait_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        for (int kk = 0; kk < steps; ++kk) {
+                            const uint64_t da = MODE == kFwd ? sdesc_kmajor_sw128(aa + kk * 32) : sdesc_mnmajor_sw128(aa + kk * 2048, 8192);
+                            const uint64_t db = MODE == kDw ? sdesc_mnmajor_sw128(bb + kk * 2048, 8192) : sdesc_kmajor_sw128(bb + kk * 32);
+                            mma_f16_pair(d, da, db, idesc, (kb | kk) != 0);
+                        }
+                        mma_commit_pair(&empty[s]);
+                        if (kb + 1 == ti.blocks) mma_commit_pair(&accf[b]);
+                    }
+                    __syncwarp();
+                }
+                if (ok && ti.blocks == 0 && rank == 0 && lane < 2) mbar_arrive_cluster(&accf[b], lane);  // (no rows: zeros are written)
+                if (!ok && lane == 0) {
+                    atomicOr(a.err, ERR_TIMEOUT);
+                    *abort_flag = 1;
                 }
                 __syncwarp();
             }
-            if (ok && ti.blocks == 0 && rank == 0 && lane < 2) mbar_arrive_cluster(&accf[b], lane);  // (no rows: zeros are written)
-            if (!ok && lane == 0) {
-                atomicOr(a.err, ERR_TIMEOUT);
-                *abort_flag = 1;
+            if (rank == 0) {
+                if (elect_one()) mma_commit_pair(mma_done);
+                __syncwarp();
             }
-            __syncwarp();
-        }
-        if (rank == 0) {
-            if (elect_one()) mma_commit_pair(mma_done);
-            __syncwarp();
         }
         if (!mbar_wait(mma_done, 0, a.wait_ns) && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
         __syncwarp();

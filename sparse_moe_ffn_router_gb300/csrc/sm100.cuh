@@ -350,6 +350,34 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
                  "h"((uint16_t)3)
                  : "memory");
 }
+// Address of the barrier at bar's place in the CTA of even rank, in the cluster's shared window.
+__device__ __forceinline__ uint32_t mbar_of_even(uint64_t* bar) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+    return a;
+}
+// TMA loads into this CTA's shared memory that complete on a barrier of either CTA of the pair (a cluster-window address).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* map, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_pair(void* dst, const void* map, uint32_t bar, int c0, int c1, int c2, int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, "
+        "%7}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
 // One arrival on the barrier at bar's place in CTA `rank` of the cluster. (What it reports is shared memory that TMA or
 // a fenced store has filled, or tensor memory that has been read: no global write has to be out first. At
 // cluster scope the release would wait for those: 1900 instead of 512 clocks a stage of the pair kernel.)
