@@ -156,12 +156,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (warp == 0) {
         // ---------------- TMA producer (one lane; the warp stays together for the cluster's barriers)
         int it = 0;
-        uint32_t last_par[kStages];
-        bool issued[kStages];
-#pragma unroll
-        for (int s = 0; s < kStages; ++s) issued[s] = false;
+        bool loads = false;
         for (int t = first; t < total; t += step) {
-            if (lane == 0 && !*abort_flag) {
+            if (elect_one() && !*abort_flag) {
+                loads = true;
                 const LinTile ti = walk.to(a, off, start, t);
                 const int kb0 = (int)((int64_t)ti.blocks * rank / split), kb1 = (int)((int64_t)ti.blocks * (rank + 1) / split);
                 const int boxes = MODE == kDw ? (ti.cols + 63) / 64 : (ti.cols + kLinBoxRows - 1) / kLinBoxRows;
@@ -193,8 +191,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     else
                         for (int p = 0; p < boxes; ++p)
                             tma_load_2d(db + p * (kLinBoxRows * 128), &mB, &full[s], kb * 64, ti.row0 + ti.c0 + p * kLinBoxRows);
-                    issued[s] = true;
-                    last_par[s] = ph;
                 }
             }
             __syncwarp();
@@ -204,10 +200,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
         }
         // every copy this CTA issued must land before shared memory is released
-        if (lane == 0)
-#pragma unroll
-            for (int s = 0; s < kStages; ++s)
-                if (issued[s] && !mbar_wait(&full[s], last_par[s], a.wait_ns)) atomicOr(a.err, ERR_TIMEOUT);
+        if (loads)
+            for (int s = 0; s < min(it, kStages); ++s)  // (its last use: number (it - 1 - s) / kStages)
+                if (!mbar_wait(&full[s], (uint32_t)((it - 1 - s) / kStages) & 1u, a.wait_ns)) atomicOr(a.err, ERR_TIMEOUT);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------- MMA issuer

@@ -287,12 +287,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
     if (warp == 0) {
         // ---------------- TMA producer of this CTA's halves
-        if (lane == 0) {
+        if (elect_one()) {
             int it = 0;
-            uint32_t last_par[kStages];
-            bool issued[kStages];
-#pragma unroll
-            for (int s = 0; s < kStages; ++s) issued[s] = false;
             for (int t = first; t < total && !*abort_flag; t += step) {
                 const LinTile ti = walk.to(a, off, start, t);
                 const int half = (ti.cols + 31) / 32 * 16;  // columns of this CTA
@@ -326,16 +322,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         }
                         for (int p = 0; p < boxes; ++p) tma_load_2d_pair(db + p * a.boxes * 128, &mB, bar, kb * 64, ti.row0 + c0 + p * a.boxes);
                     }
-                    issued[s] = true;
-                    last_par[s] = ph;
                 }
             }
             // every copy this CTA issued must land before shared memory is released. (Those of the odd CTA count in the other:
             // the last product has read them by the end; where a wait ran out, a millisecond is ample.)
             if (MODE == kDw || rank == 0) {
-#pragma unroll
-                for (int s = 0; s < kStages; ++s)
-                    if (issued[s] && !mbar_wait(&full[s], last_par[s], a.wait_ns)) atomicOr(a.err, ERR_TIMEOUT);
+                for (int s = 0; s < min(it, kStages); ++s)  // (its last use: number (it - 1 - s) / kStages)
+                    if (!mbar_wait(&full[s], (uint32_t)((it - 1 - s) / kStages) & 1u, a.wait_ns)) atomicOr(a.err, ERR_TIMEOUT);
             }
             if (*abort_flag) {
                 const uint64_t t0 = global_ns();
@@ -389,7 +382,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 if (!ok) break;
                 const LinTile ti = walk.to(a, off, start, t);
                 const int n32 = (ti.cols + 31) / 32 * 32;
-                const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 256, n32, MODE != kFwd, MODE == kDw);
+                const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 256, n32, true, true);
                 const int b = local & 1;
                 const uint32_t use = (uint32_t)(local >> 1) & 1u;
                 const uint32_t d = tmem + (uint32_t)(b * 256);
@@ -405,23 +398,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const uint32_t aa = smem_u32(sA + s * kLinA), bb = smem_u32(sB + s * kPairB);
+                    // the expert's last block: 16 rows at a time, rows of the next expert in the last 16 set to zero in
+                    // both operands (whatever they hold: 0 x infinity would stay)
                     int steps = 4;
-                    if (MODE == kDw) {
-                        // the expert's last block: 16 rows at a time, rows of the next expert in the last 16 set to zero in
-                        // both operands (whatever they hold: 0 x infinity would stay)
-                        const int left = ti.rows - kb * 64;
-                        if (left < 64) {
-                            steps = (left + 15) / 16;
-                            if (left & 15) {
-                                const int panels = 2 + (n32 / 2 + 63) / 64, rows = steps * 16 - left;
-                                const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-                                for (int p = 0; p < panels; ++p) {
-                                    const uint32_t at = (p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)left * 128u;
-                                    for (int i = lane; i < rows * 8; i += 32) sts128(at + (uint32_t)i * 16u, zero);
-                                }
-                                fence_proxy_async_smem();
-                                __syncwarp();
+                    const int left = ti.rows - kb * 64;
+                    if (left < 64) {
+                        steps = (left + 15) / 16;
+                        if (left & 15) {
+                            const int panels = 2 + (n32 / 2 + 63) / 64, rows = steps * 16 - left;
+                            const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+                            for (int p = 0; p < panels; ++p) {
+                                const uint32_t at = (p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)left * 128u;
+                                for (int i = lane; i < rows * 8; i += 32) sts128(at + (uint32_t)i * 16u, zero);
                             }
+                            fence_proxy_async_smem();
+                            __syncwarp();
                         }
                     }
                     if (rank != 0) {
@@ -433,11 +424,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        for (int kk = 0; kk < steps; ++kk) {
-                            const uint64_t da = MODE == kFwd ? sdesc_kmajor_sw128(aa + kk * 32) : sdesc_mnmajor_sw128(aa + kk * 2048, 8192);
-                            const uint64_t db = MODE == kDw ? sdesc_mnmajor_sw128(bb + kk * 2048, 8192) : sdesc_kmajor_sw128(bb + kk * 32);
-                            mma_f16_pair(d, da, db, idesc, (kb | kk) != 0);
-                        }
+                        const uint64_t da = sdesc_mnmajor_sw128(aa, 8192), db = sdesc_mnmajor_sw128(bb, 8192);
+                        for (int kk = 0; kk < steps; ++kk) mma_f16_pair(d, da + kk * 128, db + kk * 128, idesc, (kb | kk) != 0);
                         mma_commit_pair(&empty[s]);
                         if (kb + 1 == ti.blocks) mma_commit_pair(&accf[b]);
                     }

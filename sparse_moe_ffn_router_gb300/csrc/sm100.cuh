@@ -27,7 +27,7 @@ __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
 }
 
-// True in one lane of a converged warp. The compiler knows that one lane alone runs what this guards, so
+// True in one lane of a converged warp, the same one every time. The compiler knows that one lane alone runs what this guards, so
 // instructions with warp-uniform operands (TMA, tcgen05.mma and commit) are issued without a loop over lanes.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
