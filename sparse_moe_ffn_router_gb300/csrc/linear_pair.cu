@@ -5,8 +5,9 @@
 // its own 128 feature rows and half of the columns, so a 64-deep stage is 32 KB for 256 x 256 of the product's
 // tile: a tensor core reads 8 KB of shared memory for 128 cycles of work and TMA writes as much, which one SM
 // alone (16 KB of A and 32 KB of B a stage) cannot keep up with. The CTA of even rank issues the
-// MMAs of both; its barrier of a stage counts both CTAs' copies. (kDw: each CTA waits for its own half, so that it
-// can clear the rows of another expert in it, and the odd one then reports it.)
+// MMAs of both; its barrier of a stage counts both CTAs' copies. An expert's last rows of kDw, where they are no whole
+// 16, bring rows of the next expert along: those stages land on a barrier of each CTA's own, a warp clears the
+// foreign rows, and the even CTA's reports the stage once both are done.
 //
 // The epilogue reads accumulator fragments (a thread: two columns of one feature side by side), applies bias,
 // activation and residual in fp32 and transposes by stmatrix, 32 columns at a time, so that what is stored is
@@ -228,6 +229,13 @@ __device__ __forceinline__ void pair_epilogue_dw(const CUtensorMap* mC, uint32_t
     }
 }
 
+// Whether block kb of an expert's rows ends in rows of the next expert that its last 16 would take in (one matrix for all rows: its
+// last block ends in TMA's zeros).
+__device__ __forceinline__ bool pair_clears(const LinView& a, const LinTile& ti, int kb) {
+    const int left = ti.rows - kb * 64;
+    return a.offsets && left < 64 && (left & 15);
+}
+
 template <typename T, int MODE, bool GATED>
 __global__ void __launch_bounds__(kLinThreads, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mC, const LinView a) {
@@ -241,23 +249,25 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint8_t* scratch = smem + kPairRing;
     int* off = reinterpret_cast<int*>(scratch + kPairScratch);
     int* start = off + kLinMaxE + 4;
-    uint64_t* full = reinterpret_cast<uint64_t*>(scratch + kPairScratch + kPairTables);  // this CTA's half of a stage has landed
-    uint64_t* other = full + kStages;   // even rank: so has the other's
-    uint64_t* empty = other + kStages;  // both CTAs' MMAs have read it
-    uint64_t* accf = empty + kStages;
+    uint64_t* full = reinterpret_cast<uint64_t*>(scratch + kPairScratch + kPairTables);  // even rank: a stage of both CTAs is ready
+    uint64_t* empty = full + kStages;  // both CTAs' MMAs have read it
+    uint64_t* mine = empty + kStages;  // kDw: this CTA's half has landed and is to be cleared
+    uint64_t* other = mine + kStages;  // kDw, even rank: the other's is
+    uint64_t* accf = other + kStages;
     uint64_t* acce = accf + 2;          // even rank: both CTAs' epilogues have read the accumulator
     uint64_t* mma_done = acce + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((3 * kStages + 5) * 8 + 8 <= 256, "barrier area");
+    static_assert((4 * kStages + 5) * 8 + 8 <= 256, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&other[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&mine[s], 1);
+            mbar_init(&other[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf[b], 1);
@@ -306,13 +316,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     if (a.suppress && blockIdx.x == 0 && it == 0) continue;
                     uint8_t* da = sA + s * kLinA;
                     uint8_t* db = sB + s * kPairB;
+                    const bool clear = MODE == kDw && pair_clears(a, ti, kb);
+                    if (clear) mbar_arrive_expect_tx(&mine[s], bytes);
+                    else if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                    const uint32_t bar = clear ? smem_u32(&mine[s]) : mbar_of_even(&full[s]);
                     if (MODE == kDw) {
-                        mbar_arrive_expect_tx(&full[s], bytes);
-                        for (int p = 0; p < 2; ++p) tma_load_2d(da + p * 8192, &mA, &full[s], f * 128 + p * 64, ti.row0 + kb * 64);
-                        for (int p = 0; p < boxes; ++p) tma_load_2d(db + p * 8192, &mB, &full[s], c0 + p * 64, ti.row0 + kb * 64);
+                        for (int p = 0; p < 2; ++p) tma_load_2d_pair(da + p * 8192, &mA, bar, f * 128 + p * 64, ti.row0 + kb * 64);
+                        for (int p = 0; p < boxes; ++p) tma_load_2d_pair(db + p * 8192, &mB, bar, c0 + p * 64, ti.row0 + kb * 64);
                     } else {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
-                        const uint32_t bar = mbar_of_even(&full[s]);
                         if (MODE == kDx) {
                             for (int p = 0; p < 2; ++p) tma_load_3d_pair(da + p * 8192, &mA, bar, f * 128 + p * 64, kb * 64, ti.e);
                         } else if (GATED) {
@@ -326,7 +337,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
             // every copy this CTA issued must land before shared memory is released. (Those of the odd CTA count in the other:
             // the last product has read them by the end; where a wait ran out, a millisecond is ample.)
-            if (MODE == kDw || rank == 0) {
+            if (rank == 0) {
                 for (int s = 0; s < min(it, kStages); ++s)  // (its last use: number (it - 1 - s) / kStages)
                     if (!mbar_wait(&full[s], (uint32_t)((it - 1 - s) / kStages) & 1u, a.wait_ns)) atomicOr(a.err, ERR_TIMEOUT);
             }
@@ -337,112 +348,48 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ---------------- MMA issuer (even rank)
-        if (MODE != kDw) {
-            // one lane does it all: what it spends on a stage besides the products' 512 clocks is time of narrow tiles
-            if (rank == 0 && elect_one()) {
-                int it = 0, local = 0;
-                bool ok = true;
-                const uint64_t descA = MODE == kFwd ? sdesc_kmajor_sw128(smem_u32(sA)) : sdesc_mnmajor_sw128(smem_u32(sA), 8192);
-                const uint64_t descB = sdesc_kmajor_sw128(smem_u32(sB));
-                for (int t = first; t < total && ok; t += step, ++local) {
-                    if (*abort_flag) break;
-                    const LinTile ti = walk.to(a, off, start, t);
-                    const int n32 = (ti.cols + 31) / 32 * 32;
-                    const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 256, n32, MODE != kFwd, false);
-                    const int b = local & 1;
-                    const uint32_t d = tmem + (uint32_t)(b * 256);
-                    ok = mbar_wait(&acce[b], ((uint32_t)(local >> 1) & 1u) ^ 1u, a.wait_ns);
-                    tc_fence_after();
-                    for (int kb = 0; ok && kb < ti.blocks; ++kb, ++it) {
-                        const int s = it % kStages;
-                        ok = mbar_wait(&full[s], (uint32_t)(it / kStages) & 1u, a.wait_ns);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t da = descA + (uint64_t)(s * (kLinA >> 4)), db = descB + (uint64_t)(s * (kPairB >> 4));
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f16_pair(d, da + (MODE == kFwd ? kk * 2 : kk * 128), db + kk * 2, idesc, (kb | kk) != 0);
-                        mma_commit_pair(&empty[s]);
-                    }
-                    if (ok) mma_commit_pair(&accf[b]);
-                }
-                if (!ok) {
-                    atomicOr(a.err, ERR_TIMEOUT);
-                    *abort_flag = 1;
-                }
-                mma_commit_pair(mma_done);
-            }
-            __syncwarp();
-        } else {
+        // ---------------- MMA issuer (even rank). One lane does it all: what it spends on a stage besides the products'
+        // 512 clocks is time of narrow tiles.
+        if (rank == 0 && elect_one()) {
             int it = 0, local = 0;
             bool ok = true;
+            const uint64_t descA = MODE == kFwd ? sdesc_kmajor_sw128(smem_u32(sA)) : sdesc_mnmajor_sw128(smem_u32(sA), 8192);
+            const uint64_t descB = MODE == kDw ? sdesc_mnmajor_sw128(smem_u32(sB), 8192) : sdesc_kmajor_sw128(smem_u32(sB));
+            constexpr int kStepA = MODE == kFwd ? 2 : 128, kStepB = MODE == kDw ? 128 : 2;  // 16 deeper, in 16-byte units
             for (int t = first; t < total && ok; t += step, ++local) {
-                ok = __shfl_sync(0xffffffffu, (int)!*abort_flag, 0) != 0;
-                if (!ok) break;
+                if (*abort_flag) break;
                 const LinTile ti = walk.to(a, off, start, t);
                 const int n32 = (ti.cols + 31) / 32 * 32;
-                const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 256, n32, true, true);
+                const uint32_t idesc = idesc_f16_f32(std::is_same<T, bf16>::value, 256, n32, MODE != kFwd, MODE == kDw);
                 const int b = local & 1;
-                const uint32_t use = (uint32_t)(local >> 1) & 1u;
                 const uint32_t d = tmem + (uint32_t)(b * 256);
-                if (rank == 0) {
-                    ok = mbar_wait(&acce[b], use ^ 1u, a.wait_ns);
-                    ok = __all_sync(0xffffffffu, ok);
-                    tc_fence_after();
-                }
+                ok = mbar_wait(&acce[b], ((uint32_t)(local >> 1) & 1u) ^ 1u, a.wait_ns);
+                tc_fence_after();
                 for (int kb = 0; ok && kb < ti.blocks; ++kb, ++it) {
                     const int s = it % kStages;
-                    const uint32_t ph = (uint32_t)(it / kStages) & 1u;
-                    ok = mbar_wait(&full[s], ph, a.wait_ns);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    const uint32_t aa = smem_u32(sA + s * kLinA), bb = smem_u32(sB + s * kPairB);
-                    // the expert's last block: 16 rows at a time, rows of the next expert in the last 16 set to zero in
-                    // both operands (whatever they hold: 0 x infinity would stay)
-                    int steps = 4;
-                    const int left = ti.rows - kb * 64;
-                    if (left < 64) {
-                        steps = (left + 15) / 16;
-                        if (left & 15) {
-                            const int panels = 2 + (n32 / 2 + 63) / 64, rows = steps * 16 - left;
-                            const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-                            for (int p = 0; p < panels; ++p) {
-                                const uint32_t at = (p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)left * 128u;
-                                for (int i = lane; i < rows * 8; i += 32) sts128(at + (uint32_t)i * 16u, zero);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                    }
-                    if (rank != 0) {
-                        if (lane == 0) mbar_arrive_cluster(&other[s], 0);
-                        continue;
-                    }
-                    ok = mbar_wait(&other[s], ph, a.wait_ns);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = mbar_wait(&full[s], (uint32_t)(it / kStages) & 1u, a.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t da = sdesc_mnmajor_sw128(aa, 8192), db = sdesc_mnmajor_sw128(bb, 8192);
-                        for (int kk = 0; kk < steps; ++kk) mma_f16_pair(d, da + kk * 128, db + kk * 128, idesc, (kb | kk) != 0);
-                        mma_commit_pair(&empty[s]);
-                        if (kb + 1 == ti.blocks) mma_commit_pair(&accf[b]);
-                    }
-                    __syncwarp();
+                    const uint64_t da = descA + (uint64_t)(s * (kLinA >> 4)), db = descB + (uint64_t)(s * (kPairB >> 4));
+                    const int steps = MODE == kDw ? min(4, (ti.rows - kb * 64 + 15) / 16) : 4;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (kk < steps) mma_f16_pair(d, da + kk * kStepA, db + kk * kStepB, idesc, (kb | kk) != 0);
+                    mma_commit_pair(&empty[s]);
                 }
-                if (ok && ti.blocks == 0 && rank == 0 && lane < 2) mbar_arrive_cluster(&accf[b], lane);  // (no rows: zeros are written)
-                if (!ok && lane == 0) {
-                    atomicOr(a.err, ERR_TIMEOUT);
-                    *abort_flag = 1;
+                if (ok && ti.blocks > 0) mma_commit_pair(&accf[b]);
+                if (ok && ti.blocks == 0) {  // (no rows: zeros are written)
+                    mbar_arrive_cluster(&accf[b], 0);
+                    mbar_arrive_cluster(&accf[b], 1);
                 }
-                __syncwarp();
             }
-            if (rank == 0) {
-                if (elect_one()) mma_commit_pair(mma_done);
-                __syncwarp();
+            if (!ok) {
+                atomicOr(a.err, ERR_TIMEOUT);
+                *abort_flag = 1;
             }
+            mma_commit_pair(mma_done);
         }
+        __syncwarp();
         if (!mbar_wait(mma_done, 0, a.wait_ns) && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
         __syncwarp();
     } else if (warp >= kLinEpiWarp0) {
@@ -477,8 +424,40 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         if (MODE == kDw && lane == 0) tma_store_wait_all();
         __syncwarp();
-    } else if (MODE != kFwd && a.dbias) {
-        lin_dbias<T>(a, off, blockIdx.x * 2 + warp - 2, gridDim.x * 2);
+    } else {
+        if (MODE == kDw && warp == 2 && a.offsets) {
+            // ---------------- rows of the next expert in an expert's last 16: zeros in both operands (whatever they hold: 0 x
+            // infinity would stay)
+            int it = 0;
+            uint32_t turn = 0;  // a bit a stage: the phase its barriers here are in
+            for (int t = first; t < total && !__any_sync(0xffffffffu, *abort_flag); t += step) {
+                const LinTile ti = walk.to(a, off, start, t);
+                it += ti.blocks;
+                if (ti.blocks == 0 || !pair_clears(a, ti, ti.blocks - 1)) continue;
+                const int s = (it - 1) % kStages, left = ti.rows - (ti.blocks - 1) * 64, rows = (left + 15) / 16 * 16 - left;
+                const uint32_t ph = turn >> s & 1u;
+                turn ^= 1u << s;
+                bool ok = mbar_wait(&mine[s], ph, a.wait_ns);
+                const int panels = 2 + ((ti.cols + 31) / 32 * 16 + 63) / 64;
+                const uint32_t aa = smem_u32(sA + s * kLinA), bb = smem_u32(sB + s * kPairB);
+                const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+                if (ok)
+                    for (int p = 0; p < panels; ++p) {
+                        const uint32_t at = (p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)left * 128u;
+                        for (int i = lane; i < rows * 8; i += 32) sts128(at + (uint32_t)i * 16u, zero);
+                    }
+                fence_proxy_async_smem();
+                if (ok && rank == 0) ok = mbar_wait(&other[s], ph, a.wait_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok && lane == 0) {
+                    atomicOr(a.err, ERR_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                if (ok && lane == 0) mbar_arrive_cluster(rank == 0 ? &full[s] : &other[s], 0);
+                __syncwarp();
+            }
+        }
+        if (MODE != kFwd && a.dbias) lin_dbias<T>(a, off, blockIdx.x * 2 + warp - 2, gridDim.x * 2);
         __syncwarp();
     }
     tc_fence_before();
