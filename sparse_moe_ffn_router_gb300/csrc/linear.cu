@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------------
-// dz = act'(z) * dout, and the column sums of it for the bias. A CTA takes a chunk of 32 rows and 128
+// dz = act'(z) * dout, and the column sums of it for the bias. A CTA takes a chunk of 32 or 128 rows and 128
 // columns (for swiglu 128 gate columns and the matching up columns); 16 threads side by side hold 8 columns
 // each, 16 rows at a time. Sums are of dz before its rounding, row block by row block: those of the rows of
 // expert e in chunk c go to part[c + e], a place of their own as chunks and experts follow one another.
@@ -413,27 +413,22 @@ template <typename T, int VE, bool GATED>
 __global__ void __launch_bounds__(256, 3) k_dz(const LinearArgs a, int pitch) {
     __shared__ int off[kLinMaxE + 1];
     __shared__ float sums[GATED ? 2 : 1][16][128];
-    constexpr int kMore = kDzRows / 16;  // rows of a thread, all loaded before the first is used
     typedef RawOf<T> R;
     grid_dep_wait();
     grid_dep_launch();
     const int N = a.d.N, E = a.d.E, wide = GATED ? N / 2 : N;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int r0 = blockIdx.x * kDzRows, r1 = min(r0 + kDzRows, a.d.T);
+    const int r0 = blockIdx.x * a.chunk, r1 = min(r0 + a.chunk, a.d.T);
     const int f = blockIdx.y * 128 + tx * 8, n = min(8, wide - f);  // columns of this thread (none: n <= 0)
     const bool need_z = GATED || a.d.act != MOE_ACT_NONE;
     T* dz = reinterpret_cast<T*>(a.dz);
     const T *z = reinterpret_cast<const T*>(a.z_in), *dout = reinterpret_cast<const T*>(a.dout);
-    Raw dv[kMore], zv[kMore], uv[kMore];
-#pragma unroll
-    for (int k = 0; k < kMore; ++k) {
-        const int r = r0 + ty + 16 * k;
-        if (r < r1 && n > 0) {
-            dv[k] = ld_cols<T, VE>(dout, (int64_t)r * wide + f, (int64_t)a.d.T * wide, n);
-            if (need_z) zv[k] = ld_cols<T, VE>(z, (int64_t)r * N + f, (int64_t)a.d.T * N, n);
-            if (GATED) uv[k] = ld_cols<T, VE>(z, (int64_t)r * N + wide + f, (int64_t)a.d.T * N, n);
-        }
-    }
+    Raw dv, zv, uv;
+    auto load = [&](int r) {
+        dv = ld_cols<T, VE>(dout, (int64_t)r * wide + f, (int64_t)a.d.T * wide, n);
+        if (need_z) zv = ld_cols<T, VE>(z, (int64_t)r * N + f, (int64_t)a.d.T * N, n);
+        if (GATED) uv = ld_cols<T, VE>(z, (int64_t)r * N + wide + f, (int64_t)a.d.T * N, n);
+    };
     // whose rows they are matters to the column sums alone (rows behind the last expert's are read into nothing)
     const bool split = a.offsets && a.dbias;
     int lo = 0, hi = split ? E : 1;
@@ -453,17 +448,16 @@ __global__ void __launch_bounds__(256, 3) k_dz(const LinearArgs a, int pitch) {
         float sv[8], su[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) sv[i] = su[i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < kMore; ++k) {
-            const int r = r0 + ty + 16 * k;
-            if (r < b0 || r >= b1 || n <= 0) continue;
-            float d[8], v[8];
-            R::values(dv[k], d);
-            if (need_z) R::values(zv[k], v);
+        const int last = n > 0 ? b1 : b0;
+        if (b0 + ty < last) load(b0 + ty);
+        for (int r = b0 + ty; r < last; r += 16) {
+            float d[8], v[8], u[8];
+            R::values(dv, d);
+            if (need_z) R::values(zv, v);
+            if (GATED) R::values(uv, u);
+            if (r + 16 < last) load(r + 16);  // the next row comes while this one is worked on
             const int64_t at = (int64_t)r * pitch + f;
             if (GATED) {
-                float u[8];
-                R::values(uv[k], u);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float p = lin_sigmoid(v[i]), dd = d[i];
@@ -698,7 +692,7 @@ cudaError_t linear_t(const LinearArgs& a, cudaStream_t s) {
 template <typename T, int VE, bool GATED>
 cudaError_t launch_dz(const LinearArgs& a, int pitch, cudaStream_t s) {
     const int wide = GATED ? a.d.N / 2 : a.d.N;
-    return launch_pdl(k_dz<T, VE, GATED>, dim3((a.d.T + kDzRows - 1) / kDzRows, (wide + 127) / 128), dim3(256), 0, s, a, pitch);
+    return launch_pdl(k_dz<T, VE, GATED>, dim3((a.d.T + a.chunk - 1) / a.chunk, (wide + 127) / 128), dim3(256), 0, s, a, pitch);
 }
 
 template <typename T>
@@ -710,6 +704,9 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
     const bool plain = d.act == MOE_ACT_NONE && vec;  // dz is dout itself
     if (plain || (!a.dx && !a.dw)) a.dz = nullptr;
     cudaError_t e = cudaSuccess;
+    // chunks of 128 rows where they still give every SM four CTAs, else of 32
+    const int64_t strips = ((gated ? d.N / 2 : d.N) + 127) / 128;
+    a.chunk = ((int64_t)d.T + 127) / 128 * strips >= 4 * (int64_t)a.num_sms ? 4 * kDzRows : kDzRows;
     if (a.dz || a.dbias) {
         MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s,
                    (e = gated ? launch_dz<T, 8, true>(a, pitch, s) : vec ? launch_dz<T, 8, false>(a, pitch, s) : launch_dz<T, 1, false>(a, pitch, s)));
@@ -721,6 +718,7 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
     LinView v = view_of(a);
     v.F = d.K;
     v.part = a.part;
+    v.chunk = a.chunk;
     v.dbias = a.dbias;  // (the first of the products adds it up)
     if (a.dbias && !a.dx && !a.dw) {
         MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s, (e = launch_pdl(k_dbias<T>, dim3(a.num_sms), dim3(256), 0, s, v)));

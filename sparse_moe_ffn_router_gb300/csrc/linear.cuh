@@ -30,7 +30,8 @@ struct LinView {
     int vec;          // rows of out, residual and z start on 8 bytes (pair kernel: on 16)
     int boxes;        // rows of a K-major column-side TMA box
     int suppress;     // testing aid: CTA 0 never loads its first stage
-    const float* part;  // kDx, kDw: column sums to add up beside the products, or NULL
+    const float* part;  // kDx, kDw: column sums of chunks of `chunk` rows to add up beside the products, or NULL
+    int chunk;
     void* dbias;
     uint32_t* err;
     uint64_t wait_ns;
@@ -267,7 +268,7 @@ __device__ void lin_dbias(const LinView& a, const int* off, int w, int warps) {
         const int b0 = off[e], b1 = off[e + 1];
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         if (b0 < b1) {
-            const int c0 = b0 / kDzRows, c1 = (b1 - 1) / kDzRows + 1;
+            const int c0 = b0 / a.chunk, c1 = (b1 - 1) / a.chunk + 1;
             const float* p = a.part + (int64_t)(c0 + e) * a.N + n;
             int c = c0;
             for (; c + 4 <= c1; c += 4, p += (int64_t)4 * a.N) {

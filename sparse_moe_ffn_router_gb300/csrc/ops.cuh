@@ -153,13 +153,14 @@ struct LinearArgs {
     const void *z_in, *dout;
     void *dx, *dw, *dbias;
     void* dz;                // [T, N rounded up to 8]: gradient of the pre-activation
-    float* part;             // [ceil(T / kDzRows) + E, N]: column sums of a chunk's rows of one expert
+    float* part;             // [ceil(T / chunk) + E, N]: column sums of a chunk's rows of one expert
+    int chunk;               // rows of a chunk: kDzRows or more
     uint32_t* err;
     uint64_t wait_ns;
     int num_sms;
     int suppress;            // testing aid: CTA 0 of the forward kernel never loads its first stage
 };
-constexpr int kDzRows = 32;  // rows of a chunk
+constexpr int kDzRows = 32;  // rows of a chunk, at least
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 cudaError_t launch_linear_backward(const LinearArgs& a, cudaStream_t s);
 // A tensor map for TMA with 128-byte (or 64-byte) swizzle and zeros outside: dims and box innermost first, strides in

@@ -299,3 +299,12 @@ def test_nothing_is_written_behind_the_workspace(T, N, K, counts):
     room[:512] = 0
     moe.moe_linear_backward(d, x, w, off, z, dout, torch.empty_like(x), torch.empty_like(w), torch.empty_like(b), room[:size])
     assert moe.moe_last_device_error(room[:size]) == 0 and bool((room[size:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("T,N,counts,act", [(8192, 1203, None, moe.ACT_GELU), (0, 1280, [33] * 256, moe.ACT_SILU), (0, 2560, [0, 127, 1, 0, 128, 129, 6000, 700], moe.ACT_SWIGLU)])
+def test_many_rows_in_chunks_of_128(T, N, counts, act):
+    """Row counts from which the elementwise pass of the way back takes four times the rows at once."""
+    off = None if counts is None else offsets_of(counts)
+    d = moe.LinearDims(T if counts is None else int(off[-1]) + 3, N, 72, E=1 if counts is None else len(counts), act=act)
+    x, w, b, _ = inputs(d, residual=False)
+    check_backward(d, x, w, off, ref.randn(5, x.dtype, d.T, N))
