@@ -84,7 +84,7 @@ __device__ __forceinline__ NormGroup norm_group(int tpr) {
     return g;
 }
 
-// Sums over the group of N values, the warps' sums in warp order. buf is a place of this round alone until the group has
+// Sums over the group of N values, the warps' sums in warp order. buf is this sum's alone until the group has
 // passed another one.
 template <int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], float (*buf)[20], const NormGroup& g) {

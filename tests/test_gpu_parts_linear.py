@@ -308,3 +308,44 @@ def test_many_rows_in_chunks_of_128(T, N, counts, act):
     d = moe.LinearDims(T if counts is None else int(off[-1]) + 3, N, 72, E=1 if counts is None else len(counts), act=act)
     x, w, b, _ = inputs(d, residual=False)
     check_backward(d, x, w, off, ref.randn(5, x.dtype, d.T, N))
+
+
+def test_results_past_32_bits_of_elements():
+    """Rows and matrices that begin behind element 2^31."""
+    d = moe.LinearDims(32800, 65560, 64, act=moe.ACT_RELU)
+    assert d.T * d.N > 2 ** 31
+    x, w, b, _ = inputs(d, residual=False)
+    out, z = (torch.empty(d.T, d.N, dtype=x.dtype, device="cuda") for _ in range(2))
+    moe.moe_linear(d, x, w, b, None, None, out, z, moe.new_linear_workspace(d))
+    for rows in (slice(0, 40), slice(d.T // 2, d.T // 2 + 40), slice(d.T - 40, d.T)):
+        part = moe.LinearDims(40, d.N, d.K, act=d.act)
+        o64, z64, mo, mz = ref.linear(part, x[rows], w, b, None, None)
+        ref.check(out[rows], o64, mo, d.K + 2, "out")
+        ref.check(z[rows], z64, mz, d.K + 2, "z")
+    dx, db = torch.empty_like(x), torch.empty_like(b)
+    moe.moe_linear_backward(d, None, w, None, z, out, dx, None, db, moe.new_linear_workspace(d, backward=True))
+    for rows in (slice(0, 40), slice(d.T - 40, d.T)):
+        part = moe.LinearDims(40, d.N, d.K, act=d.act)
+        want, bound = ref.linear_backward(part, x[rows], w, None, z[rows], out[rows])
+        assert not bool((~((dx[rows].double() - want[0]).abs() <= bound[0])).any())
+
+
+def test_matrices_past_32_bits_of_elements():
+    d = moe.LinearDims(700, 4104, 2056, E=256)
+    assert d.E * d.N * d.K > 2 ** 31
+    off = offsets_of([2] * 250 + [0, 100, 0, 30, 0, 70])
+    x, w = ref.randn(1, torch.bfloat16, d.T, d.K), torch.empty(d.E, d.N, d.K, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, d.E, 16):
+        w[i:i + 16] = ref.randn(i, torch.bfloat16, 16, d.N, d.K, scale=d.K ** -0.5)
+    out, dout, dw = torch.empty(d.T, d.N, dtype=x.dtype, device="cuda"), ref.randn(3, torch.bfloat16, d.T, d.N), torch.empty_like(w)
+    moe.moe_linear(d, x, w, None, off, None, out, None, moe.new_linear_workspace(d))
+    dx = torch.empty_like(x)
+    moe.moe_linear_backward(d, x, w, off, None, dout, dx, dw, None, moe.new_linear_workspace(d, backward=True))
+    for e, a, c in ((0, 0, 2), (251, 500, 600), (253, 600, 630), (255, 630, 700)):
+        part = moe.LinearDims(c - a, d.N, d.K)
+        o64, _, mo, _ = ref.linear(part, x[a:c], w[e:e + 1], None, None, None)
+        ref.check(out[a:c], o64, mo, d.K, "out")
+        want, bound = ref.linear_backward(part, x[a:c], w[e:e + 1], None, None, dout[a:c])
+        for name, g, r, v in (("dx", dx[a:c], want[0], bound[0]), ("dw", dw[e], want[1][0], bound[1][0])):
+            assert not bool((~((g.double() - r).abs() <= v)).any()), name
+    assert not bool(dw[250].any()) and not bool(dw[254].any())
