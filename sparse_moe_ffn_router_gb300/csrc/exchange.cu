@@ -8,7 +8,7 @@
 //
 // All of it is bound by HBM: a token row is read once and kept in registers while its K copies are
 // written, and a token's K rows are read once, side by side, and summed in fp32 in slot order. Measured for 4096
-// tokens of 2048 bf16 by 8 slots (graph replay): spread 25 us = 6.0 TB/s, with dots 49 us = 5.9 TB/s, gather 29 us = 5.8 TB/s, with
+// tokens of 2048 bf16 by 8 slots (graph replay): spread 25 us = 6.0 TB/s, with dots 49 us = 5.9 TB/s, gather 26 us = 6.5 TB/s, with
 // dots 40 us = 4.2 TB/s (issue slots: 24 operations for each element of a row).
 // Sums and dots run in a fixed order, so results are the same bits on every call.
 #include <atomic>
@@ -215,8 +215,7 @@ cudaError_t launch_sort_pairs(const int32_t* ids, int32_t* counts, int32_t* offs
 }
 
 // ---------------------------------------------------------------------------------------
-// spread and gather. TPT threads take a token: a warp where there are tokens enough to fill the GPU,
-// a CTA of 256 where there are few and the latency of one row's loads is what counts.
+// spread and gather. TPT threads take a token: a warp, or a CTA of 256.
 
 constexpr int kSlots = 8;  // K, at most
 
@@ -347,8 +346,10 @@ template <typename T, int VE, bool GATHER, bool DOTS>
 static cudaError_t launch_exchange_t(const ExchangeArgs& a, cudaStream_t s) {
     cudaError_t e;
     const int id = GATHER ? MOE_KERNEL_GATHER_ROWS : MOE_KERNEL_SPREAD_ROWS;
-    // a warp for each token from 16 tokens an SM, where the warps fill the GPU; a CTA below
-    if (a.T >= 16 * a.num_sms)
+    // A CTA to a token where its row has 128 pieces or more, so that half of the threads at least have one: 4864 rows of 2048 bf16 by 8
+    // gathered in 30 against 33 us by warps, 1003 of 1541 by elements in 10.5 against 24; of 256, 10 against 5. With dots the CTA's
+    // sums cost more than they gain from 8 tokens an SM on (608 tokens 8.2 against 10.5 us, 1216 16.4 against 14.4).
+    if (a.H / VE < 128 || (DOTS && a.T >= 8 * a.num_sms))
         MOE_LAUNCH(id, s, (e = launch_pdl(k_exchange<T, VE, 32, GATHER, DOTS>, dim3((a.T + 7) / 8), dim3(256), 0, s, a)));
     else
         MOE_LAUNCH(id, s, (e = launch_pdl(k_exchange<T, VE, 256, GATHER, DOTS>, dim3(a.T), dim3(256), 0, s, a)));

@@ -709,9 +709,10 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
     const bool plain = d.act == MOE_ACT_NONE && vec;  // dz is dout itself
     if (plain || (!a.dx && !a.dw)) a.dz = nullptr;
     cudaError_t e = cudaSuccess;
-    // chunks of 128 rows where they still give every SM four CTAs, else of 32
+    // chunks of 128 rows where they still give every SM a CTA, else of 32 (the whole call, K = 64: 4096 rows of 2048 34.8 against
+    // 41.9 us, 2048 of 2048 25.2 against 27.8, 1024 of 1024 18.9 both)
     const int64_t strips = ((gated ? d.N / 2 : d.N) + 127) / 128;
-    a.chunk = ((int64_t)d.T + 127) / 128 * strips >= 4 * (int64_t)a.num_sms ? 4 * kDzRows : kDzRows;
+    a.chunk = ((int64_t)d.T + 127) / 128 * strips >= a.num_sms ? 4 * kDzRows : kDzRows;
     if (a.dz || a.dbias) {
         MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s,
                    (e = gated ? launch_dz<T, 8, true>(a, pitch, s) : vec ? launch_dz<T, 8, false>(a, pitch, s) : launch_dz<T, 1, false>(a, pitch, s)));
