@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_backward(const NormArg
         if (post || pre) group_sum<3>(sm, &bufs[g.id][turn][0], g);
         const float rs = pre ? rsqrtf(sm[0] * inv_h + d.eps) : 0.f;
         const float ry = post ? rsqrtf(sm[1] * inv_h + d.eps) : 1.f;
-        const float cs = pre ? rs * rs * rs * (sm[2] * inv_h) : 0.f;
+        const float cs = pre ? rs * (rs * (sm[2] * inv_h)) : 0.f;  // (r^3 by itself may leave fp32's range)
         float tval[1] = {1.f}, tslope[1] = {0.f};
         if (token) {
             tval[0] = to_f(tg);
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_backward(const NormArg
                 R::values(ds[i], v);
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    v[e] += rs * (q[e] * gm[e]) - sv[e] * cs;
+                    v[e] = fmaf(rs, fmaf(-sv[e], cs, q[e] * gm[e]), v[e]);
                     acc_pre[i][e] = fmaf(q[e] * sv[e], rs, acc_pre[i][e]);
                     o[e] = d.residual_scale * v[e];
                 }
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_backward(const NormArg
         if (t + step < d.T) load(t + step);
         if (post || token) group_sum<2>(more, &bufs[g.id][turn][3], g);
         if (token && a.dgate && g.tid == 0) ((T*)a.dgate)[t] = from_f<T>(d.branch_scale * more[1] * tslope[0]);
-        const float cy = post ? ry * ry * ry * (more[0] * inv_h) : 0.f;
+        const float cy = post ? ry * (ry * (more[0] * inv_h)) : 0.f;
         if (a.dy)
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_backward(const NormArg
                     float yv[VE];
                     R::values(yy[i], yv);
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) yv[e] = post ? ry * gs[i][e] - yv[e] * cy : gs[i][e];
+                    for (int e = 0; e < VE; ++e) yv[e] = post ? ry * fmaf(-yv[e], cy, gs[i][e]) : gs[i][e];
                     row_put<T, VE>((T*)a.dy + row, col[i], H, whole[i], R::pack(yv));
                 }
     }

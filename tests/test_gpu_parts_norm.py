@@ -161,6 +161,24 @@ def test_eps_zero_rows_and_far_values(eps, scale):
     ref.check(xn, xn64, mag * rs + xn64.abs() * (1 + rs * rs * (mag * s64.abs()).mean(1, keepdim=True)), 512, "xn")
 
 
+@pytest.mark.parametrize("eps,scale", [(1e-30, 0.0), (0.0, 1e-15), (0.0, 1e15), (1e-6, 1e-12)])
+def test_gradients_of_zero_rows_and_far_values(eps, scale):
+    """Where the cube of a norm's factor leaves fp32's range and the gradients do not."""
+    d = moe.NormDims(4, 512, dtype=moe.FP32, eps=eps)
+    y, s = ref.randn(1, torch.float32, 4, 512, scale=scale), ref.randn(2, torch.float32, 4, 512, scale=scale)
+    dxn = ref.randn(3, torch.float32, 4, 512)
+    dres, dy = torch.empty_like(y), torch.empty_like(y)
+    moe.moe_norm_residual_backward(d, None, dxn, s, y, None, None, None, dres, None, None, None, None, moe.new_norm_workspace(d))
+    moe.moe_norm_residual_backward(d, dxn, None, s, y, None, None, None, None, dy, None, None, None, moe.new_norm_workspace(d))
+    for got, v, what in ((dres, s, "dresidual"), (dy, y, "dy")):
+        v64 = v.double().requires_grad_()
+        want, = torch.autograd.grad(ref.norm(v64, None, d.eps), v64, dxn.double())
+        with torch.no_grad():
+            r = 1 / (v64.square().mean(1, keepdim=True) + d.eps).sqrt()
+            a = dxn.double().abs()
+            ref.check(got, want, r * a + v64.abs() * r ** 3 * (a * v64.abs()).mean(1, keepdim=True), 512, what)
+
+
 def test_no_rows():
     d = dims(0, 64, moe.BF16, (moe.GATE_CHANNEL, moe.ACT_NONE))
     z, h = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), torch.full((64,), 7.0, dtype=torch.bfloat16, device="cuda")
