@@ -507,7 +507,11 @@ __global__ void __launch_bounds__(256) k_dbias(const LinView a) {
     __shared__ int off[kLinMaxE + 1];
     grid_dep_wait();
     grid_dep_launch();
-    for (int e = threadIdx.x; e <= a.E; e += 256) off[e] = a.offsets ? min(max(a.offsets[e], 0), a.T) : e ? a.T : 0;
+    for (int e = threadIdx.x; e <= a.E; e += 256) {
+        const int o = a.offsets ? a.offsets[e] : e ? a.T : 0;
+        off[e] = min(max(o, 0), a.T);
+        if (off[e] != o || (a.offsets && e && o < a.offsets[e - 1])) atomicOr(a.err, ERR_BAD_ROUTE);
+    }
     __syncthreads();
     lin_dbias<T>(a, off, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8);
 }

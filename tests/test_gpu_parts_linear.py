@@ -232,6 +232,21 @@ def test_offsets_out_of_order_are_flagged_for_few_rows():
         assert moe.moe_last_device_error(ws) == 7 and moe.moe_last_device_error(ws) == 0
 
 
+@pytest.mark.parametrize("T", [64, 700])
+@pytest.mark.parametrize("wanted", ["dx", "dw", "dbias"])
+def test_offsets_out_of_order_are_flagged_by_every_gradient(T, wanted):
+    d = moe.LinearDims(T, 64, 64, E=3, act=moe.ACT_SILU)
+    x, w, b, _ = inputs(d, residual=False)
+    ws, z, dout = moe.new_linear_workspace(d, backward=True), ref.randn(7, x.dtype, T, 64), ref.randn(8, x.dtype, T, 64)
+    out = {"dx": torch.zeros_like(x), "dw": torch.zeros_like(w), "dbias": torch.zeros_like(b)}
+    one = [out[k] if k == wanted else None for k in out]
+    for off in ([0, 40, 20, T], [0, 10, 20, T + 1], [-1, 10, 20, T], [2 ** 31 - 1, -2 ** 31, 5, 6]):
+        moe.moe_linear_backward(d, x, w, torch.tensor(off, dtype=torch.int32, device="cuda"), z, dout, *one, ws)
+        assert moe.moe_last_device_error(ws) == 7 and moe.moe_last_device_error(ws) == 0
+    moe.moe_linear_backward(d, x, w, torch.tensor([0, 10, 20, T], dtype=torch.int32, device="cuda"), z, dout, *one, ws)
+    assert moe.moe_last_device_error(ws) == 0
+
+
 @pytest.mark.parametrize("T", [1, 2, 8, 9, 40, 64, 65])
 def test_residual_may_be_the_result_of_every_kernel(T):
     for act, N in ((moe.ACT_NONE, 2048), (moe.ACT_SWIGLU, 1024)):
