@@ -41,7 +41,8 @@ __device__ __forceinline__ uint32_t at64(int row, int chunk) { return (uint32_t)
 __device__ __forceinline__ uint32_t at32(int row, int chunk) { return (uint32_t)(row * 32 + ((chunk ^ ((row >> 2) & 1)) << 4)); }
 
 // Rows that do not start on 16 bytes: a warp's buffer of 32 rows of kWide features to memory, a row (two of
-// 16 features) at a time, lanes side by side. row0, ld: of the first row, between rows; f0: its first feature, of F; rows: how many exist.
+// 16 features) at a time, lanes side by side. p: the first row's element f0 in memory, ld: elements from row to row; F: features of
+// a row; rows: how many exist.
 template <int kWide>
 __device__ __forceinline__ uint32_t feature_at(int row, int f) { return (kWide == 16 ? at32(row, f >> 3) : at64(row, f >> 3)) + 2 * (f & 7); }
 template <int kWide>
@@ -55,6 +56,7 @@ __device__ __forceinline__ void rows_out(uint32_t buf, uint16_t* p, int64_t ld, 
         if (f0 + f < F) p[(int64_t)r * ld + f] = v;
     }
 }
+
 // A warp's part of a tile: 32 accumulator lanes (q), 32 columns at a time. row0: the result's row of the tile's
 // first column; fl: the CTA's first feature.
 template <typename T, int MODE, bool GATED>

@@ -91,6 +91,13 @@ def test_forward_and_backward(dtype, T, H, gate):
             ref.check(dg, got["g"], m, 2 * H + T, "dgate")
 
 
+@pytest.mark.parametrize("T,H,dtype,gate", [(5003, 1003, moe.BF16, 3), (2500, 65, moe.FP16, 4), (3100, 2048, moe.BF16, 5), (4001, 96, moe.FP32, 3), (700, 8190, moe.FP32, 4),
+                                            (640, 8187, moe.BF16, 1), (5200, 256, moe.FP16, 0), (1300, 6152, moe.BF16, 2)])
+def test_many_rows(T, H, dtype, gate):
+    """More rows than the CTAs hold at once, several rows on their way, rows that begin anywhere."""
+    test_forward_and_backward(dtype, T, H, GATES[gate])
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 def test_optional_parts(dtype):
     """What is left out is as if it were zeros (results: not written), and the rest keeps its bits."""
@@ -136,6 +143,28 @@ def test_results_over_their_inputs():
     moe.moe_norm_residual_backward(d, ds, dxn, s, y, g, gp, gq, dres, dy, None, None, None, ws)
     moe.moe_norm_residual_backward(d, ds, dxn, s, y, g, gp, gq, ds, dxn, None, None, None, ws)
     assert torch.equal(ds, dres) and torch.equal(dxn, dy)
+
+
+@pytest.mark.parametrize("H", [64, 65, 1003])
+@pytest.mark.parametrize("dtype", list(DT))
+def test_rows_do_not_reach_one_another(dtype, H):
+    """A row of NaN beside rows that share its 16-byte pieces of memory."""
+    d = dims(40, H, dtype, (moe.GATE_FULL, moe.ACT_SIGMOID))
+    y, r, g, gp, gq = inputs(d)
+    ds, dxn = ref.randn(6, y.dtype, 40, H), ref.randn(7, y.dtype, 40, H)
+
+    def run():
+        out = [torch.empty_like(y) for _ in range(5)]
+        moe.moe_norm_residual(d, y, r, g, gp, gq, out[0], out[1])
+        moe.moe_norm_residual_backward(d, ds, dxn, r, y, g, gp, gq, *out[2:], None, None, moe.new_norm_workspace(d))
+        return out
+
+    clean = run()
+    for t in (y, r, g, ds, dxn):
+        t[17] = float("nan")
+    for a, b in zip(run(), clean):
+        assert bool(a[17].isnan().all())
+        assert torch.equal(torch.cat((a[:17], a[18:])), torch.cat((b[:17], b[18:])))
 
 
 def test_agrees_with_rmsnorm():
