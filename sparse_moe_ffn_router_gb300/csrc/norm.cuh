@@ -22,7 +22,7 @@
 // into registers before it works on the current one; backward, which has up to five tensors to read, a thread copies its pieces of the next one
 // to three rows into shared memory, where it alone reads them. A thread's 16-byte vectors are aligned in memory whatever the row
 // length: the rows of a group all begin at the same place within a vector (their numbers are equal mod 8), so its columns
-// stay the same from row to row, and only a row's first and last vector are written (forward: moved) element by element.
+// stay the same from row to row, and only a row's first and last vector are masked when read and written element by element.
 //
 // Measured (graph replay): forward 4096 x 2048 bf16 14.3 us = 4.7 TB/s, with a whole sigmoid gate 16.7 us = 5.0 TB/s (issue slots 73 %);
 // backward 4096 x 2048 29.5 us, 32768 x 2048 158 us = 5.1 TB/s, 4096 x 8192 91 us, 4096 x 2048 fp32 37 us = 5.4 TB/s: 519 instructions a warp
@@ -148,7 +148,15 @@ __device__ __forceinline__ void row_put(T* p, int c, int H, bool whole, const Ra
     }
 }
 
-template <typename T, int VE, int VPT, int GATE>
+// Zeros in place of the elements outside the row.
+template <int VE>
+__device__ __forceinline__ void row_mask(Raw& r, int c, int H) {
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+        if ((unsigned)(c + e) >= (unsigned)H) r.w[e * 4 / VE] &= VE == 4 ? 0u : e & 1 ? 0x0000ffffu : 0xffff0000u;
+}
+
+template <typename T, int VE, int VPT, int GATE, bool ODD>
 __global__ void __launch_bounds__(kNormThreads, VPT == 1 ? 2 : 1) k_norm(const NormArgs a, int tpr) {
     typedef RawOf<T> R;
     __shared__ __align__(16) float bufs[16][2][2][20];
@@ -159,7 +167,7 @@ __global__ void __launch_bounds__(kNormThreads, VPT == 1 ? 2 : 1) k_norm(const N
     const int H = d.H, first = blockIdx.x * g.groups + g.id, step = gridDim.x * g.groups;
     constexpr bool full = GATE == kGateAll, channel = GATE == kGateColumn;
     const bool post = (d.flags & MOE_NORM_POST) != 0;
-    const int mis = (int)((int64_t)first * H % VE);  // the rows' place within a vector
+    const int mis = ODD ? (int)((int64_t)first * H % VE) : 0;  // the rows' place within a vector
     int col[VPT];
     bool live[VPT], whole[VPT];
     Raw y[VPT], r[VPT], ga[VPT];
@@ -168,31 +176,31 @@ __global__ void __launch_bounds__(kNormThreads, VPT == 1 ? 2 : 1) k_norm(const N
     for (int i = 0; i < VPT; ++i) {
         col[i] = (g.tid + i * g.threads) * VE - mis;
         live[i] = col[i] < H;
-        whole[i] = col[i] >= 0 && col[i] + VE <= H;
+        whole[i] = !ODD || (col[i] >= 0 && col[i] + VE <= H);
     }
+    const int last = d.T - VE;  // (from here on a row's last vector may reach past the tensor)
     auto load = [&](int t) {
         const int64_t row = (int64_t)t * H;
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
             if (live[i]) {
-                y[i] = row_get<T, VE>((const T*)a.y + row, col[i], H, whole[i]);
-                if (a.residual) r[i] = row_get<T, VE>((const T*)a.residual + row, col[i], H, whole[i]);
-                if (full) ga[i] = row_get<T, VE>((const T*)a.gate + row, col[i], H, whole[i]);
+                const bool vec = whole[i] || t < last;
+                y[i] = row_get<T, VE>((const T*)a.y + row, col[i], H, vec);
+                if (a.residual) r[i] = row_get<T, VE>((const T*)a.residual + row, col[i], H, vec);
+                if (full) ga[i] = row_get<T, VE>((const T*)a.gate + row, col[i], H, vec);
             }
         if (GATE == kGateRow && d.gate == MOE_GATE_TOKEN) tg = ((const T*)a.gate)[t];
     };
     if (first < d.T) load(first);
-    // tensors [H]: in vectors where rows are aligned, else by elements
-    const bool aligned = mis == 0 && H % VE == 0;
     Raw gp[VPT], gq[VPT];
     float gc[VPT][VE];  // act(gate) of a channel gate
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
         if (live[i]) {
-            if (post && a.gamma_post) gp[i] = row_get<T, VE>((const T*)a.gamma_post, col[i], H, aligned);
-            if (a.xn && a.gamma_pre) gq[i] = row_get<T, VE>((const T*)a.gamma_pre, col[i], H, aligned);
+            if (post && a.gamma_post) gp[i] = row_get<T, VE>((const T*)a.gamma_post, col[i], H, !ODD);
+            if (a.xn && a.gamma_pre) gq[i] = row_get<T, VE>((const T*)a.gamma_pre, col[i], H, !ODD);
             if (channel) {
-                R::values(row_get<T, VE>((const T*)a.gate, col[i], H, aligned), gc[i]);
+                R::values(row_get<T, VE>((const T*)a.gate, col[i], H, !ODD), gc[i]);
                 gate_values<T, VE>(d.gate_act, gc[i]);
             }
         }
@@ -215,6 +223,11 @@ __global__ void __launch_bounds__(kNormThreads, VPT == 1 ? 2 : 1) k_norm(const N
         for (int i = 0; i < VPT; ++i)
             if (live[i]) {
                 float f[VE];
+                if (!whole[i]) {  // (another row's elements in the same 16 bytes)
+                    row_mask<VE>(y[i], col[i], H);
+                    if (a.residual) row_mask<VE>(r[i], col[i], H);
+                    if (full) row_mask<VE>(ga[i], col[i], H);
+                }
                 rr[i] = r[i];
                 R::values(y[i], s[i]);
                 if (post) {
@@ -330,14 +343,6 @@ __device__ __forceinline__ void back_sums(float (&v)[kBackSums], float* buf, con
     for (int k = 0; k < kBackSums; ++k) v[k] = __shfl_sync(0xffffffffu, y, 4 * k);
 }
 
-// Zeros in place of the elements outside the row.
-template <int VE>
-__device__ __forceinline__ void row_mask(Raw& r, int c, int H) {
-#pragma unroll
-    for (int e = 0; e < VE; ++e)
-        if ((unsigned)(c + e) >= (unsigned)H) r.w[e * 4 / VE] &= VE == 4 ? 0u : e & 1 ? 0x0000ffffu : 0xffff0000u;
-}
-
 // How a CTA of the backward pass uses its shared memory: a thread's constants (gammas, channel gate), its copies of rows, the
 // groups' sums.
 struct BackPlan {
@@ -345,7 +350,7 @@ struct BackPlan {
     uint32_t ring, bufs, bytes;      // where the copies and the sums begin, all of it
 };
 
-template <typename T, int VE, int VPT, int GATE>
+template <typename T, int VE, int VPT, int GATE, bool ODD>
 __global__ void __launch_bounds__(kNormThreads, 1)
     k_norm_backward(const NormArgs a, const BackPlan plan) {
     typedef RawOf<T> R;
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(kNormThreads, 1)
     constexpr bool kHeld = VPT == 1;  // a row's values stay in registers from one pass over it to the other
     const bool post = (d.flags & MOE_NORM_POST) != 0, pre = a.dxn != nullptr;
     const bool token = GATE == kGateRow && d.gate == MOE_GATE_TOKEN;
-    const int mis = (int)((int64_t)first * H % VE);
+    const int mis = ODD ? (int)((int64_t)first * H % VE) : 0;
     const uint32_t smem = (uint32_t)__cvta_generic_to_shared(back_smem);
     const uint32_t pieces = (uint32_t)blockDim.x * 16u;  // one of every thread
     const uint32_t consts = smem + threadIdx.x * 16u, ring = smem + plan.ring + threadIdx.x * 16u;
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(kNormThreads, 1)
     for (int i = 0; i < VPT; ++i) {
         col[i] = (g.tid + i * g.threads) * VE - mis;
         live[i] = col[i] < H;
-        whole[i] = col[i] >= 0 && col[i] + VE <= H;
+        whole[i] = !ODD || (col[i] >= 0 && col[i] + VE <= H);
     }
     const int last = d.T - VE;  // (from here on a row's last vector may reach past the tensor)
     auto fetch = [&](int t, int stage) {
@@ -397,7 +402,6 @@ __global__ void __launch_bounds__(kNormThreads, 1)
         copies_commit();
     };
     for (int k = 0; k < plan.stages; ++k) fetch(first + k * step, k);
-    const bool aligned = mis == 0 && H % VE == 0;
     float acc_post[VPT][VE], acc_pre[VPT][VE], acc_gate[VPT][VE];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -409,11 +413,11 @@ __global__ void __launch_bounds__(kNormThreads, 1)
         Raw gp = R::pack(one), gq = gp;
         const uint32_t at = consts + (uint32_t)(i * kConsts) * pieces;
         if (live[i]) {
-            if (post && a.gamma_post) gp = row_get<T, VE>((const T*)a.gamma_post, col[i], H, aligned);
-            if (pre && a.gamma_pre) gq = row_get<T, VE>((const T*)a.gamma_pre, col[i], H, aligned);
+            if (post && a.gamma_post) gp = row_get<T, VE>((const T*)a.gamma_post, col[i], H, !ODD);
+            if (pre && a.gamma_pre) gq = row_get<T, VE>((const T*)a.gamma_pre, col[i], H, !ODD);
             if (channel) {
                 float gc[VE];
-                R::values(row_get<T, VE>((const T*)a.gate, col[i], H, aligned), gc);
+                R::values(row_get<T, VE>((const T*)a.gate, col[i], H, !ODD), gc);
                 gate_values<T, VE>(d.gate_act, gc);
 #pragma unroll
                 for (int e = 0; e < VE; e += 4)
@@ -615,7 +619,7 @@ __global__ void __launch_bounds__(kNormThreads, 1)
         for (int i = 0; i < VPT; ++i)
             if (live[i]) {
                 float ge[VE], slope[VE];
-                R::values(row_get<T, VE>((const T*)a.gate, col[i], H, aligned), ge);
+                R::values(row_get<T, VE>((const T*)a.gate, col[i], H, !ODD), ge);
                 gate_slopes<T, VE>(d.gate_act, ge, slope);
 #pragma unroll
                 for (int e = 0; e < VE; ++e) acc_gate[i][e] *= d.branch_scale * slope[e];
@@ -705,18 +709,18 @@ static int norm_grid(const NormArgs& a, int groups, int most) {
 }
 
 // Vectors that cover any row of H columns, wherever in a vector it begins; vectors and threads of a row.
-template <typename T, int VE, int VPT, int GATE>
+template <typename T, int VE, int VPT, int GATE, bool ODD>
 static cudaError_t launch_norm_t(const NormArgs& a, cudaStream_t s, int nv) {
     const int tpr = max(32, ((nv + VPT - 1) / VPT + 31) / 32 * 32);
     int groups = VPT == 1 ? max(1, min(16, 512 / tpr)) : 1;
     while (groups > 1 && a.d.T < groups * a.num_sms) groups /= 2;  // (few rows: a CTA each)
     const int blocks = norm_grid<VE>(a, groups, a.num_sms * (VPT > 1 ? 1 : 2));
     cudaError_t e;
-    MOE_LAUNCH(MOE_KERNEL_NORM, s, (e = launch_pdl(k_norm<T, VE, VPT, GATE>, dim3(blocks), dim3(tpr * groups), 0, s, a, tpr)));
+    MOE_LAUNCH(MOE_KERNEL_NORM, s, (e = launch_pdl(k_norm<T, VE, VPT, GATE, ODD>, dim3(blocks), dim3(tpr * groups), 0, s, a, tpr)));
     return e;
 }
 
-template <typename T, int VE, int VPT, int GATE>
+template <typename T, int VE, int VPT, int GATE, bool ODD>
 static cudaError_t launch_norm_backward_t(const NormArgs& a, cudaStream_t s, int nv) {
     constexpr uint32_t kRoom = 227 * 1024;
     BackPlan p = {};
@@ -740,42 +744,45 @@ static cudaError_t launch_norm_backward_t(const NormArgs& a, cudaStream_t s, int
     cudaGetDevice(&dev);
     cudaError_t e;
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(k_norm_backward<T, VE, VPT, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRoom);
+        e = cudaFuncSetAttribute(k_norm_backward<T, VE, VPT, GATE, ODD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRoom);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
     NormArgs b = a;
     const bool columns = a.dgamma_post || a.dgamma_pre || (a.dgate && a.d.gate == MOE_GATE_CHANNEL);
     if (!columns) b.part = nullptr;
-    MOE_LAUNCH(MOE_KERNEL_NORM_BACKWARD, s, (e = launch_pdl(k_norm_backward<T, VE, VPT, GATE>, dim3(blocks), dim3(p.tpr * p.groups), p.bytes, s, b, p)));
+    MOE_LAUNCH(MOE_KERNEL_NORM_BACKWARD, s, (e = launch_pdl(k_norm_backward<T, VE, VPT, GATE, ODD>, dim3(blocks), dim3(p.tpr * p.groups), p.bytes, s, b, p)));
     if (e == cudaSuccess && columns)
         MOE_LAUNCH(MOE_KERNEL_NORM_BACKWARD, s, (e = launch_pdl(k_norm_columns<T>, dim3((a.d.H + 31) / 32, GATE == kGateColumn ? 3 : 2), dim3(512), 0, s, b, blocks)));
     return e;
 }
 
-template <typename T, int VE, int VPT>
+template <typename T, int VE, int VPT, bool ODD>
 static cudaError_t launch_norm_g(const NormArgs& a, cudaStream_t s, bool backward, int nv) {
     if (backward)
-        return a.d.gate == MOE_GATE_FULL      ? launch_norm_backward_t<T, VE, VPT, kGateAll>(a, s, nv)
-               : a.d.gate == MOE_GATE_CHANNEL ? launch_norm_backward_t<T, VE, VPT, kGateColumn>(a, s, nv)
-                                              : launch_norm_backward_t<T, VE, VPT, kGateRow>(a, s, nv);
-    return a.d.gate == MOE_GATE_FULL      ? launch_norm_t<T, VE, VPT, kGateAll>(a, s, nv)
-           : a.d.gate == MOE_GATE_CHANNEL ? launch_norm_t<T, VE, VPT, kGateColumn>(a, s, nv)
-                                          : launch_norm_t<T, VE, VPT, kGateRow>(a, s, nv);
+        return a.d.gate == MOE_GATE_FULL      ? launch_norm_backward_t<T, VE, VPT, kGateAll, ODD>(a, s, nv)
+               : a.d.gate == MOE_GATE_CHANNEL ? launch_norm_backward_t<T, VE, VPT, kGateColumn, ODD>(a, s, nv)
+                                              : launch_norm_backward_t<T, VE, VPT, kGateRow, ODD>(a, s, nv);
+    return a.d.gate == MOE_GATE_FULL      ? launch_norm_t<T, VE, VPT, kGateAll, ODD>(a, s, nv)
+           : a.d.gate == MOE_GATE_CHANNEL ? launch_norm_t<T, VE, VPT, kGateColumn, ODD>(a, s, nv)
+                                          : launch_norm_t<T, VE, VPT, kGateRow, ODD>(a, s, nv);
 }
 
-// Vectors of a thread: the fewest with which 512 threads cover the row. (A row of 8192 columns less a few that begins inside
-// a vector takes one vector more than 8192 do.)
+// Vectors of a thread: the fewest with which 512 threads cover the row. ODD: rows begin anywhere in a vector. (A row of 8192 columns
+// less a few then takes one vector more than 8192 do.)
 template <typename T>
 static cudaError_t launch_norm_any(const NormArgs& a, cudaStream_t s, bool backward) {
     constexpr int VE = 16 / (int)sizeof(T);
-    const int nv = a.d.H % VE ? (a.d.H + 2 * VE - 2) / VE : a.d.H / VE, vpt = (nv + kNormThreads - 1) / kNormThreads;
-    if (vpt == 1) return launch_norm_g<T, VE, 1>(a, s, backward, nv);
-    if (vpt == 2) return launch_norm_g<T, VE, 2>(a, s, backward, nv);
-    if constexpr (VE == 8)
-        return launch_norm_g<T, VE, 3>(a, s, backward, nv);
-    else
-        return vpt <= 4 ? launch_norm_g<T, VE, 4>(a, s, backward, nv) : launch_norm_g<T, VE, 5>(a, s, backward, nv);
+    if (a.d.H % VE == 0) {
+        const int nv = a.d.H / VE;
+        if (nv <= kNormThreads) return launch_norm_g<T, VE, 1, false>(a, s, backward, nv);
+        if (nv <= 2 * kNormThreads) return launch_norm_g<T, VE, 2, false>(a, s, backward, nv);
+        if constexpr (VE == 4) return launch_norm_g<T, VE, 4, false>(a, s, backward, nv);
+    }
+    const int nv = (a.d.H + 2 * VE - 2) / VE;
+    if (nv <= kNormThreads) return launch_norm_g<T, VE, 1, true>(a, s, backward, nv);
+    if (nv <= 2 * kNormThreads) return launch_norm_g<T, VE, 2, true>(a, s, backward, nv);
+    return launch_norm_g<T, VE, VE == 8 ? 3 : 5, true>(a, s, backward, nv);
 }
 
 }  // namespace moe
