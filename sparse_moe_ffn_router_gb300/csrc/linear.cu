@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
 // ---------------------------------------------------------------------------------------
 // dz = act'(z) * dout, and the column sums of it for the bias. Bound by HBM (32768 rows of 1024, swiglu: 28 us = 5.9 TB/s) until
-// GELU's slope and the sums take the issue slots (4096 rows of 8192 with both: 43 us = 4.7 TB/s). A CTA takes a chunk of 32 or 128 rows and 128
+// GELU's slope and the sums take the issue slots (4096 rows of 8192 with both: 43 us = 4.7 TB/s). A CTA takes a chunk of 4, 32 or 128 rows and 128
 // columns (for swiglu 128 gate columns and the matching up columns); 16 threads side by side hold 8 columns
 // each, 16 rows at a time. Sums are of dz before its rounding, row block by row block: those of the rows of
 // expert e in chunk c go to part[c + e], a place of their own as chunks and experts follow one another.
@@ -713,10 +713,11 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
     const bool plain = d.act == MOE_ACT_NONE && vec;  // dz is dout itself
     if (plain || (!a.dx && !a.dw)) a.dz = nullptr;
     cudaError_t e = cudaSuccess;
-    // chunks of 128 rows where they still give every SM a CTA, else of 32 (the whole call, K = 64: 4096 rows of 2048 34.8 against
-    // 41.9 us, 2048 of 2048 25.2 against 27.8, 1024 of 1024 18.9 both)
+    // chunks of 128 rows where they still give every SM a CTA, else of 32 (the whole call: 16384 rows of 1024, K = 64, 61 against 79 us,
+    // 2984 of 4868, K = 424, 64 against 71; 1024 of 1024 17.4 both)
     const int64_t strips = ((gated ? d.N / 2 : d.N) + 127) / 128;
-    a.chunk = ((int64_t)d.T + 127) / 128 * strips >= a.num_sms ? 4 * kDzRows : kDzRows;
+    a.chunk = dz_rows(d.T, d.E);
+    if (a.chunk == 32 && ((int64_t)d.T + 127) / 128 * strips >= a.num_sms) a.chunk = 128;
     if (a.dz || a.dbias) {
         MOE_LAUNCH(MOE_KERNEL_LINEAR_BACKWARD, s,
                    (e = gated ? launch_dz<T, 8, true>(a, pitch, s) : vec ? launch_dz<T, 8, false>(a, pitch, s) : launch_dz<T, 1, false>(a, pitch, s)));

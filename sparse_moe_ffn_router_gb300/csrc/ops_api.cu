@@ -93,7 +93,10 @@ bool linear_shape(const moe_linear_dims& d) {
            !(d.act == MOE_ACT_SWIGLU && d.N % 32) && (int64_t)d.T * d.N < most && (int64_t)d.T * d.K < most && (int64_t)d.N * d.K < most / d.E;
 }
 size_t dz_bytes(const moe_linear_dims& d) { return align256((size_t)d.T * ((d.N + 7) / 8 * 8) * 2); }
-size_t part_bytes(const moe_linear_dims& d) { return align256(((size_t)(d.T + kDzRows - 1) / kDzRows + d.E) * d.N * 4); }
+size_t part_bytes(const moe_linear_dims& d) {
+    const size_t rows = dz_rows(d.T, d.E);
+    return align256(((d.T + rows - 1) / rows + d.E) * d.N * 4);
+}
 
 }  // namespace
 

@@ -325,6 +325,22 @@ def test_many_rows_in_chunks_of_128(T, N, counts, act):
     check_backward(d, x, w, off, ref.randn(5, x.dtype, d.T, N))
 
 
+@pytest.mark.parametrize("counts", [[0, 1, 3, 0, 2] * 30, [8] * 64, [0] * 255 + [5], [1] * 256, [513] + [0] * 63, [7, 0]])
+@pytest.mark.parametrize("N,act", [(317, moe.ACT_SILU), (256, moe.ACT_SWIGLU)])
+def test_experts_with_a_handful_of_rows(N, act, counts):
+    """Row counts up to which the elementwise pass of the way back takes four rows at once, and the sums' place behind its workspace."""
+    off = offsets_of(counts)
+    d = moe.LinearDims(int(off[-1]) + 2, N, 72, E=len(counts), act=act)
+    x, w, b, _ = inputs(d, residual=False)
+    z = ref.randn(5, x.dtype, d.T, N)
+    check_backward(d, x, w, off, z)
+    size = moe.new_linear_workspace(d, backward=True).numel()
+    room = torch.zeros(size + (1 << 20), dtype=torch.uint8, device="cuda")
+    room[size:] = 0x5A
+    moe.moe_linear_backward(d, x, w, off, z, torch.ones(d.T, N // 2 if act == moe.ACT_SWIGLU else N, dtype=x.dtype, device="cuda"), None, None, torch.empty_like(b), room[:size])
+    assert moe.moe_last_device_error(room[:size]) == 0 and bool((room[size:] == 0x5A).all())
+
+
 def test_results_past_32_bits_of_elements():
     """Rows and matrices that begin behind element 2^31."""
     d = moe.LinearDims(32800, 65560, 64, act=moe.ACT_RELU)
