@@ -292,7 +292,7 @@ moe_status moe_sort_pairs(int32_t T, int32_t K, int32_t E, const int32_t* ids, i
  * its place are left as they were. Sums are in fp32 in slot order, dots in fp32, each result rounded once.
  * out may be the same buffer as residual; otherwise results overlap no input. An entry of inv that is no place
  * in [0, T*K) counts as dropped. dtype: bf16, fp16 or fp32; 1 <= K <= 8, 1 <= H <= 65536, T * K <= 2^31 - 2^16;
- * rows move fastest where H elements are a multiple of 16 bytes. T = 0 is a no-op. */
+ * rows move fastest where H elements are a multiple of 16 bytes (then of 8, of 4). T = 0 is a no-op. */
 moe_status moe_dispatch(int32_t dtype, int32_t T, int32_t K, int32_t H, const void* x, const int32_t* inv,
                         const float* topk_w, void* rows, void* stream);
 moe_status moe_dispatch_backward(int32_t dtype, int32_t T, int32_t K, int32_t H, const void* drows, const int32_t* inv,

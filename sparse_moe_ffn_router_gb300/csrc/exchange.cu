@@ -9,7 +9,8 @@
 // All of it is bound by HBM: a token row is read once and kept in registers while its K copies are
 // written, and a token's K rows are read once, side by side, and summed in fp32 in slot order. Measured for 4096
 // tokens of 2048 bf16 by 8 slots (graph replay): spread 25 us = 6.0 TB/s, with dots 49 us = 5.9 TB/s, gather 26 us = 6.5 TB/s, with
-// dots 40 us = 4.2 TB/s (issue slots: 24 operations for each element of a row).
+// dots 40 us = 4.2 TB/s (issue slots: 24 operations for each element of a row). Rows of 2044 (8 bytes at a time) 27, 61, 35, 42 us, of 2046
+// (4 bytes) 37, 89, 43, 83, of 2045 (elements) 45, 129, 76, 142.
 // Sums and dots run in a fixed order, so results are the same bits on every call.
 #include <atomic>
 
@@ -245,9 +246,36 @@ __device__ __forceinline__ void store_dots(float (&v)[kSlots], float* dst, int K
     }
 }
 
-// What a thread moves at once: 16 bytes, or one element where rows do not start on 16 bytes.
+// What a thread moves at once: 16 bytes, or what rows start on: 8, 4, one element.
+template <int BYTES>
+struct Words;
+template <>
+struct Words<8> {
+    typedef uint2 type;
+};
+template <>
+struct Words<4> {
+    typedef uint32_t type;
+};
 template <typename T, int VE>
-struct Piece {
+struct Piece {  // VE elements of fewer than 16 bytes
+    typedef typename Words<VE * (int)sizeof(T)>::type type;
+    static __device__ __forceinline__ type get(const T* p) { return *reinterpret_cast<const type*>(p); }
+    static __device__ __forceinline__ void put(T* p, const type& r) { *reinterpret_cast<type*>(p) = r; }
+    static __device__ __forceinline__ void values(const type& r, float (&f)[VE]) {
+        const Vec<T, VE> v = *reinterpret_cast<const Vec<T, VE>*>(&r);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) f[i] = to_f(v.v[i]);
+    }
+    static __device__ __forceinline__ type pack(const float (&f)[VE]) {
+        Vec<T, VE> v;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v.v[i] = from_f<T>(f[i]);
+        return *reinterpret_cast<const type*>(&v);
+    }
+};
+template <typename T, int VE>
+struct PieceOf16 {
     typedef Raw type;
     static __device__ __forceinline__ Raw get(const T* p) {
         const uint4 v = *reinterpret_cast<const uint4*>(p);
@@ -257,6 +285,12 @@ struct Piece {
     static __device__ __forceinline__ void values(const Raw& r, float (&f)[VE]) { RawOf<T>::values(r, f); }
     static __device__ __forceinline__ Raw pack(const float (&f)[VE]) { return RawOf<T>::pack(f); }
 };
+template <>
+struct Piece<bf16, 8> : PieceOf16<bf16, 8> {};
+template <>
+struct Piece<fp16, 8> : PieceOf16<fp16, 8> {};
+template <>
+struct Piece<float, 4> : PieceOf16<float, 4> {};
 template <typename T>
 struct Piece<T, 1> {
     typedef T type;
@@ -348,8 +382,11 @@ static cudaError_t launch_exchange_t(const ExchangeArgs& a, cudaStream_t s) {
     const int id = GATHER ? MOE_KERNEL_GATHER_ROWS : MOE_KERNEL_SPREAD_ROWS;
     // A CTA to a token where its row has 128 pieces or more, so that half of the threads at least have one: 4864 rows of 2048 bf16 by 8
     // gathered in 30 against 33 us by warps, 1003 of 1541 by elements in 10.5 against 24; of 256, 10 against 5. With dots the CTA's
-    // sums cost more than they gain from 8 tokens an SM on (608 tokens 8.2 against 10.5 us, 1216 16.4 against 14.4).
-    if (a.H / VE < 128 || (DOTS && a.T >= 8 * a.num_sms))
+    // sums cost more than they gain from 8 tokens an SM on (608 tokens 8.2 against 10.5 us, 1216 16.4 against 14.4). Shorter rows too
+    // while there are few tokens, whose warps would be on a few SMs (8 tokens of 1000 bf16 by 8 1.9 against 3.9 us, 600 of 512 2.6 against
+    // 2.9 and with dots 5.9 against 4.2, 1200 3.4 against 3.1).
+    const bool warps = a.H / VE < 128 ? a.T >= (DOTS ? 2 : 4) * a.num_sms : DOTS && a.T >= 8 * a.num_sms;
+    if (warps)
         MOE_LAUNCH(id, s, (e = launch_pdl(k_exchange<T, VE, 32, GATHER, DOTS>, dim3((a.T + 7) / 8), dim3(256), 0, s, a)));
     else
         MOE_LAUNCH(id, s, (e = launch_pdl(k_exchange<T, VE, 256, GATHER, DOTS>, dim3(a.T), dim3(256), 0, s, a)));
@@ -361,6 +398,10 @@ static cudaError_t launch_exchange(const ExchangeArgs& a, cudaStream_t s) {
     constexpr int VE = 16 / (int)sizeof(T);
     if (a.H % VE == 0)
         return a.dots ? launch_exchange_t<T, VE, GATHER, true>(a, s) : launch_exchange_t<T, VE, GATHER, false>(a, s);
+    if (a.H % (VE / 2) == 0)
+        return a.dots ? launch_exchange_t<T, VE / 2, GATHER, true>(a, s) : launch_exchange_t<T, VE / 2, GATHER, false>(a, s);
+    if (VE == 8 && a.H % 2 == 0)
+        return a.dots ? launch_exchange_t<T, 2, GATHER, true>(a, s) : launch_exchange_t<T, 2, GATHER, false>(a, s);
     return a.dots ? launch_exchange_t<T, 1, GATHER, true>(a, s) : launch_exchange_t<T, 1, GATHER, false>(a, s);
 }
 

@@ -107,6 +107,12 @@ def test_all_directions(dtype, T, K, E, H, weights, drop):
     assert torch.equal(alone, drows)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,K,E,H", [(700, 8, 64, 2044), (2500, 4, 16, 262), (40, 3, 9, 1030), (1300, 2, 5, 516), (9, 8, 12, 6)])
+def test_rows_that_start_on_8_or_4_bytes(dtype, T, K, E, H):
+    test_all_directions(dtype, T, K, E, H, True, 0.2)
+
+
 def test_gradients_against_differences():
     """Central differences of the plain forward pass in 64 bits along a random direction: linear in each input, so exact but for
     64-bit rounding; the kernel's side carries its fp32 bounds."""
