@@ -24,11 +24,11 @@
 // length: the rows of a group all begin at the same place within a vector (their numbers are equal mod 8), so its columns
 // stay the same from row to row, and only a row's first and last vector are masked when read and written element by element.
 //
-// Measured (graph replay): forward 4096 x 2048 bf16 14.3 us = 4.7 TB/s, with a whole sigmoid gate 16.7 us = 5.0 TB/s (issue slots 73 %);
-// backward 4096 x 2048 29.5 us, 32768 x 2048 158 us = 5.1 TB/s, 4096 x 8192 91 us, 4096 x 2048 fp32 37 us = 5.4 TB/s: 519 instructions a warp
-// and row at 0.70 a clock, and some 10 us whatever the rows for two launches, the first copies and the column sums. (With two rounds of
-// sums and the next row in registers: 660 at 0.57, 37.7, 212, 155 and 60 us. 1024 threads of 64 registers that read a row's pieces twice
-// instead of 512 that hold them: 36.8 and 201 us; packed pairs of fp32: 31.3 and 171.)
+// Measured (graph replay): forward 4096 x 2048 bf16 14.4 us = 4.7 TB/s, 32768 x 2048 88 us = 6.1 TB/s, 4096 x 2048 with a whole sigmoid gate
+// 16.0 to 16.5 us = 5.1 TB/s (issue slots 75 %); backward 4096 x 2048 28 us, 32768 x 2048 146 us = 5.5 TB/s, 4096 x 8192 87 us, 4096 x 2048
+// fp32 37 us = 5.4 TB/s: some 10 us whatever the rows for two launches, the first copies and the column sums, then issue slots.
+// Tried backward: two rounds of sums and the next row in registers 37.7, 212, 155 and 60 us; 1024 threads of 64 registers that read a
+// row's pieces twice instead of 512 that hold them 36.8 and 201; packed pairs of fp32 31.3 and 171 where single ones took 29.5 and 158.
 #pragma once
 
 #include "ops.cuh"
