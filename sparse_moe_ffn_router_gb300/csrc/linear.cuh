@@ -6,6 +6,7 @@
 
 #include "ops.cuh"
 #include "sm100.cuh"
+#include "tiles.h"
 
 namespace moe {
 
@@ -152,10 +153,6 @@ __device__ __forceinline__ void lin_slope(int act, const float (&z)[N], float (&
     }
 }
 
-// Columns of each of an expert's tiles: as even as steps of STEP allow.
-template <int STEP>
-__device__ __forceinline__ int lin_width(int cols, int tiles) { return ((cols + tiles - 1) / tiles + STEP - 1) / STEP * STEP; }
-
 // Row boundaries of the experts and first tile of each, in shared memory; every bound is within [0, T].
 template <int MODE>
 __device__ void lin_tables(const LinView& a, int* off, int* start) {
@@ -177,7 +174,7 @@ __device__ void lin_tables(const LinView& a, int* off, int* start) {
                 const int rows = off[i + 1] - off[i];
                 if (rows < 0) atomicOr(a.err, ERR_BAD_ROUTE);
                 const int cols = MODE == kDw ? a.N : max(rows, 0);
-                n = (cols + a.colw - 1) / a.colw * a.ftiles;
+                n = lin_tiles(cols, a.colw) * a.ftiles;
             }
             int v = n;
 #pragma unroll
@@ -208,7 +205,7 @@ struct LinWalk {
             ti.rows = max(off[e + 1] - ti.row0, 0);
             ti.blocks = ((MODE == kDw ? ti.rows : a.C) + 63) / 64;
             cols = MODE == kDw ? a.N : ti.rows;
-            n = (cols + a.colw - 1) / a.colw;
+            n = lin_tiles(cols, a.colw);
             width = lin_width<STEP>(cols, n);
         }
         const int local = t - s0;
