@@ -289,7 +289,7 @@ moe_status moe_sort_pairs(int32_t T, int32_t K, int32_t E, const int32_t* ids, i
  *   moe_combine_backward   drows[inv[p]] = topk_w[p] * dout[t];      dtopk_w[p] = dout[t] . rows[inv[p]]
  * (the gradient of residual is dout). dtopk_w is optional, and x and rows of the backward calls are read for it
  * alone (NULL without it). Dropped slots give and receive nothing: their dtopk_w is 0, and rows that no pair has as
- * its place are left as they were. Sums are in fp32 in slot order, dots in fp32, each result rounded once.
+ * its place are left as they were. Sums are in fp32 in slot order, the residual last, dots in fp32, each result rounded once.
  * out may be the same buffer as residual; otherwise results overlap no input. An entry of inv that is no place
  * in [0, T*K) counts as dropped. dtype: bf16, fp16 or fp32; 1 <= K <= 8, 1 <= H <= 65536, T * K <= 2^31 - 2^16;
  * rows move fastest where H elements are a multiple of 16 bytes (then of 8, of 4). T = 0 is a no-op. */

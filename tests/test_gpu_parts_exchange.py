@@ -166,3 +166,36 @@ def test_empty():
     inv = torch.empty(0, dtype=torch.int32, device="cuda")
     moe.moe_dispatch(z, inv, None, z)
     moe.moe_combine(z, inv, None, None, z)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H", [520, 77])
+def test_a_large_residual_costs_one_rounding(dtype, H):
+    """Rows are added up at their own size and the residual last: its size is rounded to once. (K products and sums of the rows: 2 K
+    roundings of their magnitudes in fp32; then the sum with the residual, rounded in fp32, and to the type.)"""
+    T, K = 300, 8
+    inv = ref.sort_gpu(make_ids(1, T, 16, K, 0.1), 16)[3]
+    rows, w = ref.randn(2, dtype, T * K, H), torch.softmax(ref.randn(3, torch.float32, T, K), 1)
+    res = (4096 + 512 * ref.randn(4, torch.float32, T, H)).to(dtype)
+    out = torch.empty_like(res)
+    moe.moe_combine(rows, inv, w, res, out)
+    s, mag = ref.gather(rows, inv, w, T)
+    want = s + res.double()
+    last = 0.0 if dtype == torch.float32 else ref.unit(dtype) * (1 + ref.U32)
+    off, bound = (out.double() - want).abs(), (ref.U32 * (1 + last) + last) * want.abs() + 2 * (2 * K + 1) * ref.U32 * mag
+    assert not bool((~(off <= bound)).any()), float((off / bound).max())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_tokens_without_slots_keep_their_residual(dtype):
+    """Bit for bit, a negative zero among them; without a residual they are zeros."""
+    T, K, H = 5, 3, 24
+    inv = torch.full((T * K,), -1, dtype=torch.int32, device="cuda")
+    rows, res = ref.randn(1, dtype, T * K, H), ref.randn(2, dtype, T, H)
+    res[:, ::3] = -0.0
+    out = torch.empty_like(res)
+    for w in (None, torch.rand(T, K, device="cuda")):
+        moe.moe_combine(rows, inv, w, res, out)
+        assert torch.equal(out.view(torch.uint8), res.view(torch.uint8))
+        moe.moe_combine(rows, inv, w, None, out)
+        assert not bool(out.view(torch.uint8).any())
