@@ -445,7 +445,9 @@ uint64_t moe_launch_count(void);
 
 /* Testing aid for the bounded-wait path (the paper has no counterpart). Every wait of the
  * one-token kernel (moe_forward with T = 1 at the page's layer shape) and of the streaming
- * expert kernels (2 <= T < 256), and every wait of the kernels on 4-bit weights and of moe_linear's, gives up after a time limit, sets MOE_ERR_TIMEOUT in the
+ * expert kernels (2 <= T < 256), and every wait of the kernels on 4-bit weights and of moe_linear and
+ * moe_linear_backward (there counted from the last 64-deep stage of operands that was worked off: a
+ * call may last as long as it is), gives up after a time limit, sets MOE_ERR_TIMEOUT in the
  * workspace's error word and lets the kernel run to its end with in-range indices; the calls
  * after a timeout need moe_workspace_init on that workspace. This sets, process-wide and for
  * the calls made after it returns:

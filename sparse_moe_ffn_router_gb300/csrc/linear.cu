@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint64_t* mma_done = acce + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kStages + 5) * 8 + 8 <= 256, "barrier area");
+    volatile int* progress = abort_flag + 1;  // kDw: stages that this CTA's producer has found empty, which the longer waits go by
+    static_assert((2 * kStages + 5) * 8 + 12 <= 256, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank(), split = cluster_size();
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
+        *progress = 0;
         fence_mbar_init();
         tma_prefetch_desc(&mA);
         tma_prefetch_desc(&mB);
@@ -177,6 +179,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         *abort_flag = 1;
                         break;
                     }
+                    if (MODE == kDw) *progress = it + 1;
                     if (a.suppress && blockIdx.x == 0 && it == 0) continue;
                     mbar_arrive_expect_tx(&full[s], bytes);
                     uint8_t* da = sA + s * kLinA;
@@ -300,7 +303,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 if (GATED) lin_bias_up<T>(a, ti.e, f, bu);
             }
             bool ready = false;
-            if (!*abort_flag) ready = mbar_wait(&accf[b], use, a.wait_ns);
+            if (!*abort_flag)  // (a tile's whole contraction: of kDw as long as an expert has rows, else of 2^14 stages at most)
+                ready = MODE == kDw ? mbar_wait_progress(&accf[b], use, progress, a.wait_ns) : mbar_wait(&accf[b], use, a.wait_ns);
             ready = __all_sync(0xffffffffu, ready);
             if (!ready && lane == 0) {
                 if (!*abort_flag) atomicOr(a.err, ERR_TIMEOUT);

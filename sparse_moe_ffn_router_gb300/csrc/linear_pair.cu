@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint64_t* mma_done = acce + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((4 * kStages + 5) * 8 + 8 <= 256, "barrier area");
+    volatile int* progress = abort_flag + 1;  // kDw: stages that this CTA's producer has found empty, which the longer waits go by
+    static_assert((4 * kStages + 5) * 8 + 12 <= 256, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
+        *progress = 0;
         fence_mbar_init();
         tma_prefetch_desc(&mA);
         tma_prefetch_desc(&mB);
@@ -318,6 +320,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         *abort_flag = 1;
                         break;
                     }
+                    if (MODE == kDw) *progress = it + 1;
                     if (a.suppress && blockIdx.x == 0 && it == 0) continue;
                     uint8_t* da = sA + s * kLinA;
                     uint8_t* db = sB + s * kPairB;
@@ -395,8 +398,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             mma_commit_pair(mma_done);
         }
         __syncwarp();
-        if (!mbar_wait(mma_done, 0, a.wait_ns) && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
-        __syncwarp();
     } else if (warp >= kLinEpiWarp0) {
         // ---------------- epilogue of this CTA's features: lanes 32 q .. of the accumulator, every other 32 columns
         const int q = warp & 3, h = (warp - kLinEpiWarp0) >> 2;
@@ -407,7 +408,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             const int b = local & 1;
             const uint32_t use = (uint32_t)(local >> 1) & 1u;
             bool ready = false;
-            if (!*abort_flag) ready = mbar_wait(&accf[b], use, a.wait_ns);
+            if (!*abort_flag)  // (a tile's whole contraction: of kDw as long as an expert has rows, else of 2^14 stages at most)
+                ready = MODE == kDw ? mbar_wait_progress(&accf[b], use, progress, a.wait_ns) : mbar_wait(&accf[b], use, a.wait_ns);
             ready = __all_sync(0xffffffffu, ready);
             if (!ready) {
                 if (lane == 0) {
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 const int s = (it - 1) % kStages, left = ti.rows - (ti.blocks - 1) * 64, rows = (left + 15) / 16 * 16 - left;
                 const uint32_t ph = turn >> s & 1u;
                 turn ^= 1u << s;
-                bool ok = mbar_wait(&mine[s], ph, a.wait_ns);
+                bool ok = mbar_wait_progress(&mine[s], ph, progress, a.wait_ns);  // (whatever tiles come before)
                 const int panels = 2 + ((ti.cols + 31) / 32 * 16 + 63) / 64;
                 const uint32_t aa = smem_u32(sA + s * kLinA), bb = smem_u32(sB + s * kPairB);
                 const uint32_t zero[4] = {0u, 0u, 0u, 0u};
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                         for (int i = lane; i < rows * 8; i += 32) sts128(at + (uint32_t)i * 16u, zero);
                     }
                 fence_proxy_async_smem();
-                if (ok && rank == 0) ok = mbar_wait(&other[s], ph, a.wait_ns);
+                if (ok && rank == 0) ok = mbar_wait_progress(&other[s], ph, progress, a.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok && lane == 0) {
                     atomicOr(a.err, ERR_TIMEOUT);
@@ -467,6 +469,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // Only now, with this CTA's last tile written: from the start of the kernel the odd CTA's limit would be one of the whole call.
+    if (warp == 1 && !mbar_wait(mma_done, 0, a.wait_ns) && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
+    __syncwarp();
     cluster_sync_all();  // neither CTA leaves while the other may still arrive on its barriers or read its tiles
     if (warp == 1) {
         tc_fence_after();

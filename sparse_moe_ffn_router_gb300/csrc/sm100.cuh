@@ -126,6 +126,24 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
     }
 }
 
+// The same for a wait that lasts as long as much work of other roles of the CTA: given up when *progress, a count in shared memory
+// that a role raises as it goes, is what it was `limit` ns before. (Not the ring's own phases in place of a count: the thread is
+// woken in step with them, so they may look the same every time.)
+__device__ __forceinline__ bool mbar_wait_progress(uint64_t* bar, uint32_t parity, const volatile int* progress, uint64_t limit) {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = global_ns();
+    int seen = *progress;
+    for (;;) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (global_ns() - t0 > limit) {
+            const int now = *progress;
+            if (now == seen) return false;
+            seen = now;
+            t0 = global_ns();
+        }
+    }
+}
+
 // 16-byte shared-memory store / load at a shared-window address (explicit st/ld.shared).
 __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&v)[4]) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])

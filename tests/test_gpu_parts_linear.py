@@ -380,3 +380,37 @@ def test_matrices_past_32_bits_of_elements():
         for name, g, r, v in (("dx", dx[a:c], want[0], bound[0]), ("dw", dw[e], want[1][0], bound[1][0])):
             assert not bool((~((g.double() - r).abs() <= v)).any()), name
     assert not bool(dw[250].any()) and not bool(dw[254].any())
+
+
+@pytest.mark.parametrize("T,N,K,E,which,limit_us", [(32768, 8192, 4096, 1, "out", 300), (32768, 4096, 8192, 1, "dx", 300), (1 << 19, 1024, 1024, 1, "dw", 200), (1 << 19, 1024, 1024, 2, "dw", 200),
+                                                    (1 << 22, 256, 256, 1, "dw", 200)])
+def test_a_limit_bounds_a_stall_not_the_call(T, N, K, E, which, limit_us):
+    """Products of a millisecond or more under a limit that no wait of theirs comes near: tiles one after another, one tile's long
+    contraction, and a ragged last block of rows at the end of one. They are whole and report no time-out."""
+    d = moe.LinearDims(T, N, K, E=E)
+    x, w, _, _ = inputs(d, bias=False, residual=False)
+    off = offsets_of([T // 2, T // 2 - 5]) if E == 2 else None
+    ws, dout = moe.new_linear_workspace(d, backward=True), ref.randn(5, x.dtype, T, N)
+
+    def call():
+        o = torch.zeros_like(dout) if which == "out" else torch.zeros_like(x) if which == "dx" else torch.zeros_like(w)
+        if which == "out":
+            moe.moe_linear(d, x, w, None, off, None, o, None, ws)
+        else:
+            moe.moe_linear_backward(d, x, w, off, None, dout, o if which == "dx" else None, o if which == "dw" else None, None, ws)
+        return o
+
+    want = call()
+    assert moe.moe_last_device_error(ws) == 0
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    try:
+        moe.moe_test_set_wait(limit_us * 1000)
+        start.record()
+        got = call()
+        end.record()
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_test_set_wait()
+    assert moe.moe_last_device_error(ws) == 0
+    assert torch.equal(got, want)
+    assert start.elapsed_time(end) * 1e3 > limit_us  # (else the limit would show nothing)
