@@ -633,6 +633,13 @@ bool map_2d(CUtensorMap* m, int32_t dt, const void* p, uint64_t rows, uint64_t c
     const uint32_t b[2] = {64, box_rows};
     return encode_map(m, dt, p, 2, d, st, b);
 }
+// The same as 64 rows from any first one, [rows, 64, cols] whose two row strides are one and the same, for boxes of 64 that may begin
+// at a negative row of the 64. (What a box then reads ends with the first row's 64th at the latest, and the kernel's with an expert's last.)
+bool map_64(CUtensorMap* m, int32_t dt, const void* p, uint64_t rows, uint64_t cols, uint64_t pitch) {
+    const uint64_t d[3] = {cols, 64, rows}, st[2] = {pitch * 2, pitch * 2};
+    const uint32_t b[3] = {64, 64, 1};
+    return encode_map(m, dt, p, 3, d, st, b);
+}
 // W [E, N, K].
 bool map_w(CUtensorMap* m, const moe_linear_dims& d, const void* w, uint32_t box_rows) {
     const uint64_t dim[3] = {(uint64_t)d.K, (uint64_t)d.N, (uint64_t)d.E}, st[2] = {(uint64_t)d.K * 2, (uint64_t)d.N * d.K * 2};
@@ -750,10 +757,12 @@ cudaError_t linear_backward_t(const LinearArgs& in, cudaStream_t s) {
         v.dbias = nullptr;
     }
     if (a.dw) {
-        if (!map_2d(&A, d.dtype, a.x, d.T, d.K, d.K, 64) || !map_2d(&B, d.dtype, dz, d.T, d.N, pitch, 64)) return cudaErrorInvalidValue;
         v.out = a.dw;
         v.C = 0;
         const LinPlan p = lin_plan<T, kDw, false>(d.E, d.N, false, d.K, (int)(((d.T + g - 1) / g + 63) / 64), a.num_sms);
+        if (!(p.pair ? map_64(&A, d.dtype, a.x, d.T, d.K, d.K) && map_64(&B, d.dtype, dz, d.T, d.N, pitch)
+                     : map_2d(&A, d.dtype, a.x, d.T, d.K, d.K, 64) && map_2d(&B, d.dtype, dz, d.T, d.N, pitch, 64)))
+            return cudaErrorInvalidValue;
         CUtensorMap C = A;
         if (p.pair) {
             const uint64_t dim[3] = {(uint64_t)d.K, (uint64_t)d.N, (uint64_t)d.E}, st[2] = {(uint64_t)d.K * 2, (uint64_t)d.N * d.K * 2};

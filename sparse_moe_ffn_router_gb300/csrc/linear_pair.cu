@@ -5,9 +5,12 @@
 // its own 128 feature rows and half of the columns, so a 64-deep stage is 32 KB for 256 x 256 of the product's
 // tile: a tensor core reads 8 KB of shared memory for 128 cycles of work and TMA writes as much, which one SM
 // alone (16 KB of A and 32 KB of B a stage) cannot keep up with. The CTA of even rank issues the
-// MMAs of both; its barrier of a stage counts both CTAs' copies. An expert's last rows of kDw, where they are no whole
-// 16, bring rows of the next expert along: those stages land on a barrier of each CTA's own, a warp clears the
-// foreign rows, and the even CTA's reports the stage once both are done.
+// MMAs of both; its barrier of a stage counts both CTAs' copies. An expert's last rows of kDw, where they are no whole 64, have
+// rows of the next expert behind them, which must not be multiplied, whatever they hold (0 x infinity would stay). The maps
+// of kDw are of 64 consecutive rows from any first one, and the last block is loaded from a negative place in its 64: TMA's zeros come
+// first, in both operands alike, then the rows there are, and nothing of the next expert. (Clearing the foreign rows in shared memory
+// takes an order between those stores and the products that the other CTA issues. With the cluster scope that it needs, the 256
+// experts' dW of 512 rows takes 194 us instead of 166, of 32768 rows 250 instead of 211; with stores of the even CTA to both 236 and 240.)
 //
 // Measured (graph replay, us): 4096 x 8192 x 2048 71.5 without an activation = 1922 TFLOP/s, the rate of a library product; 76 with
 // GELU and bias; experts' products of 32768 rows, 256 x [1024, 2048]: forward 192 (5.7 TB/s), dx 186, dW 207 (5.9 TB/s).
@@ -234,13 +237,6 @@ __device__ __forceinline__ void pair_epilogue_dw(const CUtensorMap* mC, uint32_t
     }
 }
 
-// Whether block kb of an expert's rows ends in rows of the next expert that its last 16 would take in (one matrix for all rows: its
-// last block ends in TMA's zeros).
-__device__ __forceinline__ bool pair_clears(const LinView& a, const LinTile& ti, int kb) {
-    const int left = ti.rows - kb * 64;
-    return a.offsets && left < 64 && (left & 15);
-}
-
 template <typename T, int MODE, bool GATED>
 __global__ void __launch_bounds__(kLinThreads, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB, const __grid_constant__ CUtensorMap mC, const LinView a) {
@@ -256,15 +252,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     int* start = off + kLinMaxE + 4;
     uint64_t* full = reinterpret_cast<uint64_t*>(scratch + kPairScratch + kPairTables);  // even rank: a stage of both CTAs is ready
     uint64_t* empty = full + kStages;  // both CTAs' MMAs have read it
-    uint64_t* mine = empty + kStages;  // kDw: this CTA's half has landed and is to be cleared
-    uint64_t* other = mine + kStages;  // kDw, even rank: the other's is
-    uint64_t* accf = other + kStages;
+    uint64_t* accf = empty + kStages;
     uint64_t* acce = accf + 2;          // even rank: both CTAs' epilogues have read the accumulator
     uint64_t* mma_done = acce + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* progress = abort_flag + 1;  // kDw: stages that this CTA's producer has found empty, which the longer waits go by
-    static_assert((4 * kStages + 5) * 8 + 12 <= 256, "barrier area");
+    static_assert((2 * kStages + 5) * 8 + 12 <= 256, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -272,8 +266,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
-            mbar_init(&mine[s], 1);
-            mbar_init(&other[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf[b], 1);
@@ -324,13 +316,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     if (a.suppress && blockIdx.x == 0 && it == 0) continue;
                     uint8_t* da = sA + s * kLinA;
                     uint8_t* db = sB + s * kPairB;
-                    const bool clear = MODE == kDw && pair_clears(a, ti, kb);
-                    if (clear) mbar_arrive_expect_tx(&mine[s], bytes);
-                    else if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
-                    const uint32_t bar = clear ? smem_u32(&mine[s]) : mbar_of_even(&full[s]);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * bytes);
+                    const uint32_t bar = mbar_of_even(&full[s]);
                     if (MODE == kDw) {
-                        for (int p = 0; p < 2; ++p) tma_load_2d_pair(da + p * 8192, &mA, bar, f * 128 + p * 64, ti.row0 + kb * 64);
-                        for (int p = 0; p < boxes; ++p) tma_load_2d_pair(db + p * 8192, &mB, bar, c0 + p * 64, ti.row0 + kb * 64);
+                        const int row = ti.row0 + kb * 64, from = min(ti.rows - kb * 64 - 64, 0);
+                        for (int p = 0; p < 2; ++p) tma_load_3d_pair(da + p * 8192, &mA, bar, f * 128 + p * 64, from, row);
+                        for (int p = 0; p < boxes; ++p) tma_load_3d_pair(db + p * 8192, &mB, bar, c0 + p * 64, from, row);
                     } else {
                         if (MODE == kDx) {
                             for (int p = 0; p < 2; ++p) tma_load_3d_pair(da + p * 8192, &mA, bar, f * 128 + p * 64, kb * 64, ti.e);
@@ -379,10 +370,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t da = descA + (uint64_t)(s * (kLinA >> 4)), db = descB + (uint64_t)(s * (kPairB >> 4));
-                    const int steps = MODE == kDw ? min(4, (ti.rows - kb * 64 + 15) / 16) : 4;
+                    const int zeros = MODE == kDw ? max(4 - (ti.rows - kb * 64 + 15) / 16, 0) : 0;  // 16s without a row
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        if (kk < steps) mma_f16_pair(d, da + kk * kStepA, db + kk * kStepB, idesc, (kb | kk) != 0);
+                        if (kk >= zeros) mma_f16_pair(d, da + kk * kStepA, db + kk * kStepB, idesc, kb != 0 || kk != zeros);
                     mma_commit_pair(&empty[s]);
                 }
                 if (ok && ti.blocks > 0) mma_commit_pair(&accf[b]);
@@ -432,38 +423,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (MODE == kDw && lane == 0) tma_store_wait_all();
         __syncwarp();
     } else {
-        if (MODE == kDw && warp == 2 && a.offsets) {
-            // ---------------- rows of the next expert in an expert's last 16: zeros in both operands (whatever they hold: 0 x
-            // infinity would stay)
-            int it = 0;
-            uint32_t turn = 0;  // a bit a stage: the phase its barriers here are in
-            for (int t = first; t < total && !__any_sync(0xffffffffu, *abort_flag); t += step) {
-                const LinTile ti = walk.to(a, off, start, t);
-                it += ti.blocks;
-                if (ti.blocks == 0 || !pair_clears(a, ti, ti.blocks - 1)) continue;
-                const int s = (it - 1) % kStages, left = ti.rows - (ti.blocks - 1) * 64, rows = (left + 15) / 16 * 16 - left;
-                const uint32_t ph = turn >> s & 1u;
-                turn ^= 1u << s;
-                bool ok = mbar_wait_progress(&mine[s], ph, progress, a.wait_ns);  // (whatever tiles come before)
-                const int panels = 2 + ((ti.cols + 31) / 32 * 16 + 63) / 64;
-                const uint32_t aa = smem_u32(sA + s * kLinA), bb = smem_u32(sB + s * kPairB);
-                const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-                if (ok)
-                    for (int p = 0; p < panels; ++p) {
-                        const uint32_t at = (p < 2 ? aa + p * 8192 : bb + (p - 2) * 8192) + (uint32_t)left * 128u;
-                        for (int i = lane; i < rows * 8; i += 32) sts128(at + (uint32_t)i * 16u, zero);
-                    }
-                fence_proxy_async_smem();
-                if (ok && rank == 0) ok = mbar_wait_progress(&other[s], ph, progress, a.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok && lane == 0) {
-                    atomicOr(a.err, ERR_TIMEOUT);
-                    *abort_flag = 1;
-                }
-                if (ok && lane == 0) mbar_arrive_cluster(rank == 0 ? &full[s] : &other[s], 0);
-                __syncwarp();
-            }
-        }
         if (MODE != kFwd && a.dbias) lin_dbias<T>(a, off, blockIdx.x * 2 + warp - 2, gridDim.x * 2);
         __syncwarp();
     }

@@ -396,10 +396,9 @@ __device__ __forceinline__ void tma_load_5d_pair(void* dst, const void* map, uin
         "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
         : "memory");
 }
-// One arrival on the barrier at bar's place in CTA `rank` of the cluster. (What it reports is shared memory that TMA or
-// a fenced store has filled, or tensor memory that has been read: no global write has to be out first. At
-// cluster scope the release would wait for those: 1900 instead of 512 clocks a stage of the pair kernel; for
-// the cleared rows alone, after a fence for the async proxy that reads them, 490 instead of 437 us of an experts' backward pass.)
+// One arrival on the barrier at bar's place in CTA `rank` of the cluster. (What it reports is tensor memory that this thread's waited-for
+// loads have read, or nothing but the turn: no write of memory has to be seen by who waits. At cluster scope the release would wait
+// for the SM's global stores: 1900 instead of 512 clocks a stage of the pair kernel.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\t"

@@ -414,3 +414,30 @@ def test_a_limit_bounds_a_stall_not_the_call(T, N, K, E, which, limit_us):
     assert moe.moe_last_device_error(ws) == 0
     assert torch.equal(got, want)
     assert start.elapsed_time(end) * 1e3 > limit_us  # (else the limit would show nothing)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("N,K,step", [(1024, 512, 1), (520, 2048, 3)])
+def test_weight_gradients_of_ragged_experts_see_their_rows_alone(N, K, step, bad):
+    """Experts of every count around whole 16s, each second one's rows non-finite: they are in the same 64 rows of both operands of
+    both SMs of a pair as the ends of the others, tile after tile."""
+    counts = [33 + step * i % 97 for i in range(128)]
+    off = offsets_of(counts)
+    d = moe.LinearDims(int(off[-1]) + 3, N, K, E=128)
+    x, w, _, _ = inputs(d, bias=False, residual=False)
+    dout, ws = ref.randn(5, x.dtype, d.T, N), moe.new_linear_workspace(d, backward=True)
+    want = torch.empty_like(w)
+    moe.moe_linear_backward(d, x, None, off, None, dout, None, want, None, ws)
+    r64, bounds = ref.linear_backward(d, x, w, off, None, dout)
+    assert not bool((~((want.double() - r64[1]).abs() <= bounds[1])).any())
+    for turn in range(8):
+        xb, db, got = x.clone(), dout.clone(), torch.empty_like(w)
+        for e in range(turn % 2, 128, 2):
+            a, c = int(off[e]), int(off[e + 1])
+            if turn % 4 < 2:
+                xb[a:c] = bad
+            else:
+                db[a:c] = bad
+        moe.moe_linear_backward(d, xb, None, off, None, db, None, got, None, ws)
+        assert torch.equal(got[1 - turn % 2::2], want[1 - turn % 2::2])
+    assert moe.moe_last_device_error(ws) == 0
