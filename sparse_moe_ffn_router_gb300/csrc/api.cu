@@ -66,15 +66,16 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 int sm_count() {
-    static int cache[128];
+    static std::atomic<int> cache[128];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 148;
-    if (cache[dev] == 0) {
-        int n = 0;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        cache[dev] = n > 0 ? n : 148;
+        if (n <= 0) n = 148;
+        cache[dev].store(n, std::memory_order_relaxed);
     }
-    return cache[dev];
+    return n;
 }
 
 // Common validation of moe_route / moe_forward / moe_forward_w4 (w4). On success fills the plan and

@@ -30,6 +30,8 @@
 //             the group's end are zero-filled. x rows are kept in L2 (evict-last) across the K
 //             experts that read them, and no dispatched copy of x is written or read. The
 //             shared expert's A rows are x itself, loaded by TMA.
+#include <atomic>
+
 #include "ops.cuh"
 #include "sm100.cuh"
 
@@ -426,7 +428,8 @@ __global__ void __launch_bounds__(gemm_threads<EPI>(), 1)
 namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 fn = found.load(std::memory_order_acquire);
     if (!fn) {
         cudaDriverEntryPointQueryResult q;
         void* p = nullptr;
@@ -434,6 +437,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
                 cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
             fn = (PFN_cuTensorMapEncodeTiled_v12000)p;
+        found.store(fn, std::memory_order_release);
     }
     return fn;
 }

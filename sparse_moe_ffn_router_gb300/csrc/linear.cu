@@ -527,14 +527,9 @@ namespace {
 
 template <typename T, int MODE, bool GATED>
 cudaError_t launch_k(const CUtensorMap& A, const CUtensorMap& B, const LinView& v, int grid, int split, cudaStream_t s) {
-    static bool configured[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !configured[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(k_linear<T, MODE, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLinBytes);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) configured[dev] = true;
-    }
+    static std::atomic<bool> allowed[64];
+    const cudaError_t e = allow_shared(k_linear<T, MODE, GATED>, (int)kLinBytes, allowed);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kLinThreads);

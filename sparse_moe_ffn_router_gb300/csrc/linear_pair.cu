@@ -440,14 +440,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
 template <typename T, int MODE, bool GATED>
 static cudaError_t launch_pair_k(const CUtensorMap& A, const CUtensorMap& B, const CUtensorMap& C, const LinView& v, int grid, cudaStream_t s) {
-    static bool configured[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !configured[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(k_linear_pair<T, MODE, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_bytes(MODE));
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) configured[dev] = true;
-    }
+    static std::atomic<bool> allowed[64];
+    const cudaError_t e = allow_shared(k_linear_pair<T, MODE, GATED>, (int)pair_bytes(MODE), allowed);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kLinThreads);

@@ -742,15 +742,9 @@ static cudaError_t launch_norm_backward_t(const NormArgs& a, cudaStream_t s, int
     p.bufs = p.ring + pieces * p.slots * p.stages;
     p.bytes = max(p.bufs + sums, p.groups > 1 ? (uint32_t)(p.groups * (GATE == kGateColumn ? 3 : 2) * back_columns<VE>(a.d.H)) * 4u : 0u);
     if (p.stages < 1 || p.bytes > kRoom) return cudaErrorInvalidValue;  // (never)
-    static bool configured[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaError_t e;
-    if (dev < 0 || dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(k_norm_backward<T, VE, VPT, GATE, ODD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRoom);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) configured[dev] = true;
-    }
+    static std::atomic<bool> allowed[64];
+    cudaError_t e = allow_shared(k_norm_backward<T, VE, VPT, GATE, ODD>, (int)kRoom, allowed);
+    if (e != cudaSuccess) return e;
     NormArgs b = a;
     const bool columns = a.dgamma_post || a.dgamma_pre || (a.dgate && a.d.gate == MOE_GATE_CHANNEL);
     if (!columns) b.part = nullptr;

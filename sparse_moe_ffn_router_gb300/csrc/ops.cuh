@@ -2,6 +2,8 @@
 // the argument blocks passed from the C-ABI entry points to the launches.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_fp16.h>
 
 #include "launch.h"
@@ -104,6 +106,19 @@ struct RawOf<fp16> {
     }
 };
 #endif
+
+// Lets a kernel have `bytes` of dynamic shared memory, once for each device (done: which have it). Two host threads may make their first
+// calls at the same time: then both ask for it.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel* kernel, int bytes, std::atomic<bool> (&done)[64]) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const bool known = dev >= 0 && dev < 64;
+    if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_release);
+    return e;
+}
 
 // ---- exchange (exchange.cu): tokens [T, H], rows [T * K, H], inv [T * K]
 struct ExchangeArgs {
