@@ -229,3 +229,28 @@ def test_nothing_is_written_behind_the_workspace(T, H):
     new = lambda t: torch.empty_like(t)  # noqa: E731
     moe.moe_norm_residual_backward(d, ds, dxn, s, y, g, gp, gq, new(y), new(y), new(g), new(gp), new(gq), room[:size])
     assert bool((room[size:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("T,H,dtype,gate", [(2500, 1003, moe.BF16, 0), (2500, 1003, moe.FP16, 3), (1201, 77, moe.FP32, 4), (2051, 1544, moe.BF16, 4), (700, 8191, moe.FP32, 3),
+                                            (640, 8187, moe.FP32, 5), (641, 8192, moe.FP32, 1), (643, 8191, moe.BF16, 2), (5003, 33, moe.BF16, 5), (9, 8190, moe.FP32, 4), (3, 5, moe.FP16, 0)])
+def test_results_over_their_inputs_of_any_row(T, H, dtype, gate):
+    """Each pair of buffers that may be shared, with rows that begin anywhere (whose pieces of 16 bytes reach into rows that others
+    are writing), rows that are read from memory twice, and every kind of gate: the bits are those of results with buffers of
+    their own."""
+    d = dims(T, H, dtype, GATES[gate], branch_scale=0.5, residual_scale=0.75)
+    y, r, g, gp, gq = inputs(d)
+    s, xn = torch.empty_like(y), torch.empty_like(y)
+    moe.moe_norm_residual(d, y, r, g, gp, gq, s, xn)
+    for over in ("ry", "yr", "y-", "-y", "r-", "-r"):
+        b = {"y": y.clone(), "r": r.clone(), "-": torch.empty_like(y)}
+        moe.moe_norm_residual(d, b["y"], b["r"], g, gp, gq, b[over[0]], b[over[1]])
+        assert torch.equal(b[over[0]], s) and torch.equal(b[over[1]], xn), over
+    ds, dxn, ws = ref.randn(7, y.dtype, T, H), ref.randn(8, y.dtype, T, H), moe.new_norm_workspace(d)
+    new = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+    want = [new(t) for t in (y, y, g, gp, gq)]
+    moe.moe_norm_residual_backward(d, ds, dxn, s, y, g, gp, gq, *want, ws)
+    for over in ("dx", "xd", "sy", "ys", "d-", "-d", "x-", "-y"):
+        b = {"d": ds.clone(), "x": dxn.clone(), "s": s.clone(), "y": y.clone(), "-": torch.empty_like(y)}
+        got = [b[over[0]], b[over[1]], *[new(t) for t in (g, gp, gq)]]
+        moe.moe_norm_residual_backward(d, b["d"], b["x"], b["s"], b["y"], g, gp, gq, *got, ws)
+        assert all(p is None or torch.equal(p, q) for p, q in zip(got, want)), over
