@@ -624,11 +624,12 @@ _I32, _F32 = torch.int32, torch.float32
 def moe_sort_pairs(E: int, ids, counts, offsets, perm, inv, stream=None):
     """Dispatch of the expert ids [T, K] int32: counts [E], offsets [E + 1], perm [T * K] (pairs t * K + k by expert,
     -1 behind the last) and inv [T * K] (each pair's place, -1 for an id outside [0, E))."""
+    dev = _current("ids", ids)
     if ids.dim() != 2:
         raise ValueError("ids must be int32 [T, K]")
     shape = ids.shape
     T, K = shape
-    dev, flat = _current(ids), (T * K,)
+    flat = (T * K,)
     _check(load_library().moe_sort_pairs(T, K, E, _ptr_of(dev, _I32, shape, "ids", ids), _ptr_of(dev, _I32, (E,), "counts", counts),
                                          _ptr_of(dev, _I32, (E + 1,), "offsets", offsets), _ptr_of(dev, _I32, flat, "perm", perm, shape),
                                          _ptr_of(dev, _I32, flat, "inv", inv, shape), _stream_of(stream, dev)), "moe_sort_pairs")
@@ -636,6 +637,9 @@ def moe_sort_pairs(E: int, ids, counts, offsets, perm, inv, stream=None):
 
 def _exchange(token, rows):
     """Device, type, T, K and H of a call on token rows [T, H] and experts' rows [T * K, H]."""
+    dev = _current("token rows", token)
+    if not isinstance(rows, torch.Tensor):
+        raise TypeError(f"experts' rows: expected a torch.Tensor, got {type(rows).__name__}")
     if token.dim() != 2 or rows.dim() != 2:
         raise ValueError("token rows are [T, H], experts' rows [T * K, H]")
     T, H = token.shape
@@ -646,7 +650,7 @@ def _exchange(token, rows):
     code = _DTYPE.get(token.dtype)
     if code is None:
         raise TypeError(f"token rows must be bfloat16, float16 or float32, got {token.dtype}")
-    return _current(token), token.dtype, code, T, K, H
+    return dev, token.dtype, code, T, K, H
 
 
 def moe_dispatch(x, inv, topk_w, rows, stream=None):
@@ -695,12 +699,23 @@ def new_linear_workspace(dims: LinearDims, backward: bool = False, device="cuda"
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _current(t) -> int:
+def _current(name: str, t) -> int:
     """The current CUDA device, where the kernels will run; t: the first tensor of the call."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     return torch.cuda.current_device() if t.is_cuda else -2
 
 
+def _sizes(dims, kind):
+    """What the checks of a call's tensors go by, of dims of its kind."""
+    if not isinstance(dims, kind):
+        raise TypeError(f"dims: expected {kind.__name__}, got {type(dims).__name__}")
+    return dims.checked
+
+
 def _workspace(device: int, t):
+    if t is not None and not isinstance(t, torch.Tensor):
+        raise TypeError(f"workspace: expected a torch.Tensor, got {type(t).__name__}")
     if t is None or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on the current CUDA device ({device})")
     return t.data_ptr(), t.numel() * t.element_size()
@@ -709,8 +724,8 @@ def _workspace(device: int, t):
 def moe_linear(dims: LinearDims, x, w, bias, offsets, residual, out, z, workspace, stream=None):
     """out = act(x . W_e^T + bias_e) + residual, e the expert whose rows [offsets[e], offsets[e + 1]) hold x's row
     (offsets None: the one matrix); z (or None) receives the pre-activations for moe_linear_backward."""
-    dev = _current(x)
-    dt, rows, wide, pre, mat, mat1, vec, vec1, ends = dims.checked
+    dt, rows, wide, pre, mat, mat1, vec, vec1, ends = _sizes(dims, LinearDims)
+    dev = _current("x", x)
     _check(load_library().moe_linear(ctypes.byref(dims), _ptr_of(dev, dt, rows, "x", x), _ptr_of(dev, dt, mat, "w", w, mat1),
                                      _ptr_of(dev, dt, vec, "bias", bias, vec1), _ptr_of(dev, _I32, ends, "offsets", offsets),
                                      _ptr_of(dev, dt, wide, "residual", residual), _ptr_of(dev, dt, wide, "out", out),
@@ -719,8 +734,8 @@ def moe_linear(dims: LinearDims, x, w, bias, offsets, residual, out, z, workspac
 
 def moe_linear_backward(dims: LinearDims, x, w, offsets, z, dout, dx, dw, dbias, workspace, stream=None):
     """Gradients of moe_linear's x, w and bias (each may be None) for the gradient dout of its result; the residual's is dout."""
-    dev = _current(dout)
-    dt, rows, wide, pre, mat, mat1, vec, vec1, ends = dims.checked
+    dt, rows, wide, pre, mat, mat1, vec, vec1, ends = _sizes(dims, LinearDims)
+    dev = _current("dout", dout)
     _check(load_library().moe_linear_backward(
         ctypes.byref(dims), _ptr_of(dev, dt, rows, "x", x), _ptr_of(dev, dt, mat, "w", w, mat1), _ptr_of(dev, _I32, ends, "offsets", offsets),
         _ptr_of(dev, dt, pre, "z", z), _ptr_of(dev, dt, wide, "dout", dout), _ptr_of(dev, dt, rows, "dx", dx),
@@ -739,8 +754,8 @@ def new_norm_workspace(dims: NormDims, device="cuda") -> torch.Tensor:
 def moe_norm_residual(dims: NormDims, y, residual, gate, gamma_post, gamma_pre, s, xn, stream=None):
     """s = residual_scale * residual + branch_scale * act(gate) * N(y; gamma_post), xn = N(s; gamma_pre); residual, the
     gammas and either result may be None, and N(y) is y for dims without post."""
-    dev = _current(y)
-    dt, rows, cols, gs = dims.checked
+    dt, rows, cols, gs = _sizes(dims, NormDims)
+    dev = _current("y", y)
     _check(load_library().moe_norm_residual(
         ctypes.byref(dims), _ptr_of(dev, dt, rows, "y", y), _ptr_of(dev, dt, rows, "residual", residual), _ptr_of(dev, dt, gs, "gate", gate),
         _ptr_of(dev, dt, cols, "gamma_post", gamma_post), _ptr_of(dev, dt, cols, "gamma_pre", gamma_pre), _ptr_of(dev, dt, rows, "s", s),
@@ -750,8 +765,8 @@ def moe_norm_residual(dims: NormDims, y, residual, gate, gamma_post, gamma_pre, 
 def moe_norm_residual_backward(dims: NormDims, ds, dxn, s, y, gate, gamma_post, gamma_pre, dresidual, dy, dgate, dgamma_post, dgamma_pre, workspace,
                                stream=None):
     """Gradients of moe_norm_residual's inputs (each may be None) for the gradients ds and dxn of its results (either may be None)."""
-    dev = _current(y)
-    dt, rows, cols, gs = dims.checked
+    dt, rows, cols, gs = _sizes(dims, NormDims)
+    dev = _current("y", y)
     _check(load_library().moe_norm_residual_backward(
         ctypes.byref(dims), _ptr_of(dev, dt, rows, "ds", ds), _ptr_of(dev, dt, rows, "dxn", dxn), _ptr_of(dev, dt, rows, "s", s),
         _ptr_of(dev, dt, rows, "y", y), _ptr_of(dev, dt, gs, "gate", gate), _ptr_of(dev, dt, cols, "gamma_post", gamma_post),

@@ -204,3 +204,18 @@ def test_dims_may_be_changed():
     d.dtype = 9
     with pytest.raises(moe.MoEError):
         d.checked
+
+
+def test_binding_names_an_argument_of_another_kind():
+    """A tensor that is missing or something else, and dims of another call: a TypeError that says which."""
+    b, i = torch.bfloat16, torch.int32
+    x, ids, inv = torch.zeros(4, 64, dtype=b), torch.zeros(4, 2, dtype=i), torch.zeros(4, dtype=i)
+    d, n = moe.LinearDims(4, 64, 64), moe.NormDims(4, 64)
+    for what, call in (("ids", lambda: moe.moe_sort_pairs(8, None, ids, ids, ids, ids)), ("token rows", lambda: moe.moe_dispatch(None, inv, None, x)),
+                       ("experts' rows", lambda: moe.moe_combine([x], inv, None, None, x)), ("token rows", lambda: moe.moe_dispatch_backward(x, inv, None, None, 3)),
+                       ("experts' rows", lambda: moe.moe_combine_backward(x, inv, None, None, None)), ("x", lambda: moe.moe_linear(d, None, x, None, None, None, x, None, x)),
+                       ("dout", lambda: moe.moe_linear_backward(d, x, x, None, None, None, x, x, None, x)), ("y", lambda: moe.moe_norm_residual(n, None, x, None, None, None, x, x)),
+                       ("y", lambda: moe.moe_norm_residual_backward(n, x, x, x, None, None, None, None, x, x, None, None, None, x)),
+                       ("dims", lambda: moe.moe_linear(n, x, x, None, None, None, x, None, x)), ("dims", lambda: moe.moe_norm_residual((4, 64), x, x, None, None, None, x, x))):
+        with pytest.raises(TypeError, match=f"^{what}: expected"):
+            call()
