@@ -635,8 +635,9 @@ def moe_sort_pairs(E: int, ids, counts, offsets, perm, inv, stream=None):
                                          _ptr_of(dev, _I32, flat, "inv", inv, shape), _stream_of(stream, dev)), "moe_sort_pairs")
 
 
-def _exchange(token, rows):
-    """Device, type, T, K and H of a call on token rows [T, H] and experts' rows [T * K, H]."""
+def _exchange(token, rows, *pairs):
+    """Device, type, T, K and H of a call on token rows [T, H] and experts' rows [T * K, H]; pairs: the call's tensors [T, K] (or flat,
+    or None), which tell K where there are no tokens."""
     dev = _current("token rows", token)
     if not isinstance(rows, torch.Tensor):
         raise TypeError(f"experts' rows: expected a torch.Tensor, got {type(rows).__name__}")
@@ -644,7 +645,7 @@ def _exchange(token, rows):
         raise ValueError("token rows are [T, H], experts' rows [T * K, H]")
     T, H = token.shape
     n = rows.shape[0]
-    K = n // T if T else 1
+    K = n // T if T else next((p.shape[1] for p in pairs if isinstance(p, torch.Tensor) and p.dim() == 2), 1)
     if n != T * K:
         raise ValueError(f"experts' rows must be T * K, T = {T}: got {n}")
     code = _DTYPE.get(token.dtype)
@@ -655,7 +656,7 @@ def _exchange(token, rows):
 
 def moe_dispatch(x, inv, topk_w, rows, stream=None):
     """rows [T * K, H]: rows[inv[t, k]] = topk_w[t, k] * x[t] (topk_w None: the rows as they are)."""
-    dev, dt, code, T, K, H = _exchange(x, rows)
+    dev, dt, code, T, K, H = _exchange(x, rows, inv, topk_w)
     n = T * K
     _check(load_library().moe_dispatch(code, T, K, H, _ptr_of(dev, dt, (T, H), "x", x), _ptr_of(dev, _I32, (n,), "inv", inv, (T, K)),
                                        _ptr_of(dev, _F32, (T, K), "topk_w", topk_w, (n,)), _ptr_of(dev, dt, (n, H), "rows", rows),
@@ -664,7 +665,7 @@ def moe_dispatch(x, inv, topk_w, rows, stream=None):
 
 def moe_dispatch_backward(drows, inv, topk_w, x, dx, dtopk_w=None, stream=None):
     """dx [T, H] = sum_k topk_w[t, k] * drows[inv[t, k]]; dtopk_w [T, K] (optional; x is read for it) = x[t] . drows[inv[t, k]]."""
-    dev, dt, code, T, K, H = _exchange(dx, drows)
+    dev, dt, code, T, K, H = _exchange(dx, drows, inv, topk_w, dtopk_w)
     n = T * K
     _check(load_library().moe_dispatch_backward(code, T, K, H, _ptr_of(dev, dt, (n, H), "drows", drows), _ptr_of(dev, _I32, (n,), "inv", inv, (T, K)),
                                                 _ptr_of(dev, _F32, (T, K), "topk_w", topk_w, (n,)), _ptr_of(dev, dt, (T, H), "x", x),
@@ -674,7 +675,7 @@ def moe_dispatch_backward(drows, inv, topk_w, x, dx, dtopk_w=None, stream=None):
 
 def moe_combine(rows, inv, topk_w, residual, out, stream=None):
     """out [T, H] = residual + sum_k topk_w[t, k] * rows[inv[t, k]] (topk_w and residual may be None)."""
-    dev, dt, code, T, K, H = _exchange(out, rows)
+    dev, dt, code, T, K, H = _exchange(out, rows, inv, topk_w)
     n = T * K
     _check(load_library().moe_combine(code, T, K, H, _ptr_of(dev, dt, (n, H), "rows", rows), _ptr_of(dev, _I32, (n,), "inv", inv, (T, K)),
                                       _ptr_of(dev, _F32, (T, K), "topk_w", topk_w, (n,)), _ptr_of(dev, dt, (T, H), "residual", residual),
@@ -683,7 +684,7 @@ def moe_combine(rows, inv, topk_w, residual, out, stream=None):
 
 def moe_combine_backward(dout, inv, topk_w, rows, drows, dtopk_w=None, stream=None):
     """drows[inv[t, k]] = topk_w[t, k] * dout[t]; dtopk_w [T, K] (optional; rows are read for it) = dout[t] . rows[inv[t, k]]."""
-    dev, dt, code, T, K, H = _exchange(dout, drows)
+    dev, dt, code, T, K, H = _exchange(dout, drows, inv, topk_w, dtopk_w)
     n = T * K
     _check(load_library().moe_combine_backward(code, T, K, H, _ptr_of(dev, dt, (T, H), "dout", dout), _ptr_of(dev, _I32, (n,), "inv", inv, (T, K)),
                                                _ptr_of(dev, _F32, (T, K), "topk_w", topk_w, (n,)), _ptr_of(dev, dt, (n, H), "rows", rows),

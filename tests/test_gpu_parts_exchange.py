@@ -199,3 +199,13 @@ def test_tokens_without_slots_keep_their_residual(dtype):
         assert torch.equal(out.view(torch.uint8), res.view(torch.uint8))
         moe.moe_combine(rows, inv, w, None, out)
         assert not bool(out.view(torch.uint8).any())
+
+
+@pytest.mark.parametrize("K", [1, 8])
+def test_no_tokens_with_pairs_by_token(K):
+    """An empty batch of a router's own tensors [0, K]: nothing to do in any direction."""
+    z, inv, w = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(0, K, dtype=torch.int32, device="cuda"), torch.empty(0, K, device="cuda")
+    moe.moe_dispatch(z, inv, w, z)
+    moe.moe_combine(z, inv.view(-1), w, z, z)
+    moe.moe_dispatch_backward(z, inv, w, z, z, w)
+    moe.moe_combine_backward(z, inv.view(-1), None, z, z, w)
