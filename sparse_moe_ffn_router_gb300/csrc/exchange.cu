@@ -8,9 +8,10 @@
 //
 // All of it is bound by HBM: a token row is read once and kept in registers while its K copies are
 // written, and a token's K rows are read once, side by side, and summed in fp32 in slot order, the residual last. Measured for 4096
-// tokens of 2048 bf16 by 8 slots (graph replay): spread 25 us = 6.0 TB/s, with dots 49 us = 5.9 TB/s, gather 26 us = 6.5 TB/s, with
-// dots 40 us = 4.2 TB/s (issue slots: 24 operations for each element of a row). Rows of 2044 (8 bytes at a time) 27, 61, 35, 42 us, of 2046
-// (4 bytes) 37, 89, 43, 83, of 2045 (elements) 45, 129, 76, 142.
+// tokens of 2048 bf16 by 8 slots (graph replay): spread 25 us = 5.9 TB/s, with dots 49 us = 5.8 TB/s, gather into a residual 28 us = 6.0 TB/s,
+// with dots 40 us = 4.2 TB/s (at 101 registers two CTAs of 256 fit an SM, so the 512 are 1.7 waves and 21 % of the warps there could be are
+// active; each waits for its eight rows before it works: 27 % of the issue slots and 64 % of HBM's rate are used). Rows of 2044 (8 bytes at a
+// time) 27, 61, 32, 42 us, of 2046 (4 bytes) 37, 89, 42, 83, of 2045 (elements) 45, 131, 76, 142.
 // Sums and dots run in a fixed order, so results are the same bits on every call.
 #include <atomic>
 
@@ -301,7 +302,7 @@ struct Piece<T, 1> {
 };
 
 // (The residual waiting for the sum takes registers of the fourth CTA of 256 on an SM: with it 4096 x 2048 by 8 are gathered in 28.1 us,
-// without 30.8. Pieces of one or two elements do better unbound: 42 against 48 us of 2046 bf16, 29 against 32 of 1022 fp32.)
+// without 30.8 (1024 fp32 30.2 and 32.1). Pieces of one or two elements do better unbound: 42 against 48 us of 2046 bf16, 29 against 32 of 1022 fp32.)
 template <typename T, int VE, int TPT, bool GATHER, bool DOTS>
 __global__ void __launch_bounds__(256, TPT == 256 && GATHER && !DOTS && VE >= 4 ? 4 : 0) k_exchange(const ExchangeArgs a) {
     typedef Piece<T, VE> P;

@@ -414,7 +414,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // GELU's slope and the sums take the issue slots (4096 rows of 8192 with both: 43 us = 4.7 TB/s). A CTA takes a chunk of 4, 32 or 128 rows and 128
 // columns (for swiglu 128 gate columns and the matching up columns); 16 threads side by side hold 8 columns
 // each, 16 rows at a time. Sums are of dz before its rounding, row block by row block: those of the rows of
-// expert e in chunk c go to part[c + e], a place of their own as chunks and experts follow one another.
+// expert e in chunk c go to part[c + e], a place of their own as chunks and experts follow one another. dz itself is rounded to the
+// tensors' type, which the tensor cores take: dx and dW are then 1.41 times as far from 64 bits as by an fp32 dz (bf16 2.35e-3 of the norm against
+// 1.66e-3, fp16 2.9e-4 against 2.1e-4); to hold the rest of it in a second matrix would double both products.
 
 template <typename T>
 __device__ __forceinline__ void st_cols(T* p, const Raw& r) { *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]); }

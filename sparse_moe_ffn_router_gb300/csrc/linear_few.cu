@@ -4,7 +4,7 @@
 // of W of one to four features (of a gated one, gate and up) with 16-byte loads, eight of each kind on their way at once,
 // and keeps the sums of up to RB rows of x in registers; x comes from L1. No tensor maps, barriers or tensor memory: a
 // launch, one pass, warp sums. Rows of experts are taken one at a time: two rows of one expert read its matrix twice, the second
-// time from L2. Measured: one row, 2048 x 2048 4.1 us (weights in L2), 8192 x 4096 12.3 us = 5.5 TB/s; 8 experts'
+// time from L2. Measured: one row, 2048 x 2048 3.6 us (weights in L2), 8192 x 4096 12.3 us = 5.5 TB/s; 8 experts'
 // 1024 x 2048 7.2 us = 4.7 TB/s.
 #include "linear.cuh"
 

@@ -13,7 +13,7 @@
 // experts' dW of 512 rows takes 194 us instead of 166, of 32768 rows 250 instead of 211; with stores of the even CTA to both 236 and 240.)
 //
 // Measured (graph replay, us): 4096 x 8192 x 2048 71.5 without an activation = 1922 TFLOP/s, the rate of a library product; 76 with
-// GELU and bias; experts' products of 32768 rows, 256 x [1024, 2048]: forward 192 (5.7 TB/s), dx 186, dW 207 (5.9 TB/s).
+// GELU and bias; experts' products of 32768 rows, 256 x [1024, 2048]: forward 191 (5.7 TB/s), dx 184, dW 211 (5.8 TB/s).
 //
 // The epilogue reads accumulator fragments (a thread: two columns of one feature side by side), applies bias,
 // activation and residual in fp32 and transposes by stmatrix, 32 columns at a time, so that what is stored is

@@ -3,8 +3,10 @@
 //   n    = N(y; gamma_post)  (or y)             N(v; g) = v * rsqrt(mean(v^2) + eps) * g
 //   s    = residual_scale * residual + branch_scale * act(gate) * n
 //   xn   = N(s; gamma_pre)                      from s before its rounding
-// and the gradients of all of it. Bound by HBM: each tensor is read or written once, a row stays in
-// registers between its two sums. Everything is computed in fp32 and rounded once where it is stored.
+// and the gradients of all of it. Bound by HBM: each tensor is read or written once. Forward a row stays in registers between its two
+// sums, as far as they go: of rows of three to five vectors a thread most kernels spill 28 to 336 bytes a thread. Backward it stays in
+// shared memory, and in registers too where a thread has one vector of it (rows of 8185 fp32 and more that begin anywhere have no room
+// for ds and a whole gate there: those are read from memory twice). Everything is computed in fp32 and rounded once where it is stored.
 //
 // Backward, for g_s = ds + (gradient through xn), r = rsqrt(mean(v^2) + eps) of each norm:
 //   g_s  = ds + r_s * (dxn * gamma_pre) - s * r_s^3 * mean(dxn * gamma_pre * s)
@@ -24,9 +26,10 @@
 // length: the rows of a group all begin at the same place within a vector (their numbers are equal mod 8), so its columns
 // stay the same from row to row, and only a row's first and last vector are masked when read and written element by element.
 //
-// Measured (graph replay): forward 4096 x 2048 bf16 14.4 us = 4.7 TB/s, 32768 x 2048 88 us = 6.1 TB/s, 4096 x 2048 with a whole sigmoid gate
-// 16.0 to 16.5 us = 5.1 TB/s (issue slots 75 %); backward 4096 x 2048 28 us, 32768 x 2048 146 us = 5.5 TB/s, 4096 x 8192 87 us, 4096 x 2048
-// fp32 37 us = 5.4 TB/s: some 10 us whatever the rows for two launches, the first copies and the column sums, then issue slots.
+// Measured (graph replay): forward 4096 x 2048 bf16 14.0 us = 4.8 TB/s, 32768 x 2048 87 us = 6.2 TB/s, 4096 x 2048 with a whole sigmoid gate
+// 16.0 to 16.5 us = 5.1 TB/s (issue slots 75 %), fp32 24.8 us = 5.4 TB/s; long and odd rows: 2048 x 8191 bf16 41 us = 3.3 TB/s, fp32 96 us = 2.8 TB/s,
+// 2048 x 8192 fp32 63 us = 4.3 TB/s. Backward 4096 x 2048 28 us, 32768 x 2048 145 us = 5.6 TB/s, 4096 x 8192 86 us, 4096 x 2048
+// fp32 37 us = 5.4 TB/s, 2048 x 8191 bf16 66, fp32 126 us: some 10 us whatever the rows for two launches, the first copies and the column sums, then issue slots.
 // Tried backward: two rounds of sums and the next row in registers 37.7, 212, 155 and 60 us; 1024 threads of 64 registers that read a
 // row's pieces twice instead of 512 that hold them 36.8 and 201; packed pairs of fp32 31.3 and 171 where single ones took 29.5 and 158.
 #pragma once

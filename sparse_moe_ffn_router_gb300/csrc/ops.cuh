@@ -28,7 +28,7 @@ __device__ __forceinline__ bf16 from_f<bf16>(float v) { return __float2bfloat16_
 template <>
 __device__ __forceinline__ fp16 from_f<fp16>(float v) { return __float2half_rn(v); }
 
-// VE elements moved by one load or store: 16 bytes where every row starts on 16 bytes, else one element.
+// VE elements side by side, as one load or store moves them where their rows start on as many bytes.
 template <typename T, int VE>
 struct alignas(sizeof(T) * VE) Vec {
     T v[VE];
